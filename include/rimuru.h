@@ -499,6 +499,171 @@ int rimuru_offload_resident(rimuru_offload_t off, int layer, int expert, int* sl
  * synchronised; clear != 0 resets it to RIMURU_DEV_OK. */
 int rimuru_get_device_error(rimuru_view_t view, int* code, int clear);
 
+/* ------------------------------------------- rotary positions, KV cache */
+
+/*
+ * The attention side of the pool: what a decoder layer needs next to the MoE
+ * layer, on KV pages of the same pool.  The Rimuru pages describe KV blocks
+ * as one more view of the pool (explainer page, memory-manager paragraph) and
+ * leave the attention kernels to the serving engine; these entry points read
+ * and write those pages directly.
+ */
+
+/* Element types of activations. */
+enum { RIMURU_BF16 = 0, RIMURU_F16 = 1, RIMURU_F32 = 2 };
+
+/* Device activations [tokens][heads][head_dim]: element (t, h, d) is at
+ * data + t * token_stride + h * head_stride + d, in elements.  data must be
+ * 16-byte aligned and both strides (in bytes) multiples of 16, so q, k and v
+ * may be slices of one fused projection, and heads may be the outer axis. */
+typedef struct rimuru_heads {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t heads;
+  int32_t dtype; /* RIMURU_BF16, RIMURU_F16 or RIMURU_F32 */
+} rimuru_heads;
+
+/*
+ * Rotary positions.  The first rot_dim elements of each head form rot_dim / 2
+ * pairs: (i, i + rot_dim / 2) in RIMURU_ROPE_HALF, (2 i, 2 i + 1) in
+ * RIMURU_ROPE_INTERLEAVED.  Pair i of a head at position p turns by p * f_i
+ * and is multiplied by `mscale`; the other elements pass unchanged.
+ * f_i = base^(-2 i / rot_dim), and for contexts longer than the trained ones
+ *   RIMURU_ROPE_LINEAR    f_i / factor (position interpolation);
+ *   RIMURU_ROPE_BASE      the base raised to base * factor^(rot_dim / (rot_dim - 2));
+ *   RIMURU_ROPE_BY_PARTS  with r_i = orig_len * f_i / (2 pi) turns over the
+ *                         trained length and g_i = clamp((r_i - low) / (high -
+ *                         low), 0, 1): (1 - g_i) * f_i / factor + g_i * f_i.
+ * Angles are kept as 64-bit fractions of a turn, so they are exact to fp32
+ * rounding at every int32 position; a negative position turns back (the
+ * inverse of the rotation when mscale is 1).
+ * Requirements: base > 1, factor > 0, mscale finite; rot_dim positive, at
+ * most 256, a multiple of 16 (half) or 8 (interleaved); BY_PARTS: orig_len >
+ * 0 and high > low; BASE: rot_dim > 2.  The handle lives on the host only.
+ */
+enum { RIMURU_ROPE_HALF = 0, RIMURU_ROPE_INTERLEAVED = 1 };
+enum { RIMURU_ROPE_PLAIN = 0, RIMURU_ROPE_LINEAR = 1, RIMURU_ROPE_BASE = 2, RIMURU_ROPE_BY_PARTS = 3 };
+typedef struct rimuru_rope_s* rimuru_rope_t;
+int rimuru_rope_create(int rot_dim, int layout, double base, int scaling, double factor,
+                       double orig_len, double low, double high, double mscale, rimuru_rope_t* out);
+int rimuru_rope_destroy(rimuru_rope_t rope);
+
+/* Rotate n_arrays (1 to 4, e.g. q and k) activation arrays of the same tokens
+ * in one launch on `stream`.  positions: device int32 [num_tokens].  in[i] and
+ * out[i] (host arrays of descriptors) have the same heads and dtype; out[i]
+ * may be in[i] itself and may not overlap it otherwise.  head_dim: a multiple of 8,
+ * >= the rotation's rot_dim, at most 1024; num_tokens >= 0.
+ * Errors: RIMURU_ERR_ARG, RIMURU_ERR_ALIGN, RIMURU_ERR_UNSUPPORTED, RIMURU_ERR_CUDA. */
+int rimuru_rope_apply(rimuru_rope_t rope, const int32_t* positions, int num_tokens, int head_dim,
+                      const rimuru_heads* in, const rimuru_heads* out, int n_arrays, void* stream);
+
+/*
+ * Declare that `view` holds key/value pages of attention layers: each page
+ * holds `page_tokens` tokens of one layer as 8-bit codes (float8 e4m3), laid
+ * out [K, V][kv_heads][page_tokens][head_dim] from the page base.  A value is
+ * its code times the scale of its (page, K or V, head); dev_scales is a device
+ * array float [pages of the view][2][kv_heads] owned by the caller, of at
+ * least rimuru_kv_scale_bytes(view, kv_heads) bytes.  Every scale is a power
+ * of two in [2^-60, 2^60], which makes code * scale exact.
+ * Requirements: kv_heads >= 1; head_dim 64, 128 or 256; page_tokens 16, 32 or
+ * 64; 2 * kv_heads * page_tokens * head_dim <= page_bytes and page_bytes a
+ * multiple of page_tokens * head_dim (RIMURU_ERR_UNSUPPORTED otherwise).
+ * RIMURU_ERR_STATE if the view already has a shape of either kind. */
+int rimuru_view_set_kv_shape(rimuru_view_t view, int kv_heads, int head_dim, int page_tokens,
+                             float* dev_scales, uint64_t scales_bytes);
+/* Bytes of the scales array of a view with `kv_heads` heads; 0 on a bad argument. */
+uint64_t rimuru_kv_scale_bytes(rimuru_view_t view, int kv_heads);
+
+/*
+ * Where a sequence's tokens lie, for the entry points below:
+ *   page_table  device int32 [num_seqs][table_stride]: token t of sequence b is
+ *               slot t % page_tokens of page page_table[b][t / page_tokens];
+ *               entries past the sequence's tokens are not read
+ *   kv_lens     device int32 [num_seqs]: tokens of the sequence in the cache,
+ *               the new ones of this call included
+ * An entry outside the view, or a length past table_stride * page_tokens, is
+ * recorded in the view's device error word (RIMURU_DEV_BAD_PAGE,
+ * RIMURU_DEV_BAD_SHAPE); its tokens are then neither read nor written.
+ * The first call on a view allocates its error word: make it outside a stream
+ * capture.  Later calls only launch kernels and can be captured.
+ */
+
+/* Write new tokens' keys and values into the cache.
+ *   k, v    device [num_tokens][kv_heads][head_dim], the new tokens of all
+ *           sequences one after another
+ *   cu_new  device int32 [num_seqs + 1]: sequence b's new tokens are rows
+ *           cu_new[b] .. cu_new[b + 1] - 1; they get positions
+ *           kv_lens[b] - (number of new tokens) onwards
+ * A page's scale is the smallest power of two that brings its largest
+ * magnitude to at most 448.  When a page already holds earlier tokens its
+ * scale never shrinks; if it has to grow, their codes are rounded again at the
+ * new scale.  Codes are rounded to nearest even.  A NaN is stored as 0 and an
+ * infinity as the largest code, and either sets RIMURU_DEV_NONFINITE, so a
+ * cache written here holds finite values only.  A page of the table is written
+ * through at most one sequence: shared pages must be full (rimuru_kv_fork). */
+int rimuru_kv_append(rimuru_view_t view, const rimuru_heads* k, const rimuru_heads* v,
+                     const int32_t* cu_new, const int32_t* kv_lens, int num_seqs, int num_tokens,
+                     const int32_t* page_table, int64_t table_stride, void* stream);
+
+/* Attention over the cache, grouped heads: query head h reads key/value head
+ * h / (q->heads / kv_heads).  Query row i of sequence b (of n_b) stands at
+ * position p = kv_lens[b] - n_b + i and sees the keys at positions j <= p, and
+ * j > p - window when window > 0:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j.
+ * A row that sees no key gives 0 (and lse -inf).  Statistics and sums are fp32.
+ *   q, out    device [num_q][q heads][head_dim], RIMURU_BF16 or RIMURU_F16 and
+ *             the same type; q->heads a multiple of kv_heads
+ *   lse       device float [num_q][q heads], or NULL: log of the softmax's sum
+ *             plus its maximum (natural logarithm of sum_j exp(scale q.k_j))
+ *   cu_q      device int32 [num_seqs + 1] row offsets, or NULL for one query
+ *             row per sequence (num_q == num_seqs)
+ *   max_q     an upper bound of n_b
+ *   workspace device, 1024-byte aligned, at least
+ *             rimuru_kv_attention_workspace_bytes(...) bytes */
+uint64_t rimuru_kv_attention_workspace_bytes(rimuru_view_t view, int q_heads, int num_seqs,
+                                             int num_q, int max_q);
+int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, const rimuru_heads* out,
+                        float* lse, const int32_t* cu_q, const int32_t* kv_lens, int num_seqs,
+                        int num_q, int max_q, const int32_t* page_table, int64_t table_stride,
+                        double scale, int window, void* workspace, uint64_t workspace_bytes,
+                        void* stream);
+
+/* Copy whole pages (codes and scales): page src[i] to page dst[i], i < n, in one
+ * launch.  src and dst are device int32 arrays; no page may be in dst twice, or
+ * in both.  A pair with an id outside the view is skipped and recorded
+ * (RIMURU_DEV_BAD_PAGE). */
+int rimuru_kv_copy_pages(rimuru_view_t view, const int32_t* src, const int32_t* dst, int n,
+                         void* stream);
+
+/* References to a page the view owns.  rimuru_page_share adds one;
+ * rimuru_page_free drops one and returns the page to the allocator when it was
+ * the last.  A new page has one. */
+int rimuru_page_share(rimuru_view_t view, int64_t page_id);
+int rimuru_page_refs(rimuru_view_t view, int64_t page_id, int* refs);
+
+/* Fork a sequence of kv_len cached tokens into n children (beams, parallel
+ * samples).  pages: host int32, the parent's ceil(kv_len / page_tokens) pages.
+ * children: host int32 [n][child_stride] receives each child's pages: full
+ * pages are shared with the parent (one more reference each), a partly filled
+ * last page is copied on `stream` into a new page near the parent's.
+ * RIMURU_ERR_OOM (nothing changed) when the pool has no page left. */
+int rimuru_kv_fork(rimuru_view_t view, const int32_t* pages, int kv_len, int n, int32_t* children,
+                   int64_t child_stride, void* stream);
+
+/* Compact the view's pages so that partly used parent pages merge back and can
+ * serve other views (experts) again.  tables: host int32 array of n_entries
+ * page ids in use, in any order and with repeats; negative entries are
+ * skipped.  Parents whose pages in use all belong to this view and appear in
+ * `tables` are emptied, the sparsest first, into free pages of fuller parents,
+ * as long as a whole parent can be emptied and at most max_moves pages move.
+ * Entries of `tables` are rewritten, references move along, the copies are
+ * queued on `stream`, and the emptied pages are free at once: work that
+ * touches them must come later on the same stream.  *moved receives the
+ * number of pages moved. */
+int rimuru_kv_compact(rimuru_view_t view, int32_t* tables, int64_t n_entries, int max_moves,
+                      int* moved, void* stream);
+
 /* ------------------------------------------------------------- profiling */
 
 /* Kernel slots of one forward.  A decode-sized batch (see

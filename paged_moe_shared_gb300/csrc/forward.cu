@@ -386,13 +386,14 @@ int rimuru_get_device_error(rimuru_view_t view, int* code, int clear) {
   rimuru::clear_error();
   if (!view || !code) return fail(RIMURU_ERR_ARG, "null argument");
   rimuru::View& v = view->v;
-  if (!v.dev) {
+  int* word = v.dev ? v.dev->d_err : rimuru::kv_error_word(&v);
+  if (!word) {
     *code = RIMURU_DEV_OK;
     return RIMURU_OK;
   }
   int h = 0;
-  cudaError_t e = cudaMemcpy(&h, v.dev->d_err, sizeof(int), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && clear) e = cudaMemset(v.dev->d_err, 0, sizeof(int));
+  cudaError_t e = cudaMemcpy(&h, word, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && clear) e = cudaMemset(word, 0, sizeof(int));
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, rimuru::cuda_msg("reading the device error", e));
   *code = h;
   return RIMURU_OK;

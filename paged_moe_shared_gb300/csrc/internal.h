@@ -8,6 +8,7 @@
 #include <mutex>
 #include <set>
 #include <string>
+#include <unordered_map>
 #include <vector>
 
 #include "../../include/rimuru.h"
@@ -61,6 +62,8 @@ struct Pool {
 
 // Device-side resources of one expert view (created on first forward).
 struct DeviceState;
+// Device-side resources of one KV view (created by the first call that launches).
+struct KvState;
 
 struct View {
   Pool* pool = nullptr;
@@ -80,9 +83,19 @@ struct View {
   bool table_dirty = true;
 
   DeviceState* dev = nullptr;  // owned; freed by destroy_device_state
+
+  // KV shape (set once)
+  bool has_kv = false;
+  int kv_heads = 0, head_dim = 0, page_tokens = 0;
+  float* scales = nullptr;  // caller's device array [n_pages][2][kv_heads]
+  std::unordered_map<int64_t, int32_t> extra_refs;  // pages with more than one reference
+  KvState* kv = nullptr;  // owned; freed by destroy_kv_state
 };
 
 void destroy_device_state(View* v);
+void destroy_kv_state(View* v);
+// Device word of the view's KV state, or nullptr when no call has needed it yet.
+int* kv_error_word(const View* v);
 // RIMURU_OK when `device` (the caller's current device) holds the view's pool
 // and, once the view has device state, that state; RIMURU_ERR_ARG otherwise.
 int check_device(View* v, int device);

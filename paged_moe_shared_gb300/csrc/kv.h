@@ -1,0 +1,56 @@
+// Internals shared by the rotary, KV-cache and attention code.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "internal.h"
+
+namespace rimuru {
+
+struct KvState {
+  int device = -1;
+  int sms = 0;
+  int* d_err = nullptr;  // device error word
+  CUtensorMap tm_codes{};  // [pages][page_bytes / head_dim][head_dim] bytes over the pool
+};
+
+// Checks that the view has a KV shape and the current device holds its pool,
+// and creates the view's device state on first use.
+int kv_ready(View* v);
+// Checks one activation descriptor; `what` names it in the message.
+int check_heads(const rimuru_heads* h, const char* what);
+std::string kv_cuda_msg(const char* what, cudaError_t e);
+
+inline int64_t element_bytes(int dtype) { return dtype == RIMURU_F32 ? 4 : 2; }
+
+// Geometry of a KV view as the kernels see it.
+struct KvGeom {
+  uint8_t* pool;
+  float* scales;  // [num_pages][2][kv_heads]
+  uint64_t page_bytes;
+  int num_pages;
+  int kv_heads, head_dim, page_tokens;
+  int* err;
+};
+inline KvGeom kv_geom(const View& v) {
+  return {static_cast<uint8_t*>(v.pool->base), v.scales,   v.page_bytes,    static_cast<int>(v.n_pages),
+          v.kv_heads,                          v.head_dim, v.page_tokens, v.kv->d_err};
+}
+
+// Where the sequences lie (see the header: page_table, kv_lens).
+struct KvSeqs {
+  const int32_t* cu;  // row offsets [num_seqs + 1], or null: one row per sequence
+  const int32_t* lens;
+  const int32_t* table;
+  int64_t table_stride;
+  int num_seqs;
+  int rows;  // rows of all sequences
+};
+
+}  // namespace rimuru

@@ -345,6 +345,7 @@ int rimuru_view_destroy(rimuru_view_t view) {
   rimuru::View& v = view->v;
   rimuru::Pool& p = *v.pool;
   rimuru::destroy_device_state(&v);
+  rimuru::destroy_kv_state(&v);
   {
     std::lock_guard<std::mutex> g(p.mu);
     int lvl = p.level_of(v.page_bytes);
@@ -422,7 +423,38 @@ int rimuru_page_free(rimuru_view_t view, int64_t page_id) {
   if (page_id >= 0 && page_id < static_cast<int64_t>(v.map_count.size()) && v.map_count[page_id] > 0)
     return fail(RIMURU_ERR_STATE, "page is still mapped as an expert projection");
   std::lock_guard<std::mutex> g(v.pool->mu);
+  auto shared = v.extra_refs.find(page_id);
+  if (shared != v.extra_refs.end()) {  // other sequences still use the page
+    if (--shared->second == 0) v.extra_refs.erase(shared);
+    return RIMURU_OK;
+  }
   return v.pool->release(v.pool->level_of(v.page_bytes), v.id, page_id);
+}
+
+int rimuru_page_share(rimuru_view_t view, int64_t page_id) {
+  rimuru::clear_error();
+  if (!view) return fail(RIMURU_ERR_ARG, "null view");
+  rimuru::View& v = view->v;
+  std::lock_guard<std::mutex> g(v.pool->mu);
+  const rimuru::Level& L = v.pool->levels[v.pool->level_of(v.page_bytes)];
+  if (page_id < 0 || page_id >= L.n_pages) return fail(RIMURU_ERR_RANGE, "page id out of range");
+  if (L.state[page_id] != rimuru::Level::OWNED || L.owner[page_id] != v.id)
+    return fail(RIMURU_ERR_STATE, "page is not owned by this view");
+  v.extra_refs[page_id] += 1;
+  return RIMURU_OK;
+}
+
+int rimuru_page_refs(rimuru_view_t view, int64_t page_id, int* refs) {
+  rimuru::clear_error();
+  if (!view || !refs) return fail(RIMURU_ERR_ARG, "null argument");
+  rimuru::View& v = view->v;
+  std::lock_guard<std::mutex> g(v.pool->mu);
+  const rimuru::Level& L = v.pool->levels[v.pool->level_of(v.page_bytes)];
+  if (page_id < 0 || page_id >= L.n_pages) return fail(RIMURU_ERR_RANGE, "page id out of range");
+  const bool owned = L.state[page_id] == rimuru::Level::OWNED && L.owner[page_id] == v.id;
+  auto it = v.extra_refs.find(page_id);
+  *refs = owned ? 1 + (it == v.extra_refs.end() ? 0 : it->second) : 0;
+  return RIMURU_OK;
 }
 
 int rimuru_page_owned(rimuru_view_t view, int64_t page_id, int* owned) {
@@ -450,6 +482,7 @@ int rimuru_view_set_moe_shape(rimuru_view_t view, int layers, int experts, int h
   if (!view) return fail(RIMURU_ERR_ARG, "null view");
   rimuru::View& v = view->v;
   if (v.has_shape) return fail(RIMURU_ERR_STATE, "view already has an MoE shape");
+  if (v.has_kv) return fail(RIMURU_ERR_STATE, "view already has a KV shape");
   if (layers <= 0 || experts <= 0 || hidden <= 0 || inter <= 0 || top_k <= 0)
     return fail(RIMURU_ERR_ARG, "shape values must be positive");
   if (hidden % 128 != 0 || inter % 128 != 0)

@@ -49,7 +49,15 @@ EXPORTS = [
     "rimuru_offload_set_policy",
     "rimuru_page_alloc_near", "rimuru_pool_fragmentation", "rimuru_offload_resize",
     "rimuru_offload_capacity", "rimuru_adjust",
+    "rimuru_rope_create", "rimuru_rope_destroy", "rimuru_rope_apply", "rimuru_view_set_kv_shape",
+    "rimuru_kv_scale_bytes", "rimuru_kv_append", "rimuru_kv_attention_workspace_bytes",
+    "rimuru_kv_attention", "rimuru_kv_copy_pages", "rimuru_page_share", "rimuru_page_refs",
+    "rimuru_kv_fork", "rimuru_kv_compact",
 ]
+
+BF16, F16, F32 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_PARTS = 0, 1, 2, 3
 
 
 class RimuruError(RuntimeError):
@@ -76,11 +84,20 @@ class OffloadCounters(ctypes.Structure):
         "forwards", "hits", "misses", "prefetch_loads", "evictions", "bytes_h2d")]
 
 
+class Heads(ctypes.Structure):
+    """Activations [tokens][heads][head_dim]: base address, token and head strides in elements,
+    head count and element type (BF16, F16, F32)."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"librimuru.so not built ({LIB_PATH}); run __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
     P, i32, i64, u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
+    f64, H = ctypes.c_double, ctypes.POINTER(Heads)
     sig = {
         "rimuru_last_error": ([], ctypes.c_char_p),
         "rimuru_status_string": ([i32], ctypes.c_char_p),
@@ -126,6 +143,19 @@ def _load():
         "rimuru_offload_resize": ([P, i32], i32),
         "rimuru_offload_capacity": ([P, ctypes.POINTER(i32)], i32),
         "rimuru_adjust": ([P, P, i64, i32, i32, ctypes.POINTER(i32)], i32),
+        "rimuru_rope_create": ([i32, i32, f64, i32, f64, f64, f64, f64, f64, ctypes.POINTER(P)], i32),
+        "rimuru_rope_destroy": ([P], i32),
+        "rimuru_rope_apply": ([P, P, i32, i32, H, H, i32, P], i32),
+        "rimuru_view_set_kv_shape": ([P, i32, i32, i32, P, u64], i32),
+        "rimuru_kv_scale_bytes": ([P, i32], u64),
+        "rimuru_kv_append": ([P, H, H, P, P, i32, i32, P, i64, P], i32),
+        "rimuru_kv_attention_workspace_bytes": ([P, i32, i32, i32, i32], u64),
+        "rimuru_kv_attention": ([P, H, H, P, P, P, i32, i32, i32, P, i64, f64, i32, P, u64, P], i32),
+        "rimuru_kv_copy_pages": ([P, P, P, i32, P], i32),
+        "rimuru_page_share": ([P, i64], i32),
+        "rimuru_page_refs": ([P, i64, ctypes.POINTER(i32)], i32),
+        "rimuru_kv_fork": ([P, P, i32, i32, P, i64, P], i32),
+        "rimuru_kv_compact": ([P, P, i64, i32, ctypes.POINTER(i32), P], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -400,3 +430,103 @@ def rimuru_adjust(off, kv_view, kv_blocks_wanted: int, min_capacity: int, max_ca
     _check(lib.rimuru_adjust(off, kv_view, kv_blocks_wanted, min_capacity, max_capacity,
                              ctypes.byref(c)))
     return c.value
+
+
+def heads_of(t) -> Heads:
+    """Descriptor of a tensor [tokens, heads, head_dim] whose last axis is contiguous."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.size(2) > 1):
+        raise ValueError("expected [tokens, heads, head_dim] with a contiguous last axis")
+    name = str(t.dtype)
+    kinds = {"torch.bfloat16": BF16, "torch.float16": F16, "torch.float32": F32}
+    if name not in kinds:
+        raise ValueError(f"unsupported element type {name}")
+    return Heads(t.data_ptr(), t.stride(0), t.stride(1), t.size(1), kinds[name])
+
+
+def rimuru_rope_create(rot_dim: int, layout: int = ROPE_HALF, base: float = 10000.0,
+                       scaling: int = ROPE_PLAIN, factor: float = 1.0, orig_len: float = 0.0,
+                       low: float = 0.0, high: float = 0.0, mscale: float = 1.0):
+    h = ctypes.c_void_p()
+    _check(lib.rimuru_rope_create(rot_dim, layout, base, scaling, factor, orig_len, low, high,
+                                  mscale, ctypes.byref(h)))
+    return h
+
+
+def rimuru_rope_destroy(rope) -> None:
+    _check(lib.rimuru_rope_destroy(rope))
+
+
+def rimuru_rope_apply(rope, positions_ptr: int, num_tokens: int, head_dim: int, ins, outs,
+                      stream: int = 0) -> None:
+    """Rotate the arrays ``ins`` (a list of ``Heads``, e.g. q and k) into ``outs``."""
+    n = len(ins)
+    if len(outs) != n:
+        raise ValueError("as many outputs as inputs")
+    _check(lib.rimuru_rope_apply(rope, positions_ptr, num_tokens, head_dim, (Heads * n)(*ins),
+                                 (Heads * n)(*outs), n, stream))
+
+
+def rimuru_view_set_kv_shape(view, kv_heads: int, head_dim: int, page_tokens: int, scales_ptr: int,
+                             scales_bytes: int) -> None:
+    _check(lib.rimuru_view_set_kv_shape(view, kv_heads, head_dim, page_tokens, scales_ptr,
+                                        scales_bytes))
+
+
+def rimuru_kv_scale_bytes(view, kv_heads: int) -> int:
+    return int(lib.rimuru_kv_scale_bytes(view, kv_heads))
+
+
+def rimuru_kv_append(view, k, v, cu_new_ptr: int, kv_lens_ptr: int, num_seqs: int, num_tokens: int,
+                     page_table_ptr: int, table_stride: int, stream: int = 0) -> None:
+    _check(lib.rimuru_kv_append(view, k, v, cu_new_ptr, kv_lens_ptr, num_seqs, num_tokens,
+                                page_table_ptr, table_stride, stream))
+
+
+def rimuru_kv_attention_workspace_bytes(view, q_heads: int, num_seqs: int, num_q: int,
+                                        max_q: int) -> int:
+    return int(lib.rimuru_kv_attention_workspace_bytes(view, q_heads, num_seqs, num_q, max_q))
+
+
+def rimuru_kv_attention(view, q, out, lse_ptr: int, cu_q_ptr: int, kv_lens_ptr: int, num_seqs: int,
+                        num_q: int, max_q: int, page_table_ptr: int, table_stride: int,
+                        scale: float, window: int, workspace_ptr: int, workspace_bytes: int,
+                        stream: int = 0) -> None:
+    """``lse_ptr`` and ``cu_q_ptr`` may be 0 (no statistics; one query row per sequence)."""
+    _check(lib.rimuru_kv_attention(view, q, out, lse_ptr or None, cu_q_ptr or None, kv_lens_ptr,
+                                   num_seqs, num_q, max_q, page_table_ptr, table_stride, scale,
+                                   window, workspace_ptr, workspace_bytes, stream))
+
+
+def rimuru_kv_copy_pages(view, src_ptr: int, dst_ptr: int, n: int, stream: int = 0) -> None:
+    _check(lib.rimuru_kv_copy_pages(view, src_ptr, dst_ptr, n, stream))
+
+
+def rimuru_page_share(view, page_id: int) -> None:
+    _check(lib.rimuru_page_share(view, page_id))
+
+
+def rimuru_page_refs(view, page_id: int) -> int:
+    n = ctypes.c_int()
+    _check(lib.rimuru_page_refs(view, page_id, ctypes.byref(n)))
+    return n.value
+
+
+def rimuru_kv_fork(view, pages, kv_len: int, n: int, stream: int = 0):
+    """Fork a sequence into n children; returns the children's page lists."""
+    m = len(pages)
+    src = (ctypes.c_int32 * max(m, 1))(*[int(p) for p in pages])
+    got = (ctypes.c_int32 * max(m * n, 1))()
+    _check(lib.rimuru_kv_fork(view, ctypes.cast(src, ctypes.c_void_p), kv_len, n,
+                              ctypes.cast(got, ctypes.c_void_p), m, stream))
+    return [list(got[i * m:(i + 1) * m]) for i in range(n)]
+
+
+def rimuru_kv_compact(view, tables, max_moves: int, stream: int = 0):
+    """Compact the view's pages; ``tables`` is a flat list of page ids in use (negative entries
+    are skipped).  Returns (the rewritten list, pages moved)."""
+    n = len(tables)
+    arr = (ctypes.c_int32 * max(n, 1))(*[int(p) for p in tables])
+    moved = ctypes.c_int()
+    _check(lib.rimuru_kv_compact(view, ctypes.cast(arr, ctypes.c_void_p), n, max_moves,
+                                 ctypes.byref(moved), stream))
+    return list(arr[:n]), moved.value
