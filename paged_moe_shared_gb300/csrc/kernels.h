@@ -194,6 +194,10 @@ cudaError_t launch_decode_gemm2(DecodeArgs a, const LaunchOpts& o);
 // strides in bytes for dims 1..rank-1).  Returns a rimuru status.
 int make_bf16_map(CUtensorMap* m, void* base, int rank, const cuuint64_t* dims,
                   const cuuint64_t* strides, const cuuint32_t* box);
+// A 3-D map of bytes (8-bit codes) with the given box and swizzle.
+int make_byte_map(CUtensorMap* m, void* base, const cuuint64_t (&dims)[3],
+                  const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3],
+                  CUtensorMapSwizzle swizzle);
 // The expert view as two 3-D maps over the whole pool: [pages][H][I] (w1, w3)
 // and [pages][I][H] (w2), 64 x 64 boxes.
 int make_weight_maps(void* pool_base, uint64_t page_bytes, int64_t n_pages, int hidden, int inter,

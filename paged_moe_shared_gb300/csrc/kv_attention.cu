@@ -5,25 +5,10 @@
 #include <cmath>
 #include <limits>
 
-#include "device.cuh"
-#include "kv.h"
+#include "kv_attn.h"
 
 namespace rimuru {
 namespace {
-
-struct AttnArgs {
-  const void* q;
-  void* out;
-  float* lse;  // [rows][q_heads] or null
-  int64_t q_ts, q_hs, o_ts, o_hs;
-  int q_heads, group;  // group = q_heads / kv_heads
-  float scale_log2;    // scale * log2(e): scores are kept in base 2
-  int window;          // 0: none
-  KvSeqs s;
-  KvGeom g;
-};
-
-constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -110,6 +95,24 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+// How a call is cut: rows and number of units, and the workspace's two regions.
+struct AttnSplit {
+  int unit_rows, units_per_pair;
+  uint64_t join_bytes, part_bytes;
+};
+AttnSplit split_of(const View& v, int q_heads, int num_seqs, int max_q) {
+  const int group = q_heads / v.kv_heads;
+  AttnSplit w{};
+  const int64_t rows = static_cast<int64_t>(max_q) * group;
+  w.unit_rows = rows <= 8 ? 8 : kDecodeMaxRows;
+  w.units_per_pair = 1;
+  const uint64_t units = static_cast<uint64_t>(num_seqs) * v.kv_heads * w.units_per_pair;
+  w.join_bytes = (units * sizeof(int2) + 1023) / 1024 * 1024;
+  w.part_bytes = 2ull * kMaxRuns * w.unit_rows * (v.head_dim + 1) * sizeof(float);
+  return w;
+}
+
 }  // namespace rimuru
 
 using rimuru::fail;
@@ -118,7 +121,8 @@ extern "C" uint64_t rimuru_kv_attention_workspace_bytes(rimuru_view_t view, int 
                                                         int num_seqs, int num_q, int max_q) {
   if (!view || !view->v.has_kv || q_heads <= 0 || num_seqs < 0 || num_q < 0 || max_q < 0) return 0;
   if (q_heads % view->v.kv_heads != 0) return 0;
-  return 1024;
+  const rimuru::AttnSplit w = rimuru::split_of(view->v, q_heads, num_seqs, max_q);
+  return w.join_bytes + w.part_bytes;
 }
 
 extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, const rimuru_heads* out,
@@ -169,7 +173,20 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.s = {cu_q, kv_lens, page_table, table_stride, num_seqs, num_q};
   a.g = kv_geom(v);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = q->dtype == RIMURU_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_rows<__half>(a, s);
+  const AttnSplit w = split_of(v, q->heads, num_seqs, max_q);
+  a.max_q = max_q;
+  a.unit_rows = w.unit_rows;
+  a.units_per_pair = w.units_per_pair;
+  a.joins = static_cast<int2*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.join_bytes);
+  cudaError_t e;
+  if (static_cast<int64_t>(max_q) * a.group <= kDecodeMaxRows) {
+    a.runs = std::min(kMaxRuns, kv_decode_runs(v.kv->sms, v.head_dim));
+    e = launch_kv_decode(a, q->dtype, v.kv->tm_codes, s);
+    if (e == cudaSuccess) e = launch_kv_join(a, q->dtype, s);
+  } else {
+    e = q->dtype == RIMURU_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_rows<__half>(a, s);
+  }
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("attention launch", e));
   return RIMURU_OK;
 }

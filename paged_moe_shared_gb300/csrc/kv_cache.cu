@@ -66,6 +66,20 @@ int kv_ready(View* v) {
     destroy_kv_state(v);
     return fail(RIMURU_ERR_CUDA, kv_cuda_msg("device state of the KV view", e));
   }
+  // the pool as pages of rows of head_dim codes; a box is one head's tokens of a
+  // page, at most 128 bytes of each
+  const uint64_t dim = static_cast<uint64_t>(v->head_dim);
+  const cuuint32_t inner = static_cast<cuuint32_t>(std::min<uint64_t>(dim, 128));
+  const cuuint64_t dims[3] = {dim, v->page_bytes / dim, static_cast<cuuint64_t>(v->n_pages)};
+  const cuuint64_t strides[2] = {dim, v->page_bytes};
+  const cuuint32_t box[3] = {inner, static_cast<cuuint32_t>(v->page_tokens), 1};
+  st = make_byte_map(&k->tm_codes, v->pool->base, dims, strides, box,
+                     inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != RIMURU_OK) {
+    const std::string msg = rimuru_last_error();
+    destroy_kv_state(v);
+    return fail(st, msg);
+  }
   return RIMURU_OK;
 }
 

@@ -56,6 +56,20 @@ int make_bf16_map(CUtensorMap* m, void* base, int rank, const cuuint64_t* dims,
   return RIMURU_OK;
 }
 
+int make_byte_map(CUtensorMap* m, void* base, const cuuint64_t (&dims)[3],
+                  const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3],
+                  CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(RIMURU_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(RIMURU_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(r));
+  return RIMURU_OK;
+}
+
 int make_weight_maps(void* pool_base, uint64_t page_bytes, int64_t n_pages, int hidden, int inter,
                      CUtensorMap* tm_w13, CUtensorMap* tm_w2) {
   const uint64_t H = hidden, I = inter, P = static_cast<uint64_t>(n_pages);
