@@ -109,7 +109,7 @@ AttnSplit split_of(const View& v, int q_heads, int num_seqs, int max_q) {
   w.units_per_pair = 1;
   const uint64_t units = static_cast<uint64_t>(num_seqs) * v.kv_heads * w.units_per_pair;
   w.join_bytes = (units * sizeof(int2) + 1023) / 1024 * 1024;
-  w.part_bytes = 2ull * kMaxRuns * w.unit_rows * (v.head_dim + 1) * sizeof(float);
+  w.part_bytes = 2ull * kMaxRuns * w.unit_rows * (v.head_dim + 1) * sizeof(float);  // and statistics
   return w;
 }
 
@@ -178,10 +178,15 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.unit_rows = w.unit_rows;
   a.units_per_pair = w.units_per_pair;
   a.joins = static_cast<int2*>(workspace);
+  a.unit_q = w.unit_rows / a.group;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.join_bytes);
+  a.stat = a.part + 2ll * kMaxRuns * w.unit_rows * v.head_dim;
+  const double tiles = (static_cast<double>(table_stride) * v.page_tokens / kTileTokens + 1) *
+                       num_seqs * v.kv_heads * w.units_per_pair;
+  if (tiles > 2e9) return fail(RIMURU_ERR_UNSUPPORTED, "too many keys and queries for one call");
   cudaError_t e;
   if (static_cast<int64_t>(max_q) * a.group <= kDecodeMaxRows) {
-    a.runs = std::min(kMaxRuns, kv_decode_runs(v.kv->sms, v.head_dim));
+    a.runs = std::min(kMaxRuns, kv_decode_runs(v.kv->sms, v.head_dim, w.unit_rows));
     e = launch_kv_decode(a, q->dtype, v.kv->tm_codes, s);
     if (e == cudaSuccess) e = launch_kv_join(a, q->dtype, s);
   } else {

@@ -33,9 +33,11 @@ struct AttnArgs {
   // work split
   int runs;            // CTAs that share the tiles
   int unit_rows;       // query rows (query x group) of a unit
+  int unit_q;          // whole query rows of a unit: unit_rows / group
   int units_per_pair;  // bound of the units of one (sequence, head)
   int2* joins;         // [num_seqs][kv_heads][units_per_pair]: runs (first, last) of a unit cut up
-  float* part;         // [2 runs][unit_rows][head_dim + 1] partial results
+  float* part;         // [2 runs][unit_rows][head_dim] partial results, then
+  float* stat;         // [2 runs][unit_rows] their log2 sums
 };
 
 constexpr float kLn2 = 0.69314718055994531f;
@@ -67,19 +69,16 @@ __device__ __forceinline__ TileSpan tile_span(const AttnArgs& p, const SeqShape&
   t.first = p.window > 0 && p0 >= p.window ? (p0 - p.window + 1) / kTileTokens : 0;
   return t;
 }
-// Query rows [i0, i1) of unit w of a sequence.  A unit holds unit_rows / group
-// whole query rows.
+// A unit holds the query rows [w unit_q, (w + 1) unit_q) of its sequence.
 __device__ __forceinline__ int units_of(const AttnArgs& p, const SeqShape& s) {
-  const int per = p.unit_rows / p.group;
-  return (s.n + per - 1) / per;
+  return p.units_per_pair == 1 ? (s.n > 0) : (s.n + p.unit_q - 1) / p.unit_q;
 }
 __device__ __forceinline__ TileSpan unit_span(const AttnArgs& p, const SeqShape& s, int w) {
-  const int per = p.unit_rows / p.group;
-  return tile_span(p, s, w * per, min(s.n, (w + 1) * per));
+  return tile_span(p, s, w * p.unit_q, min(s.n, (w + 1) * p.unit_q));
 }
 // Tiles of one head of a sequence, over all its units.
-__device__ __forceinline__ int64_t pair_tiles(const AttnArgs& p, const SeqShape& s) {
-  int64_t n = 0;
+__device__ __forceinline__ int pair_tiles(const AttnArgs& p, const SeqShape& s) {
+  int n = 0;
   const int u = units_of(p, s);
   for (int w = 0; w < u; ++w) {
     const TileSpan t = unit_span(p, s, w);
@@ -88,104 +87,115 @@ __device__ __forceinline__ int64_t pair_tiles(const AttnArgs& p, const SeqShape&
   return n;
 }
 
-// Run c holds the tiles [run_start(c), run_start(c + 1)) of the total.
-__device__ __forceinline__ int64_t run_start(int64_t total, int runs, int c) {
-  return total * c / runs;
-}
-__device__ __forceinline__ int run_of(int64_t total, int runs, int64_t tile) {
-  return static_cast<int>(((tile + 1) * runs + total - 1) / total) - 1;
+// The total is cut into `runs` runs of base or base + 1 tiles, the longer first.
+struct RunCut {
+  int base, longer, runs;
+};
+__device__ __forceinline__ int run_start(const RunCut& k, int c) { return c * k.base + min(c, k.longer); }
+__device__ __forceinline__ int run_of(const RunCut& k, int tile) {
+  const int head = k.longer * (k.base + 1);
+  return tile < head ? tile / (k.base + 1) : k.longer + (tile - head) / k.base;
 }
 
-// Where a run begins: sequence, head and tile offset within the head's tiles.
+// One run: its tiles and where its first one lies.
 struct RunStart {
-  int64_t tiles;  // tiles of this run
-  int64_t at;     // first tile within (b, h)
-  int64_t begin;  // first tile, counted over all units
-  int64_t total;
-  int runs;       // runs that have tiles
-  int b, h;
+  RunCut cut;
+  int begin, tiles;  // of the total
+  int b, h, w, at;   // sequence, head, unit, and the tile within the unit
+  SeqShape s;
 };
 
-// Found by the whole CTA (every thread calls it; `scratch` is 40 int64 of
-// shared memory): thread t sums the tiles of a contiguous share of the
-// sequences, the shares are scanned, and the thread whose share holds the
-// run's first tile walks its share.
-__device__ __forceinline__ void find_run(const AttnArgs& p, int c, int64_t* scratch, RunStart* out) {
+// Found by the whole CTA (every thread calls it; `scratch` has an int per
+// warp): thread t sums the tiles of a contiguous share of the sequences, the
+// shares are scanned, and the thread whose share holds the run's first tile
+// walks its share.  Totals fit an int (checked on the host).
+__device__ __forceinline__ void find_run(const AttnArgs& p, int c, int* scratch, RunStart* out) {
   const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5;
-  const int b0 = static_cast<int>(static_cast<int64_t>(p.s.num_seqs) * t / nt);
-  const int b1 = static_cast<int>(static_cast<int64_t>(p.s.num_seqs) * (t + 1) / nt);
-  int64_t mine = 0;
+  const int share = p.s.num_seqs <= nt ? 1 : (p.s.num_seqs + nt - 1) / nt;
+  const int b0 = min(p.s.num_seqs, t * share), b1 = min(p.s.num_seqs, b0 + share);
+  int mine = 0, n0 = 0;
+  SeqShape s0{};
   for (int b = b0; b < b1; ++b) {
     const SeqShape s = seq_shape(p, b);
     if (!s.ok && c == 0) dev::set_error(p.g.err, RIMURU_DEV_BAD_SHAPE);
-    mine += pair_tiles(p, s) * p.g.kv_heads;
+    const int n = pair_tiles(p, s);
+    if (b == b0) s0 = s, n0 = n;
+    mine += n * p.g.kv_heads;
   }
-  int64_t scan = mine;
+  int scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+    const int v = __shfl_up_sync(0xffffffffu, scan, o);
     if (lane >= o) scan += v;
   }
   if (lane == 31) scratch[warp] = scan;
   __syncthreads();
-  int64_t before = scan - mine, total = 0;
+  int before = scan - mine, total = 0;
   for (int w = 0; w < nt / 32; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
   // no run between the first and the last is empty, so every run of a unit leaves a part
-  const int runs = static_cast<int>(min(total, static_cast<int64_t>(p.runs)));
-  const int64_t begin = c < runs ? run_start(total, runs, c) : total;
-  const int64_t end = c < runs ? run_start(total, runs, c + 1) : total;
+  RunCut k;
+  k.runs = min(total, p.runs);
+  k.base = k.runs > 0 ? total / k.runs : 0;
+  k.longer = total - k.base * k.runs;
+  const int begin = c < k.runs ? run_start(k, c) : total;
+  const int tiles = c < k.runs ? k.base + (c < k.longer ? 1 : 0) : 0;
   if (t == 0) {
-    out->tiles = end - begin;
+    out->cut = k;
     out->begin = begin;
-    out->total = total;
-    out->runs = runs;
+    out->tiles = tiles;
   }
-  if (begin < end && begin >= before && begin < before + mine) {
-    int64_t at = begin - before;
-    for (int b = b0; b < b1; ++b) {
-      const int64_t n = pair_tiles(p, seq_shape(p, b));
-      if (at < n * p.g.kv_heads) {
-        out->b = b;
-        out->h = static_cast<int>(at / n);
-        out->at = at % n;
-        break;
-      }
+  if (tiles > 0 && begin >= before && begin < before + mine) {
+    int at = begin - before, b = b0, n = n0;
+    SeqShape s = s0;
+    while (at >= n * p.g.kv_heads) {
       at -= n * p.g.kv_heads;
+      s = seq_shape(p, ++b);
+      n = pair_tiles(p, s);
     }
+    int h = 0, w = 0;
+    while (at >= n) at -= n, ++h;
+    while (true) {
+      const TileSpan x = unit_span(p, s, w);
+      if (at < x.last - x.first) break;
+      at -= x.last - x.first;
+      ++w;
+    }
+    out->b = b;
+    out->h = h;
+    out->w = w;
+    out->at = at;
+    out->s = s;
   }
   __syncthreads();
 }
 
 // Walks a run segment by segment: the part of a unit that lies in the run.
 struct Segment {
-  int b, h, w;          // sequence, head, unit
+  int b, h, w;        // sequence, head, unit
   SeqShape s;
-  int i0, i1;           // query rows of the unit
-  int t0, t1;           // its tiles within this run
-  bool starts, ends;    // holds the unit's first / last tile
+  int i0, i1;         // query rows of the unit
+  int t0, t1;         // its tiles within this run
+  int first;          // the first of them, counted over all units
+  int unit_tiles;     // tiles of the whole unit
+  bool starts, ends;  // holds the unit's first / last tile
 };
 struct RunWalk {
-  int64_t left, at;
+  int left, at, begin;
   int b, h, w, u;  // next unit; u: units of sequence b
   SeqShape s;
-  __device__ __forceinline__ void begin(const AttnArgs& p, const RunStart& r) {
+  __device__ __forceinline__ void begin_run(const AttnArgs& p, const RunStart& r) {
     left = r.tiles;
     if (left <= 0) return;
+    begin = r.begin;
     b = r.b;
     h = r.h;
+    w = r.w;
     at = r.at;
-    s = seq_shape(p, b);
+    s = r.s;
     u = units_of(p, s);
-    w = 0;
-    while (true) {  // the unit that holds tile `at`
-      const TileSpan t = unit_span(p, s, w);
-      if (at < t.last - t.first) break;
-      at -= t.last - t.first;
-      ++w;
-    }
   }
   __device__ __forceinline__ bool next(const AttnArgs& p, Segment* g) {
     if (left <= 0) return false;
@@ -204,18 +214,20 @@ struct RunWalk {
         u = units_of(p, s);
       }
     }
-    const int per = p.unit_rows / p.group;
     g->b = b;
     g->h = h;
     g->w = w;
     g->s = s;
-    g->i0 = w * per;
-    g->i1 = min(s.n, (w + 1) * per);
-    g->t0 = t.first + static_cast<int>(at);
-    g->t1 = static_cast<int>(min(static_cast<int64_t>(t.last), g->t0 + left));
+    g->i0 = w * p.unit_q;
+    g->i1 = min(s.n, g->i0 + p.unit_q);
+    g->t0 = t.first + at;
+    g->t1 = min(t.last, g->t0 + left);
+    g->first = begin;
+    g->unit_tiles = t.last - t.first;
     g->starts = at == 0;
     g->ends = g->t1 == t.last;
     left -= g->t1 - g->t0;
+    begin += g->t1 - g->t0;
     at = 0;
     ++w;
     return true;
@@ -224,12 +236,16 @@ struct RunWalk {
 
 // Slot of a segment that is not a whole unit: the run's first segment when it
 // continues a unit, its last one when it begins a unit.
-__device__ __forceinline__ float* part_slot(const AttnArgs& p, int run, bool starts) {
-  const int64_t slot = 2ll * run + (starts ? 1 : 0);
-  return p.part + slot * p.unit_rows * (p.g.head_dim + 1);
+__device__ __forceinline__ int64_t part_slot(const AttnArgs& p, int run, bool starts) {
+  return static_cast<int64_t>(2 * run + (starts ? 1 : 0)) * p.unit_rows;
 }
 __device__ __forceinline__ int2* join_of(const AttnArgs& p, int b, int h, int w) {
   return p.joins + (static_cast<int64_t>(b) * p.g.kv_heads + h) * p.units_per_pair + w;
+}
+// Notes which runs hold the parts of a unit (called where the unit begins).
+__device__ __forceinline__ void note_join(const AttnArgs& p, const Segment& g, const RunCut& k, int run) {
+  *join_of(p, g.b, g.h, g.w) =
+      g.ends ? make_int2(-1, -1) : make_int2(run, run_of(k, g.first + g.unit_tiles - 1));
 }
 
 // Sets a kernel's dynamic shared memory limit once per device.
@@ -255,6 +271,6 @@ cudaError_t launch_kv_decode(const AttnArgs& a, int dtype, const CUtensorMap& tm
 cudaError_t launch_kv_join(const AttnArgs& a, int dtype, cudaStream_t s);
 // Rows of a unit of the decode kernel: 8 or 16.
 constexpr int kDecodeMaxRows = 16;
-int kv_decode_runs(int sms, int head_dim);
+int kv_decode_runs(int sms, int head_dim, int rows);
 
 }  // namespace rimuru

@@ -21,10 +21,14 @@
 // are relative to the tile's own maximum, so no accumulator is ever rescaled:
 // tiles are joined in fp32 registers.
 //
-// Warp 0 issues the copies, warp 1 the MMAs, warps 2-5 do the softmax; S and O
-// are double buffered in TMEM, so K Q^T of the next tile runs during the
-// softmax of this one.  With 8 rows and head_dim 128 a tile costs the softmax
-// warps about 400 instructions each, a third of the time its bytes take.
+// The parts of Q and of P lie side by side as columns of one MMA (8 rows: N = 16
+// or 32), so each byte of K and V is read from shared memory once, and are
+// added up in registers.
+//
+// Warp 0 copies (it also reads the page table and the scales, 32 pages at a
+// time), warp 1 issues the MMAs, warp 2 prepares Q of the next segment, warps
+// 3-6 do the softmax.  S and O are double buffered in TMEM, so K Q^T of the next
+// tile, of the next segment too, runs during the softmax of this one.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -36,37 +40,42 @@ namespace {
 
 using namespace dev;
 
-constexpr int kDecodeThreads = 192;
+constexpr int kDecodeThreads = 224;
 constexpr int kWeightParts = 4;
 constexpr float kWeightTop = 15.f;  // weights are scaled by 2^15: e5m2 ends at 1.75 * 2^15
+constexpr int kMetaRing = 8;
+
+constexpr int decode_ctas(int head_dim, int rows) { return head_dim <= 128 && rows <= 8 ? 2 : 1; }
 
 template <int kD, int kR, int kQParts>
 struct DecodeCfg {
   static constexpr int kRowBytes = kD < 128 ? kD : 128;  // bytes of a token in one slab
   static constexpr int kSlabs = kD / kRowBytes;           // slabs of a K or V tile
   static constexpr int kSlabBytes = kTileTokens * kRowBytes;
-  static constexpr int kCtas = kD <= 128 ? 2 : 1;  // per SM
-  static constexpr int kRing = kD <= 128 ? (kD == 64 ? 10 : 6) : 12;  // slabs
-  static constexpr int kN = kR < 16 ? 16 : kR;  // columns of an MMA
-  static constexpr int kQBytes = kN * kD;       // one part of Q: kSlabs x [kN][kRowBytes]
-  static constexpr int kPBytes = kN * 128;      // one part of P: [kN][128 tokens]
-  static constexpr int kTmem = 2 * kN + 2 * kSlabs * kN;  // S twice, O twice
-  static constexpr int kTmemCols = kTmem <= 32 ? 32 : kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : 256;
-  static constexpr int kSmem =
-      1024 + kRing * kSlabBytes + kQParts * kQBytes + kWeightParts * kPBytes + 1024;
+  static constexpr int kCtas = decode_ctas(kD, kR);  // per SM
+  static constexpr int kRing = kCtas == 1 ? 12 : kD == 64 ? 10 : 6;  // slabs
+  static constexpr int kNS = (kQParts * kR + 15) / 16 * 16;  // columns of S: part x row
+  static constexpr int kNO = kWeightParts * kR;              // columns of O
+  static constexpr int kQBytes = kNS * kD;  // Q: kSlabs x [kNS][kRowBytes]
+  static constexpr int kPBytes = kNO * 128;  // P: [128 tokens][kNO]
+  static constexpr int kTmem = 2 * kNS + 2 * kSlabs * kNO;  // S twice, O twice
+  static constexpr int kTmemCols = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
+  static constexpr int kSmem = 1024 + kRing * kSlabBytes + 2 * kQBytes + kPBytes;
 };
 
 struct DecodeShared {
   uint64_t full[12], empty[12];
-  uint64_t q_full, p_full;
+  uint64_t meta_full[kMetaRing];
+  uint64_t q_full[2], q_empty[2], p_full;
   uint64_t s_full[2], o_full[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
   RunStart run;
-  int64_t scratch[8];
+  int scratch[8];
+  float2 meta[kMetaRing][8];  // per page of a tile: scales of K and V; V 0: no such page
   float tile_max[2][4][kDecodeMaxRows];
-  float row_scale[kDecodeMaxRows];
+  float row_scale[2][kDecodeMaxRows];
   float row_sum[4][kDecodeMaxRows];
 };
 
@@ -106,18 +115,31 @@ __device__ __forceinline__ int swz(int r, int d) {
   if (kRowBytes == 128) return r * 128 + ((((d >> 4) ^ r) & 7) << 4) + (d & 15);
   return r * 64 + ((((d >> 4) ^ (r >> 1)) & 3) << 4) + (d & 15);
 }
-template <int kN>
-__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[kN]) {
-  if constexpr (kN == 8) tmem_ld8(t, r);
-  else tmem_ld16(t, r);
+// Sums of kParts blocks of kR columns of this thread's TMEM lane.
+template <int kParts, int kR>
+__device__ __forceinline__ void tmem_sum(uint32_t t, float (&x)[kR]) {
+  uint32_t v[kParts][kR];
+#pragma unroll
+  for (int part = 0; part < kParts; ++part) {
+    if constexpr (kR == 8) tmem_ld8(t + part * kR, v[part]);
+    else tmem_ld16(t + part * kR, v[part]);
+  }
+  tmem_ld_wait();
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    x[r] = __uint_as_float(v[kParts - 1][r]);  // smallest parts first
+#pragma unroll
+    for (int part = kParts - 2; part >= 0; --part) x[r] += __uint_as_float(v[part][r]);
+  }
 }
 
 template <typename T, int kD, int kR>
-__global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
     kv_decode_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap tm) {
-  constexpr int kQParts = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 2 : 3;
+  constexpr int kQParts = std::is_same<T, __nv_bfloat16>::value ? 2 : 3;
   using C = DecodeCfg<kD, kR, kQParts>;
-  constexpr int kN = C::kN, kSlabs = C::kSlabs, kRing = C::kRing, kRowBytes = C::kRowBytes;
+  constexpr int kNS = C::kNS, kNO = C::kNO;
+  constexpr int kSlabs = C::kSlabs, kRing = C::kRing, kRowBytes = C::kRowBytes;
   constexpr uint32_t kSwizzle = kRowBytes == 128 ? 2 : 4;
   constexpr uint32_t kAtom = 8 * kRowBytes;  // eight rows
   extern __shared__ uint8_t smem_raw[];
@@ -125,7 +147,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sRing = smem;
   uint8_t* sQ = sRing + kRing * C::kSlabBytes;
-  uint8_t* sP = sQ + kQParts * C::kQBytes;
+  uint8_t* sP = sQ + 2 * C::kQBytes;
   __shared__ DecodeShared sh_;
   DecodeShared* sh = &sh_;
   volatile int* abort = &sh->abort;
@@ -136,9 +158,11 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], 1);
     }
-    mbar_init(&sh->q_full, 4);
+    for (int i = 0; i < kMetaRing; ++i) mbar_init(&sh->meta_full[i], 1);
     mbar_init(&sh->p_full, 4);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->q_full[i], 1);
+      mbar_init(&sh->q_empty[i], 4);
       mbar_init(&sh->s_full[i], 1);
       mbar_init(&sh->o_full[i], 1);
     }
@@ -158,50 +182,79 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
-  const uint32_t tS = tmem, tO = tmem + 2 * kN;
-  const int P = p.g.page_tokens;
+  const uint32_t tS = tmem, tO = tmem + 2 * kNS;
+  const int P = p.g.page_tokens, log_p = 31 - __clz(P);
   RunWalk walk;
-  walk.begin(p, sh->run);
+  walk.begin_run(p, sh->run);
   Segment g;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
     // Unit 2 i is the K tile i of the run, unit 2 i + 1 its V tile; a unit is
-    // kSlabs slots of the ring.  Lane l copies page l of the tile.
+    // kSlabs slots of the ring.  The warp holds the ids and scales of 32 pages,
+    // one per lane (`boxes` pages are a tile), and the ids of the next 32.
     const uint64_t pol = policy_evict_first();
-    const int boxes = kTileTokens / P;
-    uint32_t slot = 0;
+    const int boxes = kTileTokens >> log_p;
+    uint32_t slot = 0, tile = 0;
     bool ok = true;
     while (ok && walk.next(p, &g)) {
       const int lo = p.window > 0 ? max(0, g.s.len - g.s.n + g.i0 - p.window + 1) : 0;
-      for (int t = g.t0; ok && t < g.t1; ++t) {
-        const int tok = t * kTileTokens + lane * P;  // first token of this lane's page
+      const int32_t* row = p.s.table + g.b * p.s.table_stride;
+      const auto page_at = [&](int c) {  // page c of the sequence, -1 when none of its tokens count
         int page = -1;
-        if (lane < boxes && tok < g.s.len && tok + P > lo) {
-          page = p.s.table[g.b * p.s.table_stride + tok / P];
+        if (c << log_p < g.s.len && (c + 1) << log_p > lo && c < g.t1 * boxes) {
+          page = row[c];
           if (page < 0 || page >= p.g.num_pages) {
             set_error(p.g.err, RIMURU_DEV_BAD_PAGE);
             page = -1;
           }
         }
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * P * kRowBytes;
+        return page;
+      };
+      int c = g.t0 * boxes + lane, at = 32;
+      int ahead = page_at(c), page = -1;
+      float ks = 0.f, vs = 0.f;
+      for (int t = g.t0; ok && t < g.t1; ++t, ++tile) {
+        if (at == 32) {
+          page = ahead;
+          ks = vs = 0.f;
+          if (page >= 0) {
+            const float* sc = p.g.scales + static_cast<int64_t>(page) * 2 * p.g.kv_heads + g.h;
+            ks = sc[0];
+            vs = sc[p.g.kv_heads];
+          }
+          c += 32;
+          ahead = page_at(c);
+          at = 0;
+        }
+        const int mine = __shfl_sync(0xffffffffu, page, (at + lane) & 31);  // for lanes below `boxes`
+        const bool copies = lane < boxes && mine >= 0;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copies)) * P * kRowBytes;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const int row = (kv * p.g.kv_heads + g.h) * P;  // first row of the head in the page
+          const int y = (kv * p.g.kv_heads + g.h) << log_p;  // first row of the head in the page
 #pragma unroll
-          for (int sl = 0; sl < kSlabs; ++sl, ++slot) {
+          for (int sl = 0; sl < kSlabs; ++sl) {
+            if (!ok) break;
             const uint32_t i = slot % kRing, ph = (slot / kRing) & 1u;
-            ok = ok && mbar_wait(&sh->empty[i], ph ^ 1u, abort);
+            ok = mbar_wait(&sh->empty[i], ph ^ 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&sh->full[i], bytes);
             __syncwarp();
-            if (page >= 0)
-              tma_load_3d(sRing + i * C::kSlabBytes + lane * P * kRowBytes, &tm, &sh->full[i],
-                          sl * kRowBytes, row, page, pol);
+            if (copies)
+              tma_load_3d(sRing + i * C::kSlabBytes + (lane << log_p) * kRowBytes, &tm, &sh->full[i],
+                          sl * kRowBytes, y, mine, pol);
+            ++slot;
           }
-          if (!ok) break;
         }
+        // The tile's scales.  The entry's last reader was at least eight tiles back, and
+        // the slots just waited for were freed by the MMAs of a later tile than that.
+        if (lane >= at && lane < at + boxes)
+          sh->meta[tile % kMetaRing][lane - at] = make_float2(ks, vs);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->meta_full[tile % kMetaRing]);
+        at += boxes;
       }
     }
     if (!ok && lane == 0) {
@@ -215,26 +268,20 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f8_f32(128, kN, false, false, false);
-      constexpr uint32_t id_o = idesc_f8_f32(128, kN, /*a_mn=*/true, false, /*b_e5m2=*/true);
-      uint32_t tile = 0, seg = 0;
-      bool ok = true;
-      const auto scores = [&](uint32_t i) {  // S^T of the run's tile i
+      constexpr uint32_t id_s = idesc_f8_f32(128, kNS, false, false, false);
+      constexpr uint32_t id_o = idesc_f8_f32(128, kNO, /*a_mn=*/true, /*b_mn=*/true, /*b_e5m2=*/true);
+      const auto scores = [&](uint32_t i, uint32_t seg) {  // S^T of the run's tile i
 #pragma unroll
         for (int sl = 0; sl < kSlabs; ++sl) {
           const uint32_t u = 2 * i * kSlabs + sl, slot = u % kRing;
           if (!mbar_wait(&sh->full[slot], (u / kRing) & 1u, abort)) return false;
           tc_fence_after();
           const uint32_t a0 = smem_u32(sRing + slot * C::kSlabBytes);
+          const uint32_t b0 = smem_u32(sQ + (seg & 1u) * C::kQBytes + sl * kNS * kRowBytes);
 #pragma unroll
-          for (int part = 0; part < kQParts; ++part) {
-            const uint32_t b0 = smem_u32(sQ + part * C::kQBytes + sl * kN * kRowBytes);
-#pragma unroll
-            for (int k = 0; k < kRowBytes / 32; ++k)
-              umma_f8(tS + (i & 1u) * kN, smem_desc(a0 + 32 * k, 16, kAtom, kSwizzle),
-                      smem_desc(b0 + 32 * k, 16, kAtom, kSwizzle), id_s,
-                      (sl | part | k) != 0 ? 1u : 0u);
-          }
+          for (int k = 0; k < kRowBytes / 32; ++k)
+            umma_f8(tS + (i & 1u) * kNS, smem_desc(a0 + 32 * k, 16, kAtom, kSwizzle),
+                    smem_desc(b0 + 32 * k, 16, kAtom, kSwizzle), id_s, (sl | k) != 0 ? 1u : 0u);
           umma_commit(&sh->empty[slot]);
         }
         umma_commit(&sh->s_full[i & 1u]);
@@ -249,28 +296,37 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
           tc_fence_after();
           const uint32_t a0 = smem_u32(sRing + slot * C::kSlabBytes);
 #pragma unroll
-          for (int part = 0; part < kWeightParts; ++part) {
-            const uint32_t b0 = smem_u32(sP + part * C::kPBytes);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // 32 tokens: four groups of eight rows
-              umma_f8(tO + ((i & 1u) * kSlabs + sl) * kN,
-                      smem_desc(a0 + 4 * k * kAtom, C::kSlabBytes, kAtom, kSwizzle),
-                      smem_desc(b0 + 32 * k, 16, 1024, 2), id_o, (part | k) != 0 ? 1u : 0u);
-          }
+          for (int k = 0; k < 4; ++k)  // 32 tokens: four groups of eight rows
+            umma_f8(tO + ((i & 1u) * kSlabs + sl) * kNO,
+                    smem_desc(a0 + 4 * k * kAtom, C::kSlabBytes, kAtom, kSwizzle),
+                    smem_desc(smem_u32(sP) + 32 * k * kNO, C::kPBytes, 8 * kNO, kNO == 64 ? 4 : 6), id_o,
+                    k != 0 ? 1u : 0u);
           umma_commit(&sh->empty[slot]);
         }
         umma_commit(&sh->o_full[i & 1u]);
         return true;
       };
-      while (ok && walk.next(p, &g)) {
-        ok = mbar_wait(&sh->q_full, seg & 1u, abort);
-        tc_fence_after();
-        ok = ok && scores(tile);
-        for (int t = g.t0; ok && t < g.t1; ++t, ++tile) {
-          if (t + 1 < g.t1) ok = scores(tile + 1);
+      // S of the next tile is issued before O of this one.  Its buffer and this
+      // one's are free: the weights of the tile before were written after the
+      // softmax warps had read them.
+      bool ok = true;
+      uint32_t tile = 0, seg = 0;
+      if (walk.next(p, &g)) {
+        ok = mbar_wait(&sh->q_full[0], 0, abort) && scores(0, 0);
+        for (int t = g.t0; ok; ++tile) {
+          bool more = true;
+          if (++t == g.t1) {
+            more = walk.next(p, &g);
+            if (more) {
+              ++seg;
+              t = g.t0;
+              ok = mbar_wait(&sh->q_full[seg & 1u], (seg >> 1) & 1u, abort);
+            }
+          }
+          if (more) ok = ok && scores(tile + 1, seg);
           ok = ok && outputs(tile);
+          if (!more) break;
         }
-        ++seg;
       }
       if (!ok) {
         set_error(p.g.err, RIMURU_DEV_TIMEOUT);
@@ -280,129 +336,147 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
       volatile int never = 0;
       mbar_wait(&sh->drain, 0, &never);
     }
+  } else if (warp == 2) {
+    // --------------------------------------------------------------------- Q
+    uint32_t seg = 0;
+    bool ok = true;
+    while (ok && walk.next(p, &g)) {
+      constexpr int kPer = kD / 32;
+      const uint32_t buf = seg & 1u;
+      const int rows = (g.i1 - g.i0) * p.group;
+      uint8_t* q_s = sQ + buf * C::kQBytes;
+      const T* src = static_cast<const T*>(p.q) + (g.s.row0 + g.i0) * p.q_ts + g.h * p.group * p.q_hs + lane * kPer;
+      int of_group = 0;  // the row's place in its group; src is its address
+#pragma unroll 1
+      for (int half = 0; half < kR; half += 8) {
+        T raw[8][kPer];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = half + k;
+          if (r < rows) {
+            if constexpr (kPer == 8) *reinterpret_cast<uint4*>(raw[k]) = *reinterpret_cast<const uint4*>(src);
+            else if constexpr (kPer == 4) *reinterpret_cast<uint2*>(raw[k]) = *reinterpret_cast<const uint2*>(src);
+            else *reinterpret_cast<uint32_t*>(raw[k]) = *reinterpret_cast<const uint32_t*>(src);
+            src += p.q_hs;
+            if (++of_group == p.group) of_group = 0, src += p.q_ts - p.group * p.q_hs;
+          } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) from_f(0.f, &raw[k][i]);
+          }
+        }
+        if (half == 0) {
+          ok = mbar_wait(&sh->q_empty[buf], ((seg >> 1) & 1u) ^ 1u, abort);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = half + k;
+          float x[kPer], amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            x[i] = to_f(raw[k][i]);
+            amax = fmaxf(amax, fabsf(x[i]));
+          }
+          amax = warp_max(amax);
+          // power of two that brings the row's largest magnitude into (224, 448]
+          const uint32_t ab = __float_as_uint(amax);
+          const int e = max(-100, min(100, static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u)));
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) x[i] *= inv;
+          const int d0 = lane * kPer, sl = d0 / kRowBytes;
+#pragma unroll
+          for (int part = 0; part < kQParts; ++part) {
+            uint8_t* dst = q_s + sl * kNS * kRowBytes + swz<kRowBytes>(part * kR + r, d0 % kRowBytes);
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2) {
+              const uint32_t c = e4m3x2(x[i], x[i + 1]);
+              const float2 f = from_e4m3x2(c);
+              x[i] -= f.x;
+              x[i + 1] -= f.y;
+              *reinterpret_cast<uint16_t*>(dst + i) = static_cast<uint16_t>(c);
+            }
+          }
+          // an infinite query has no finite score: its row becomes NaN
+          if (lane == 0)
+            sh->row_scale[buf][r] =
+                amax <= 3.4028234664e38f
+                    ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2
+                    : __int_as_float(0x7FFFFFFF);
+        }
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->q_full[buf]);
+      ++seg;
+    }
+    if (!ok && lane == 0) {
+      set_error(p.g.err, RIMURU_DEV_TIMEOUT);
+      sh->abort = 1;
+    }
   } else {
     // --------------------------------------------------------------- softmax
     const int quad = warp & 3;             // TMEM lanes this warp may read
     const int tok = quad * 32 + lane;      // token of the tile, and row of O^T
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    uint32_t tile = 0;
+    uint32_t tile = 0, seg = 0;
     // `ok`: this warp's waits came through; `all`: the four warps' did, as agreed
     // at the last barrier.  Only `all` leaves the loops, so no warp waits at a
     // barrier for one that has left.
     bool ok = true, all = true;
     while (all && walk.next(p, &g)) {
-      // Q of the segment, as parts; warp `quad` takes rows quad, quad + 4, ...
       const int rows = (g.i1 - g.i0) * p.group;
       const int pos0 = g.s.len - g.s.n + g.i0;  // position of the first query row
-      for (int r = quad; r < kR; r += 4) {
-        constexpr int kPer = kD / 32;
-        float x[kPer];
-        float amax = 0.f;
-        if (r < rows) {
-          const int64_t at = (g.s.row0 + g.i0 + r / p.group) * p.q_ts +
-                             (g.h * p.group + r % p.group) * p.q_hs + lane * kPer;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) x[i] = to_f(static_cast<const T*>(p.q)[at + i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) x[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, fabsf(x[i]));
-        amax = warp_max(amax);
-        // power of two that brings the row's largest magnitude into (224, 448]
-        const uint32_t ab = __float_as_uint(amax);
-        const int e = max(-100, min(100, static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u)));
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] *= inv;
-        const int d0 = lane * kPer, sl = d0 / kRowBytes;
-        uint8_t* dst = sQ + sl * kN * kRowBytes + swz<kRowBytes>(r, d0 % kRowBytes);
-#pragma unroll
-        for (int part = 0; part < kQParts; ++part) {
-#pragma unroll
-          for (int i = 0; i < kPer; i += 2) {
-            const uint32_t c = e4m3x2(x[i], x[i + 1]);
-            const float2 f = from_e4m3x2(c);
-            x[i] -= f.x;
-            x[i + 1] -= f.y;
-            *reinterpret_cast<uint16_t*>(dst + part * C::kQBytes + i) = static_cast<uint16_t>(c);
-          }
-        }
-        // an infinite query has no finite score: its row becomes NaN
-        if (lane == 0)
-          sh->row_scale[r] = amax <= 3.4028234664e38f
-                                 ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2
-                                 : __int_as_float(0x7FFFFFFF);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->q_full);
-      if (!(all = named_bar_and(ok))) break;
+      const int lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+      const uint32_t buf = seg & 1u;
+      ok = mbar_wait(&sh->q_full[buf], (seg >> 1) & 1u, abort);
+      ok = __all_sync(0xffffffffu, ok);
       float rs[kR], m[kR], l[kR], pa[kR], pb[kR], o[kSlabs][kR];
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
-        rs[r] = sh->row_scale[r];
+        rs[r] = sh->row_scale[buf][r];
         m[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
         for (int sl = 0; sl < kSlabs; ++sl) o[sl][r] = 0.f;
       }
-      // The token's page and scales, fetched a tile ahead.
-      const int lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
-      float k_next = 0.f, v_next = 0.f;
-      const auto fetch = [&](int t) {  // v_next 0: the token does not count
-        const int j = t * kTileTokens + tok;
-        k_next = v_next = 0.f;
-        if (j >= lo && j < g.s.len) {
-          const int page = p.s.table[g.b * p.s.table_stride + j / P];
-          if (page >= 0 && page < p.g.num_pages) {
-            const float* sc = p.g.scales + static_cast<int64_t>(page) * 2 * p.g.kv_heads + g.h;
-            k_next = sc[0];
-            v_next = sc[p.g.kv_heads];
-          }
-        }
-      };
       const auto take_output = [&](uint32_t i) {  // adds O^T of tile i, scaled by pa and pb
         tc_fence_after();
 #pragma unroll
         for (int sl = 0; sl < kSlabs; ++sl) {
-          uint32_t v[kR];
-          tmem_ld<kR>(tO + ((i & 1u) * kSlabs + sl) * kN + lane_off, v);
-          tmem_ld_wait();
+          float v[kR];
+          tmem_sum<kWeightParts, kR>(tO + ((i & 1u) * kSlabs + sl) * kNO + lane_off, v);
 #pragma unroll
-          for (int r = 0; r < kR; ++r) o[sl][r] = o[sl][r] * pa[r] + __uint_as_float(v[r]) * pb[r];
+          for (int r = 0; r < kR; ++r) o[sl][r] = o[sl][r] * pa[r] + v[r] * pb[r];
         }
         tc_fence_before();
       };
-      fetch(g.t0);
       for (int t = g.t0; t < g.t1; ++t, ++tile) {
-        const float ks = k_next, vs = v_next;
-        if (t + 1 < g.t1) fetch(t + 1);
+        ok = mbar_wait(&sh->meta_full[tile % kMetaRing], (tile / kMetaRing) & 1u, abort) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        const float2 kvs = sh->meta[tile % kMetaRing][tok >> log_p];
         const int j = t * kTileTokens + tok;
-        const bool live = vs != 0.f;
-        const float kv = static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
-        const float inv_v = live ? 1.f / vs : 0.f;
+        const bool live = kvs.y != 0.f && j >= lo && j < g.s.len;
+        const float kv = static_cast<float>(static_cast<int>(__float_as_uint(kvs.y) >> 23) - 127);
+        const float inv_v = live ? 1.f / kvs.y : 0.f;
         ok = mbar_wait(&sh->s_full[tile & 1u], (tile >> 1) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         float x[kR];
-        {
-          uint32_t v[kR];
-          tmem_ld<kR>(tS + (tile & 1u) * kN + lane_off, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int r = 0; r < kR; ++r) x[r] = __uint_as_float(v[r]) * (ks * rs[r]) + kv;
-        }
+        tmem_sum<kQParts, kR>(tS + (tile & 1u) * kNS + lane_off, x);
         tc_fence_before();
+#pragma unroll
+        for (int r = 0; r < kR; ++r) x[r] = x[r] * (kvs.x * rs[r]) + kv;
         // rows see j <= pos and j > pos - window; every row sees a tile inside both
         const bool inside = (t + 1) * kTileTokens <= pos0 + 1 &&
                             (p.window == 0 || t * kTileTokens > pos0 + g.i1 - g.i0 - 1 - p.window);
         if (!inside) {
+          int pos = pos0, of_group = 0;
 #pragma unroll
           for (int r = 0; r < kR; ++r) {
-            const int pos = pos0 + r / p.group;
             if (j > pos || (p.window > 0 && j <= pos - p.window)) x[r] = -INFINITY;
+            if (++of_group == p.group) of_group = 0, ++pos;
           }
         }
         float* mine = sh->tile_max[tile & 1u][quad];
@@ -424,7 +498,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
         // P of the tile before has been read, and its O is ready
         if (t > g.t0) {
           const uint32_t i = tile - 1;
-          ok = ok && mbar_wait(&sh->o_full[i & 1u], (i >> 1) & 1u, abort);
+          ok = mbar_wait(&sh->o_full[i & 1u], (i >> 1) & 1u, abort) && ok;
           ok = __all_sync(0xffffffffu, ok);
         }
         // tokens that do not count may hold anything: their rows of V become zero
@@ -432,7 +506,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
 #pragma unroll
           for (int sl = 0; sl < kSlabs; ++sl) {
             const uint32_t u = (2 * tile + 1) * kSlabs + sl, slot = u % kRing;
-            ok = ok && mbar_wait(&sh->full[slot], (u / kRing) & 1u, abort);
+            ok = mbar_wait(&sh->full[slot], (u / kRing) & 1u, abort) && ok;
             ok = __all_sync(0xffffffffu, ok);
             if (ok && !live) {
               uint4* row = reinterpret_cast<uint4*>(sRing + slot * C::kSlabBytes + tok * kRowBytes);
@@ -443,20 +517,32 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
         }
         if (!ok) sh->abort = 1;  // found at the next barrier; nothing below waits
         {
+          // the token's row of P: kNO bytes, part x row, in 16-byte chunks
           float y[kR];
+          uint32_t c[kNO / 4];
 #pragma unroll
           for (int r = 0; r < kR; ++r) y[r] = x[r];
 #pragma unroll
           for (int part = 0; part < kWeightParts; ++part) {
 #pragma unroll
-            for (int r = 0; r < kR; r += 2) {
-              const uint32_t c = e5m2x2(y[r], y[r + 1]);
-              const float2 f = from_e5m2x2(c);
-              y[r] -= f.x;
-              y[r + 1] -= f.y;
-              sP[part * C::kPBytes + swz<128>(r, tok)] = static_cast<uint8_t>(c);
-              sP[part * C::kPBytes + swz<128>(r + 1, tok)] = static_cast<uint8_t>(c >> 8);
+            for (int r = 0; r < kR; r += 4) {
+              const uint32_t lo2 = e5m2x2(y[r], y[r + 1]), hi2 = e5m2x2(y[r + 2], y[r + 3]);
+              c[(part * kR + r) / 4] = lo2 | hi2 << 16;
+              if (part + 1 < kWeightParts) {
+                const float2 f = from_e5m2x2(lo2), f2 = from_e5m2x2(hi2);
+                y[r] -= f.x;
+                y[r + 1] -= f.y;
+                y[r + 2] -= f2.x;
+                y[r + 3] -= f2.y;
+              }
             }
+          }
+          uint8_t* row = sP + tok * kNO;
+#pragma unroll
+          for (int i = 0; i < kNO / 16; ++i) {
+            const int at = kNO == 64 ? (i ^ (tok >> 1)) & 3 : (i ^ (tok >> 2)) & 1;
+            *reinterpret_cast<uint4*>(row + 16 * at) =
+                make_uint4(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]);
           }
         }
         fence_proxy_async_smem();
@@ -473,8 +559,9 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
         }
       }
       if (!all) break;
+      if (lane == 0) mbar_arrive(&sh->q_empty[buf]);  // S of the segment's last tile is complete
       const uint32_t i = tile - 1;
-      ok = mbar_wait(&sh->o_full[i & 1u], (i >> 1) & 1u, abort);
+      ok = mbar_wait(&sh->o_full[i & 1u], (i >> 1) & 1u, abort) && ok;
       ok = __all_sync(0xffffffffu, ok);
       take_output(i);
       // row sums over the tile's tokens, then the rows
@@ -486,37 +573,46 @@ __global__ void __launch_bounds__(kDecodeThreads, kD <= 128 ? 2 : 1)
       }
       if (!(all = named_bar_and(ok))) break;
       const bool whole = g.starts && g.ends;
-      float* part = part_slot(p, blockIdx.x, g.starts);
+      // lane r finishes the statistics of row r
+      float sum = 0.f, mr = 0.f;
+      if (lane < kR)
+        sum = (sh->row_sum[0][lane] + sh->row_sum[1][lane]) + (sh->row_sum[2][lane] + sh->row_sum[3][lane]);
 #pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        if (r >= rows) break;
-        const float sum = (sh->row_sum[0][r] + sh->row_sum[1][r]) + (sh->row_sum[2][r] + sh->row_sum[3][r]);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const float stat = sum > 0.f ? m[r] - kWeightTop + log2f(sum) : -INFINITY;
-        const int row = g.s.row0 + g.i0 + r / p.group, head = g.h * p.group + r % p.group;
+      for (int r = 0; r < kR; ++r) mr = lane == r ? m[r] : mr;
+      const float inv = sum > 0.f ? 1.f / sum : sum;  // 0 for a row that sees nothing; NaN stays
+      const float stat = sum > 0.f ? mr - kWeightTop + __log2f(sum) : sum == 0.f ? -INFINITY : sum;
+      const int64_t slot = part_slot(p, blockIdx.x, g.starts);
+      const bool has_d = kRowBytes == 128 || tok < kRowBytes;  // head_dim 64: lanes past the head
+      if (whole) {
+        const int row = g.s.row0 + g.i0, head = g.h * p.group;
+        T* dst = static_cast<T*>(p.out) + row * p.o_ts + head * p.o_hs + tok;
+        int of_group = 0;
 #pragma unroll
-        for (int sl = 0; sl < kSlabs; ++sl) {
-          const int d = sl * kRowBytes + tok;
-          if (kRowBytes < 128 && tok >= kRowBytes) continue;  // head_dim 64: lanes past the head
-          if (whole) from_f(o[sl][r] * inv, static_cast<T*>(p.out) + row * p.o_ts + head * p.o_hs + d);
-          else part[r * (kD + 1) + d] = o[sl][r] * inv;
+        for (int r = 0; r < kR; ++r) {
+          const float f = __shfl_sync(0xffffffffu, inv, r);
+          if (r >= rows) break;
+#pragma unroll
+          for (int sl = 0; sl < kSlabs; ++sl)
+            if (has_d) from_f(o[sl][r] * f, dst + sl * kRowBytes);
+          dst += p.o_hs;
+          if (++of_group == p.group) of_group = 0, dst += p.o_ts - p.group * p.o_hs;
         }
-        if (tok == 0) {
-          if (!whole) part[r * (kD + 1) + kD] = stat;
-          else if (p.lse) p.lse[static_cast<int64_t>(row) * p.q_heads + head] = stat * kLn2;
+        if (p.lse && quad == 0 && lane < rows)
+          p.lse[static_cast<int64_t>(row + lane / p.group) * p.q_heads + head + lane % p.group] = stat * kLn2;
+      } else {
+        float* dst = p.part + slot * kD + tok;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          const float f = __shfl_sync(0xffffffffu, inv, r);
+          if (r >= rows) break;
+#pragma unroll
+          for (int sl = 0; sl < kSlabs; ++sl)
+            if (has_d) dst[r * kD + sl * kRowBytes] = o[sl][r] * f;
         }
+        if (quad == 0 && lane < rows) p.stat[slot + lane] = stat;
       }
-      if (g.starts && tok == 0) {
-        int2 j = make_int2(-1, -1);
-        if (!whole) {
-          const TileSpan sp = unit_span(p, g.s, g.w);
-          // the unit's tiles are contiguous in the total; this run holds the first of them
-          const int64_t first = sh->run.begin + (sh->run.tiles - walk.left) - (g.t1 - g.t0);
-          j = make_int2(blockIdx.x, run_of(sh->run.total, sh->run.runs, first + (sp.last - sp.first) - 1));
-        }
-        *join_of(p, g.b, g.h, g.w) = j;
-      }
-      if (!(all = named_bar_and(ok))) break;  // row_sum and row_scale are free again
+      if (g.starts && tok == 0) note_join(p, g, sh->run.cut, blockIdx.x);
+      ++seg;
     }
     if (!all && lane == 0) {
       set_error(p.g.err, RIMURU_DEV_TIMEOUT);
@@ -561,76 +657,120 @@ cudaError_t launch_dim(const AttnArgs& a, const CUtensorMap& tm, cudaStream_t s)
 }
 
 // ---------------------------------------------------------------------- join
-// One CTA per (unit, query row x group): adds the runs' partial rows, weighted
-// by their share of the softmax sum, in run order.  Rows of sequences without
-// any tile become zero here.
-template <typename T>
-__global__ void __launch_bounds__(128) kv_join_kernel(const __grid_constant__ AttnArgs p) {
-  const int r = blockIdx.y, w = blockIdx.x % p.units_per_pair;
-  const int pair = blockIdx.x / p.units_per_pair, b = pair / p.g.kv_heads, h = pair % p.g.kv_heads;
+// Adds the runs' partial rows, weighted by their share of the softmax sum, in
+// run order.  Rows of units without any tile become zero here.  A CTA takes
+// kRows rows of a unit; its warps split the rows, or with one row the runs
+// (few units cut into many runs: a long context), whose sums meet in shared
+// memory in warp order.
+constexpr int kJoinWarps = 8;
+
+template <typename T, int kD, bool kSplitRuns>
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ AttnArgs p) {
+  constexpr int kPer = kD / 32;
+  __shared__ float sums[kJoinWarps][kD];
+  __shared__ float weight[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = p.units_per_pair == 1 ? 0 : blockIdx.x % p.units_per_pair;
+  const int pair = p.units_per_pair == 1 ? blockIdx.x : blockIdx.x / p.units_per_pair;
+  const int b = pair / p.g.kv_heads, h = pair - b * p.g.kv_heads;
   grid_dep_wait();
-  const int D = p.g.head_dim;
-  int row0 = p.s.cu ? p.s.cu[b] : b;
-  int n = p.s.cu ? p.s.cu[b + 1] - row0 : 1;
   const SeqShape s = seq_shape(p, b);
+  int row0 = s.row0, n = s.n;
   if (!s.ok) {  // inconsistent arguments: zero what of its rows lies inside the arrays
-    n = min(min(n, p.max_q), p.s.rows - row0);
-    if (row0 < 0) n = 0;
+    n = p.s.cu ? p.s.cu[b + 1] - row0 : 1;
+    n = row0 < 0 ? 0 : min(min(n, p.max_q), p.s.rows - row0);
   }
-  const int per = p.unit_rows / p.group, i = w * per + r / p.group;
-  if (r >= per * p.group || i >= n) return;
-  const int row = row0 + i, head = h * p.group + r % p.group;
-  T* out = static_cast<T*>(p.out) + row * p.o_ts + head * p.o_hs;
-  float* lse = p.lse ? p.lse + static_cast<int64_t>(row) * p.q_heads + head : nullptr;
+  const int i0 = w * p.unit_q, rows = (min(n, i0 + p.unit_q) - i0) * p.group;
+  if (rows <= 0) return;
   TileSpan t{0, 0};
   if (s.ok) t = unit_span(p, s, w);
-  if (t.first >= t.last) {
-    for (int d = threadIdx.x; d < D; d += blockDim.x) from_f(0.f, out + d);
-    if (lse && threadIdx.x == 0) *lse = -INFINITY;
-    return;
-  }
-  const int2 j = *join_of(p, b, h, w);
+  const bool none = t.first >= t.last;
+  const int2 j = none ? make_int2(0, -1) : *join_of(p, b, h, w);
   if (j.x < 0) return;  // finished by one run
-  float top = -INFINITY;
-  const auto slot = [&](int c) { return part_slot(p, c, c == j.x) + static_cast<int64_t>(r) * (D + 1); };
-  for (int c = j.x; c <= j.y; ++c) top = fmaxf(top, slot(c)[D]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc[2] = {0.f, 0.f};
+  const int r0 = kSplitRuns ? blockIdx.y : warp, step = kSplitRuns ? p.unit_rows : kJoinWarps;
+  for (int r = r0; r < rows; r += step) {
+    const auto slot = [&](int c) { return part_slot(p, c, c == j.x) + r; };
+    float top = -INFINITY, sum = 0.f, acc[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    for (int c = j.x + lane; c <= j.y; c += 32) top = fmaxf(top, p.stat[slot(c)]);
+    top = warp_max(top);
+    const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
-  for (int c = j.x; c <= j.y; ++c) {
-    const float* q = slot(c);
-    const float e = ex2(q[D] - ref);
-    sum += e;
-    if (threadIdx.x < D) acc[0] += e * q[threadIdx.x];
-    if (threadIdx.x + 128 < D) acc[1] += e * q[threadIdx.x + 128];
+    for (int c = j.x + (kSplitRuns ? warp : 0); c <= j.y; c += kSplitRuns ? kJoinWarps : 1) {
+      const float e = ex2(p.stat[slot(c)] - ref);
+      const float* q = p.part + slot(c) * kD + lane * kPer;
+      sum += e;
+      float v[kPer];
+      if constexpr (kPer >= 4) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(q + i);
+      } else {
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(q);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] += e * v[i];
+    }
+    if (kSplitRuns) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sums[warp][lane * kPer + i] = acc[i];
+      if (lane == 0) weight[warp] = sum;
+      __syncthreads();
+      if (warp != 0) return;
+#pragma unroll
+      for (int k = 1; k < kJoinWarps; ++k) {
+        sum += weight[k];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] += sums[k][lane * kPer + i];
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : sum;
+    const int i = r / p.group, head = h * p.group + r - i * p.group;
+    T v[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) from_f(acc[k] * inv, v + k);
+    T* out = static_cast<T*>(p.out) + (row0 + i0 + i) * p.o_ts + head * p.o_hs + lane * kPer;
+    if constexpr (kPer == 8) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<uint4*>(v);
+    else if constexpr (kPer == 4) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<uint2*>(v);
+    else *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<uint32_t*>(v);
+    if (p.lse && lane == 0)
+      p.lse[static_cast<int64_t>(row0 + i0 + i) * p.q_heads + head] =
+          sum > 0.f ? (ref + __log2f(sum)) * kLn2 : sum == 0.f ? -INFINITY : sum;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (threadIdx.x < D) from_f(acc[0] * inv, out + threadIdx.x);
-  if (threadIdx.x + 128 < D) from_f(acc[1] * inv, out + threadIdx.x + 128);
-  if (lse && threadIdx.x == 0) *lse = sum > 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-}  // namespace
-
-int kv_decode_runs(int sms, int head_dim) { return sms * (head_dim <= 128 ? 2 : 1); }
-
-cudaError_t launch_kv_decode(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s) {
-  return dtype == RIMURU_BF16 ? launch_dim<__nv_bfloat16>(a, tm, s) : launch_dim<__half>(a, tm, s);
-}
-
-cudaError_t launch_kv_join(const AttnArgs& a, int dtype, cudaStream_t s) {
+template <typename T>
+cudaError_t launch_join(const AttnArgs& a, cudaStream_t s) {
+  const int64_t units = static_cast<int64_t>(a.s.num_seqs) * a.g.kv_heads * a.units_per_pair;
+  // With four runs a unit or more, one CTA per row whose warps split the runs.
+  const bool split = units * 4 <= a.runs;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.s.num_seqs * a.g.kv_heads * a.units_per_pair),
-                     static_cast<unsigned>(a.unit_rows));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(units), split ? static_cast<unsigned>(a.unit_rows) : 1u);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return dtype == RIMURU_BF16 ? cudaLaunchKernelEx(&cfg, kv_join_kernel<__nv_bfloat16>, a)
-                              : cudaLaunchKernelEx(&cfg, kv_join_kernel<__half>, a);
+  const auto go = [&](auto kernel_split, auto kernel_rows) {
+    return split ? cudaLaunchKernelEx(&cfg, kernel_split, a) : cudaLaunchKernelEx(&cfg, kernel_rows, a);
+  };
+  if (a.g.head_dim == 64) return go(kv_join_kernel<T, 64, true>, kv_join_kernel<T, 64, false>);
+  if (a.g.head_dim == 128) return go(kv_join_kernel<T, 128, true>, kv_join_kernel<T, 128, false>);
+  return go(kv_join_kernel<T, 256, true>, kv_join_kernel<T, 256, false>);
+}
+
+}  // namespace
+
+int kv_decode_runs(int sms, int head_dim, int rows) { return sms * decode_ctas(head_dim, rows); }
+
+cudaError_t launch_kv_decode(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s) {
+  return dtype == RIMURU_BF16 ? launch_dim<__nv_bfloat16>(a, tm, s) : launch_dim<__half>(a, tm, s);
+}
+
+cudaError_t launch_kv_join(const AttnArgs& a, int dtype, cudaStream_t s) {
+  return dtype == RIMURU_BF16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<__half>(a, s);
 }
 
 }  // namespace rimuru
