@@ -6,20 +6,22 @@
 // swizzled shared memory, and tcgen05 multiplies them as the M = 128 operand,
 //   S^T [tokens x rows] = K Q^T,     O^T [head_dim x rows] = V^T P,
 // so nothing is ever widened.  The few-row operands Q and P are 16-bit or fp32
-// quantities: each is written as a sum of 8-bit floats (rounded, then the rest
-// rounded, ...) and the parts are multiplied one after another into the same
-// fp32 accumulator.  Q takes e4m3 parts, 4 significant bits each: two hold a
-// bf16 query exactly, three an f16 query.  P takes four e5m2 parts, 12 bits;
-// e5m2 spans 2^-16 .. 2^15, so a weight is kept down to 2^-32 of the largest
-// (three e4m3 parts flushed below 2^-18, which showed in output elements whose
-// heaviest tokens have a V near zero).
+// quantities: each is written as a sum of 8-bit floats and the products of the
+// parts are added.  Q takes e4m3 parts (rounded, then the rest rounded), 4
+// significant bits each: two hold a bf16 query exactly, three an f16 query.  P
+// is rounded to f16 and cut into four e5m2 parts, which is exact: an e5m2 number
+// is the upper byte of an f16 one, so a part is that byte and the rest an exact
+// f16 difference.  Weights are kept down to 2^-27 of the reference (three e4m3
+// parts flushed below 2^-18, which showed in output elements whose heaviest
+// tokens have a V near zero).
 //
 // Softmax: thread = token.  The V scale of a token is a power of two 2^k and is
 // added to its score, x + k, so the weight that meets the code of V is
-// 2^(x + k - m) with m the tile's largest x + k: at most one whatever the
-// scales, and the row sum takes 2^(x - m) by an exact multiplication.  Weights
-// are relative to the tile's own maximum, so no accumulator is ever rescaled:
-// tiles are joined in fp32 registers.
+// 2^(x + k - ref), bounded whatever the scales, and the row sum takes 2^(x - ref)
+// by an exact multiplication.  ref follows the largest x + k seen, but only once
+// a token passes it by more than 2^4: until then O stays in TMEM and adds up
+// there, and a tile costs its barrier one predicate.  When ref moves, O is
+// brought into registers, rescaled, and TMEM starts afresh.
 //
 // The parts of Q and of P lie side by side as columns of one MMA (8 rows: N = 16
 // or 32), so each byte of K and V is read from shared memory once, and are
@@ -42,7 +44,9 @@ using namespace dev;
 
 constexpr int kDecodeThreads = 224;
 constexpr int kWeightParts = 4;
-constexpr float kWeightTop = 15.f;  // weights are scaled by 2^15: e5m2 ends at 1.75 * 2^15
+constexpr float kWeightTop = 11.f;   // a weight at the reference is 2^11
+constexpr float kWeightSlack = 4.f;  // and may pass it by 2^4: f16 ends at 2^16
+constexpr float kNoRef = -1e30f;     // the reference of a row that has seen no key
 constexpr int kMetaRing = 8;
 
 constexpr int decode_ctas(int head_dim, int rows) { return head_dim <= 128 && rows <= 8 ? 2 : 1; }
@@ -53,28 +57,29 @@ struct DecodeCfg {
   static constexpr int kSlabs = kD / kRowBytes;           // slabs of a K or V tile
   static constexpr int kSlabBytes = kTileTokens * kRowBytes;
   static constexpr int kCtas = decode_ctas(kD, kR);  // per SM
-  static constexpr int kRing = kCtas == 1 ? 12 : kD == 64 ? 10 : 6;  // slabs
+  static constexpr int kRing = kCtas == 1 ? (kR == 8 ? 12 : 10) : kD == 64 ? 10 : 6;  // slabs
   static constexpr int kNS = (kQParts * kR + 15) / 16 * 16;  // columns of S: part x row
   static constexpr int kNO = kWeightParts * kR;              // columns of O
   static constexpr int kQBytes = kNS * kD;  // Q: kSlabs x [kNS][kRowBytes]
   static constexpr int kPBytes = kNO * 128;  // P: [128 tokens][kNO]
-  static constexpr int kTmem = 2 * kNS + 2 * kSlabs * kNO;  // S twice, O twice
+  static constexpr int kTmem = 2 * kNS + kSlabs * kNO;  // S twice, O
   static constexpr int kTmemCols = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
-  static constexpr int kSmem = 1024 + kRing * kSlabBytes + 2 * kQBytes + kPBytes;
+  static constexpr int kSmem = 1024 + kRing * kSlabBytes + 2 * kQBytes + 2 * kPBytes;
 };
 
 struct DecodeShared {
   uint64_t full[12], empty[12];
   uint64_t meta_full[kMetaRing];
-  uint64_t q_full[2], q_empty[2], p_full;
+  uint64_t q_full[2], q_empty[2], p_full[2];
   uint64_t s_full[2], o_full[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  int fresh[2];  // the tile's O starts afresh
   RunStart run;
   int scratch[8];
   float2 meta[kMetaRing][8];  // per page of a tile: scales of K and V; V 0: no such page
-  float tile_max[2][4][kDecodeMaxRows];
+  float tile_max[4][kDecodeMaxRows];
   float row_scale[2][kDecodeMaxRows];
   float row_sum[4][kDecodeMaxRows];
 };
@@ -96,13 +101,18 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
 }
-// The same in e5m2, whose codes are the upper halves of f16 numbers.
-__device__ __forceinline__ uint32_t e5m2x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
-}
-__device__ __forceinline__ float2 from_e5m2x2(uint32_t c) {
-  const uint32_t h = __byte_perm(c, 0, 0x1404);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// 1 when the predicate holds in any of the 128 softmax threads (barrier 1).
+__device__ __forceinline__ bool named_bar_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "bar.red.or.pred b, 1, 128, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}\n"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -159,8 +169,8 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
       mbar_init(&sh->empty[i], 1);
     }
     for (int i = 0; i < kMetaRing; ++i) mbar_init(&sh->meta_full[i], 1);
-    mbar_init(&sh->p_full, 4);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->p_full[i], 4);
       mbar_init(&sh->q_full[i], 1);
       mbar_init(&sh->q_empty[i], 4);
       mbar_init(&sh->s_full[i], 1);
@@ -288,7 +298,8 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
         return true;
       };
       const auto outputs = [&](uint32_t i) {  // O^T of the run's tile i
-        if (!mbar_wait(&sh->p_full, i & 1u, abort)) return false;
+        if (!mbar_wait(&sh->p_full[i & 1u], (i >> 1) & 1u, abort)) return false;
+        const uint32_t keep = sh->fresh[i & 1u] ? 0u : 1u;
 #pragma unroll
         for (int sl = 0; sl < kSlabs; ++sl) {
           const uint32_t u = (2 * i + 1) * kSlabs + sl, slot = u % kRing;
@@ -297,10 +308,11 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
           const uint32_t a0 = smem_u32(sRing + slot * C::kSlabBytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 tokens: four groups of eight rows
-            umma_f8(tO + ((i & 1u) * kSlabs + sl) * kNO,
+            umma_f8(tO + sl * kNO,
                     smem_desc(a0 + 4 * k * kAtom, C::kSlabBytes, kAtom, kSwizzle),
-                    smem_desc(smem_u32(sP) + 32 * k * kNO, C::kPBytes, 8 * kNO, kNO == 64 ? 4 : 6), id_o,
-                    k != 0 ? 1u : 0u);
+                    smem_desc(smem_u32(sP + (i & 1u) * C::kPBytes) + 32 * k * kNO, C::kPBytes, 8 * kNO,
+                              kNO == 64 ? 4 : 6),
+                    id_o, k != 0 ? 1u : keep);
           umma_commit(&sh->empty[slot]);
         }
         umma_commit(&sh->o_full[i & 1u]);
@@ -432,23 +444,24 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
       const uint32_t buf = seg & 1u;
       ok = mbar_wait(&sh->q_full[buf], (seg >> 1) & 1u, abort);
       ok = __all_sync(0xffffffffu, ok);
-      float rs[kR], m[kR], l[kR], pa[kR], pb[kR], o[kSlabs][kR];
+      // A weight is 2^(x + add) with add = kWeightTop - ref.
+      float rs[kR], ref[kR], l[kR], o[kSlabs][kR];
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         rs[r] = sh->row_scale[buf][r];
-        m[r] = -INFINITY;
+        ref[r] = kNoRef;
         l[r] = 0.f;
 #pragma unroll
         for (int sl = 0; sl < kSlabs; ++sl) o[sl][r] = 0.f;
       }
-      const auto take_output = [&](uint32_t i) {  // adds O^T of tile i, scaled by pa and pb
+      const auto add_output = [&]() {  // O of the tiles so far, out of TMEM
         tc_fence_after();
 #pragma unroll
         for (int sl = 0; sl < kSlabs; ++sl) {
           float v[kR];
-          tmem_sum<kWeightParts, kR>(tO + ((i & 1u) * kSlabs + sl) * kNO + lane_off, v);
+          tmem_sum<kWeightParts, kR>(tO + sl * kNO + lane_off, v);
 #pragma unroll
-          for (int r = 0; r < kR; ++r) o[sl][r] = o[sl][r] * pa[r] + v[r] * pb[r];
+          for (int r = 0; r < kR; ++r) o[sl][r] += v[r];
         }
         tc_fence_before();
       };
@@ -458,8 +471,9 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
         const float2 kvs = sh->meta[tile % kMetaRing][tok >> log_p];
         const int j = t * kTileTokens + tok;
         const bool live = kvs.y != 0.f && j >= lo && j < g.s.len;
-        const float kv = static_cast<float>(static_cast<int>(__float_as_uint(kvs.y) >> 23) - 127);
-        const float inv_v = live ? 1.f / kvs.y : 0.f;
+        const int ke = static_cast<int>(__float_as_uint(kvs.y) >> 23);  // V scale = 2^(ke - 127)
+        const float kv = static_cast<float>(ke - 127);
+        const float inv_v = __uint_as_float(static_cast<uint32_t>(254 - ke) << 23);
         ok = mbar_wait(&sh->s_full[tile & 1u], (tile >> 1) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
@@ -467,7 +481,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
         tmem_sum<kQParts, kR>(tS + (tile & 1u) * kNS + lane_off, x);
         tc_fence_before();
 #pragma unroll
-        for (int r = 0; r < kR; ++r) x[r] = x[r] * (kvs.x * rs[r]) + kv;
+        for (int r = 0; r < kR; ++r) x[r] = live ? x[r] * (kvs.x * rs[r]) + kv : -INFINITY;
         // rows see j <= pos and j > pos - window; every row sees a tile inside both
         const bool inside = (t + 1) * kTileTokens <= pos0 + 1 &&
                             (p.window == 0 || t * kTileTokens > pos0 + g.i1 - g.i0 - 1 - p.window);
@@ -479,26 +493,47 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
             if (++of_group == p.group) of_group = 0, ++pos;
           }
         }
-        float* mine = sh->tile_max[tile & 1u][quad];
+        bool raise = !ok;  // a wait that gave up is settled where the reference moves
+#pragma unroll
+        for (int r = 0; r < kR; ++r) raise |= x[r] > ref[r] + kWeightSlack;
+        if (named_bar_or(raise)) {
+          float top[kR];
+#pragma unroll
+          for (int r = 0; r < kR; ++r) top[r] = warp_max(x[r]);
+          if (lane == 0) {
+#pragma unroll
+            for (int r = 0; r < kR; r += 4)
+              *reinterpret_cast<float4*>(&sh->tile_max[quad][r]) =
+                  make_float4(top[r], top[r + 1], top[r + 2], top[r + 3]);
+          }
+          if (!(all = named_bar_and(ok))) break;
+          if (t > g.t0) {  // every O MMA so far is done
+            ok = mbar_wait(&sh->o_full[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            add_output();
+          }
+#pragma unroll
+          for (int r = 0; r < kR; ++r) {
+            const float now = fmaxf(fmaxf(fmaxf(sh->tile_max[0][r], sh->tile_max[1][r]),
+                                          fmaxf(sh->tile_max[2][r], sh->tile_max[3][r])),
+                                    ref[r]);
+            const float f = ex2(ref[r] - now);
+            ref[r] = now;
+            l[r] *= f;
+#pragma unroll
+            for (int sl = 0; sl < kSlabs; ++sl) o[sl][r] *= f;
+          }
+          if (tok == 0) sh->fresh[tile & 1u] = 1;
+        } else if (tok == 0) {
+          sh->fresh[tile & 1u] = t == g.t0;
+        }
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-          if (!live) x[r] = -INFINITY;
-          const float w = warp_max(x[r]);
-          if (lane == 0) mine[r] = w;
+          x[r] = ex2(x[r] + (kWeightTop - ref[r]));
+          l[r] += x[r] * inv_v;
         }
-        // a wait that gave up in any warp, here or since the last barrier, ends all four
-        if (!(all = named_bar_and(ok))) break;
-        float mt[kR];
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          mt[r] = fmaxf(fmaxf(sh->tile_max[tile & 1u][0][r], sh->tile_max[tile & 1u][1][r]),
-                        fmaxf(sh->tile_max[tile & 1u][2][r], sh->tile_max[tile & 1u][3][r]));
-          x[r] = ex2(x[r] - (mt[r] == -INFINITY ? 0.f : mt[r]) + kWeightTop);
-        }
-        // P of the tile before has been read, and its O is ready
-        if (t > g.t0) {
-          const uint32_t i = tile - 1;
-          ok = mbar_wait(&sh->o_full[i & 1u], (i >> 1) & 1u, abort) && ok;
+        if (t > g.t0 + 1) {  // the weights two tiles back have been read
+          ok = mbar_wait(&sh->o_full[tile & 1u], ((tile - 2) >> 1) & 1u, abort) && ok;
           ok = __all_sync(0xffffffffu, ok);
         }
         // tokens that do not count may hold anything: their rows of V become zero
@@ -518,26 +553,25 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
         if (!ok) sh->abort = 1;  // found at the next barrier; nothing below waits
         {
           // the token's row of P: kNO bytes, part x row, in 16-byte chunks
-          float y[kR];
           uint32_t c[kNO / 4];
+          __half2 y[kR / 2];
 #pragma unroll
-          for (int r = 0; r < kR; ++r) y[r] = x[r];
+          for (int r = 0; r < kR / 2; ++r) y[r] = __floats2half2_rn(x[2 * r], x[2 * r + 1]);
 #pragma unroll
           for (int part = 0; part < kWeightParts; ++part) {
 #pragma unroll
-            for (int r = 0; r < kR; r += 4) {
-              const uint32_t lo2 = e5m2x2(y[r], y[r + 1]), hi2 = e5m2x2(y[r + 2], y[r + 3]);
-              c[(part * kR + r) / 4] = lo2 | hi2 << 16;
+            for (int r = 0; r < kR / 2; r += 2) {
+              const uint32_t a = *reinterpret_cast<const uint32_t*>(&y[r]);
+              const uint32_t b = *reinterpret_cast<const uint32_t*>(&y[r + 1]);
+              c[(part * kR + 2 * r) / 4] = __byte_perm(a, b, 0x7531);
               if (part + 1 < kWeightParts) {
-                const float2 f = from_e5m2x2(lo2), f2 = from_e5m2x2(hi2);
-                y[r] -= f.x;
-                y[r + 1] -= f.y;
-                y[r + 2] -= f2.x;
-                y[r + 3] -= f2.y;
+                const uint32_t ah = a & 0xFF00FF00u, bh = b & 0xFF00FF00u;
+                y[r] = __hsub2(y[r], *reinterpret_cast<const __half2*>(&ah));
+                y[r + 1] = __hsub2(y[r + 1], *reinterpret_cast<const __half2*>(&bh));
               }
             }
           }
-          uint8_t* row = sP + tok * kNO;
+          uint8_t* row = sP + (tile & 1u) * C::kPBytes + tok * kNO;
 #pragma unroll
           for (int i = 0; i < kNO / 16; ++i) {
             const int at = kNO == 64 ? (i ^ (tok >> 1)) & 3 : (i ^ (tok >> 2)) & 1;
@@ -547,30 +581,31 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full);
-        if (t > g.t0) take_output(tile - 1);
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          const float mn = fmaxf(m[r], mt[r]), ref = mn == -INFINITY ? 0.f : mn;
-          pa[r] = ex2(m[r] - ref);
-          pb[r] = ex2(mt[r] - ref);
-          m[r] = mn;
-          l[r] = l[r] * pa[r] + (x[r] * inv_v) * pb[r];
-        }
+        if (lane == 0) mbar_arrive(&sh->p_full[tile & 1u]);
       }
       if (!all) break;
       if (lane == 0) mbar_arrive(&sh->q_empty[buf]);  // S of the segment's last tile is complete
+      // Row sums over the tokens: each exchange halves the rows a lane holds, so
+      // lane bits 4, 3, (2, 1) name its row in the end.
+#pragma unroll
+      for (int n = kR / 2, bit = 16; bit > 0; n /= 2, bit /= 2) {
+        if (n >= 1) {
+#pragma unroll
+          for (int r = 0; r < (n >= 1 ? n : 1); ++r) {
+            const bool up = lane & bit;
+            const float give = up ? l[r] : l[r + n];
+            l[r] = (up ? l[r + n] : l[r]) + __shfl_xor_sync(0xffffffffu, give, bit);
+          }
+        } else {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], bit);
+        }
+      }
+      constexpr int kLanesPerRow = 32 / kR;
+      if (lane % kLanesPerRow == 0) sh->row_sum[quad][lane / kLanesPerRow] = l[0];
       const uint32_t i = tile - 1;
       ok = mbar_wait(&sh->o_full[i & 1u], (i >> 1) & 1u, abort) && ok;
       ok = __all_sync(0xffffffffu, ok);
-      take_output(i);
-      // row sums over the tile's tokens, then the rows
-#pragma unroll
-      for (int r = 0; r < kR; ++r) {
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
-        if (lane == 0) sh->row_sum[quad][r] = l[r];
-      }
+      add_output();
       if (!(all = named_bar_and(ok))) break;
       const bool whole = g.starts && g.ends;
       // lane r finishes the statistics of row r
@@ -578,7 +613,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
       if (lane < kR)
         sum = (sh->row_sum[0][lane] + sh->row_sum[1][lane]) + (sh->row_sum[2][lane] + sh->row_sum[3][lane]);
 #pragma unroll
-      for (int r = 0; r < kR; ++r) mr = lane == r ? m[r] : mr;
+      for (int r = 0; r < kR; ++r) mr = lane == r ? ref[r] : mr;
       const float inv = sum > 0.f ? 1.f / sum : sum;  // 0 for a row that sees nothing; NaN stays
       const float stat = sum > 0.f ? mr - kWeightTop + __log2f(sum) : sum == 0.f ? -INFINITY : sum;
       const int64_t slot = part_slot(p, blockIdx.x, g.starts);
