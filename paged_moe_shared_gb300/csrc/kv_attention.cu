@@ -1,6 +1,4 @@
 // Attention over the 8-bit paged cache.
-#include <cuda_fp8.h>
-
 #include <algorithm>
 #include <cmath>
 #include <limits>
@@ -8,96 +6,9 @@
 #include "kv_attn.h"
 
 namespace rimuru {
-namespace {
-
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(float x, __half* y) { *y = __float2half_rn(x); }
-
-__device__ __forceinline__ float code_to_f(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
-// Simple form: one warp per (query row, head) walks the keys one at a time.
-template <typename T, int kD>
-__global__ void __launch_bounds__(128) kv_attention_rows_kernel(const __grid_constant__ AttnArgs p) {
-  constexpr int kPer = kD / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * 4ll + (threadIdx.x >> 5);
-  const int row = static_cast<int>(w / p.q_heads), h = static_cast<int>(w % p.q_heads);
-  if (row >= p.s.rows) return;
-  int b = row, first = row, n = 1;
-  if (p.s.cu) {
-    int lo = 0, hi = p.s.num_seqs;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (row < p.s.cu[mid + 1]) hi = mid;
-      else lo = mid + 1;
-    }
-    b = lo;
-    if (b >= p.s.num_seqs) return;
-    first = p.s.cu[b];
-    n = p.s.cu[b + 1] - first;
-  }
-  const int P = p.g.page_tokens;
-  int len = p.s.lens[b];
-  if (len < 0 || len > p.s.table_stride * P) {
-    if (lane == 0) dev::set_error(p.g.err, RIMURU_DEV_BAD_SHAPE);
-    len = 0;
-  }
-  const int pos = len - n + (row - first);
-  const int j1 = min(len, pos + 1), j0 = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  const int kvh = h / p.group;
-  float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = to_f(static_cast<const T*>(p.q)[row * p.q_ts + h * p.q_hs + lane * kPer + i]) * p.scale_log2;
-    o[i] = 0.f;
-  }
-  for (int j = j0; j < j1; ++j) {
-    const int page = p.s.table[b * p.s.table_stride + j / P];
-    if (page < 0 || page >= p.g.num_pages) {
-      if (lane == 0) dev::set_error(p.g.err, RIMURU_DEV_BAD_PAGE);
-      continue;
-    }
-    const uint8_t* kp = p.g.pool + page * p.g.page_bytes + (static_cast<uint64_t>(kvh) * P + j % P) * kD;
-    const uint8_t* vp = kp + static_cast<uint64_t>(p.g.kv_heads) * P * kD;
-    const float* sc = p.g.scales + static_cast<int64_t>(page) * 2 * p.g.kv_heads + kvh;
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) x += q[i] * code_to_f(kp[lane * kPer + i]);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    x *= sc[0];
-    const float m2 = fmaxf(m, x), a = exp2f(m - m2), e = exp2f(x - m2);
-    m = m2;
-    l = l * a + e;
-    const float ev = e * sc[p.g.kv_heads];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = o[i] * a + ev * code_to_f(vp[lane * kPer + i]);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    from_f(o[i] * inv, static_cast<T*>(p.out) + row * p.o_ts + h * p.o_hs + lane * kPer + i);
-  if (p.lse && lane == 0)
-    p.lse[static_cast<int64_t>(row) * p.q_heads + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
-template <typename T>
-cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.s.rows) * a.q_heads + 3) / 4);
-  if (a.g.head_dim == 64) kv_attention_rows_kernel<T, 64><<<grid, 128, 0, s>>>(a);
-  else if (a.g.head_dim == 128) kv_attention_rows_kernel<T, 128><<<grid, 128, 0, s>>>(a);
-  else kv_attention_rows_kernel<T, 256><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
 // How a call is cut: rows and number of units, and the workspace's two regions.
 struct AttnSplit {
+  bool decode;
   int unit_rows, units_per_pair;
   uint64_t join_bytes, part_bytes;
 };
@@ -105,11 +16,15 @@ AttnSplit split_of(const View& v, int q_heads, int num_seqs, int max_q) {
   const int group = q_heads / v.kv_heads;
   AttnSplit w{};
   const int64_t rows = static_cast<int64_t>(max_q) * group;
-  w.unit_rows = rows <= 8 ? 8 : kDecodeMaxRows;
-  w.units_per_pair = 1;
+  // Up to 16 rows take the decode kernel.  Beyond, a unit is 128 rows, or 256 where two query
+  // tiles fit the tensor memory and there are rows for them.
+  w.decode = rows <= kDecodeMaxRows;
+  w.unit_rows = rows <= 8 ? 8 : rows <= kDecodeMaxRows ? 16 : rows <= 128 ? 128 : tile_rows(v.head_dim);
+  const int unit_q = std::max(1, w.unit_rows / group);
+  w.units_per_pair = std::max(1, (max_q + unit_q - 1) / unit_q);
   const uint64_t units = static_cast<uint64_t>(num_seqs) * v.kv_heads * w.units_per_pair;
   w.join_bytes = (units * sizeof(int2) + 1023) / 1024 * 1024;
-  w.part_bytes = 2ull * kMaxRuns * w.unit_rows * (v.head_dim + 1) * sizeof(float);  // and statistics
+  w.part_bytes = 2ull * (w.decode ? kMaxRuns : kMaxTileRuns) * w.unit_rows * (v.head_dim + 1) * sizeof(float);  // and statistics
   return w;
 }
 
@@ -147,6 +62,8 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
     return fail(RIMURU_ERR_ARG, "output and queries must agree in heads and type");
   if (q->heads % v.kv_heads != 0)
     return fail(RIMURU_ERR_UNSUPPORTED, "query heads must be a multiple of kv_heads");
+  if (q->heads / v.kv_heads > 128)
+    return fail(RIMURU_ERR_UNSUPPORTED, "at most 128 query heads share a key/value head");
   if (!kv_lens || !page_table || !workspace) return fail(RIMURU_ERR_ARG, "null device pointer");
   if (table_stride <= 0) return fail(RIMURU_ERR_ARG, "table_stride must be positive");
   if (!cu_q && num_q != num_seqs)
@@ -180,18 +97,19 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.joins = static_cast<int2*>(workspace);
   a.unit_q = w.unit_rows / a.group;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.join_bytes);
-  a.stat = a.part + 2ll * kMaxRuns * w.unit_rows * v.head_dim;
+  a.stat = a.part + 2ll * (w.decode ? kMaxRuns : kMaxTileRuns) * w.unit_rows * v.head_dim;
   const double tiles = (static_cast<double>(table_stride) * v.page_tokens / kTileTokens + 1) *
                        num_seqs * v.kv_heads * w.units_per_pair;
   if (tiles > 2e9) return fail(RIMURU_ERR_UNSUPPORTED, "too many keys and queries for one call");
   cudaError_t e;
-  if (static_cast<int64_t>(max_q) * a.group <= kDecodeMaxRows) {
+  if (w.decode) {
     a.runs = std::min(kMaxRuns, kv_decode_runs(v.kv->sms, v.head_dim, w.unit_rows));
     e = launch_kv_decode(a, q->dtype, v.kv->tm_codes, s);
-    if (e == cudaSuccess) e = launch_kv_join(a, q->dtype, s);
   } else {
-    e = q->dtype == RIMURU_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_rows<__half>(a, s);
+    a.runs = std::min(kMaxTileRuns, v.kv->sms);
+    e = launch_kv_tiles(a, q->dtype, v.kv->tm_codes, s);
   }
+  if (e == cudaSuccess) e = launch_kv_join(a, q->dtype, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("attention launch", e));
   return RIMURU_OK;
 }

@@ -76,15 +76,45 @@ __device__ __forceinline__ int units_of(const AttnArgs& p, const SeqShape& s) {
 __device__ __forceinline__ TileSpan unit_span(const AttnArgs& p, const SeqShape& s, int w) {
   return tile_span(p, s, w * p.unit_q, min(s.n, (w + 1) * p.unit_q));
 }
+// Sum of floor((a i + b) / 128) over 0 <= i < n; a > 0, b >= 0.  Whole parts of
+// a / m and b / m are taken out, and what is left counts lattice points under a
+// line, which are counted along the other axis with smaller numbers.
+__device__ __forceinline__ int64_t floor_sum(int64_t n, uint32_t a, uint32_t b) {
+  int64_t sum = 0;
+  uint32_t m = kTileTokens;
+  while (n > 0) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const uint64_t top = a * static_cast<uint64_t>(n) + b;
+    if (top < m) break;
+    n = static_cast<int64_t>(top / m);
+    b = static_cast<uint32_t>(top % m);
+    const uint32_t x = m;
+    m = a;
+    a = x;
+  }
+  return sum;
+}
+// Tiles of the first w units of one head of a sequence (all of them full units).
+__device__ __forceinline__ int tiles_before(const AttnArgs& p, const SeqShape& s, int w) {
+  const int q = p.unit_q, base = s.len - s.n;  // unit v: positions base + v q .. base + (v + 1) q - 1
+  const int v0 = base + q > 0 ? 0 : -base / q;   // units before end at or below position 0
+  int64_t n = 0;
+  if (w > v0) n = floor_sum(w - v0, q, base + (v0 + 1) * q + kTileTokens - 1);
+  if (p.window > 0) {
+    const int out = p.window - 1 - base;  // first position minus `out` leaves the window's reach
+    const int v1 = out <= 0 ? 0 : (out + q - 1) / q;
+    if (w > v1) n -= floor_sum(w - v1, q, base + v1 * q - p.window + 1);
+  }
+  return static_cast<int>(n);
+}
 // Tiles of one head of a sequence, over all its units.
 __device__ __forceinline__ int pair_tiles(const AttnArgs& p, const SeqShape& s) {
-  int n = 0;
   const int u = units_of(p, s);
-  for (int w = 0; w < u; ++w) {
-    const TileSpan t = unit_span(p, s, w);
-    n += t.last - t.first;
-  }
-  return n;
+  if (u == 0) return 0;
+  const TileSpan t = unit_span(p, s, u - 1);
+  return (u > 1 ? tiles_before(p, s, u - 1) : 0) + t.last - t.first;
 }
 
 // The total is cut into `runs` runs of base or base + 1 tiles, the longer first.
@@ -157,11 +187,15 @@ __device__ __forceinline__ void find_run(const AttnArgs& p, int c, int* scratch,
     }
     int h = 0, w = 0;
     while (at >= n) at -= n, ++h;
-    while (true) {
-      const TileSpan x = unit_span(p, s, w);
-      if (at < x.last - x.first) break;
-      at -= x.last - x.first;
-      ++w;
+    const int u = units_of(p, s);
+    if (u > 1) {  // the last unit with at most `at` tiles before it
+      int hi = u;
+      while (hi - w > 1) {
+        const int mid = (w + hi) >> 1;
+        if (tiles_before(p, s, mid) <= at) w = mid;
+        else hi = mid;
+      }
+      at -= tiles_before(p, s, w);
     }
     out->b = b;
     out->h = h;
@@ -264,13 +298,17 @@ struct SmemOnce {
 };
 
 // No grid has more runs than this, so the workspace has one size on every device.
-constexpr int kMaxRuns = 320;
+constexpr int kMaxRuns = 320;      // decode kernel: up to two CTAs per SM
+constexpr int kMaxTileRuns = 160;  // tile kernel: one
 
 // Launchers (the result is cudaGetLastError's).
 cudaError_t launch_kv_decode(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s);
+cudaError_t launch_kv_tiles(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s);
 cudaError_t launch_kv_join(const AttnArgs& a, int dtype, cudaStream_t s);
 // Rows of a unit of the decode kernel: 8 or 16.
 constexpr int kDecodeMaxRows = 16;
+// Most rows of a unit of the tile kernel (two query tiles of 128; one at head_dim 256).
+constexpr int tile_rows(int head_dim) { return head_dim <= 128 ? 256 : 128; }
 int kv_decode_runs(int sms, int head_dim, int rows);
 
 }  // namespace rimuru

@@ -1,0 +1,718 @@
+// Attention of many query rows (prompts, chunks, drafted tokens of wide groups)
+// over the 8-bit paged cache.
+//
+// Bound: the tensor cores (4 head_dim operations per query head and key).  Rows
+// are (query, head of the group) pairs, so the heads that share a key/value
+// head share its tiles.  Per 128-token tile of keys and 128 rows:
+//   S = Q K^T   e4m3 x e4m3: K is multiplied as it lies in the page, Q as a sum
+//               of e4m3 parts (two hold a bf16 query exactly, three an f16 one)
+//               into one fp32 accumulator: two parts cost what one bf16 product
+//               costs, without widening K;
+//   O += P V    f16 x f16: P rounded to f16 stays in TMEM as the A operand; V is
+//               widened on its way to shared memory by four warps.  An e4m3 code
+//               placed in the upper bits of an f16 is that value times 2^-8,
+//               exactly, with no conversion instruction (and finite, whatever
+//               the byte, so unused slots need no clearing).
+// The V scale 2^k of a page is added to the score, x + k, so that the weight that
+// meets the codes stays bounded; the row sum takes the weight without it by an
+// exact multiplication.  Weights are relative to a reference that follows the
+// row's largest x + k only when a tile passes it by more than 2^8; then the
+// softmax warps rescale O in TMEM.
+//
+// Two softmax warpgroups alternate on two score buffers ("items"), so that the
+// tensor cores work on one while the other is in softmax.  With head_dim <= 128
+// and more than 128 rows the items are two query tiles (each K and V tile serves
+// 256 rows, a row is a thread); otherwise successive key tiles of one query
+// tile, whose columns the two warpgroups halve.
+//
+// Warps 0-3 and 4-7: softmax.  8-11: V.  12: K copies and page scales.  13: MMAs.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "kv_attn.h"
+
+namespace rimuru {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 512;
+constexpr int kMetaRing = 8;
+constexpr int kGroups = kTileTokens / 16;
+constexpr float kWeightTop = 7.f;    // a weight at the reference is 2^7
+constexpr float kWeightSlack = 8.f;  // and may pass it by 2^8: f16 ends at 2^16
+constexpr float kNoRef = -1e30f;     // the reference of a row that has seen no key
+
+template <int kD, int kTiles, int kQParts>
+struct TileCfg {
+  static constexpr int kRowBytes = kD < 128 ? kD : 128;  // bytes of a K or Q row in one slab
+  static constexpr int kSlabs = kD / kRowBytes;
+  static constexpr int kSlabBytes = 128 * kRowBytes;
+  static constexpr int kKBytes = kSlabs * kSlabBytes;           // one K tile
+  static constexpr int kKRing = kD <= 128 ? 3 : 2;              // K tiles
+  static constexpr int kQBytes = kQParts * kTiles * kKBytes;    // [part][tile][slab][128 rows]
+  static constexpr int kVTok = kD <= 128 ? 64 : 32;             // tokens of a V stage
+  static constexpr int kVStages = kTileTokens / kVTok;          // stages of a tile
+  static constexpr int kVBytes = kVTok * kD * 2;                // [64 f16 of a token: 128 bytes][tokens]
+  static constexpr int kVRing = kD == 256 && kQParts == 3 ? 3 : 4;
+  static constexpr int kSmem = 1024 + kQBytes + kKRing * kKBytes + kVRing * kVBytes;
+  static constexpr int kCols = kTiles == 2 ? 128 : 64;          // score columns of a thread
+  static constexpr uint32_t kO = 256;                           // TMEM column of O; scores are at 0 and 128
+};
+
+struct Meta {  // a 16-token group of a tile
+  float k, v;  // scales; v == 0: no such page
+};
+struct TileShared {
+  uint64_t k_full[4], k_empty[4];
+  uint64_t v_full[4], v_empty[4];
+  uint64_t meta_full[kMetaRing];
+  uint64_t q_full;
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  RunStart run;
+  int scratch[16];
+  Meta meta[kMetaRing][kGroups];
+  int page[kMetaRing][kGroups];   // of each group, -1: none
+  int gap[kMetaRing];             // some group of the tile has no page
+  float row_scale[128];           // one query tile: score per unit of S and K scale
+  float other[2][2][128];         // one query tile: row maxima, and sums, of the two halves
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
+}
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) { return pack_bf16x2(a, b); }
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Holds in all 256 softmax threads (barrier 2).
+__device__ __forceinline__ bool softmax_and(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "bar.red.and.pred b, 2, 256, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}\n"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+// Byte offset of byte d of row r in a swizzled K-major block.
+template <int kRowBytes>
+__device__ __forceinline__ int swz(int r, int d) {
+  if (kRowBytes == 128) return r * 128 + ((((d >> 4) ^ r) & 7) << 4) + (d & 15);
+  return r * 64 + ((((d >> 4) ^ (r >> 1)) & 3) << 4) + (d & 15);
+}
+// Two e4m3 codes (bytes 0 and 1 of w, or 2 and 3) as f16 numbers times 2^-8.
+__device__ __forceinline__ uint32_t widen(uint32_t w, bool upper) {
+  const uint32_t t = __byte_perm(w, 0, upper ? 0x3424 : 0x1404);  // code in the high byte of each half
+  return (t & 0x80008000u) | ((t >> 1) & 0x3F803F80u);
+}
+
+template <typename T, int kD, int kTiles>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_tiles_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap tm) {
+  constexpr int kQParts = std::is_same<T, __nv_bfloat16>::value ? 2 : 3;
+  using C = TileCfg<kD, kTiles, kQParts>;
+  constexpr int kSlabs = C::kSlabs, kRowBytes = C::kRowBytes, kCols = C::kCols;
+  constexpr uint32_t kSwizzle = kRowBytes == 128 ? 2 : 4;
+  constexpr uint32_t kAtom = 8 * kRowBytes;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + C::kQBytes;
+  uint8_t* sV = sK + C::kKRing * C::kKBytes;
+  __shared__ TileShared sh_;
+  TileShared* sh = &sh_;
+  volatile int* abort = &sh->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh->k_full[i], 1);
+      mbar_init(&sh->k_empty[i], 1);
+      mbar_init(&sh->v_full[i], 4);
+      mbar_init(&sh->v_empty[i], 1);
+    }
+    for (int i = 0; i < kMetaRing; ++i) mbar_init(&sh->meta_full[i], 1);
+    mbar_init(&sh->q_full, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_full[i], kTiles == 2 ? 4 : 8);
+      mbar_init(&sh->o_full[i], 1);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tm);
+  }
+  if (warp == 13) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  grid_dep_wait();  // lengths, tables, q and the cache come from earlier kernels
+  grid_dep_launch();
+  find_run(p, blockIdx.x, sh->scratch, &sh->run);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const int P = p.g.page_tokens, log_p = 31 - __clz(P);
+  RunWalk walk;
+  walk.begin_run(p, sh->run);
+  Segment g;
+
+  if (warp >= 12) {
+    if (warp == 12) {
+      // -------------------------------------------------------------- K copies
+      // The warp holds the ids and scales of 32 pages, one per lane (`boxes`
+      // pages are a tile), and the ids of the next 32.
+      const uint64_t pol = policy_evict_last();  // other query tiles read the same keys
+      const int boxes = kTileTokens >> log_p, groups = P / 16;
+      uint32_t tile = 0;
+      bool ok = true;
+      while (ok && walk.next(p, &g)) {
+        const int lo = p.window > 0 ? max(0, g.s.len - g.s.n + g.i0 - p.window + 1) : 0;
+        const int32_t* row = p.s.table + g.b * p.s.table_stride;
+        const auto page_at = [&](int c) {  // page c of the sequence, -1 when none of its tokens count
+          int page = -1;
+          if (c << log_p < g.s.len && (c + 1) << log_p > lo && c < g.t1 * boxes) {
+            page = row[c];
+            if (page < 0 || page >= p.g.num_pages) {
+              set_error(p.g.err, RIMURU_DEV_BAD_PAGE);
+              page = -1;
+            }
+          }
+          return page;
+        };
+        int c = g.t0 * boxes + lane, at = 32;
+        int ahead = page_at(c), page = -1;
+        float ks = 0.f, vs = 0.f;
+        const int y = g.h << log_p;  // first K row of the head in a page
+        for (int t = g.t0; ok && t < g.t1; ++t, ++tile) {
+          if (at == 32) {
+            page = ahead;
+            ks = vs = 0.f;
+            if (page >= 0) {
+              const float* sc = p.g.scales + static_cast<int64_t>(page) * 2 * p.g.kv_heads + g.h;
+              ks = sc[0];
+              vs = sc[p.g.kv_heads];
+            }
+            c += 32;
+            ahead = page_at(c);
+            at = 0;
+          }
+          const int mine = __shfl_sync(0xffffffffu, page, (at + lane) & 31);  // for lanes below `boxes`
+          const bool copies = lane < boxes && mine >= 0;
+          const uint32_t which = __ballot_sync(0xffffffffu, copies);
+          const uint32_t i = tile % C::kKRing;
+          ok = mbar_wait(&sh->k_empty[i], ((tile / C::kKRing) & 1u) ^ 1u, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh->k_full[i], __popc(which) * P * kD);
+          __syncwarp();
+          if (copies) {
+#pragma unroll
+            for (int sl = 0; sl < kSlabs; ++sl)
+              tma_load_3d(sK + i * C::kKBytes + sl * C::kSlabBytes + (lane << log_p) * kRowBytes, &tm,
+                          &sh->k_full[i], sl * kRowBytes, y, mine, pol);
+          }
+          // The tile's pages and scales by groups of 16 tokens.  Their last readers, eight
+          // tiles back, were done before the K tile just waited for could be reused.
+          const uint32_t m = tile % kMetaRing;
+          if (lane >= at && lane < at + boxes)
+            for (int k = 0; k < groups; ++k) {
+              sh->meta[m][(lane - at) * groups + k] = {ks, vs};
+              sh->page[m][(lane - at) * groups + k] = page;
+            }
+          if (lane == 0) sh->gap[m] = which != (1u << boxes) - 1u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->meta_full[m]);
+          at += boxes;
+        }
+      }
+      if (!ok && lane == 0) {
+        set_error(p.g.err, RIMURU_DEV_TIMEOUT);
+        sh->abort = 1;
+      }
+      // every copy this warp issued must have landed before the CTA exits
+      volatile int never = 0;
+      for (uint32_t j = tile > C::kKRing ? tile - C::kKRing : 0u; j < tile; ++j)
+        mbar_wait(&sh->k_full[j % C::kKRing], (j / C::kKRing) & 1u, &never);
+    } else if (warp == 13 && lane == 0) {
+      // ------------------------------------------------------------------ MMAs
+      // Items: (key tile, query tile) pairs in order; item i uses score buffer i & 1.
+      // The scores of item i + 2 follow the output of item i, whose weights lie in
+      // the same buffer; MMAs of one thread run in the order they were issued.
+      constexpr uint32_t id_s = idesc_f8_f32(128, 128, false, false, false);
+      constexpr uint32_t id_o = idesc_f16_f32(128, kD, false, /*b_mn=*/true);
+      uint32_t tile0 = 0, item0 = 0, seg = 0;  // tiles and items of the segments before
+      bool ok = true;
+      while (ok && walk.next(p, &g)) {
+        const uint32_t tiles = g.t1 - g.t0, items = tiles * kTiles;
+        ok = mbar_wait(&sh->q_full, seg & 1u, abort);
+        tc_fence_after();
+        const auto scores = [&](uint32_t i) {  // item i of the segment
+          const uint32_t tile = tile0 + i / kTiles, q = i % kTiles, s = tile % C::kKRing;
+          if (q == 0 && !mbar_wait(&sh->k_full[s], (tile / C::kKRing) & 1u, abort)) return false;
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sQ + q * C::kKBytes), b0 = smem_u32(sK + s * C::kKBytes);
+          const uint32_t d = tmem + 128 * ((item0 + i) & 1u);
+#pragma unroll
+          for (int part = 0; part < kQParts; ++part) {
+#pragma unroll
+            for (int sl = 0; sl < kSlabs; ++sl) {
+#pragma unroll
+              for (int k = 0; k < kRowBytes / 32; ++k)
+                umma_f8(d,
+                        smem_desc(a0 + part * kTiles * C::kKBytes + sl * C::kSlabBytes + 32 * k, 16,
+                                  kAtom, kSwizzle),
+                        smem_desc(b0 + sl * C::kSlabBytes + 32 * k, 16, kAtom, kSwizzle), id_s,
+                        (part | sl | k) != 0 ? 1u : 0u);
+            }
+          }
+          umma_commit(&sh->s_full[(item0 + i) & 1u]);
+          if (q == kTiles - 1) umma_commit(&sh->k_empty[s]);
+          return true;
+        };
+        ok = ok && scores(0);
+        if (ok && items > 1) ok = scores(1);
+        for (uint32_t i = 0; ok && i < items; ++i) {
+          const uint32_t slot = (item0 + i) & 1u, tile = tile0 + i / kTiles, q = i % kTiles;
+          ok = mbar_wait(&sh->p_full[slot], ((item0 + i) >> 1) & 1u, abort);
+#pragma unroll
+          for (int h = 0; h < C::kVStages; ++h) {
+            const uint32_t v = C::kVStages * tile + h, s = v % C::kVRing;
+            if (q == 0) ok = ok && mbar_wait(&sh->v_full[s], (v / C::kVRing) & 1u, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t b0 = smem_u32(sV + s * C::kVBytes);
+#pragma unroll
+            for (int k = 0; k < C::kVTok / 16; ++k)  // 16 tokens: eight columns of P, 16 rows of V
+              umma_f16_ts(tmem + C::kO + q * kD, tmem + 128 * slot + C::kVTok / 2 * h + 8 * k,
+                          smem_desc_sw128(b0 + 2048 * k, C::kVTok * 128, 1024), id_o,
+                          (i >= kTiles || h + k != 0) ? 1u : 0u);
+            if (q == kTiles - 1) umma_commit(&sh->v_empty[s]);
+          }
+          umma_commit(&sh->o_full[slot]);
+          if (ok && i + 2 < items) ok = scores(i + 2);
+        }
+        tile0 += tiles;
+        item0 += items;
+        ++seg;
+      }
+      if (!ok) {
+        set_error(p.g.err, RIMURU_DEV_TIMEOUT);
+        sh->abort = 1;
+      }
+      umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
+      volatile int never = 0;
+      mbar_wait(&sh->drain, 0, &never);
+    }
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------------- V
+    // A stage is kVTok tokens: thread `t128` takes 16 codes (chunk c) of the
+    // tokens r0, r0 + kStep, ...; the next two stages are loaded ahead.
+    constexpr int kChunks = kD / 16, kStep = 128 / kChunks, kPer = C::kVTok / kStep;
+    const int t128 = threadIdx.x - 256, c = t128 % kChunks, r0 = t128 / kChunks;
+    bool ok = true;
+    uint4 raw[2][kPer];
+    // the load cursor: stage `lh` of key tile lt, tile `ltile` of the run
+    int lt = 0, lh = C::kVStages;
+    uint32_t ltile = 0xFFFFFFFFu;
+    g.t1 = 0;
+    const auto load = [&](uint4(&x)[kPer]) {
+      if (lh == C::kVStages) {
+        lh = 0;
+        ++ltile;
+        if (++lt >= g.t1) {
+          walk.next(p, &g);
+          lt = g.t0;
+        }
+        ok = mbar_wait(&sh->meta_full[ltile % kMetaRing], (ltile / kMetaRing) & 1u, abort) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+      }
+      const uint64_t base = static_cast<uint64_t>(p.g.kv_heads + g.h) * P * kD + 16 * c;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int r = C::kVTok * lh + r0 + k * kStep;
+        const int page = sh->page[ltile % kMetaRing][r >> 4];
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (page >= 0)
+          x[k] = *reinterpret_cast<const uint4*>(p.g.pool + page * p.g.page_bytes + base +
+                                                 static_cast<uint64_t>(r & (P - 1)) * kD);
+      }
+      ++lh;
+    };
+    const auto store = [&](uint32_t v, const uint4(&x)[kPer]) {
+      const uint32_t s = v % C::kVRing;
+      ok = mbar_wait(&sh->v_empty[s], ((v / C::kVRing) & 1u) ^ 1u, abort) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      uint8_t* dst = sV + s * C::kVBytes + (c >> 2) * (C::kVTok * 128);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int r = r0 + k * kStep, ch = 2 * (c & 3);  // chunks of eight f16 in the 128-byte row
+        *reinterpret_cast<uint4*>(dst + r * 128 + (((ch ^ r) & 7) << 4)) =
+            make_uint4(widen(x[k].x, false), widen(x[k].x, true), widen(x[k].y, false), widen(x[k].y, true));
+        *reinterpret_cast<uint4*>(dst + r * 128 + ((((ch + 1) ^ r) & 7) << 4)) =
+            make_uint4(widen(x[k].z, false), widen(x[k].z, true), widen(x[k].w, false), widen(x[k].w, true));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->v_full[s]);
+    };
+    const uint32_t total = C::kVStages * sh->run.tiles;  // even
+    if (total > 0) {
+      load(raw[0]);
+      if (ok) load(raw[1]);
+    }
+    for (uint32_t v = 0; ok && v < total; v += 2) {
+      store(v, raw[0]);
+      if (ok && v + 2 < total) load(raw[0]);
+      if (ok) store(v + 1, raw[1]);
+      if (ok && v + 3 < total) load(raw[1]);
+    }
+    if (!ok && lane == 0) {
+      set_error(p.g.err, RIMURU_DEV_TIMEOUT);
+      sh->abort = 1;
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int wg = warp >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;  // row of the query tile, and TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const int qt = kTiles == 2 ? wg : 0;             // query tile
+    const int col0 = kTiles == 2 ? 0 : 64 * wg;      // first score column of this thread
+    const uint32_t tO = tmem + C::kO + qt * kD + lane_off;
+    uint32_t tile = 0, item0 = 0;
+    bool ok = true;
+    while (ok && walk.next(p, &g)) {
+      const int rows = (g.i1 - g.i0) * p.group;
+      // Q of the segment, as parts: warp `quad` writes its own 32 rows, one at a
+      // time (with one query tile the two warpgroups take every other row)
+      float c_row = 1e-30f;  // score per unit of S and K scale; never 0, so masked scores stay masked
+      constexpr int kPer = kD / 32;
+      const int q_first = kTiles == 2 ? 0 : wg, q_step = kTiles == 2 ? 1 : 2;
+      const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
+      for (int k0 = q_first; k0 < 32; k0 += 4 * q_step) {
+        T raw[4][kPer];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = qt * 128 + quad * 32 + k0 + k * q_step;
+          if (r < rows) {
+            const int i = r / p.group;
+            const T* src = static_cast<const T*>(p.q) + (g.s.row0 + g.i0 + i) * p.q_ts +
+                           (g.h * p.group + r - i * p.group) * p.q_hs + lane * kPer;
+            if constexpr (kPer == 8) *reinterpret_cast<uint4*>(raw[k]) = *reinterpret_cast<const uint4*>(src);
+            else if constexpr (kPer == 4) *reinterpret_cast<uint2*>(raw[k]) = *reinterpret_cast<const uint2*>(src);
+            else *reinterpret_cast<uint32_t*>(raw[k]) = *reinterpret_cast<const uint32_t*>(src);
+          } else {
+            uint32_t* z = reinterpret_cast<uint32_t*>(raw[k]);
+#pragma unroll
+            for (int i = 0; i < kPer / 2; ++i) z[i] = 0u;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rl = k0 + k * q_step;  // row within the warp's 32
+          float x[kPer], amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            x[i] = to_f(raw[k][i]);
+            amax = fmaxf(amax, fabsf(x[i]));
+          }
+          amax = warp_max(amax);
+          // power of two that brings the row's largest magnitude into (224, 448]
+          const uint32_t ab = __float_as_uint(amax);
+          const int e = max(-100, min(100, static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u)));
+          const float inv = sign * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          // an infinite query has no finite score: its row becomes NaN
+          const float scale = amax <= 3.4028234664e38f
+                                  ? fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) *
+                                              fabsf(p.scale_log2),
+                                          1e-30f)
+                                  : __int_as_float(0x7FFFFFFF);
+          if (kTiles == 2) {
+            if (lane == rl) c_row = scale;
+          } else if (lane == 0) {
+            sh->row_scale[quad * 32 + rl] = scale;
+          }
+          const int d0 = lane * kPer, sl = d0 / kRowBytes;
+          uint8_t* dst = sQ + qt * C::kKBytes + sl * C::kSlabBytes +
+                         swz<kRowBytes>(quad * 32 + rl, d0 % kRowBytes);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) x[i] *= inv;
+#pragma unroll
+          for (int part = 0; part < kQParts; ++part) {
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2) {
+              const uint32_t code = e4m3x2(x[i], x[i + 1]);
+              const float2 f = from_e4m3x2(code);
+              x[i] -= f.x;
+              x[i + 1] -= f.y;
+              *reinterpret_cast<uint16_t*>(dst + part * kTiles * C::kKBytes + i) = static_cast<uint16_t>(code);
+            }
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->q_full);
+      if (kTiles == 1) {
+        if (!softmax_and(ok)) {
+          ok = false;
+          break;
+        }
+        c_row = sh->row_scale[row];
+      }
+      // keys [j_lo, j_hi) of this row; rows past the unit see every column and are not written
+      const int r = qt * 128 + row, qi = r / p.group, gi = r - qi * p.group;
+      const bool real = r < rows;
+      const int pos = g.s.len - g.s.n + g.i0 + qi;
+      const int j_hi = real ? min(pos + 1, g.s.len) : 0x7FFFFFFF;
+      const int j_lo = real && p.window > 0 ? pos - p.window + 1 : -0x7FFFFFFF;
+      float ref = kNoRef, l = 0.f;
+      const int n_tiles = g.t1 - g.t0;
+      for (int n = 0; n < n_tiles; ++n) {
+        const int t = g.t0 + n;
+        const uint32_t item = item0 + (kTiles == 2 ? 2 * n + wg : n), slot = item & 1u;
+        const uint32_t m = (tile + n) % kMetaRing;
+        ok = mbar_wait(&sh->meta_full[m], ((tile + n) / kMetaRing) & 1u, abort) && ok;
+        ok = mbar_wait(&sh->s_full[slot], (item >> 1) & 1u, abort) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (kTiles == 2 && !ok) break;
+        tc_fence_after();
+        const uint32_t tS = tmem + 128 * slot + lane_off;
+        // Scores come 32 columns at a time, the next 32 on their way: read once for the
+        // maximum and, where the row is one thread's, again for the weights (64 of them
+        // stay in registers otherwise).
+        uint32_t s[2][32];
+        const int j0 = t * kTileTokens + col0;
+        const bool edge = __any_sync(0xffffffffu, sh->gap[m] != 0 || j_lo > j0 || j_hi < j0 + kCols);
+        const auto hide = [&](uint32_t(&v)[32], int k0) {  // scores that the row does not see
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int j = j0 + k0 + k;
+            const bool see = j >= j_lo && j < j_hi && sh->meta[m][(col0 + k0 + k) / 16].v != 0.f;
+            if (!see) v[k] = 0xFF800000u;
+          }
+        };
+        // x + k of a 16-column group is S * mul + add
+        const auto affine = [&](int q, float* mul, float* add) {
+          const Meta kv = sh->meta[m][col0 / 16 + q];
+          *mul = c_row * (kv.v != 0.f ? kv.k : 1.f);
+          *add = static_cast<float>(static_cast<int>(__float_as_uint(kv.v) >> 23) - 127);
+        };
+        float top = -INFINITY;
+        tmem_ld32(tS + col0, s[0]);
+        tmem_ld_wait32(s[0]);
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          if (c + 1 < kCols / 32) tmem_ld32(tS + col0 + 32 * (c + 1), s[(c + 1) & 1]);
+          uint32_t(&v)[32] = s[c & 1];
+          if (edge) hide(v, 32 * c);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float mul, add, x = __uint_as_float(v[16 * q]);
+            affine(2 * c + q, &mul, &add);
+#pragma unroll
+            for (int k = 1; k < 15; k += 2)
+              x = fmaxf(fmaxf(x, __uint_as_float(v[16 * q + k])), __uint_as_float(v[16 * q + k + 1]));
+            x = fmaxf(x, __uint_as_float(v[16 * q + 15]));
+            top = fmaxf(top, x * mul + add);
+          }
+          if (c + 1 < kCols / 32) tmem_ld_wait32(s[(c + 1) & 1]);
+        }
+        if (kTiles == 2) tmem_ld32(tS, s[0]);
+        if (kTiles == 1) {  // the other half of the row
+          sh->other[n & 1][wg][row] = top;
+          ok = softmax_and(ok);
+          if (!ok) break;
+          top = fmaxf(top, sh->other[n & 1][wg ^ 1][row]);
+        }
+        const bool raise = top > ref + kWeightSlack;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float now = raise ? top : ref, f = ex2(ref - now);
+          ref = now;
+          l *= f;
+          if (n > 0) {  // O of the row is complete up to the tile before: rescale it
+            const uint32_t last = kTiles == 2 ? item - 2 : item - 1;
+            ok = mbar_wait(&sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            constexpr int kO = kTiles == 2 ? kD : kD / 2;
+#pragma unroll 1
+            for (int k = 0; k < kO; k += 32) {
+              uint32_t v[32];
+              const uint32_t at = tO + (kTiles == 2 ? 0 : wg * kO) + k;
+              tmem_ld32(at, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              tmem_st32(at, v);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float base = kWeightTop - ref;
+        if (kTiles == 2) tmem_ld_wait32(s[0]);
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          uint32_t(&v)[32] = s[c & 1];
+          if (kTiles == 2) {
+            if (c + 1 < kCols / 32) tmem_ld32(tS + 32 * (c + 1), s[(c + 1) & 1]);
+            if (edge) hide(v, 32 * c);
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float mul, add, sum = 0.f;
+            affine(2 * c + q, &mul, &add);
+            const float a = add + base;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float x = ex2(__uint_as_float(v[16 * q + k]) * mul + a);
+              const float y = ex2(__uint_as_float(v[16 * q + k + 1]) * mul + a);
+              sum += x + y;
+              const __half2 h = __floats2half2_rn(x, y);
+              w[8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            l += sum * ex2(-add);
+          }
+          // the weights lie where scores were that this row has read
+          tmem_st16(tS + col0 / 2 + 16 * c, w);
+          if (kTiles == 2 && c + 1 < kCols / 32) tmem_ld_wait32(s[(c + 1) & 1]);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_full[slot]);
+      }
+      const uint32_t items = n_tiles * kTiles;
+      if (kTiles == 2 && !ok) break;
+      // the rows: O / l, with the 2^8 that V was widened without
+      {
+        const uint32_t last = item0 + items - 1 - (kTiles == 2 ? 1 - wg : 0);
+        ok = mbar_wait(&sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (kTiles == 1) {  // the two halves of the row's sum
+        sh->other[n_tiles & 1][wg][row] = l;
+        ok = softmax_and(ok);
+        if (!ok) break;
+        l = sh->other[n_tiles & 1][0][row] + sh->other[n_tiles & 1][1][row];
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = l > 0.f ? 256.f / l : l;
+      const float stat = l > 0.f ? ref - kWeightTop + __log2f(l) : l == 0.f ? -INFINITY : l;
+      const bool whole = g.starts && g.ends;
+      const int64_t at = part_slot(p, blockIdx.x, g.starts) + r;
+      const int64_t orow = g.s.row0 + g.i0 + qi;
+      const int head = g.h * p.group + gi;
+      constexpr int kO = kTiles == 2 ? kD : kD / 2;
+      const int d0 = kTiles == 2 ? 0 : wg * kO;
+      T* out = static_cast<T*>(p.out) + orow * p.o_ts + head * p.o_hs + d0;
+      float* part = p.part + at * kD + d0;
+#pragma unroll 1
+      for (int k = 0; k < kO; k += 32) {
+        uint32_t v[32];
+        tmem_ld32(tO + d0 + k, v);
+        tmem_ld_wait();
+        if (!real) continue;
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              u[e] = pack2(__uint_as_float(v[i + 2 * e]) * inv, __uint_as_float(v[i + 2 * e + 1]) * inv, T{});
+            *reinterpret_cast<uint4*>(out + k + i) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(part + k + i) =
+                make_float4(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
+                            __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+        }
+      }
+      tc_fence_before();
+      if (real && (kTiles == 2 || wg == 0)) {
+        if (!whole) p.stat[at] = stat;
+        else if (p.lse) p.lse[orow * p.q_heads + head] = stat * kLn2;
+      }
+      if (g.starts && threadIdx.x == 0) note_join(p, g, sh->run.cut, blockIdx.x);
+      tile += n_tiles;
+      item0 += items;
+    }
+    if (!ok && lane == 0) {
+      set_error(p.g.err, RIMURU_DEV_TIMEOUT);
+      sh->abort = 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int kD, int kTiles>
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& tm, cudaStream_t s) {
+  constexpr int kQParts = std::is_same<T, __nv_bfloat16>::value ? 2 : 3;
+  constexpr int smem = TileCfg<kD, kTiles, kQParts>::kSmem;
+  auto* fn = kv_tiles_kernel<T, kD, kTiles>;
+  static SmemOnce once;
+  cudaError_t e = once.set(reinterpret_cast<const void*>(fn), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.runs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, a, tm);
+}
+template <typename T>
+cudaError_t launch_dim(const AttnArgs& a, const CUtensorMap& tm, cudaStream_t s) {
+  const bool two = a.unit_rows == 256;
+  if (a.g.head_dim == 64) return two ? launch<T, 64, 2>(a, tm, s) : launch<T, 64, 1>(a, tm, s);
+  if (a.g.head_dim == 128) return two ? launch<T, 128, 2>(a, tm, s) : launch<T, 128, 1>(a, tm, s);
+  return launch<T, 256, 1>(a, tm, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_tiles(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s) {
+  return dtype == RIMURU_BF16 ? launch_dim<__nv_bfloat16>(a, tm, s) : launch_dim<__half>(a, tm, s);
+}
+
+}  // namespace rimuru
