@@ -277,77 +277,98 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
       mbar_wait(&sh->full[j % kRing], (j / kRing) & 1u, &never);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f8_f32(128, kNS, false, false, false);
-      constexpr uint32_t id_o = idesc_f8_f32(128, kNO, /*a_mn=*/true, /*b_mn=*/true, /*b_e5m2=*/true);
-      const auto scores = [&](uint32_t i, uint32_t seg) {  // S^T of the run's tile i
+    // The whole warp walks and waits, and one lane issues, so that addresses stay
+    // warp-uniform.
+    constexpr uint32_t id_s = idesc_f8_f32(128, kNS, false, false, false);
+    constexpr uint32_t id_o = idesc_f8_f32(128, kNO, /*a_mn=*/true, /*b_mn=*/true, /*b_e5m2=*/true);
+    const uint32_t tb = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t ring_s = smem_u32(sRing), q_s = smem_u32(sQ), p_s = smem_u32(sP);
+    uint32_t slot = 0, phase = 0;  // the next slot of the ring
+    bool ok = true;
+    const auto wait = [&](uint64_t* bar, uint32_t ph) {
+      ok = ok && mbar_wait(bar, ph, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    };
+    const auto step = [&](uint32_t* at, uint32_t* ph, uint32_t n) {
+      *at += n;
+      if (*at >= kRing) *at -= kRing, *ph ^= 1u;
+    };
+    const auto scores = [&](uint32_t i, uint32_t seg) {  // S^T of the run's tile i, in the next K unit
+      uint32_t at = slot, ph = phase;
 #pragma unroll
-        for (int sl = 0; sl < kSlabs; ++sl) {
-          const uint32_t u = 2 * i * kSlabs + sl, slot = u % kRing;
-          if (!mbar_wait(&sh->full[slot], (u / kRing) & 1u, abort)) return false;
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sRing + slot * C::kSlabBytes);
-          const uint32_t b0 = smem_u32(sQ + (seg & 1u) * C::kQBytes + sl * kNS * kRowBytes);
+      for (int sl = 0; sl < kSlabs; ++sl) {
+        wait(&sh->full[at], ph);
+        if (ok && elect_one()) {
+          const uint32_t a0 = ring_s + at * C::kSlabBytes;
+          const uint32_t b0 = q_s + (seg & 1u) * C::kQBytes + sl * kNS * kRowBytes;
 #pragma unroll
           for (int k = 0; k < kRowBytes / 32; ++k)
-            umma_f8(tS + (i & 1u) * kNS, smem_desc(a0 + 32 * k, 16, kAtom, kSwizzle),
+            umma_f8(tb + (i & 1u) * kNS, smem_desc(a0 + 32 * k, 16, kAtom, kSwizzle),
                     smem_desc(b0 + 32 * k, 16, kAtom, kSwizzle), id_s, (sl | k) != 0 ? 1u : 0u);
-          umma_commit(&sh->empty[slot]);
+          umma_commit(&sh->empty[at]);
+          if (sl == kSlabs - 1) umma_commit(&sh->s_full[i & 1u]);
         }
-        umma_commit(&sh->s_full[i & 1u]);
-        return true;
-      };
-      const auto outputs = [&](uint32_t i) {  // O^T of the run's tile i
-        if (!mbar_wait(&sh->p_full[i & 1u], (i >> 1) & 1u, abort)) return false;
-        const uint32_t keep = sh->fresh[i & 1u] ? 0u : 1u;
+        __syncwarp();
+        step(&at, &ph, 1);
+      }
+      step(&slot, &phase, 2 * kSlabs);  // past the tile's V unit
+    };
+    uint32_t v_slot = kSlabs, v_phase = 0;
+    const auto outputs = [&](uint32_t i) {  // O^T of the run's tile i, in the next V unit
+      wait(&sh->p_full[i & 1u], (i >> 1) & 1u);
+      const uint32_t keep = sh->fresh[i & 1u] ? 0u : 1u;
+      uint32_t at = v_slot, ph = v_phase;
 #pragma unroll
-        for (int sl = 0; sl < kSlabs; ++sl) {
-          const uint32_t u = (2 * i + 1) * kSlabs + sl, slot = u % kRing;
-          if (!mbar_wait(&sh->full[slot], (u / kRing) & 1u, abort)) return false;
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sRing + slot * C::kSlabBytes);
+      for (int sl = 0; sl < kSlabs; ++sl) {
+        wait(&sh->full[at], ph);
+        if (ok && elect_one()) {
+          const uint32_t a0 = ring_s + at * C::kSlabBytes;
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 tokens: four groups of eight rows
-            umma_f8(tO + sl * kNO,
+            umma_f8(tb + 2 * kNS + sl * kNO,
                     smem_desc(a0 + 4 * k * kAtom, C::kSlabBytes, kAtom, kSwizzle),
-                    smem_desc(smem_u32(sP + (i & 1u) * C::kPBytes) + 32 * k * kNO, C::kPBytes, 8 * kNO,
+                    smem_desc(p_s + (i & 1u) * C::kPBytes + 32 * k * kNO, C::kPBytes, 8 * kNO,
                               kNO == 64 ? 4 : 6),
                     id_o, k != 0 ? 1u : keep);
-          umma_commit(&sh->empty[slot]);
+          umma_commit(&sh->empty[at]);
+          if (sl == kSlabs - 1) umma_commit(&sh->o_full[i & 1u]);
         }
-        umma_commit(&sh->o_full[i & 1u]);
-        return true;
-      };
-      // S of the next tile is issued before O of this one.  Its buffer and this
-      // one's are free: the weights of the tile before were written after the
-      // softmax warps had read them.
-      bool ok = true;
-      uint32_t tile = 0, seg = 0;
-      if (walk.next(p, &g)) {
-        ok = mbar_wait(&sh->q_full[0], 0, abort) && scores(0, 0);
-        for (int t = g.t0; ok; ++tile) {
-          bool more = true;
-          if (++t == g.t1) {
-            more = walk.next(p, &g);
-            if (more) {
-              ++seg;
-              t = g.t0;
-              ok = mbar_wait(&sh->q_full[seg & 1u], (seg >> 1) & 1u, abort);
-            }
+        __syncwarp();
+        step(&at, &ph, 1);
+      }
+      step(&v_slot, &v_phase, 2 * kSlabs);
+    };
+    // S of the next tile is issued before O of this one.  Its buffer and this
+    // one's are free: the weights of the tile before were written after the
+    // softmax warps had read them.
+    uint32_t tile = 0, seg = 0;
+    if (walk.next(p, &g)) {
+      wait(&sh->q_full[0], 0);
+      scores(0, 0);
+      for (int t = g.t0; ok; ++tile) {
+        bool more = true;
+        if (++t == g.t1) {
+          more = walk.next(p, &g);
+          if (more) {
+            ++seg;
+            t = g.t0;
+            wait(&sh->q_full[seg & 1u], (seg >> 1) & 1u);
           }
-          if (more) ok = ok && scores(tile + 1, seg);
-          ok = ok && outputs(tile);
-          if (!more) break;
         }
+        if (more) scores(tile + 1, seg);
+        outputs(tile);
+        if (!more) break;
       }
-      if (!ok) {
-        set_error(p.g.err, RIMURU_DEV_TIMEOUT);
-        sh->abort = 1;
-      }
-      umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
-      volatile int never = 0;
-      mbar_wait(&sh->drain, 0, &never);
     }
+    if (!ok && lane == 0) {
+      set_error(p.g.err, RIMURU_DEV_TIMEOUT);
+      sh->abort = 1;
+    }
+    if (elect_one()) umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
+    __syncwarp();
+    volatile int never = 0;
+    mbar_wait(&sh->drain, 0, &never);
   } else if (warp == 2) {
     // --------------------------------------------------------------------- Q
     uint32_t seg = 0;

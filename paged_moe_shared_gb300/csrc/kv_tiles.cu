@@ -261,25 +261,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int never = 0;
       for (uint32_t j = tile > C::kKRing ? tile - C::kKRing : 0u; j < tile; ++j)
         mbar_wait(&sh->k_full[j % C::kKRing], (j / C::kKRing) & 1u, &never);
-    } else if (warp == 13 && lane == 0) {
+    } else if (warp == 13) {
       // ------------------------------------------------------------------ MMAs
       // Items: (key tile, query tile) pairs in order; item i uses score buffer i & 1.
       // The scores of item i + 2 follow the output of item i, whose weights lie in
       // the same buffer; MMAs of one thread run in the order they were issued.
+      // The whole warp walks and waits, and one lane issues: addresses stay
+      // warp-uniform (issued from a one-lane branch, an MMA took 160 cycles to issue
+      // instead of the 64 it runs).
       constexpr uint32_t id_s = idesc_f8_f32(128, 128, false, false, false);
       constexpr uint32_t id_o = idesc_f16_f32(128, kD, false, /*b_mn=*/true);
-      uint32_t tile0 = 0, item0 = 0, seg = 0;  // tiles and items of the segments before
+      const uint32_t tb = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_s = smem_u32(sQ), k_s = smem_u32(sK), v_s = smem_u32(sV);
+      uint32_t item = 0, k_slot = 0, k_phase = 0, v_slot = 0, v_phase = 0, seg = 0;
       bool ok = true;
-      while (ok && walk.next(p, &g)) {
-        const uint32_t tiles = g.t1 - g.t0, items = tiles * kTiles;
-        ok = mbar_wait(&sh->q_full, seg & 1u, abort);
+      const auto wait = [&](uint64_t* bar, uint32_t phase) {
+        ok = ok && mbar_wait(bar, phase, abort);
+        ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        const auto scores = [&](uint32_t i) {  // item i of the segment
-          const uint32_t tile = tile0 + i / kTiles, q = i % kTiles, s = tile % C::kKRing;
-          if (q == 0 && !mbar_wait(&sh->k_full[s], (tile / C::kKRing) & 1u, abort)) return false;
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sQ + q * C::kKBytes), b0 = smem_u32(sK + s * C::kKBytes);
-          const uint32_t d = tmem + 128 * ((item0 + i) & 1u);
+      };
+      // The next scores go to buffer `item`'s parity; `q`: its query tile.
+      const auto scores = [&](uint32_t buffer, uint32_t q) {
+        if (q == 0) wait(&sh->k_full[k_slot], k_phase);
+        if (ok && elect_one()) {
+          const uint32_t a0 = q_s + q * C::kKBytes, b0 = k_s + k_slot * C::kKBytes;
+          const uint32_t d = tb + 128 * buffer;
 #pragma unroll
           for (int part = 0; part < kQParts; ++part) {
 #pragma unroll
@@ -293,41 +299,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (part | sl | k) != 0 ? 1u : 0u);
             }
           }
-          umma_commit(&sh->s_full[(item0 + i) & 1u]);
-          if (q == kTiles - 1) umma_commit(&sh->k_empty[s]);
-          return true;
-        };
-        ok = ok && scores(0);
-        if (ok && items > 1) ok = scores(1);
-        for (uint32_t i = 0; ok && i < items; ++i) {
-          const uint32_t slot = (item0 + i) & 1u, tile = tile0 + i / kTiles, q = i % kTiles;
-          ok = mbar_wait(&sh->p_full[slot], ((item0 + i) >> 1) & 1u, abort);
-#pragma unroll
-          for (int h = 0; h < C::kVStages; ++h) {
-            const uint32_t v = C::kVStages * tile + h, s = v % C::kVRing;
-            if (q == 0) ok = ok && mbar_wait(&sh->v_full[s], (v / C::kVRing) & 1u, abort);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t b0 = smem_u32(sV + s * C::kVBytes);
-#pragma unroll
-            for (int k = 0; k < C::kVTok / 16; ++k)  // 16 tokens: eight columns of P, 16 rows of V
-              umma_f16_ts(tmem + C::kO + q * kD, tmem + 128 * slot + C::kVTok / 2 * h + 8 * k,
-                          smem_desc_sw128(b0 + 2048 * k, C::kVTok * 128, 1024), id_o,
-                          (i >= kTiles || h + k != 0) ? 1u : 0u);
-            if (q == kTiles - 1) umma_commit(&sh->v_empty[s]);
-          }
-          umma_commit(&sh->o_full[slot]);
-          if (ok && i + 2 < items) ok = scores(i + 2);
+          umma_commit(&sh->s_full[buffer]);
+          if (q == kTiles - 1) umma_commit(&sh->k_empty[k_slot]);
         }
-        tile0 += tiles;
-        item0 += items;
+        __syncwarp();
+        if (q == kTiles - 1 && ++k_slot == C::kKRing) k_slot = 0, k_phase ^= 1u;
+      };
+      while (ok && walk.next(p, &g)) {
+        const int tiles = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
+        wait(&sh->q_full, seg & 1u);
+        scores(item & 1u, 0);
+        if (kTiles == 2) scores((item + 1) & 1u, 1);
+        else if (tiles > 1) scores((item + 1) & 1u, 0);
+        for (int n = 0; ok && n < tiles; ++n) {
+          const uint32_t v_slot0 = v_slot, v_phase0 = v_phase;
+#pragma unroll
+          for (int q = 0; q < kTiles; ++q, ++item) {
+            const uint32_t buffer = item & 1u;
+            wait(&sh->p_full[buffer], (item >> 1) & 1u);
+            v_slot = v_slot0, v_phase = v_phase0;
+#pragma unroll
+            for (int h = 0; h < C::kVStages; ++h) {
+              if (q == 0) wait(&sh->v_full[v_slot], v_phase);
+              if (ok && elect_one()) {
+                const uint32_t b0 = v_s + v_slot * C::kVBytes;
+#pragma unroll
+                for (int k = 0; k < C::kVTok / 16; ++k)  // 16 tokens: eight columns of P, 16 rows of V
+                  umma_f16_ts(tb + C::kO + q * kD, tb + 128 * buffer + C::kVTok / 2 * h + 8 * k,
+                              smem_desc_sw128(b0 + 2048 * k, C::kVTok * 128, 1024), id_o,
+                              (n > 0 || h + k != 0) ? 1u : 0u);
+                if (q == kTiles - 1) umma_commit(&sh->v_empty[v_slot]);
+                if (h == C::kVStages - 1) umma_commit(&sh->o_full[buffer]);
+              }
+              __syncwarp();
+              if (++v_slot == C::kVRing) v_slot = 0, v_phase ^= 1u;
+            }
+            if (kTiles == 2 ? n + 1 < tiles : n + 2 < tiles) scores(buffer, q);
+          }
+        }
         ++seg;
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         set_error(p.g.err, RIMURU_DEV_TIMEOUT);
         sh->abort = 1;
       }
-      umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
+      if (elect_one()) umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
+      __syncwarp();
       volatile int never = 0;
       mbar_wait(&sh->drain, 0, &never);
     }
