@@ -79,35 +79,35 @@ __device__ __forceinline__ TileSpan unit_span(const AttnArgs& p, const SeqShape&
 // Sum of floor((a i + b) / 128) over 0 <= i < n; a > 0, b >= 0.  Whole parts of
 // a / m and b / m are taken out, and what is left counts lattice points under a
 // line, which are counted along the other axis with smaller numbers.
-__device__ __forceinline__ int64_t floor_sum(int64_t n, uint32_t a, uint32_t b) {
-  int64_t sum = 0;
-  uint32_t m = kTileTokens;
+__device__ __forceinline__ int floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+  uint32_t sum = 0, m = kTileTokens;  // a count of tiles: fits an int (checked on the host)
   while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const uint64_t top = a * static_cast<uint64_t>(n) + b;
+    const uint32_t qa = a / m, qb = b / m;
+    sum += static_cast<uint32_t>(static_cast<uint64_t>(n) * (n - 1) / 2) * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const uint32_t top = a * n + b;
     if (top < m) break;
-    n = static_cast<int64_t>(top / m);
-    b = static_cast<uint32_t>(top % m);
+    n = top / m;
+    b = top - n * m;
     const uint32_t x = m;
     m = a;
     a = x;
   }
-  return sum;
+  return static_cast<int>(sum);
 }
 // Tiles of the first w units of one head of a sequence (all of them full units).
 __device__ __forceinline__ int tiles_before(const AttnArgs& p, const SeqShape& s, int w) {
   const int q = p.unit_q, base = s.len - s.n;  // unit v: positions base + v q .. base + (v + 1) q - 1
   const int v0 = base + q > 0 ? 0 : -base / q;   // units before end at or below position 0
-  int64_t n = 0;
+  int n = 0;
   if (w > v0) n = floor_sum(w - v0, q, base + (v0 + 1) * q + kTileTokens - 1);
   if (p.window > 0) {
     const int out = p.window - 1 - base;  // first position minus `out` leaves the window's reach
     const int v1 = out <= 0 ? 0 : (out + q - 1) / q;
     if (w > v1) n -= floor_sum(w - v1, q, base + v1 * q - p.window + 1);
   }
-  return static_cast<int>(n);
+  return n;
 }
 // Tiles of one head of a sequence, over all its units.
 __device__ __forceinline__ int pair_tiles(const AttnArgs& p, const SeqShape& s) {
@@ -185,23 +185,33 @@ __device__ __forceinline__ void find_run(const AttnArgs& p, int c, int* scratch,
       s = seq_shape(p, ++b);
       n = pair_tiles(p, s);
     }
-    int h = 0, w = 0;
+    int h = 0;
     while (at >= n) at -= n, ++h;
-    const int u = units_of(p, s);
-    if (u > 1) {  // the last unit with at most `at` tiles before it
-      int hi = u;
-      while (hi - w > 1) {
-        const int mid = (w + hi) >> 1;
-        if (tiles_before(p, s, mid) <= at) w = mid;
-        else hi = mid;
-      }
-      at -= tiles_before(p, s, w);
-    }
     out->b = b;
     out->h = h;
-    out->w = w;
+    out->w = 0;
     out->at = at;
     out->s = s;
+  }
+  __syncthreads();
+  if (p.units_per_pair == 1 || tiles == 0) return;
+  // the unit: the last one with at most `at` tiles before it, one thread per group of units
+  const SeqShape s = out->s;
+  const int at = out->at, u = units_of(p, s), per = (u + nt - 1) / nt;
+  const int w0 = t * per, w1 = min(u, w0 + per);
+  if (w0 < u) {
+    int n = tiles_before(p, s, w0);
+    const int after = w1 < u ? tiles_before(p, s, w1) : at + 1;
+    if (n <= at && at < after) {
+      int w = w0;
+      for (; w + 1 < w1; ++w) {
+        const TileSpan x = unit_span(p, s, w);
+        if (n + x.last - x.first > at) break;
+        n += x.last - x.first;
+      }
+      out->w = w;
+      out->at = at - n;
+    }
   }
   __syncthreads();
 }

@@ -61,8 +61,11 @@ struct TileCfg {
   static constexpr uint32_t kO = 256;                           // TMEM column of O; scores are at 0 and 128
 };
 
-struct Meta {  // a 16-token group of a tile
-  float k, v;  // scales; v == 0: no such page
+struct __align__(16) Meta {  // a 16-token group of a tile
+  float k;      // scale of K
+  float add;    // log2 of the scale of V
+  float inv;    // 1 / scale of V
+  int page;     // -1: none
 };
 struct TileShared {
   uint64_t k_full[4], k_empty[4];
@@ -76,9 +79,8 @@ struct TileShared {
   RunStart run;
   int scratch[16];
   Meta meta[kMetaRing][kGroups];
-  int page[kMetaRing][kGroups];   // of each group, -1: none
-  int gap[kMetaRing];             // some group of the tile has no page
-  float row_scale[128];           // one query tile: score per unit of S and K scale
+  uint32_t seen[kMetaRing][4];    // a bit per token of the tile: its group has a page
+  float row_max[2][128];          // one query tile: largest magnitudes of the halves of Q's rows
   float other[2][2][128];         // one query tile: row maxima, and sums, of the two halves
 };
 
@@ -104,6 +106,22 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) { ret
 __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
 }
 // Holds in all 256 softmax threads (barrier 2).
 __device__ __forceinline__ bool softmax_and(bool v) {
@@ -242,12 +260,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The tile's pages and scales by groups of 16 tokens.  Their last readers, eight
           // tiles back, were done before the K tile just waited for could be reused.
           const uint32_t m = tile % kMetaRing;
-          if (lane >= at && lane < at + boxes)
-            for (int k = 0; k < groups; ++k) {
-              sh->meta[m][(lane - at) * groups + k] = {ks, vs};
-              sh->page[m][(lane - at) * groups + k] = page;
-            }
-          if (lane == 0) sh->gap[m] = which != (1u << boxes) - 1u;
+          if (lane >= at && lane < at + boxes) {
+            const int e = static_cast<int>(__float_as_uint(vs) >> 23) - 127;
+            const Meta x = {page >= 0 ? ks : 1.f, page >= 0 ? static_cast<float>(e) : 0.f,
+                            page >= 0 ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f, page};
+            for (int k = 0; k < groups; ++k) sh->meta[m][(lane - at) * groups + k] = x;
+          }
+          if (lane < 4) {  // 32 tokens a word: a page of 64 fills two, of 16 half of one
+            const uint32_t two = log_p == 4 ? which >> (2 * lane) & 3u
+                                            : (which >> (lane >> (log_p - 5)) & 1u) * 3u;
+            sh->seen[m][lane] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->meta_full[m]);
           at += boxes;
@@ -376,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const int r = C::kVTok * lh + r0 + k * kStep;
-        const int page = sh->page[ltile % kMetaRing][r >> 4];
+        const int page = sh->meta[ltile % kMetaRing][r >> 4].page;
         x[k] = make_uint4(0, 0, 0, 0);
         if (page >= 0)
           x[k] = *reinterpret_cast<const uint4*>(p.g.pool + page * p.g.page_bytes + base +
@@ -429,89 +452,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && walk.next(p, &g)) {
       const int rows = (g.i1 - g.i0) * p.group;
-      // Q of the segment, as parts: warp `quad` writes its own 32 rows, one at a
-      // time (with one query tile the two warpgroups take every other row)
-      float c_row = 1e-30f;  // score per unit of S and K scale; never 0, so masked scores stay masked
-      constexpr int kPer = kD / 32;
-      const int q_first = kTiles == 2 ? 0 : wg, q_step = kTiles == 2 ? 1 : 2;
-      const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
-      for (int k0 = q_first; k0 < 32; k0 += 4 * q_step) {
-        T raw[4][kPer];
+      // keys [j_lo, j_hi) of this thread's row; rows past the unit see every column and are
+      // not written
+      const int r = qt * 128 + row, qi = r / p.group, gi = r - qi * p.group;
+      const bool real = r < rows;
+      // Q of the row, as parts; with one query tile the two warpgroups halve the row
+      constexpr int kQ = kTiles == 2 ? kD : kD / 2;
+      const int d0q = kTiles == 2 ? 0 : wg * kQ;
+      float c_row;  // score per unit of S and K scale; never 0, so masked scores stay masked
+      {
+        uint4 raw[kQ / 8];
+        const T* src = static_cast<const T*>(p.q) + (g.s.row0 + g.i0 + qi) * p.q_ts +
+                       (g.h * p.group + gi) * p.q_hs + d0q;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = qt * 128 + quad * 32 + k0 + k * q_step;
-          if (r < rows) {
-            const int i = r / p.group;
-            const T* src = static_cast<const T*>(p.q) + (g.s.row0 + g.i0 + i) * p.q_ts +
-                           (g.h * p.group + r - i * p.group) * p.q_hs + lane * kPer;
-            if constexpr (kPer == 8) *reinterpret_cast<uint4*>(raw[k]) = *reinterpret_cast<const uint4*>(src);
-            else if constexpr (kPer == 4) *reinterpret_cast<uint2*>(raw[k]) = *reinterpret_cast<const uint2*>(src);
-            else *reinterpret_cast<uint32_t*>(raw[k]) = *reinterpret_cast<const uint32_t*>(src);
-          } else {
-            uint32_t* z = reinterpret_cast<uint32_t*>(raw[k]);
+        for (int k = 0; k < kQ / 8; ++k)
+          raw[k] = real ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+        float amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < kPer / 2; ++i) z[i] = 0u;
-          }
+        for (int k = 0; k < kQ / 8; ++k) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(to_f(reinterpret_cast<const T*>(&raw[k])[i])));
         }
+        if (kTiles == 1) {
+          sh->row_max[wg][row] = amax;
+          ok = softmax_and(ok);
+          if (!ok) break;
+          amax = fmaxf(amax, sh->row_max[wg ^ 1][row]);
+        }
+        // power of two that brings the row's largest magnitude into (224, 448]; the sign of
+        // the scale goes into Q, so that a larger S is always a larger score
+        const uint32_t ab = __float_as_uint(amax);
+        const int e = max(-100, min(100, static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u)));
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23 | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
+        c_row = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(p.scale_log2), 1e-30f);
+        if (!(amax <= 3.4028234664e38f)) c_row = __int_as_float(0x7FFFFFFF);  // an infinite query: NaN
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rl = k0 + k * q_step;  // row within the warp's 32
-          float x[kPer], amax = 0.f;
+        for (int k = 0; k < kQ / 16; ++k) {  // 16 codes of each part at a time
+          float x[16];
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            x[i] = to_f(raw[k][i]);
-            amax = fmaxf(amax, fabsf(x[i]));
-          }
-          amax = warp_max(amax);
-          // power of two that brings the row's largest magnitude into (224, 448]
-          const uint32_t ab = __float_as_uint(amax);
-          const int e = max(-100, min(100, static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u)));
-          const float inv = sign * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          // an infinite query has no finite score: its row becomes NaN
-          const float scale = amax <= 3.4028234664e38f
-                                  ? fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) *
-                                              fabsf(p.scale_log2),
-                                          1e-30f)
-                                  : __int_as_float(0x7FFFFFFF);
-          if (kTiles == 2) {
-            if (lane == rl) c_row = scale;
-          } else if (lane == 0) {
-            sh->row_scale[quad * 32 + rl] = scale;
-          }
-          const int d0 = lane * kPer, sl = d0 / kRowBytes;
-          uint8_t* dst = sQ + qt * C::kKBytes + sl * C::kSlabBytes +
-                         swz<kRowBytes>(quad * 32 + rl, d0 % kRowBytes);
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) x[i] *= inv;
+          for (int i = 0; i < 16; ++i) x[i] = to_f(reinterpret_cast<const T*>(&raw[2 * k])[i]) * inv;
+          const int d = d0q + 16 * k;
+          uint8_t* dst = sQ + qt * C::kKBytes + d / kRowBytes * C::kSlabBytes + swz<kRowBytes>(row, d % kRowBytes);
 #pragma unroll
           for (int part = 0; part < kQParts; ++part) {
+            uint32_t c[4];
 #pragma unroll
-            for (int i = 0; i < kPer; i += 2) {
-              const uint32_t code = e4m3x2(x[i], x[i + 1]);
-              const float2 f = from_e4m3x2(code);
-              x[i] -= f.x;
-              x[i + 1] -= f.y;
-              *reinterpret_cast<uint16_t*>(dst + part * kTiles * C::kKBytes + i) = static_cast<uint16_t>(code);
+            for (int i = 0; i < 16; i += 4) {
+              const uint32_t lo2 = e4m3x2(x[i], x[i + 1]), hi2 = e4m3x2(x[i + 2], x[i + 3]);
+              c[i / 4] = lo2 | hi2 << 16;
+              if (part + 1 < kQParts) {
+                const float2 f = from_e4m3x2(lo2), h = from_e4m3x2(hi2);
+                x[i] -= f.x, x[i + 1] -= f.y, x[i + 2] -= h.x, x[i + 3] -= h.y;
+              }
             }
+            *reinterpret_cast<uint4*>(dst + part * kTiles * C::kKBytes) = make_uint4(c[0], c[1], c[2], c[3]);
           }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_full);
-      if (kTiles == 1) {
-        if (!softmax_and(ok)) {
-          ok = false;
-          break;
-        }
-        c_row = sh->row_scale[row];
-      }
-      // keys [j_lo, j_hi) of this row; rows past the unit see every column and are not written
-      const int r = qt * 128 + row, qi = r / p.group, gi = r - qi * p.group;
-      const bool real = r < rows;
       const int pos = g.s.len - g.s.n + g.i0 + qi;
       const int j_hi = real ? min(pos + 1, g.s.len) : 0x7FFFFFFF;
-      const int j_lo = real && p.window > 0 ? pos - p.window + 1 : -0x7FFFFFFF;
+      const int j_lo = real && p.window > 0 ? max(0, pos - p.window + 1) : 0;
       float ref = kNoRef, l = 0.f;
       const int n_tiles = g.t1 - g.t0;
       for (int n = 0; n < n_tiles; ++n) {
@@ -526,45 +529,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + 128 * slot + lane_off;
         // Scores come 32 columns at a time, the next 32 on their way: read once for the
         // maximum and, where the row is one thread's, again for the weights (64 of them
-        // stay in registers otherwise).
-        uint32_t s[2][32];
+        // stay in registers otherwise).  The loops are kept rolled: two warpgroups and
+        // the V warps share the instruction caches.
+        uint32_t s0[32], s1[32];
         const int j0 = t * kTileTokens + col0;
-        const bool edge = __any_sync(0xffffffffu, sh->gap[m] != 0 || j_lo > j0 || j_hi < j0 + kCols);
-        const auto hide = [&](uint32_t(&v)[32], int k0) {  // scores that the row does not see
+        bool edge = j_lo > j0 || j_hi < j0 + kCols;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int j = j0 + k0 + k;
-            const bool see = j >= j_lo && j < j_hi && sh->meta[m][(col0 + k0 + k) / 16].v != 0.f;
-            if (!see) v[k] = 0xFF800000u;
-          }
-        };
-        // x + k of a 16-column group is S * mul + add
-        const auto affine = [&](int q, float* mul, float* add) {
-          const Meta kv = sh->meta[m][col0 / 16 + q];
-          *mul = c_row * (kv.v != 0.f ? kv.k : 1.f);
-          *add = static_cast<float>(static_cast<int>(__float_as_uint(kv.v) >> 23) - 127);
+        for (int k = 0; k < kCols / 32; ++k) edge |= sh->seen[m][col0 / 32 + k] != 0xFFFFFFFFu;
+        edge = __any_sync(0xffffffffu, edge);
+        const auto hide = [&](uint32_t(&v)[32], int k0) {  // scores that the row does not see
+          const int lo = max(0, min(32, j_lo - (j0 + k0))), hi = max(0, min(32, j_hi - (j0 + k0)));
+          uint32_t see = sh->seen[m][(col0 + k0) / 32];
+          see &= static_cast<uint32_t>((1ull << hi) - (1ull << lo)) & (hi > lo ? 0xFFFFFFFFu : 0u);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
         };
         float top = -INFINITY;
-        tmem_ld32(tS + col0, s[0]);
-        tmem_ld_wait32(s[0]);
-#pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) {
-          if (c + 1 < kCols / 32) tmem_ld32(tS + col0 + 32 * (c + 1), s[(c + 1) & 1]);
-          uint32_t(&v)[32] = s[c & 1];
-          if (edge) hide(v, 32 * c);
+        const auto maximum = [&](uint32_t(&v)[32], int k0) {  // x + k of a group is S * mul + add
+          if (edge) hide(v, k0);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            float mul, add, x = __uint_as_float(v[16 * q]);
-            affine(2 * c + q, &mul, &add);
+            const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + k0) / 16 + q]);
+            float x = __uint_as_float(v[16 * q]);
 #pragma unroll
             for (int k = 1; k < 15; k += 2)
               x = fmaxf(fmaxf(x, __uint_as_float(v[16 * q + k])), __uint_as_float(v[16 * q + k + 1]));
             x = fmaxf(x, __uint_as_float(v[16 * q + 15]));
-            top = fmaxf(top, x * mul + add);
+            top = fmaxf(top, x * (c_row * kv.x) + kv.y);
           }
-          if (c + 1 < kCols / 32) tmem_ld_wait32(s[(c + 1) & 1]);
+        };
+        tmem_ld32(tS + col0, s0);
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 64) {
+          tmem_ld_wait32(s0);
+          tmem_ld32(tS + col0 + c + 32, s1);
+          maximum(s0, c);
+          tmem_ld_wait32(s1);
+          if (kTiles == 2) tmem_ld32(tS + ((c + 64) & 127), s0);  // in the end: the first again
+          maximum(s1, c + 32);
         }
-        if (kTiles == 2) tmem_ld32(tS, s[0]);
         if (kTiles == 1) {  // the other half of the row
           sh->other[n & 1][wg][row] = top;
           ok = softmax_and(ok);
@@ -596,33 +599,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float base = kWeightTop - ref;
-        if (kTiles == 2) tmem_ld_wait32(s[0]);
-#pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) {
-          uint32_t(&v)[32] = s[c & 1];
-          if (kTiles == 2) {
-            if (c + 1 < kCols / 32) tmem_ld32(tS + 32 * (c + 1), s[(c + 1) & 1]);
-            if (edge) hide(v, 32 * c);
-          }
+        const auto weights = [&](uint32_t(&v)[32], int k0) {
           uint32_t w[16];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            float mul, add, sum = 0.f;
-            affine(2 * c + q, &mul, &add);
-            const float a = add + base;
+            const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + k0) / 16 + q]);
+            const float mul = c_row * kv.x, a = kv.y + base;
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              const float x = ex2(__uint_as_float(v[16 * q + k]) * mul + a);
-              const float y = ex2(__uint_as_float(v[16 * q + k + 1]) * mul + a);
-              sum += x + y;
-              const __half2 h = __floats2half2_rn(x, y);
+              const float2 x = fma2(make_float2(__uint_as_float(v[16 * q + k]), __uint_as_float(v[16 * q + k + 1])),
+                                    make_float2(mul, mul), make_float2(a, a));
+              const float2 y = make_float2(ex2(x.x), ex2(x.y));
+              sum = add2(sum, y);
+              const __half2 h = __floats2half2_rn(y.x, y.y);
               w[8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            l += sum * ex2(-add);
+            l += (sum.x + sum.y) * kv.z;
           }
           // the weights lie where scores were that this row has read
-          tmem_st16(tS + col0 / 2 + 16 * c, w);
-          if (kTiles == 2 && c + 1 < kCols / 32) tmem_ld_wait32(s[(c + 1) & 1]);
+          tmem_st16(tS + (col0 + k0) / 2, w);
+        };
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 64) {
+          if (kTiles == 2) {
+            tmem_ld_wait32(s0);
+            tmem_ld32(tS + c + 32, s1);
+            if (edge) hide(s0, c);
+          }
+          weights(s0, c);
+          if (kTiles == 2) {
+            tmem_ld_wait32(s1);
+            if (c + 64 < kCols) tmem_ld32(tS + c + 64, s0);
+            if (edge) hide(s1, c + 32);
+          }
+          weights(s1, c + 32);
         }
         tmem_st_wait();
         tc_fence_before();
