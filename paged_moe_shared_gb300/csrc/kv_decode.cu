@@ -715,8 +715,8 @@ cudaError_t launch_dim(const AttnArgs& a, const CUtensorMap& tm, cudaStream_t s)
 // ---------------------------------------------------------------------- join
 // Adds the runs' partial rows, weighted by their share of the softmax sum, in
 // run order.  Rows of units without any tile become zero here.  A CTA takes
-// kRows rows of a unit; its warps split the rows, or with one row the runs
-// (few units cut into many runs: a long context), whose sums meet in shared
+// eight rows of a unit, one per warp, or one row, whose runs the warps split
+// (few units cut into many runs: a long context); their sums meet in shared
 // memory in warp order.
 constexpr int kJoinWarps = 8;
 
@@ -743,8 +743,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
   const bool none = t.first >= t.last;
   const int2 j = none ? make_int2(0, -1) : *join_of(p, b, h, w);
   if (j.x < 0) return;  // finished by one run
-  const int r0 = kSplitRuns ? blockIdx.y : warp, step = kSplitRuns ? p.unit_rows : kJoinWarps;
-  for (int r = r0; r < rows; r += step) {
+  const int r = kSplitRuns ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
+  if (r < rows) {
     const auto slot = [&](int c) { return part_slot(p, c, c == j.x) + r; };
     float top = -INFINITY, sum = 0.f, acc[kPer];
 #pragma unroll
@@ -801,7 +801,8 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t s) {
   // With four runs a unit or more, one CTA per row whose warps split the runs.
   const bool split = units * 4 <= a.runs;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units), split ? static_cast<unsigned>(a.unit_rows) : 1u);
+  cfg.gridDim = dim3(static_cast<unsigned>(units),
+                     static_cast<unsigned>(split ? a.unit_rows : a.unit_rows / kJoinWarps));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr{};

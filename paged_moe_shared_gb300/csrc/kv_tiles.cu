@@ -81,7 +81,8 @@ struct TileShared {
   Meta meta[kMetaRing][kGroups];
   uint32_t seen[kMetaRing][4];    // a bit per token of the tile: its group has a page
   float row_max[2][128];          // one query tile: largest magnitudes of the halves of Q's rows
-  float other[2][2][128];         // one query tile: row maxima, and sums, of the two halves
+  float other[2][128];            // one query tile: row maxima of the halves
+  float row_sum[2][128];          // and their sums
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -135,6 +136,29 @@ __device__ __forceinline__ bool softmax_and(bool v) {
       : "r"(v ? 1u : 0u)
       : "memory");
   return r != 0;
+}
+__device__ __forceinline__ bool softmax_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "bar.red.or.pred b, 2, 256, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}\n"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+// Registers per thread of a warpgroup; the four groups' shares add up to the 4 x 128
+// that the block was launched with (2 x 176 + 2 x 80 = 512).
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 // Byte offset of byte d of row r in a swizzled K-major block.
 template <int kRowBytes>
@@ -203,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Segment g;
 
   if (warp >= 12) {
+    regs_down<kOtherRegs>();
     if (warp == 12) {
       // -------------------------------------------------------------- K copies
       // The warp holds the ids and scales of 32 pages, one per lane (`boxes`
@@ -372,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&sh->drain, 0, &never);
     }
   } else if (warp >= 8) {
+    regs_down<kOtherRegs>();
     // ---------------------------------------------------------------------- V
     // A stage is kVTok tokens: thread `t128` takes 16 codes (chunk c) of the
     // tokens r0, r0 + kStep, ...; the next two stages are loaded ahead.
@@ -442,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax
+    regs_up<kSoftmaxRegs>();
     const int wg = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;  // row of the query tile, and TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -527,56 +554,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kTiles == 2 && !ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + 128 * slot + lane_off;
-        // Scores come 32 columns at a time, the next 32 on their way: read once for the
-        // maximum and, where the row is one thread's, again for the weights (64 of them
-        // stay in registers otherwise).  The loops are kept rolled: two warpgroups and
-        // the V warps share the instruction caches.
-        uint32_t s0[32], s1[32];
         const int j0 = t * kTileTokens + col0;
         bool edge = j_lo > j0 || j_hi < j0 + kCols;
 #pragma unroll
         for (int k = 0; k < kCols / 32; ++k) edge |= sh->seen[m][col0 / 32 + k] != 0xFFFFFFFFu;
         edge = __any_sync(0xffffffffu, edge);
-        const auto hide = [&](uint32_t(&v)[32], int k0) {  // scores that the row does not see
-          const int lo = max(0, min(32, j_lo - (j0 + k0))), hi = max(0, min(32, j_hi - (j0 + k0)));
-          uint32_t see = sh->seen[m][(col0 + k0) / 32];
-          see &= static_cast<uint32_t>((1ull << hi) - (1ull << lo)) & (hi > lo ? 0xFFFFFFFFu : 0u);
+        const auto hide = [&](uint32_t(&v)[32], int k0) {  // -inf where the row does not see
+          if (edge) {
+            const int lo = max(0, min(32, j_lo - (j0 + k0))), hi = max(0, min(32, j_hi - (j0 + k0)));
+            uint32_t see = sh->seen[m][(col0 + k0) / 32];
+            see &= static_cast<uint32_t>((1ull << hi) - (1ull << lo)) & (hi > lo ? 0xFFFFFFFFu : 0u);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
-        };
-        float top = -INFINITY;
-        const auto maximum = [&](uint32_t(&v)[32], int k0) {  // x + k of a group is S * mul + add
-          if (edge) hide(v, k0);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + k0) / 16 + q]);
-            float x = __uint_as_float(v[16 * q]);
-#pragma unroll
-            for (int k = 1; k < 15; k += 2)
-              x = fmaxf(fmaxf(x, __uint_as_float(v[16 * q + k])), __uint_as_float(v[16 * q + k + 1]));
-            x = fmaxf(x, __uint_as_float(v[16 * q + 15]));
-            top = fmaxf(top, x * (c_row * kv.x) + kv.y);
+            for (int k = 0; k < 32; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
           }
         };
-        tmem_ld32(tS + col0, s0);
+        // The weights are taken with the reference as it stands, and their maximum on the
+        // way: only a tile that passes it by more than the slack is looked through for its
+        // largest score, and its weights taken again.  A group's x + k is S * mul + add.
+        uint32_t w[kCols / 2];
+        float sum_l;
+        while (true) {
+          const float base = kWeightTop - ref;
+          float most = 0.f, most2 = 0.f;
+          sum_l = 0.f;
+          uint32_t s0[32], s1[32];  // 32 columns at hand, 32 on their way
+          tmem_ld32(tS + col0, s0);
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            uint32_t(&v)[32] = c & 32 ? s1 : s0;
+            tmem_ld_wait32(v);
+            if (c + 32 < kCols) tmem_ld32(tS + col0 + c + 32, c & 32 ? s0 : s1);
+            hide(v, c);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + c) / 16 + q]);
+              const float mul = c_row * kv.x, a = kv.y + base;
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float2 x = fma2(make_float2(__uint_as_float(v[16 * q + k]), __uint_as_float(v[16 * q + k + 1])),
+                                      make_float2(mul, mul), make_float2(a, a));
+                const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                sum = add2(sum, y);
+                if (k & 2) most2 = fmaxf(fmaxf(most2, y.x), y.y);
+                else most = fmaxf(fmaxf(most, y.x), y.y);
+                const __half2 h = __floats2half2_rn(y.x, y.y);
+                w[c / 2 + 8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              sum_l += (sum.x + sum.y) * kv.z;
+            }
+          }
+          most = fmaxf(most, most2);
+          constexpr float kMost = static_cast<float>(1 << static_cast<int>(kWeightTop + kWeightSlack));
+          if (kTiles == 2) {
+            if (!__any_sync(0xffffffffu, most > kMost)) break;
+          } else {
+            if (!softmax_or(most > kMost || !ok)) break;
+            if (!(ok = softmax_and(ok))) break;
+          }
+          float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < kCols; c += 64) {
-          tmem_ld_wait32(s0);
-          tmem_ld32(tS + col0 + c + 32, s1);
-          maximum(s0, c);
-          tmem_ld_wait32(s1);
-          if (kTiles == 2) tmem_ld32(tS + ((c + 64) & 127), s0);  // in the end: the first again
-          maximum(s1, c + 32);
-        }
-        if (kTiles == 1) {  // the other half of the row
-          sh->other[n & 1][wg][row] = top;
-          ok = softmax_and(ok);
-          if (!ok) break;
-          top = fmaxf(top, sh->other[n & 1][wg ^ 1][row]);
-        }
-        const bool raise = top > ref + kWeightSlack;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float now = raise ? top : ref, f = ex2(ref - now);
+          for (int c = 0; c < kCols; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(tS + col0 + c, v);
+            tmem_ld_wait32(v);
+            hide(v, c);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + c) / 16 + q]);
+              float x = __uint_as_float(v[16 * q]);
+#pragma unroll
+              for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[16 * q + k]));
+              top = fmaxf(top, x * (c_row * kv.x) + kv.y);
+            }
+          }
+          if (kTiles == 1) {  // the other half of the row
+            sh->other[wg][row] = top;
+            if (!(ok = softmax_and(ok))) break;
+            top = fmaxf(top, sh->other[wg ^ 1][row]);
+          }
+          const float now = top > ref + kWeightSlack ? top : ref, f = ex2(ref - now);
           ref = now;
           l *= f;
           if (n > 0) {  // O of the row is complete up to the tile before: rescale it
@@ -590,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t v[32];
               const uint32_t at = tO + (kTiles == 2 ? 0 : wg * kO) + k;
               tmem_ld32(at, v);
-              tmem_ld_wait();
+              tmem_ld_wait32(v);
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
               tmem_st32(at, v);
@@ -598,43 +655,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
         }
-        const float base = kWeightTop - ref;
-        const auto weights = [&](uint32_t(&v)[32], int k0) {
-          uint32_t w[16];
+        if (kTiles == 1 && !ok) break;
+        l += sum_l;
+        // The weights lie where the scores were (with one query tile, where the other half
+        // had its own: it has read them, or the barrier above would not have let go).
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + k0) / 16 + q]);
-            const float mul = c_row * kv.x, a = kv.y + base;
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float2 x = fma2(make_float2(__uint_as_float(v[16 * q + k]), __uint_as_float(v[16 * q + k + 1])),
-                                    make_float2(mul, mul), make_float2(a, a));
-              const float2 y = make_float2(ex2(x.x), ex2(x.y));
-              sum = add2(sum, y);
-              const __half2 h = __floats2half2_rn(y.x, y.y);
-              w[8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            l += (sum.x + sum.y) * kv.z;
-          }
-          // the weights lie where scores were that this row has read
-          tmem_st16(tS + (col0 + k0) / 2, w);
-        };
-#pragma unroll 1
-        for (int c = 0; c < kCols; c += 64) {
-          if (kTiles == 2) {
-            tmem_ld_wait32(s0);
-            tmem_ld32(tS + c + 32, s1);
-            if (edge) hide(s0, c);
-          }
-          weights(s0, c);
-          if (kTiles == 2) {
-            tmem_ld_wait32(s1);
-            if (c + 64 < kCols) tmem_ld32(tS + c + 64, s0);
-            if (edge) hide(s1, c + 32);
-          }
-          weights(s1, c + 32);
-        }
+        for (int c = 0; c < kCols / 2; c += 32)
+          tmem_st32(tS + col0 / 2 + c, *reinterpret_cast<const uint32_t(*)[32]>(&w[c]));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -649,10 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
       }
       if (kTiles == 1) {  // the two halves of the row's sum
-        sh->other[n_tiles & 1][wg][row] = l;
+        sh->row_sum[wg][row] = l;
         ok = softmax_and(ok);
         if (!ok) break;
-        l = sh->other[n_tiles & 1][0][row] + sh->other[n_tiles & 1][1][row];
+        l = sh->row_sum[0][row] + sh->row_sum[1][row];
       }
       if (!ok) break;
       tc_fence_after();
