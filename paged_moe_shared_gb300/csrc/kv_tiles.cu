@@ -55,8 +55,13 @@ struct TileCfg {
   static constexpr int kVTok = kD <= 128 ? 64 : 32;             // tokens of a V stage
   static constexpr int kVStages = kTileTokens / kVTok;          // stages of a tile
   static constexpr int kVBytes = kVTok * kD * 2;                // [64 f16 of a token: 128 bytes][tokens]
-  static constexpr int kVRing = kD == 256 && kQParts == 3 ? 3 : 4;
-  static constexpr int kSmem = 1024 + kQBytes + kKRing * kKBytes + kVRing * kVBytes;
+  static constexpr bool kWide = kQParts == 3 && (kD == 256 || kTiles == 2);  // Q takes 96 KiB
+  static constexpr int kVRing = kWide ? 2 : 4;
+  static constexpr int kVRaw = kVTok * kD;                      // codes of a stage
+  static constexpr int kFifo = kD == 256 ? (kWide ? 2 : 3) : kTiles == 2 ? 4 : 6;  // stages of codes
+  static constexpr int kStage = kD == 64 ? 8 * 4096 : 0;        // output staging; else in Q's place
+  static constexpr int kSmem =
+      1024 + kQBytes + kKRing * kKBytes + kVRing * kVBytes + kFifo * kVRaw + kStage;
   static constexpr int kCols = kTiles == 2 ? 128 : 64;          // score columns of a thread
   static constexpr uint32_t kO = 256;                           // TMEM column of O; scores are at 0 and 128
 };
@@ -80,7 +85,7 @@ struct TileShared {
   int scratch[16];
   Meta meta[kMetaRing][kGroups];
   uint32_t seen[kMetaRing][4];    // a bit per token of the tile: its group has a page
-  float row_max[2][128];          // one query tile: largest magnitudes of the halves of Q's rows
+  float row_scale[2][128];        // of each row: score per unit of S and K scale
   float other[2][128];            // one query tile: row maxima of the halves
   float row_sum[2][128];          // and their sums
 };
@@ -186,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + C::kQBytes;
   uint8_t* sV = sK + C::kKRing * C::kKBytes;
+  uint8_t* sRaw = sV + C::kVRing * C::kVBytes;
   __shared__ TileShared sh_;
   TileShared* sh = &sh_;
   volatile int* abort = &sh->abort;
@@ -399,69 +405,74 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     regs_down<kOtherRegs>();
     // ---------------------------------------------------------------------- V
-    // A stage is kVTok tokens: thread `t128` takes 16 codes (chunk c) of the
-    // tokens r0, r0 + kStep, ...; the next two stages are loaded ahead.
+    // A stage is kVTok tokens: thread `t128` takes 16 codes (chunk c) of the tokens
+    // r0, r0 + kStep, ...  Codes arrive kFifo - 1 stages ahead in a shared-memory
+    // queue of which each thread reads only what it copied itself.
     constexpr int kChunks = kD / 16, kStep = 128 / kChunks, kPer = C::kVTok / kStep;
     const int t128 = threadIdx.x - 256, c = t128 % kChunks, r0 = t128 / kChunks;
     bool ok = true;
-    uint4 raw[2][kPer];
     // the load cursor: stage `lh` of key tile lt, tile `ltile` of the run
     int lt = 0, lh = C::kVStages;
-    uint32_t ltile = 0xFFFFFFFFu;
+    uint32_t ltile = 0xFFFFFFFFu, lslot = 0;
+    const uint8_t* head = nullptr;
     g.t1 = 0;
-    const auto load = [&](uint4(&x)[kPer]) {
+    const auto load = [&]() {
       if (lh == C::kVStages) {
         lh = 0;
         ++ltile;
         if (++lt >= g.t1) {
           walk.next(p, &g);
           lt = g.t0;
+          head = p.g.pool + static_cast<uint64_t>(p.g.kv_heads + g.h) * P * kD + 16 * c;
         }
         ok = mbar_wait(&sh->meta_full[ltile % kMetaRing], (ltile / kMetaRing) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
       }
-      const uint64_t base = static_cast<uint64_t>(p.g.kv_heads + g.h) * P * kD + 16 * c;
+      uint8_t* dst = sRaw + lslot * C::kVRaw + t128 * 16;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const int r = C::kVTok * lh + r0 + k * kStep;
         const int page = sh->meta[ltile % kMetaRing][r >> 4].page;
-        x[k] = make_uint4(0, 0, 0, 0);
-        if (page >= 0)
-          x[k] = *reinterpret_cast<const uint4*>(p.g.pool + page * p.g.page_bytes + base +
-                                                 static_cast<uint64_t>(r & (P - 1)) * kD);
+        if (page >= 0) cp_async16(smem_u32(dst + k * 2048), head + page * p.g.page_bytes + (r & (P - 1)) * kD);
+        else *reinterpret_cast<uint4*>(dst + k * 2048) = make_uint4(0, 0, 0, 0);
       }
       ++lh;
+      if (++lslot == C::kFifo) lslot = 0;
     };
-    const auto store = [&](uint32_t v, const uint4(&x)[kPer]) {
-      const uint32_t s = v % C::kVRing;
-      ok = mbar_wait(&sh->v_empty[s], ((v / C::kVRing) & 1u) ^ 1u, abort) && ok;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      uint8_t* dst = sV + s * C::kVBytes + (c >> 2) * (C::kVTok * 128);
+    const uint32_t total = C::kVStages * sh->run.tiles;
+#pragma unroll 1
+    for (uint32_t v = 0; ok && v < C::kFifo - 1; ++v) {
+      if (v < total) load();
+      cp_async_commit();
+    }
+    uint32_t v_slot = 0, v_phase = 1, raw_slot = 0;
+#pragma unroll 1
+    for (uint32_t v = 0; ok && v < total; ++v) {
+      if (v + C::kFifo - 1 < total) load();
+      cp_async_commit();
+      if (!ok) break;
+      cp_async_wait<C::kFifo - 1>();
+      ok = mbar_wait(&sh->v_empty[v_slot], v_phase, abort);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const uint8_t* src = sRaw + raw_slot * C::kVRaw + t128 * 16;
+      uint8_t* dst = sV + v_slot * C::kVBytes + (c >> 2) * (C::kVTok * 128);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src + k * 2048);
         const int r = r0 + k * kStep, ch = 2 * (c & 3);  // chunks of eight f16 in the 128-byte row
         *reinterpret_cast<uint4*>(dst + r * 128 + (((ch ^ r) & 7) << 4)) =
-            make_uint4(widen(x[k].x, false), widen(x[k].x, true), widen(x[k].y, false), widen(x[k].y, true));
+            make_uint4(widen(x.x, false), widen(x.x, true), widen(x.y, false), widen(x.y, true));
         *reinterpret_cast<uint4*>(dst + r * 128 + ((((ch + 1) ^ r) & 7) << 4)) =
-            make_uint4(widen(x[k].z, false), widen(x[k].z, true), widen(x[k].w, false), widen(x[k].w, true));
+            make_uint4(widen(x.z, false), widen(x.z, true), widen(x.w, false), widen(x.w, true));
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->v_full[s]);
-    };
-    const uint32_t total = C::kVStages * sh->run.tiles;  // even
-    if (total > 0) {
-      load(raw[0]);
-      if (ok) load(raw[1]);
+      if (lane == 0) mbar_arrive(&sh->v_full[v_slot]);
+      if (++v_slot == C::kVRing) v_slot = 0, v_phase ^= 1u;
+      if (++raw_slot == C::kFifo) raw_slot = 0;
     }
-    for (uint32_t v = 0; ok && v < total; v += 2) {
-      store(v, raw[0]);
-      if (ok && v + 2 < total) load(raw[0]);
-      if (ok) store(v + 1, raw[1]);
-      if (ok && v + 3 < total) load(raw[1]);
-    }
+    cp_async_wait_all();  // no copy of this thread is in flight when the CTA exits
     if (!ok && lane == 0) {
       set_error(p.g.err, RIMURU_DEV_TIMEOUT);
       sh->abort = 1;
@@ -475,56 +486,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qt = kTiles == 2 ? wg : 0;             // query tile
     const int col0 = kTiles == 2 ? 0 : 64 * wg;      // first score column of this thread
     const uint32_t tO = tmem + C::kO + qt * kD + lane_off;
+    const uint32_t group_mul = 65536u / p.group + 1;  // r / group = r * group_mul >> 16 for r < 256
     uint32_t tile = 0, item0 = 0;
     bool ok = true;
     while (ok && walk.next(p, &g)) {
       const int rows = (g.i1 - g.i0) * p.group;
       // keys [j_lo, j_hi) of this thread's row; rows past the unit see every column and are
       // not written
-      const int r = qt * 128 + row, qi = r / p.group, gi = r - qi * p.group;
+      const int r = qt * 128 + row, qi = static_cast<int>(r * group_mul >> 16), gi = r - qi * p.group;
       const bool real = r < rows;
-      // Q of the row, as parts; with one query tile the two warpgroups halve the row
-      constexpr int kQ = kTiles == 2 ? kD : kD / 2;
-      const int d0q = kTiles == 2 ? 0 : wg * kQ;
-      float c_row;  // score per unit of S and K scale; never 0, so masked scores stay masked
-      {
-        uint4 raw[kQ / 8];
-        const T* src = static_cast<const T*>(p.q) + (g.s.row0 + g.i0 + qi) * p.q_ts +
-                       (g.h * p.group + gi) * p.q_hs + d0q;
+      // Q of the warp's 32 rows, as parts (with one query tile the two warpgroups take 16
+      // each).  A lane holds eight elements; kLanes lanes are a row.
+      constexpr int kLanes = kD / 8, kRows = 32 / kLanes;  // rows of one load
+      constexpr int kSteps = (kTiles == 2 ? 32 : 16) / kRows, kBatch = kSteps < 8 ? kSteps : 8;
+      const int row0 = quad * 32 + (kTiles == 2 ? 0 : 16 * wg);
+      const T* q_base = static_cast<const T*>(p.q) + (g.s.row0 + g.i0) * p.q_ts + g.h * p.group * p.q_hs +
+                        lane % kLanes * 8;
+      if (kTiles == 1 && !(ok = softmax_and(ok))) break;  // Q's place has been left by all warps
+#pragma unroll 1
+      for (int b0 = 0; b0 < kSteps; b0 += kBatch) {
+        uint4 raw[kBatch];
 #pragma unroll
-        for (int k = 0; k < kQ / 8; ++k)
-          raw[k] = real ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < kQ / 8; ++k) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(to_f(reinterpret_cast<const T*>(&raw[k])[i])));
+        for (int k = 0; k < kBatch; ++k) {
+          const int rr = qt * 128 + row0 + (b0 + k) * kRows + lane / kLanes;
+          const int i = static_cast<int>(rr * group_mul >> 16);
+          raw[k] = make_uint4(0, 0, 0, 0);
+          if (rr < rows)
+            raw[k] = *reinterpret_cast<const uint4*>(q_base + i * p.q_ts + (rr - i * p.group) * p.q_hs);
         }
-        if (kTiles == 1) {
-          sh->row_max[wg][row] = amax;
-          ok = softmax_and(ok);
-          if (!ok) break;
-          amax = fmaxf(amax, sh->row_max[wg ^ 1][row]);
-        }
-        // power of two that brings the row's largest magnitude into (224, 448]; the sign of
-        // the scale goes into Q, so that a larger S is always a larger score
-        const uint32_t ab = __float_as_uint(amax);
-        const int e = max(-100, min(100, static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u)));
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23 | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
-        c_row = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(p.scale_log2), 1e-30f);
-        if (!(amax <= 3.4028234664e38f)) c_row = __int_as_float(0x7FFFFFFF);  // an infinite query: NaN
 #pragma unroll
-        for (int k = 0; k < kQ / 16; ++k) {  // 16 codes of each part at a time
-          float x[16];
+        for (int k = 0; k < kBatch; ++k) {
+          float x[8], amax = 0.f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = to_f(reinterpret_cast<const T*>(&raw[2 * k])[i]) * inv;
-          const int d = d0q + 16 * k;
-          uint8_t* dst = sQ + qt * C::kKBytes + d / kRowBytes * C::kSlabBytes + swz<kRowBytes>(row, d % kRowBytes);
+          for (int i = 0; i < 8; ++i) {
+            x[i] = to_f(reinterpret_cast<const T*>(&raw[k])[i]);
+            amax = fmaxf(amax, fabsf(x[i]));
+          }
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // power of two that brings the row's largest magnitude into (224, 448]; the sign of
+          // the scale goes into Q, so that a larger S is always a larger score
+          const uint32_t ab = __float_as_uint(amax);
+          const int e = max(-100, min(100, static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u)));
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23 | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
+          const int rl = row0 + (b0 + k) * kRows + lane / kLanes;
+          if (lane % kLanes == 0)  // never 0, so masked scores stay masked; an infinite query gives NaN
+            sh->row_scale[qt][rl] =
+                amax <= 3.4028234664e38f
+                    ? fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(p.scale_log2), 1e-30f)
+                    : __int_as_float(0x7FFFFFFF);
+          const int d = lane % kLanes * 8;
+          uint8_t* dst = sQ + qt * C::kKBytes + d / kRowBytes * C::kSlabBytes + swz<kRowBytes>(rl, d % kRowBytes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= inv;
 #pragma unroll
           for (int part = 0; part < kQParts; ++part) {
-            uint32_t c[4];
+            uint32_t c[2];
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = 0; i < 8; i += 4) {
               const uint32_t lo2 = e4m3x2(x[i], x[i + 1]), hi2 = e4m3x2(x[i + 2], x[i + 3]);
               c[i / 4] = lo2 | hi2 << 16;
               if (part + 1 < kQParts) {
@@ -532,13 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x[i] -= f.x, x[i + 1] -= f.y, x[i + 2] -= h.x, x[i + 3] -= h.y;
               }
             }
-            *reinterpret_cast<uint4*>(dst + part * kTiles * C::kKBytes) = make_uint4(c[0], c[1], c[2], c[3]);
+            *reinterpret_cast<uint2*>(dst + part * kTiles * C::kKBytes) = make_uint2(c[0], c[1]);
           }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_full);
+      if (kTiles == 1 && !(ok = softmax_and(ok))) break;  // the other half of the row scales
+      const float c_row = sh->row_scale[qt][row];  // score per unit of S and K scale
       const int pos = g.s.len - g.s.n + g.i0 + qi;
       const int j_hi = real ? min(pos + 1, g.s.len) : 0x7FFFFFFF;
       const int j_lo = real && p.window > 0 ? max(0, pos - p.window + 1) : 0;
@@ -560,108 +581,143 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kCols / 32; ++k) edge |= sh->seen[m][col0 / 32 + k] != 0xFFFFFFFFu;
         edge = __any_sync(0xffffffffu, edge);
         const auto hide = [&](uint32_t(&v)[32], int k0) {  // -inf where the row does not see
-          if (edge) {
-            const int lo = max(0, min(32, j_lo - (j0 + k0))), hi = max(0, min(32, j_hi - (j0 + k0)));
-            uint32_t see = sh->seen[m][(col0 + k0) / 32];
-            see &= static_cast<uint32_t>((1ull << hi) - (1ull << lo)) & (hi > lo ? 0xFFFFFFFFu : 0u);
+          const int lo = max(0, min(32, j_lo - (j0 + k0))), hi = max(0, min(32, j_hi - (j0 + k0)));
+          uint32_t see = sh->seen[m][(col0 + k0) / 32];
+          see &= static_cast<uint32_t>((1ull << hi) - (1ull << lo)) & (hi > lo ? 0xFFFFFFFFu : 0u);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
-          }
+          for (int k = 0; k < 32; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
         };
-        // The weights are taken with the reference as it stands, and their maximum on the
-        // way: only a tile that passes it by more than the slack is looked through for its
-        // largest score, and its weights taken again.  A group's x + k is S * mul + add.
-        uint32_t w[kCols / 2];
-        float sum_l;
-        while (true) {
-          const float base = kWeightTop - ref;
-          float most = 0.f, most2 = 0.f;
-          sum_l = 0.f;
-          uint32_t s0[32], s1[32];  // 32 columns at hand, 32 on their way
-          tmem_ld32(tS + col0, s0);
-#pragma unroll
-          for (int c = 0; c < kCols; c += 32) {
-            uint32_t(&v)[32] = c & 32 ? s1 : s0;
-            tmem_ld_wait32(v);
-            if (c + 32 < kCols) tmem_ld32(tS + col0 + c + 32, c & 32 ? s0 : s1);
-            hide(v, c);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + c) / 16 + q]);
-              const float mul = c_row * kv.x, a = kv.y + base;
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float2 x = fma2(make_float2(__uint_as_float(v[16 * q + k]), __uint_as_float(v[16 * q + k + 1])),
-                                      make_float2(mul, mul), make_float2(a, a));
-                const float2 y = make_float2(ex2(x.x), ex2(x.y));
-                sum = add2(sum, y);
-                if (k & 2) most2 = fmaxf(fmaxf(most2, y.x), y.y);
-                else most = fmaxf(fmaxf(most, y.x), y.y);
-                const __half2 h = __floats2half2_rn(y.x, y.y);
-                w[c / 2 + 8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              sum_l += (sum.x + sum.y) * kv.z;
-            }
-          }
-          most = fmaxf(most, most2);
-          constexpr float kMost = static_cast<float>(1 << static_cast<int>(kWeightTop + kWeightSlack));
-          if (kTiles == 2) {
-            if (!__any_sync(0xffffffffu, most > kMost)) break;
-          } else {
-            if (!softmax_or(most > kMost || !ok)) break;
-            if (!(ok = softmax_and(ok))) break;
-          }
-          float top = -INFINITY;
+        // Multiplies O of the row, complete up to the tile before, by f.
+        const auto rescale = [&](float f) {
+          const uint32_t last = kTiles == 2 ? item - 2 : item - 1;
+          ok = mbar_wait(&sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          constexpr int kO = kTiles == 2 ? kD : kD / 2;
 #pragma unroll 1
-          for (int c = 0; c < kCols; c += 32) {
+          for (int k = 0; k < kO; k += 32) {
             uint32_t v[32];
-            tmem_ld32(tS + col0 + c, v);
+            const uint32_t at = tO + (kTiles == 2 ? 0 : wg * kO) + k;
+            tmem_ld32(at, v);
             tmem_ld_wait32(v);
-            hide(v, c);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + c) / 16 + q]);
-              float x = __uint_as_float(v[16 * q]);
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+            tmem_st32(at, v);
+          }
+          tmem_st_wait();
+        };
+        // Of 32 scores: x + k + shift (a 16-column group's x + k is S * mul + add), in place,
+        // and the largest.
+        const auto logs = [&](uint32_t(&v)[32], int k0, float shift) {
+          float most = -INFINITY, most2 = -INFINITY;
 #pragma unroll
-              for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[16 * q + k]));
-              top = fmaxf(top, x * (c_row * kv.x) + kv.y);
+          for (int q = 0; q < 2; ++q) {
+            const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + k0) / 16 + q]);
+            const float mul = c_row * kv.x, a = kv.y + shift;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float2 x = fma2(make_float2(__uint_as_float(v[16 * q + k]), __uint_as_float(v[16 * q + k + 1])),
+                                    make_float2(mul, mul), make_float2(a, a));
+              v[16 * q + k] = __float_as_uint(x.x);
+              v[16 * q + k + 1] = __float_as_uint(x.y);
+              if (k & 2) most2 = fmaxf(fmaxf(most2, x.x), x.y);
+              else most = fmaxf(fmaxf(most, x.x), x.y);
             }
           }
-          if (kTiles == 1) {  // the other half of the row
-            sh->other[wg][row] = top;
-            if (!(ok = softmax_and(ok))) break;
-            top = fmaxf(top, sh->other[wg ^ 1][row]);
+          return fmaxf(most, most2);
+        };
+        // Their weights, packed, and what they add to the row's sum.
+        const auto weigh = [&](const uint32_t(&v)[32], int k0, uint32_t(&w)[16]) {
+          float got = 0.f;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float2 y = make_float2(ex2(__uint_as_float(v[16 * q + k])), ex2(__uint_as_float(v[16 * q + k + 1])));
+              sum = add2(sum, y);
+              const __half2 h = __floats2half2_rn(y.x, y.y);
+              w[8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            got += (sum.x + sum.y) * sh->meta[m][(col0 + k0) / 16 + q].inv;
           }
-          const float now = top > ref + kWeightSlack ? top : ref, f = ex2(ref - now);
-          ref = now;
-          l *= f;
-          if (n > 0) {  // O of the row is complete up to the tile before: rescale it
-            const uint32_t last = kTiles == 2 ? item - 2 : item - 1;
-            ok = mbar_wait(&sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-            constexpr int kO = kTiles == 2 ? kD : kD / 2;
+          return got;
+        };
+        // A row without a reference takes its largest score for one, others move theirs when
+        // a score passes it by more than the slack.
+        const auto moves = [&](float most) { return ref == kNoRef ? most > -INFINITY : most > kWeightTop + kWeightSlack; };
+        if (kTiles == 2) {
+          // A row is one thread's: 32 columns at a time, the weights laid over scores already
+          // read.  When the reference moves, what the row has so far is scaled: its sum, this
+          // tile's weights and O.  The loop is kept rolled: past the first few KiB of
+          // instructions a warp runs three times slower.
 #pragma unroll 1
-            for (int k = 0; k < kO; k += 32) {
-              uint32_t v[32];
-              const uint32_t at = tO + (kTiles == 2 ? 0 : wg * kO) + k;
-              tmem_ld32(at, v);
+          for (int c = 0; c < kCols; c += 32) {
+            uint32_t v[32], w[16];
+            while (true) {
+              tmem_ld32(tS + c, v);
               tmem_ld_wait32(v);
+              if (edge) hide(v, c);
+              const float shift = ref == kNoRef ? 0.f : kWeightTop - ref;
+              const float most = logs(v, c, shift);
+              const bool move = moves(most);
+              if (!__any_sync(0xffffffffu, move)) break;
+              const float now = move ? most - shift : ref;
+              const float f = ref == kNoRef ? 1.f : ex2(ref - now);
+              ref = now;
+              l *= f;
+              if (n > 0) rescale(f);
+              const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+              for (int k = 0; k < c / 2; k += 16) {
+                tmem_ld16(tS + k, w);
+                tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tmem_st32(at, v);
+                for (int i = 0; i < 16; ++i) {
+                  const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&w[i]), f2);
+                  w[i] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                tmem_st16(tS + k, w);
+              }
+              tmem_st_wait();
             }
-            tmem_st_wait();
+            l += weigh(v, c, w);
+            tmem_st16(tS + c / 2, w);
           }
-        }
-        if (kTiles == 1 && !ok) break;
-        l += sum_l;
-        // The weights lie where the scores were (with one query tile, where the other half
-        // had its own: it has read them, or the barrier above would not have let go).
+        } else {
+          // Two threads have the row's halves and have to agree on its reference: the largest
+          // score of the two is exchanged when either moves it.
+          uint32_t w[2][16];
+          float got;
+          while (true) {
+            const float shift = ref == kNoRef ? 0.f : kWeightTop - ref;
+            float most = -INFINITY;
+            got = 0.f;
 #pragma unroll
-        for (int c = 0; c < kCols / 2; c += 32)
-          tmem_st32(tS + col0 / 2 + c, *reinterpret_cast<const uint32_t(*)[32]>(&w[c]));
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[32];
+              tmem_ld32(tS + col0 + 32 * c, v);
+              tmem_ld_wait32(v);
+              if (edge) hide(v, 32 * c);
+              most = fmaxf(most, logs(v, 32 * c, shift));
+              got += weigh(v, 32 * c, w[c]);
+            }
+            if (!softmax_or(moves(most) || !ok)) break;
+            sh->other[wg][row] = most;
+            if (!(ok = softmax_and(ok))) break;
+            most = fmaxf(most, sh->other[wg ^ 1][row]);
+            const float now = moves(most) ? most - shift : ref;
+            const float f = ref == kNoRef ? 1.f : ex2(ref - now);
+            ref = now;
+            l *= f;
+            if (n > 0) rescale(f);
+          }
+          if (!ok) break;
+          l += got;
+          // The other half's scores lie here too; the barrier above came after their last use.
+          tmem_st16(tS + col0 / 2, w[0]);
+          tmem_st16(tS + col0 / 2 + 16, w[1]);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -686,40 +742,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l > 0.f ? 256.f / l : l;
       const float stat = l > 0.f ? ref - kWeightTop + __log2f(l) : l == 0.f ? -INFINITY : l;
       const bool whole = g.starts && g.ends;
-      const int64_t at = part_slot(p, blockIdx.x, g.starts) + r;
-      const int64_t orow = g.s.row0 + g.i0 + qi;
-      const int head = g.h * p.group + gi;
+      const int64_t at = part_slot(p, blockIdx.x, g.starts);
       constexpr int kO = kTiles == 2 ? kD : kD / 2;
       const int d0 = kTiles == 2 ? 0 : wg * kO;
-      T* out = static_cast<T*>(p.out) + orow * p.o_ts + head * p.o_hs + d0;
-      float* part = p.part + at * kD + d0;
+      // 32 columns at a time go through 4 KiB of the warp's own, so that stores are whole
+      // row segments: 32 rows x 64 bytes of results or 128 bytes of parts, in 16-byte
+      // chunks at the place their row's number turns them to.
+      uint8_t* stage = kD == 64 ? sRaw + C::kFifo * C::kVRaw + warp * 4096
+                                : sQ + (kTiles == 2 ? qt : wg * kTiles) * C::kKBytes + quad * 4096;
 #pragma unroll 1
       for (int k = 0; k < kO; k += 32) {
         uint32_t v[32];
         tmem_ld32(tO + d0 + k, v);
-        tmem_ld_wait();
-        if (!real) continue;
+        tmem_ld_wait32(v);
+        __syncwarp();
         if (whole) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
+          for (int i = 0; i < 4; ++i) {
             uint32_t u[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              u[e] = pack2(__uint_as_float(v[i + 2 * e]) * inv, __uint_as_float(v[i + 2 * e + 1]) * inv, T{});
-            *reinterpret_cast<uint4*>(out + k + i) = make_uint4(u[0], u[1], u[2], u[3]);
+              u[e] = pack2(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv, T{});
+            *reinterpret_cast<uint4*>(stage + lane * 64 + (((i ^ (lane >> 1)) & 3) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          __syncwarp();
+          const int ch = lane & 3;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // eight rows a store
+            const int rl = 8 * i + (lane >> 2), rr = qt * 128 + quad * 32 + rl;
+            const int qr = static_cast<int>(rr * group_mul >> 16);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + rl * 64 + (((ch ^ (rl >> 1)) & 3) << 4));
+            if (rr < rows)
+              *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + static_cast<int64_t>(g.s.row0 + g.i0 + qr) * p.o_ts +
+                                        (g.h * p.group + rr - qr * p.group) * p.o_hs + d0 + k + 8 * ch) = x;
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(part + k + i) =
-                make_float4(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
-                            __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(stage + lane * 128 + (((i ^ lane) & 7) << 4)) =
+                make_float4(__uint_as_float(v[4 * i]) * inv, __uint_as_float(v[4 * i + 1]) * inv,
+                            __uint_as_float(v[4 * i + 2]) * inv, __uint_as_float(v[4 * i + 3]) * inv);
+          __syncwarp();
+          const int ch = lane & 7;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // four rows a store
+            const int rl = 4 * i + (lane >> 3), rr = qt * 128 + quad * 32 + rl;
+            const float4 x = *reinterpret_cast<const float4*>(stage + rl * 128 + (((ch ^ rl) & 7) << 4));
+            if (rr < rows) *reinterpret_cast<float4*>(p.part + (at + rr) * kD + d0 + k + 4 * ch) = x;
+          }
         }
       }
+      __syncwarp();
       tc_fence_before();
       if (real && (kTiles == 2 || wg == 0)) {
-        if (!whole) p.stat[at] = stat;
-        else if (p.lse) p.lse[orow * p.q_heads + head] = stat * kLn2;
+        if (!whole) p.stat[at + r] = stat;
+        else if (p.lse)
+          p.lse[static_cast<int64_t>(g.s.row0 + g.i0 + qi) * p.q_heads + g.h * p.group + gi] = stat * kLn2;
       }
       if (g.starts && threadIdx.x == 0) note_join(p, g, sh->run.cut, blockIdx.x);
       tile += n_tiles;
