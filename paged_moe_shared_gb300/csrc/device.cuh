@@ -89,6 +89,30 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 
+// The same wait for warps that share a scheduler with busy ones: each try may
+// suspend the warp for up to 20 us, so that waiting costs few issue slots.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                               uint64_t timeout_ns = kWaitTimeoutNs) {
+  const auto tried = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+        : "memory");
+    return ok != 0;
+  };
+  if (tried()) return true;
+  const uint64_t t0 = globaltimer();
+  while (!tried()) {
+    if (*abort) return false;
+    if (globaltimer() - t0 > timeout_ns) return false;
+  }
+  return true;
+}
+
 // ------------------------------------------------------------- TMA
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");

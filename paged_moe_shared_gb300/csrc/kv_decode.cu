@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
           for (int sl = 0; sl < kSlabs; ++sl) {
             if (!ok) break;
             const uint32_t i = slot % kRing, ph = (slot / kRing) & 1u;
-            ok = mbar_wait(&sh->empty[i], ph ^ 1u, abort);
+            ok = mbar_wait_idle(&sh->empty[i], ph ^ 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&sh->full[i], bytes);
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
     // every copy this warp issued must have landed before the CTA exits
     volatile int never = 0;
     for (uint32_t j = slot > kRing ? slot - kRing : 0u; j < slot; ++j)
-      mbar_wait(&sh->full[j % kRing], (j / kRing) & 1u, &never);
+      mbar_wait_idle(&sh->full[j % kRing], (j / kRing) & 1u, &never);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
     // The whole warp walks and waits, and one lane issues, so that addresses stay
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
     uint32_t slot = 0, phase = 0;  // the next slot of the ring
     bool ok = true;
     const auto wait = [&](uint64_t* bar, uint32_t ph) {
-      ok = ok && mbar_wait(bar, ph, abort);
+      ok = ok && mbar_wait_idle(bar, ph, abort);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     };
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
     if (elect_one()) umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
     __syncwarp();
     volatile int never = 0;
-    mbar_wait(&sh->drain, 0, &never);
+    mbar_wait_idle(&sh->drain, 0, &never);
   } else if (warp == 2) {
     // --------------------------------------------------------------------- Q
     uint32_t seg = 0;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
           }
         }
         if (half == 0) {
-          ok = mbar_wait(&sh->q_empty[buf], ((seg >> 1) & 1u) ^ 1u, abort);
+          ok = mbar_wait_idle(&sh->q_empty[buf], ((seg >> 1) & 1u) ^ 1u, abort);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
 #pragma unroll
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
       const int pos0 = g.s.len - g.s.n + g.i0;  // position of the first query row
       const int lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
       const uint32_t buf = seg & 1u;
-      ok = mbar_wait(&sh->q_full[buf], (seg >> 1) & 1u, abort);
+      ok = mbar_wait_idle(&sh->q_full[buf], (seg >> 1) & 1u, abort);
       ok = __all_sync(0xffffffffu, ok);
       // A weight is 2^(x + add) with add = kWeightTop - ref.
       float rs[kR], ref[kR], l[kR], o[kSlabs][kR];
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
         tc_fence_before();
       };
       for (int t = g.t0; t < g.t1; ++t, ++tile) {
-        ok = mbar_wait(&sh->meta_full[tile % kMetaRing], (tile / kMetaRing) & 1u, abort) && ok;
+        ok = mbar_wait_idle(&sh->meta_full[tile % kMetaRing], (tile / kMetaRing) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
         const float2 kvs = sh->meta[tile % kMetaRing][tok >> log_p];
         const int j = t * kTileTokens + tok;
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
         const int ke = static_cast<int>(__float_as_uint(kvs.y) >> 23);  // V scale = 2^(ke - 127)
         const float kv = static_cast<float>(ke - 127);
         const float inv_v = __uint_as_float(static_cast<uint32_t>(254 - ke) << 23);
-        ok = mbar_wait(&sh->s_full[tile & 1u], (tile >> 1) & 1u, abort) && ok;
+        ok = mbar_wait_idle(&sh->s_full[tile & 1u], (tile >> 1) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         float x[kR];
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
           }
           if (!(all = named_bar_and(ok))) break;
           if (t > g.t0) {  // every O MMA so far is done
-            ok = mbar_wait(&sh->o_full[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort);
+            ok = mbar_wait_idle(&sh->o_full[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
             add_output();
           }
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
           l[r] += x[r] * inv_v;
         }
         if (t > g.t0 + 1) {  // the weights two tiles back have been read
-          ok = mbar_wait(&sh->o_full[tile & 1u], ((tile - 2) >> 1) & 1u, abort) && ok;
+          ok = mbar_wait_idle(&sh->o_full[tile & 1u], ((tile - 2) >> 1) & 1u, abort) && ok;
           ok = __all_sync(0xffffffffu, ok);
         }
         // tokens that do not count may hold anything: their rows of V become zero
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
 #pragma unroll
           for (int sl = 0; sl < kSlabs; ++sl) {
             const uint32_t u = (2 * tile + 1) * kSlabs + sl, slot = u % kRing;
-            ok = mbar_wait(&sh->full[slot], (u / kRing) & 1u, abort) && ok;
+            ok = mbar_wait_idle(&sh->full[slot], (u / kRing) & 1u, abort) && ok;
             ok = __all_sync(0xffffffffu, ok);
             if (ok && !live) {
               uint4* row = reinterpret_cast<uint4*>(sRing + slot * C::kSlabBytes + tok * kRowBytes);
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
       constexpr int kLanesPerRow = 32 / kR;
       if (lane % kLanesPerRow == 0) sh->row_sum[quad][lane / kLanesPerRow] = l[0];
       const uint32_t i = tile - 1;
-      ok = mbar_wait(&sh->o_full[i & 1u], (i >> 1) & 1u, abort) && ok;
+      ok = mbar_wait_idle(&sh->o_full[i & 1u], (i >> 1) & 1u, abort) && ok;
       ok = __all_sync(0xffffffffu, ok);
       add_output();
       if (!(all = named_bar_and(ok))) break;

@@ -8,11 +8,9 @@
 //               of e4m3 parts (two hold a bf16 query exactly, three an f16 one)
 //               into one fp32 accumulator: two parts cost what one bf16 product
 //               costs, without widening K;
-//   O += P V    f16 x f16: P rounded to f16 stays in TMEM as the A operand; V is
-//               widened on its way to shared memory by four warps.  An e4m3 code
-//               placed in the upper bits of an f16 is that value times 2^-8,
-//               exactly, with no conversion instruction (and finite, whatever
-//               the byte, so unused slots need no clearing).
+//   O += P V    f16 x f16: P rounded to f16 stays in TMEM as the A operand; the
+//               codes of V are widened (exactly) by four warps on their way to
+//               shared memory.
 // The V scale 2^k of a page is added to the score, x + k, so that the weight that
 // meets the codes stays bounded; the row sum takes the weight without it by an
 // exact multiplication.  Weights are relative to a reference that follows the
@@ -62,7 +60,6 @@ struct TileCfg {
   static constexpr int kStage = kD == 64 ? 8 * 4096 : 0;        // output staging; else in Q's place
   static constexpr int kSmem =
       1024 + kQBytes + kKRing * kKBytes + kVRing * kVBytes + kFifo * kVRaw + kStage;
-  static constexpr int kCols = kTiles == 2 ? 128 : 64;          // score columns of a thread
   static constexpr uint32_t kO = 256;                           // TMEM column of O; scores are at 0 and 128
 };
 
@@ -77,7 +74,8 @@ struct TileShared {
   uint64_t v_full[4], v_empty[4];
   uint64_t meta_full[kMetaRing];
   uint64_t q_full;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], o_full[2];
+  uint64_t p_full[2][2], o_half[2];  // by halves of the key tile
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -155,8 +153,8 @@ __device__ __forceinline__ bool softmax_or(bool v) {
   return r != 0;
 }
 // Registers per thread of a warpgroup; the four groups' shares add up to the 4 x 128
-// that the block was launched with (2 x 176 + 2 x 80 = 512).
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+// that the block was launched with (2 x 160 + 2 x 96 = 512).
+constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;
 template <int kRegs>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -171,10 +169,16 @@ __device__ __forceinline__ int swz(int r, int d) {
   if (kRowBytes == 128) return r * 128 + ((((d >> 4) ^ r) & 7) << 4) + (d & 15);
   return r * 64 + ((((d >> 4) ^ (r >> 1)) & 3) << 4) + (d & 15);
 }
-// Two e4m3 codes (bytes 0 and 1 of w, or 2 and 3) as f16 numbers times 2^-8.
-__device__ __forceinline__ uint32_t widen(uint32_t w, bool upper) {
-  const uint32_t t = __byte_perm(w, 0, upper ? 0x3424 : 0x1404);  // code in the high byte of each half
-  return (t & 0x80008000u) | ((t >> 1) & 0x3F803F80u);
+// Four e4m3 codes as f16 numbers.
+__device__ __forceinline__ uint2 widen(uint32_t w) {
+  uint2 r;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
 }
 
 template <typename T, int kD, int kTiles>
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     kv_tiles_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap tm) {
   constexpr int kQParts = std::is_same<T, __nv_bfloat16>::value ? 2 : 3;
   using C = TileCfg<kD, kTiles, kQParts>;
-  constexpr int kSlabs = C::kSlabs, kRowBytes = C::kRowBytes, kCols = C::kCols;
+  constexpr int kSlabs = C::kSlabs, kRowBytes = C::kRowBytes;
   constexpr uint32_t kSwizzle = kRowBytes == 128 ? 2 : 4;
   constexpr uint32_t kAtom = 8 * kRowBytes;
   extern __shared__ uint8_t smem_raw[];
@@ -208,7 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->q_full, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
-      mbar_init(&sh->p_full[i], kTiles == 2 ? 4 : 8);
+      mbar_init(&sh->p_full[i][0], 4);
+      mbar_init(&sh->p_full[i][1], 4);
+      mbar_init(&sh->o_half[i], 1);
       mbar_init(&sh->o_full[i], 1);
     }
     mbar_init(&sh->drain, 1);
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool copies = lane < boxes && mine >= 0;
           const uint32_t which = __ballot_sync(0xffffffffu, copies);
           const uint32_t i = tile % C::kKRing;
-          ok = mbar_wait(&sh->k_empty[i], ((tile / C::kKRing) & 1u) ^ 1u, abort);
+          ok = mbar_wait_idle(&sh->k_empty[i], ((tile / C::kKRing) & 1u) ^ 1u, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&sh->k_full[i], __popc(which) * P * kD);
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every copy this warp issued must have landed before the CTA exits
       volatile int never = 0;
       for (uint32_t j = tile > C::kKRing ? tile - C::kKRing : 0u; j < tile; ++j)
-        mbar_wait(&sh->k_full[j % C::kKRing], (j / C::kKRing) & 1u, &never);
+        mbar_wait_idle(&sh->k_full[j % C::kKRing], (j / C::kKRing) & 1u, &never);
     } else if (warp == 13) {
       // ------------------------------------------------------------------ MMAs
       // Items: (key tile, query tile) pairs in order; item i uses score buffer i & 1.
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t item = 0, k_slot = 0, k_phase = 0, v_slot = 0, v_phase = 0, seg = 0;
       bool ok = true;
       const auto wait = [&](uint64_t* bar, uint32_t phase) {
-        ok = ok && mbar_wait(bar, phase, abort);
+        ok = ok && mbar_wait_idle(bar, phase, abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       };
@@ -370,10 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < kTiles; ++q, ++item) {
             const uint32_t buffer = item & 1u;
-            wait(&sh->p_full[buffer], (item >> 1) & 1u);
             v_slot = v_slot0, v_phase = v_phase0;
 #pragma unroll
             for (int h = 0; h < C::kVStages; ++h) {
+              if (h % (C::kVStages / 2) == 0)
+                wait(&sh->p_full[buffer][h / (C::kVStages / 2)], (item >> 1) & 1u);
               if (q == 0) wait(&sh->v_full[v_slot], v_phase);
               if (ok && elect_one()) {
                 const uint32_t b0 = v_s + v_slot * C::kVBytes;
@@ -383,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               smem_desc_sw128(b0 + 2048 * k, C::kVTok * 128, 1024), id_o,
                               (n > 0 || h + k != 0) ? 1u : 0u);
                 if (q == kTiles - 1) umma_commit(&sh->v_empty[v_slot]);
+                if (h == C::kVStages / 2 - 1) umma_commit(&sh->o_half[buffer]);
                 if (h == C::kVStages - 1) umma_commit(&sh->o_full[buffer]);
               }
               __syncwarp();
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
       __syncwarp();
       volatile int never = 0;
-      mbar_wait(&sh->drain, 0, &never);
+      mbar_wait_idle(&sh->drain, 0, &never);
     }
   } else if (warp >= 8) {
     regs_down<kOtherRegs>();
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t128 = threadIdx.x - 256, c = t128 % kChunks, r0 = t128 / kChunks;
     bool ok = true;
     // the load cursor: stage `lh` of key tile lt, tile `ltile` of the run
-    int lt = 0, lh = C::kVStages;
+    int lt = 0, lh = C::kVStages, lo = 0;
     uint32_t ltile = 0xFFFFFFFFu, lslot = 0;
     const uint8_t* head = nullptr;
     g.t1 = 0;
@@ -423,18 +431,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++lt >= g.t1) {
           walk.next(p, &g);
           lt = g.t0;
+          lo = p.window > 0 ? max(0, g.s.len - g.s.n + g.i0 - p.window + 1) : 0;
           head = p.g.pool + static_cast<uint64_t>(p.g.kv_heads + g.h) * P * kD + 16 * c;
         }
-        ok = mbar_wait(&sh->meta_full[ltile % kMetaRing], (ltile / kMetaRing) & 1u, abort) && ok;
+        ok = mbar_wait_idle(&sh->meta_full[ltile % kMetaRing], (ltile / kMetaRing) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
       }
       uint8_t* dst = sRaw + lslot * C::kVRaw + t128 * 16;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const int r = C::kVTok * lh + r0 + k * kStep;
+        const int r = C::kVTok * lh + r0 + k * kStep, j = lt * kTileTokens + r;
         const int page = sh->meta[ltile % kMetaRing][r >> 4].page;
-        if (page >= 0) cp_async16(smem_u32(dst + k * 2048), head + page * p.g.page_bytes + (r & (P - 1)) * kD);
+        // slots that no counted token owns may hold anything, and 0 * NaN is not 0
+        if (page >= 0 && j >= lo && j < g.s.len) cp_async16(smem_u32(dst + k * 2048), head + page * p.g.page_bytes + (r & (P - 1)) * kD);
         else *reinterpret_cast<uint4*>(dst + k * 2048) = make_uint4(0, 0, 0, 0);
       }
       ++lh;
@@ -453,18 +463,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_commit();
       if (!ok) break;
       cp_async_wait<C::kFifo - 1>();
-      ok = mbar_wait(&sh->v_empty[v_slot], v_phase, abort);
+      ok = mbar_wait_idle(&sh->v_empty[v_slot], v_phase, abort);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const uint8_t* src = sRaw + raw_slot * C::kVRaw + t128 * 16;
       uint8_t* dst = sV + v_slot * C::kVBytes + (c >> 2) * (C::kVTok * 128);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const uint4 x = *reinterpret_cast<const uint4*>(src + k * 2048);
+        const uint2 f0 = widen(x.x), f1 = widen(x.y), f2 = widen(x.z), f3 = widen(x.w);
         const int r = r0 + k * kStep, ch = 2 * (c & 3);  // chunks of eight f16 in the 128-byte row
         *reinterpret_cast<uint4*>(dst + r * 128 + (((ch ^ r) & 7) << 4)) =
-            make_uint4(widen(x.x, false), widen(x.x, true), widen(x.y, false), widen(x.y, true));
+            make_uint4(f0.x, f0.y, f1.x, f1.y);
         *reinterpret_cast<uint4*>(dst + r * 128 + ((((ch + 1) ^ r) & 7) << 4)) =
-            make_uint4(widen(x.z, false), widen(x.z, true), widen(x.w, false), widen(x.w, true));
+            make_uint4(f2.x, f2.y, f3.x, f3.y);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -484,7 +495,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;  // row of the query tile, and TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const int qt = kTiles == 2 ? wg : 0;             // query tile
-    const int col0 = kTiles == 2 ? 0 : 64 * wg;      // first score column of this thread
     const uint32_t tO = tmem + C::kO + qt * kD + lane_off;
     const uint32_t group_mul = 65536u / p.group + 1;  // r / group = r * group_mul >> 16 for r < 256
     uint32_t tile = 0, item0 = 0;
@@ -569,166 +579,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = g.t0 + n;
         const uint32_t item = item0 + (kTiles == 2 ? 2 * n + wg : n), slot = item & 1u;
         const uint32_t m = (tile + n) % kMetaRing;
-        ok = mbar_wait(&sh->meta_full[m], ((tile + n) / kMetaRing) & 1u, abort) && ok;
-        ok = mbar_wait(&sh->s_full[slot], (item >> 1) & 1u, abort) && ok;
+        ok = mbar_wait_idle(&sh->meta_full[m], ((tile + n) / kMetaRing) & 1u, abort) && ok;
+        ok = mbar_wait_idle(&sh->s_full[slot], (item >> 1) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (kTiles == 2 && !ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + 128 * slot + lane_off;
-        const int j0 = t * kTileTokens + col0;
-        bool edge = j_lo > j0 || j_hi < j0 + kCols;
-#pragma unroll
-        for (int k = 0; k < kCols / 32; ++k) edge |= sh->seen[m][col0 / 32 + k] != 0xFFFFFFFFu;
-        edge = __any_sync(0xffffffffu, edge);
-        const auto hide = [&](uint32_t(&v)[32], int k0) {  // -inf where the row does not see
-          const int lo = max(0, min(32, j_lo - (j0 + k0))), hi = max(0, min(32, j_hi - (j0 + k0)));
-          uint32_t see = sh->seen[m][(col0 + k0) / 32];
-          see &= static_cast<uint32_t>((1ull << hi) - (1ull << lo)) & (hi > lo ? 0xFFFFFFFFu : 0u);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
-        };
-        // Multiplies O of the row, complete up to the tile before, by f.
-        const auto rescale = [&](float f) {
-          const uint32_t last = kTiles == 2 ? item - 2 : item - 1;
-          ok = mbar_wait(&sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
-          ok = __all_sync(0xffffffffu, ok);
-          tc_fence_after();
-          constexpr int kO = kTiles == 2 ? kD : kD / 2;
+        // A row without a reference takes its largest score for one, others move theirs when
+        // a score passes it by more than the slack.
+        const auto moves = [&](float most) { return ref == kNoRef ? most > -INFINITY : most > kWeightTop + kWeightSlack; };
+        // Half a tile, 64 columns, at a time; with one query tile each warpgroup has its half.
+        // The loop is kept rolled: past the first 10 KiB of instructions, which the warps of a
+        // scheduler share, a warp runs three times slower.
 #pragma unroll 1
-          for (int k = 0; k < kO; k += 32) {
-            uint32_t v[32];
-            const uint32_t at = tO + (kTiles == 2 ? 0 : wg * kO) + k;
-            tmem_ld32(at, v);
-            tmem_ld_wait32(v);
+        for (int h = kTiles == 2 ? 0 : wg; h < (kTiles == 2 ? 2 : wg + 1); ++h) {
+          const int j0 = t * kTileTokens + 64 * h;
+          const uint2 seen = *reinterpret_cast<const uint2*>(&sh->seen[m][2 * h]);
+          const bool edge = __any_sync(0xffffffffu, j_lo > j0 || j_hi < j0 + 64 || (seen.x & seen.y) != 0xFFFFFFFFu);
+          uint32_t v[64];
+          while (true) {
+            tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+            tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+            if (edge) {  // -inf where the row does not see
+              const int lo = max(0, min(64, j_lo - j0)), hi = max(0, min(64, j_hi - j0));
+              uint64_t see = (hi == 64 ? ~0ull : (1ull << hi) - 1) & (lo == 64 ? 0ull : ~0ull << lo);
+              see &= static_cast<uint64_t>(seen.y) << 32 | seen.x;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tmem_st32(at, v);
-          }
-          tmem_st_wait();
-        };
-        // Of 32 scores: x + k + shift (a 16-column group's x + k is S * mul + add), in place,
-        // and the largest.
-        const auto logs = [&](uint32_t(&v)[32], int k0, float shift) {
-          float most = -INFINITY, most2 = -INFINITY;
+              for (int k = 0; k < 64; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
+            }
+            // x + k + shift (a 16-column group's x + k is S * mul + add), in place, and the largest
+            const float shift = ref == kNoRef ? 0.f : kWeightTop - ref;
+            float most[4];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][(col0 + k0) / 16 + q]);
-            const float mul = c_row * kv.x, a = kv.y + shift;
+            for (int q = 0; q < 4; ++q) {
+              const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][4 * h + q]);
+              const float mul = c_row * kv.x, a = kv.y + shift;
+              float top = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float2 x = fma2(make_float2(__uint_as_float(v[16 * q + k]), __uint_as_float(v[16 * q + k + 1])),
-                                    make_float2(mul, mul), make_float2(a, a));
-              v[16 * q + k] = __float_as_uint(x.x);
-              v[16 * q + k + 1] = __float_as_uint(x.y);
-              if (k & 2) most2 = fmaxf(fmaxf(most2, x.x), x.y);
-              else most = fmaxf(fmaxf(most, x.x), x.y);
+              for (int k = 0; k < 16; k += 2) {
+                const float2 x = fma2(make_float2(__uint_as_float(v[16 * q + k]), __uint_as_float(v[16 * q + k + 1])),
+                                      make_float2(mul, mul), make_float2(a, a));
+                v[16 * q + k] = __float_as_uint(x.x);
+                v[16 * q + k + 1] = __float_as_uint(x.y);
+                top = fmaxf(fmaxf(top, x.x), x.y);
+              }
+              most[q] = top;
+            }
+            float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+            if (kTiles == 2) {
+              if (!__any_sync(0xffffffffu, moves(top))) break;
+            } else {
+              // two threads have the row's halves and agree on its reference
+              if (!softmax_or(moves(top) || !ok)) break;
+              sh->other[wg][row] = top;
+              if (!(ok = softmax_and(ok))) break;
+              top = fmaxf(top, sh->other[wg ^ 1][row]);
+            }
+            const float now = moves(top) ? top - shift : ref;
+            const float f = ref == kNoRef ? 1.f : ex2(ref - now);
+            ref = now;
+            l *= f;
+            // O of the row, once the MMAs so far are done: those of the tile before, or of
+            // this tile's first half
+            if (n > 0 || (kTiles == 2 && h > 0)) {
+              const bool second = kTiles == 2 && h > 0;
+              const uint32_t last = second ? item : kTiles == 2 ? item - 2 : item - 1;
+              ok = mbar_wait_idle(second ? &sh->o_half[slot] : &sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
+              ok = __all_sync(0xffffffffu, ok);
+              tc_fence_after();
+              constexpr int kO = kTiles == 2 ? kD : kD / 2;
+#pragma unroll 1
+              for (int k = 0; k < kO; k += 32) {
+                uint32_t o[32];
+                const uint32_t at = tO + (kTiles == 2 ? 0 : wg * kO) + k;
+                tmem_ld32(at, o);
+                tmem_ld_wait32(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(at, o);
+              }
+              tmem_st_wait();
             }
           }
-          return fmaxf(most, most2);
-        };
-        // Their weights, packed, and what they add to the row's sum.
-        const auto weigh = [&](const uint32_t(&v)[32], int k0, uint32_t(&w)[16]) {
-          float got = 0.f;
+          if (kTiles == 1 && !ok) break;
+          // The weights, packed, and what they add to the row's sum.  They lie over scores
+          // already read (with one query tile, by both halves: the barrier above).
+          uint32_t w[32];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
               const float2 y = make_float2(ex2(__uint_as_float(v[16 * q + k])), ex2(__uint_as_float(v[16 * q + k + 1])));
               sum = add2(sum, y);
-              const __half2 h = __floats2half2_rn(y.x, y.y);
-              w[8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+              const __half2 hh = __floats2half2_rn(y.x, y.y);
+              w[8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-            got += (sum.x + sum.y) * sh->meta[m][(col0 + k0) / 16 + q].inv;
+            l += (sum.x + sum.y) * sh->meta[m][4 * h + q].inv;
           }
-          return got;
-        };
-        // A row without a reference takes its largest score for one, others move theirs when
-        // a score passes it by more than the slack.
-        const auto moves = [&](float most) { return ref == kNoRef ? most > -INFINITY : most > kWeightTop + kWeightSlack; };
-        if (kTiles == 2) {
-          // A row is one thread's: 32 columns at a time, the weights laid over scores already
-          // read.  When the reference moves, what the row has so far is scaled: its sum, this
-          // tile's weights and O.  The loop is kept rolled: past the first few KiB of
-          // instructions a warp runs three times slower.
-#pragma unroll 1
-          for (int c = 0; c < kCols; c += 32) {
-            uint32_t v[32], w[16];
-            while (true) {
-              tmem_ld32(tS + c, v);
-              tmem_ld_wait32(v);
-              if (edge) hide(v, c);
-              const float shift = ref == kNoRef ? 0.f : kWeightTop - ref;
-              const float most = logs(v, c, shift);
-              const bool move = moves(most);
-              if (!__any_sync(0xffffffffu, move)) break;
-              const float now = move ? most - shift : ref;
-              const float f = ref == kNoRef ? 1.f : ex2(ref - now);
-              ref = now;
-              l *= f;
-              if (n > 0) rescale(f);
-              const __half2 f2 = __float2half2_rn(f);
-#pragma unroll 1
-              for (int k = 0; k < c / 2; k += 16) {
-                tmem_ld16(tS + k, w);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&w[i]), f2);
-                  w[i] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-                tmem_st16(tS + k, w);
-              }
-              tmem_st_wait();
-            }
-            l += weigh(v, c, w);
-            tmem_st16(tS + c / 2, w);
-          }
-        } else {
-          // Two threads have the row's halves and have to agree on its reference: the largest
-          // score of the two is exchanged when either moves it.
-          uint32_t w[2][16];
-          float got;
-          while (true) {
-            const float shift = ref == kNoRef ? 0.f : kWeightTop - ref;
-            float most = -INFINITY;
-            got = 0.f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t v[32];
-              tmem_ld32(tS + col0 + 32 * c, v);
-              tmem_ld_wait32(v);
-              if (edge) hide(v, 32 * c);
-              most = fmaxf(most, logs(v, 32 * c, shift));
-              got += weigh(v, 32 * c, w[c]);
-            }
-            if (!softmax_or(moves(most) || !ok)) break;
-            sh->other[wg][row] = most;
-            if (!(ok = softmax_and(ok))) break;
-            most = fmaxf(most, sh->other[wg ^ 1][row]);
-            const float now = moves(most) ? most - shift : ref;
-            const float f = ref == kNoRef ? 1.f : ex2(ref - now);
-            ref = now;
-            l *= f;
-            if (n > 0) rescale(f);
-          }
-          if (!ok) break;
-          l += got;
-          // The other half's scores lie here too; the barrier above came after their last use.
-          tmem_st16(tS + col0 / 2, w[0]);
-          tmem_st16(tS + col0 / 2 + 16, w[1]);
+          tmem_st32(tS + 32 * h, w);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->p_full[slot][h]);  // this half's MMAs may begin
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full[slot]);
+        if (kTiles == 1 && !ok) break;
       }
       const uint32_t items = n_tiles * kTiles;
       if (kTiles == 2 && !ok) break;
-      // the rows: O / l, with the 2^8 that V was widened without
+      // the rows: O / l
       {
         const uint32_t last = item0 + items - 1 - (kTiles == 2 ? 1 - wg : 0);
-        ok = mbar_wait(&sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
+        ok = mbar_wait_idle(&sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
       }
       if (kTiles == 1) {  // the two halves of the row's sum
@@ -739,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       tc_fence_after();
-      const float inv = l > 0.f ? 256.f / l : l;
+      const float inv = l > 0.f ? 1.f / l : l;
       const float stat = l > 0.f ? ref - kWeightTop + __log2f(l) : l == 0.f ? -INFINITY : l;
       const bool whole = g.starts && g.ends;
       const int64_t at = part_slot(p, blockIdx.x, g.starts);
