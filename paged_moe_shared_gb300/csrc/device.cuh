@@ -538,6 +538,39 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same descriptor in halves: the lower word moves with the address (16-byte
+// units, so a step of n bytes adds n / 16), the upper one is a constant.  MMAs
+// issued from these cost one addition per operand.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo_bytes, uint32_t swizzle) {
+  return (sbo_bytes >> 4) | (1u << 14) | (swizzle << 29);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | (lbo_bytes >> 4) << 16;
+}
+template <uint32_t kAHi, uint32_t kBHi, uint32_t kIdesc>
+__device__ __forceinline__ void umma_f8_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 a, {%1, %4};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %6, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(accumulate), "n"(kAHi), "n"(kBHi), "n"(kIdesc)
+      : "memory");
+}
+template <uint32_t kBHi, uint32_t kIdesc>
+__device__ __forceinline__ void umma_f16_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %5, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(accumulate), "n"(kBHi), "n"(kIdesc)
+      : "memory");
+}
+
 // silu(g) * u with silu(g) = g / (1 + e^-g).  The result is rounded to bf16,
 // so the fast exponential and division (a few ulp of fp32) are far below that
 // rounding; for g < -87 the denominator overflows and the result is 0.

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ TileShared sh_;
   TileShared* sh = &sh_;
   volatile int* abort = &sh->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -331,8 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // instead of the 64 it runs).
       constexpr uint32_t id_s = idesc_f8_f32(128, 128, false, false, false);
       constexpr uint32_t id_o = idesc_f16_f32(128, kD, false, /*b_mn=*/true);
+      constexpr uint32_t kHiQK = desc_hi(kAtom, kSwizzle), kHiV = desc_hi(1024, 2);
       const uint32_t tb = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint32_t q_s = smem_u32(sQ), k_s = smem_u32(sK), v_s = smem_u32(sV);
+      const uint32_t q_lo = __shfl_sync(0xffffffffu, desc_lo(smem_u32(sQ), 16), 0);
+      const uint32_t k_lo = __shfl_sync(0xffffffffu, desc_lo(smem_u32(sK), 16), 0);
+      const uint32_t v_lo = __shfl_sync(0xffffffffu, desc_lo(smem_u32(sV), C::kVTok * 128), 0);
       uint32_t item = 0, k_slot = 0, k_phase = 0, v_slot = 0, v_phase = 0, seg = 0;
       bool ok = true;
       const auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const auto scores = [&](uint32_t buffer, uint32_t q) {
         if (q == 0) wait(&sh->k_full[k_slot], k_phase);
         if (ok && elect_one()) {
-          const uint32_t a0 = q_s + q * C::kKBytes, b0 = k_s + k_slot * C::kKBytes;
+          const uint32_t a0 = q_lo + q * (C::kKBytes / 16), b0 = k_lo + k_slot * (C::kKBytes / 16);
           const uint32_t d = tb + 128 * buffer;
 #pragma unroll
           for (int part = 0; part < kQParts; ++part) {
@@ -352,11 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int sl = 0; sl < kSlabs; ++sl) {
 #pragma unroll
               for (int k = 0; k < kRowBytes / 32; ++k)
-                umma_f8(d,
-                        smem_desc(a0 + part * kTiles * C::kKBytes + sl * C::kSlabBytes + 32 * k, 16,
-                                  kAtom, kSwizzle),
-                        smem_desc(b0 + sl * C::kSlabBytes + 32 * k, 16, kAtom, kSwizzle), id_s,
-                        (part | sl | k) != 0 ? 1u : 0u);
+                umma_f8_lo<kHiQK, kHiQK, id_s>(
+                    d, a0 + (part * kTiles * C::kKBytes + sl * C::kSlabBytes) / 16 + 2 * k,
+                    b0 + sl * (C::kSlabBytes / 16) + 2 * k, (part | sl | k) != 0 ? 1u : 0u);
             }
           }
           umma_commit(&sh->s_full[buffer]);
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (q == kTiles - 1 && ++k_slot == C::kKRing) k_slot = 0, k_phase ^= 1u;
       };
-      while (ok && walk.next(p, &g)) {
+      while (__any_sync(0xffffffffu, ok && walk.next(p, &g))) {
         const int tiles = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
         wait(&sh->q_full, seg & 1u);
         scores(item & 1u, 0);
@@ -383,12 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(&sh->p_full[buffer][h / (C::kVStages / 2)], (item >> 1) & 1u);
               if (q == 0) wait(&sh->v_full[v_slot], v_phase);
               if (ok && elect_one()) {
-                const uint32_t b0 = v_s + v_slot * C::kVBytes;
+                const uint32_t b0 = v_lo + v_slot * (C::kVBytes / 16);
 #pragma unroll
                 for (int k = 0; k < C::kVTok / 16; ++k)  // 16 tokens: eight columns of P, 16 rows of V
-                  umma_f16_ts(tb + C::kO + q * kD, tb + 128 * buffer + C::kVTok / 2 * h + 8 * k,
-                              smem_desc_sw128(b0 + 2048 * k, C::kVTok * 128, 1024), id_o,
-                              (n > 0 || h + k != 0) ? 1u : 0u);
+                  umma_f16_ts_lo<kHiV, id_o>(tb + C::kO + q * kD, tb + 128 * buffer + C::kVTok / 2 * h + 8 * k,
+                                             b0 + 128 * k, (h + k != 0) ? 1u : n > 0 ? 1u : 0u);
                 if (q == kTiles - 1) umma_commit(&sh->v_empty[v_slot]);
                 if (h == C::kVStages / 2 - 1) umma_commit(&sh->o_half[buffer]);
                 if (h == C::kVStages - 1) umma_commit(&sh->o_full[buffer]);
