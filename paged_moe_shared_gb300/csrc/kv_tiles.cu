@@ -14,8 +14,8 @@
 // The V scale 2^k of a page is added to the score, x + k, so that the weight that
 // meets the codes stays bounded; the row sum takes the weight without it by an
 // exact multiplication.  Weights are relative to a reference that follows the
-// row's largest x + k only when a tile passes it by more than 2^8; then the
-// softmax warps rescale O in TMEM.
+// row's largest x + k only when 64 weights add up to more than 2^8 times the
+// weight at the reference; then the softmax warps rescale O in TMEM.
 //
 // Two softmax warpgroups alternate on two score buffers ("items"), so that the
 // tensor cores work on one while the other is in softmax.  With head_dim <= 128
@@ -38,8 +38,8 @@ using namespace dev;
 constexpr int kThreads = 512;
 constexpr int kMetaRing = 8;
 constexpr int kGroups = kTileTokens / 16;
-constexpr float kWeightTop = 7.f;    // a weight at the reference is 2^7
-constexpr float kWeightSlack = 8.f;  // and may pass it by 2^8: f16 ends at 2^16
+constexpr float kWeightTop = 7.f;     // a weight at the reference is 2^7
+constexpr float kMostSum = 32768.f;   // of 64 weights, so that none passes 2^15: f16 ends at 2^16
 constexpr float kNoRef = -1e30f;     // the reference of a row that has seen no key
 
 template <int kD, int kTiles, int kQParts>
@@ -580,65 +580,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t item = item0 + (kTiles == 2 ? 2 * n + wg : n), slot = item & 1u;
         const uint32_t m = (tile + n) % kMetaRing;
         ok = mbar_wait_idle(&sh->meta_full[m], ((tile + n) / kMetaRing) & 1u, abort) && ok;
+        // whether some row of the warp does not see all of a half, by halves
+        uint32_t edges = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint2 seen = *reinterpret_cast<const uint2*>(&sh->seen[m][2 * h]);
+          const int j0 = t * kTileTokens + 64 * h;
+          if (__any_sync(0xffffffffu, j_lo > j0 || j_hi < j0 + 64 || (seen.x & seen.y) != 0xFFFFFFFFu)) edges |= 1u << h;
+        }
         ok = mbar_wait_idle(&sh->s_full[slot], (item >> 1) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (kTiles == 2 && !ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + 128 * slot + lane_off;
-        // A row without a reference takes its largest score for one, others move theirs when
-        // a score passes it by more than the slack.
-        const auto moves = [&](float most) { return ref == kNoRef ? most > -INFINITY : most > kWeightTop + kWeightSlack; };
         // Half a tile, 64 columns, at a time; with one query tile each warpgroup has its half.
         // The loop is kept rolled: past the first 10 KiB of instructions, which the warps of a
         // scheduler share, a warp runs three times slower.
 #pragma unroll 1
         for (int h = kTiles == 2 ? 0 : wg; h < (kTiles == 2 ? 2 : wg + 1); ++h) {
-          const int j0 = t * kTileTokens + 64 * h;
-          const uint2 seen = *reinterpret_cast<const uint2*>(&sh->seen[m][2 * h]);
-          const bool edge = __any_sync(0xffffffffu, j_lo > j0 || j_hi < j0 + 64 || (seen.x & seen.y) != 0xFFFFFFFFu);
-          uint32_t v[64];
-          while (true) {
-            tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-            tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-            if (edge) {  // -inf where the row does not see
-              const int lo = max(0, min(64, j_lo - j0)), hi = max(0, min(64, j_hi - j0));
-              uint64_t see = (hi == 64 ? ~0ull : (1ull << hi) - 1) & (lo == 64 ? 0ull : ~0ull << lo);
-              see &= static_cast<uint64_t>(seen.y) << 32 | seen.x;
+          uint32_t v[64], w[32];
+          tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+          tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+          bool sees = true;
+          if (edges >> h & 1u) {  // -inf where the row does not see
+            const int j0 = t * kTileTokens + 64 * h;
+            const int lo = max(0, min(64, j_lo - j0)), hi = max(0, min(64, j_hi - j0));
+            const uint2 seen = *reinterpret_cast<const uint2*>(&sh->seen[m][2 * h]);
+            uint64_t see = (hi == 64 ? ~0ull : (1ull << hi) - 1) & (lo == 64 ? 0ull : ~0ull << lo);
+            see &= static_cast<uint64_t>(seen.y) << 32 | seen.x;
+            sees = see != 0;
 #pragma unroll
-              for (int k = 0; k < 64; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
-            }
-            // x + k + shift (a 16-column group's x + k is S * mul + add), in place, and the largest
+            for (int k = 0; k < 64; ++k) v[k] = see >> k & 1u ? v[k] : 0xFF800000u;
+          }
+          float got;
+          for (bool settled = false;; settled = true) {
+            // The weights with the reference as it stands: x + k of a 16-column group is S * mul
+            // + add.  Their sum says whether a score passes the reference by too much: only then
+            // (and for a row's first keys) the largest score is looked for, the reference moved
+            // and the weights taken again.
             const float shift = ref == kNoRef ? 0.f : kWeightTop - ref;
-            float most[4];
+            float raw = 0.f;
+            got = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][4 * h + q]);
               const float mul = c_row * kv.x, a = kv.y + shift;
-              float top = -INFINITY;
+              float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
                 const float2 x = fma2(make_float2(__uint_as_float(v[16 * q + k]), __uint_as_float(v[16 * q + k + 1])),
                                       make_float2(mul, mul), make_float2(a, a));
-                v[16 * q + k] = __float_as_uint(x.x);
-                v[16 * q + k + 1] = __float_as_uint(x.y);
-                top = fmaxf(fmaxf(top, x.x), x.y);
+                const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                sum = add2(sum, y);
+                const __half2 hh = __floats2half2_rn(y.x, y.y);
+                w[8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&hh);
               }
-              most[q] = top;
+              raw += sum.x + sum.y;
+              got += (sum.x + sum.y) * kv.z;
             }
-            float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+            const bool redo = !settled && ((ref == kNoRef && sees) || raw > kMostSum);
             if (kTiles == 2) {
-              if (!__any_sync(0xffffffffu, moves(top))) break;
+              if (!__any_sync(0xffffffffu, redo)) break;
             } else {
-              // two threads have the row's halves and agree on its reference
-              if (!softmax_or(moves(top) || !ok)) break;
+              if (!softmax_or(redo || !ok)) break;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][4 * h + q]);
+              float x = __uint_as_float(v[16 * q]);
+#pragma unroll
+              for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[16 * q + k]));
+              top = fmaxf(top, x * (c_row * kv.x) + kv.y);
+            }
+            if (kTiles == 1) {  // two threads have the row's halves and agree on its reference
               sh->other[wg][row] = top;
               if (!(ok = softmax_and(ok))) break;
               top = fmaxf(top, sh->other[wg ^ 1][row]);
             }
-            const float now = moves(top) ? top - shift : ref;
-            const float f = ref == kNoRef ? 1.f : ex2(ref - now);
+            const float now = fmaxf(top, ref), f = ref == kNoRef ? 1.f : ex2(ref - now);
             ref = now;
             l *= f;
             // O of the row, once the MMAs so far are done: those of the tile before, or of
@@ -651,34 +673,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               constexpr int kO = kTiles == 2 ? kD : kD / 2;
 #pragma unroll 1
-              for (int k = 0; k < kO; k += 32) {
-                uint32_t o[32];
+              for (int k = 0; k < kO; k += 16) {
+                uint32_t o[16];
                 const uint32_t at = tO + (kTiles == 2 ? 0 : wg * kO) + k;
-                tmem_ld32(at, o);
-                tmem_ld_wait32(o);
+                tmem_ld16(at, o);
+                tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(at, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(at, o);
               }
               tmem_st_wait();
             }
           }
           if (kTiles == 1 && !ok) break;
-          // The weights, packed, and what they add to the row's sum.  They lie over scores
-          // already read (with one query tile, by both halves: the barrier above).
-          uint32_t w[32];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float2 y = make_float2(ex2(__uint_as_float(v[16 * q + k])), ex2(__uint_as_float(v[16 * q + k + 1])));
-              sum = add2(sum, y);
-              const __half2 hh = __floats2half2_rn(y.x, y.y);
-              w[8 * q + k / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-            }
-            l += (sum.x + sum.y) * sh->meta[m][4 * h + q].inv;
-          }
+          l += got;
+          // over scores already read (with one query tile, by both halves: the barrier above)
           tmem_st32(tS + 32 * h, w);
           tmem_st_wait();
           tc_fence_before();
