@@ -17,7 +17,9 @@ struct KvState {
   int device = -1;
   int sms = 0;
   int* d_err = nullptr;  // device error word
-  CUtensorMap tm_codes{};  // [pages][page_bytes / head_dim][head_dim] bytes over the pool
+  // the pool as bytes [pages][page_bytes / head_dim][head_dim]
+  CUtensorMap tm_codes{};   // swizzled boxes of a page's tokens (MMA operands)
+  CUtensorMap tm_values{};  // plain boxes, at most a stage of the tile kernel's V
 };
 
 // Checks that the view has a KV shape and the current device holds its pool,
@@ -26,6 +28,9 @@ int kv_ready(View* v);
 // Checks one activation descriptor; `what` names it in the message.
 int check_heads(const rimuru_heads* h, const char* what);
 std::string kv_cuda_msg(const char* what, cudaError_t e);
+
+// Tokens of a box of tm_values.
+int kv_value_box(int head_dim, int page_tokens);
 
 inline int64_t element_bytes(int dtype) { return dtype == RIMURU_F32 ? 4 : 2; }
 

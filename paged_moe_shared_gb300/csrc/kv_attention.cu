@@ -107,7 +107,7 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
     e = launch_kv_decode(a, q->dtype, v.kv->tm_codes, s);
   } else {
     a.runs = std::min(kMaxTileRuns, v.kv->sms);
-    e = launch_kv_tiles(a, q->dtype, v.kv->tm_codes, s);
+    e = launch_kv_tiles(a, q->dtype, v.kv->tm_codes, v.kv->tm_values, s);
   }
   if (e == cudaSuccess) e = launch_kv_join(a, q->dtype, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("attention launch", e));

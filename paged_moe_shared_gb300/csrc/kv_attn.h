@@ -313,7 +313,8 @@ constexpr int kMaxTileRuns = 160;  // tile kernel: one
 
 // Launchers (the result is cudaGetLastError's).
 cudaError_t launch_kv_decode(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s);
-cudaError_t launch_kv_tiles(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s);
+cudaError_t launch_kv_tiles(const AttnArgs& a, int dtype, const CUtensorMap& tm, const CUtensorMap& tm_v,
+                            cudaStream_t s);
 cudaError_t launch_kv_join(const AttnArgs& a, int dtype, cudaStream_t s);
 // Rows of a unit of the decode kernel: 8 or 16.
 constexpr int kDecodeMaxRows = 16;

@@ -75,6 +75,10 @@ int kv_ready(View* v) {
   const cuuint32_t box[3] = {inner, static_cast<cuuint32_t>(v->page_tokens), 1};
   st = make_byte_map(&k->tm_codes, v->pool->base, dims, strides, box,
                      inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  const cuuint32_t box_v[3] = {static_cast<cuuint32_t>(dim),
+                               static_cast<cuuint32_t>(kv_value_box(v->head_dim, v->page_tokens)), 1};
+  if (st == RIMURU_OK)
+    st = make_byte_map(&k->tm_values, v->pool->base, dims, strides, box_v, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (st != RIMURU_OK) {
     const std::string msg = rimuru_last_error();
     destroy_kv_state(v);

@@ -23,7 +23,8 @@
 // 256 rows, a row is a thread); otherwise successive key tiles of one query
 // tile, whose columns the two warpgroups halve.
 //
-// Warps 0-3 and 4-7: softmax.  8-11: V.  12: K copies and page scales.  13: MMAs.
+// Warps 0-3 and 4-7: softmax.  8-11: widening V.  12: K copies, and the pages and
+// scales of each key tile for the others.  13: MMAs.  14: V copies.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -72,6 +73,7 @@ struct __align__(16) Meta {  // a 16-token group of a tile
 struct TileShared {
   uint64_t k_full[4], k_empty[4];
   uint64_t v_full[4], v_empty[4];
+  uint64_t raw_full[6], raw_empty[6];
   uint64_t meta_full[kMetaRing];
   uint64_t q_full;
   uint64_t s_full[2], o_full[2];
@@ -83,6 +85,7 @@ struct TileShared {
   int scratch[16];
   Meta meta[kMetaRing][kGroups];
   uint32_t seen[kMetaRing][4];    // a bit per token of the tile: its group has a page
+  int4 span[kMetaRing];           // tokens [x, y) of the tile count (and have pages if z); w: head
   float row_scale[2][128];        // of each row: score per unit of S and K scale
   float other[2][128];            // one query tile: row maxima of the halves
   float row_sum[2][128];          // and their sums
@@ -183,7 +186,8 @@ __device__ __forceinline__ uint2 widen(uint32_t w) {
 
 template <typename T, int kD, int kTiles>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv_tiles_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap tm) {
+    kv_tiles_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap tm,
+                    const __grid_constant__ CUtensorMap tm_v) {
   constexpr int kQParts = std::is_same<T, __nv_bfloat16>::value ? 2 : 3;
   using C = TileCfg<kD, kTiles, kQParts>;
   constexpr int kSlabs = C::kSlabs, kRowBytes = C::kRowBytes;
@@ -208,6 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->v_full[i], 4);
       mbar_init(&sh->v_empty[i], 1);
     }
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&sh->raw_full[i], 1);
+      mbar_init(&sh->raw_empty[i], 4);
+    }
     for (int i = 0; i < kMetaRing; ++i) mbar_init(&sh->meta_full[i], 1);
     mbar_init(&sh->q_full, 8);
     for (int i = 0; i < 2; ++i) {
@@ -221,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh->abort = 0;
     fence_barrier_init();
     prefetch_tmap(&tm);
+    prefetch_tmap(&tm_v);
   }
   if (warp == 13) {
     tmem_alloc(&sh->tmem_base, 512);
@@ -307,6 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t two = log_p == 4 ? which >> (2 * lane) & 3u
                                             : (which >> (lane >> (log_p - 5)) & 1u) * 3u;
             sh->seen[m][lane] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+          }
+          if (lane == 0) {
+            const int first = max(0, lo - t * kTileTokens), last = min(kTileTokens, g.s.len - t * kTileTokens);
+            sh->span[m] = make_int4(first, last, which == (1u << boxes) - 1u, g.h);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->meta_full[m]);
@@ -409,81 +422,87 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       volatile int never = 0;
       mbar_wait_idle(&sh->drain, 0, &never);
+    } else if (warp == 14) {
+      // -------------------------------------------------------------- V copies
+      // A box is a page's tokens, at most a stage's; lane l copies box l of a stage.
+      const uint64_t pol = policy_evict_last();
+      const int per = min(P, C::kVTok), boxes = C::kVTok / per;
+      const uint32_t total = sh->run.tiles * C::kVStages;
+      uint32_t slot = 0, phase = 1;
+      bool ok = true;
+      uint32_t v = 0;
+#pragma unroll 1
+      for (; v < total; ++v) {
+        const uint32_t tile = v / C::kVStages, m = tile % kMetaRing;
+        ok = mbar_wait_idle(&sh->meta_full[m], (tile / kMetaRing) & 1u, abort);
+        ok = ok && mbar_wait_idle(&sh->raw_empty[slot], phase, abort);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const int tok = v % C::kVStages * C::kVTok + lane * per;
+        const int page = lane < boxes ? sh->meta[m][tok >> 4].page : -1;
+        const uint32_t which = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&sh->raw_full[slot], __popc(which) * per * kD);
+        __syncwarp();
+        if (page >= 0)
+          tma_load_3d(sRaw + slot * C::kVRaw + lane * per * kD, &tm_v, &sh->raw_full[slot], 0,
+                      ((p.g.kv_heads + sh->span[m].w) << log_p) + (tok & (P - 1)), page, pol);
+        if (++slot == C::kFifo) slot = 0, phase ^= 1u;
+      }
+      if (!ok && lane == 0) {
+        set_error(p.g.err, RIMURU_DEV_TIMEOUT);
+        sh->abort = 1;
+      }
+      // every copy this warp issued must have landed before the CTA exits
+      volatile int never = 0;
+      for (uint32_t j = v > C::kFifo ? v - C::kFifo : 0u; j < v; ++j)
+        mbar_wait_idle(&sh->raw_full[j % C::kFifo], (j / C::kFifo) & 1u, &never);
     }
   } else if (warp >= 8) {
     regs_down<kOtherRegs>();
-    // ---------------------------------------------------------------------- V
+    // --------------------------------------------------------------- widening V
     // A stage is kVTok tokens: thread `t128` takes 16 codes (chunk c) of the tokens
-    // r0, r0 + kStep, ...  Codes arrive kFifo - 1 stages ahead in a shared-memory
-    // queue of which each thread reads only what it copied itself.
+    // r0, r0 + kStep, ...
     constexpr int kChunks = kD / 16, kStep = 128 / kChunks, kPer = C::kVTok / kStep;
     const int t128 = threadIdx.x - 256, c = t128 % kChunks, r0 = t128 / kChunks;
+    const int ch = 2 * (c & 3);  // its chunks of eight f16 in a 128-byte row: ch and ch + 1
+    uint8_t* const dst0 = sV + (c >> 2) * (C::kVTok * 128) + r0 * 128;
+    const uint8_t* const src0 = sRaw + r0 * kD + 16 * c;
     bool ok = true;
-    // the load cursor: stage `lh` of key tile lt, tile `ltile` of the run
-    int lt = 0, lh = C::kVStages, lo = 0;
-    uint32_t ltile = 0xFFFFFFFFu, lslot = 0;
-    const uint8_t* head = nullptr;
-    g.t1 = 0;
-    const auto load = [&]() {
-      if (lh == C::kVStages) {
-        lh = 0;
-        ++ltile;
-        if (++lt >= g.t1) {
-          walk.next(p, &g);
-          lt = g.t0;
-          lo = p.window > 0 ? max(0, g.s.len - g.s.n + g.i0 - p.window + 1) : 0;
-          head = p.g.pool + static_cast<uint64_t>(p.g.kv_heads + g.h) * P * kD + 16 * c;
-        }
-        ok = mbar_wait_idle(&sh->meta_full[ltile % kMetaRing], (ltile / kMetaRing) & 1u, abort) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-      }
-      uint8_t* dst = sRaw + lslot * C::kVRaw + t128 * 16;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int r = C::kVTok * lh + r0 + k * kStep, j = lt * kTileTokens + r;
-        const int page = sh->meta[ltile % kMetaRing][r >> 4].page;
-        // slots that no counted token owns may hold anything, and 0 * NaN is not 0
-        if (page >= 0 && j >= lo && j < g.s.len) cp_async16(smem_u32(dst + k * 2048), head + page * p.g.page_bytes + (r & (P - 1)) * kD);
-        else *reinterpret_cast<uint4*>(dst + k * 2048) = make_uint4(0, 0, 0, 0);
-      }
-      ++lh;
-      if (++lslot == C::kFifo) lslot = 0;
-    };
-    const uint32_t total = C::kVStages * sh->run.tiles;
+    const uint32_t total = sh->run.tiles * C::kVStages;
+    uint32_t v_slot = 0, v_phase = 1, raw_slot = 0, raw_phase = 0;
 #pragma unroll 1
-    for (uint32_t v = 0; ok && v < C::kFifo - 1; ++v) {
-      if (v < total) load();
-      cp_async_commit();
-    }
-    uint32_t v_slot = 0, v_phase = 1, raw_slot = 0;
-#pragma unroll 1
-    for (uint32_t v = 0; ok && v < total; ++v) {
-      if (v + C::kFifo - 1 < total) load();
-      cp_async_commit();
-      if (!ok) break;
-      cp_async_wait<C::kFifo - 1>();
-      ok = mbar_wait_idle(&sh->v_empty[v_slot], v_phase, abort);
+    for (uint32_t v = 0; v < total; ++v) {
+      ok = mbar_wait_idle(&sh->raw_full[raw_slot], raw_phase, abort);
+      ok = ok && mbar_wait_idle(&sh->v_empty[v_slot], v_phase, abort);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const uint8_t* src = sRaw + raw_slot * C::kVRaw + t128 * 16;
-      uint8_t* dst = sV + v_slot * C::kVBytes + (c >> 2) * (C::kVTok * 128);
+      // slots that no counted token owns may hold anything, and 0 * NaN is not 0
+      const uint32_t m = v / C::kVStages % kMetaRing;
+      const int4 span = sh->span[m];
+      const bool all = span.x <= 0 && span.y >= kTileTokens && span.z;
+      const int r_tile = v % C::kVStages * C::kVTok + r0;
+      uint8_t* const dst = dst0 + v_slot * C::kVBytes;
+      const uint8_t* const src = src0 + raw_slot * C::kVRaw;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src + k * 2048);
+        uint4 x = *reinterpret_cast<const uint4*>(src + k * kStep * kD);
+        if (!all) {
+          const int r = r_tile + k * kStep;
+          if (r < span.x || r >= span.y || sh->meta[m][r >> 4].page < 0) x = make_uint4(0, 0, 0, 0);
+        }
         const uint2 f0 = widen(x.x), f1 = widen(x.y), f2 = widen(x.z), f3 = widen(x.w);
-        const int r = r0 + k * kStep, ch = 2 * (c & 3);  // chunks of eight f16 in the 128-byte row
-        *reinterpret_cast<uint4*>(dst + r * 128 + (((ch ^ r) & 7) << 4)) =
-            make_uint4(f0.x, f0.y, f1.x, f1.y);
-        *reinterpret_cast<uint4*>(dst + r * 128 + ((((ch + 1) ^ r) & 7) << 4)) =
+        const int r = r0 + k * kStep;
+        *reinterpret_cast<uint4*>(dst + k * kStep * 128 + (((ch ^ r) & 7) << 4)) = make_uint4(f0.x, f0.y, f1.x, f1.y);
+        *reinterpret_cast<uint4*>(dst + k * kStep * 128 + ((((ch + 1) ^ r) & 7) << 4)) =
             make_uint4(f2.x, f2.y, f3.x, f3.y);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->v_full[v_slot]);
+      if (lane == 0) {
+        mbar_arrive(&sh->v_full[v_slot]);
+        mbar_arrive(&sh->raw_empty[raw_slot]);
+      }
       if (++v_slot == C::kVRing) v_slot = 0, v_phase ^= 1u;
-      if (++raw_slot == C::kFifo) raw_slot = 0;
+      if (++raw_slot == C::kFifo) raw_slot = 0, raw_phase ^= 1u;
     }
-    cp_async_wait_all();  // no copy of this thread is in flight when the CTA exits
     if (!ok && lane == 0) {
       set_error(p.g.err, RIMURU_DEV_TIMEOUT);
       sh->abort = 1;
@@ -788,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename T, int kD, int kTiles>
-cudaError_t launch(const AttnArgs& a, const CUtensorMap& tm, cudaStream_t s) {
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& tm, const CUtensorMap& tm_v, cudaStream_t s) {
   constexpr int kQParts = std::is_same<T, __nv_bfloat16>::value ? 2 : 3;
   constexpr int smem = TileCfg<kD, kTiles, kQParts>::kSmem;
   auto* fn = kv_tiles_kernel<T, kD, kTiles>;
@@ -805,20 +824,26 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& tm, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, a, tm);
+  return cudaLaunchKernelEx(&cfg, fn, a, tm, tm_v);
 }
 template <typename T>
-cudaError_t launch_dim(const AttnArgs& a, const CUtensorMap& tm, cudaStream_t s) {
+cudaError_t launch_dim(const AttnArgs& a, const CUtensorMap& tm, const CUtensorMap& tm_v, cudaStream_t s) {
   const bool two = a.unit_rows == 256;
-  if (a.g.head_dim == 64) return two ? launch<T, 64, 2>(a, tm, s) : launch<T, 64, 1>(a, tm, s);
-  if (a.g.head_dim == 128) return two ? launch<T, 128, 2>(a, tm, s) : launch<T, 128, 1>(a, tm, s);
-  return launch<T, 256, 1>(a, tm, s);
+  if (a.g.head_dim == 64) return two ? launch<T, 64, 2>(a, tm, tm_v, s) : launch<T, 64, 1>(a, tm, tm_v, s);
+  if (a.g.head_dim == 128) return two ? launch<T, 128, 2>(a, tm, tm_v, s) : launch<T, 128, 1>(a, tm, tm_v, s);
+  return launch<T, 256, 1>(a, tm, tm_v, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_tiles(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s) {
-  return dtype == RIMURU_BF16 ? launch_dim<__nv_bfloat16>(a, tm, s) : launch_dim<__half>(a, tm, s);
+int kv_value_box(int head_dim, int page_tokens) {
+  const int stage = head_dim <= 128 ? 64 : 32;
+  return page_tokens < stage ? page_tokens : stage;
+}
+
+cudaError_t launch_kv_tiles(const AttnArgs& a, int dtype, const CUtensorMap& tm, const CUtensorMap& tm_v,
+                            cudaStream_t s) {
+  return dtype == RIMURU_BF16 ? launch_dim<__nv_bfloat16>(a, tm, tm_v, s) : launch_dim<__half>(a, tm, tm_v, s);
 }
 
 }  // namespace rimuru
