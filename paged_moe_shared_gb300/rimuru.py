@@ -432,15 +432,21 @@ def rimuru_adjust(off, kv_view, kv_blocks_wanted: int, min_capacity: int, max_ca
     return c.value
 
 
+_KINDS = {}  # element type of a tensor -> BF16, F16 or F32
+
+
 def heads_of(t) -> Heads:
     """Descriptor of a tensor [tokens, heads, head_dim] whose last axis is contiguous."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.size(2) > 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
         raise ValueError("expected [tokens, heads, head_dim] with a contiguous last axis")
-    name = str(t.dtype)
-    kinds = {"torch.bfloat16": BF16, "torch.float16": F16, "torch.float32": F32}
-    if name not in kinds:
-        raise ValueError(f"unsupported element type {name}")
-    return Heads(t.data_ptr(), t.stride(0), t.stride(1), t.size(1), kinds[name])
+    kind = _KINDS.get(t.dtype)
+    if kind is None:
+        kind = {"torch.bfloat16": BF16, "torch.float16": F16, "torch.float32": F32}.get(str(t.dtype))
+        if kind is None:
+            raise ValueError(f"unsupported element type {t.dtype}")
+        _KINDS[t.dtype] = kind
+    return Heads(t.data_ptr(), stride[0], stride[1], shape[1], kind)
 
 
 def rimuru_rope_create(rot_dim: int, layout: int = ROPE_HALF, base: float = 10000.0,
