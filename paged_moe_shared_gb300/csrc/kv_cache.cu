@@ -93,6 +93,7 @@ namespace {
 struct AppendArgs {
   const void* x[2];  // keys, values
   int64_t ts[2], hs[2];
+  int warps_per_slice;
   KvSeqs s;
   KvGeom g;
 };
@@ -146,12 +147,34 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
-// One CTA per unit, a page that one sequence's new tokens touch; its warps take
-// the (K or V, head) slices of the page in turn.  Sequence b has at most
-// n_b / P + 2 units, at unit numbers cu[b] / P + 2 b onwards, so a unit finds
-// its sequence by bisection and the grid needs no lengths on the host.
+// One CTA per unit, a page that one sequence's new tokens touch.  Sequence b has
+// at most n_b / P + 2 units, at unit numbers cu[b] / P + 2 b onwards, so a unit
+// finds its sequence by bisection and the grid needs no lengths on the host.
+//
+// Bound: HBM (two bytes read and one written per element).  `wps` warps share a
+// (K or V, head) slice of the page, a lane has eight elements of a token at a
+// time, and everything a warp has to read is in flight at once: up to kHold
+// vectors a lane, which stay in registers between the maximum and the encoding
+// (a slice with more per warp is read again).
+constexpr int kHold = 8;
+constexpr int kAppendWarps = 16;
+
 template <typename T>
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendArgs p) {
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kAppendWarps, 2)
+    kv_append_kernel(const __grid_constant__ AppendArgs p) {
+  __shared__ float tops[kAppendWarps];
   const int P = p.g.page_tokens, D = p.g.head_dim;
   const int u = blockIdx.x;
   int lo = 0, hi = p.s.num_seqs;  // first sequence with u < cu[b + 1] / P + 2 (b + 1)
@@ -179,34 +202,50 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
   const int s0 = max(start - c * P, 0), s1 = min(len - c * P, P);  // slots to write
   const int row0 = r0 + c * P - start;                              // row of slot 0
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lanes = D / 8, at = lane % lanes, sub = lane / lanes, per = 32 / lanes;
-  for (int w = warp; w < 2 * p.g.kv_heads; w += blockDim.x >> 5) {
-    const int kv = w / p.g.kv_heads, h = w - kv * p.g.kv_heads;
-    const T* x = static_cast<const T*>(p.x[kv]) + h * p.hs[kv] + 8 * at;
-    uint8_t* codes = p.g.pool + page * p.g.page_bytes +
-                     static_cast<uint64_t>(w) * P * D + 8 * at;
-    float* scale = p.g.scales + (static_cast<int64_t>(page) * 2 * p.g.kv_heads + w);
-    float amax = 0.f;
+  const int lanes = D / 8, at = lane % lanes, per = 32 / lanes;
+  const int slices = 2 * p.g.kv_heads, wps = p.warps_per_slice;
+  const int part = warp % wps, team = warp / wps, teams = (blockDim.x >> 5) / wps;
+  const int step = per * wps, first = part * per + lane / lanes;  // this lane's rows: first, + step, ...
+  for (int w0 = 0; w0 < slices; w0 += teams) {
+    const int w = w0 + team;
+    const bool busy = w < slices;
+    const int kv = w >= p.g.kv_heads, h = w - kv * p.g.kv_heads;
+    const T* x = static_cast<const T*>(p.x[kv]) + h * p.hs[kv] + row0 * p.ts[kv] + 8 * at;
+    uint8_t* codes = p.g.pool + page * p.g.page_bytes + static_cast<uint64_t>(w) * P * D + 8 * at;
+    float* scale = p.g.scales + (static_cast<int64_t>(page) * slices + w);
+    float amax = 0.f, s_old = 0.f;
     bool odd = false;  // a NaN or an infinity among the new elements
-    for (int t = s0 + sub; t < s1; t += per) {
+    const auto look = [&](const Raw8<T>& raw) {
       float v[8];
-      load8f(x + (row0 + t) * p.ts[kv], v);
+      load8f(reinterpret_cast<const T*>(&raw), v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(v[i]);
+      for (int e = 0; e < 8; ++e) {
+        const float m = fabsf(v[e]);
         if (m <= 3.4028234664e38f) amax = fmaxf(amax, m);
         else odd = true;
       }
+    };
+    Raw8<T> held[kHold];
+    if (busy) {
+      if (s0 > 0) s_old = *scale;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+        if (s0 + first + i * step < s1) held[i] = load_raw(x + (s0 + first + i * step) * p.ts[kv]);
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+        if (s0 + first + i * step < s1) look(held[i]);
+      for (int t = s0 + first + kHold * step; t < s1; t += step) look(load_raw(x + t * p.ts[kv]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float s_new = scale_for(amax);
-    if (s0 > 0) {
-      const float s_old = *scale;
-      s_new = fmaxf(s_new, s_old);
-      if (s_new > s_old) {  // earlier tokens are rounded again at the larger scale
+    if (lane == 0) tops[warp] = amax;
+    __syncthreads();  // also: every warp of the slice has read the old scale
+    for (int i = 0; i < wps; ++i) amax = fmaxf(amax, tops[warp - part + i]);
+    if (busy) {
+      const float s_new = fmaxf(scale_for(amax), s_old);
+      if (s0 > 0 && s_new > s_old) {  // earlier tokens are rounded again at the larger scale
         const float f = s_old / s_new;
-        for (int t = sub; t < s0; t += per) {
+        for (int t = first; t < s0; t += step) {
           uint2 q = *reinterpret_cast<uint2*>(codes + t * D);
           const uint32_t in[2] = {q.x, q.y};
           float v[8];
@@ -221,16 +260,24 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
           *reinterpret_cast<uint2*>(codes + t * D) = encode8(v, f);
         }
       }
+      const float inv = 1.f / s_new;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) {
+        const int t = s0 + first + i * step;
+        if (t >= s1) continue;
+        float v[8];
+        load8f(reinterpret_cast<const T*>(&held[i]), v);
+        *reinterpret_cast<uint2*>(codes + t * D) = encode8(v, inv);
+      }
+      for (int t = s0 + first + kHold * step; t < s1; t += step) {
+        float v[8];
+        load8f(x + t * p.ts[kv], v);
+        *reinterpret_cast<uint2*>(codes + t * D) = encode8(v, inv);
+      }
+      if (part == 0 && lane == 0) *scale = s_new;
+      if (odd) dev::set_error(p.g.err, RIMURU_DEV_NONFINITE);
     }
-    const float inv = 1.f / s_new;
-    for (int t = s0 + sub; t < s1; t += per) {
-      float v[8];
-      load8f(x + (row0 + t) * p.ts[kv], v);
-      *reinterpret_cast<uint2*>(codes + t * D) = encode8(v, inv);
-    }
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *scale = s_new;
-    if (odd) dev::set_error(p.g.err, RIMURU_DEV_NONFINITE);
+    __syncthreads();  // `tops` is free again
   }
 }
 
@@ -388,7 +435,12 @@ int rimuru_kv_append(rimuru_view_t view, const rimuru_heads* k, const rimuru_hea
   a.g = kv_geom(v);
   const int64_t units = num_tokens / v.page_tokens + 2ll * num_seqs;
   if (units > std::numeric_limits<int32_t>::max()) return fail(RIMURU_ERR_ARG, "too many sequences");
-  const int threads = 32 * std::min(8, 2 * v.kv_heads);
+  // Sixteen warps, shared out over the slices.  With a token or two a sequence (a
+  // decode step) there is nothing to share: one warp a slice, eight at most.
+  const int slices = 2 * v.kv_heads;
+  const bool few = num_tokens < 4ll * num_seqs;
+  a.warps_per_slice = few ? 1 : std::max(1, kAppendWarps / slices);
+  const int threads = 32 * std::min(few ? 8 : kAppendWarps, slices * a.warps_per_slice);
   const dim3 grid(static_cast<unsigned>(units));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (k->dtype == RIMURU_BF16) kv_append_kernel<__nv_bfloat16><<<grid, threads, 0, s>>>(a);

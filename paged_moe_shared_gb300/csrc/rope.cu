@@ -39,6 +39,7 @@ struct RopeArgs {
   float mscale;
   int pairs, layout, head_dim, num_tokens;
   int turn_items, items_per_head;
+  uint64_t head_mul;  // item / items_per_head = item * head_mul >> 32
 };
 
 template <typename T>
@@ -67,15 +68,14 @@ __device__ __forceinline__ void from_f(float x, float* y) { *y = x; }
 // An item is one thread's unit of work in a head: items below `turn_items` turn
 // pairs (two vectors of eight in the half layout, one in the interleaved one),
 // the others copy a vector of eight past the rotated part.
-template <typename T, int kPer>
+template <typename T, bool kHalf, int kPer>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs p) {
   __shared__ float2 cs[kMaxPairs];
   const int t = blockIdx.x;
   const int n_items = p.first_item[kMaxArrays];
-  const bool half = p.layout == RIMURU_ROPE_HALF;
   const int rot = 2 * p.pairs;
   for (int base = 0; base < n_items; base += kPer * blockDim.x) {
-    Vec8<T> a[kPer], b[kPer];
+    Vec8<T> a[kPer], b[kHalf ? kPer : 1];
     T* dst[kPer];
     int off[kPer];  // first element of the item in its head
 #pragma unroll
@@ -88,12 +88,12 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
       for (int i = 1; i < kMaxArrays; ++i) s += item >= p.first_item[i];
       const RopeArray& A = p.arr[s];
       const int local = item - p.first_item[s];
-      const int h = local / p.items_per_head, i = local - h * p.items_per_head;
+      const int h = static_cast<int>(local * p.head_mul >> 32), i = local - h * p.items_per_head;
       off[j] = i < p.turn_items ? 8 * i : rot + 8 * (i - p.turn_items);
       const T* src = static_cast<const T*>(A.in) + t * A.in_ts + h * A.in_hs + off[j];
       dst[j] = static_cast<T*>(A.out) + t * A.out_ts + h * A.out_hs + off[j];
       a[j] = load8(src);
-      if (half && off[j] < rot) b[j] = load8(src + p.pairs);
+      if (kHalf && off[j] < rot) b[kHalf ? j : 0] = load8(src + p.pairs);
     }
     if (base == 0) {
       const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t]));
@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
       if (!dst[j]) continue;
       if (off[j] < rot) {
         T* x = reinterpret_cast<T*>(&a[j]);
-        T* y = reinterpret_cast<T*>(&b[j]);
-        if (half) {
+        T* y = reinterpret_cast<T*>(&b[kHalf ? j : 0]);
+        if (kHalf) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 w = cs[off[j] + e];
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
             from_f(u * w.x - v * w.y, &x[e]);
             from_f(v * w.x + u * w.y, &y[e]);
           }
-          store8(dst[j] + p.pairs, b[j]);
+          store8(dst[j] + p.pairs, b[kHalf ? j : 0]);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -138,8 +138,10 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
 template <typename T>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const int items = a.first_item[kMaxArrays];
-  const int threads = std::min(256, (items + 31) / 32 * 32);
-  rope_kernel<T, 2><<<a.num_tokens, threads, 0, stream>>>(a);
+  // four items a thread, so that a thread has 64 bytes (half layout: 128) in flight
+  const int threads = std::min(256, ((items + 3) / 4 + 31) / 32 * 32);
+  if (a.layout == RIMURU_ROPE_HALF) rope_kernel<T, true, 4><<<a.num_tokens, threads, 0, stream>>>(a);
+  else rope_kernel<T, false, 4><<<a.num_tokens, threads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -243,8 +245,9 @@ extern "C" int rimuru_rope_apply(rimuru_rope_t rope, const int32_t* positions, i
   for (int i = 0; i <= kMaxArrays; ++i) {
     a.first_item[i] = static_cast<int>(items);
     if (i < n_arrays) items += static_cast<int64_t>(in[i].heads) * a.items_per_head;
-    if (items > (1 << 28)) return fail(RIMURU_ERR_UNSUPPORTED, "too many heads");
+    if (items > (1 << 24)) return fail(RIMURU_ERR_UNSUPPORTED, "too many heads");
   }
+  a.head_mul = (1ull << 32) / a.items_per_head + 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = in[0].dtype == RIMURU_BF16  ? launch<__nv_bfloat16>(a, s)
                   : in[0].dtype == RIMURU_F16 ? launch<__half>(a, s)
