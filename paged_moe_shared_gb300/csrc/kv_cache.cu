@@ -176,14 +176,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     kv_append_kernel(const __grid_constant__ AppendArgs p) {
   __shared__ float tops[kAppendWarps];
   const int P = p.g.page_tokens, D = p.g.head_dim;
-  const int u = blockIdx.x;
-  int lo = 0, hi = p.s.num_seqs;  // first sequence with u < cu[b + 1] / P + 2 (b + 1)
-  while (lo < hi) {
+  const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // first sequence with u < cu[b + 1] / P + 2 (b + 1): by halves, the last 32 at once
+  int lo = 0, hi = p.s.num_seqs;
+  while (hi - lo > 32) {
     const int mid = (lo + hi) >> 1;
     if (u < p.s.cu[mid + 1] / P + 2 * (mid + 1)) hi = mid;
     else lo = mid + 1;
   }
-  const int b = lo;
+  const int probe = lo + lane;
+  const bool past = probe >= hi || u < p.s.cu[probe + 1] / P + 2 * (probe + 1);
+  const uint32_t hits = __ballot_sync(0xffffffffu, past);
+  const int b = hits ? lo + __ffs(hits) - 1 : hi;
   if (b >= p.s.num_seqs) return;
   const int r0 = p.s.cu[b], n = p.s.cu[b + 1] - r0;
   const int len = p.s.lens[b], start = len - n;
@@ -201,7 +205,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   }
   const int s0 = max(start - c * P, 0), s1 = min(len - c * P, P);  // slots to write
   const int row0 = r0 + c * P - start;                              // row of slot 0
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lanes = D / 8, at = lane % lanes, per = 32 / lanes;
   const int slices = 2 * p.g.kv_heads, wps = p.warps_per_slice;
   const int part = warp % wps, team = warp / wps, teams = (blockDim.x >> 5) / wps;

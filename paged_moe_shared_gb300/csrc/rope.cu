@@ -7,10 +7,10 @@
 // p * 2^-64 turns, and only the final conversion to fp32 rounds.  A negative
 // position is the same product modulo 2^64.
 //
-// Bound: HBM (each element is read and written once).  One CTA per token:
-// every thread first issues its loads, then the CTA computes the token's
-// cosines and sines once into shared memory (they serve all heads of all
-// arrays), then each thread turns what it loaded.
+// Bound: HBM (each element is read and written once).  A CTA takes one token, or
+// four of a long array: it computes their cosines and sines once into shared
+// memory (they serve all heads of all arrays), then every thread loads, turns
+// and stores 64 bytes (half layout: 128) at a time, without another barrier.
 #include <algorithm>
 #include <cmath>
 #include <limits>
@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kMaxPairs = 128;
 constexpr int kMaxArrays = 4;
+constexpr int kMaxTokens = 4;  // of a CTA
 
 struct RopeArray {
   const void* in;
@@ -37,7 +38,7 @@ struct RopeArgs {
   int first_item[kMaxArrays + 1];  // items (see kernel) of the arrays before this one
   const int32_t* positions;
   float mscale;
-  int pairs, layout, head_dim, num_tokens;
+  int pairs, layout, head_dim, num_tokens, tokens_per_cta;
   int turn_items, items_per_head;
   uint64_t head_mul;  // item / items_per_head = item * head_mul >> 32
 };
@@ -70,67 +71,69 @@ __device__ __forceinline__ void from_f(float x, float* y) { *y = x; }
 // the others copy a vector of eight past the rotated part.
 template <typename T, bool kHalf, int kPer>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs p) {
-  __shared__ float2 cs[kMaxPairs];
-  const int t = blockIdx.x;
+  __shared__ float2 cosines[kMaxTokens * kMaxPairs];
+  const int t0 = blockIdx.x * p.tokens_per_cta, n_tokens = min(p.tokens_per_cta, p.num_tokens - t0);
   const int n_items = p.first_item[kMaxArrays];
   const int rot = 2 * p.pairs;
-  for (int base = 0; base < n_items; base += kPer * blockDim.x) {
-    Vec8<T> a[kPer], b[kHalf ? kPer : 1];
-    T* dst[kPer];
-    int off[kPer];  // first element of the item in its head
+  for (int k = threadIdx.x; k < n_tokens * p.pairs; k += blockDim.x) {
+    const int t = k / p.pairs, i = k - t * p.pairs;
+    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + t]));
+    const int32_t turn = static_cast<int32_t>((pos * p.turn[i]) >> 32);  // 2^-32 turns
+    float s, c;
+    sincospif(static_cast<float>(turn) * 0x1p-31f, &s, &c);
+    cosines[k] = make_float2(c * p.mscale, s * p.mscale);
+  }
+  __syncthreads();
+  for (int t = t0; t < t0 + n_tokens; ++t) {
+    const float2* cs = cosines + (t - t0) * p.pairs;
+    for (int base = 0; base < n_items; base += kPer * blockDim.x) {
+      Vec8<T> a[kPer], b[kHalf ? kPer : 1];
+      T* dst[kPer];
+      int off[kPer];  // first element of the item in its head
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int item = base + j * blockDim.x + threadIdx.x;
-      dst[j] = nullptr;
-      if (item >= n_items) continue;
-      int s = 0;
+      for (int j = 0; j < kPer; ++j) {
+        const int item = base + j * blockDim.x + threadIdx.x;
+        dst[j] = nullptr;
+        if (item >= n_items) continue;
+        int s = 0;
 #pragma unroll
-      for (int i = 1; i < kMaxArrays; ++i) s += item >= p.first_item[i];
-      const RopeArray& A = p.arr[s];
-      const int local = item - p.first_item[s];
-      const int h = static_cast<int>(local * p.head_mul >> 32), i = local - h * p.items_per_head;
-      off[j] = i < p.turn_items ? 8 * i : rot + 8 * (i - p.turn_items);
-      const T* src = static_cast<const T*>(A.in) + t * A.in_ts + h * A.in_hs + off[j];
-      dst[j] = static_cast<T*>(A.out) + t * A.out_ts + h * A.out_hs + off[j];
-      a[j] = load8(src);
-      if (kHalf && off[j] < rot) b[kHalf ? j : 0] = load8(src + p.pairs);
-    }
-    if (base == 0) {
-      const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t]));
-      for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
-        const int32_t turn = static_cast<int32_t>((pos * p.turn[i]) >> 32);  // 2^-32 turns
-        float s, c;
-        sincospif(static_cast<float>(turn) * 0x1p-31f, &s, &c);
-        cs[i] = make_float2(c * p.mscale, s * p.mscale);
+        for (int i = 1; i < kMaxArrays; ++i) s += item >= p.first_item[i];
+        const RopeArray& A = p.arr[s];
+        const int local = item - p.first_item[s];
+        const int h = static_cast<int>(local * p.head_mul >> 32), i = local - h * p.items_per_head;
+        off[j] = i < p.turn_items ? 8 * i : rot + 8 * (i - p.turn_items);
+        const T* src = static_cast<const T*>(A.in) + t * A.in_ts + h * A.in_hs + off[j];
+        dst[j] = static_cast<T*>(A.out) + t * A.out_ts + h * A.out_hs + off[j];
+        a[j] = load8(src);
+        if (kHalf && off[j] < rot) b[kHalf ? j : 0] = load8(src + p.pairs);
       }
-      __syncthreads();
-    }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (!dst[j]) continue;
-      if (off[j] < rot) {
-        T* x = reinterpret_cast<T*>(&a[j]);
-        T* y = reinterpret_cast<T*>(&b[kHalf ? j : 0]);
-        if (kHalf) {
+      for (int j = 0; j < kPer; ++j) {
+        if (!dst[j]) continue;
+        if (off[j] < rot) {
+          T* x = reinterpret_cast<T*>(&a[j]);
+          T* y = reinterpret_cast<T*>(&b[kHalf ? j : 0]);
+          if (kHalf) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 w = cs[off[j] + e];
-            const float u = to_f(x[e]), v = to_f(y[e]);
-            from_f(u * w.x - v * w.y, &x[e]);
-            from_f(v * w.x + u * w.y, &y[e]);
-          }
-          store8(dst[j] + p.pairs, b[kHalf ? j : 0]);
-        } else {
+            for (int e = 0; e < 8; ++e) {
+              const float2 w = cs[off[j] + e];
+              const float u = to_f(x[e]), v = to_f(y[e]);
+              from_f(u * w.x - v * w.y, &x[e]);
+              from_f(v * w.x + u * w.y, &y[e]);
+            }
+            store8(dst[j] + p.pairs, b[kHalf ? j : 0]);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 w = cs[off[j] / 2 + e];
-            const float u = to_f(x[2 * e]), v = to_f(x[2 * e + 1]);
-            from_f(u * w.x - v * w.y, &x[2 * e]);
-            from_f(v * w.x + u * w.y, &x[2 * e + 1]);
+            for (int e = 0; e < 4; ++e) {
+              const float2 w = cs[off[j] / 2 + e];
+              const float u = to_f(x[2 * e]), v = to_f(x[2 * e + 1]);
+              from_f(u * w.x - v * w.y, &x[2 * e]);
+              from_f(v * w.x + u * w.y, &x[2 * e + 1]);
+            }
           }
         }
+        store8(dst[j], a[j]);
       }
-      store8(dst[j], a[j]);
     }
   }
 }
@@ -140,8 +143,9 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const int items = a.first_item[kMaxArrays];
   // four items a thread, so that a thread has 64 bytes (half layout: 128) in flight
   const int threads = std::min(256, ((items + 3) / 4 + 31) / 32 * 32);
-  if (a.layout == RIMURU_ROPE_HALF) rope_kernel<T, true, 4><<<a.num_tokens, threads, 0, stream>>>(a);
-  else rope_kernel<T, false, 4><<<a.num_tokens, threads, 0, stream>>>(a);
+  const int grid = (a.num_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta;
+  if (a.layout == RIMURU_ROPE_HALF) rope_kernel<T, true, 4><<<grid, threads, 0, stream>>>(a);
+  else rope_kernel<T, false, 4><<<grid, threads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -226,6 +230,7 @@ extern "C" int rimuru_rope_apply(rimuru_rope_t rope, const int32_t* positions, i
   a.positions = positions;
   a.head_dim = head_dim;
   a.num_tokens = num_tokens;
+  a.tokens_per_cta = num_tokens >= 2048 ? kMaxTokens : 1;  // below, one token a CTA fills the GPU better
   a.turn_items = (a.layout == RIMURU_ROPE_HALF ? a.pairs : rot) / 8;
   int64_t items = 0;
   bool inplace = true;
