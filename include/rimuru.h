@@ -569,7 +569,9 @@ int rimuru_rope_apply(rimuru_rope_t rope, const int32_t* positions, int num_toke
  * Requirements: kv_heads >= 1; head_dim 64, 128 or 256; page_tokens 16, 32 or
  * 64; 2 * kv_heads * page_tokens * head_dim <= page_bytes and page_bytes a
  * multiple of page_tokens * head_dim (RIMURU_ERR_UNSUPPORTED otherwise).
- * RIMURU_ERR_STATE if the view already has a shape of either kind. */
+ * RIMURU_ERR_STATE if the view already has a shape of either kind.
+ * rimuru_kv_append keeps every code of a token finite; a caller that writes
+ * codes itself must too (slots past a sequence's length may hold anything). */
 int rimuru_view_set_kv_shape(rimuru_view_t view, int kv_heads, int head_dim, int page_tokens,
                              float* dev_scales, uint64_t scales_bytes);
 /* Bytes of the scales array of a view with `kv_heads` heads; 0 on a bad argument. */
@@ -620,7 +622,12 @@ int rimuru_kv_append(rimuru_view_t view, const rimuru_heads* k, const rimuru_hea
  *             row per sequence (num_q == num_seqs)
  *   max_q     an upper bound of n_b
  *   workspace device, 1024-byte aligned, at least
- *             rimuru_kv_attention_workspace_bytes(...) bytes */
+ *             rimuru_kv_attention_workspace_bytes(...) bytes; calls that may run
+ *             at the same time need one each
+ * At most 128 query heads may share a key/value head, and the tiles of 128
+ * keys, summed over sequences (each at table_stride pages), kv heads and
+ * blocks of query rows, must stay below 2^31 (RIMURU_ERR_UNSUPPORTED).
+ * The value scales of the keys that one row sees may differ by up to 2^100. */
 uint64_t rimuru_kv_attention_workspace_bytes(rimuru_view_t view, int q_heads, int num_seqs,
                                              int num_q, int max_q);
 int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, const rimuru_heads* out,

@@ -73,6 +73,10 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   const uint64_t need = rimuru_kv_attention_workspace_bytes(view, q->heads, num_seqs, num_q, max_q);
   if (workspace_bytes < need)
     return fail(RIMURU_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  const AttnSplit w = split_of(v, q->heads, num_seqs, max_q);
+  const double tiles = (static_cast<double>(table_stride) * v.page_tokens / kTileTokens + 1) *
+                       num_seqs * v.kv_heads * w.units_per_pair;
+  if (tiles > 2e9) return fail(RIMURU_ERR_UNSUPPORTED, "too many keys and queries for one call");
   st = kv_ready(&v);
   if (st != RIMURU_OK) return st;
   AttnArgs a{};
@@ -90,7 +94,6 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.s = {cu_q, kv_lens, page_table, table_stride, num_seqs, num_q};
   a.g = kv_geom(v);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const AttnSplit w = split_of(v, q->heads, num_seqs, max_q);
   a.max_q = max_q;
   a.unit_rows = w.unit_rows;
   a.units_per_pair = w.units_per_pair;
@@ -98,9 +101,6 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.unit_q = w.unit_rows / a.group;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.join_bytes);
   a.stat = a.part + 2ll * (w.decode ? kMaxRuns : kMaxTileRuns) * w.unit_rows * v.head_dim;
-  const double tiles = (static_cast<double>(table_stride) * v.page_tokens / kTileTokens + 1) *
-                       num_seqs * v.kv_heads * w.units_per_pair;
-  if (tiles > 2e9) return fail(RIMURU_ERR_UNSUPPORTED, "too many keys and queries for one call");
   cudaError_t e;
   if (w.decode) {
     a.runs = std::min(kMaxRuns, kv_decode_runs(v.kv->sms, v.head_dim, w.unit_rows));

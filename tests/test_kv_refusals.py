@@ -100,7 +100,9 @@ def test_attention(views):
                    (dict(q=heads(n=7), out=heads(n=7)), R.ERR_UNSUPPORTED), (dict(lens=0), R.ERR_ARG),
                    (dict(table=0), R.ERR_ARG), (dict(stride=0), R.ERR_ARG), (dict(ws=0), R.ERR_ARG),
                    (dict(ws=4112), R.ERR_ALIGN), (dict(nbytes=need - 1), R.ERR_WORKSPACE),
-                   (dict(q=heads(n=8, data=4098)), R.ERR_ALIGN)):
+                   (dict(q=heads(n=8, data=4098)), R.ERR_ALIGN),
+                   (dict(q=heads(n=258), out=heads(n=258)), R.ERR_UNSUPPORTED),
+                   (dict(stride=1 << 40), R.ERR_UNSUPPORTED)):
         with pytest.raises(R.RimuruError) as e:
             go(**kw)
         assert e.value.status == st, kw
