@@ -10,7 +10,7 @@ namespace rimuru {
 struct AttnSplit {
   bool decode;
   int unit_rows, units_per_pair;
-  uint64_t join_bytes, part_bytes;
+  uint64_t cut_bytes, part_bytes;
 };
 AttnSplit split_of(const View& v, int q_heads, int num_seqs, int max_q) {
   const int group = q_heads / v.kv_heads;
@@ -22,8 +22,7 @@ AttnSplit split_of(const View& v, int q_heads, int num_seqs, int max_q) {
   w.unit_rows = rows <= 8 ? 8 : rows <= kDecodeMaxRows ? 16 : rows <= 128 ? 128 : tile_rows(v.head_dim);
   const int unit_q = std::max(1, w.unit_rows / group);
   w.units_per_pair = std::max(1, (max_q + unit_q - 1) / unit_q);
-  const uint64_t units = static_cast<uint64_t>(num_seqs) * v.kv_heads * w.units_per_pair;
-  w.join_bytes = (units * sizeof(int2) + 1023) / 1024 * 1024;
+  w.cut_bytes = (kMaxRuns * sizeof(int4) + 1023) / 1024 * 1024;
   w.part_bytes = 2ull * (w.decode ? kMaxRuns : kMaxTileRuns) * w.unit_rows * (v.head_dim + 1) * sizeof(float);  // and statistics
   return w;
 }
@@ -37,7 +36,7 @@ extern "C" uint64_t rimuru_kv_attention_workspace_bytes(rimuru_view_t view, int 
   if (!view || !view->v.has_kv || q_heads <= 0 || num_seqs < 0 || num_q < 0 || max_q < 0) return 0;
   if (q_heads % view->v.kv_heads != 0) return 0;
   const rimuru::AttnSplit w = rimuru::split_of(view->v, q_heads, num_seqs, max_q);
-  return w.join_bytes + w.part_bytes;
+  return w.cut_bytes + w.part_bytes;
 }
 
 extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, const rimuru_heads* out,
@@ -97,9 +96,9 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.max_q = max_q;
   a.unit_rows = w.unit_rows;
   a.units_per_pair = w.units_per_pair;
-  a.joins = static_cast<int2*>(workspace);
+  a.cuts = static_cast<int4*>(workspace);
   a.unit_q = w.unit_rows / a.group;
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.join_bytes);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.cut_bytes);
   a.stat = a.part + 2ll * (w.decode ? kMaxRuns : kMaxTileRuns) * w.unit_rows * v.head_dim;
   cudaError_t e;
   if (w.decode) {

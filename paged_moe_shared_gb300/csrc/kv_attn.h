@@ -35,7 +35,8 @@ struct AttnArgs {
   int unit_rows;       // query rows (query x group) of a unit
   int unit_q;          // whole query rows of a unit: unit_rows / group
   int units_per_pair;  // bound of the units of one (sequence, head)
-  int2* joins;         // [num_seqs][kv_heads][units_per_pair]: runs (first, last) of a unit cut up
+  int4* cuts;          // [runs] the unit that begins in a run and ends in a later one: first
+                       // query row, head * 512 + rows, unit, last run; 0 rows: there is none
   float* part;         // [2 runs][unit_rows][head_dim] partial results, then
   float* stat;         // [2 runs][unit_rows] their log2 sums
 };
@@ -283,13 +284,13 @@ struct RunWalk {
 __device__ __forceinline__ int64_t part_slot(const AttnArgs& p, int run, bool starts) {
   return static_cast<int64_t>(2 * run + (starts ? 1 : 0)) * p.unit_rows;
 }
-__device__ __forceinline__ int2* join_of(const AttnArgs& p, int b, int h, int w) {
-  return p.joins + (static_cast<int64_t>(b) * p.g.kv_heads + h) * p.units_per_pair + w;
-}
-// Notes which runs hold the parts of a unit (called where the unit begins).
-__device__ __forceinline__ void note_join(const AttnArgs& p, const Segment& g, const RunCut& k, int run) {
-  *join_of(p, g.b, g.h, g.w) =
-      g.ends ? make_int2(-1, -1) : make_int2(run, run_of(k, g.first + g.unit_tiles - 1));
+// Notes the unit that a run's last segment begins and does not end (a run cuts
+// no other one); called for every segment, over the zeros that the CTA begins with.
+__device__ __forceinline__ void note_cut(const AttnArgs& p, const Segment& g, const RunCut& k, int run) {
+  if (g.starts && !g.ends)
+    p.cuts[run] = make_int4(g.s.row0 + g.i0, g.h * 512 + (g.i1 - g.i0) * p.group,
+                            (g.b * p.g.kv_heads + g.h) * p.units_per_pair + g.w,
+                            run_of(k, g.first + g.unit_tiles - 1));
 }
 
 // Sets a kernel's dynamic shared memory limit once per device.

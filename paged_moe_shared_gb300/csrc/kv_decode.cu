@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
   grid_dep_wait();  // lengths, tables, q and the cache come from earlier kernels
   grid_dep_launch();
   find_run(p, blockIdx.x, sh->scratch, &sh->run);
+  if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
         }
         if (quad == 0 && lane < rows) p.stat[slot + lane] = stat;
       }
-      if (g.starts && tok == 0) note_join(p, g, sh->run.cut, blockIdx.x);
+      if (tok == 0) note_cut(p, g, sh->run.cut, blockIdx.x);
       ++seg;
     }
     if (!all && lane == 0) {
@@ -714,95 +715,173 @@ cudaError_t launch_dim(const AttnArgs& a, const CUtensorMap& tm, cudaStream_t s)
 
 // ---------------------------------------------------------------------- join
 // Adds the runs' partial rows, weighted by their share of the softmax sum, in
-// run order.  Rows of units without any tile become zero here.  A CTA takes
-// eight rows of a unit, one per warp, or one row, whose runs the warps split
-// (few units cut into many runs: a long context); their sums meet in shared
-// memory in warp order.
+// run order.  At most one unit is cut per run, so the grid goes over the runs and
+// blocks of rows (over the units, most of which one run has finished, the join
+// of a 2048-token chunk took 21 us instead of 15, for 40 MB of parts).  A warp takes
+// kRows rows, whose loads it keeps under way together; or, when few units are cut
+// into many runs (a long context), a CTA takes one row of a unit, its warps split
+// the runs, and their sums meet in shared memory in warp order.
 constexpr int kJoinWarps = 8;
 
-template <typename T, int kD, bool kSplitRuns>
-__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ AttnArgs p) {
-  constexpr int kPer = kD / 32;
-  __shared__ float sums[kJoinWarps][kD];
-  __shared__ float weight[kJoinWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int w = p.units_per_pair == 1 ? 0 : blockIdx.x % p.units_per_pair;
-  const int pair = p.units_per_pair == 1 ? blockIdx.x : blockIdx.x / p.units_per_pair;
-  const int b = pair / p.g.kv_heads, h = pair - b * p.g.kv_heads;
-  grid_dep_wait();
-  const SeqShape s = seq_shape(p, b);
-  int row0 = s.row0, n = s.n;
-  if (!s.ok) {  // inconsistent arguments: zero what of its rows lies inside the arrays
-    n = p.s.cu ? p.s.cu[b + 1] - row0 : 1;
-    n = row0 < 0 ? 0 : min(min(n, p.max_q), p.s.rows - row0);
-  }
-  const int i0 = w * p.unit_q, rows = (min(n, i0 + p.unit_q) - i0) * p.group;
-  if (rows <= 0) return;
-  TileSpan t{0, 0};
-  if (s.ok) t = unit_span(p, s, w);
-  const bool none = t.first >= t.last;
-  const int2 j = none ? make_int2(0, -1) : *join_of(p, b, h, w);
-  if (j.x < 0) return;  // finished by one run
-  const int r = kSplitRuns ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
-  if (r < rows) {
-    const auto slot = [&](int c) { return part_slot(p, c, c == j.x) + r; };
-    float top = -INFINITY, sum = 0.f, acc[kPer];
+template <typename T, int kPer>
+__device__ __forceinline__ void store_row(T* out, const float (&x)[kPer]) {
+  T v[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    for (int c = j.x + lane; c <= j.y; c += 32) top = fmaxf(top, p.stat[slot(c)]);
-    top = warp_max(top);
-    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-    for (int c = j.x + (kSplitRuns ? warp : 0); c <= j.y; c += kSplitRuns ? kJoinWarps : 1) {
-      const float e = ex2(p.stat[slot(c)] - ref);
-      const float* q = p.part + slot(c) * kD + lane * kPer;
-      sum += e;
-      float v[kPer];
-      if constexpr (kPer >= 4) {
+  for (int k = 0; k < kPer; ++k) from_f(x[k], v + k);
+  if constexpr (kPer == 8) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<uint4*>(v);
+  else if constexpr (kPer == 4) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<uint2*>(v);
+  else *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<uint32_t*>(v);
+}
+template <int kPer>
+__device__ __forceinline__ void load_part(const float* q, float (&v)[kPer]) {
+  if constexpr (kPer >= 4) {
 #pragma unroll
-        for (int i = 0; i < kPer; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(q + i);
-      } else {
-        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(q);
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += e * v[i];
-    }
-    if (kSplitRuns) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sums[warp][lane * kPer + i] = acc[i];
-      if (lane == 0) weight[warp] = sum;
-      __syncthreads();
-      if (warp != 0) return;
-#pragma unroll
-      for (int k = 1; k < kJoinWarps; ++k) {
-        sum += weight[k];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] += sums[k][lane * kPer + i];
-      }
-    }
-    const float inv = sum > 0.f ? 1.f / sum : sum;
-    const int i = r / p.group, head = h * p.group + r - i * p.group;
-    T v[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) from_f(acc[k] * inv, v + k);
-    T* out = static_cast<T*>(p.out) + (row0 + i0 + i) * p.o_ts + head * p.o_hs + lane * kPer;
-    if constexpr (kPer == 8) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<uint4*>(v);
-    else if constexpr (kPer == 4) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<uint2*>(v);
-    else *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<uint32_t*>(v);
-    if (p.lse && lane == 0)
-      p.lse[static_cast<int64_t>(row0 + i0 + i) * p.q_heads + head] =
-          sum > 0.f ? (ref + __log2f(sum)) * kLn2 : sum == 0.f ? -INFINITY : sum;
+    for (int i = 0; i < kPer; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(q + i);
+  } else {
+    *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(q);
   }
 }
 
-template <typename T>
+// The rows of units without any tile are zero (every query head's, by the warps
+// of the CTAs past the runs): a lane looks at a unit, the warp writes its rows.
+template <typename T, int kD>
+__device__ void zero_rows(const AttnArgs& p, int first, int step) {
+  const int lane = threadIdx.x & 31;
+  const int64_t units = static_cast<int64_t>(p.s.num_seqs) * p.units_per_pair;
+  for (int64_t at = static_cast<int64_t>(first) * 32; at < units; at += static_cast<int64_t>(step) * 32) {
+    int row0 = 0, n = 0;
+    if (at + lane < units) {
+      const int b = static_cast<int>((at + lane) / p.units_per_pair), w = static_cast<int>((at + lane) % p.units_per_pair);
+      const SeqShape s = seq_shape(p, b);
+      row0 = s.row0, n = s.n;
+      if (!s.ok) {  // inconsistent arguments: zero what of its rows lies inside the arrays
+        n = p.s.cu ? p.s.cu[b + 1] - row0 : 1;
+        n = row0 < 0 ? 0 : min(min(n, p.max_q), p.s.rows - row0);
+      }
+      const int i0 = w * p.unit_q;
+      // one unit a pair holds all of its rows, be they more than a unit's (arguments that disagree)
+      n = p.units_per_pair == 1 ? n : min(n - i0, p.unit_q);
+      row0 += i0;
+      if (n > 0 && s.ok) {
+        const TileSpan t = unit_span(p, s, w);
+        if (t.first < t.last) n = 0;
+      }
+    }
+    for (uint32_t todo = __ballot_sync(0xffffffffu, n > 0); todo != 0; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;
+      const int r0 = __shfl_sync(0xffffffffu, row0, from), m = __shfl_sync(0xffffffffu, n, from);
+      const float none[kD / 32] = {};
+      for (int i = 0; i < m * p.q_heads; ++i) {
+        const int64_t row = r0 + i / p.q_heads, head = i % p.q_heads;
+        store_row(static_cast<T*>(p.out) + row * p.o_ts + head * p.o_hs + lane * (kD / 32), none);
+        if (p.lse && lane == 0) p.lse[row * p.q_heads + head] = -INFINITY;
+      }
+    }
+  }
+}
+
+template <typename T, int kD, int kRows>  // kRows 0: a row per CTA, its runs split over the warps
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ AttnArgs p) {
+  constexpr int kPer = kD / 32, kN = kRows > 0 ? kRows : 1;
+  __shared__ float sums[kRows == 0 ? kJoinWarps : 1][kD];
+  __shared__ float weight[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int units = kRows == 0 ? p.s.num_seqs * p.g.kv_heads * p.units_per_pair : p.runs;
+  grid_dep_wait();
+  if (static_cast<int>(blockIdx.x) >= units) {
+    if (blockIdx.y == 0)
+      zero_rows<T, kD>(p, (blockIdx.x - units) * kJoinWarps + warp, (gridDim.x - units) * kJoinWarps);
+    return;
+  }
+  int c0 = blockIdx.x;
+  int4 cut;
+  if (kRows == 0) {  // the unit's entry, if it is cut
+    __shared__ int4 found;
+    __shared__ int where;
+    if (threadIdx.x == 0) where = -1;
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.runs; c += 32 * kJoinWarps) {
+      const int4 e = p.cuts[c];
+      if (e.y > 0 && e.z == static_cast<int>(blockIdx.x)) found = e, where = c;
+    }
+    __syncthreads();
+    c0 = where;
+    if (c0 < 0) return;
+    cut = found;
+  } else {
+    cut = p.cuts[c0];
+  }
+  const int rows = cut.y % 512, h = cut.y / 512;  // no rows: no entry
+  const int r0 = kRows == 0 ? blockIdx.y : (blockIdx.y * kJoinWarps + warp) * kN;
+  if (r0 >= rows) return;
+  const auto slot = [&](int c, int r) { return part_slot(p, c, c == c0) + min(r, rows - 1); };
+  float ref[kN], sum[kN], acc[kN][kPer];
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= cut.w; c += 32) top = fmaxf(top, p.stat[slot(c, r0 + k)]);
+    top = warp_max(top);
+    ref[k] = top == -INFINITY ? 0.f : top;
+    sum[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[k][i] = 0.f;
+  }
+#pragma unroll 2
+  for (int c = c0 + (kRows == 0 ? warp : 0); c <= cut.w; c += kRows == 0 ? kJoinWarps : 1) {
+    float v[kN][kPer];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) load_part(p.part + slot(c, r0 + k) * kD + lane * kPer, v[k]);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const float e = ex2(p.stat[slot(c, r0 + k)] - ref[k]);
+      sum[k] += e;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[k][i] += e * v[k][i];
+    }
+  }
+  if (kRows == 0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sums[warp][lane * kPer + i] = acc[0][i];
+    if (lane == 0) weight[warp] = sum[0];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int k = 1; k < kJoinWarps; ++k) {
+      sum[0] += weight[k];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[0][i] += sums[k][lane * kPer + i];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int r = r0 + k;
+    if (r >= rows) return;
+    const float inv = sum[k] > 0.f ? 1.f / sum[k] : sum[k];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[k][i] *= inv;
+    const int i = r / p.group;
+    const int64_t row = cut.x + i, head = h * p.group + r - i * p.group;
+    store_row(static_cast<T*>(p.out) + row * p.o_ts + head * p.o_hs + lane * kPer, acc[k]);
+    if (p.lse && lane == 0)
+      p.lse[row * p.q_heads + head] =
+          sum[k] > 0.f ? (ref[k] + __log2f(sum[k])) * kLn2 : sum[k] == 0.f ? -INFINITY : sum[k];
+  }
+}
+
+template <typename T, int kD>
 cudaError_t launch_join(const AttnArgs& a, cudaStream_t s) {
-  const int64_t units = static_cast<int64_t>(a.s.num_seqs) * a.g.kv_heads * a.units_per_pair;
-  // With four runs a unit or more, one CTA per row whose warps split the runs.
+  const int64_t pairs = static_cast<int64_t>(a.s.num_seqs) * a.units_per_pair, units = pairs * a.g.kv_heads;
+  // With four runs a unit or more, one CTA per row whose warps split the runs.  Else a row a warp
+  // while that fits the 64 warps of the SMs (16 sequences of 40 rows: 35.9 us the call, 40.4 with
+  // four rows a warp), four rows beyond.
   const bool split = units * 4 <= a.runs;
+  const int64_t bound = std::max<int64_t>(1, std::min<int64_t>(a.unit_rows, static_cast<int64_t>(a.max_q) * a.group));
+  const int per = split ? 0 : a.runs * bound <= 152 * 64 ? 1 : 4;
+  const int rows = split ? 1 : per * kJoinWarps;  // of a CTA
+  const int64_t zero = std::min<int64_t>(a.runs, (pairs + 32 * kJoinWarps - 1) / (32 * kJoinWarps));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units),
-                     static_cast<unsigned>(split ? a.unit_rows : a.unit_rows / kJoinWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>((split ? units : a.runs) + zero),
+                     static_cast<unsigned>((bound + rows - 1) / rows));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
@@ -810,12 +889,15 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const auto go = [&](auto kernel_split, auto kernel_rows) {
-    return split ? cudaLaunchKernelEx(&cfg, kernel_split, a) : cudaLaunchKernelEx(&cfg, kernel_rows, a);
-  };
-  if (a.g.head_dim == 64) return go(kv_join_kernel<T, 64, true>, kv_join_kernel<T, 64, false>);
-  if (a.g.head_dim == 128) return go(kv_join_kernel<T, 128, true>, kv_join_kernel<T, 128, false>);
-  return go(kv_join_kernel<T, 256, true>, kv_join_kernel<T, 256, false>);
+  return split ? cudaLaunchKernelEx(&cfg, kv_join_kernel<T, kD, 0>, a)
+         : per == 1 ? cudaLaunchKernelEx(&cfg, kv_join_kernel<T, kD, 1>, a)
+                    : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, kD, 4>, a);
+}
+template <typename T>
+cudaError_t join_dim(const AttnArgs& a, cudaStream_t s) {
+  if (a.g.head_dim == 64) return launch_join<T, 64>(a, s);
+  if (a.g.head_dim == 128) return launch_join<T, 128>(a, s);
+  return launch_join<T, 256>(a, s);
 }
 
 }  // namespace
@@ -827,7 +909,7 @@ cudaError_t launch_kv_decode(const AttnArgs& a, int dtype, const CUtensorMap& tm
 }
 
 cudaError_t launch_kv_join(const AttnArgs& a, int dtype, cudaStream_t s) {
-  return dtype == RIMURU_BF16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<__half>(a, s);
+  return dtype == RIMURU_BF16 ? join_dim<__nv_bfloat16>(a, s) : join_dim<__half>(a, s);
 }
 
 }  // namespace rimuru

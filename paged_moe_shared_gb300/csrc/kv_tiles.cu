@@ -20,11 +20,13 @@
 // Two softmax warpgroups alternate on two score buffers ("items"), so that the
 // tensor cores work on one while the other is in softmax.  With head_dim <= 128
 // and more than 128 rows the items are two query tiles (each K and V tile serves
-// 256 rows, a row is a thread); otherwise successive key tiles of one query
-// tile, whose columns the two warpgroups halve.
+// 256 rows, a row is a thread).  With one query tile the items are successive key
+// tiles: where O fits the tensor memory twice (head_dim <= 128) the warpgroups take
+// them in turns, each with a reference, a sum and an O of its own that are added up
+// at the end; with head_dim 256 both work on each item and halve its columns.
 //
 // Warps 0-3 and 4-7: softmax.  8-11: widening V.  12: K copies, and the pages and
-// scales of each key tile for the others.  13: MMAs.  14: V copies.
+// scales of each key tile for the others.  13 and 15: MMAs.  14: V copies.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -49,7 +51,10 @@ struct TileCfg {
   static constexpr int kSlabs = kD / kRowBytes;
   static constexpr int kSlabBytes = 128 * kRowBytes;
   static constexpr int kKBytes = kSlabs * kSlabBytes;           // one K tile
-  static constexpr int kKRing = kD <= 128 ? 3 : 2;              // K tiles
+  // One query tile whose O fits the tensor memory twice: the warpgroups take key tiles in turns.
+  static constexpr bool kTurns = kTiles == 1 && kD <= 128;
+  // K tiles.  In turns an even number: then a slot belongs to one of the two MMA warps.
+  static constexpr int kKRing = kTurns ? 4 : kD <= 128 ? 3 : 2;
   static constexpr int kQBytes = kQParts * kTiles * kKBytes;    // [part][tile][slab][128 rows]
   static constexpr int kVTok = kD <= 128 ? 64 : 32;             // tokens of a V stage
   static constexpr int kVStages = kTileTokens / kVTok;          // stages of a tile
@@ -57,11 +62,13 @@ struct TileCfg {
   static constexpr bool kWide = kQParts == 3 && (kD == 256 || kTiles == 2);  // Q takes 96 KiB
   static constexpr int kVRing = kWide ? 2 : 4;
   static constexpr int kVRaw = kVTok * kD;                      // codes of a stage
-  static constexpr int kFifo = kD == 256 ? (kWide ? 2 : 3) : kTiles == 2 ? 4 : 6;  // stages of codes
+  static constexpr int kFifo = kD == 256 ? (kWide ? 2 : 3) : kTiles == 2 || kQParts == 3 ? 4 : 6;  // stages of codes
   static constexpr int kStage = kD == 64 ? 8 * 4096 : 0;        // output staging; else in Q's place
   static constexpr int kSmem =
       1024 + kQBytes + kKRing * kKBytes + kVRing * kVBytes + kFifo * kVRaw + kStage;
   static constexpr uint32_t kO = 256;                           // TMEM column of O; scores are at 0 and 128
+  static constexpr int kIssuers = kTiles == 2 || kTurns ? 2 : 1;     // MMA warps
+  static constexpr int kScoreN = kTiles == 1 && !kTurns ? 128 : 64;  // keys of one batch of scores
 };
 
 struct __align__(16) Meta {  // a 16-token group of a tile
@@ -76,8 +83,8 @@ struct TileShared {
   uint64_t raw_full[6], raw_empty[6];
   uint64_t meta_full[kMetaRing];
   uint64_t q_full;
-  uint64_t s_full[2], o_full[2];
-  uint64_t p_full[2][2], o_half[2];  // by halves of the key tile
+  uint64_t o_full[2];
+  uint64_t s_full[2][2], p_full[2][2], o_half[2];  // by halves of the key tile
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -203,9 +210,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh->k_full[i], 1);
-      mbar_init(&sh->k_empty[i], 1);
+      mbar_init(&sh->k_empty[i], kTiles);
       mbar_init(&sh->v_full[i], 4);
-      mbar_init(&sh->v_empty[i], 1);
+      mbar_init(&sh->v_empty[i], kTiles);
     }
     for (int i = 0; i < 6; ++i) {
       mbar_init(&sh->raw_full[i], 1);
@@ -214,13 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMetaRing; ++i) mbar_init(&sh->meta_full[i], 1);
     mbar_init(&sh->q_full, 8);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->s_full[i][0], 1);
+      mbar_init(&sh->s_full[i][1], 1);
       mbar_init(&sh->p_full[i][0], 4);
       mbar_init(&sh->p_full[i][1], 4);
       mbar_init(&sh->o_half[i], 1);
       mbar_init(&sh->o_full[i], 1);
     }
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->drain, C::kIssuers);
     sh->abort = 0;
     fence_barrier_init();
     prefetch_tmap(&tm);
@@ -233,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();  // lengths, tables, q and the cache come from earlier kernels
   grid_dep_launch();
   find_run(p, blockIdx.x, sh->scratch, &sh->run);
+  if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -329,34 +338,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int never = 0;
       for (uint32_t j = tile > C::kKRing ? tile - C::kKRing : 0u; j < tile; ++j)
         mbar_wait_idle(&sh->k_full[j % C::kKRing], (j / C::kKRing) & 1u, &never);
-    } else if (warp == 13) {
+    } else if (warp == 13 || (C::kIssuers == 2 && warp == 15)) {
       // ------------------------------------------------------------------ MMAs
       // Items: (key tile, query tile) pairs in order; item i uses score buffer i & 1.
-      // The scores of item i + 2 follow the output of item i, whose weights lie in
-      // the same buffer; MMAs of one thread run in the order they were issued.
+      // Weights lie in the same buffer, each half of 64 keys over its own scores, so
+      // the scores of half h of item i + 2 follow the output of half h of item i, and
+      // are there when its softmax warps come back (with 128 keys at a time they
+      // waited 1,250 of 3,900 cycles a tile for them).  MMAs of one thread run in the
+      // order they were issued.
       // The whole warp walks and waits, and one lane issues: addresses stay
       // warp-uniform (issued from a one-lane branch, an MMA took 160 cycles to issue
       // instead of the 64 it runs).
-      constexpr uint32_t id_s = idesc_f8_f32(128, 128, false, false, false);
+      constexpr uint32_t id_s = idesc_f8_f32(128, C::kScoreN, false, false, false);
       constexpr uint32_t id_o = idesc_f16_f32(128, kD, false, /*b_mn=*/true);
       constexpr uint32_t kHiQK = desc_hi(kAtom, kSwizzle), kHiV = desc_hi(1024, 2);
       const uint32_t tb = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t q_lo = __shfl_sync(0xffffffffu, desc_lo(smem_u32(sQ), 16), 0);
       const uint32_t k_lo = __shfl_sync(0xffffffffu, desc_lo(smem_u32(sK), 16), 0);
       const uint32_t v_lo = __shfl_sync(0xffffffffu, desc_lo(smem_u32(sV), C::kVTok * 128), 0);
-      uint32_t item = 0, k_slot = 0, k_phase = 0, v_slot = 0, v_phase = 0, seg = 0;
+      // Two warps issue, each for one query tile or turn: an MMA takes as long to issue as
+      // it runs, and while one warp waits on its barriers the other's are under way.
+      const int mine = C::kIssuers == 2 && warp == 15 ? 1 : 0;
+      uint32_t item0 = 0, tile = 0, seg = 0;
       bool ok = true;
       const auto wait = [&](uint64_t* bar, uint32_t phase) {
         ok = ok && mbar_wait_idle(bar, phase, abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       };
-      // The next scores go to buffer `item`'s parity; `q`: its query tile.
-      const auto scores = [&](uint32_t buffer, uint32_t q) {
-        if (q == 0) wait(&sh->k_full[k_slot], k_phase);
+      // The scores of key tile kt, its half h (128 keys at a time: h is 0), into `buffer`.
+      constexpr int kLastHalf = 128 / C::kScoreN - 1;
+      const auto scores = [&](uint32_t kt, uint32_t buffer, int h) {
+        const uint32_t slot = kt % C::kKRing;
+        if (h == 0) wait(&sh->k_full[slot], (kt / C::kKRing) & 1u);
         if (ok && elect_one()) {
-          const uint32_t a0 = q_lo + q * (C::kKBytes / 16), b0 = k_lo + k_slot * (C::kKBytes / 16);
-          const uint32_t d = tb + 128 * buffer;
+          const uint32_t a0 = q_lo + (kTiles == 2 ? mine : 0) * (C::kKBytes / 16);
+          const uint32_t b0 = k_lo + slot * (C::kKBytes / 16) + h * (64 * kRowBytes / 16);
+          const uint32_t d = tb + 128 * buffer + 64 * h;
 #pragma unroll
           for (int part = 0; part < kQParts; ++part) {
 #pragma unroll
@@ -368,45 +386,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                     b0 + sl * (C::kSlabBytes / 16) + 2 * k, (part | sl | k) != 0 ? 1u : 0u);
             }
           }
-          umma_commit(&sh->s_full[buffer]);
-          if (q == kTiles - 1) umma_commit(&sh->k_empty[k_slot]);
+          umma_commit(&sh->s_full[buffer][h]);
+          if (h == kLastHalf) umma_commit(&sh->k_empty[slot]);
         }
         __syncwarp();
-        if (q == kTiles - 1 && ++k_slot == C::kKRing) k_slot = 0, k_phase ^= 1u;
       };
+      constexpr int kStep = C::kTurns ? 2 : 1;       // key tiles from one item of this warp's to the next
+      constexpr int kAhead = C::kIssuers == 2 ? kStep : 2;  // from an item to the next one in its buffer
+      const auto buffer_of = [&](int n) { return kTiles == 2 ? static_cast<uint32_t>(mine) : (item0 + n) & 1u; };
       while (__any_sync(0xffffffffu, ok && walk.next(p, &g))) {
         const int tiles = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
         wait(&sh->q_full, seg & 1u);
-        scores(item & 1u, 0);
-        if (kTiles == 2) scores((item + 1) & 1u, 1);
-        else if (tiles > 1) scores((item + 1) & 1u, 0);
-        for (int n = 0; ok && n < tiles; ++n) {
-          const uint32_t v_slot0 = v_slot, v_phase0 = v_phase;
+        const int n0 = C::kTurns ? mine : 0;
+        for (int n = n0; n < min(tiles, n0 + kAhead); n += kStep) {
 #pragma unroll
-          for (int q = 0; q < kTiles; ++q, ++item) {
-            const uint32_t buffer = item & 1u;
-            v_slot = v_slot0, v_phase = v_phase0;
-#pragma unroll
-            for (int h = 0; h < C::kVStages; ++h) {
-              if (h % (C::kVStages / 2) == 0)
-                wait(&sh->p_full[buffer][h / (C::kVStages / 2)], (item >> 1) & 1u);
-              if (q == 0) wait(&sh->v_full[v_slot], v_phase);
-              if (ok && elect_one()) {
-                const uint32_t b0 = v_lo + v_slot * (C::kVBytes / 16);
-#pragma unroll
-                for (int k = 0; k < C::kVTok / 16; ++k)  // 16 tokens: eight columns of P, 16 rows of V
-                  umma_f16_ts_lo<kHiV, id_o>(tb + C::kO + q * kD, tb + 128 * buffer + C::kVTok / 2 * h + 8 * k,
-                                             b0 + 128 * k, (h + k != 0) ? 1u : n > 0 ? 1u : 0u);
-                if (q == kTiles - 1) umma_commit(&sh->v_empty[v_slot]);
-                if (h == C::kVStages / 2 - 1) umma_commit(&sh->o_half[buffer]);
-                if (h == C::kVStages - 1) umma_commit(&sh->o_full[buffer]);
-              }
-              __syncwarp();
-              if (++v_slot == C::kVRing) v_slot = 0, v_phase ^= 1u;
-            }
-            if (kTiles == 2 ? n + 1 < tiles : n + 2 < tiles) scores(buffer, q);
-          }
+          for (int h = 0; h <= kLastHalf; ++h) scores(tile + n, buffer_of(n), h);
         }
+        for (int n = n0; ok && n < tiles; n += kStep) {
+          const uint32_t buffer = buffer_of(n), item = item0 + (kTiles == 2 ? 2 * n + mine : n);
+          const uint32_t o = tb + C::kO + (kTiles == 2 || C::kTurns ? mine : 0) * kD;
+#pragma unroll
+          for (int st = 0; st < C::kVStages; ++st) {
+            constexpr int kPer = C::kVStages / 2;  // stages of a half
+            const uint32_t v = (tile + n) * C::kVStages + st, slot = v % C::kVRing;
+            wait(&sh->v_full[slot], (v / C::kVRing) & 1u);
+            if (st % kPer == 0) wait(&sh->p_full[buffer][st / kPer], (item >> 1) & 1u);
+            if (ok && elect_one()) {
+              const uint32_t b0 = v_lo + slot * (C::kVBytes / 16);
+              const uint32_t a0 = tb + 128 * buffer + 64 * (st / kPer) + C::kVTok / 2 * (st % kPer);
+#pragma unroll
+              for (int k = 0; k < C::kVTok / 16; ++k)  // 16 tokens: eight columns of P, 16 rows of V
+                umma_f16_ts_lo<kHiV, id_o>(o, a0 + 8 * k, b0 + 128 * k, (st + k != 0) || n >= kStep ? 1u : 0u);
+              umma_commit(&sh->v_empty[slot]);
+              if (st == kPer - 1) umma_commit(&sh->o_half[buffer]);
+              if (st == C::kVStages - 1) umma_commit(&sh->o_full[buffer]);
+            }
+            __syncwarp();
+            if (kLastHalf == 1 && n + kAhead < tiles) scores(tile + n + kAhead, buffer, st);
+          }
+          if (kLastHalf == 0 && n + kAhead < tiles) scores(tile + n + kAhead, buffer, 0);
+        }
+        item0 += tiles * kTiles;
+        tile += tiles;
         ++seg;
       }
       if (!ok && lane == 0) {
@@ -509,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;  // row of the query tile, and TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const int qt = kTiles == 2 ? wg : 0;             // query tile
-    const uint32_t tO = tmem + C::kO + qt * kD + lane_off;
+    constexpr bool kTurns = C::kTurns, kHalves = kTiles == 1 && !kTurns;  // kHalves: both have a part of each tile
+    const uint32_t tO = tmem + C::kO + (kHalves ? 0 : wg) * kD + lane_off;
     const uint32_t group_mul = 65536u / p.group + 1;  // r / group = r * group_mul >> 16 for r < 256
     uint32_t tile = 0, item0 = 0;
     bool ok = true;
@@ -589,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j_lo = real && p.window > 0 ? max(0, pos - p.window + 1) : 0;
       float ref = kNoRef, l = 0.f;
       const int n_tiles = g.t1 - g.t0;
-      for (int n = 0; n < n_tiles; ++n) {
+      for (int n = kTurns ? wg : 0; n < n_tiles; n += kTurns ? 2 : 1) {
         const int t = g.t0 + n;
         const uint32_t item = item0 + (kTiles == 2 ? 2 * n + wg : n), slot = item & 1u;
         const uint32_t m = (tile + n) % kMetaRing;
@@ -602,17 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int j0 = t * kTileTokens + 64 * h;
           if (__any_sync(0xffffffffu, j_lo > j0 || j_hi < j0 + 64 || (seen.x & seen.y) != 0xFFFFFFFFu)) edges |= 1u << h;
         }
-        ok = mbar_wait_idle(&sh->s_full[slot], (item >> 1) & 1u, abort) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (kTiles == 2 && !ok) break;
-        tc_fence_after();
         const uint32_t tS = tmem + 128 * slot + lane_off;
-        // Half a tile, 64 columns, at a time; with one query tile each warpgroup has its half.
+        // Half a tile, 64 columns, at a time; with kHalves each warpgroup has its half.
         // The loop is kept rolled: past the first 10 KiB of instructions, which the warps of a
         // scheduler share, a warp runs three times slower.
 #pragma unroll 1
-        for (int h = kTiles == 2 ? 0 : wg; h < (kTiles == 2 ? 2 : wg + 1); ++h) {
+        for (int h = kHalves ? wg : 0; h < (kHalves ? wg + 1 : 2); ++h) {
           uint32_t v[64], w[32];
+          ok = mbar_wait_idle(&sh->s_full[slot][C::kScoreN == 128 ? 0 : h], (item >> 1) & 1u, abort) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!kHalves && !ok) break;
+          tc_fence_after();
           tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
           tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
           tmem_ld_wait32(*reinterpret_cast<uint32_t(*)[32]>(&v[0]));
@@ -655,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               got += (sum.x + sum.y) * kv.z;
             }
             const bool redo = !settled && ((ref == kNoRef && sees) || raw > kMostSum);
-            if (kTiles == 2) {
+            if (!kHalves) {
               if (!__any_sync(0xffffffffu, redo)) break;
             } else {
               if (!softmax_or(redo || !ok)) break;
@@ -669,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[16 * q + k]));
               top = fmaxf(top, x * (c_row * kv.x) + kv.y);
             }
-            if (kTiles == 1) {  // two threads have the row's halves and agree on its reference
+            if (kHalves) {  // two threads have the row's halves and agree on its reference
               sh->other[wg][row] = top;
               if (!(ok = softmax_and(ok))) break;
               top = fmaxf(top, sh->other[wg ^ 1][row]);
@@ -677,19 +699,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float now = fmaxf(top, ref), f = ref == kNoRef ? 1.f : ex2(ref - now);
             ref = now;
             l *= f;
-            // O of the row, once the MMAs so far are done: those of the tile before, or of
-            // this tile's first half
-            if (n > 0 || (kTiles == 2 && h > 0)) {
-              const bool second = kTiles == 2 && h > 0;
-              const uint32_t last = second ? item : kTiles == 2 ? item - 2 : item - 1;
+            // O of the row, once the MMAs so far are done: those of the row's tile before, or
+            // of this tile's first half
+            if (n > (kTurns ? 1 : 0) || (!kHalves && h > 0)) {
+              const bool second = !kHalves && h > 0;
+              const uint32_t last = second ? item : kHalves ? item - 1 : item - 2;
               ok = mbar_wait_idle(second ? &sh->o_half[slot] : &sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
               ok = __all_sync(0xffffffffu, ok);
               tc_fence_after();
-              constexpr int kO = kTiles == 2 ? kD : kD / 2;
+              constexpr int kO = kHalves ? kD / 2 : kD;
 #pragma unroll 1
               for (int k = 0; k < kO; k += 16) {
                 uint32_t o[16];
-                const uint32_t at = tO + (kTiles == 2 ? 0 : wg * kO) + k;
+                const uint32_t at = tO + (kHalves ? wg * kO : 0) + k;
                 tmem_ld16(at, o);
                 tmem_ld_wait();
 #pragma unroll
@@ -699,30 +721,41 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_wait();
             }
           }
-          if (kTiles == 1 && !ok) break;
+          if (kHalves && !ok) break;
           l += got;
-          // over scores already read (with one query tile, by both halves: the barrier above)
-          tmem_st32(tS + 32 * h, w);
+          tmem_st32(tS + 64 * h, w);  // over the half's own scores
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->p_full[slot][h]);  // this half's MMAs may begin
         }
-        if (kTiles == 1 && !ok) break;
+        if (!ok) break;
       }
       const uint32_t items = n_tiles * kTiles;
       if (kTiles == 2 && !ok) break;
-      // the rows: O / l
-      {
-        const uint32_t last = item0 + items - 1 - (kTiles == 2 ? 1 - wg : 0);
+      // the rows: O / l, once this warpgroup's last item is done
+      if (!kTurns || wg < n_tiles) {
+        const uint32_t last = item0 + items - 1 -
+                              (kTiles == 2 ? 1 - wg : kTurns ? (n_tiles - 1 - wg) & 1 : 0);
         ok = mbar_wait_idle(&sh->o_full[last & 1u], (last >> 1) & 1u, abort) && ok;
         ok = __all_sync(0xffffffffu, ok);
       }
-      if (kTiles == 1) {  // the two halves of the row's sum
+      float f0 = 1.f, f1 = 0.f;  // of the two O of a row, with kTurns
+      if (kTiles == 1) {  // the two parts of the row's sum
         sh->row_sum[wg][row] = l;
+        if (kTurns) sh->other[wg][row] = ref;
         ok = softmax_and(ok);
         if (!ok) break;
-        l = sh->row_sum[0][row] + sh->row_sum[1][row];
+        const float l0 = sh->row_sum[0][row], l1 = sh->row_sum[1][row];
+        if (kTurns) {
+          const float r0 = sh->other[0][row], r1 = sh->other[1][row];
+          ref = fmaxf(r0, r1);
+          f0 = r0 == kNoRef ? 0.f : ex2(r0 - ref);
+          f1 = r1 == kNoRef ? 0.f : ex2(r1 - ref);
+          l = l0 * f0 + l1 * f1;
+        } else {
+          l = l0 + l1;
+        }
       }
       if (!ok) break;
       tc_fence_after();
@@ -740,8 +773,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int k = 0; k < kO; k += 32) {
         uint32_t v[32];
-        tmem_ld32(tO + d0 + k, v);
+        const uint32_t t0 = kTurns ? tmem + C::kO + lane_off : tO;
+        tmem_ld32(t0 + d0 + k, v);
         tmem_ld_wait32(v);
+        if (kTurns) {
+          if (n_tiles > 1) {  // the other one has held no key otherwise
+            uint32_t u[32];
+            tmem_ld32(t0 + kD + d0 + k, u);
+            tmem_ld_wait32(u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = __float_as_uint(__uint_as_float(v[i]) * f0 + __uint_as_float(u[i]) * f1);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f0);
+          }
+        }
         __syncwarp();
         if (whole) {
 #pragma unroll
@@ -786,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (p.lse)
           p.lse[static_cast<int64_t>(g.s.row0 + g.i0 + qi) * p.q_heads + g.h * p.group + gi] = stat * kLn2;
       }
-      if (g.starts && threadIdx.x == 0) note_join(p, g, sh->run.cut, blockIdx.x);
+      if (threadIdx.x == 0) note_cut(p, g, sh->run.cut, blockIdx.x);
       tile += n_tiles;
       item0 += items;
     }
