@@ -73,9 +73,10 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   if (workspace_bytes < need)
     return fail(RIMURU_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
   const AttnSplit w = split_of(v, q->heads, num_seqs, max_q);
-  const double tiles = (static_cast<double>(table_stride) * v.page_tokens / kTileTokens + 1) *
-                       num_seqs * v.kv_heads * w.units_per_pair;
-  if (tiles > 2e9) return fail(RIMURU_ERR_UNSUPPORTED, "too many keys and queries for one call");
+  const int cost = w.decode ? kDecodeUnitCost : kTileUnitCost;
+  const double places = (static_cast<double>(table_stride) * v.page_tokens / kTileTokens + 1 + cost) *
+                        num_seqs * v.kv_heads * w.units_per_pair;
+  if (places > 2e9) return fail(RIMURU_ERR_UNSUPPORTED, "too many keys and queries for one call");
   st = kv_ready(&v);
   if (st != RIMURU_OK) return st;
   AttnArgs a{};
@@ -96,6 +97,7 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.max_q = max_q;
   a.unit_rows = w.unit_rows;
   a.units_per_pair = w.units_per_pair;
+  a.unit_cost = cost;
   a.cuts = static_cast<int4*>(workspace);
   a.unit_q = w.unit_rows / a.group;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.cut_bytes);

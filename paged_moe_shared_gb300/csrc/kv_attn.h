@@ -2,10 +2,11 @@
 // layout of the partial results that are joined afterwards.
 //
 // A unit is a (sequence, key/value head, block of query rows); its work is the
-// 128-token tiles of keys that any of its rows sees.  The tiles of all units,
-// laid end to end, are cut into equal runs, one per CTA, so the CTAs finish
-// together whatever the lengths are, and no length has to be known on the
-// host.  A unit that lies within one run is finished there; the others leave
+// 128-token tiles of keys that any of its rows sees, and before them `unit_cost`
+// places for what it costs to begin and end one.  The places of all units, laid
+// end to end, are cut into equal runs, one per CTA, so the CTAs finish together
+// whatever the lengths are, and no length has to be known on the host (with tiles
+// alone, the CTAs that had many short units were the last ones).  A unit that lies within one run is finished there; the others leave
 // one partial result per run (normalised rows and their log2 sums), which the
 // join kernel adds up in run order.
 #pragma once
@@ -35,6 +36,7 @@ struct AttnArgs {
   int unit_rows;       // query rows (query x group) of a unit
   int unit_q;          // whole query rows of a unit: unit_rows / group
   int units_per_pair;  // bound of the units of one (sequence, head)
+  int unit_cost;       // places of a unit before its tiles
   int4* cuts;          // [runs] the unit that begins in a run and ends in a later one: first
                        // query row, head * 512 + rows, unit, last run; 0 rows: there is none
   float* part;         // [2 runs][unit_rows][head_dim] partial results, then
@@ -118,100 +120,129 @@ __device__ __forceinline__ int pair_tiles(const AttnArgs& p, const SeqShape& s) 
   return (u > 1 ? tiles_before(p, s, u - 1) : 0) + t.last - t.first;
 }
 
-// The total is cut into `runs` runs of base or base + 1 tiles, the longer first.
+// All places are cut into `runs` runs of base or base + 1 places, the longer first.
 struct RunCut {
   int base, longer, runs;
 };
 __device__ __forceinline__ int run_start(const RunCut& k, int c) { return c * k.base + min(c, k.longer); }
-__device__ __forceinline__ int run_of(const RunCut& k, int tile) {
+__device__ __forceinline__ int run_of(const RunCut& k, int place) {
   const int head = k.longer * (k.base + 1);
-  return tile < head ? tile / (k.base + 1) : k.longer + (tile - head) / k.base;
+  return place < head ? place / (k.base + 1) : k.longer + (place - head) / k.base;
 }
 
-// One run: its tiles and where its first one lies.
+// One run: where its first tile lies, and its tiles.
 struct RunStart {
   RunCut cut;
-  int begin, tiles;  // of the total
-  int b, h, w, at;   // sequence, head, unit, and the tile within the unit
+  int before[2];      // tiles before the run's first and after its last place
+  int place;          // of its first tile
+  int b, h, w, at;    // sequence, head, unit, and the tile within the unit
   SeqShape s;
+  struct {            // an end of the run within its (sequence, head): places from there, tiles before
+    int at, before;
+    SeqShape s;
+  } end[2];
+  __device__ __forceinline__ int tiles() const { return before[1] - before[0]; }
 };
 
-// Found by the whole CTA (every thread calls it; `scratch` has an int per
-// warp): thread t sums the tiles of a contiguous share of the sequences, the
-// shares are scanned, and the thread whose share holds the run's first tile
-// walks its share.  Totals fit an int (checked on the host).
-__device__ __forceinline__ void find_run(const AttnArgs& p, int c, int* scratch, RunStart* out) {
-  const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5;
+// Found by the whole CTA (every thread calls it; `scratch` has a number per
+// warp): thread t sums the tiles and units of a contiguous share of the
+// sequences, the shares are scanned, and the thread whose share holds an end of
+// the run walks its share.  Totals fit an int (checked on the host).
+__device__ __forceinline__ void find_run(const AttnArgs& p, int c, uint64_t* scratch, RunStart* out) {
+  const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5, cost = p.unit_cost;
   const int share = p.s.num_seqs <= nt ? 1 : (p.s.num_seqs + nt - 1) / nt;
   const int b0 = min(p.s.num_seqs, t * share), b1 = min(p.s.num_seqs, b0 + share);
-  int mine = 0, n0 = 0;
+  uint64_t mine = 0;  // tiles, and units in the upper half
   SeqShape s0{};
+  int n0 = 0;
   for (int b = b0; b < b1; ++b) {
     const SeqShape s = seq_shape(p, b);
     if (!s.ok && c == 0) dev::set_error(p.g.err, RIMURU_DEV_BAD_SHAPE);
     const int n = pair_tiles(p, s);
     if (b == b0) s0 = s, n0 = n;
-    mine += n * p.g.kv_heads;
+    mine += (static_cast<uint64_t>(units_of(p, s)) << 32 | static_cast<uint32_t>(n)) * p.g.kv_heads;
   }
-  int scan = mine;
+  uint64_t scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, scan, o);
+    const uint64_t v = __shfl_up_sync(0xffffffffu, scan, o);
     if (lane >= o) scan += v;
   }
   if (lane == 31) scratch[warp] = scan;
   __syncthreads();
-  int before = scan - mine, total = 0;
+  uint64_t before = scan - mine, total = 0;
   for (int w = 0; w < nt / 32; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
-  // no run between the first and the last is empty, so every run of a unit leaves a part
+  const auto tiles_in = [](uint64_t x) { return static_cast<int>(static_cast<uint32_t>(x)); };
+  const auto places_in = [&](uint64_t x) { return tiles_in(x) + static_cast<int>(x >> 32) * cost; };
+  // Runs may hold no tile; but those from the first to the last tile of a unit all hold some of
+  // it, so every one of them leaves a part.
+  const int places = places_in(total), first = places_in(before), own = places_in(mine);
   RunCut k;
-  k.runs = min(total, p.runs);
-  k.base = k.runs > 0 ? total / k.runs : 0;
-  k.longer = total - k.base * k.runs;
-  const int begin = c < k.runs ? run_start(k, c) : total;
-  const int tiles = c < k.runs ? k.base + (c < k.longer ? 1 : 0) : 0;
+  k.runs = min(places, p.runs);
+  k.base = k.runs > 0 ? places / k.runs : 0;
+  k.longer = places - k.base * k.runs;
+  const int ends[2] = {c < k.runs ? run_start(k, c) : places, c < k.runs ? run_start(k, c + 1) : places};
   if (t == 0) {
     out->cut = k;
-    out->begin = begin;
-    out->tiles = tiles;
-  }
-  if (tiles > 0 && begin >= before && begin < before + mine) {
-    int at = begin - before, b = b0, n = n0;
-    SeqShape s = s0;
-    while (at >= n * p.g.kv_heads) {
-      at -= n * p.g.kv_heads;
-      s = seq_shape(p, ++b);
-      n = pair_tiles(p, s);
-    }
-    int h = 0;
-    while (at >= n) at -= n, ++h;
-    out->b = b;
-    out->h = h;
-    out->w = 0;
-    out->at = at;
-    out->s = s;
+    out->before[0] = out->before[1] = tiles_in(total);
   }
   __syncthreads();
-  if (p.units_per_pair == 1 || tiles == 0) return;
-  // the unit: the last one with at most `at` tiles before it, one thread per group of units
-  const SeqShape s = out->s;
-  const int at = out->at, u = units_of(p, s), per = (u + nt - 1) / nt;
-  const int w0 = t * per, w1 = min(u, w0 + per);
-  if (w0 < u) {
-    int n = tiles_before(p, s, w0);
-    const int after = w1 < u ? tiles_before(p, s, w1) : at + 1;
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    if (ends[e] < first || ends[e] >= first + own) continue;
+    int at = ends[e] - first, b = b0, n = n0, sum = tiles_in(before);
+    SeqShape s = s0;
+    int each = n + units_of(p, s) * cost;
+    while (at >= each * p.g.kv_heads) {
+      at -= each * p.g.kv_heads;
+      sum += n * p.g.kv_heads;
+      s = seq_shape(p, ++b);
+      n = pair_tiles(p, s);
+      each = n + units_of(p, s) * cost;
+    }
+    int h = 0;
+    while (at >= each) at -= each, sum += n, ++h;
+    if (p.units_per_pair == 1) {
+      const int tile = max(0, at - cost);
+      out->before[e] = sum + tile;
+      if (e == 0) out->w = 0, out->at = tile, out->place = ends[0] - at + max(at, cost);
+    } else {
+      out->end[e].at = at;
+      out->end[e].before = sum;
+      out->end[e].s = s;
+    }
+    if (e == 0) {
+      out->b = b;
+      out->h = h;
+      out->s = s;
+    }
+  }
+  __syncthreads();
+  if (p.units_per_pair == 1) return;
+  // the unit: the last one with at most `at` places before it, one thread per group of units
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    if (ends[e] >= places) break;
+    const SeqShape s = out->end[e].s;
+    const int at = out->end[e].at, u = units_of(p, s), per = (u + nt - 1) / nt;
+    const int w0 = t * per, w1 = min(u, w0 + per);
+    if (w0 >= u) continue;
+    const auto places_before = [&](int w) { return tiles_before(p, s, w) + w * cost; };
+    int n = places_before(w0);
+    const int after = w1 < u ? places_before(w1) : at + 1;
     if (n <= at && at < after) {
       int w = w0;
       for (; w + 1 < w1; ++w) {
         const TileSpan x = unit_span(p, s, w);
-        if (n + x.last - x.first > at) break;
-        n += x.last - x.first;
+        if (n + cost + max(0, x.last - x.first) > at) break;
+        n += cost + max(0, x.last - x.first);
       }
-      out->w = w;
-      out->at = at - n;
+      const int y = at - n, tile = max(0, y - cost);
+      out->before[e] = out->end[e].before + n - w * cost + tile;
+      if (e == 0) out->w = w, out->at = tile, out->place = ends[0] - y + max(y, cost);
     }
   }
   __syncthreads();
@@ -223,18 +254,18 @@ struct Segment {
   SeqShape s;
   int i0, i1;         // query rows of the unit
   int t0, t1;         // its tiles within this run
-  int first;          // the first of them, counted over all units
+  int place;          // of the first of them
   int unit_tiles;     // tiles of the whole unit
   bool starts, ends;  // holds the unit's first / last tile
 };
 struct RunWalk {
-  int left, at, begin;
+  int left, at, place;  // tiles of the run still to come; the next one's within its unit, and its place
   int b, h, w, u;  // next unit; u: units of sequence b
   SeqShape s;
   __device__ __forceinline__ void begin_run(const AttnArgs& p, const RunStart& r) {
-    left = r.tiles;
+    left = r.tiles();
     if (left <= 0) return;
-    begin = r.begin;
+    place = r.place;
     b = r.b;
     h = r.h;
     w = r.w;
@@ -250,6 +281,7 @@ struct RunWalk {
         t = unit_span(p, s, w);
         if (t.last > t.first) break;
         ++w;
+        place += p.unit_cost;
       } else if (h + 1 < p.g.kv_heads && u > 0) {
         ++h, w = 0;
       } else {
@@ -267,12 +299,12 @@ struct RunWalk {
     g->i1 = min(s.n, g->i0 + p.unit_q);
     g->t0 = t.first + at;
     g->t1 = min(t.last, g->t0 + left);
-    g->first = begin;
+    g->place = place;
     g->unit_tiles = t.last - t.first;
     g->starts = at == 0;
     g->ends = g->t1 == t.last;
     left -= g->t1 - g->t0;
-    begin += g->t1 - g->t0;
+    place += g->t1 - g->t0 + p.unit_cost;
     at = 0;
     ++w;
     return true;
@@ -290,7 +322,7 @@ __device__ __forceinline__ void note_cut(const AttnArgs& p, const Segment& g, co
   if (g.starts && !g.ends)
     p.cuts[run] = make_int4(g.s.row0 + g.i0, g.h * 512 + (g.i1 - g.i0) * p.group,
                             (g.b * p.g.kv_heads + g.h) * p.units_per_pair + g.w,
-                            run_of(k, g.first + g.unit_tiles - 1));
+                            run_of(k, g.place + g.unit_tiles - 1));
 }
 
 // Sets a kernel's dynamic shared memory limit once per device.
@@ -311,6 +343,12 @@ struct SmemOnce {
 // No grid has more runs than this, so the workspace has one size on every device.
 constexpr int kMaxRuns = 320;      // decode kernel: up to two CTAs per SM
 constexpr int kMaxTileRuns = 160;  // tile kernel: one
+
+// What it costs to begin and end a unit, in tiles.  Decode, 64 sequences of 1 to 4014 keys: 23.3 us
+// the call at 0, 16.9 at 2, 17.3 at 3, 17.7 at 4, 19.0 at 6.  Tiles, six prompts of 209 to 855
+// tokens at head_dim 256: 110 us at 0, 66.0 at 3, 63.2 at 4, 66.4 at 5, 70.5 at 8; 16 sequences of
+// 3 to 5 rows: 36.0, 30.6, 29.4, 29.5, 30.7.
+constexpr int kDecodeUnitCost = 2, kTileUnitCost = 4;
 
 // Launchers (the result is cudaGetLastError's).
 cudaError_t launch_kv_decode(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s);

@@ -77,7 +77,7 @@ struct DecodeShared {
   int abort;
   int fresh[2];  // the tile's O starts afresh
   RunStart run;
-  int scratch[8];
+  uint64_t scratch[8];
   float2 meta[kMetaRing][8];  // per page of a tile: scales of K and V; V 0: no such page
   float tile_max[4][kDecodeMaxRows];
   float row_scale[2][kDecodeMaxRows];

@@ -89,7 +89,7 @@ struct TileShared {
   uint32_t tmem_base;
   int abort;
   RunStart run;
-  int scratch[16];
+  uint64_t scratch[16];
   Meta meta[kMetaRing][kGroups];
   uint32_t seen[kMetaRing][4];    // a bit per token of the tile: its group has a page
   int4 span[kMetaRing];           // tokens [x, y) of the tile count (and have pages if z); w: head
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A box is a page's tokens, at most a stage's; lane l copies box l of a stage.
       const uint64_t pol = policy_evict_last();
       const int per = min(P, C::kVTok), boxes = C::kVTok / per;
-      const uint32_t total = sh->run.tiles * C::kVStages;
+      const uint32_t total = sh->run.tiles() * C::kVStages;
       uint32_t slot = 0, phase = 1;
       bool ok = true;
       uint32_t v = 0;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const dst0 = sV + (c >> 2) * (C::kVTok * 128) + r0 * 128;
     const uint8_t* const src0 = sRaw + r0 * kD + 16 * c;
     bool ok = true;
-    const uint32_t total = sh->run.tiles * C::kVStages;
+    const uint32_t total = sh->run.tiles() * C::kVStages;
     uint32_t v_slot = 0, v_phase = 1, raw_slot = 0, raw_phase = 0;
 #pragma unroll 1
     for (uint32_t v = 0; v < total; ++v) {
