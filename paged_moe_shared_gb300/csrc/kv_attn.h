@@ -187,9 +187,9 @@ __device__ __forceinline__ void find_run(const AttnArgs& p, int c, uint64_t* scr
   const int ends[2] = {c < k.runs ? run_start(k, c) : places, c < k.runs ? run_start(k, c + 1) : places};
   if (t == 0) {
     out->cut = k;
-    out->before[0] = out->before[1] = tiles_in(total);
+    for (int e = 0; e < 2; ++e)
+      if (ends[e] == places) out->before[e] = tiles_in(total);
   }
-  __syncthreads();
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     if (ends[e] < first || ends[e] >= first + own) continue;
@@ -222,18 +222,17 @@ __device__ __forceinline__ void find_run(const AttnArgs& p, int c, uint64_t* scr
   }
   __syncthreads();
   if (p.units_per_pair == 1) return;
-  // the unit: the last one with at most `at` places before it, one thread per group of units
-#pragma unroll 1
-  for (int e = 0; e < 2; ++e) {
-    if (ends[e] >= places) break;
+  // the unit: the last one with at most `at` places before it, one thread per group of units;
+  // half of the CTA looks for either end
+  const int half = nt / 64 * 32, e = t >= half, te = e ? t - half : t, ne = e ? nt - half : half;
+  if (ends[e] < places) {
     const SeqShape s = out->end[e].s;
-    const int at = out->end[e].at, u = units_of(p, s), per = (u + nt - 1) / nt;
-    const int w0 = t * per, w1 = min(u, w0 + per);
-    if (w0 >= u) continue;
+    const int at = out->end[e].at, u = units_of(p, s), per = (u + ne - 1) / ne;
+    const int w0 = min(u, te * per), w1 = min(u, w0 + per);
     const auto places_before = [&](int w) { return tiles_before(p, s, w) + w * cost; };
     int n = places_before(w0);
     const int after = w1 < u ? places_before(w1) : at + 1;
-    if (n <= at && at < after) {
+    if (w0 < w1 && n <= at && at < after) {
       int w = w0;
       for (; w + 1 < w1; ++w) {
         const TileSpan x = unit_span(p, s, w);
