@@ -16,10 +16,13 @@ AttnSplit split_of(const View& v, int q_heads, int num_seqs, int max_q) {
   const int group = q_heads / v.kv_heads;
   AttnSplit w{};
   const int64_t rows = static_cast<int64_t>(max_q) * group;
-  // Up to 16 rows take the decode kernel.  Beyond, a unit is 128 rows, or 256 where two query
-  // tiles fit the tensor memory and there are rows for them.
+  // Up to 16 rows take the decode kernel, in units of 8 or 16 rows (32 sequences of 2000 keys,
+  // head_dim 128: 8 rows 18.2 us, in units of 16 25.6; 16 rows 26.9 us, with the tile kernel
+  // 31.9).  Beyond, a unit is 128 rows, or 256 from 257 rows on where two query tiles fit the
+  // tensor memory (eight sequences of 2000 keys: 256 rows 29.0 us in units of 128, 37.9 of 256;
+  // 512 rows 38.0 and 38.2; one of 8000 keys: 8192 rows 137 and 121).
   w.decode = rows <= kDecodeMaxRows;
-  w.unit_rows = rows <= 8 ? 8 : rows <= kDecodeMaxRows ? 16 : rows <= 128 ? 128 : tile_rows(v.head_dim);
+  w.unit_rows = rows <= 8 ? 8 : rows <= kDecodeMaxRows ? 16 : rows <= 256 ? 128 : tile_rows(v.head_dim);
   const int unit_q = std::max(1, w.unit_rows / group);
   w.units_per_pair = std::max(1, (max_q + unit_q - 1) / unit_q);
   w.cut_bytes = (kMaxRuns * sizeof(int4) + 1023) / 1024 * 1024;

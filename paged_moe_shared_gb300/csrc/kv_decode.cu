@@ -31,6 +31,10 @@
 // time), warp 1 issues the MMAs, warp 2 prepares Q of the next segment, warps
 // 3-6 do the softmax.  S and O are double buffered in TMEM, so K Q^T of the next
 // tile, of the next segment too, runs during the softmax of this one.
+//
+// Two sequences of 130,000 keys, 16/2 heads of 256 (264 MB): 50 us with the join,
+// 5.3 TB/s; a CTA takes 2,790 cycles a 64 KiB tile, the copy rate, after 5 us to its
+// first.  64 sequences of 1 to 4014 keys, 32/4 heads of 128 (32 MB): 16.9 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>

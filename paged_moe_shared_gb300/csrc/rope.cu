@@ -11,6 +11,8 @@
 // four of a long array: it computes their cosines and sines once into shared
 // memory (they serve all heads of all arrays), then every thread loads, turns
 // and stores 64 bytes (half layout: 128) at a time, without another barrier.
+// 8192 tokens of 36 heads of 128, bf16 (151 MB): 30.3 us, 5.0 TB/s, 0.74 of the copy
+// rate; 35 us with one token a CTA.  One token: 3.0 us, a launch.
 #include <algorithm>
 #include <cmath>
 #include <limits>

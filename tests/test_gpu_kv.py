@@ -491,6 +491,34 @@ def test_a_sequence_alone_and_in_a_batch_agree():
     c.close()
 
 
+@pytest.mark.parametrize("G,D", [(8, 128), (7, 64), (8, 256)])
+@pytest.mark.parametrize("q_len", [1, 2, 3, 16, 17, 18, 32, 33, 37])
+def test_where_the_kernels_change(q_len, G, D):
+    c = Cache(2, D, 16, 80)
+    lens = [300, 513, q_len]
+    table = c.tables(lens, seed=q_len)
+    c.fill(table, lens, seed=1)
+    cu = [0, q_len, 2 * q_len, 3 * q_len]
+    q = qkv(cu[-1], (2 * G,), D, "bf16", q_len)[0]
+    check_attention(c, q, cu, lens, table, "bf16")
+    c.close()
+
+
+@pytest.mark.parametrize("q_max", [1, 4, 40])
+def test_many_short_sequences_and_some_without_keys_or_rows(q_max):
+    rng = np.random.default_rng(q_max)
+    lens = rng.choice([0, 1, 2, 15, 16, 17, 40, 127, 128, 129, 260], size=400).tolist()
+    c = Cache(2, 64, 16, sum(-(-n // 16) for n in lens))
+    table = c.tables(lens, seed=1)
+    c.fill(table, lens, seed=2)
+    n = rng.integers(0, q_max + 1, size=400) if q_max > 1 else np.ones(400, int)
+    cu = [0] + np.cumsum(n).tolist()
+    q = qkv(cu[-1], (6,), 64, "bf16", 3)[0]
+    check_attention(c, q, cu, lens, table, "bf16", max_q=q_max)
+    check_attention(c, q, cu, lens, table, "bf16", max_q=q_max, window=30)
+    c.close()
+
+
 # ------------------------------------------------------------------ pages
 @pytest.mark.parametrize("Hk,D,P,extra", [(4, 128, 16, 0), (2, 256, 32, 32768), (1, 64, 16, 0)])
 @pytest.mark.parametrize("n", [1, 7, 500])
