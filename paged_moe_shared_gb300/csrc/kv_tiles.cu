@@ -19,7 +19,7 @@
 //
 // Two softmax warpgroups alternate on two score buffers ("items"), so that the
 // tensor cores work on one while the other is in softmax.  With head_dim <= 128
-// and more than 128 rows the items are two query tiles (each K and V tile serves
+// and units of 256 rows the items are two query tiles (each K and V tile serves
 // 256 rows, a row is a thread).  With one query tile the items are successive key
 // tiles: where O fits the tensor memory twice (head_dim <= 128) the warpgroups take
 // them in turns, each with a reference, a sum and an O of its own that are added up
