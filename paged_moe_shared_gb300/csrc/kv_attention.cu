@@ -105,15 +105,15 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.unit_q = w.unit_rows / a.group;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.cut_bytes);
   a.stat = a.part + 2ll * (w.decode ? kMaxRuns : kMaxTileRuns) * w.unit_rows * v.head_dim;
-  cudaError_t e;
-  if (w.decode) {
-    a.runs = std::min(kMaxRuns, kv_decode_runs(v.kv->sms, v.head_dim, w.unit_rows));
-    e = launch_kv_decode(a, q->dtype, v.kv->tm_codes, s);
-  } else {
-    a.runs = std::min(kMaxTileRuns, v.kv->sms);
-    e = launch_kv_tiles(a, q->dtype, v.kv->tm_codes, v.kv->tm_values, s);
-  }
-  if (e == cudaSuccess) e = launch_kv_join(a, q->dtype, s);
+  const int64_t units = static_cast<int64_t>(num_seqs) * v.kv_heads * w.units_per_pair;
+  const int64_t most = (table_stride * v.page_tokens + kTileTokens - 1) / kTileTokens;  // tiles of a unit
+  a.runs = w.decode ? std::min(kMaxRuns, kv_decode_runs(v.kv->sms, v.head_dim, w.unit_rows))
+                    : std::min(kMaxTileRuns, v.kv->sms);
+  a.direct = leave_whole(units, most, a.runs, cost, w.unit_rows, v.head_dim);
+  if (a.direct) a.runs = static_cast<int>(units);
+  cudaError_t e = w.decode ? launch_kv_decode(a, q->dtype, v.kv->tm_codes, s)
+                           : launch_kv_tiles(a, q->dtype, v.kv->tm_codes, v.kv->tm_values, s);
+  if (e == cudaSuccess && !a.direct) e = launch_kv_join(a, q->dtype, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("attention launch", e));
   return RIMURU_OK;
 }

@@ -37,6 +37,7 @@ struct AttnArgs {
   int unit_q;          // whole query rows of a unit: unit_rows / group
   int units_per_pair;  // bound of the units of one (sequence, head)
   int unit_cost;       // places of a unit before its tiles
+  bool direct;         // a CTA per unit, none is cut and nothing joined
   int4* cuts;          // [runs] the unit that begins in a run and ends in a later one: first
                        // query row, head * 512 + rows, unit, last run; 0 rows: there is none
   float* part;         // [2 runs][unit_rows][head_dim] partial results, then
@@ -247,6 +248,57 @@ __device__ __forceinline__ void find_run(const AttnArgs& p, int c, uint64_t* scr
   __syncthreads();
 }
 
+// First row and number of the query rows of a unit that has no tile: they become
+// zero.  Where the arguments disagree, what of its rows lies inside the arrays.
+struct RowSpan {
+  int row0, n;
+};
+__device__ __forceinline__ RowSpan empty_rows(const AttnArgs& p, const SeqShape& s, int b, int w) {
+  int n = s.n;
+  if (!s.ok) {
+    n = p.s.cu ? p.s.cu[b + 1] - s.row0 : 1;
+    n = s.row0 < 0 ? 0 : min(min(n, p.max_q), p.s.rows - s.row0);
+  }
+  const int i0 = w * p.unit_q;
+  // one unit a pair holds all of its rows, be they more than a unit's (arguments that disagree)
+  n = p.units_per_pair == 1 ? n : min(n - i0, p.unit_q);
+  if (n > 0 && s.ok) {
+    const TileSpan t = unit_span(p, s, w);
+    if (t.first < t.last) n = 0;
+  }
+  return {s.row0 + i0, n};
+}
+
+// The same for a CTA that has one unit, `u` in the order of the cuts; it also
+// writes the zeros of a unit without tiles.  T: type of the results.
+template <typename T>
+__device__ __forceinline__ void find_unit(const AttnArgs& p, int u, RunStart* out) {
+  const int w = u % p.units_per_pair, pair = u / p.units_per_pair, b = pair / p.g.kv_heads;
+  const int h = pair - b * p.g.kv_heads;
+  const SeqShape s = seq_shape(p, b);  // every thread: one broadcast load each
+  const bool has = w < units_of(p, s);
+  const TileSpan t = has ? unit_span(p, s, w) : TileSpan{0, 0};
+  if (threadIdx.x == 0) {
+    if (!s.ok) dev::set_error(p.g.err, RIMURU_DEV_BAD_SHAPE);
+    out->before[0] = 0;
+    out->before[1] = max(0, t.last - t.first);
+    out->place = out->at = 0;
+    out->b = b;
+    out->h = h;
+    out->w = w;
+    out->s = s;
+  }
+  const RowSpan r = empty_rows(p, s, b, w);
+  const int per = p.g.head_dim / 8;  // 16 bytes a thread
+  for (int i = threadIdx.x; i < r.n * p.group * per; i += blockDim.x) {
+    const int row = i / per, q = row / p.group;
+    const int64_t to = r.row0 + q, head = h * p.group + row - q * p.group;
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to * p.o_ts + head * p.o_hs + (i - row * per) * 8) =
+        make_uint4(0, 0, 0, 0);
+    if (p.lse && i == row * per) p.lse[to * p.q_heads + head] = -INFINITY;
+  }
+}
+
 // Walks a run segment by segment: the part of a unit that lies in the run.
 struct Segment {
   int b, h, w;        // sequence, head, unit
@@ -348,6 +400,17 @@ constexpr int kMaxTileRuns = 160;  // tile kernel: one
 // tokens at head_dim 256: 110 us at 0, 66.0 at 3, 63.2 at 4, 66.4 at 5, 70.5 at 8; 16 sequences of
 // 3 to 5 rows: 36.0, 30.6, 29.4, 29.5, 30.7.
 constexpr int kDecodeUnitCost = 2, kTileUnitCost = 4;
+
+// What cutting costs, in tiles: the second kernel, the parts and the search for the run.  Where the
+// longest unit has at most as many tiles as that and a run of half-full units together, and all
+// units run at the same time, they are better left whole.  Cut and whole, us: one sequence, 8 rows
+// a head, of 500 keys 9.8 and 8.4, of 2000 keys 10.4 and 20.1; 64 of 1000 keys 19.3 and 14.3; eight,
+// 40 rows, of 500 keys 15.7 and 11.4, of 2000 19.5 and 25.0; the last 256 of 1000 tokens, 32/4 heads,
+// 36.2 and 23.5.
+inline bool leave_whole(int64_t units, int64_t most, int runs, int unit_cost, int unit_rows, int head_dim) {
+  const int cut = unit_rows == 256 ? 10 : unit_rows <= 16 && head_dim == 256 ? 4 : 6;
+  return units <= runs && 2 * most * runs <= 2 * cut * runs + units * (most + 2 * unit_cost);
+}
 
 // Launchers (the result is cudaGetLastError's).
 cudaError_t launch_kv_decode(const AttnArgs& a, int dtype, const CUtensorMap& tm, cudaStream_t s);

@@ -191,8 +191,12 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas(kD, kR))
   }
   grid_dep_wait();  // lengths, tables, q and the cache come from earlier kernels
   grid_dep_launch();
-  find_run(p, blockIdx.x, sh->scratch, &sh->run);
-  if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (p.direct) {
+    find_unit<T>(p, blockIdx.x, &sh->run);
+  } else {
+    find_run(p, blockIdx.x, sh->scratch, &sh->run);
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -756,20 +760,8 @@ __device__ void zero_rows(const AttnArgs& p, int first, int step) {
     int row0 = 0, n = 0;
     if (at + lane < units) {
       const int b = static_cast<int>((at + lane) / p.units_per_pair), w = static_cast<int>((at + lane) % p.units_per_pair);
-      const SeqShape s = seq_shape(p, b);
-      row0 = s.row0, n = s.n;
-      if (!s.ok) {  // inconsistent arguments: zero what of its rows lies inside the arrays
-        n = p.s.cu ? p.s.cu[b + 1] - row0 : 1;
-        n = row0 < 0 ? 0 : min(min(n, p.max_q), p.s.rows - row0);
-      }
-      const int i0 = w * p.unit_q;
-      // one unit a pair holds all of its rows, be they more than a unit's (arguments that disagree)
-      n = p.units_per_pair == 1 ? n : min(n - i0, p.unit_q);
-      row0 += i0;
-      if (n > 0 && s.ok) {
-        const TileSpan t = unit_span(p, s, w);
-        if (t.first < t.last) n = 0;
-      }
+      const RowSpan r = empty_rows(p, seq_shape(p, b), b, w);
+      row0 = r.row0, n = r.n;
     }
     for (uint32_t todo = __ballot_sync(0xffffffffu, n > 0); todo != 0; todo &= todo - 1) {
       const int from = __ffs(todo) - 1;

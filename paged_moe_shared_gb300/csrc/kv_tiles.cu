@@ -251,8 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dep_wait();  // lengths, tables, q and the cache come from earlier kernels
   grid_dep_launch();
-  find_run(p, blockIdx.x, sh->scratch, &sh->run);
-  if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (p.direct) {
+    find_unit<T>(p, blockIdx.x, &sh->run);
+  } else {
+    find_run(p, blockIdx.x, sh->scratch, &sh->run);
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

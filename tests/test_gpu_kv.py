@@ -504,6 +504,23 @@ def test_where_the_kernels_change(q_len, G, D):
     c.close()
 
 
+@pytest.mark.parametrize("G,D,dtype", [(8, 128, "bf16"), (5, 64, "f16"), (8, 256, "bf16")])
+@pytest.mark.parametrize("q_len", [1, 3, 40])
+def test_a_wide_page_table_changes_nothing_but_the_split(q_len, G, D, dtype):
+    """The bound of the lengths that the table gives decides whether units are cut."""
+    lens = [0, 900, 17, 130, q_len]
+    c = Cache(2, D, 16, sum(-(-n // 16) for n in lens))
+    cu = [i * q_len for i in range(len(lens) + 1)]
+    q = qkv(cu[-1], (2 * G,), D, dtype, q_len)[0]
+    for spare in (0, 4000):
+        table = c.tables(lens, seed=1, spare=spare)
+        if spare == 0:
+            c.fill(table, lens, seed=1)
+        check_attention(c, q, cu, lens, table, dtype)
+        check_attention(c, q, cu, lens, table, dtype, window=150)
+    c.close()
+
+
 @pytest.mark.parametrize("q_max", [1, 4, 40])
 def test_many_short_sequences_and_some_without_keys_or_rows(q_max):
     rng = np.random.default_rng(q_max)
