@@ -625,8 +625,9 @@ int rimuru_kv_append(rimuru_view_t view, const rimuru_heads* k, const rimuru_hea
  *             rimuru_kv_attention_workspace_bytes(...) bytes; calls that may run
  *             at the same time need one each
  * At most 128 query heads may share a key/value head, and the tiles of 128
- * keys, summed over sequences (each at table_stride pages), kv heads and
- * blocks of query rows, must stay below 2^31 (RIMURU_ERR_UNSUPPORTED).
+ * keys (a few more for each unit), summed over sequences (each at table_stride
+ * pages), kv heads and blocks of query rows, must stay below 2 * 10^9
+ * (RIMURU_ERR_UNSUPPORTED).
  * The value scales of the keys that one row sees may differ by up to 2^100. */
 uint64_t rimuru_kv_attention_workspace_bytes(rimuru_view_t view, int q_heads, int num_seqs,
                                              int num_q, int max_q);
