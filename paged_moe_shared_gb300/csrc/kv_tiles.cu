@@ -60,7 +60,7 @@ struct TileCfg {
   static constexpr int kKBytes = kSlabs * kSlabBytes;           // one K tile
   // One query tile whose O fits the tensor memory twice: the warpgroups take key tiles in turns.
   static constexpr bool kTurns = kTiles == 1 && kD <= 128;
-  // K tiles.  In turns an even number: then a slot belongs to one of the two MMA warps.
+  // K tiles.  In turns an even number: within a unit a slot then belongs to one of the two MMA warps.
   static constexpr int kKRing = kTurns ? 4 : kD <= 128 ? 3 : 2;
   static constexpr int kQBytes = kQParts * kTiles * kKBytes;    // [part][tile][slab][128 rows]
   static constexpr int kVTok = kD <= 128 ? 64 : 32;             // tokens of a V stage
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->raw_empty[i], 4);
     }
     for (int i = 0; i < kMetaRing; ++i) mbar_init(&sh->meta_full[i], 1);
-    mbar_init(&sh->q_full, 8);
+    mbar_init(&sh->q_full, C::kTurns ? 9 : 8);  // the softmax warps, and in turns MMA warp 15
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i][0], 1);
       mbar_init(&sh->s_full[i][1], 1);
@@ -411,6 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const auto buffer_of = [&](int n) { return kTiles == 2 ? static_cast<uint32_t>(mine) : (item0 + n) & 1u; };
       while (__any_sync(0xffffffffu, ok && walk.next(p, &g))) {
         const int tiles = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
+        // In turns this unit may have no key tile for warp 15, and then nobody waits for it.  Its
+        // arrival for each unit keeps Q's phases from passing it: a barrier waited for by parity
+        // must not be two phases ahead of its waiter, nor may a waiter skip one.
+        if (C::kTurns && mine == 1 && lane == 0) mbar_arrive(&sh->q_full);
         wait(&sh->q_full, seg & 1u);
         const int n0 = C::kTurns ? mine : 0;
         for (int n = n0; n < min(tiles, n0 + kAhead); n += kStep) {
