@@ -584,8 +584,8 @@ uint64_t rimuru_kv_scale_bytes(rimuru_view_t view, int kv_heads);
  *               entries past the sequence's tokens are not read
  *   kv_lens     device int32 [num_seqs]: tokens of the sequence in the cache,
  *               the new ones of this call included
- * An entry outside the view, or a length past table_stride * page_tokens, is
- * recorded in the view's device error word (RIMURU_DEV_BAD_PAGE,
+ * An entry outside the view, or a length past table_stride * page_tokens or
+ * 2^30, is recorded in the view's device error word (RIMURU_DEV_BAD_PAGE,
  * RIMURU_DEV_BAD_SHAPE); its tokens are then neither read nor written.
  * The first call on a view allocates its error word: make it outside a stream
  * capture.  Later calls only launch kernels and can be captured.
@@ -620,7 +620,8 @@ int rimuru_kv_append(rimuru_view_t view, const rimuru_heads* k, const rimuru_hea
  *             plus its maximum (natural logarithm of sum_j exp(scale q.k_j))
  *   cu_q      device int32 [num_seqs + 1] row offsets, or NULL for one query
  *             row per sequence (num_q == num_seqs)
- *   max_q     an upper bound of n_b
+ *   max_q     an upper bound of n_b (num_q bounds it too)
+ *   window    any int >= 0; one that is as long as the sequences hides nothing
  *   workspace device, 1024-byte aligned, at least
  *             rimuru_kv_attention_workspace_bytes(...) bytes; calls that may run
  *             at the same time need one each

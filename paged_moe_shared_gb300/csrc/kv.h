@@ -55,7 +55,15 @@ struct KvSeqs {
   const int32_t* table;
   int64_t table_stride;
   int num_seqs;
-  int rows;  // rows of all sequences
+  int rows;     // rows of all sequences
+  int max_len;  // longest sequence that the table and kMostTokens admit
 };
+
+// Tokens of the longest sequence: positions, windows and their sums then stay inside an int.
+constexpr int64_t kMostTokens = 1 << 30;
+inline int max_len(const View& v, int64_t table_stride) {
+  return table_stride >= kMostTokens / v.page_tokens ? static_cast<int>(kMostTokens)
+                                                    : static_cast<int>(table_stride * v.page_tokens);
+}
 
 }  // namespace rimuru

@@ -12,7 +12,7 @@ struct AttnSplit {
   int unit_rows, units_per_pair;
   uint64_t cut_bytes, part_bytes;
 };
-AttnSplit split_of(const View& v, int q_heads, int num_seqs, int max_q) {
+AttnSplit split_of(const View& v, int q_heads, int max_q) {
   const int group = q_heads / v.kv_heads;
   AttnSplit w{};
   const int64_t rows = static_cast<int64_t>(max_q) * group;
@@ -24,7 +24,7 @@ AttnSplit split_of(const View& v, int q_heads, int num_seqs, int max_q) {
   w.decode = rows <= kDecodeMaxRows;
   w.unit_rows = rows <= 8 ? 8 : rows <= kDecodeMaxRows ? 16 : rows <= 256 ? 128 : tile_rows(v.head_dim);
   const int unit_q = std::max(1, w.unit_rows / group);
-  w.units_per_pair = std::max(1, (max_q + unit_q - 1) / unit_q);
+  w.units_per_pair = std::max(1, max_q / unit_q + (max_q % unit_q != 0));
   w.cut_bytes = (kMaxRuns * sizeof(int4) + 1023) / 1024 * 1024;
   w.part_bytes = 2ull * (w.decode ? kMaxRuns : kMaxTileRuns) * w.unit_rows * (v.head_dim + 1) * sizeof(float);  // and statistics
   return w;
@@ -38,7 +38,7 @@ extern "C" uint64_t rimuru_kv_attention_workspace_bytes(rimuru_view_t view, int 
                                                         int num_seqs, int num_q, int max_q) {
   if (!view || !view->v.has_kv || q_heads <= 0 || num_seqs < 0 || num_q < 0 || max_q < 0) return 0;
   if (q_heads % view->v.kv_heads != 0) return 0;
-  const rimuru::AttnSplit w = rimuru::split_of(view->v, q_heads, num_seqs, max_q);
+  const rimuru::AttnSplit w = rimuru::split_of(view->v, q_heads, std::min(max_q, num_q));
   return w.cut_bytes + w.part_bytes;
 }
 
@@ -56,6 +56,7 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
     return fail(RIMURU_ERR_ARG, "negative count or window");
   if (!std::isfinite(scale)) return fail(RIMURU_ERR_ARG, "scale must be finite");
   if (num_seqs == 0 || num_q == 0) return RIMURU_OK;
+  max_q = std::min(max_q, num_q);  // no sequence has more rows than all have together
   int st = check_heads(q, "queries");
   if (st == RIMURU_OK) st = check_heads(out, "output");
   if (st != RIMURU_OK) return st;
@@ -75,11 +76,11 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   const uint64_t need = rimuru_kv_attention_workspace_bytes(view, q->heads, num_seqs, num_q, max_q);
   if (workspace_bytes < need)
     return fail(RIMURU_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
-  const AttnSplit w = split_of(v, q->heads, num_seqs, max_q);
+  const AttnSplit w = split_of(v, q->heads, max_q);
   const int cost = w.decode ? kDecodeUnitCost : kTileUnitCost;
   const double places = (static_cast<double>(table_stride) * v.page_tokens / kTileTokens + 1 + cost) *
                         num_seqs * v.kv_heads * w.units_per_pair;
-  if (places > 2e9) return fail(RIMURU_ERR_UNSUPPORTED, "too many keys and queries for one call");
+  if (places > 2e9 || max_q > kMostTokens) return fail(RIMURU_ERR_UNSUPPORTED, "too many keys and queries for one call");
   st = kv_ready(&v);
   if (st != RIMURU_OK) return st;
   AttnArgs a{};
@@ -93,8 +94,8 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.q_heads = q->heads;
   a.group = q->heads / v.kv_heads;
   a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-  a.window = window;
-  a.s = {cu_q, kv_lens, page_table, table_stride, num_seqs, num_q};
+  a.s = {cu_q, kv_lens, page_table, table_stride, num_seqs, num_q, max_len(v, table_stride)};
+  a.window = window < a.s.max_len ? window : 0;  // as long as every sequence: none
   a.g = kv_geom(v);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   a.max_q = max_q;

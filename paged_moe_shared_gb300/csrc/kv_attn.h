@@ -52,13 +52,13 @@ struct SeqShape {
   int row0, n, len;
   bool ok;
 };
-__device__ __forceinline__ SeqShape seq_shape(const AttnArgs& p, int b) {
+__host__ __device__ __forceinline__ SeqShape seq_shape(const AttnArgs& p, int b) {
   SeqShape s;
   s.row0 = p.s.cu ? p.s.cu[b] : b;
   s.n = p.s.cu ? p.s.cu[b + 1] - s.row0 : 1;
   s.len = p.s.lens[b];
   s.ok = s.n >= 0 && s.n <= p.max_q && s.row0 >= 0 && s.row0 <= p.s.rows - s.n && s.len >= 0 &&
-         s.len <= p.s.table_stride * p.g.page_tokens;
+         s.len <= p.s.max_len;
   if (!s.ok || s.n == 0) s.n = 0, s.len = 0;
   return s;
 }
@@ -66,7 +66,7 @@ __device__ __forceinline__ SeqShape seq_shape(const AttnArgs& p, int b) {
 struct TileSpan {
   int first, last;
 };
-__device__ __forceinline__ TileSpan tile_span(const AttnArgs& p, const SeqShape& s, int i0, int i1) {
+__host__ __device__ __forceinline__ TileSpan tile_span(const AttnArgs& p, const SeqShape& s, int i0, int i1) {
   const int p0 = s.len - s.n + i0, p1 = s.len - s.n + i1;  // positions p0 .. p1 - 1
   TileSpan t;
   t.last = p1 > 0 ? (p1 + kTileTokens - 1) / kTileTokens : 0;
@@ -74,16 +74,16 @@ __device__ __forceinline__ TileSpan tile_span(const AttnArgs& p, const SeqShape&
   return t;
 }
 // A unit holds the query rows [w unit_q, (w + 1) unit_q) of its sequence.
-__device__ __forceinline__ int units_of(const AttnArgs& p, const SeqShape& s) {
+__host__ __device__ __forceinline__ int units_of(const AttnArgs& p, const SeqShape& s) {
   return p.units_per_pair == 1 ? (s.n > 0) : (s.n + p.unit_q - 1) / p.unit_q;
 }
-__device__ __forceinline__ TileSpan unit_span(const AttnArgs& p, const SeqShape& s, int w) {
+__host__ __device__ __forceinline__ TileSpan unit_span(const AttnArgs& p, const SeqShape& s, int w) {
   return tile_span(p, s, w * p.unit_q, min(s.n, (w + 1) * p.unit_q));
 }
 // Sum of floor((a i + b) / 128) over 0 <= i < n; a > 0, b >= 0.  Whole parts of
 // a / m and b / m are taken out, and what is left counts lattice points under a
 // line, which are counted along the other axis with smaller numbers.
-__device__ __forceinline__ int floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+__host__ __device__ __forceinline__ int floor_sum(uint32_t n, uint32_t a, uint32_t b) {
   uint32_t sum = 0, m = kTileTokens;  // a count of tiles: fits an int (checked on the host)
   while (n > 0) {
     const uint32_t qa = a / m, qb = b / m;
@@ -101,20 +101,23 @@ __device__ __forceinline__ int floor_sum(uint32_t n, uint32_t a, uint32_t b) {
   return static_cast<int>(sum);
 }
 // Tiles of the first w units of one head of a sequence (all of them full units).
-__device__ __forceinline__ int tiles_before(const AttnArgs& p, const SeqShape& s, int w) {
+__host__ __device__ __forceinline__ int tiles_before(const AttnArgs& p, const SeqShape& s, int w) {
   const int q = p.unit_q, base = s.len - s.n;  // unit v: positions base + v q .. base + (v + 1) q - 1
   const int v0 = base + q > 0 ? 0 : -base / q;   // units before end at or below position 0
   int n = 0;
   if (w > v0) n = floor_sum(w - v0, q, base + (v0 + 1) * q + kTileTokens - 1);
   if (p.window > 0) {
-    const int out = p.window - 1 - base;  // first position minus `out` leaves the window's reach
-    const int v1 = out <= 0 ? 0 : (out + q - 1) / q;
-    if (w > v1) n -= floor_sum(w - v1, q, base + v1 * q - p.window + 1);
+    // first position minus `out` leaves the window's reach.  Unsigned: with a large window, or rows
+    // before position 0, it passes 2^31.
+    const uint32_t out = p.window - 1 > base ? static_cast<uint32_t>(p.window - 1) - static_cast<uint32_t>(base) : 0u;
+    const uint32_t v1 = out / q + (out % q != 0);
+    if (static_cast<uint32_t>(w) > v1)
+      n -= floor_sum(w - v1, q, static_cast<uint32_t>(base) + v1 * q - static_cast<uint32_t>(p.window) + 1u);
   }
   return n;
 }
 // Tiles of one head of a sequence, over all its units.
-__device__ __forceinline__ int pair_tiles(const AttnArgs& p, const SeqShape& s) {
+__host__ __device__ __forceinline__ int pair_tiles(const AttnArgs& p, const SeqShape& s) {
   const int u = units_of(p, s);
   if (u == 0) return 0;
   const TileSpan t = unit_span(p, s, u - 1);

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   const int r0 = p.s.cu[b], n = p.s.cu[b + 1] - r0;
   const int len = p.s.lens[b], start = len - n;
   if (n <= 0) return;
-  if (r0 < 0 || r0 + n > p.s.rows || start < 0 || len > p.s.table_stride * P) {
+  if (r0 < 0 || r0 + n > p.s.rows || start < 0 || len > p.s.max_len) {
     if (threadIdx.x == 0) dev::set_error(p.g.err, RIMURU_DEV_BAD_SHAPE);
     return;
   }
@@ -438,7 +438,7 @@ int rimuru_kv_append(rimuru_view_t view, const rimuru_heads* k, const rimuru_hea
   a.ts[1] = v_in->token_stride;
   a.hs[0] = k->head_stride;
   a.hs[1] = v_in->head_stride;
-  a.s = {cu_new, kv_lens, page_table, table_stride, num_seqs, num_tokens};
+  a.s = {cu_new, kv_lens, page_table, table_stride, num_seqs, num_tokens, max_len(v, table_stride)};
   a.g = kv_geom(v);
   const int64_t units = num_tokens / v.page_tokens + 2ll * num_seqs;
   if (units > std::numeric_limits<int32_t>::max()) return fail(RIMURU_ERR_ARG, "too many sequences");

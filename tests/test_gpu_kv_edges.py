@@ -35,3 +35,49 @@ def test_units_of_one_key_tile_among_longer_ones(order, D, dtype):
         assert torch.equal(first, again) and torch.equal(lse, lse2)
     assert R.rimuru_get_device_error(c.view) == R.DEV_OK
     c.close()
+
+
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("q_len", [1, 5, 40, 300])
+@pytest.mark.parametrize("spare", [2, 4000])
+def test_a_window_beyond_every_sequence_is_none(q_len, spare):
+    """Fresh prompts, a prefix, more rows than keys; windows up to the largest int."""
+    lens = [q_len, q_len + 700, max(0, q_len - 3), 0]
+    cu = [i * q_len for i in range(5)]
+    c = Cache(2, 128, 16, sum(-(-n // 16) for n in lens))
+    table = c.tables(lens, seed=1, spare=spare)
+    c.fill(table, lens, seed=2)
+    q = qkv(cu[-1], (16,), 128, "bf16", 3)[0]
+    none, lse = check_attention(c, q, cu, lens, table, "bf16")
+    most = 16 * table.shape[1]
+    for window in (q_len + 700, most - 1, most, most + 1, 1 << 30, INT_MAX - 1, INT_MAX):
+        out, st = run_attention(c, q, cu, lens, table, window=window)
+        assert torch.equal(out, none) and torch.equal(st, lse), window
+    c.close()
+
+
+@pytest.mark.parametrize("q_len", [1, 3, 40])
+def test_any_upper_bound_of_the_rows_serves(q_len):
+    lens = [q_len + 100, 500]
+    cu = [0, q_len, 2 * q_len]
+    c = Cache(2, 128, 16, sum(-(-n // 16) for n in lens))
+    table = c.tables(lens, seed=1)
+    c.fill(table, lens, seed=2)
+    q = qkv(cu[-1], (8,), 128, "bf16", 3)[0]
+    for max_q in (q_len, 2 * q_len + 1, 1 << 20, INT_MAX):
+        check_attention(c, q, cu, lens, table, "bf16", max_q=max_q)
+    c.close()
+
+
+def test_lengths_past_the_limit_are_reported():
+    c = Cache(1, 64, 16, 8)
+    table = c.tables([100], seed=1)
+    c.fill(table, [100], seed=2)
+    q = qkv(2, (4,), 64, "bf16", 3)[0]
+    good, _ = run_attention(c, q[:1], None, [100], table)
+    for n in (INT_MAX, INT_MAX - 127, -3):
+        out, _ = run_attention(c, q, None, [n, 100], table.expand(2, -1).contiguous(), expect=R.DEV_BAD_SHAPE)
+        assert (out[0] == 0).all() and torch.isfinite(out[1]).all()
+    c.close()
