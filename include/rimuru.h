@@ -596,7 +596,8 @@ uint64_t rimuru_kv_scale_bytes(rimuru_view_t view, int kv_heads);
  *           sequences one after another
  *   cu_new  device int32 [num_seqs + 1]: sequence b's new tokens are rows
  *           cu_new[b] .. cu_new[b + 1] - 1; they get positions
- *           kv_lens[b] - (number of new tokens) onwards
+ *           kv_lens[b] - (number of new tokens) onwards.  Offsets do not
+ *           decrease and need not begin at 0 (part of a larger batch)
  * A page's scale is the smallest power of two that brings its largest
  * magnitude to at most 448.  When a page already holds earlier tokens its
  * scale never shrinks; if it has to grow, their codes are rounded again at the

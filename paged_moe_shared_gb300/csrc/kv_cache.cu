@@ -149,7 +149,8 @@ __device__ __forceinline__ float scale_for(float amax) {
 
 // One CTA per unit, a page that one sequence's new tokens touch.  Sequence b has
 // at most n_b / P + 2 units, at unit numbers cu[b] / P + 2 b onwards, so a unit
-// finds its sequence by bisection and the grid needs no lengths on the host.
+// finds its sequence by bisection and the grid needs no lengths on the host.  The
+// units below cu[0] / P have nothing to do.
 //
 // Bound: HBM (two bytes read and one written per element).  `wps` warps share a
 // (K or V, head) slice of the page, a lane has eight elements of a token at a
@@ -198,8 +199,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     if (threadIdx.x == 0) dev::set_error(p.g.err, RIMURU_DEV_BAD_SHAPE);
     return;
   }
-  const int c = start / P + (u - (r0 / P + 2 * b));  // page index within the sequence
-  if (c * P >= len) return;
+  const int d = u - (r0 / P + 2 * b);  // of the sequence's units; below 0 where its rows are not the array's first
+  const int c = start / P + d;         // page index within the sequence
+  if (d < 0 || c * P >= len) return;
   const int page = p.s.table[b * p.s.table_stride + c];
   if (page < 0 || page >= p.g.num_pages) {
     if (threadIdx.x == 0) dev::set_error(p.g.err, RIMURU_DEV_BAD_PAGE);

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from kv_reference import Cache
+import kv_reference as ref
+from kv_reference import DEV, Cache
 from paged_moe_shared_gb300 import rimuru as R
 from test_gpu_kv import check_attention, qkv, run_attention
 
@@ -80,4 +81,48 @@ def test_lengths_past_the_limit_are_reported():
     for n in (INT_MAX, INT_MAX - 127, -3):
         out, _ = run_attention(c, q, None, [n, 100], table.expand(2, -1).contiguous(), expect=R.DEV_BAD_SHAPE)
         assert (out[0] == 0).all() and torch.isfinite(out[1]).all()
+    c.close()
+
+
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("first", [1, 3, 5])
+def test_append_of_the_last_sequences_of_a_batch(first, P):
+    """Offsets that do not begin at 0: the sequences before are neither read nor written."""
+    before, new = [0, 2 * P, 5, 0, P - 1, 1, 3], [3 * P, 40, 2 * P + 1, 3, P + 2, 1, 0]
+    lens = [a + b for a, b in zip(before, new)]
+    cu = [0] + np.cumsum(new).tolist()
+    c = Cache(2, 128, P, 40)
+    table = c.tables(lens, seed=1)
+    for b in range(len(lens)):
+        c.fill(table[b:b + 1], before[b:b + 1], seed=b)
+    values, scales = c.values().numpy(), c.scales.cpu().double().numpy()
+    _, k, v = qkv(cu[-1], (3, 2, 2), 128, "bf16", 4)
+    want = table.clone()
+    table[:first] = c.pages + 5  # what lies in front of the table names no page
+    cu_t = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    lens_t = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    n = len(lens) - first
+    R.rimuru_kv_append(c.view, R.heads_of(k), R.heads_of(v), cu_t[first:].data_ptr(), lens_t[first:].data_ptr(), n,
+                       cu[-1], table[first:].data_ptr(), table.stride(0), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert R.rimuru_get_device_error(c.view, clear=True) == R.DEV_OK
+    ref.append(values, scales, want.cpu().numpy()[first:], cu[first:], lens[first:], k, v, P)
+    np.testing.assert_array_equal(c.scales.cpu().double().numpy(), scales)
+    np.testing.assert_array_equal(c.values().numpy(), values)
+    # attention takes the same offsets
+    q = qkv(cu[-1], (8,), 128, "bf16", 3)[0]
+    out = torch.full((cu[-1], 8, 128), 7.0, dtype=q.dtype, device=DEV)
+    ws = torch.empty(R.rimuru_kv_attention_workspace_bytes(c.view, 8, n, cu[-1], max(new)) + 1024,
+                     dtype=torch.uint8, device=DEV)
+    R.rimuru_kv_attention(c.view, R.heads_of(q), R.heads_of(out), 0, cu_t[first:].data_ptr(),
+                          lens_t[first:].data_ptr(), n, cu[-1], max(new), table[first:].data_ptr(), table.stride(0),
+                          128 ** -0.5, 0, (ws.data_ptr() + 1023) // 1024 * 1024, ws.numel() - 1024,
+                          torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert R.rimuru_get_device_error(c.view, clear=True) == R.DEV_OK
+    assert (out[:cu[first]] == 7.0).all()
+    alone = [x - cu[first] for x in cu[first:]]
+    want, _ = run_attention(c, q[cu[first]:], alone, lens[first:], table[first:])
+    d = (out[cu[first]:].double() - want.double()).abs()
+    assert (d <= 2.0 ** -7 * want.double().abs() + 2.0 ** -9 * want.abs().max()).all()
     c.close()
