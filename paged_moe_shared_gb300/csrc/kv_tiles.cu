@@ -127,6 +127,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Score per unit of S: the row's factor times the scale of K.  Both may be tiny (a row of zeros, scale 0,
+// a page of zeros: 2^-60), and a masked S, -inf, times a factor that has become 0 would be NaN: 2^-120
+// is added, which vanishes beside a factor above 2^-95, and below that no S (at most 2^26) gives a score
+// that counts.  (A maximum in its place would cost an instruction: a chunk of 2048 took 207.6 us, not 205.3.)
+__device__ __forceinline__ float score_factor(float row, float k) { return fmaf(row, k, 0x1p-120f); }
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -617,11 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ab = __float_as_uint(amax);
           const int e = max(-100, min(100, static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u)));
           const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23 | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
-          if (lane % kLanes == 0)  // never 0, so masked scores stay masked; an infinite query gives NaN
+          if (lane % kLanes == 0)  // an infinite query gives NaN
             sh->row_scale[qt][row0 + (k0 + k) * kRows] =
-                amax <= 3.4028234664e38f
-                    ? fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(p.scale_log2), 1e-30f)
-                    : __int_as_float(0x7FFFFFFF);
+                amax <= 3.4028234664e38f ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(p.scale_log2)
+                                         : __int_as_float(0x7FFFFFFF);
           // scaled values need no more bits than f16 has above 2^-10, below which no part reaches
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -706,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float4 kv = *reinterpret_cast<const float4*>(&sh->meta[m][4 * h + q]);
-              const float mul = c_row * kv.x, a = kv.y + shift;
+              const float mul = score_factor(c_row, kv.x), a = kv.y + shift;
               float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
@@ -733,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float x = __uint_as_float(v[16 * q]);
 #pragma unroll
               for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[16 * q + k]));
-              top = fmaxf(top, x * (c_row * kv.x) + kv.y);
+              top = fmaxf(top, x * score_factor(c_row, kv.x) + kv.y);
             }
             if (kHalves) {  // two threads have the row's halves and agree on its reference
               sh->other[wg][row] = top;

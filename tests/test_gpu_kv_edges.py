@@ -126,3 +126,86 @@ def test_append_of_the_last_sequences_of_a_batch(first, P):
     d = (out[cu[first]:].double() - want.double()).abs()
     assert (d <= 2.0 ** -7 * want.double().abs() + 2.0 ** -9 * want.abs().max()).all()
     c.close()
+
+
+# ------------------------------------------------------------------ nothing to multiply
+def zero_cache(D, lens, seed=1, spare=2):
+    """Pages as the append writes them for keys of zero (codes 0, scale 2^-60), and random values."""
+    c = Cache(2, D, 16, sum(-(-n // 16) for n in lens))
+    table = c.tables(lens, seed=seed, spare=spare)
+    c.fill(table, lens, seed=seed)
+    c.codes()[:, 0] = 0
+    c.scales[:, 0] = 2.0 ** -60
+    return c, table
+
+
+ROWS = [(1, 8), (5, 3), (40, 3), (40, 8), (300, 1), (70, 16)]  # query rows, query heads per key head
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("q_len,G", ROWS)
+def test_zero_queries_over_zero_keys_give_the_mean_of_the_values(q_len, G, dtype, D):
+    """Scores of exactly 0 whatever the factors: rows of zeros, one zero head among others, scale 0,
+    over keys of zero, with masked columns in every unit's last tile."""
+    lens = [q_len, q_len + 203, 1000]
+    cu = [i * q_len for i in range(4)]
+    c, table = zero_cache(D, lens)
+    q = qkv(cu[-1], (2 * G,), D, dtype, 3)[0].contiguous()
+    some, none = q.clone(), torch.zeros_like(q)
+    some[:, ::3] = 0
+    for x in (none, some, q):
+        check_attention(c, x, cu, lens, table, dtype)
+        check_attention(c, x, cu, lens, table, dtype, scale=0.0)
+    check_attention(c, none, cu, lens, table, dtype, window=50)
+    # the smallest numbers that the types have
+    tiny = torch.full_like(q, 2.0 ** -24 if dtype == "f16" else 2.0 ** -126)
+    check_attention(c, tiny, cu, lens, table, dtype)
+    # zero queries over other keys, and pages of zero keys among others
+    c.fill(table, lens, seed=5)
+    check_attention(c, none, cu, lens, table, dtype)
+    check_attention(c, some, cu, lens, table, dtype, scale=0.0)
+    c.codes()[::2, 0] = 0
+    c.scales[::2, 0] = 2.0 ** -60
+    check_attention(c, some, cu, lens, table, dtype)
+    c.close()
+
+
+@pytest.mark.parametrize("q_len", [1, 40, 300])
+def test_a_pass_over_nothing_but_zeros_is_zero(q_len):
+    """A warm-up: q = k = v = 0 through the append."""
+    lens, cu = [q_len], [0, q_len]
+    c = Cache(2, 128, 16, -(-q_len // 16))
+    table = c.tables(lens)
+    z = torch.zeros(q_len, 2, 128, dtype=torch.bfloat16, device=DEV)
+    cu_t, lens_t = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (cu, lens))
+    R.rimuru_kv_append(c.view, R.heads_of(z), R.heads_of(z), cu_t.data_ptr(), lens_t.data_ptr(), 1, q_len,
+                       table.data_ptr(), table.stride(0), torch.cuda.current_stream().cuda_stream)
+    out, lse = run_attention(c, torch.zeros(q_len, 16, 128, dtype=torch.bfloat16, device=DEV), cu, lens, table)
+    assert (out == 0).all()
+    want = torch.arange(1, q_len + 1, device=DEV).float().log()[:, None].expand(-1, 16)
+    assert (lse - want).abs().max() <= 2.0 ** -16 * max(1.0, float(want.max()))
+    c.close()
+
+
+@pytest.mark.parametrize("q_len", [1, 5, 40, 300])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(q_len):
+    lens, cu = [q_len + 77], [0, q_len]
+    c, table = zero_cache(128, lens)
+    q = qkv(q_len, (16,), 128, "bf16", 3)[0].contiguous()
+    for keys in ("zero", "some"):
+        if keys == "some":
+            c.fill(table, lens, seed=5)
+        bad = q.clone()
+        bad[0, 3, 5], bad[q_len - 1, 9, 0] = float("inf"), float("nan")
+        out, lse = run_attention(c, bad, cu, lens, table)
+        hit = torch.zeros(q_len, 16, dtype=torch.bool, device=DEV)
+        hit[0, 3] = hit[q_len - 1, 9] = True
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+        # the other rows: the tolerance of check_attention
+        want, want_lse, mag, top = ref.attention(c.values(), table.cpu().numpy(), lens, q, cu, 128 ** -0.5, 0, c.P)
+        tol = ref.HALF_ULP["bf16"] * want.abs() + (2.0 ** -10 + 2.0 ** -16 * top[..., None]) * mag + 1e-7
+        keep = ~hit.cpu()
+        assert ((out.double().cpu() - want).abs() <= tol)[keep].all()
+        assert ((lse.double().cpu() - want_lse).abs() <= 2.0 ** -17 * top + 2.0 ** -16)[keep].all()
+    c.close()
