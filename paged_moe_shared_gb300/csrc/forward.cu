@@ -128,8 +128,7 @@ int ensure_device_state(View* v) {
   cudaError_t e = cudaGetDevice(&d->device);
   const size_t n = v->page_table.size();
   if (e == cudaSuccess) e = cudaMalloc(&d->d_table, n * sizeof(int32_t));
-  if (e == cudaSuccess) e = cudaMalloc(&d->d_err, 4 * sizeof(int));
-  if (e == cudaSuccess) e = cudaMemset(d->d_err, 0, 4 * sizeof(int));
+  if (e == cudaSuccess) e = alloc_words(&d->d_err, 4);
   if (e == cudaSuccess) e = cudaMallocHost(&d->h_stage, n * sizeof(int32_t));
   if (e == cudaSuccess) e = cudaEventCreateWithFlags(&d->upload_done, cudaEventDisableTiming);
   if (e != cudaSuccess) {
@@ -394,6 +393,7 @@ int rimuru_get_device_error(rimuru_view_t view, int* code, int clear) {
   int h = 0;
   cudaError_t e = cudaMemcpy(&h, word, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && clear) e = cudaMemset(word, 0, sizeof(int));
+  if (e == cudaSuccess && clear) e = cudaStreamSynchronize(nullptr);  // later kernels may be on any stream
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, rimuru::cuda_msg("reading the device error", e));
   *code = h;
   return RIMURU_OK;

@@ -194,6 +194,9 @@ cudaError_t launch_decode_gemm2(DecodeArgs a, const LaunchOpts& o);
 // strides in bytes for dims 1..rank-1).  Returns a rimuru status.
 int make_bf16_map(CUtensorMap* m, void* base, int rank, const cuuint64_t* dims,
                   const cuuint64_t* strides, const cuuint32_t* box);
+// Allocates n device words and zeroes them before it returns, whatever the default stream is doing:
+// the caller's first kernel may run on a stream that does not wait for that one.
+cudaError_t alloc_words(int** words, int n);
 // A 3-D map of bytes (8-bit codes) with the given box and swizzle.
 int make_byte_map(CUtensorMap* m, void* base, const cuuint64_t (&dims)[3],
                   const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3],

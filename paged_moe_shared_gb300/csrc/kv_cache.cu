@@ -60,8 +60,7 @@ int kv_ready(View* v) {
   v->kv = k;
   k->device = cur;
   e = cudaDeviceGetAttribute(&k->sms, cudaDevAttrMultiProcessorCount, cur);
-  if (e == cudaSuccess) e = cudaMalloc(&k->d_err, sizeof(int));
-  if (e == cudaSuccess) e = cudaMemset(k->d_err, 0, sizeof(int));
+  if (e == cudaSuccess) e = alloc_words(&k->d_err, 1);
   if (e != cudaSuccess) {
     destroy_kv_state(v);
     return fail(RIMURU_ERR_CUDA, kv_cuda_msg("device state of the KV view", e));

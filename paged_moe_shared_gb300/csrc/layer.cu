@@ -56,6 +56,17 @@ int make_bf16_map(CUtensorMap* m, void* base, int rank, const cuuint64_t* dims,
   return RIMURU_OK;
 }
 
+cudaError_t alloc_words(int** words, int n) {
+  cudaStream_t own = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMalloc(words, n * sizeof(int));
+  if (e == cudaSuccess) e = cudaMemsetAsync(*words, 0, n * sizeof(int), own);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+  cudaStreamDestroy(own);
+  return e;
+}
+
 int make_byte_map(CUtensorMap* m, void* base, const cuuint64_t (&dims)[3],
                   const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3],
                   CUtensorMapSwizzle swizzle) {

@@ -209,3 +209,47 @@ def test_a_query_that_is_not_finite_spoils_its_own_row_only(q_len):
         assert ((out.double().cpu() - want).abs() <= tol)[keep].all()
         assert ((lse.double().cpu() - want_lse).abs() <= 2.0 ** -17 * top + 2.0 ** -16)[keep].all()
     c.close()
+
+
+# ------------------------------------------------------------------ errors and streams
+def busy_default_stream():
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)  # about 0.2 s
+
+
+def test_an_error_of_the_first_call_is_kept_on_a_side_stream():
+    """The default stream is busy, and a side stream does not wait for it."""
+    c = Cache(2, 128, 16, 8)
+    _, k, v = qkv(5, (1, 2, 2), 128, "bf16", 4)
+    bad = torch.full((1, 2), c.pages + 3, dtype=torch.int32, device=DEV)
+    cu_t, lens_t = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 5], [5]))
+    side = torch.cuda.Stream()
+    other = Cache(2, 128, 16, 8)  # loads the kernel, which would wait for the device
+    R.rimuru_kv_append(other.view, R.heads_of(k), R.heads_of(v), cu_t.data_ptr(), lens_t.data_ptr(), 1, 5,
+                       other.tables([5]).data_ptr(), 3, side.cuda_stream)
+    busy_default_stream()
+    R.rimuru_kv_append(c.view, R.heads_of(k), R.heads_of(v), cu_t.data_ptr(), lens_t.data_ptr(), 1, 5,
+                       bad.data_ptr(), 2, side.cuda_stream)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert R.rimuru_get_device_error(c.view, clear=True) == R.DEV_BAD_PAGE
+    assert R.rimuru_get_device_error(c.view) == R.DEV_OK
+    other.close()
+    c.close()
+
+
+def test_an_error_of_the_first_forward_is_kept_on_a_side_stream():
+    import workloads as W
+    from gpu_harness import Runner
+    r, other = Runner(W.tiny(3)), Runner(W.tiny(3))
+    r.logits[2, 5] = float("nan")
+    side = torch.cuda.Stream()
+    other.forward(side)  # loads the kernels
+    busy_default_stream()
+    r.forward(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert R.rimuru_get_device_error(r.ev, clear=True) == R.DEV_NONFINITE
+    assert R.rimuru_get_device_error(r.ev) == R.DEV_OK
+    other.close()
+    r.close()
