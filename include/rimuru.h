@@ -654,7 +654,8 @@ int rimuru_page_refs(rimuru_view_t view, int64_t page_id, int* refs);
 
 /* Fork a sequence of kv_len cached tokens into n children (beams, parallel
  * samples).  pages: host int32, the parent's ceil(kv_len / page_tokens) pages.
- * children: host int32 [n][child_stride] receives each child's pages: full
+ * children: host int32 [n][child_stride] receives each child's pages (of a
+ * row as many entries as the parent has; the others are left alone): full
  * pages are shared with the parent (one more reference each), a partly filled
  * last page is copied on `stream` into a new page near the parent's.
  * RIMURU_ERR_OOM (nothing changed) when the pool has no page left. */

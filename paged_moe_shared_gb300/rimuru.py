@@ -518,13 +518,14 @@ def rimuru_page_refs(view, page_id: int) -> int:
 
 
 def rimuru_kv_fork(view, pages, kv_len: int, n: int, stream: int = 0):
-    """Fork a sequence into n children; returns the children's page lists."""
+    """Fork a sequence into n children; returns the children's page lists, the pages of ``kv_len``
+    tokens (``pages`` may hold more)."""
     m = len(pages)
     src = (ctypes.c_int32 * max(m, 1))(*[int(p) for p in pages])
-    got = (ctypes.c_int32 * max(m * n, 1))()
+    got = (ctypes.c_int32 * max(m * n, 1))(*[-1] * (m * n))  # entries past the tokens stay as they are
     _check(lib.rimuru_kv_fork(view, ctypes.cast(src, ctypes.c_void_p), kv_len, n,
                               ctypes.cast(got, ctypes.c_void_p), m, stream))
-    return [list(got[i * m:(i + 1) * m]) for i in range(n)]
+    return [[p for p in got[i * m:(i + 1) * m] if p >= 0] for i in range(n)]
 
 
 def rimuru_kv_compact(view, tables, max_moves: int, stream: int = 0):
