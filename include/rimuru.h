@@ -648,7 +648,8 @@ int rimuru_kv_copy_pages(rimuru_view_t view, const int32_t* src, const int32_t* 
 
 /* References to a page the view owns.  rimuru_page_share adds one;
  * rimuru_page_free drops one and returns the page to the allocator when it was
- * the last.  A new page has one. */
+ * the last, and so does an expert cache with its slots' pages.  A new page has
+ * one. */
 int rimuru_page_share(rimuru_view_t view, int64_t page_id);
 int rimuru_page_refs(rimuru_view_t view, int64_t page_id, int* refs);
 

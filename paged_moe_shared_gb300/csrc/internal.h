@@ -92,6 +92,9 @@ struct View {
   KvState* kv = nullptr;  // owned; freed by destroy_kv_state
 };
 
+// Drops one reference to a page of the view and releases it with the last (caller holds the pool's mu).
+int drop_page(View* v, int lvl, int64_t id);
+
 void destroy_device_state(View* v);
 void destroy_kv_state(View* v);
 // Device word of the view's KV state, or nullptr when no call has needed it yet.

@@ -231,7 +231,7 @@ struct Offload {
           key_slot[slot_key[s]] = -1;
           st_.evictions += 1;
         }
-        for (int p = 0; p < 3; ++p) pool.release(lvl, v->id, slot_page[static_cast<size_t>(s) * 3 + p]);
+        for (int p = 0; p < 3; ++p) drop_page(v, lvl, slot_page[static_cast<size_t>(s) * 3 + p]);
       }
       keep.resize(new_cap);
     } else {
@@ -299,7 +299,7 @@ void release_offload(Offload* o) {
     std::lock_guard<std::mutex> g(o->v->pool->mu);
     const int lvl = o->v->pool->level_of(o->v->page_bytes);
     for (int64_t pg : o->slot_page)
-      if (pg >= 0) o->v->pool->release(lvl, o->v->id, pg);
+      if (pg >= 0) drop_page(o->v, lvl, pg);
   }
 }
 

@@ -208,6 +208,15 @@ int Pool::release(int lvl, int32_t owner_id, int64_t id) {
   return RIMURU_OK;
 }
 
+int drop_page(View* v, int lvl, int64_t id) {
+  auto shared = v->extra_refs.find(id);
+  if (shared != v->extra_refs.end()) {  // others still use the page
+    if (--shared->second == 0) v->extra_refs.erase(shared);
+    return RIMURU_OK;
+  }
+  return v->pool->release(lvl, v->id, id);
+}
+
 }  // namespace rimuru
 
 using rimuru::fail;
@@ -423,12 +432,7 @@ int rimuru_page_free(rimuru_view_t view, int64_t page_id) {
   if (page_id >= 0 && page_id < static_cast<int64_t>(v.map_count.size()) && v.map_count[page_id] > 0)
     return fail(RIMURU_ERR_STATE, "page is still mapped as an expert projection");
   std::lock_guard<std::mutex> g(v.pool->mu);
-  auto shared = v.extra_refs.find(page_id);
-  if (shared != v.extra_refs.end()) {  // other sequences still use the page
-    if (--shared->second == 0) v.extra_refs.erase(shared);
-    return RIMURU_OK;
-  }
-  return v.pool->release(v.pool->level_of(v.page_bytes), v.id, page_id);
+  return rimuru::drop_page(&v, v.pool->level_of(v.page_bytes), page_id);
 }
 
 int rimuru_page_share(rimuru_view_t view, int64_t page_id) {

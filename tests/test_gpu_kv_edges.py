@@ -253,3 +253,37 @@ def test_an_error_of_the_first_forward_is_kept_on_a_side_stream():
     assert R.rimuru_get_device_error(r.ev) == R.DEV_OK
     other.close()
     r.close()
+
+
+# ------------------------------------------------------------------ references
+@pytest.mark.parametrize("how", ["destroy", "shrink"])
+def test_the_expert_cache_drops_its_reference_only(how):
+    """A slot's page that somebody else has a reference to outlives the slot, and comes back once."""
+    import workloads as W
+    from paged_moe_shared_gb300.device_pool import DevicePool
+    shape = W.MoEShape(H=256, I=128, E=8, k=2)
+    pb, n = shape.H * shape.I * 2, 12
+    st = W.offload_stack(shape, 2, 4, steps=1, seed=7)
+    host = torch.from_numpy(st.host_pages).pin_memory()
+    pool = DevicePool(n * pb, pb, DEV)
+    ev = pool.view(pb)
+    R.rimuru_view_set_moe_shape(ev, 2, shape.E, shape.H, shape.I, shape.k, shape.renorm)
+    off = R.rimuru_offload_create(ev, host.data_ptr(), 4, 0)
+    pages = list(range(n))
+    assert [R.rimuru_page_refs(ev, p) for p in pages] == [1] * n
+    for p in pages:
+        R.rimuru_page_share(ev, p)
+    if how == "shrink":
+        R.rimuru_offload_resize(off, 1)
+        assert sum(R.rimuru_page_refs(ev, p) for p in pages) == 3 * 2 + 9
+        R.rimuru_offload_resize(off, 1)
+    R.rimuru_offload_destroy(off)
+    assert [R.rimuru_page_refs(ev, p) for p in pages] == [1] * n
+    for p in pages:
+        R.rimuru_page_free(ev, p)
+    assert [R.rimuru_page_refs(ev, p) for p in pages] == [0] * n
+    p = R.rimuru_page_alloc(ev)
+    assert R.rimuru_page_refs(ev, p) == 1
+    R.rimuru_page_free(ev, p)
+    assert R.rimuru_pool_level_stats(pool.handle, 0)["pages_free"] == n
+    pool.close()
