@@ -509,19 +509,34 @@ int rimuru_kv_fork(rimuru_view_t view, const int32_t* pages, int kv_len, int n, 
       if (L.state[pages[i]] != Level::OWNED || L.owner[pages[i]] != v.id)
         return fail(RIMURU_ERR_STATE, "page is not owned by this view");
     }
-    if (full < used) {
-      for (int c = 0; c < n; ++c) {
+    // whatever may fail comes first: entries for the references, and the children's own pages
+    const auto undo = [&] {
+      for (const auto& p : copies) v.pool->release(lvl, v.id, p.second);
+      for (int64_t i = 0; i < full; ++i) {
+        auto r = v.extra_refs.find(pages[i]);
+        if (r != v.extra_refs.end() && r->second == 0) v.extra_refs.erase(r);
+      }
+    };
+    try {
+      for (int64_t i = 0; i < full; ++i) v.extra_refs.try_emplace(pages[i], 0);
+      for (int c = 0; full < used && c < n; ++c) {
+        copies.emplace_back(pages[used - 1], -1);
         int64_t id = -1;
         int st = v.pool->alloc_near(lvl, v.id, pages[used - 1], &id);
         if (st != RIMURU_OK) {
+          copies.pop_back();
           const std::string msg = rimuru_last_error();
-          for (const auto& p : copies) v.pool->release(lvl, v.id, p.second);
+          undo();
           return fail(st, msg);
         }
-        copies.emplace_back(pages[used - 1], static_cast<int32_t>(id));
+        copies.back().second = static_cast<int32_t>(id);
       }
+    } catch (const std::bad_alloc&) {
+      if (!copies.empty() && copies.back().second < 0) copies.pop_back();
+      undo();
+      return fail(RIMURU_ERR_OOM, "host allocation failed");
     }
-    for (int64_t i = 0; i < full; ++i) v.extra_refs[pages[i]] += n;
+    for (int64_t i = 0; i < full; ++i) v.extra_refs.find(pages[i])->second += n;
   }
   for (int c = 0; c < n; ++c) {
     int32_t* row = children + c * child_stride;
@@ -545,7 +560,7 @@ int rimuru_kv_compact(rimuru_view_t view, int32_t* tables, int64_t n_entries, in
   int st = kv_ready(&v);
   if (st != RIMURU_OK) return st;
   std::vector<std::pair<int32_t, int32_t>> moves;
-  {
+  try {
     std::lock_guard<std::mutex> g(v.pool->mu);
     const int lvl = v.pool->level_of(v.page_bytes);
     if (lvl == 0) return RIMURU_OK;  // huge pages have no parent to merge into
@@ -558,6 +573,7 @@ int rimuru_kv_compact(rimuru_view_t view, int32_t* tables, int64_t n_entries, in
         return fail(RIMURU_ERR_STATE, "page is not owned by this view");
       to.emplace(tables[i], -1);
     }
+    moves.reserve(std::min<size_t>(max_moves, to.size()));
     // every parent that holds a page of the tables: how many are in use, how many
     // free, and whether all in use can move
     struct Parent {
@@ -615,11 +631,10 @@ int rimuru_kv_compact(rimuru_view_t view, int32_t* tables, int64_t n_entries, in
     }
     for (const auto& m : moves) {
       to[m.first] = m.second;
-      auto r = v.extra_refs.find(m.first);
-      if (r != v.extra_refs.end()) {
-        const int32_t extra = r->second;
-        v.extra_refs.erase(r);
-        v.extra_refs[m.second] = extra;
+      auto extra = v.extra_refs.extract(m.first);
+      if (!extra.empty()) {
+        extra.key() = m.second;
+        v.extra_refs.insert(std::move(extra));
       }
       v.pool->release(lvl, v.id, m.first);
     }
@@ -628,6 +643,8 @@ int rimuru_kv_compact(rimuru_view_t view, int32_t* tables, int64_t n_entries, in
       const int32_t t = to[tables[i]];
       if (t >= 0) tables[i] = t;
     }
+  } catch (const std::bad_alloc&) {
+    return fail(RIMURU_ERR_OOM, "host allocation failed");
   }
   *moved = static_cast<int>(moves.size());
   return copy_pairs(&v, moves, static_cast<cudaStream_t>(stream));

@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cstring>
 #include <limits>
+#include <new>
 #include <numeric>
 
 #include "internal.h"
@@ -444,7 +445,11 @@ int rimuru_page_share(rimuru_view_t view, int64_t page_id) {
   if (page_id < 0 || page_id >= L.n_pages) return fail(RIMURU_ERR_RANGE, "page id out of range");
   if (L.state[page_id] != rimuru::Level::OWNED || L.owner[page_id] != v.id)
     return fail(RIMURU_ERR_STATE, "page is not owned by this view");
-  v.extra_refs[page_id] += 1;
+  try {
+    v.extra_refs[page_id] += 1;
+  } catch (const std::bad_alloc&) {
+    return fail(RIMURU_ERR_OOM, "host allocation failed");
+  }
   return RIMURU_OK;
 }
 

@@ -25,3 +25,38 @@ def test_children_have_the_pages_of_the_tokens_and_no_others(kv):
     assert R.rimuru_kv_fork(kv, pages, 0, 2) == [[], []]
     assert R.rimuru_kv_fork(kv, [], 0, 2) == [[], []]
     assert R.rimuru_kv_fork(kv, pages, 16, 0) == []
+
+
+NO_MEMORY = """
+import ctypes, resource, sys
+sys.path.insert(0, {root!r})
+from paged_moe_shared_gb300 import rimuru as R
+page, n = 2 * 64 * 16, 1 << 18
+pool = R.rimuru_pool_create(64 << 20, n * page, 16 * page)
+kv = R.rimuru_view_create(pool, page)
+R.rimuru_view_set_kv_shape(kv, 1, 64, 16, 4096, R.rimuru_kv_scale_bytes(kv, 1))
+pages = (ctypes.c_int32 * n)(*[R.rimuru_page_alloc(kv) for _ in range(n)])
+kids = (ctypes.c_int32 * n)()
+at = lambda a: ctypes.cast(a, ctypes.c_void_p)
+R.lib.rimuru_kv_fork(kv, at(pages), 16, 1, at(kids), n, None)   # every path has run once
+R.rimuru_page_free(kv, pages[0])
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (4 << 20), resource.RLIM_INFINITY))
+st = R.lib.rimuru_kv_fork(kv, at(pages), 16 * n, 1, at(kids), n, None)
+resource.setrlimit(resource.RLIMIT_AS, (resource.RLIM_INFINITY, resource.RLIM_INFINITY))
+assert st == R.ERR_OOM, st
+assert all(R.rimuru_page_refs(kv, p) == 1 for p in pages)
+assert R.lib.rimuru_kv_fork(kv, at(pages), 16 * n, 1, at(kids), n, None) == 0
+assert list(kids) == list(pages) and all(R.rimuru_page_refs(kv, p) == 2 for p in pages)
+print("fine")
+"""
+
+
+def test_fork_without_host_memory_is_an_error_and_changes_nothing():
+    """A host allocation that fails inside the call ends in a status, not in the process's end."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", NO_MEMORY.format(root=root)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "fine" in r.stdout, (r.returncode, r.stderr[-500:])
