@@ -615,6 +615,11 @@ int rimuru_kv_append(rimuru_view_t view, const rimuru_heads* k, const rimuru_hea
  * j > p - window when window > 0:
  *   out = sum_j softmax_j(scale * q . k_j) v_j.
  * A row that sees no key gives 0 (and lse -inf).  Statistics and sums are fp32.
+ * Fewer bits are held in two places.  A query element below 2^-13 of its row's
+ * largest magnitude is off by up to 2^-21 (f16: 2^-24) of that magnitude.
+ * Softmax weights are rounded to f16 where they meet the values, and what a
+ * weight has below 2^-27 of the row's reference is left out there (the sum that
+ * they are divided by has it).
  *   q, out    device [num_q][q heads][head_dim], RIMURU_BF16 or RIMURU_F16 and
  *             the same type; q->heads a multiple of kv_heads
  *   lse       device float [num_q][q heads], or NULL: log of the softmax's sum

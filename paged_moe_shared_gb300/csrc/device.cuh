@@ -505,6 +505,8 @@ __host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool a_mn_majo
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+constexpr uint32_t kIdescAE5m2 = 1u << 7;  // in the same: e5m2 A (format 1)
+
 // Instruction descriptor for kind::f16 with f16 A/B (format 0) and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major,
                                                      bool b_mn_major) {

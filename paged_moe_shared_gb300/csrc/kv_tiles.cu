@@ -4,10 +4,13 @@
 // Bound: the tensor cores (4 head_dim operations per query head and key).  Rows
 // are (query, head of the group) pairs, so the heads that share a key/value
 // head share its tiles.  Per 128-token tile of keys and 128 rows:
-//   S = Q K^T   e4m3 x e4m3: K is multiplied as it lies in the page, Q as a sum
-//               of e4m3 parts (two hold a bf16 query exactly, three an f16 one)
-//               into one fp32 accumulator: two parts cost what one bf16 product
-//               costs, without widening K;
+//   S = Q K^T   8 bits x 8 bits: K is multiplied as it lies in the page, Q as a sum
+//               of 8-bit parts into one fp32 accumulator: two parts cost what one
+//               bf16 product costs, without widening K.  The first part is e4m3 (4
+//               significant bits), the rest e5m2 (3 bits, and small enough numbers):
+//               with the row scaled to (224, 448], two parts hold a bf16 element
+//               exactly down to 2^-6 of that scale and within 2^-14 below, three an
+//               f16 element exactly down to 2^-6 and within 2^-17 below;
 //   O += P V    f16 x f16: P rounded to f16 stays in TMEM as the A operand; the
 //               codes of V are widened (exactly) by four warps on their way to
 //               shared memory.
@@ -370,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // warp-uniform (issued from a one-lane branch, an MMA took 160 cycles to issue
       // instead of the 64 it runs).
       constexpr uint32_t id_s = idesc_f8_f32(128, C::kScoreN, false, false, false);
+      constexpr uint32_t id_rest = id_s | kIdescAE5m2;  // the parts of Q after the first
       constexpr uint32_t id_o = idesc_f16_f32(128, kD, false, /*b_mn=*/true);
       constexpr uint32_t kHiQK = desc_hi(kAtom, kSwizzle), kHiV = desc_hi(1024, 2);
       const uint32_t tb = __shfl_sync(0xffffffffu, tmem, 0);
@@ -400,10 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int sl = 0; sl < kSlabs; ++sl) {
 #pragma unroll
-              for (int k = 0; k < kRowBytes / 32; ++k)
-                umma_f8_lo<kHiQK, kHiQK, id_s>(
-                    d, a0 + (part * kTiles * C::kKBytes + sl * C::kSlabBytes) / 16 + 2 * k,
-                    b0 + sl * (C::kSlabBytes / 16) + 2 * k, (part | sl | k) != 0 ? 1u : 0u);
+              for (int k = 0; k < kRowBytes / 32; ++k) {
+                const uint32_t a = a0 + (part * kTiles * C::kKBytes + sl * C::kSlabBytes) / 16 + 2 * k;
+                const uint32_t b = b0 + sl * (C::kSlabBytes / 16) + 2 * k;
+                if (part == 0) umma_f8_lo<kHiQK, kHiQK, id_s>(d, a, b, (sl | k) != 0 ? 1u : 0u);
+                else umma_f8_lo<kHiQK, kHiQK, id_rest>(d, a, b, 1u);
+              }
             }
           }
           umma_commit(&sh->s_full[buffer][h]);
@@ -626,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh->row_scale[qt][row0 + (k0 + k) * kRows] =
                 amax <= 3.4028234664e38f ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(p.scale_log2)
                                          : __int_as_float(0x7FFFFFFF);
-          // scaled values need no more bits than f16 has above 2^-10, below which no part reaches
+          // f16 holds the scaled values exactly above 2^-14, and within 2^-25 below
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 f = unpack2<T>(raw[k][i]);
@@ -640,10 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t c[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              c[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x[k][i]), __NV_SATFINITE, __NV_E4M3);
+              const __nv_fp8_interpretation_t type = part == 0 ? __NV_E4M3 : __NV_E5M2;
+              c[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x[k][i]), __NV_SATFINITE, type);
               if (part + 1 < kQParts)
                 x[k][i] = __hsub2(x[k][i], __half2(__nv_cvt_fp8x2_to_halfraw2(
-                                               static_cast<__nv_fp8x2_storage_t>(c[i]), __NV_E4M3)));
+                                               static_cast<__nv_fp8x2_storage_t>(c[i]), type)));
             }
             *reinterpret_cast<uint2*>(dst[k] + part * kPart) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
           }

@@ -287,3 +287,37 @@ def test_the_expert_cache_drops_its_reference_only(how):
     R.rimuru_page_free(ev, p)
     assert R.rimuru_pool_level_stats(pool.handle, 0)["pages_free"] == n
     pool.close()
+
+
+# ------------------------------------------------------------------ queries of a wide range
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_len,G", [(1, 8), (2, 8), (40, 3), (300, 1)])
+@pytest.mark.parametrize("loud", [30.0, 1000.0, 4096.0, 20000.0])
+def test_small_elements_beside_a_loud_one_keep_their_weight(loud, q_len, G, D, dtype):
+    """One query channel far above the others, over keys that have nothing there.  With a window of
+    one key the log-sum is the score itself.
+
+    A row is scaled so that its largest magnitude lies in (224, 448], and its last part has steps of
+    2^-13 (bf16) or 2^-16 (f16) there, or three significant bits: an element is off by at most 2^-14 or
+    2^-17, that is 2^-14 / 224 of the largest one; times sum |k| and the scale.  The products' sum is
+    off by 2^-17 of sum |q k| and the logarithm by 2^-16, as in check_attention."""
+    lens = [q_len + 100, q_len]
+    cu = [0, q_len, 2 * q_len]
+    c = Cache(2, D, 16, sum(-(-n // 16) for n in lens))
+    table = c.tables(lens, seed=1)
+    c.fill(table, lens, seed=2)
+    c.codes()[:, 0, :, :, D // 2 + 3] = 0
+    q = qkv(cu[-1], (2 * G,), D, dtype, 3)[0].contiguous()
+    q[:, :, D // 2 + 3] = loud
+    scale = D ** -0.5
+    _, lse = run_attention(c, q, cu, lens, table, window=1)
+    values = c.values()
+    _, want, _, top = ref.attention(values, table.cpu().numpy(), lens, q, cu, scale, 1, 16)
+    keys = values[table.cpu().clamp(min=0).long(), 0].nan_to_num()  # [sequences, pages, heads, 16, D]
+    total = keys.abs().sum(-1).amax()
+    step = 2.0 ** -14 if dtype == "bf16" else 2.0 ** -17
+    tol = 2.0 ** -16 + 2.0 ** -17 * top + scale * loud * step / 224 * float(total)
+    err = (lse.double().cpu() - want).abs()
+    assert (err <= tol).all(), (float(err.max()), float((err / tol).max()))
+    c.close()
