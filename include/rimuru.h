@@ -535,8 +535,9 @@ typedef struct rimuru_heads {
  *   RIMURU_ROPE_BY_PARTS  with r_i = orig_len * f_i / (2 pi) turns over the
  *                         trained length and g_i = clamp((r_i - low) / (high -
  *                         low), 0, 1): (1 - g_i) * f_i / factor + g_i * f_i.
- * Angles are kept as 64-bit fractions of a turn, so they are exact to fp32
- * rounding at every int32 position; a negative position turns back (the
+ * Angles are kept as 64-bit fractions of a turn and rounded to fp32 once, also
+ * small ones; the frequencies are doubles, so at positions near 2^31 the fastest
+ * pair may be off by 2^-24 of a turn.  A negative position turns back (the
  * inverse of the rotation when mscale is 1).
  * Requirements: base > 1, factor > 0, mscale finite; rot_dim positive, at
  * most 256, a multiple of 16 (half) or 8 (interleaved); BY_PARTS: orig_len >

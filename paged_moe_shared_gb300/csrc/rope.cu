@@ -3,9 +3,11 @@
 //
 // An fp32 product p * f_i is off by up to half an ulp of the product: 0.004 rad
 // at 65536 positions for the fastest pair.  Here f_i is a 64-bit fraction of a
-// turn, so p times it modulo 2^64 is the angle modulo one turn, exact to
-// p * 2^-64 turns, and only the final conversion to fp32 rounds.  A negative
-// position is the same product modulo 2^64.
+// turn, so p times it modulo 2^64 is the angle modulo one turn.  It is rounded to
+// fp32 once, as a signed number, so that a small angle keeps its bits too.  f_i
+// itself is a double, good to a few times 2^-53 of itself: at 2^31 positions the
+// fastest pair is off by about 2^-24 of a turn.  A negative position is the same
+// product modulo 2^64.
 //
 // Bound: HBM (each element is read and written once).  A CTA takes one token, or
 // four of a long array: it computes their cosines and sines once into shared
@@ -80,9 +82,9 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
   for (int k = threadIdx.x; k < n_tokens * p.pairs; k += blockDim.x) {
     const int t = k / p.pairs, i = k - t * p.pairs;
     const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + t]));
-    const int32_t turn = static_cast<int32_t>((pos * p.turn[i]) >> 32);  // 2^-32 turns
+    const int64_t turn = static_cast<int64_t>(pos * p.turn[i]);  // 2^-64 turns
     float s, c;
-    sincospif(static_cast<float>(turn) * 0x1p-31f, &s, &c);
+    sincospif(__ll2float_rn(turn) * 0x1p-63f, &s, &c);
     cosines[k] = make_float2(c * p.mscale, s * p.mscale);
   }
   __syncthreads();

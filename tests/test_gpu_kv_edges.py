@@ -321,3 +321,33 @@ def test_small_elements_beside_a_loud_one_keep_their_weight(loud, q_len, G, D, d
     err = (lse.double().cpu() - want).abs()
     assert (err <= tol).all(), (float(err.max()), float((err / tol).max()))
     c.close()
+
+
+# ------------------------------------------------------------------ rotary positions
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("scaling,factor", [(R.ROPE_PLAIN, 1.0), (R.ROPE_LINEAR, 64.0)])
+def test_slow_pairs_turn_by_small_angles(scaling, factor, interleaved):
+    """A pair (0, v) becomes (-v sin, v cos): the sine of a small angle to a few ulp of itself.  The
+    angle is rounded to fp32 once, the sine is good to an ulp or two and the product is rounded: at
+    most 4 ulp, 2^-22."""
+    rot, T = 256, 12
+    h = R.rimuru_rope_create(rot, R.ROPE_INTERLEAVED if interleaved else R.ROPE_HALF, 500000.0, scaling, factor)
+    f = ref.inv_freq(rot, 500000.0, scaling, factor)
+    pos = torch.tensor([1, 2, 3, 4, 5, 6, 7, 8, 9, 10, -1, -7], dtype=torch.int32, device=DEV)
+    x = torch.zeros(T, 3, rot, device=DEV)
+    v = torch.rand(T, 3, rot // 2, generator=torch.Generator().manual_seed(1)).to(DEV) + 0.5
+    (x[..., 1::2] if interleaved else x[..., rot // 2:]).copy_(v)
+    out = torch.empty_like(x)
+    R.rimuru_rope_apply(h, pos.data_ptr(), T, rot, [R.heads_of(x)], [R.heads_of(out)],
+                        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    ang = pos.cpu().double()[:, None] * torch.from_numpy(f)
+    y = out.cpu().double()
+    u, w = (y[..., 0::2], y[..., 1::2]) if interleaved else (y[..., :rot // 2], y[..., rot // 2:])
+    want_u, want_w = -v.cpu().double() * torch.sin(ang)[:, None], v.cpu().double() * torch.cos(ang)[:, None]
+    small = (ang.abs() < 1.5)[:, None].expand_as(u)  # past that a small cosine makes an ulp of the angle larger
+    assert ((u - want_u).abs() <= 2.0 ** -22 * want_u.abs())[small].all(), \
+        float(((u - want_u).abs() / want_u.abs())[small].max())
+    small = (ang.abs() < 0.7)[:, None].expand_as(u)
+    assert ((w - want_w).abs() <= 2.0 ** -22 * want_w.abs())[small].all()
+    R.rimuru_rope_destroy(h)
