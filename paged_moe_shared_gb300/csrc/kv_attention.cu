@@ -54,7 +54,8 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   if (!v.has_kv) return fail(RIMURU_ERR_STATE, "view has no KV shape");
   if (num_seqs < 0 || num_q < 0 || max_q < 0 || window < 0)
     return fail(RIMURU_ERR_ARG, "negative count or window");
-  if (!std::isfinite(scale)) return fail(RIMURU_ERR_ARG, "scale must be finite");
+  const float scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return fail(RIMURU_ERR_ARG, "scale must be finite in fp32");
   if (num_seqs == 0 || num_q == 0) return RIMURU_OK;
   max_q = std::min(max_q, num_q);  // no sequence has more rows than all have together
   int st = check_heads(q, "queries");
@@ -93,7 +94,7 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.o_hs = out->head_stride;
   a.q_heads = q->heads;
   a.group = q->heads / v.kv_heads;
-  a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.s = {cu_q, kv_lens, page_table, table_stride, num_seqs, num_q, max_len(v, table_stride)};
   a.window = window < a.s.max_len ? window : 0;  // as long as every sequence: none
   a.g = kv_geom(v);

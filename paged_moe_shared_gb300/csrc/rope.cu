@@ -171,8 +171,8 @@ extern "C" int rimuru_rope_create(int rot_dim, int layout, double base, int scal
     return fail(RIMURU_ERR_ARG, "unknown rotary layout");
   if (scaling < RIMURU_ROPE_PLAIN || scaling > RIMURU_ROPE_BY_PARTS)
     return fail(RIMURU_ERR_ARG, "unknown rotary scaling");
-  if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(mscale))
-    return fail(RIMURU_ERR_ARG, "base must be finite and above 1, mscale finite");
+  if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(static_cast<float>(mscale)))
+    return fail(RIMURU_ERR_ARG, "base must be finite and above 1, mscale finite in fp32");
   const bool scaled = scaling != RIMURU_ROPE_PLAIN;
   if (scaled && !(factor > 0.0 && std::isfinite(factor)))
     return fail(RIMURU_ERR_ARG, "factor must be finite and positive");
@@ -181,7 +181,7 @@ extern "C" int rimuru_rope_create(int rot_dim, int layout, double base, int scal
     return fail(RIMURU_ERR_UNSUPPORTED,
                 "rot_dim must be in (0, 256] and a multiple of 16 (half) or 8 (interleaved)");
   if (scaling == RIMURU_ROPE_BY_PARTS &&
-      !(orig_len > 0.0 && std::isfinite(orig_len) && std::isfinite(low) && std::isfinite(high) && high > low))
+      !(orig_len > 0.0 && std::isfinite(orig_len) && std::isfinite(high - low) && high > low))
     return fail(RIMURU_ERR_ARG, "by-parts scaling needs orig_len > 0 and high > low");
   if (scaling == RIMURU_ROPE_BASE) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
   if (!(base > 0.0 && std::isfinite(base))) return fail(RIMURU_ERR_ARG, "scaled base out of range");
@@ -194,6 +194,10 @@ extern "C" int rimuru_rope_create(int rot_dim, int layout, double base, int scal
     if (scaling == RIMURU_ROPE_BY_PARTS) {
       const double g = std::min(1.0, std::max(0.0, (orig_len * f / two_pi - low) / (high - low)));
       f = (1.0 - g) * f / factor + g * f;
+    }
+    if (!std::isfinite(f)) {
+      delete r;
+      return fail(RIMURU_ERR_ARG, "scaled frequencies out of range");
     }
     double turns = f / two_pi;
     turns -= std::floor(turns);  // the phase is taken modulo one turn

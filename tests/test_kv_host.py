@@ -60,3 +60,22 @@ def test_fork_without_host_memory_is_an_error_and_changes_nothing():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", NO_MEMORY.format(root=root)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "fine" in r.stdout, (r.returncode, r.stderr[-500:])
+
+
+def refused(status, fn, *args):
+    with pytest.raises(R.RimuruError) as e:
+        fn(*args)
+    assert e.value.status == status, str(e.value)
+
+
+@pytest.mark.parametrize("big", [1e39, -1e300])
+def test_factors_that_are_not_finite_in_fp32_are_refused(kv, big):
+    h = R.Heads(4096, 256, 128, 2, R.BF16)
+    refused(R.ERR_ARG, R.rimuru_kv_attention, kv, h, h, 0, 0, 16, 1, 1, 1, 16, 4, big, 0, 4096, 1 << 30)
+    refused(R.ERR_ARG, R.rimuru_rope_create, 128, R.ROPE_HALF, 1e4, R.ROPE_PLAIN, 1.0, 0.0, 0.0, 0.0, big)
+
+
+def test_frequencies_that_are_not_finite_are_refused():
+    refused(R.ERR_ARG, R.rimuru_rope_create, 128, R.ROPE_HALF, 1e4, R.ROPE_LINEAR, 5e-324)
+    refused(R.ERR_ARG, R.rimuru_rope_create, 128, R.ROPE_HALF, 1e4, R.ROPE_BY_PARTS, 5e-324, 8192.0, 1.0, 4.0)
+    refused(R.ERR_ARG, R.rimuru_rope_create, 128, R.ROPE_HALF, 1e4, R.ROPE_BY_PARTS, 4.0, 1e308, -1e308, 1e308)
