@@ -351,3 +351,22 @@ def test_slow_pairs_turn_by_small_angles(scaling, factor, interleaved):
     small = (ang.abs() < 0.7)[:, None].expand_as(u)
     assert ((w - want_w).abs() <= 2.0 ** -22 * want_w.abs())[small].all()
     R.rimuru_rope_destroy(h)
+
+
+# ------------------------------------------------------------------ head layouts
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("Hk,G,D", [(1, 128, 128), (2, 100, 64), (1, 33, 256), (1, 17, 128), (40, 1, 64), (1024, 1, 64)])
+def test_wide_groups_and_many_heads(Hk, G, D, dtype):
+    """Units of one query row, of a few, and of rows that do not fill them."""
+    lens, new = [140, 3, 515], [1, 3, 9]
+    cu = [0] + np.cumsum(new).tolist()
+    c = Cache(Hk, D, 16, sum(-(-n // 16) for n in lens))
+    q = qkv(cu[-1], (Hk * G,), D, dtype, 3)[0]
+    for spare in (2, 3000):
+        table = c.tables(lens, seed=1, spare=spare)
+        if spare == 2:
+            c.fill(table, lens, seed=2)
+        check_attention(c, q, cu, lens, table, dtype)
+        check_attention(c, q, cu, lens, table, dtype, window=20)
+        check_attention(c, q[:3], None, lens, table, dtype)
+    c.close()
