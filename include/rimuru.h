@@ -535,6 +535,8 @@ typedef struct rimuru_heads {
  *   RIMURU_ROPE_BY_PARTS  with r_i = orig_len * f_i / (2 pi) turns over the
  *                         trained length and g_i = clamp((r_i - low) / (high -
  *                         low), 0, 1): (1 - g_i) * f_i / factor + g_i * f_i.
+ *                         (The ramp is linear in turns; one that is linear in
+ *                         the pair's index is another rotation.)
  * Angles are kept as 64-bit fractions of a turn and rounded to fp32 once, also
  * small ones; the frequencies are doubles, so at positions near 2^31 the fastest
  * pair may be off by 2^-24 of a turn.  A negative position turns back (the
@@ -582,7 +584,10 @@ uint64_t rimuru_kv_scale_bytes(rimuru_view_t view, int kv_heads);
  * Where a sequence's tokens lie, for the entry points below:
  *   page_table  device int32 [num_seqs][table_stride]: token t of sequence b is
  *               slot t % page_tokens of page page_table[b][t / page_tokens];
- *               entries past the sequence's tokens are not read
+ *               entries past the sequence's tokens are not read.  The stride
+ *               bounds the lengths before a launch: attention leaves short
+ *               sequences whole where table_stride * page_tokens says that they
+ *               are short, and a wide table of short ones costs a few us more
  *   kv_lens     device int32 [num_seqs]: tokens of the sequence in the cache,
  *               the new ones of this call included
  * An entry outside the view, or a length past table_stride * page_tokens or
@@ -604,7 +609,8 @@ uint64_t rimuru_kv_scale_bytes(rimuru_view_t view, int kv_heads);
  * scale never shrinks; if it has to grow, their codes are rounded again at the
  * new scale.  Codes are rounded to nearest even.  A NaN is stored as 0 and an
  * infinity as the largest code, and either sets RIMURU_DEV_NONFINITE, so a
- * cache written here holds finite values only.  A page of the table is written
+ * cache written here holds finite values only (a magnitude past 448 * 2^60, the
+ * largest scale, becomes the largest code).  A page of the table is written
  * through at most one sequence: shared pages must be full (rimuru_kv_fork). */
 int rimuru_kv_append(rimuru_view_t view, const rimuru_heads* k, const rimuru_heads* v,
                      const int32_t* cu_new, const int32_t* kv_lens, int num_seqs, int num_tokens,
@@ -661,8 +667,8 @@ int rimuru_page_refs(rimuru_view_t view, int64_t page_id, int* refs);
 
 /* Fork a sequence of kv_len cached tokens into n children (beams, parallel
  * samples).  pages: host int32, the parent's ceil(kv_len / page_tokens) pages.
- * children: host int32 [n][child_stride] receives each child's pages (of a
- * row as many entries as the parent has; the others are left alone): full
+ * children: host int32 [n][child_stride] receives each child's pages, the first
+ * ceil(kv_len / page_tokens) entries of a row (the others are left alone): full
  * pages are shared with the parent (one more reference each), a partly filled
  * last page is copied on `stream` into a new page near the parent's.
  * RIMURU_ERR_OOM (nothing changed) when the pool has no page left. */
@@ -675,7 +681,8 @@ int rimuru_kv_fork(rimuru_view_t view, const int32_t* pages, int kv_len, int n, 
  * skipped.  Parents whose pages in use all belong to this view and appear in
  * `tables` are emptied, the sparsest first, into free pages of fuller parents,
  * as long as a whole parent can be emptied and at most max_moves pages move.
- * Entries of `tables` are rewritten, references move along, the copies are
+ * Entries of `tables` are rewritten, references move along (whoever holds one
+ * learns the page's new id from `tables` only), the copies are
  * queued on `stream`, and the emptied pages are free at once: work that
  * touches them must come later on the same stream.  *moved receives the
  * number of pages moved. */

@@ -155,9 +155,12 @@ __device__ __forceinline__ float scale_for(float amax) {
 // (K or V, head) slice of the page, a lane has eight elements of a token at a
 // time, and everything a warp has to read is in flight at once: up to kHold
 // vectors a lane, which stay in registers between the maximum and the encoding
-// (a slice with more per warp is read again).  Ragged prompts of 33 MB: 12.2 us,
-// 2.7 TB/s; 64 sequences of one token: 4.0 us.  What is left is the chain length ->
-// page table -> values -> scale -> codes, of which each step waits for the last.
+// (a slice with more per warp is read again).  Ragged prompts of 33 MB: 12.0 us,
+// 2.8 TB/s (f16 11.7; f32, 56 MB, 22.6: held as four words a vector they spill 244 bytes a
+// thread); 64 sequences of one token: 4.0 us.  What is left is the chain length ->
+// page table -> values -> scale -> codes, of which each step waits for the last, and
+// that two CTAs of 512 threads fit an SM: of the prompts' 354 pages 304 are written at
+// the same time and the others after them.
 constexpr int kHold = 8;
 constexpr int kAppendWarps = 16;
 

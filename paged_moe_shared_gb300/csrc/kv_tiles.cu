@@ -28,12 +28,15 @@
 // them in turns, each with a reference, a sum and an O of its own that are added up
 // at the end; with head_dim 256 both work on each item and halve its columns.
 //
-// 2048 rows x 32 heads after 6144 keys, 32/4 heads of 128: 206 us with the join, 1.17
-// PFLOP/s (0.60 of cuBLAS bf16); about 3,500 cycles a 256 x 128 tile whose MMAs take
+// 2048 rows x 32 heads after 6144 keys, 32/4 heads of 128: 207 us with the join, 1.16
+// PFLOP/s (0.59 of cuBLAS bf16; f16 208 us); about 3,500 cycles a 256 x 128 tile whose MMAs take
 // 3,072 (of them 1,024 for the second halves of the scores, see the MMA warps).  16
-// sequences of 24 to 40 rows over 900 to 6600 keys: 29.4 us.  What bounds both is the
+// sequences of 24 to 40 rows over 900 to 6600 keys: 29.4 us (f16 30.9).  What bounds both is the
 // chain scores -> softmax -> weights -> MMA, 150 to 300 cycles a hand-over, with the
 // two chains in flight that the tensor memory holds.
+//
+// The block is launched with 128 registers a thread, and every instance spills 168 to 280
+// bytes a thread; what that costs was not measured.
 //
 // Warps 0-3 and 4-7: softmax.  8-11: widening V.  12: K copies, and the pages and
 // scales of each key tile for the others.  13 and 15: MMAs.  14: V copies.
