@@ -100,6 +100,7 @@ extern "C" int rimuru_kv_attention(rimuru_view_t view, const rimuru_heads* q, co
   a.g = kv_geom(v);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   a.max_q = max_q;
+  a.sms = v.kv->sms;
   a.unit_rows = w.unit_rows;
   a.units_per_pair = w.units_per_pair;
   a.unit_cost = cost;

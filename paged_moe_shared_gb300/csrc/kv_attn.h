@@ -32,6 +32,7 @@ struct AttnArgs {
   KvSeqs s;
   KvGeom g;
   // work split
+  int sms;             // of the device
   int runs;            // CTAs that share the tiles
   int unit_rows;       // query rows (query x group) of a unit
   int unit_q;          // whole query rows of a unit: unit_rows / group

@@ -880,7 +880,7 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t s) {
   // four rows a warp), four rows beyond.
   const bool split = units * 4 <= a.runs;
   const int64_t bound = std::max<int64_t>(1, std::min<int64_t>(a.unit_rows, static_cast<int64_t>(a.max_q) * a.group));
-  const int per = split ? 0 : a.runs * bound <= 152 * 64 ? 1 : 4;
+  const int per = split ? 0 : a.runs * bound <= a.sms * 64 ? 1 : 4;
   const int rows = split ? 1 : per * kJoinWarps;  // of a CTA
   const int64_t zero = std::min<int64_t>(a.runs, (pairs + 32 * kJoinWarps - 1) / (32 * kJoinWarps));
   cudaLaunchConfig_t cfg{};
