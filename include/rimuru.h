@@ -561,6 +561,27 @@ int rimuru_rope_destroy(rimuru_rope_t rope);
 int rimuru_rope_apply(rimuru_rope_t rope, const int32_t* positions, int num_tokens, int head_dim,
                       const rimuru_heads* in, const rimuru_heads* out, int n_arrays, void* stream);
 
+/* The norm of one array's heads: x -> x / sqrt(mean(x^2) + eps) * (weight + offset), the mean
+ * over a head's head_dim elements in fp32.  weight: device [head_dim] of `dtype`, 16-byte
+ * aligned, or NULL for no weight (a factor of 1; offset is then not read).  offset is 1 for
+ * models that store their weights less one.  eps in [1e-20, 1]. */
+typedef struct rimuru_head_norm {
+  const void* weight;
+  double eps;
+  double offset;
+  int32_t dtype; /* of the weight: RIMURU_BF16, RIMURU_F16 or RIMURU_F32 */
+} rimuru_head_norm;
+
+/* rimuru_rope_apply with the norm of each head before its rotation, in the same pass: array i's
+ * heads are normalised by norms[i] (a host array), then turned.  The norm covers the whole head,
+ * the rotation its first rot_dim elements; nothing is rounded in between.  A squared sum past
+ * fp32 is taken on scaled elements; a NaN or an infinity in a head makes the head NaN or 0 as the
+ * formula does.  rope may be NULL: norms alone, positions is then not read.
+ * Other arguments, in-place use and errors as rimuru_rope_apply. */
+int rimuru_norm_rope_apply(rimuru_rope_t rope, const int32_t* positions, int num_tokens, int head_dim,
+                           const rimuru_heads* in, const rimuru_heads* out, const rimuru_head_norm* norms,
+                           int n_arrays, void* stream);
+
 /*
  * Declare that `view` holds key/value pages of attention layers: each page
  * holds `page_tokens` tokens of one layer as 8-bit codes (float8 e4m3), laid
@@ -688,6 +709,105 @@ int rimuru_kv_fork(rimuru_view_t view, const int32_t* pages, int kv_len, int n, 
  * number of pages moved. */
 int rimuru_kv_compact(rimuru_view_t view, int32_t* tables, int64_t n_entries, int max_moves,
                       int* moved, void* stream);
+
+/* -------------------------------------------- linear attention, beams */
+
+/*
+ * Declare that `view` holds recurrent states of linear-attention layers (Rimuru page, Table 1:
+ * state pages of [heads, key_dim, value_dim] share the pool and set its huge pages): page p holds
+ * the state of one sequence in one layer, fp32 [heads][key_dim][value_dim] from the page base.
+ * Requirements: key_dim and value_dim 64 or 128; heads in [1, 1024]; heads * key_dim * value_dim
+ * * 4 <= page_bytes (RIMURU_ERR_UNSUPPORTED).  RIMURU_ERR_STATE if the view already has a shape of
+ * any kind.  Pages are placed, shared and freed with the calls above; the library never clears one. */
+int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int value_dim);
+
+/* Linear attention with a decay for each head and token.  Head h of a sequence holds a state S
+ * [key_dim][value_dim]; its new tokens t, in order, do
+ *   S <- exp(g_t) S + k_t v_t^T,      out_t = scale * S^T q_t
+ * with query/key head h / (heads / q->heads).  A few new tokens go one by one with the state in
+ * registers, more of them in chunks on the tensor cores; no choice needs the host.
+ *   q, k      device [num_tokens][key heads][key_dim], RIMURU_BF16 or RIMURU_F16; the view's heads
+ *             are a multiple of their heads
+ *   v, out    device [num_tokens][heads][value_dim], the same type
+ *   log_decay device float: g of token t and head h is log_decay[t * decay_token_stride + h *
+ *             decay_head_stride].  A stride of 0 makes it one for all tokens (heads).  Any value
+ *             <= 0, also -inf (the state starts anew with that token).  A g above 0 grows the state.
+ *   cu_new    device int32 [num_seqs + 1]: sequence b's new tokens are rows cu_new[b] ..
+ *             cu_new[b + 1] - 1; or NULL for one token a sequence (num_tokens == num_seqs).
+ *             Offsets do not decrease and need not begin at 0; other rows are neither read nor
+ *             written.  A sequence without new tokens passes its state on.
+ *   max_new   an upper bound of a sequence's new tokens (num_tokens bounds it too)
+ *   state_in  device int32 [num_seqs]: the page of S before the tokens, -1 for zeros
+ *   state_out device int32 [num_seqs]: the page that receives S after them; may be state_in[b].
+ *             Beams that go on from one parent read its page and write pages of their own, so that
+ *             a reordering copies no state.  Otherwise no page may be written that another sequence
+ *             of the call reads or writes.
+ *   workspace device, 1024-byte aligned, at least rimuru_linear_attention_workspace_bytes(...)
+ *             bytes; calls that may run at the same time need one each
+ * States and sums are fp32; in the chunked form the factors of a product are held as sums of bf16
+ * parts (2^-16 of a factor, 2^-24 where they add to the state).  A page outside the view or
+ * bad offsets (a sequence longer than max_new, a row past num_tokens) are recorded in the view's
+ * device error word (RIMURU_DEV_BAD_PAGE, RIMURU_DEV_BAD_SHAPE) and the sequence is left alone.
+ * The first call on a view allocates its error word: make it outside a stream capture.  Later
+ * calls only launch kernels and can be captured. */
+uint64_t rimuru_linear_attention_workspace_bytes(rimuru_view_t view, int num_seqs, int num_tokens,
+                                                 int max_new);
+int rimuru_linear_attention(rimuru_view_t view, const rimuru_heads* q, const rimuru_heads* k,
+                            const rimuru_heads* v, const rimuru_heads* out, const float* log_decay,
+                            int64_t decay_token_stride, int64_t decay_head_stride, const int32_t* cu_new,
+                            int num_seqs, int num_tokens, int max_new, const int32_t* state_in,
+                            const int32_t* state_out, double scale, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+
+/* Device rows [rows][cols]: element (r, c) is at data + r * row_stride + c, in elements.  Rows may
+ * begin anywhere their type may. */
+typedef struct rimuru_rows {
+  const void* data;
+  int64_t row_stride;
+  int32_t cols;
+  int32_t dtype; /* RIMURU_BF16, RIMURU_F16 or RIMURU_F32 */
+} rimuru_rows;
+
+/* A step of beam search: for each of num_groups batch entries the n_select best of
+ *   scores[b] + log_softmax(logits[b])[v]
+ * over its beams b and the vocabulary v, best first, the lowest (b, v) first on ties.
+ *   logits     rows num_groups * beams, cols the vocabulary.  -inf masks a token; a NaN counts as
+ *              -inf, +inf as the largest finite value
+ *   scores     device float [num_groups][beams]; -inf takes a beam out
+ *   done       device uint8 [num_groups][beams] or NULL: a finished beam (non-zero) offers one
+ *              candidate, pad_token at scores[b]; its logits are not read
+ *   out_scores, out_rows, out_tokens  device [num_groups][n_select]: the sum, the beam's row
+ *              (entry * beams + b) and the token; where fewer candidates are above -inf the rest
+ *              are -inf, -1, -1
+ *   workspace  device, 1024-byte aligned, rimuru_beam_select_workspace_bytes(...) bytes; calls that
+ *              may run at the same time need one each
+ * Sums of exponentials are fp32, the worths that are compared are doubles of them and of the
+ * logits.  At most 128 beams and n_select 128; beams * (vocabulary + 128) at most 2^30.  A worth below
+ * fp32's range counts as -inf.  The
+ * descriptor's cols is the vocabulary.  Errors: RIMURU_ERR_ARG, _ALIGN, _WORKSPACE, _UNSUPPORTED,
+ * _CUDA. */
+uint64_t rimuru_beam_select_workspace_bytes(int num_groups, int beams, int vocab, int n_select);
+int rimuru_beam_select(const rimuru_rows* logits, const float* scores, const uint8_t* done, int num_groups,
+                       int beams, int pad_token, int n_select, float* out_scores, int32_t* out_rows,
+                       int32_t* out_tokens, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Reorder cached sequences after a beam step, on the device and for all layers in one launch: child
+ * i goes on from sequence parents[i].
+ *   parents    device int32 [num_seqs], values in [0, num_parents); -1: no child (its length is 0)
+ *   kv_lens    device int32 [num_parents]: cached tokens of the parents
+ *   table_in   device int32 [num_layers][num_parents][table_stride], see page_table above
+ *   table_out  device int32 [num_layers][num_seqs][table_stride]: receives the parent's row; where
+ *              the last page is partly filled, the child's fresh page in its place, into which codes
+ *              and scales are copied.  Entries past the tokens are left as they are
+ *   fresh      device int32 [num_layers][num_seqs]: pages that hold nothing any table_in names
+ *   lens_out   device int32 [num_seqs]: the children's lengths
+ * Outputs may not overlap inputs.  References to pages are the host's: pages that several children
+ * name, or none, are shared and freed there (rimuru_page_share, rimuru_page_free).  A bad parent,
+ * length or page is recorded in the view's error word (RIMURU_DEV_BAD_SHAPE with length 0,
+ * RIMURU_DEV_BAD_PAGE with -1 in the page's place).  First call and capture as above. */
+int rimuru_kv_reorder(rimuru_view_t view, const int32_t* parents, int num_seqs, const int32_t* kv_lens,
+                      int num_parents, const int32_t* table_in, int32_t* table_out, int num_layers,
+                      int64_t table_stride, const int32_t* fresh, int32_t* lens_out, void* stream);
 
 /* ------------------------------------------------------------- profiling */
 

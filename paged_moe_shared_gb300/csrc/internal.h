@@ -62,7 +62,7 @@ struct Pool {
 
 // Device-side resources of one expert view (created on first forward).
 struct DeviceState;
-// Device-side resources of one KV view (created by the first call that launches).
+// Device-side resources of one KV or state view (created by the first call that launches).
 struct KvState;
 
 struct View {
@@ -89,7 +89,11 @@ struct View {
   int kv_heads = 0, head_dim = 0, page_tokens = 0;
   float* scales = nullptr;  // caller's device array [n_pages][2][kv_heads]
   std::unordered_map<int64_t, int32_t> extra_refs;  // pages with more than one reference
-  KvState* kv = nullptr;  // owned; freed by destroy_kv_state
+  KvState* kv = nullptr;  // owned; freed by destroy_kv_state; a state view's error word too
+
+  // recurrent-state shape (set once)
+  bool has_state = false;
+  int state_heads = 0, key_dim = 0, value_dim = 0;
 };
 
 // Drops one reference to a page of the view and releases it with the last (caller holds the pool's mu).

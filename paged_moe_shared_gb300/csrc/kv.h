@@ -22,6 +22,9 @@ struct KvState {
   CUtensorMap tm_values{};  // plain boxes, at most a stage of the tile kernel's V
 };
 
+// Checks that the current device holds the view's pool, and creates the view's
+// device number and error word on first use (*made is then set).
+int paged_state_ready(View* v, bool* made);
 // Checks that the view has a KV shape and the current device holds its pool,
 // and creates the view's device state on first use.
 int kv_ready(View* v);

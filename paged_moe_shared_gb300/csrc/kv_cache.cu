@@ -43,8 +43,7 @@ void destroy_kv_state(View* v) {
   v->kv = nullptr;
 }
 
-int kv_ready(View* v) {
-  if (!v->has_kv) return fail(RIMURU_ERR_STATE, "view has no KV shape");
+int paged_state_ready(View* v, bool* made) {
   int cur = 0;
   cudaError_t e = cudaGetDevice(&cur);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("cudaGetDevice", e));
@@ -63,8 +62,18 @@ int kv_ready(View* v) {
   if (e == cudaSuccess) e = alloc_words(&k->d_err, 1);
   if (e != cudaSuccess) {
     destroy_kv_state(v);
-    return fail(RIMURU_ERR_CUDA, kv_cuda_msg("device state of the KV view", e));
+    return fail(RIMURU_ERR_CUDA, kv_cuda_msg("device state of the view", e));
   }
+  *made = true;
+  return RIMURU_OK;
+}
+
+int kv_ready(View* v) {
+  if (!v->has_kv) return fail(RIMURU_ERR_STATE, "view has no KV shape");
+  bool made = false;
+  int st = paged_state_ready(v, &made);
+  if (st != RIMURU_OK || !made) return st;
+  KvState* k = v->kv;
   // the pool as pages of rows of head_dim codes; a box is one head's tokens of a
   // page, at most 128 bytes of each
   const uint64_t dim = static_cast<uint64_t>(v->head_dim);
@@ -389,6 +398,7 @@ int rimuru_view_set_kv_shape(rimuru_view_t view, int kv_heads, int head_dim, int
   rimuru::View& v = view->v;
   if (v.has_shape) return fail(RIMURU_ERR_STATE, "view already has an MoE shape");
   if (v.has_kv) return fail(RIMURU_ERR_STATE, "view already has a KV shape");
+  if (v.has_state) return fail(RIMURU_ERR_STATE, "view already has a state shape");
   if (kv_heads <= 0 || head_dim <= 0 || page_tokens <= 0)
     return fail(RIMURU_ERR_ARG, "shape values must be positive");
   if (!dev_scales) return fail(RIMURU_ERR_ARG, "null scales");

@@ -1,0 +1,54 @@
+// Internals shared by the linear-attention kernels.
+#pragma once
+
+#include "kv.h"
+
+namespace rimuru {
+
+// One call as the kernels see it.  S <- exp(g) S + k v^T, out = scale S^T q.
+struct LinearArgs {
+  const void *q, *k, *v;
+  void* out;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;  // strides in elements
+  const float* decay;
+  int64_t g_ts, g_hs;
+  float scale;
+  int heads, per_key_head;  // heads, and how many of them share a query/key head
+  int key_dim, value_dim;
+  const int32_t* cu;  // row offsets [num_seqs + 1], or null: one row per sequence
+  int num_seqs, num_tokens, max_new;
+  const int32_t *state_in, *state_out;
+  uint8_t* pool;
+  uint64_t page_bytes;
+  int num_pages;
+  int* err;
+  int sms;
+};
+
+// Rows and pages of a sequence.  `ok` is false where the tables are bad (recorded by the
+// thread that asks for it): the sequence is then left alone.
+struct LinearSeq {
+  int64_t row;
+  int n;
+  const float* in;  // state before the tokens, or null: zeros
+  float* out;
+  bool ok;
+};
+__device__ __forceinline__ LinearSeq linear_seq(const LinearArgs& a, int b, bool record) {
+  LinearSeq s;
+  const int r0 = a.cu ? a.cu[b] : b, r1 = a.cu ? a.cu[b + 1] : b + 1;
+  const int in = a.state_in[b], out = a.state_out[b];
+  s.row = r0;
+  s.n = r1 - r0;
+  const bool shape = r0 >= 0 && r1 >= r0 && r1 <= a.num_tokens && s.n <= a.max_new;
+  const bool pages = in >= -1 && in < a.num_pages && out >= 0 && out < a.num_pages;
+  s.ok = shape && pages;
+  if (record && !s.ok) dev::set_error(a.err, shape ? RIMURU_DEV_BAD_PAGE : RIMURU_DEV_BAD_SHAPE);
+  s.in = in >= 0 ? reinterpret_cast<const float*>(a.pool + static_cast<uint64_t>(in) * a.page_bytes) : nullptr;
+  s.out = reinterpret_cast<float*>(a.pool + static_cast<uint64_t>(out) * a.page_bytes);
+  return s;
+}
+
+cudaError_t launch_linear_steps(const LinearArgs& a, int dtype, cudaStream_t s);
+
+}  // namespace rimuru

@@ -492,6 +492,7 @@ int rimuru_view_set_moe_shape(rimuru_view_t view, int layers, int experts, int h
   rimuru::View& v = view->v;
   if (v.has_shape) return fail(RIMURU_ERR_STATE, "view already has an MoE shape");
   if (v.has_kv) return fail(RIMURU_ERR_STATE, "view already has a KV shape");
+  if (v.has_state) return fail(RIMURU_ERR_STATE, "view already has a state shape");
   if (layers <= 0 || experts <= 0 || hidden <= 0 || inter <= 0 || top_k <= 0)
     return fail(RIMURU_ERR_ARG, "shape values must be positive");
   if (hidden % 128 != 0 || inter % 128 != 0)

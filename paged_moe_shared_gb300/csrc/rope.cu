@@ -25,11 +25,11 @@
 
 #include "device.cuh"
 #include "kv.h"
+#include "rope.h"
 
 namespace rimuru {
 namespace {
 
-constexpr int kMaxPairs = 128;
 constexpr int kMaxArrays = 4;
 constexpr int kMaxTokens = 4;  // of a CTA
 
@@ -164,6 +164,13 @@ struct rimuru_rope_s {
 };
 
 using rimuru::fail;
+
+void rimuru::rope_turns(rimuru_rope_t rope, RopeTurns* out) {
+  for (int i = 0; i < rope->a.pairs; ++i) out->turn[i] = rope->a.turn[i];
+  out->mscale = rope->a.mscale;
+  out->pairs = rope->a.pairs;
+  out->layout = rope->a.layout;
+}
 
 extern "C" int rimuru_rope_create(int rot_dim, int layout, double base, int scaling, double factor,
                                   double orig_len, double low, double high, double mscale,

@@ -53,6 +53,9 @@ EXPORTS = [
     "rimuru_kv_scale_bytes", "rimuru_kv_append", "rimuru_kv_attention_workspace_bytes",
     "rimuru_kv_attention", "rimuru_kv_copy_pages", "rimuru_page_share", "rimuru_page_refs",
     "rimuru_kv_fork", "rimuru_kv_compact",
+    "rimuru_norm_rope_apply", "rimuru_view_set_state_shape", "rimuru_linear_attention_workspace_bytes",
+    "rimuru_linear_attention", "rimuru_beam_select_workspace_bytes", "rimuru_beam_select",
+    "rimuru_kv_reorder",
 ]
 
 BF16, F16, F32 = 0, 1, 2
@@ -89,6 +92,19 @@ class Heads(ctypes.Structure):
     head count and element type (BF16, F16, F32)."""
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class HeadNorm(ctypes.Structure):
+    """Norm of one array's heads: weight [head_dim] (0: none), eps, what is added to the weight, and
+    the weight's element type."""
+    _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_double), ("offset", ctypes.c_double),
+                ("dtype", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    """Rows [rows][cols]: base address, row stride in elements, columns and element type."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("cols", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
 
 
@@ -156,6 +172,13 @@ def _load():
         "rimuru_page_refs": ([P, i64, ctypes.POINTER(i32)], i32),
         "rimuru_kv_fork": ([P, P, i32, i32, P, i64, P], i32),
         "rimuru_kv_compact": ([P, P, i64, i32, ctypes.POINTER(i32), P], i32),
+        "rimuru_norm_rope_apply": ([P, P, i32, i32, H, H, ctypes.POINTER(HeadNorm), i32, P], i32),
+        "rimuru_view_set_state_shape": ([P, i32, i32, i32], i32),
+        "rimuru_linear_attention_workspace_bytes": ([P, i32, i32, i32], u64),
+        "rimuru_linear_attention": ([P, H, H, H, H, P, i64, i64, P, i32, i32, i32, P, P, f64, P, u64, P], i32),
+        "rimuru_beam_select_workspace_bytes": ([i32, i32, i32, i32], u64),
+        "rimuru_beam_select": ([ctypes.POINTER(Rows), P, P, i32, i32, i32, i32, P, P, P, P, u64, P], i32),
+        "rimuru_kv_reorder": ([P, P, i32, P, i32, P, P, i32, i64, P, P, P], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -435,18 +458,22 @@ def rimuru_adjust(off, kv_view, kv_blocks_wanted: int, min_capacity: int, max_ca
 _KINDS = {}  # element type of a tensor -> BF16, F16 or F32
 
 
-def heads_of(t) -> Heads:
-    """Descriptor of a tensor [tokens, heads, head_dim] whose last axis is contiguous."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
-        raise ValueError("expected [tokens, heads, head_dim] with a contiguous last axis")
+def _kind_of(t) -> int:
     kind = _KINDS.get(t.dtype)
     if kind is None:
         kind = {"torch.bfloat16": BF16, "torch.float16": F16, "torch.float32": F32}.get(str(t.dtype))
         if kind is None:
             raise ValueError(f"unsupported element type {t.dtype}")
         _KINDS[t.dtype] = kind
-    return Heads(t.data_ptr(), stride[0], stride[1], shape[1], kind)
+    return kind
+
+
+def heads_of(t) -> Heads:
+    """Descriptor of a tensor [tokens, heads, head_dim] whose last axis is contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
+        raise ValueError("expected [tokens, heads, head_dim] with a contiguous last axis")
+    return Heads(t.data_ptr(), stride[0], stride[1], shape[1], _kind_of(t))
 
 
 def rimuru_rope_create(rot_dim: int, layout: int = ROPE_HALF, base: float = 10000.0,
@@ -537,3 +564,69 @@ def rimuru_kv_compact(view, tables, max_moves: int, stream: int = 0):
     _check(lib.rimuru_kv_compact(view, ctypes.cast(arr, ctypes.c_void_p), n, max_moves,
                                  ctypes.byref(moved), stream))
     return list(arr[:n]), moved.value
+
+
+def head_norm_of(weight, eps: float = 1e-6, offset: float = 0.0) -> HeadNorm:
+    """Descriptor of a head's norm; ``weight`` is a contiguous tensor [head_dim] or None."""
+    if weight is None:
+        return HeadNorm(None, eps, offset, F32)
+    if weight.dim() != 1 or (weight.stride(0) != 1 and weight.shape[0] > 1):
+        raise ValueError("expected a contiguous weight [head_dim]")
+    return HeadNorm(weight.data_ptr(), eps, offset, _kind_of(weight))
+
+
+def rimuru_norm_rope_apply(rope, positions_ptr: int, num_tokens: int, head_dim: int, ins, outs, norms,
+                           stream: int = 0) -> None:
+    """Normalise and rotate the arrays ``ins`` into ``outs``; ``norms`` has a ``HeadNorm`` for each.
+    ``rope`` may be None (norms alone; ``positions_ptr`` may then be 0)."""
+    n = len(ins)
+    if len(outs) != n or len(norms) != n:
+        raise ValueError("as many outputs and norms as inputs")
+    _check(lib.rimuru_norm_rope_apply(rope, positions_ptr or None, num_tokens, head_dim, (Heads * n)(*ins),
+                                      (Heads * n)(*outs), (HeadNorm * n)(*norms), n, stream))
+
+
+def rimuru_view_set_state_shape(view, heads: int, key_dim: int, value_dim: int) -> None:
+    _check(lib.rimuru_view_set_state_shape(view, heads, key_dim, value_dim))
+
+
+def rimuru_linear_attention_workspace_bytes(view, num_seqs: int, num_tokens: int, max_new: int) -> int:
+    return int(lib.rimuru_linear_attention_workspace_bytes(view, num_seqs, num_tokens, max_new))
+
+
+def rimuru_linear_attention(view, q, k, v, out, log_decay_ptr: int, decay_token_stride: int,
+                            decay_head_stride: int, cu_new_ptr: int, num_seqs: int, num_tokens: int,
+                            max_new: int, state_in_ptr: int, state_out_ptr: int, scale: float,
+                            workspace_ptr: int, workspace_bytes: int, stream: int = 0) -> None:
+    """``cu_new_ptr`` may be 0 (one token per sequence)."""
+    _check(lib.rimuru_linear_attention(view, q, k, v, out, log_decay_ptr or None, decay_token_stride,
+                                       decay_head_stride, cu_new_ptr or None, num_seqs, num_tokens,
+                                       max_new, state_in_ptr, state_out_ptr, scale, workspace_ptr,
+                                       workspace_bytes, stream))
+
+
+def rows_of(t) -> Rows:
+    """Descriptor of a tensor [rows, cols] whose last axis is contiguous."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("expected [rows, cols] with a contiguous last axis")
+    return Rows(t.data_ptr(), t.stride(0), t.shape[1], _kind_of(t))
+
+
+def rimuru_beam_select_workspace_bytes(num_groups: int, beams: int, vocab: int, n_select: int) -> int:
+    return int(lib.rimuru_beam_select_workspace_bytes(num_groups, beams, vocab, n_select))
+
+
+def rimuru_beam_select(logits, scores_ptr: int, done_ptr: int, num_groups: int, beams: int, pad_token: int,
+                       n_select: int, out_scores_ptr: int, out_rows_ptr: int, out_tokens_ptr: int,
+                       workspace_ptr: int, workspace_bytes: int, stream: int = 0) -> None:
+    """``logits`` is a ``Rows`` of num_groups * beams rows; ``done_ptr`` may be 0 (no beam is finished)."""
+    _check(lib.rimuru_beam_select(logits, scores_ptr, done_ptr or None, num_groups, beams, pad_token, n_select,
+                                  out_scores_ptr, out_rows_ptr, out_tokens_ptr, workspace_ptr,
+                                  workspace_bytes, stream))
+
+
+def rimuru_kv_reorder(view, parents_ptr: int, num_seqs: int, kv_lens_ptr: int, num_parents: int,
+                      table_in_ptr: int, table_out_ptr: int, num_layers: int, table_stride: int,
+                      fresh_ptr: int, lens_out_ptr: int, stream: int = 0) -> None:
+    _check(lib.rimuru_kv_reorder(view, parents_ptr, num_seqs, kv_lens_ptr, num_parents, table_in_ptr,
+                                 table_out_ptr, num_layers, table_stride, fresh_ptr, lens_out_ptr, stream))
