@@ -20,7 +20,7 @@ LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "librimuru.so")
 
 SOURCES = ["pool.cpp", "forward.cu", "layer.cu", "moe_small.cu", "moe_gemm.cu", "moe_gemm_2sm.cu", "moe_gemm_wide.cu", "moe_decode.cu", "noalloc.cu", "selftest.cu", "offload.cu",
-           "rope.cu", "norm_rope.cu", "linear.cu", "beam.cu", "kv_cache.cu", "kv_attention.cu", "kv_decode.cu", "kv_tiles.cu"]
+           "rope.cu", "norm_rope.cu", "linear.cu", "linear_chunk.cu", "beam.cu", "kv_cache.cu", "kv_attention.cu", "kv_decode.cu", "kv_tiles.cu"]
 HEADERS = ["internal.h", "kernels.h", "device.cuh", "route.cuh", "kv.h", "kv_attn.h", "rope.h", "linear.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

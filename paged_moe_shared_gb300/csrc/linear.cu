@@ -118,6 +118,13 @@ cudaError_t launch_steps(const LinearArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// How a call is cut; the number of SMs is the device's, or the usual one without a device.
+LinearCut cut_of(const View& v, int num_seqs, int num_tokens, int max_new) {
+  if (max_new <= kStepsMost) return {};
+  const int sms = rimuru_device_sm_count();
+  return linear_cut(v.state_heads, v.key_dim, v.value_dim, sms > 0 ? sms : 152, num_seqs, num_tokens, max_new);
+}
+
 int state_ready(View* v) {
   if (!v->has_state) return fail(RIMURU_ERR_STATE, "view has no state shape");
   bool made = false;
@@ -160,7 +167,7 @@ extern "C" int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int ke
 extern "C" uint64_t rimuru_linear_attention_workspace_bytes(rimuru_view_t view, int num_seqs,
                                                             int num_tokens, int max_new) {
   if (!view || !view->v.has_state || num_seqs < 0 || num_tokens < 0 || max_new < 0) return 0;
-  return 1024;
+  return 1024 + rimuru::cut_of(view->v, num_seqs, num_tokens, std::min(max_new, num_tokens)).state_bytes;
 }
 
 extern "C" int rimuru_linear_attention(rimuru_view_t view, const rimuru_heads* q, const rimuru_heads* k,
@@ -234,7 +241,12 @@ extern "C" int rimuru_linear_attention(rimuru_view_t view, const rimuru_heads* q
   a.num_pages = static_cast<int>(v.n_pages);
   a.err = v.kv->d_err;
   a.sms = v.kv->sms;
-  const cudaError_t e = launch_linear_steps(a, num_tokens > 0 ? q->dtype : RIMURU_BF16, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int dtype = num_tokens > 0 ? q->dtype : RIMURU_BF16;
+  // One by one a token costs about 0.6 us, a chunk of 64 with its start several us.
+  const cudaError_t e = max_new <= kStepsMost
+                            ? launch_linear_steps(a, dtype, s)
+                            : launch_linear_chunks(a, cut_of(v, num_seqs, num_tokens, max_new), workspace, dtype, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("linear attention launch", e));
   return RIMURU_OK;
 }

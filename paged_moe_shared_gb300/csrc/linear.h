@@ -25,6 +25,17 @@ struct LinearArgs {
   int sms;
 };
 
+// How the chunked form cuts a call: pieces of at most `piece` rows, cut where the row number is a
+// multiple of it (0: sequences are left whole).
+struct LinearCut {
+  int piece = 0;
+  int pieces = 0;            // of all sequences, empty ones included
+  uint64_t state_bytes = 0;  // of the pieces' states, then of the sequences' first ones, then decays
+};
+LinearCut linear_cut(int heads, int key_dim, int value_dim, int sms, int num_seqs, int num_tokens, int max_new);
+// New tokens that the recurrent form still takes.
+constexpr int kStepsMost = 16;
+
 // Rows and pages of a sequence.  `ok` is false where the tables are bad (recorded by the
 // thread that asks for it): the sequence is then left alone.
 struct LinearSeq {
@@ -50,5 +61,6 @@ __device__ __forceinline__ LinearSeq linear_seq(const LinearArgs& a, int b, bool
 }
 
 cudaError_t launch_linear_steps(const LinearArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearCut& cut, void* workspace, int dtype, cudaStream_t s);
 
 }  // namespace rimuru
