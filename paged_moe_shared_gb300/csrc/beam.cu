@@ -2,14 +2,14 @@
 // cache that follows it.
 //
 // Selection.  A candidate (beam b, token v) is worth (x_v - m_b) + c_b with m_b
-// the row's maximum and c_b = score_b - log(sum exp(x - m_b)), so one row's candidates stand in the order of its logits, and the sum
-// and the order need one read of them.  The first kernel streams the logits once: for
-// each run of 64 tokens (a group) it keeps the largest logit, for each of its chunks of a
-// row the maximum and the sum of exponentials.  The n best candidates lie in the n best
-// groups (by value, then by position: whoever is outside has n better group leaders
-// before it), so the second kernel, one CTA a batch entry, looks at the group maxima,
-// reads n groups of logits again and ranks what may be among the n best.
-// Comparisons that decide are made on doubles; fp32 only sieves, with a margin.
+// the row's maximum and c_b = score_b - log(sum exp(x - m_b)), so one row's candidates
+// stand in the order of its logits, and the sum and the order need one read of them.  The
+// first kernel streams the logits once, a warp for each chunk of 1024 tokens, and keeps
+// the chunk's maximum and sum of exponentials.  The n best candidates lie in the n best
+// chunks (by maximum, then by position: whoever is outside has n better chunk leaders
+// before it), so the second kernel, one CTA a batch entry, picks those chunks, reads them
+// again and ranks what may be among the n best.  Comparisons that decide are made on
+// doubles; fp32 only sieves, with a margin.
 #include <algorithm>
 #include <cmath>
 
@@ -19,13 +19,13 @@
 namespace rimuru {
 namespace {
 
-constexpr int kGroup = 64;             // tokens of a group
-constexpr int kChunk = 8192;           // tokens of a first-kernel CTA
+constexpr int kChunk = 1024;           // tokens of a first-kernel warp
 constexpr int kScanThreads = 256;
 constexpr int kPickThreads = 1024;
 constexpr int kLeaders = 256;          // subsets whose best give the sieve
+constexpr int kShare = kPickThreads / kLeaders;
 constexpr int kMostSelect = 128;
-constexpr int kList = 512;             // candidates that are ranked by counting
+constexpr int kList = 1024;            // candidates that are ranked by counting
 constexpr int kMostBeams = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -38,11 +38,9 @@ struct BeamArgs {
   int groups, beams, pad, n_select;
   float* best;
   int32_t *rows, *tokens;
-  int shift_elems;   // elements of 16 bytes
-  int n_groups;      // groups of a row
-  int n_chunks;
-  float* top;        // [rows][n_groups]
-  float2* parts;     // [rows][n_chunks] maximum and sum of exp(x - maximum)
+  int n_chunks;      // of a row
+  int ctas;          // of the scan
+  float *tops, *sums;  // [rows][n_chunks]: a chunk's maximum, its sum of exp(x - maximum)
 };
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -55,6 +53,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+__device__ __forceinline__ __nv_bfloat16 lowest(__nv_bfloat16) { return __ushort_as_bfloat16(0xFF80); }
+__device__ __forceinline__ __half lowest(__half) { return __ushort_as_half(0xFC00); }
+__device__ __forceinline__ float lowest(float) { return -INFINITY; }
 
 // A NaN counts as -inf, infinities as the largest finite value.
 __device__ __forceinline__ float tame(float x) {
@@ -69,93 +71,108 @@ __device__ __forceinline__ const T* row_base(const BeamArgs& a, int row, int* sk
   return p - *skip;
 }
 
-// Eight elements from place `at` (a multiple of 8); places outside [skip, end) are -inf.
+// Eight elements from place `at` (a multiple of 8), as they lie in memory; places outside
+// [skip, end) are -inf.
 template <typename T>
-__device__ __forceinline__ void load8(const T* base, int at, int skip, int end, float (&x)[8]) {
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load8(const T* base, int at, int skip, int end) {
+  Raw<T> v;
   if (at >= skip && at + 8 <= end) {
-    uint4 w[sizeof(T) / 2];
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) w[i] = dev::ld_nc_na_v4(base + at + i * (16 / sizeof(T)));
-    const T* t = reinterpret_cast<const T*>(w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = to_f(t[e]);
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v.w[i] = dev::ld_nc_na_v4(base + at + i * (16 / sizeof(T)));
   } else {
+    T* t = reinterpret_cast<T*>(&v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = at + e >= skip && at + e < end ? to_f(base[at + e]) : -INFINITY;
+    for (int e = 0; e < 8; ++e) t[e] = at + e >= skip && at + e < end ? base[at + e] : lowest(T());
   }
+  return v;
 }
 
-// Maximum and sum of two parts.
-__device__ __forceinline__ float2 join(float2 a, float2 b) {
-  const float m = fmaxf(a.x, b.x);
-  float s = 0.f;
-  if (a.x > -INFINITY) s += a.y * ex2((a.x - m) * kLog2e);
-  if (b.x > -INFINITY) s += b.y * ex2((b.x - m) * kLog2e);
-  return make_float2(m, s);
+// Largest of eight elements and `m`, a number where there is one among them.
+__device__ __forceinline__ float max8(const Raw<__nv_bfloat16>& r) {
+  const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&r);
+  const __nv_bfloat162 m = __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float max8(const Raw<__half>& r) {
+  const __half2* x = reinterpret_cast<const __half2*>(&r);
+  const __half2 m = __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float max8(const Raw<float>& r) {
+  const float* x = reinterpret_cast<const float*>(&r);
+  float m = x[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) m = fmaxf(m, x[e]);
+  return m;
 }
 
+// A warp goes from chunk to chunk and loads the next one before it works on its own.
+// exp(x - m) is 2^(x L - fl(m L)) with L = log2(e) in fp32: one multiply-add; what the
+// rounding of m L puts into every term alike is taken out of the sum.
 template <typename T>
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
   dev::grid_dep_launch();
-  __shared__ float2 warp_part[kScanThreads / 32];
-  const int row = blockIdx.y, tid = threadIdx.x;
-  if (a.done && a.done[row]) return;
-  int skip;
-  const T* base = row_base<T>(a, row, &skip);
-  const int end = skip + a.vocab;
-  constexpr int kVec = 4;  // vectors of eight in flight
-  float2 part = make_float2(-INFINITY, 0.f);
-  const int c0 = blockIdx.x * kChunk;
-#pragma unroll 1
-  for (int c = c0; c < c0 + kChunk && c < end; c += kScanThreads * 8 * kVec) {
-    float x[kVec][8];
+  const int lane = threadIdx.x & 31;
+  constexpr int kVec = kChunk / 256;  // vectors of eight of a lane
+  const int64_t total = static_cast<int64_t>(a.groups) * a.beams * a.n_chunks;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kScanThreads / 32);
+  Raw<T> next[kVec];
+  const auto load = [&](int64_t at) {
+    const int row = static_cast<int>(at / a.n_chunks), chunk = static_cast<int>(at - static_cast<int64_t>(row) * a.n_chunks);
+    if (a.done && a.done[row]) return false;
+    int skip;
+    const T* base = row_base<T>(a, row, &skip);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) load8(base, c + (j * kScanThreads + tid) * 8, skip, end, x[j]);
-    float m = -INFINITY;
+    for (int j = 0; j < kVec; ++j) next[j] = load8(base, chunk * kChunk + j * 256 + lane * 8, skip, skip + a.vocab);
+    return true;
+  };
+  int64_t at = static_cast<int64_t>(blockIdx.x) * (kScanThreads / 32) + (threadIdx.x >> 5);
+  bool live = at < total && load(at);
+  for (; at < total; at += stride) {
+    Raw<T> raw[kVec];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      float v = x[j][0];
+    for (int j = 0; j < kVec; ++j) raw[j] = next[j];
+    const bool mine = live;
+    live = at + stride < total && load(at + stride);
+    if (!mine) continue;
+    float m = -INFINITY;  // fmaxf takes the number where the other is a NaN
 #pragma unroll
-      for (int e = 1; e < 8; ++e) v = fmaxf(v, x[j][e]);
-      v = fmaxf(v, -INFINITY);
-      m = fmaxf(m, v);
+    for (int j = 0; j < kVec; ++j) m = fmaxf(m, max8(raw[j]));
 #pragma unroll
-      for (int s = 1; s < 8; s <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, s));
-      const int g = (c + (j * kScanThreads + tid) * 8) / kGroup;
-      if (tid % 8 == 0 && g < a.n_groups) a.top[static_cast<int64_t>(row) * a.n_groups + g] = fminf(v, 3.402823466e38f);
-    }
-    if (m > part.x) {
-      part.y = part.x > -INFINITY ? part.y * ex2((part.x - fminf(m, 3.402823466e38f)) * kLog2e) : 0.f;
-      part.x = fminf(m, 3.402823466e38f);
-    }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    m = fminf(m, 3.402823466e38f);
+    const float scaled = m * kLog2e;
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
+      const T* x = reinterpret_cast<const T*>(&raw[j]);
       float u = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u += ex2((x[j][e] - part.x) * kLog2e);
+      for (int e = 0; e < 8; ++e) u += ex2(fmaf(to_f(x[e]), kLog2e, -scaled));
       s += u;
     }
-    if (!(s <= 3.402823466e38f)) {  // a NaN or an infinity among them, or nothing finite so far
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    s *= ex2(-fmaf(m, kLog2e, -scaled));
+    if (!(s <= 3.402823466e38f)) {  // a NaN or an infinity among them, or nothing above -inf
       s = 0.f;
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
+      for (int j = 0; j < kVec; ++j) {
+        const T* x = reinterpret_cast<const T*>(&raw[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = tame(x[j][e]);
-          if (v > -INFINITY) s += ex2((v - part.x) * kLog2e);
+          const float v = tame(to_f(x[e]));
+          if (v > -INFINITY) s += ex2((v - m) * kLog2e);
         }
-    }
-    part.y += s;
-  }
+      }
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1)
-    part = join(part, make_float2(__shfl_xor_sync(~0u, part.x, m), __shfl_xor_sync(~0u, part.y, m)));
-  if (tid % 32 == 0) warp_part[tid / 32] = part;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kScanThreads / 32; ++w) part = join(part, warp_part[w]);
-    a.parts[static_cast<int64_t>(row) * a.n_chunks + blockIdx.x] = part;
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    }
+    if (lane == 0) a.tops[at] = m, a.sums[at] = s;
   }
 }
 
@@ -177,79 +194,55 @@ __device__ __forceinline__ bool before(Candidate a, Candidate b) {
   return a.key > b.key || (a.key == b.key && a.index < b.index);
 }
 
+constexpr int kTops = 4096;  // chunk maxima that are kept in shared memory
+
 struct PickShared {
   double c[kMostBeams];  // a candidate is worth (x - m) + c
   float c32[kMostBeams], m[kMostBeams];
   uint8_t done[kMostBeams];
-  float leader[kLeaders];
+  float leader[kLeaders], seen[kPickThreads];
   Candidate list[kList], chosen[kMostSelect], next[kPickThreads / 32];
   int count, n_chosen;
   float sieve;
+  float tops[kTops];
 };
 
-// The `want` first candidates of a stream in order, into s.chosen[0 .. s.n_chosen).
-// rough(i, &err): fp32 worth of item i and a bound of its error; exact(i): the candidate.
-// Candidates worth -inf (in fp32) are left out.  All threads of the CTA call it.
-template <typename Rough, typename Exact>
-__device__ void pick(PickShared& s, int n, int want, const Rough& rough, const Exact& exact) {
+__device__ __forceinline__ void note(PickShared& s, const Candidate& c) {
+  const int at = atomicAdd(&s.count, 1);
+  if (at < kList) s.list[at] = c;
+}
+
+// The `want` first of the listed candidates, if the list holds them all; a warp for each
+// of them counts those before it.  Candidates worth -inf are left out.
+__device__ bool rank(PickShared& s, int want) {
+  const int count = s.count, lane = threadIdx.x % 32;
+  if (count > kList) return false;
+  for (int i = threadIdx.x / 32; i < count; i += kPickThreads / 32) {
+    const Candidate mine = s.list[i];
+    int n = 0;
+    for (int j = lane; j < count; j += 32) n += before(s.list[j], mine);
+    n = __reduce_add_sync(~0u, n);
+    if (lane == 0 && n < want && mine.key > kNothing) {
+      s.chosen[n] = mine;
+      atomicAdd(&s.n_chosen, 1);
+    }
+  }
+  __syncthreads();
+  return true;
+}
+
+// The same where many candidates are near the border (rows that are alike): one at a time.
+// item(i, &c): whether item i passes the sieve, and its candidate.
+template <typename Item>
+__device__ void one_by_one(PickShared& s, int n, int want, const Item& item) {
   const int tid = threadIdx.x;
-  // The best of each of 256 subsets, from below: the want-th largest of them bounds the
-  // want-th best of all.
-  float m = -INFINITY;
-  for (int i = tid; i < n; i += kPickThreads) {
-    float err;
-    const float r = rough(i, &err);
-    m = fmaxf(m, r - err);
-  }
-  m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-  m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-  if (tid % 4 == 0) s.leader[tid / 4] = m;
-  if (tid == 0) s.count = s.n_chosen = 0;
-  __syncthreads();
-  if (tid < kLeaders) {
-    const float mine = s.leader[tid];
-    int above = 0;
-#pragma unroll 8
-    for (int i = 0; i < kLeaders; ++i) above += s.leader[i] > mine || (s.leader[i] == mine && i < tid);
-    if (above == want - 1) s.sieve = mine;
-  }
-  __syncthreads();
-  const float sieve = s.sieve;
-  const auto passes = [&](int i) {
-    float err;
-    const float r = rough(i, &err);
-    return r > -INFINITY && r + err >= sieve;
-  };
-  for (int i = tid; i < n; i += kPickThreads)
-    if (passes(i)) {
-      const int at = atomicAdd(&s.count, 1);
-      if (at < kList) s.list[at] = exact(i);
-    }
-  __syncthreads();
-  if (s.count <= kList) {
-    const int count = s.count;
-    // a warp for each listed candidate: how many come before it
-    for (int i = tid / 32; i < count; i += kPickThreads / 32) {
-      const Candidate mine = s.list[i];
-      int n_before = 0;
-      for (int j = tid % 32; j < count; j += 32) n_before += before(s.list[j], mine);
-      n_before = __reduce_add_sync(~0u, n_before);
-      if (tid % 32 == 0 && n_before < want && mine.key > kNothing) {
-        s.chosen[n_before] = mine;
-        atomicAdd(&s.n_chosen, 1);
-      }
-    }
-    __syncthreads();
-    return;
-  }
-  // Many candidates near the border (rows that are alike): one at a time.
   Candidate last{~0ull, -1};
   for (int k = 0; k < want; ++k) {
     Candidate mine{0, 0x7FFFFFFF};
+#pragma unroll 1
     for (int i = tid; i < n; i += kPickThreads) {
-      if (!passes(i)) continue;
-      const Candidate c = exact(i);
-      if (before(last, c) && before(c, mine)) mine = c;
+      Candidate c;
+      if (item(i, &c) && before(last, c) && before(c, mine)) mine = c;
     }
     for (int w = 16; w > 0; w >>= 1) {
       const Candidate c{__shfl_xor_sync(~0u, mine.key, w), __shfl_xor_sync(~0u, mine.index, w)};
@@ -268,27 +261,93 @@ __device__ void pick(PickShared& s, int n, int want, const Rough& rough, const E
   __syncthreads();
 }
 
+// A lower bound of the want-th best of a stream of which each thread has seen a part; `m`
+// is the best of that part, from below.  The best of 256 subsets are ranked; a subset is
+// what threads 256 apart have seen, so that neighbours, which may all be good, count apart.
+__device__ float bound_of(PickShared& s, float m, int want) {
+  const int tid = threadIdx.x;
+  s.seen[tid] = m;
+  __syncthreads();
+  if (tid < kLeaders) {
+    m = s.seen[tid];
+#pragma unroll
+    for (int k = 1; k < kShare; ++k) m = fmaxf(m, s.seen[tid + k * kLeaders]);
+    s.leader[tid] = m;
+  }
+  __syncthreads();
+  // kShare threads count for a leader, a part of the others each
+  const int me = tid / kShare;
+  const float mine = s.leader[me];
+  int above = 0;
+#pragma unroll 8
+  for (int i = tid % kShare; i < kLeaders; i += kShare) above += s.leader[i] > mine || (s.leader[i] == mine && i < me);
+#pragma unroll
+  for (int o = 1; o < kShare; o <<= 1) above += __shfl_xor_sync(~0u, above, o);
+  if (above == want - 1) s.sieve = mine;
+  __syncthreads();
+  return s.sieve;
+}
+
+// log(y) of an fp32 y > 0: the exponent's share in a double, the fraction's in fp32.
+__device__ __forceinline__ double log_of(float y) {
+  int e;
+  float f = frexpf(y, &e);  // in [0.5, 1)
+  if (f < 0.70710678f) f *= 2.f, --e;
+  return fma(static_cast<double>(e), 0.693147180559945309417, static_cast<double>(logf(f)));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
   __shared__ PickShared s;
-  __shared__ int group_of[kMostSelect];
-  const int entry = blockIdx.x, tid = threadIdx.x;
+  __shared__ int chunk_of[kMostSelect];
+  const int entry = blockIdx.x, tid = threadIdx.x, lane = tid % 32;
   const int row0 = entry * a.beams;
+  const int N = a.n_chunks, n_tops = a.beams * N;
+  if (tid == 0) s.count = s.n_chosen = 0;
   dev::grid_dep_wait();
+  const float* all_tops = a.tops + static_cast<int64_t>(row0) * N;
+  const bool fits = n_tops <= kTops;
   // what a beam's logits have to be raised by: a warp for each beam
   for (int b = tid / 32; b < a.beams; b += kPickThreads / 32) {
     const int row = row0 + b;
     const bool done = a.done && a.done[row];
-    float2 part = make_float2(-INFINITY, 0.f);
-    if (!done)
-      for (int c = tid % 32; c < a.n_chunks; c += 32) part = join(part, a.parts[static_cast<int64_t>(row) * a.n_chunks + c]);
-    for (int m = 16; m > 0; m >>= 1)
-      part = join(part, make_float2(__shfl_xor_sync(~0u, part.x, m), __shfl_xor_sync(~0u, part.y, m)));
-    if (tid % 32 == 0) {
-      const float score = tame(a.scores[row]);
+    const float score = tame(a.scores[row]);
+    const float* tops = all_tops + b * N;
+    const float* sums = a.sums + static_cast<int64_t>(row) * N;
+    float m = -INFINITY, y = 0.f;
+    for (int c0 = 0; c0 < N; c0 += 256) {
+      float top[8], sum[8], t = m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = c0 + 32 * k + lane;
+        const bool in = c < N && !done;
+        top[k] = in ? tops[c] : -INFINITY;
+        sum[k] = in ? sums[c] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = c0 + 32 * k + lane;
+        t = fmaxf(t, top[k]);
+        // a finished beam is one chunk of one candidate, its pad token
+        if (fits && c < N) s.tops[b * N + c] = done && c == 0 ? 0.f : top[k];
+      }
+      if (t > -INFINITY) {
+        y *= ex2((m - t) * kLog2e);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y = fmaf(sum[k], ex2((top[k] - t) * kLog2e), y);
+        m = t;
+      }
+    }
+    float t = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
+    y = m > -INFINITY ? y * ex2((m - t) * kLog2e) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(~0u, y, o);
+    if (lane == 0) {
       double c = static_cast<double>(score);
-      if (!done) c = part.y > 0.f ? c - log(static_cast<double>(part.y)) : -INFINITY;
-      s.m[b] = done || !(part.x > -INFINITY) ? 0.f : part.x;
+      if (!done) c = y > 0.f ? c - log_of(y) : -INFINITY;
+      s.m[b] = t > -INFINITY ? t : 0.f;
       s.c[b] = c;
       s.c32[b] = static_cast<float>(c);
       s.done[b] = done;
@@ -304,46 +363,121 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   const auto worth = [&](int b, float x) {
     return ordered((static_cast<double>(x) - static_cast<double>(s.m[b])) + s.c[b]);
   };
-  // A finished beam is one group of one candidate, its pad token.
-  const int G = a.n_groups;
-  const auto group_top = [&](int i, int b) -> float {
-    if (s.done[b]) return i == b * G ? 0.f : -INFINITY;
-    return a.top[static_cast<int64_t>(row0) * G + i];
+  const auto passes = [&](int b, float x, float sieve) {
+    float err;
+    const float r = sum32(b, x, &err);
+    return r > -INFINITY && r + err >= sieve;
   };
-  const int want = a.n_select;
-  pick(s, a.beams * G, want,
-       [&](int i, float* err) { return sum32(i / G, group_top(i, i / G), err); },
-       [&](int i) { return Candidate{worth(i / G, group_top(i, i / G)), i}; });
-  const int n_groups = s.n_chosen;
-  if (tid < n_groups) group_of[tid] = s.chosen[tid].index;
-  __syncthreads();
+  const auto chunk_top = [&](int i, int b) {
+    return fits ? s.tops[i] : s.done[b] ? (i == b * N ? 0.f : -INFINITY) : all_tops[i];
+  };
 
-  // the elements of those groups; an index is beam * vocab + token
-  const auto element = [&](int i, int* beam, int* token) -> float {
-    const int g = group_of[i / kGroup], e = i % kGroup;
-    *beam = g / G;
-    const int row = row0 + *beam;
-    if (s.done[*beam]) {
-      *token = a.pad;
-      return e == 0 ? 0.f : -INFINITY;
+  // ---- the `want` best chunks
+  const int want = a.n_select;
+  float sieve = -INFINITY;
+  if (n_tops > 64) {  // below, all are ranked sooner
+    float best = -INFINITY;
+    for (int i = tid; i < n_tops; i += kPickThreads) {
+      float err;
+      const float r = sum32(i / N, chunk_top(i, i / N), &err);
+      best = fmaxf(best, r - err);
     }
-    int skip;
-    const T* base = row_base<T>(a, row, &skip);
-    const int at = (g - *beam * G) * kGroup + e;
-    *token = at - skip;
-    return at >= skip && at < skip + a.vocab ? tame(to_f(base[at])) : -INFINITY;
+    sieve = bound_of(s, best, want);
+  }
+  const auto chunk = [&](int i, Candidate* c) {
+    const int b = i / N;
+    const float x = chunk_top(i, b);
+    if (!passes(b, x, sieve)) return false;
+    *c = Candidate{worth(b, x), i};
+    return true;
   };
-  pick(s, n_groups * kGroup, want,
-       [&](int i, float* err) {
-         int b, v;
-         const float x = element(i, &b, &v);
-         return sum32(b, x, err);
-       },
-       [&](int i) {
-         int b, v;
-         const float x = element(i, &b, &v);
-         return Candidate{worth(b, x), b * a.vocab + v};
-       });
+  for (int i = tid; i < n_tops; i += kPickThreads) {
+    Candidate c;
+    if (chunk(i, &c)) note(s, c);
+  }
+  __syncthreads();
+  if (!rank(s, want)) one_by_one(s, n_tops, want, chunk);
+  const int n_chosen = s.n_chosen;
+  if (tid < n_chosen) chunk_of[tid] = s.chosen[tid].index;
+  // with `want` chunks the last one's leader is worth no more than the want-th best
+  sieve = n_chosen == want ? __double2float_rd(unordered(s.chosen[want - 1].key)) : -INFINITY;
+  __syncthreads();
+  if (tid == 0) s.count = s.n_chosen = 0;
+
+  // ---- the candidates of those chunks, a warp for each; an index is beam * vocab + token.
+  // What passes the chunks' sieve is listed.  Where that is too much (one beam far ahead of the
+  // others) or there is no such sieve, the candidates themselves give one.
+  constexpr int kVec = kChunk / 256;
+  const auto load = [&](int b, int g, Raw<T> (&x)[kVec]) {  // the place of its first token
+    int skip;
+    const T* base = row_base<T>(a, row0 + b, &skip);
+    const int at = (g - b * N) * kChunk + lane * 8;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[j] = load8(base, at + 256 * j, skip, skip + a.vocab);
+    return at - skip;
+  };
+  __syncthreads();
+  for (int turn = sieve == -INFINITY; turn < 2; ++turn) {
+    if (turn == 1) {
+      float best = -INFINITY;
+      for (int k = tid / 32; k < n_chosen; k += kPickThreads / 32) {
+        const int g = chunk_of[k], b = g / N;
+        float top = s.done[b] && lane == 0 ? 0.f : -INFINITY;
+        if (!s.done[b]) {
+          Raw<T> x[kVec];
+          load(b, g, x);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) top = fmaxf(top, max8(x[j]));
+          top = fminf(top, 3.402823466e38f);
+        }
+        float err;
+        const float r = sum32(b, top, &err);
+        best = fmaxf(best, r - err);
+      }
+      sieve = fmaxf(sieve, bound_of(s, best, want));
+      if (tid == 0) s.count = 0;
+      __syncthreads();
+    }
+    for (int k = tid / 32; k < n_chosen; k += kPickThreads / 32) {
+      const int g = chunk_of[k], b = g / N;
+      if (s.done[b]) {
+        if (lane == 0) note(s, Candidate{worth(b, 0.f), b * a.vocab + a.pad});
+        continue;
+      }
+      Raw<T> x[kVec];
+      const int token = load(b, g, x);
+      // what a logit has to reach, from below
+      const float least = sieve > -INFINITY ? s.m[b] + (sieve - s.c32[b]) - (fabsf(s.m[b]) + fabsf(sieve) + fabsf(s.c32[b])) * 0x1p-21f
+                                            : -3.402823466e38f;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (!(max8(x[j]) >= least)) continue;
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          const float f = tame(to_f(reinterpret_cast<const T*>(&x[j])[e]));
+          if (f >= least && passes(b, f, sieve)) note(s, Candidate{worth(b, f), b * a.vocab + token + 256 * j + e});
+        }
+      }
+    }
+    __syncthreads();
+    if (s.count <= kList) break;
+  }
+  if (!rank(s, want))
+    one_by_one(s, n_chosen * kChunk, want, [&](int i, Candidate* c) {
+      const int g = chunk_of[i / kChunk], b = g / N, e = i % kChunk;
+      float f = e == 0 ? 0.f : -INFINITY;
+      int token = a.pad;
+      if (!s.done[b]) {
+        int skip;
+        const T* base = row_base<T>(a, row0 + b, &skip);
+        const int at = (g - b * N) * kChunk + e;
+        token = at - skip;
+        f = at >= skip && at < skip + a.vocab ? tame(to_f(base[at])) : -INFINITY;
+      }
+      if (!passes(b, f, sieve)) return false;
+      *c = Candidate{worth(b, f), b * a.vocab + token};
+      return true;
+    });
   for (int k = tid; k < want; k += kPickThreads) {
     const int64_t at = static_cast<int64_t>(entry) * want + k;
     const bool live = k < s.n_chosen;
@@ -356,16 +490,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
 
 template <typename T>
 cudaError_t launch(const BeamArgs& a, cudaStream_t s) {
-  const int rows = a.groups * a.beams;
-  for (int r = 0; r < rows; r += 65535 / a.beams * a.beams) {  // grid.y ends at 65535
-    BeamArgs p = a;
-    const int n = std::min(65535 / a.beams * a.beams, rows - r);
-    p.logits = static_cast<const T*>(a.logits) + r * a.row_stride;
-    p.done = a.done ? a.done + r : nullptr;
-    p.top += static_cast<int64_t>(r) * a.n_groups;
-    p.parts += static_cast<int64_t>(r) * a.n_chunks;
-    beam_scan_kernel<T><<<dim3(a.n_chunks, n), kScanThreads, 0, s>>>(p);
-  }
+  beam_scan_kernel<T><<<a.ctas, kScanThreads, 0, s>>>(a);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.groups);
   cfg.blockDim = dim3(kPickThreads);
@@ -462,15 +587,14 @@ __global__ void __launch_bounds__(kReorderThreads) kv_reorder_kernel(const __gri
 using rimuru::fail;
 
 namespace {
-// Groups of a row: a row may begin up to eight elements past a 16-byte boundary.
-int64_t row_groups(int vocab) { return (static_cast<int64_t>(vocab) + 7 + rimuru::kGroup - 1) / rimuru::kGroup; }
+// A row may begin up to seven elements past a 16-byte boundary.
 int64_t row_chunks(int vocab) { return (static_cast<int64_t>(vocab) + 7 + rimuru::kChunk - 1) / rimuru::kChunk; }
 }  // namespace
 
 extern "C" uint64_t rimuru_beam_select_workspace_bytes(int num_groups, int beams, int vocab, int n_select) {
   if (num_groups < 0 || beams <= 0 || vocab <= 0 || n_select <= 0) return 0;
   const uint64_t rows = static_cast<uint64_t>(num_groups) * beams;
-  return (rows * row_groups(vocab) * sizeof(float) + 1023) / 1024 * 1024 + rows * row_chunks(vocab) * sizeof(float2) + 1024;
+  return 2 * rows * row_chunks(vocab) * sizeof(float) + 1024;
 }
 
 extern "C" int rimuru_beam_select(const rimuru_rows* logits, const float* scores, const uint8_t* done,
@@ -487,7 +611,7 @@ extern "C" int rimuru_beam_select(const rimuru_rows* logits, const float* scores
     return fail(RIMURU_ERR_ARG, "logits: unknown element type");
   if (beams > kMostBeams || n_select > kMostSelect)
     return fail(RIMURU_ERR_UNSUPPORTED, "at most 128 beams and 128 selected candidates");
-  if (static_cast<int64_t>(beams) * (logits->cols + 2ll * kGroup) > (1 << 30) ||
+  if (static_cast<int64_t>(beams) * (logits->cols + 2ll * kChunk) > (1 << 30) ||
       static_cast<int64_t>(num_groups) * beams > (1 << 24))
     return fail(RIMURU_ERR_UNSUPPORTED, "too many beams and tokens for one call");
   if (num_groups == 0) return RIMURU_OK;
@@ -514,16 +638,19 @@ extern "C" int rimuru_beam_select(const rimuru_rows* logits, const float* scores
   a.done = done;
   a.groups = num_groups, a.beams = beams, a.pad = pad_token, a.n_select = n_select;
   a.best = out_scores, a.rows = out_rows, a.tokens = out_tokens;
-  a.n_groups = static_cast<int>(row_groups(logits->cols));
   a.n_chunks = static_cast<int>(row_chunks(logits->cols));
-  a.top = static_cast<float*>(workspace);
-  const uint64_t rows = static_cast<uint64_t>(num_groups) * beams;
-  a.parts = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) +
-                                      (rows * a.n_groups * sizeof(float) + 1023) / 1024 * 1024);
+  const int64_t chunks = static_cast<int64_t>(num_groups) * beams * a.n_chunks;
+  a.tops = static_cast<float*>(workspace);
+  a.sums = a.tops + chunks;
+  int sms = 0, device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("device attributes", e));
+  a.ctas = static_cast<int>(std::min<int64_t>((chunks + 7) / 8, 4ll * sms));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = logits->dtype == RIMURU_BF16  ? launch<__nv_bfloat16>(a, s)
-                        : logits->dtype == RIMURU_F16 ? launch<__half>(a, s)
-                                                      : launch<float>(a, s);
+  e = logits->dtype == RIMURU_BF16  ? launch<__nv_bfloat16>(a, s)
+      : logits->dtype == RIMURU_F16 ? launch<__half>(a, s)
+                                    : launch<float>(a, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("beam selection launch", e));
   return RIMURU_OK;
 }

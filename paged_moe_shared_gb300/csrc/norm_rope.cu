@@ -2,11 +2,10 @@
 // rot_p(x * r * (w + offset)) with r = 1 / sqrt(mean(x^2) + eps).
 //
 // Each element is read and written once; a head stays in the registers of the lanes
-// that loaded it.  A group of 2^n lanes takes one token and some of its heads: a lane
-// holds two vectors of eight elements of a head (in the half layout the two members of
-// eight pairs, so that pairs turn within a lane), the squares are added up over the
-// group by shuffles, and the token's cosines and sines, which a lane computes once for
-// the pairs that it holds, serve every head that the group takes.
+// that loaded it.  A group of 2^n lanes takes some heads of one token: a lane holds two
+// vectors of eight elements of a head (in the half layout the two members of eight pairs,
+// so that pairs turn within a lane), and the squares are added up over the group by
+// shuffles.  A CTA computes its tokens' cosines and sines once, for all heads.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -36,51 +35,87 @@ struct NormArgs {
   int first_head[kMaxArrays + 1];  // heads of the arrays before this one
   const int32_t* positions;
   int num_tokens, head_dim;
-  int lanes_log2;       // of a group
-  int heads_per_group, groups_per_token;
+  int lanes_log2;         // of a group
+  int heads_per_group;
+  int groups, groups_mul; // groups of a token in a CTA; g / groups = g * groups_mul >> 16
+  int tokens;             // of a CTA
   int turn_slots, slots;  // of a head: slots whose vectors are a pair's members, and all
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(v[i] << 16);
-    x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-  }
+// Two fp32 in one register pair.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ float2 split(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+template <typename T>
+struct Raw {  // eight elements as they lie in memory
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
+  Raw<T> v;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return v;
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, uint64_t (&x)[4]) {
+  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack(const Raw<__half>& r, uint64_t (&x)[4]) {
+  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    x[i] = pair(f.x, f.y);
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ void unpack(const Raw<float>& r, uint64_t (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[2 * i] = pair(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+    x[2 * i + 1] = pair(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
+  }
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(dev::pack_bf16x2(x[0], x[1]), dev::pack_bf16x2(x[2], x[3]),
-                                            dev::pack_bf16x2(x[4], x[5]), dev::pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const uint64_t (&x)[4]) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = dev::pack_bf16x2(split(x[i]).x, split(x[i]).y);
+  *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
+__device__ __forceinline__ void store8(__half* p, const uint64_t (&x)[4]) {
   uint32_t v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    const __half2 h = __floats2half2_rn(split(x[i]).x, split(x[i]).y);
     v[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store8(float* p, const uint64_t (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = split(x[2 * i]), b = split(x[2 * i + 1]);
+    reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
+  }
 }
 
 // Offsets of a slot's two vectors in a head, -1 where there is none.  Slots below
@@ -101,173 +136,254 @@ __device__ __forceinline__ void place(const NormArgs& p, int slot, int (&off)[2]
   if (off[1] >= p.head_dim) off[1] = -1;
 }
 
-// kSlots: slots of a lane.
-template <typename T, bool kHalf, int kSlots>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormArgs p) {
-  constexpr int kRows = kSlots == 1 ? 4 : 2;  // heads in flight in a group
-  __shared__ uint64_t turn[kMaxPairs];
-  for (int i = threadIdx.x; i < p.rope.pairs; i += blockDim.x) turn[i] = p.rope.turn[i];
-  __syncthreads();
+// A group's place among the heads of the arrays.
+template <typename T>
+struct Cursor {
+  T* at;       // the head's first element
+  int64_t hs;
+  int left, i; // heads left of array i
+};
+template <bool kOut, typename T>
+__device__ __forceinline__ void begin(const NormArgs& p, Cursor<T>* c, unsigned t, int h) {
+  int i = 0;
+#pragma unroll
+  for (int k = 1; k < kMaxArrays; ++k) i += h >= p.first_head[k];
+  const NormArray& A = p.arr[i];
+  c->i = i;
+  c->left = p.first_head[i + 1] - h;
+  c->hs = kOut ? A.out_hs : A.in_hs;
+  c->at = static_cast<T*>(kOut ? A.out : const_cast<void*>(A.in)) + static_cast<int64_t>(t) * (kOut ? A.out_ts : A.in_ts) +
+          (h - p.first_head[i]) * c->hs;
+}
+template <bool kOut, typename T>
+__device__ __forceinline__ void step(const NormArgs& p, Cursor<T>* c, unsigned t) {
+  c->at += c->hs;
+  if (--c->left == 0 && c->i + 1 < kMaxArrays) begin<kOut>(p, c, t, p.first_head[c->i + 1]);
+}
+
+// kSlots: slots of a lane; kFull: every lane has both vectors of each of its slots.  Heads
+// wait as they were loaded and are unpacked twice, for the sum and for the result: half the
+// registers for 16-bit types.  The next kRows heads are loaded before these are worked on.
+template <typename T, bool kHalf, int kSlots, bool kFull>
+__global__ void __launch_bounds__(kThreads, 2)
+    norm_rope_kernel(const __grid_constant__ NormArgs p) {
+  constexpr int kRows = kSlots == 1 ? 2 : 1;
+  extern __shared__ float4 dynamic[];
+  float* const weights = reinterpret_cast<float*>(dynamic);  // [arrays][head_dim], the offset added, ones without a weight
+  float2* const cosines = reinterpret_cast<float2*>(weights + kMaxArrays * p.head_dim);  // [tokens of the CTA][pairs]
   const int lanes = 1 << p.lanes_log2, lane = threadIdx.x & (lanes - 1);
-  const int64_t group = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> p.lanes_log2;
-  const int64_t t = group / p.groups_per_token;
-  // groups past the last token stay for the shuffles and take no head
-  const int h0 = t < p.num_tokens ? static_cast<int>(group - t * p.groups_per_token) * p.heads_per_group : 1 << 30;
-  const int rot = 2 * p.rope.pairs;
-
+  const int g = threadIdx.x >> p.lanes_log2, u = g * p.groups_mul >> 16;
+  const unsigned t0 = blockIdx.x * p.tokens, t = t0 + u, num_tokens = p.num_tokens;
+  const int h0 = (blockIdx.y * p.groups + g - u * p.groups) * p.heads_per_group;
+  // groups past the last token or head stay for the shuffles and take none
+  const int heads = u < p.tokens && t < num_tokens ? min(p.heads_per_group, p.first_head[kMaxArrays] - h0) : 0;
+  const int pairs = p.rope.pairs, rot = 2 * pairs;
   int off[kSlots][2];
-  float2 cs[kSlots][8];
-  const uint64_t pos =
-      rot > 0 && t < p.num_tokens ? static_cast<uint64_t>(static_cast<int64_t>(p.positions[t])) : 0;
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    place<kHalf>(p, lane + s * lanes, off[s]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // pair e of the slot: elements (e, e) of its two vectors, or (2 e, 2 e + 1) of one
-      const int at = kHalf ? (off[s][0] >= 0 && off[s][0] < rot ? off[s][0] + e : -1)
-                           : (off[s][e / 4] >= 0 && off[s][e / 4] < rot ? off[s][e / 4] / 2 + e % 4 : -1);
-      cs[s][e] = make_float2(1.f, 0.f);
-      if (at >= 0) {
-        float sn, c;
-        sincospif(__ll2float_rn(static_cast<int64_t>(pos * turn[at])) * 0x1p-63f, &sn, &c);
-        cs[s][e] = make_float2(c * p.rope.mscale, sn * p.rope.mscale);
-      }
-    }
-  }
+  for (int s = 0; s < kSlots; ++s) place<kHalf>(p, lane + s * lanes, off[s]);
 
-#pragma unroll 1
-  for (int i = 0; i < kMaxArrays; ++i) {
-    const int first = p.first_head[i], last = p.first_head[i + 1];
-    if (first == last) continue;
-    const NormArray& A = p.arr[i];
-    const int from = max(h0, first) - first, to = min(h0 + p.heads_per_group, last) - first;
-    // the same number of turns in every group of the warp: shuffles take all lanes
-    const int turns = __reduce_max_sync(~0u, max(0, to - from));
-    if (turns == 0) continue;
-    float w[kSlots][2][8];
+  Raw<T> next[kRows][kSlots][2];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
 #pragma unroll
     for (int s = 0; s < kSlots; ++s)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (A.weight && off[s][v] >= 0) {
-          if (A.weight_dtype == RIMURU_BF16) load8(static_cast<const __nv_bfloat16*>(A.weight) + off[s][v], w[s][v]);
-          else if (A.weight_dtype == RIMURU_F16) load8(static_cast<const __half*>(A.weight) + off[s][v], w[s][v]);
-          else load8(static_cast<const float*>(A.weight) + off[s][v], w[s][v]);
+      for (int v = 0; v < 2; ++v) next[r][s][v] = Raw<T>{};
+  Cursor<T> in{}, out{};
+  if (heads > 0) {
+    begin<false>(p, &in, t, h0);
+    begin<true>(p, &out, t, h0);
+  }
+  const auto load = [&](int h) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[s][v][e] += A.offset;
-        } else {
+    for (int r = 0; r < kRows; ++r)
+      if (h + r < heads) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[s][v][e] = 1.f;
-        }
+        for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            if (kFull || off[s][v] >= 0) next[r][s][v] = load_raw(in.at + off[s][v]);
+        step<false>(p, &in, t);
       }
-    const T* in = static_cast<const T*>(A.in) + t * A.in_ts + from * A.in_hs;
-    T* out = static_cast<T*>(A.out) + t * A.out_ts + from * A.out_hs;
-#pragma unroll 1
-    for (int h = 0; h < turns; h += kRows) {
-      float x[kRows][kSlots][2][8], sum[kRows];
+  };
+  load(0);
+  if (rot > 0) {
+    const int n = min(static_cast<unsigned>(p.tokens), num_tokens - t0);
+    for (int k = threadIdx.x; k < n * pairs; k += blockDim.x) {
+      const int w = k / pairs, i = k - w * pairs;
+      const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + w]));
+      float sn, c;
+      sincospif(__ll2float_rn(static_cast<int64_t>(pos * p.rope.turn[i])) * 0x1p-63f, &sn, &c);
+      cosines[k] = make_float2(c * p.rope.mscale, sn * p.rope.mscale);
+    }
+  }
+  for (int i = 0; i < kMaxArrays; ++i) {
+    const NormArray& A = p.arr[i];
+    if (p.first_head[i] == p.first_head[i + 1]) continue;
+    for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) {
+      const float w = !A.weight                        ? 1.f
+                      : A.weight_dtype == RIMURU_BF16  ? __bfloat162float(static_cast<const __nv_bfloat16*>(A.weight)[d])
+                      : A.weight_dtype == RIMURU_F16 ? __half2float(static_cast<const __half*>(A.weight)[d])
+                                                     : static_cast<const float*>(A.weight)[d];
+      weights[i * p.head_dim + d] = A.weight ? w + A.offset : w;
+    }
+  }
+  __syncthreads();
+
+  // of the slot's eight pairs: elements (e, e) of its two vectors, or (2 e, 2 e + 1) of one
+  uint64_t cs[kSlots][4], sn[kSlots][4];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r)
+  for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const int at = kHalf ? (off[s][0] >= 0 && off[s][0] < rot ? off[s][0] + e : -1)
+                           : (off[s][e / 4] >= 0 && off[s][e / 4] < rot ? off[s][e / 4] / 2 + e % 4 : -1);
+      const float2* w = cosines + u * pairs + at;
+      const float2 w0 = at >= 0 && heads > 0 ? w[0] : make_float2(1.f, 0.f), w1 = at >= 0 && heads > 0 ? w[1] : make_float2(1.f, 0.f);
+      cs[s][e / 2] = pair(w0.x, w1.x);
+      sn[s][e / 2] = pair(w0.y, w1.y);
+    }
+
+  const float per_dim = 1.f / p.head_dim;
+  const uint64_t minus = pair(-1.f, -1.f);
+#pragma unroll 1
+  for (int h = 0; h < p.heads_per_group; h += kRows) {  // as often in every group: shuffles take all lanes
+    Raw<T> x[kRows][kSlots][2];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) x[r][s][v] = next[r][s][v];
+    load(h + kRows);
+    float sum[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      uint64_t acc = 0;
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          uint64_t y[4];
+          unpack(x[r][s][v], y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc = fma2(y[e], y[e], acc);
+        }
+      sum[r] = split(acc).x + split(acc).y;
+    }
+    for (int m = lanes >> 1; m > 0; m >>= 1)
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) sum[r] += __shfl_xor_sync(~0u, sum[r], m);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      float eps = p.arr[out.i].eps, f = 1.f;
+      // squares past fp32: the head is taken 2^-96 times as large, where eps is nothing
+      const bool large = !std::is_same<T, __half>::value && isinf(sum[r]);
+      if (__any_sync(~0u, large)) {
+        float again = 0.f;
 #pragma unroll
         for (int s = 0; s < kSlots; ++s)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
-            if (from + h + r < to && off[s][v] >= 0) {
-              load8(in + (h + r) * A.in_hs + off[s][v], x[r][s][v]);
-            } else {
+            uint64_t y[4];
+            unpack(x[r][s][v], y);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[r][s][v][e] = 0.f;
+            for (int e = 0; e < 4; ++e) {
+              const float2 z = split(y[e]);
+              again = fmaf(z.x * 0x1p-96f, z.x * 0x1p-96f, again);
+              again = fmaf(z.y * 0x1p-96f, z.y * 0x1p-96f, again);
             }
           }
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        sum[r] = 0.f;
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-#pragma unroll
-          for (int v = 0; v < 2; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[r] = fmaf(x[r][s][v][e], x[r][s][v][e], sum[r]);
+        for (int m = lanes >> 1; m > 0; m >>= 1) again += __shfl_xor_sync(~0u, again, m);
+        if (large) sum[r] = again, eps = 0.f, f = 0x1p-96f;
       }
-      for (int m = lanes >> 1; m > 0; m >>= 1)
+      const float mean = fmaf(sum[r], per_dim, eps);
+      float k = rsqrtf(mean);
+      if (sizeof(T) == 4) k = isinf(mean) ? 0.f : k * fmaf(-0.5f * mean * k, k, 1.5f);  // to the last bit
+      k *= f;
+      if (h + r >= heads) continue;
+      const uint64_t k2 = pair(k, k);
+      const float* weight = weights + out.i * p.head_dim;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) sum[r] += __shfl_xor_sync(~0u, sum[r], m);
+      for (int s = 0; s < kSlots; ++s) {
+        uint64_t y[2][4];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        float eps = A.eps;
-        // squares past fp32: the head is taken 2^-96 times as large, where eps is nothing
-        const bool large = !std::is_same<T, __half>::value && isinf(sum[r]);
-        if (__any_sync(~0u, large)) {
-          float again = 0.f;
-          const float f = large ? 0x1p-96f : 1.f;
+        for (int v = 0; v < 2; ++v) {
+          unpack(x[r][s][v], y[v]);
+          if (kFull || off[s][v] >= 0) {
 #pragma unroll
-          for (int s = 0; s < kSlots; ++s)
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                x[r][s][v][e] *= f;
-                again = fmaf(x[r][s][v][e], x[r][s][v][e], again);
-              }
-          for (int m = lanes >> 1; m > 0; m >>= 1) again += __shfl_xor_sync(~0u, again, m);
-          if (large) sum[r] = again, eps = 0.f;
+            for (int e = 0; e < 4; e += 2) {
+              const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(weight + off[s][v] + 2 * e);
+              y[v][e] = mul2(y[v][e], mul2(k2, w.x));
+              y[v][e + 1] = mul2(y[v][e + 1], mul2(k2, w.y));
+            }
+          }
         }
-        const float mean = fmaf(sum[r], 1.f / p.head_dim, eps);
-        float k = rsqrtf(mean);
-        if (sizeof(T) == 4) k = isinf(mean) ? 0.f : k * fmaf(-0.5f * mean * k, k, 1.5f);  // to the last bit
-        if (from + h + r >= to) continue;
+        if (kHalf) {
+          if (off[s][0] >= 0 && off[s][0] < rot) {
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
-          float y[2][8];
+            for (int e = 0; e < 4; ++e) {
+              const uint64_t a = y[0][e], b = y[1][e];
+              y[0][e] = fma2(mul2(b, sn[s][e]), minus, mul2(a, cs[s][e]));
+              y[1][e] = fma2(a, sn[s][e], mul2(b, cs[s][e]));
+            }
+          }
+        } else {
 #pragma unroll
           for (int v = 0; v < 2; ++v)
+            if (off[s][v] >= 0 && off[s][v] < rot) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[v][e] = x[r][s][v][e] * k * w[s][v][e];
-          if (kHalf) {
-            if (off[s][0] >= 0 && off[s][0] < rot) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float a = y[0][e], b = y[1][e];
-                y[0][e] = a * cs[s][e].x - b * cs[s][e].y;
-                y[1][e] = b * cs[s][e].x + a * cs[s][e].y;
+              for (int e = 0; e < 4; ++e) {
+                const float2 z = split(y[v][e]);
+                const float2 c2 = split(cs[s][2 * v + e / 2]), s2 = split(sn[s][2 * v + e / 2]);
+                const float c = e % 2 ? c2.y : c2.x, q = e % 2 ? s2.y : s2.x;
+                y[v][e] = pair(z.x * c - z.y * q, z.y * c + z.x * q);
               }
             }
-          } else {
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-              if (off[s][v] >= 0 && off[s][v] < rot) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float a = y[v][2 * e], b = y[v][2 * e + 1];
-                  const float2 c = cs[s][4 * v + e];
-                  y[v][2 * e] = a * c.x - b * c.y;
-                  y[v][2 * e + 1] = b * c.x + a * c.y;
-                }
-              }
-          }
-#pragma unroll
-          for (int v = 0; v < 2; ++v)
-            if (off[s][v] >= 0) store8(out + (h + r) * A.out_hs + off[s][v], y[v]);
         }
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          if (kFull || off[s][v] >= 0) store8(out.at + off[s][v], y[v]);
       }
+      step<true>(p, &out, t);
     }
   }
 }
 
-template <typename T>
-cudaError_t launch(const NormArgs& a, int per_lane, cudaStream_t stream) {
-  const int64_t threads = static_cast<int64_t>(a.num_tokens) * a.groups_per_token << a.lanes_log2;
-  // few threads: small CTAs, on many SMs
-  const int block = threads < 152 * kThreads ? 64 : kThreads;
-  const unsigned grid = static_cast<unsigned>((threads + block - 1) / block);
-  if (a.rope.layout == RIMURU_ROPE_HALF) {
-    if (per_lane == 1) norm_rope_kernel<T, true, 1><<<grid, block, 0, stream>>>(a);
-    else norm_rope_kernel<T, true, 2><<<grid, block, 0, stream>>>(a);
+template <typename T, bool kHalf>
+cudaError_t launch_layout(const NormArgs& a, int per_lane, dim3 grid, int block, int smem, cudaStream_t stream) {
+  const bool full = a.head_dim == 16 * (per_lane << a.lanes_log2);
+  if (per_lane == 1) {
+    if (full) norm_rope_kernel<T, kHalf, 1, true><<<grid, block, smem, stream>>>(a);
+    else norm_rope_kernel<T, kHalf, 1, false><<<grid, block, smem, stream>>>(a);
   } else {
-    if (per_lane == 1) norm_rope_kernel<T, false, 1><<<grid, block, 0, stream>>>(a);
-    else norm_rope_kernel<T, false, 2><<<grid, block, 0, stream>>>(a);
+    if (full) norm_rope_kernel<T, kHalf, 2, true><<<grid, block, smem, stream>>>(a);
+    else norm_rope_kernel<T, kHalf, 2, false><<<grid, block, smem, stream>>>(a);
   }
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch(NormArgs a, int per_lane, int heads, int sms, cudaStream_t stream) {
+  // A group takes several heads of its token where that leaves 512 threads an SM, else fewer, down
+  // to one; more groups pay for the prologue more often (8192 tokens of 18 heads of 256: 31.8 us,
+  // 35.8 with 1024 threads, 39.1 with 3072; 1000 tokens 8.6, 9.9 and 17.5).
+  const int64_t want = 512ll * sms >> a.lanes_log2;  // groups
+  const int64_t per_token = std::max<int64_t>(1, std::min<int64_t>(std::min(heads, 32768), (want + a.num_tokens - 1) / a.num_tokens));
+  a.heads_per_group = static_cast<int>((heads + per_token - 1) / per_token);
+  const int all = (heads + a.heads_per_group - 1) / a.heads_per_group;  // groups of a token
+  // few threads: small CTAs, on many SMs
+  const int most = (static_cast<int64_t>(a.num_tokens) * all << a.lanes_log2) < static_cast<int64_t>(sms) * kThreads ? 64 : kThreads;
+  const int fit = std::max(1, most >> a.lanes_log2);  // groups of a CTA
+  a.groups = std::min(all, fit);
+  a.groups_mul = 65536 / a.groups + 1;  // exact for g < 256
+  a.tokens = std::max(1, fit / a.groups);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.num_tokens) + a.tokens - 1) / a.tokens), (all + a.groups - 1) / a.groups);
+  const int block = (((a.tokens * a.groups) << a.lanes_log2) + 31) / 32 * 32;
+  const int smem = kMaxArrays * a.head_dim * static_cast<int>(sizeof(float)) +
+                   a.tokens * a.rope.pairs * static_cast<int>(sizeof(float2));
+  return a.rope.layout == RIMURU_ROPE_HALF ? launch_layout<T, true>(a, per_lane, grid, block, smem, stream)
+                                           : launch_layout<T, false>(a, per_lane, grid, block, smem, stream);
 }
 
 }  // namespace
@@ -326,20 +442,15 @@ extern "C" int rimuru_norm_rope_apply(rimuru_rope_t rope, const int32_t* positio
   a.slots = a.turn_slots + (vectors - 2 * a.turn_slots + 1) / 2;
   while ((1 << a.lanes_log2) < a.slots && a.lanes_log2 < 5) ++a.lanes_log2;
   const int per_lane = a.slots > 32 ? 2 : 1;
-  // A group takes all heads of its token when that leaves 512 threads an SM, else fewer
-  // (the angles are then computed by several groups).
   int sms = 0, dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("device attributes", e));
-  const int64_t want = 512ll * sms >> a.lanes_log2;  // groups
-  const int64_t per_token = std::max<int64_t>(1, std::min<int64_t>(heads, want / num_tokens));
-  a.heads_per_group = static_cast<int>((heads + per_token - 1) / per_token);
-  a.groups_per_token = static_cast<int>((heads + a.heads_per_group - 1) / a.heads_per_group);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  e = in[0].dtype == RIMURU_BF16  ? launch<__nv_bfloat16>(a, per_lane, s)
-      : in[0].dtype == RIMURU_F16 ? launch<__half>(a, per_lane, s)
-                                  : launch<float>(a, per_lane, s);
+  const int n = static_cast<int>(heads);
+  e = in[0].dtype == RIMURU_BF16  ? launch<__nv_bfloat16>(a, per_lane, n, sms, s)
+      : in[0].dtype == RIMURU_F16 ? launch<__half>(a, per_lane, n, sms, s)
+                                  : launch<float>(a, per_lane, n, sms, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("norm launch", e));
   return RIMURU_OK;
 }
