@@ -34,8 +34,9 @@ __global__ void __launch_bounds__(kStepThreads) linear_steps_kernel(const __grid
   constexpr int kWarps = kStepThreads / 32;
   constexpr int kSums = kWarps;                  // partial sums of a column that meet in shared memory
   static_assert(kLanes <= 32 && kRows >= 1, "");
-  __shared__ float qs[kStepTokens][kKey], ks[kStepTokens][kKey], vs[kStepTokens][kCols], decay[kStepTokens];
-  __shared__ float sums[kStepTokens][kSums][kCols];
+  __shared__ alignas(16) float qs[kStepTokens][kKey], ks[kStepTokens][kKey], vs[kStepTokens][kCols];
+  __shared__ float decay[kStepTokens];
+  __shared__ alignas(16) float sums[kStepTokens][kSums][kCols];
   const int slices = a.value_dim / kCols;
   const int unit = blockIdx.x / slices, col0 = (blockIdx.x - unit * slices) * kCols;
   const int b = unit / a.heads, h = unit - b * a.heads;
@@ -245,9 +246,9 @@ extern "C" int rimuru_linear_attention(rimuru_view_t view, const rimuru_heads* q
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int dtype = num_tokens > 0 ? q->dtype : RIMURU_BF16;
   // One by one a token costs about 0.6 us, a chunk of 64 with its start several us.
-  const cudaError_t e = max_new <= kStepsMost
-                            ? launch_linear_steps(a, dtype, s)
-                            : launch_linear_chunks(a, cut_of(v, num_seqs, num_tokens, max_new), workspace, dtype, s);
+  if (max_new > kStepsMost)
+    return launch_linear_chunks(a, cut_of(v, num_seqs, num_tokens, max_new), workspace, dtype, s);
+  const cudaError_t e = launch_linear_steps(a, dtype, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("linear attention launch", e));
   return RIMURU_OK;
 }

@@ -61,6 +61,7 @@ __device__ __forceinline__ LinearSeq linear_seq(const LinearArgs& a, int b, bool
 }
 
 cudaError_t launch_linear_steps(const LinearArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearCut& cut, void* workspace, int dtype, cudaStream_t s);
+// Makes its own message; returns a rimuru status.
+int launch_linear_chunks(const LinearArgs& a, const LinearCut& cut, void* workspace, int dtype, cudaStream_t s);
 
 }  // namespace rimuru

@@ -12,7 +12,7 @@
 //   update  V^T Kd         Kd = decayed keys, three bf16 parts: an fp32 number exactly
 // S^T itself stays in the registers of eight warps in fp32 and takes each chunk's update
 // there: sums inside the tensor cores truncate, and over thousands of tokens that would
-// show.  f16 inputs are split into two bf16 parts as they are loaded, exactly.
+// show.  f16 inputs are split into two bf16 parts in shared memory, exactly.
 //
 // Differences G_i - G_j are taken on sums in 64-bit fixed point, so that a huge decay
 // early in a chunk costs the small ones after it nothing.
@@ -22,9 +22,11 @@
 // starts every piece from the states of the pieces before it.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <type_traits>
 
 #include "device.cuh"
+#include "kernels.h"
 #include "kv_attn.h"
 #include "linear.h"
 
@@ -37,19 +39,25 @@ constexpr int kC = 64;               // tokens of a chunk
 constexpr uint32_t kBlock = 8192;    // 64 rows of 128 bytes, swizzled
 constexpr int kGates = 4;            // chunks whose decays are ready
 constexpr int kThreads = 768;
-constexpr int kStateRegs = 112, kProductRegs = 64, kOutRegs = 72, kOtherRegs = 56;
+constexpr int kStateRegs = 104, kProductRegs = 72, kOutRegs = 72, kOtherRegs = 56;
 static_assert((2 * kStateRegs + 2 * kProductRegs + kOutRegs + kOtherRegs) * 128 <= 80 * kThreads, "");
 
-struct Gate {
+struct alignas(16) Gate {  // read four numbers at a time
   float2 sum[kC];   // G in two parts whose differences are exact, log2
+  float row[kC], col[kC];  // scale * exp(G - G_middle), exp(G_middle - G)
   float before[kC]; // scale * exp(G)
-  float after[kC];  // exp(G_last - G), 0 past the chunk's tokens
+  float after[kC];  // exp(G_last - G)
   float all;        // exp(G_last)
+  int wide;         // G spans too much for row * col: decays come from `sum`
+  int pad[2];
 };
+
+static_assert(sizeof(Gate) % 16 == 0 && offsetof(Gate, col) % 16 == 0 && offsetof(Gate, before) % 16 == 0, "");
 
 struct ChunkShared {
   Gate gate[kGates];
   uint64_t full[2], empty[2];             // loaded tiles
+  uint64_t raw;                           // f16: tiles before they are split
   uint64_t gate_full[kGates], gate_empty[kGates];
   uint64_t score_full[2], score_empty[2];
   uint64_t key_full[2], key_empty[2];     // decayed keys
@@ -77,6 +85,7 @@ struct Cfg {
 
 struct ChunkArgs {
   LinearArgs l;
+  int q_one, k_one, v_one;  // heads that lie on one another (a stride of 0)
   int piece, units;
   float* states;  // [pieces][heads][key_dim][value_dim]: what pieces add, sequences' first ones whole
   float* firsts;  // [num_seqs][heads][...]: states before sequences that are cut
@@ -161,10 +170,6 @@ __device__ __forceinline__ void umma_f16_lo(uint32_t d_tmem, uint32_t a_lo, uint
       "r"(a_lo), "r"(b_lo), "r"(accumulate), "n"(kAHi), "n"(kBHi), "n"(kIdesc)
       : "memory");
 }
-// 16 bytes from global memory, or zeros where `real` is false (nothing is read).
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -172,11 +177,46 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // 16-byte piece `c` of row r in a swizzled block of 128-byte rows.
 __device__ __forceinline__ uint32_t place(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_bf16x2(lo, hi);
+  }
+}
 // The upper halves of two numbers as a pair of bf16: what is below is cut off.
 __device__ __forceinline__ uint32_t tops(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 __device__ __forceinline__ float top(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+
+// Two numbers less their upper halves.
+__device__ __forceinline__ uint64_t below(uint64_t x) {
+  const float2 f = split(x);
+  return fma2(pair(top(f.x), top(f.y)), pair(-1.f, -1.f), x);
+}
+// That, as a pair of bf16.
+__device__ __forceinline__ uint32_t rest(uint64_t x) {
+  const float2 r = split(below(x));
+  return pack_bf16x2(r.x, r.y);
+}
+__device__ __forceinline__ uint32_t tops(uint64_t x) { return tops(split(x).x, split(x).y); }
+
+// Eight f16 as two bf16 parts: their 11 bits are 8 and 3.
+__device__ __forceinline__ void split_f16(const uint4& w, uint4* hi, uint4* lo) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[i]));
+    h[i] = tops(f.x, f.y);
+    l[i] = tops(f.x - top(f.x), f.y - top(f.y));
+  }
+  *hi = make_uint4(h[0], h[1], h[2], h[3]);
+  *lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
 
 // Fixed point with 40 bits below the point.
 __device__ __forceinline__ int64_t fixed_log2(float g) {
@@ -186,16 +226,36 @@ __device__ __forceinline__ int64_t fixed_log2(float g) {
   const float rest = fmaf(g, kHi, -x) + g * kLo;
   return __float2ll_rn(x * 0x1p40f) + __float2ll_rn(rest * 0x1p40f);
 }
-__device__ __forceinline__ float exp2_fixed(int64_t d) {
-  const int64_t n = (d + (1ll << 39)) >> 40;
-  const float f = __ll2float_rn(d - (n << 40)) * 0x1p-40f;
-  return ldexpf(exp2f(f), static_cast<int>(n));
+// In two parts: a multiple of 2^-6 below 2^17, and what is left, below 2^-6.
+__device__ __forceinline__ float2 parts_of(int64_t G) {
+  return make_float2(__int2float_rn(static_cast<int>(G >> 34)) * 0x1p-6f,
+                     __uint2float_rn(static_cast<uint32_t>(static_cast<uint64_t>(G) >> 2)) * 0x1p-38f);
+}
+// 2^(a - b), of numbers in parts: the first ones' difference is exact.
+__device__ __forceinline__ float exp2_of(float2 a, float2 b) {
+  const float hi = a.x - b.x, n = rintf(hi);
+  const float f = (hi - n) + (a.y - b.y);
+  const int e = static_cast<int>(fminf(fmaxf(n, -127.f), 128.f)) + 127;
+  // 2^f as its power series up to f^8, |f| <= 0.52: the rest is below 2^-31.  A chunk's whole decay
+  // meets the state once a chunk, and the instruction's 2^-22 would add up.
+  float y = 1.321548679e-6f;
+  y = fmaf(y, f, 1.525273380e-5f);
+  y = fmaf(y, f, 1.540353039e-4f);
+  y = fmaf(y, f, 1.333355815e-3f);
+  y = fmaf(y, f, 9.618129108e-3f);
+  y = fmaf(y, f, 5.550410866e-2f);
+  y = fmaf(y, f, 2.402265070e-1f);
+  y = fmaf(y, f, 6.931471806e-1f);
+  return fmaf(y, f, 1.f) * __int_as_float(e << 23);
 }
 
 template <typename T, int kDk, int kDv, bool kOut>
-__global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_constant__ ChunkArgs p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_chunk_kernel(const __grid_constant__ ChunkArgs p, const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<T, kDk, kDv>;
   constexpr int kStages = C::kStages, kIn = C::kIn;
+  constexpr int kKeyWarps = kOut ? 4 : 12;  // the first kernel has no outputs to make
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ ChunkShared sh_;
@@ -206,17 +266,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->full[i], 64);
-      mbar_init(&sh->empty[i], 1 + 4);   // the MMAs, the warps that decay keys
+      mbar_init(&sh->full[i], kIn == 1 ? 1 : 2 + kKeyWarps);
+      mbar_init(&sh->empty[i], 1 + kKeyWarps);  // the MMAs, the warps that decay keys
       mbar_init(&sh->score_full[i], 1);
       mbar_init(&sh->score_empty[i], 4);
-      mbar_init(&sh->key_full[i], 4);
+      mbar_init(&sh->key_full[i], kKeyWarps);
       mbar_init(&sh->key_empty[i], 1);
     }
     for (int i = 0; i < kGates; ++i) {
       mbar_init(&sh->gate_full[i], 1);
-      mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + 4 + 4 : 8 + 4);
+      mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + 4 + kKeyWarps : 8 + kKeyWarps);
     }
+    mbar_init(&sh->raw, 1);
     mbar_init(&sh->p_full, 4);
     mbar_init(&sh->p_empty, 1);
     mbar_init(&sh->state_full, 8);
@@ -253,60 +314,191 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   Unit x;
   uint32_t it = 0;  // chunks so far
 
+  const auto products = [&]() {
+    // P: a thread has row i (token i) and columns [32 half, 32 half + 32)
+    const int quad = warp & 3, half = (warp - 8) >> 2, i = quad * 32 + lane;
+    const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kScore + 32 * half;
+    uint8_t* dst = smem + C::kPAt;
+    while (ok && walk.next(p, &x)) {
+      for (int c = 0; ok && c < x.n; c += kC, ++it) {
+        const uint32_t slot = it % kGates, buffer = it & 1u;
+        wait(&sh->gate_full[slot], it / kGates);
+        wait(&sh->score_full[buffer], it >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[32];
+        tmem_ld32(at + 64 * buffer, s);
+        tmem_ld_wait32(s);
+        tc_fence_before();
+        arrive(&sh->score_empty[buffer]);
+        const Gate& t = sh->gate[slot];
+        if (half > quad) {  // all columns are later tokens
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = 0u;
+        } else if (!t.wide) {
+          const uint64_t mine = pair(t.row[i], t.row[i]);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&t.col[32 * half + j]);
+            const float2 y0 = split(mul2(pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), mul2(f.x, mine)));
+            const float2 y1 = split(mul2(pair(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), mul2(f.y, mine)));
+            s[j] = __float_as_uint(y0.x), s[j + 1] = __float_as_uint(y0.y);
+            s[j + 2] = __float_as_uint(y1.x), s[j + 3] = __float_as_uint(y1.y);
+          }
+        } else {
+          const float2 mine = t.sum[i];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float2 other = t.sum[32 * half + j];
+            const float f = ex2((mine.x - other.x) + (mine.y - other.y));
+            s[j] = __float_as_uint(__uint_as_float(s[j]) * (f * a.scale));
+          }
+        }
+        if (half == quad) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = j <= lane ? s[j] : 0u;
+        }
+        arrive(&sh->gate_empty[slot]);
+        wait(&sh->p_empty, it ^ 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a0 = __uint_as_float(s[8 * v + 2 * e]), a1 = __uint_as_float(s[8 * v + 2 * e + 1]);
+            hi[e] = tops(a0, a1);
+            lo[e] = rest(pair(a0, a1));
+          }
+          const uint32_t o = place(i, 4 * half + v);
+          *reinterpret_cast<uint4*>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(dst + kBlock + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        arrive(&sh->p_full);
+      }
+    }
+  };
+  const auto keys = [&](int which) {
+    // decayed keys, by vectors of eight
+    const int tid = which * 32 + lane;
+    constexpr int kVec = kDk / 8, kStep = 32 * kKeyWarps / kVec;
+    const int col = tid % kVec, r0 = tid / kVec;
+    const uint32_t from = kBlock + col / 8 * (2 * kBlock), to = C::kKeyAt + col / 8 * kBlock;
+    while (ok && walk.next(p, &x)) {
+      for (int c = 0; ok && c < x.n; c += kC, ++it) {
+        const uint32_t slot = it % kGates, stage = it % kStages, buffer = it & 1u;
+        wait(&sh->gate_full[slot], it / kGates);
+        if (kIn == 1) wait(&sh->full[stage], it / kStages);
+        else wait(&sh->raw, it);
+        wait(&sh->key_empty[buffer], (it >> 1) ^ 1u);
+        if (!ok) break;
+        const Gate& t = sh->gate[slot];
+        const int n = min(kC, x.n - c);
+        uint8_t* src = smem + stage * C::kStage + from;
+        uint8_t* dst = smem + to + buffer * 3 * C::kKeyPart;
+#pragma unroll 2
+        for (int r = r0; r < kC; r += kStep) {
+          const uint32_t o = place(r, col & 7);
+          const uint64_t w2 = pair(t.after[r], t.after[r]);
+          uint4 h = *reinterpret_cast<const uint4*>(src + o);
+          if (r >= n) h = make_uint4(0, 0, 0, 0);
+          uint32_t part[3][4];
+          const uint32_t in[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint64_t y;
+            if constexpr (kIn == 2) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[e]));
+              y = pair(f.x, f.y);
+            } else {
+              y = pair(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u));
+            }
+            y = mul2(y, w2);
+            part[0][e] = tops(y);
+            y = below(y);
+            part[1][e] = tops(y);
+            part[2][e] = tops(below(y));
+          }
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint4*>(dst + k * C::kKeyPart + o) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
+          if (kIn == 2) {
+            uint4 lo;
+            split_f16(h, &h, &lo);
+            *reinterpret_cast<uint4*>(src + o) = h;
+            *reinterpret_cast<uint4*>(src + C::kQk + o) = lo;
+          }
+        }
+        if (kIn == 1 && n < kC) {  // values past the piece: 0 times what they hold may be NaN
+          uint8_t* v = smem + stage * C::kStage + kIn * C::kQk;
+          for (int i = tid; i < (kC - n) * 8 * C::kVb; i += 32 * kKeyWarps) {
+            const int b = i / ((kC - n) * 8), k = i - b * ((kC - n) * 8);
+            *reinterpret_cast<uint4*>(v + b * kBlock + n * 128 + 16 * k) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        arrive(&sh->key_full[buffer]);
+        if (lane == 0) {
+          if (kIn == 2) mbar_arrive(&sh->full[stage]);
+          mbar_arrive(&sh->empty[stage]);
+          mbar_arrive(&sh->gate_empty[slot]);
+        }
+      }
+    }
+  };
+
   if (warp >= 20) {
     regs_down<kOtherRegs>();
     if (warp >= 22) {
       // ------------------------------------------------------------------ loads
-      const int tid = threadIdx.x - 22 * 32;
-      while (ok && walk.next(p, &x)) {
-        const T* q = static_cast<const T*>(a.q) + x.row * a.q_ts + x.h / a.per_key_head * a.q_hs;
-        const T* k = static_cast<const T*>(a.k) + x.row * a.k_ts + x.h / a.per_key_head * a.k_hs;
-        const T* v = static_cast<const T*>(a.v) + x.row * a.v_ts + x.h * a.v_hs;
+      // Rows past the piece come along: their outputs are not written, their scores and decayed
+      // keys are replaced by zeros, and the warps that decay keys clear their values.
+      while ((kIn == 2 || warp == 22) && ok && walk.next(p, &x)) {
+        const int hq = p.q_one ? 0 : x.h / a.per_key_head, hk = p.k_one ? 0 : x.h / a.per_key_head;
+        const int hv = p.v_one ? 0 : x.h;
         for (int c = 0; ok && c < x.n; c += kC, ++it) {
           const uint32_t stage = it % kStages;
+          uint8_t* base = smem + stage * C::kStage;
+          uint64_t* bar = kIn == 1 ? &sh->full[stage] : &sh->raw;
           wait(&sh->empty[stage], (it / kStages) ^ 1u);
           if (!ok) break;
-          const int n = min(kC, x.n - c);
-          uint8_t* base = smem + stage * C::kStage;
-          // rows of `src` into blocks `pitch` bytes apart; parts lie `part` bytes apart
-          const auto tile = [&](const T* src, int64_t ts, int vectors, uint8_t* dst, uint32_t pitch, uint32_t part) {
-            const int per = 64 / vectors;  // rows of a turn
-            const int col = tid % vectors, r0 = tid / vectors;
-            dst += col / 8 * pitch;
-#pragma unroll 8
-            for (int r = r0; r < kC; r += per) {
-              const T* from = src + (c + r) * ts + 8 * col;
-              const uint32_t at = place(r, col & 7);
-              if (kIn == 1) {
-                cp_async16_or_zero(smem_u32(dst + at), r < n ? from : src, r < n);
-              } else {
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (r < n) w = ld_nc_na_v4(from);
-                uint32_t hi[4], lo[4];
-                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+          if (warp == 22 && elect_one()) {
+            const uint64_t pol = policy_evict_normal();
+            const int row = static_cast<int>(x.row) + c;
+            mbar_arrive_expect_tx(bar, ((kOut ? 2 : 1) * C::kKb + C::kVb) * kBlock);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[i]));
-                  hi[i] = tops(f.x, f.y);
-                  lo[i] = tops(f.x - top(f.x), f.y - top(f.y));
-                }
-                *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(dst + part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              }
+            for (int b = 0; b < C::kKb; ++b) {
+              tma_load_3d(base + (2 * b + 1) * kBlock, &tm_k, bar, 64 * b, hk, row, pol);
+              if (kOut) tma_load_3d(base + 2 * b * kBlock, &tm_q, bar, 64 * b, hq, row, pol);
             }
-          };
-          tile(k, a.k_ts, kDk / 8, base + kBlock, 2 * kBlock, C::kQk);
-          if (kOut) tile(q, a.q_ts, kDk / 8, base, 2 * kBlock, C::kQk);
-          tile(v, a.v_ts, kDv / 8, base + kIn * C::kQk, kBlock, C::kV);
-          if (kIn == 1) {
-            cp_async_arrive_noinc(&sh->full[stage]);
-          } else {
+#pragma unroll
+            for (int b = 0; b < C::kVb; ++b) tma_load_3d(base + kIn * C::kQk + b * kBlock, &tm_v, bar, 64 * b, hv, row, pol);
+          }
+          __syncwarp();
+          if (kIn == 2) {
+            // queries and values into their parts; keys are split where they are decayed
+            wait(&sh->raw, it);
+            if (!ok) break;
+            const int n = min(kC, x.n - c), tid = threadIdx.x - 22 * 32;
+            const auto split = [&](uint8_t* dst, uint32_t part) {
+#pragma unroll 4
+              for (int v = tid; v < static_cast<int>(kBlock / 16); v += 64) {
+                uint4* at = reinterpret_cast<uint4*>(dst + 16 * v);
+                uint4 lo, hi = *at;
+                if (v / 8 >= n) hi = make_uint4(0, 0, 0, 0);
+                split_f16(hi, &hi, &lo);
+                *at = hi;
+                *reinterpret_cast<uint4*>(dst + part + 16 * v) = lo;
+              }
+            };
+            for (int b = 0; kOut && b < C::kKb; ++b) split(base + 2 * b * kBlock, C::kQk);
+            for (int b = 0; b < C::kVb; ++b) split(base + kIn * C::kQk + b * kBlock, C::kV);
             fence_proxy_async_smem();
-            mbar_arrive(&sh->full[stage]);
+            arrive(&sh->full[stage]);
           }
         }
       }
-      cp_async_wait_all();
     } else if (warp == 21) {
       // ------------------------------------------------------------------ decays
       while (ok && walk.next(p, &x)) {
@@ -314,46 +506,58 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         constexpr int64_t kFar = 1ll << 53;  // 2^8192 either way is 0 or infinity
         int64_t total = 0;
         bool nan = false;
+        const int i = 2 * lane;
+        float g0 = i < x.n ? g[i * a.g_ts] : 0.f, g1 = i + 1 < x.n ? g[(i + 1) * a.g_ts] : 0.f;
         for (int c = 0; ok && c < x.n; c += kC, ++it) {
           const uint32_t slot = it % kGates;
-          const int n = min(kC, x.n - c), i = 2 * lane;
-          const float g0 = i < n ? g[(c + i) * a.g_ts] : 0.f, g1 = i + 1 < n ? g[(c + i + 1) * a.g_ts] : 0.f;
-          const int64_t x1 = fixed_log2(g1);
-          int64_t G1 = fixed_log2(g0) + x1;
+          const float now0 = g0, now1 = g1;
+          const int next = c + kC + i;  // loaded before they are needed
+          g0 = next < x.n ? g[next * a.g_ts] : 0.f;
+          g1 = next + 1 < x.n ? g[(next + 1) * a.g_ts] : 0.f;
+          const int64_t x1 = fixed_log2(now1);
+          int64_t G1 = fixed_log2(now0) + x1;
 #pragma unroll
           for (int m = 1; m < 32; m <<= 1) {
             const int64_t up = __shfl_up_sync(0xffffffffu, G1, m);
             if (lane >= m) G1 += up;
           }
-          const int64_t G0 = G1 - x1, last = __shfl_sync(0xffffffffu, G1, 31);
-          const uint32_t bad0 = __ballot_sync(0xffffffffu, g0 != g0), bad1 = __ballot_sync(0xffffffffu, g0 != g0 || g1 != g1);
+          const int64_t last = __shfl_sync(0xffffffffu, G1, 31);
+          const uint32_t bad0 = __ballot_sync(0xffffffffu, now0 != now0);
+          const uint32_t bad1 = __ballot_sync(0xffffffffu, now0 != now0 || now1 != now1);
           // a NaN counts for every token from its own on
           const uint32_t below = (2u << lane) - 1u;
           const bool nan0 = ((bad0 & below) | (bad1 & (below >> 1))) != 0, nan1 = (bad1 & below) != 0;
           const float none = __int_as_float(0x7FFFFFFF);
+          float2 p0 = parts_of(G1 - x1), p1 = parts_of(G1);
+          const float2 end = parts_of(last), zero = make_float2(0.f, 0.f);
+          const float after0 = exp2_of(end, p0), after1 = exp2_of(end, p1), all = exp2_of(end, zero);
           wait(&sh->gate_empty[slot], (it / kGates) ^ 1u);
           if (!ok) break;
           Gate& t = sh->gate[slot];
           if (kOut) {
-            const auto parts = [&](int64_t G, bool is_nan) {
-              return make_float2(is_nan ? none : __int2float_rn(static_cast<int>(G >> 34)) * 0x1p-6f,
-                                 __ll2float_rn(G & ((1ll << 34) - 1)) * 0x1p-40f);
-            };
-            t.sum[i] = parts(G0, nan0);
-            t.sum[i + 1] = parts(G1, nan1);
-            t.before[i] = nan0 ? none : exp2_fixed(G0) * a.scale;
-            t.before[i + 1] = nan1 ? none : exp2_fixed(G1) * a.scale;
+            if (nan0) p0.x = none;
+            if (nan1) p1.x = none;
+            *reinterpret_cast<float4*>(&t.sum[i]) = make_float4(p0.x, p0.y, p1.x, p1.y);
+            *reinterpret_cast<float2*>(&t.before[i]) = make_float2(exp2_of(p0, zero) * a.scale, exp2_of(p1, zero) * a.scale);
+            // products of exp(G - middle) and its inverse do while these stay within 2^40
+            const float2 middle = parts_of(last / 2);
+            const bool far = !(fabsf(p0.x - middle.x) <= 40.f && fabsf(p1.x - middle.x) <= 40.f);
+            const bool wide = __any_sync(0xffffffffu, far);
+            if (lane == 0) t.wide = wide;
+            *reinterpret_cast<float2*>(&t.row[i]) = make_float2(exp2_of(p0, middle) * a.scale, exp2_of(p1, middle) * a.scale);
+            *reinterpret_cast<float2*>(&t.col[i]) = make_float2(exp2_of(middle, p0), exp2_of(middle, p1));
           }
-          t.after[i] = i < n ? exp2_fixed(last - G0) : 0.f;
-          t.after[i + 1] = i + 1 < n ? exp2_fixed(last - G1) : 0.f;
-          if (lane == 0) t.all = bad1 ? none : exp2_fixed(last);
+          *reinterpret_cast<float2*>(&t.after[i]) = make_float2(after0, after1);
+          if (lane == 0) t.all = bad1 ? none : all;
           total = min(max(total + last, -kFar), kFar);
           nan |= bad1 != 0;
           arrive(&sh->gate_full[slot]);
         }
-        if (!kOut && lane == 0)
+        if (!kOut && lane == 0) {
+          const int64_t far = 1ll << 50;  // the parts hold 2^17
           p.decays[static_cast<int64_t>(x.slot) * a.heads + x.h] =
-              nan ? __int_as_float(0x7FFFFFFF) : exp2_fixed(total);
+              nan ? __int_as_float(0x7FFFFFFF) : exp2_of(parts_of(min(max(total, -far), far)), make_float2(0.f, 0.f));
+        }
       }
     } else {
       // ------------------------------------------------------------------ MMAs
@@ -372,7 +576,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         wait(&sh->score_empty[buffer], (scored >> 1) ^ 1u);
         tc_fence_after();
         if (ok && elect_one()) {
-          fence_proxy_async_smem();
           const uint32_t q0 = base_lo + stage * (C::kStage / 16), k0 = q0 + kBlock / 16;
           uint32_t more = 0;
 #pragma unroll
@@ -401,7 +604,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           wait(&sh->update_empty, it ^ 1u);
           tc_fence_after();
           if (ok && elect_one()) {
-            if (!kOut) fence_proxy_async_smem();
             const uint32_t k0 = cols_lo + (C::kKeyAt + buffer * 3 * C::kKeyPart) / 16;
             uint32_t more = 0;
             // small parts first: what the sum cuts off is then small too
@@ -473,142 +675,67 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
   } else if (warp >= 16) {
     // -------------------------------------------------------------------- outputs
     regs_down<kOutRegs>();
+    if (!kOut) keys(warp - 8);
     const int quad = warp & 3, col = quad * 32 + lane;
     const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     while (kOut && ok && walk.next(p, &x, warp == 16 && lane == 0)) {
-      T* out = static_cast<T*>(a.out) + x.row * a.o_ts + x.h * a.o_hs + col;
+      // Lanes are value columns.  Four neighbouring lanes change places for four tokens, so that each
+      // writes four columns of one token.
+      T* out = static_cast<T*>(a.out) + (x.row + (lane & 3)) * a.o_ts + x.h * a.o_hs + (col & ~3);
       for (int c = 0; ok && c < x.n; c += kC, ++it) {
         const uint32_t slot = it % kGates;
-        const int n = min(kC, x.n - c);
+        const int n = min(kC, x.n - c) - (lane & 3);
         wait(&sh->gate_full[slot], it / kGates);
         wait(&sh->out_full, it);
         if (!ok) break;
         tc_fence_after();
         const Gate& t = sh->gate[slot];
 #pragma unroll 1
-        for (int j0 = 0; j0 < kC; j0 += 16) {
-          uint32_t u[16], w[16];
-          tmem_ld16(at + kInter + j0, u);
-          tmem_ld16(at + kIntra + j0, w);
-          tmem_ld_wait();
-          if (j0 + 16 == kC) {
-            tc_fence_before();
-            arrive(&sh->out_empty);
-          }
-          if (col < kDv) {
+        for (int h = 0; h < kC; h += 32) {
+          uint32_t y[16];  // pairs of columns
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float y = fmaf(t.before[j0 + j], __uint_as_float(u[j]), a.scale * __uint_as_float(w[j]));
-              if (j0 + j < n) {
-                T* o = out + (c + j0 + j) * a.o_ts;
-                if constexpr (kIn == 2) *o = __float2half_rn(y);
-                else *o = __float2bfloat16_rn(y);
-              }
+          for (int j0 = 0; j0 < 32; j0 += 16) {
+            uint32_t u[16], w[16];
+            tmem_ld16(at + kInter + h + j0, u);
+            tmem_ld16(at + kIntra + h + j0, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const ulonglong2 before = *reinterpret_cast<const ulonglong2*>(&t.before[h + j0 + j]);
+              const auto two = [](uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); };
+              const float2 f01 = split(fma2(before.x, two(u[j], u[j + 1]), two(w[j], w[j + 1])));
+              const float2 f23 = split(fma2(before.y, two(u[j + 2], u[j + 3]), two(w[j + 2], w[j + 3])));
+              const float f[4] = {f01.x, f01.y, f23.x, f23.y};
+              // even lanes take tokens 0 and 2, odd ones 1 and 3
+              const bool odd = lane & 1;
+              const float g0 = __shfl_xor_sync(0xffffffffu, odd ? f[0] : f[1], 1);
+              const float g1 = __shfl_xor_sync(0xffffffffu, odd ? f[2] : f[3], 1);
+              y[(j0 + j) / 2] = odd ? pack<T>(g0, f[1]) : pack<T>(f[0], g0);
+              y[(j0 + j) / 2 + 1] = odd ? pack<T>(g1, f[3]) : pack<T>(f[2], g1);
             }
           }
+          if (h + 32 == kC) {
+            tc_fence_before();
+            arrive(&sh->out_empty);
+            if (lane == 0) mbar_arrive(&sh->gate_empty[slot]);
+          }
+          T* o = out + (c + h) * a.o_ts;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            // the lower lanes of each four keep tokens 0 and 1, the upper ones 2 and 3
+            const bool up = lane & 2;
+            const uint32_t mine = up ? y[j / 2 + 1] : y[j / 2];
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? y[j / 2] : y[j / 2 + 1], 2);
+            if (col < kDv && h + j < n)
+              *reinterpret_cast<uint2*>(o + j * a.o_ts) = up ? make_uint2(other, mine) : make_uint2(mine, other);
+          }
         }
-        arrive(&sh->gate_empty[slot]);
       }
     }
   } else if (warp >= 8) {
     regs_down<kProductRegs>();
-    const int quad = warp & 3, half = (warp - 8) >> 2;
-    if (quad < 2) {
-      // ------------------------------------------------------------------ P
-      const int i = quad * 32 + lane;  // row: token i, columns [32 half, 32 half + 32)
-      const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kScore + 32 * half;
-      uint8_t* dst = smem + C::kPAt;
-      while (kOut && ok && walk.next(p, &x)) {
-        for (int c = 0; ok && c < x.n; c += kC, ++it) {
-          const uint32_t slot = it % kGates, buffer = it & 1u;
-          wait(&sh->gate_full[slot], it / kGates);
-          wait(&sh->score_full[buffer], it >> 1);
-          if (!ok) break;
-          tc_fence_after();
-          uint32_t s[32];
-          tmem_ld32(at + 64 * buffer, s);
-          tmem_ld_wait32(s);
-          tc_fence_before();
-          arrive(&sh->score_empty[buffer]);
-          const Gate& t = sh->gate[slot];
-          const float2 mine = t.sum[i];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 other = t.sum[32 * half + j];
-            const float f = ex2((mine.x - other.x) + (mine.y - other.y));
-            s[j] = 32 * half + j <= i ? __float_as_uint(__uint_as_float(s[j]) * f) : 0u;
-          }
-          arrive(&sh->gate_empty[slot]);
-          wait(&sh->p_empty, it ^ 1u);
-          if (!ok) break;
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a0 = __uint_as_float(s[8 * v + 2 * e]), a1 = __uint_as_float(s[8 * v + 2 * e + 1]);
-              hi[e] = tops(a0, a1);
-              lo[e] = pack_bf16x2(a0 - top(a0), a1 - top(a1));
-            }
-            const uint32_t o = place(i, 4 * half + v);
-            *reinterpret_cast<uint4*>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + kBlock + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-          fence_proxy_async_smem();
-          arrive(&sh->p_full);
-        }
-      }
-    } else {
-      // ------------------------------------------------------------------ decayed keys
-      const int tid = (half * 2 + quad - 2) * 32 + lane;  // of 128
-      constexpr int kVec = kDk / 8;
-      const int col = tid % kVec, r0 = tid / kVec;
-      const uint32_t from = kBlock + col / 8 * (2 * kBlock), to = C::kKeyAt + col / 8 * kBlock;
-      while (ok && walk.next(p, &x)) {
-        for (int c = 0; ok && c < x.n; c += kC, ++it) {
-          const uint32_t slot = it % kGates, stage = it % kStages, buffer = it & 1u;
-          wait(&sh->gate_full[slot], it / kGates);
-          wait(&sh->full[stage], it / kStages);
-          wait(&sh->key_empty[buffer], (it >> 1) ^ 1u);
-          if (!ok) break;
-          const Gate& t = sh->gate[slot];
-          const uint8_t* src = smem + stage * C::kStage + from;
-          uint8_t* dst = smem + to + buffer * 3 * C::kKeyPart;
-#pragma unroll 2
-          for (int r = r0; r < kC; r += 128 / kVec) {
-            const uint32_t o = place(r, col & 7);
-            const float w = t.after[r];
-            const uint4 h = *reinterpret_cast<const uint4*>(src + o);
-            const uint4 l = kIn == 2 ? *reinterpret_cast<const uint4*>(src + C::kQk + o) : make_uint4(0, 0, 0, 0);
-            const uint32_t in[4] = {h.x, h.y, h.z, h.w}, in_lo[4] = {l.x, l.y, l.z, l.w};
-            uint32_t part[3][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x0 = __uint_as_float(in[e] << 16), x1 = __uint_as_float(in[e] & 0xFFFF0000u);
-              if (kIn == 2) {
-                x0 += __uint_as_float(in_lo[e] << 16);
-                x1 += __uint_as_float(in_lo[e] & 0xFFFF0000u);
-              }
-              x0 *= w, x1 *= w;
-              part[0][e] = tops(x0, x1);
-              x0 -= top(x0), x1 -= top(x1);
-              part[1][e] = tops(x0, x1);
-              x0 -= top(x0), x1 -= top(x1);
-              part[2][e] = tops(x0, x1);
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              *reinterpret_cast<uint4*>(dst + k * C::kKeyPart + o) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
-          }
-          fence_proxy_async_smem();
-          arrive(&sh->key_full[buffer]);
-          if (lane == 0) {
-            mbar_arrive(&sh->empty[stage]);
-            mbar_arrive(&sh->gate_empty[slot]);
-          }
-        }
-      }
-    }
+    if (kOut && (warp & 3) < 2) products();
+    else keys(kOut ? (warp - 8) / 4 * 2 + (warp & 1) : warp - 8);
   } else {
     // -------------------------------------------------------------------- states
     regs_up<kStateRegs>();
@@ -619,21 +746,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
     const int64_t mine = static_cast<int64_t>(wg) * kN * kDv + col;
     constexpr int64_t kState1 = static_cast<int64_t>(kDk) * kDv;
     while (ok && walk.next(p, &x, !kOut && warp == 0 && lane == 0)) {
-      float S[kN];
+      uint64_t S[kN / 2];  // pairs of key rows
       const auto load = [&](const float* src) {
 #pragma unroll
-        for (int d = 0; d < kN; ++d) S[d] = src && real ? src[mine + d * kDv] : 0.f;
+        for (int d = 0; d < kN; d += 2)
+          S[d / 2] = src && real ? pair(src[mine + d * kDv], src[mine + (d + 1) * kDv]) : 0ull;
       };
       const int64_t head = static_cast<int64_t>(x.h) * kState1;
+      const auto store = [&](float* dst) {
+#pragma unroll
+        for (int d = 0; d < kN; d += 2) {
+          const float2 y = split(S[d / 2]);
+          dst[mine + d * kDv] = y.x;
+          dst[mine + (d + 1) * kDv] = y.y;
+        }
+      };
       const auto slot_state = [&](int slot) { return p.states + (static_cast<int64_t>(slot) * a.heads + x.h) * kState1; };
       if (x.first) {
         float* copy = p.firsts + (static_cast<int64_t>(x.b) * a.heads + x.h) * kState1;
         // a sequence in pieces: its first kernel keeps the state, whose page the second may overwrite early
         load(!x.in ? nullptr : kOut && !x.last ? copy : x.in + head);
-        if (!kOut && x.in && real) {
-#pragma unroll
-          for (int d = 0; d < kN; ++d) copy[mine + d * kDv] = S[d];
-        }
+        if (!kOut && x.in && real) store(copy);
       } else if (kOut) {
         load(slot_state(x.b));
         for (int slot = a.num_seqs + x.seq0 / p.piece; slot < x.slot; ++slot) {
@@ -641,7 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
           const float* src = slot_state(slot);
           if (real) {
 #pragma unroll
-            for (int d = 0; d < kN; ++d) S[d] = fmaf(S[d], f, src[mine + d * kDv]);
+            for (int d = 0; d < kN; d += 2)
+              S[d / 2] = fma2(S[d / 2], pair(f, f), pair(src[mine + d * kDv], src[mine + (d + 1) * kDv]));
           }
         }
       } else {
@@ -658,9 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int d = 0; d < 16; ++d) {
-              const float s0 = S[d0 + 2 * d], s1 = S[d0 + 2 * d + 1];
-              hi[d] = tops(s0, s1);
-              lo[d] = pack_bf16x2(s0 - top(s0), s1 - top(s1));
+              hi[d] = tops(S[d0 / 2 + d]);
+              lo[d] = rest(S[d0 / 2 + d]);
             }
             tmem_st16(at + kState + (wg * kN + d0) / 2, hi);
             tmem_st16(at + kState + kDk / 2 + (wg * kN + d0) / 2, lo);
@@ -675,24 +808,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
         tc_fence_after();
         const float f = sh->gate[slot].all;
 #pragma unroll
-        for (int d0 = 0; d0 < kN; d0 += 16) {
-          uint32_t u[16];
-          tmem_ld16(at + kUpdate + wg * kN + d0, u);
-          tmem_ld_wait();
-          if (d0 + 16 == kN) {
+        for (int d0 = 0; d0 < kN; d0 += 32) {
+          uint32_t u[32];
+          tmem_ld32(at + kUpdate + wg * kN + d0, u);
+          tmem_ld_wait32(u);
+          if (d0 + 32 == kN) {
             tc_fence_before();
             arrive(&sh->update_empty);
           }
 #pragma unroll
-          for (int d = 0; d < 16; ++d) S[d0 + d] = fmaf(S[d0 + d], f, __uint_as_float(u[d]));
+          for (int d = 0; d < 32; d += 2)
+            S[(d0 + d) / 2] = fma2(S[(d0 + d) / 2], pair(f, f), pair(__uint_as_float(u[d]), __uint_as_float(u[d + 1])));
         }
         arrive(&sh->gate_empty[slot]);
       }
       float* dst = kOut ? (x.last ? x.out + head : nullptr) : slot_state(x.slot);
-      if (ok && dst && real) {
-#pragma unroll
-        for (int d = 0; d < kN; ++d) dst[mine + d * kDv] = S[d];
-      }
+      if (ok && dst && real) store(dst);
     }
   }
   if (!ok && lane == 0) {
@@ -706,27 +837,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_chunk_kernel(const __grid_
 }
 
 template <typename T, int kDk, int kDv, bool kOut>
-cudaError_t launch_one(const ChunkArgs& p, cudaStream_t s) {
+cudaError_t launch_one(const ChunkArgs& p, const CUtensorMap* tm, cudaStream_t s) {
   constexpr int smem = Cfg<T, kDk, kDv>::kSmem;
   auto* fn = linear_chunk_kernel<T, kDk, kDv, kOut>;
   static SmemOnce once;
   const cudaError_t e = once.set(reinterpret_cast<const void*>(fn), smem);
   if (e != cudaSuccess) return e;
-  fn<<<std::min(p.units, p.l.sms), kThreads, smem, s>>>(p);
+  fn<<<std::min(p.units, p.l.sms), kThreads, smem, s>>>(p, tm[0], tm[1], tm[2]);
   return cudaGetLastError();
 }
 template <typename T, int kDk, int kDv>
-cudaError_t launch(const ChunkArgs& p, cudaStream_t s) {
+cudaError_t launch(const ChunkArgs& p, const CUtensorMap* tm, cudaStream_t s) {
   if (p.piece > 0) {
-    const cudaError_t e = launch_one<T, kDk, kDv, false>(p, s);
+    const cudaError_t e = launch_one<T, kDk, kDv, false>(p, tm, s);
     if (e != cudaSuccess) return e;
   }
-  return launch_one<T, kDk, kDv, true>(p, s);
+  return launch_one<T, kDk, kDv, true>(p, tm, s);
 }
 template <typename T>
-cudaError_t launch_dims(const ChunkArgs& p, cudaStream_t s) {
-  if (p.l.key_dim == 128) return p.l.value_dim == 128 ? launch<T, 128, 128>(p, s) : launch<T, 128, 64>(p, s);
-  return p.l.value_dim == 128 ? launch<T, 64, 128>(p, s) : launch<T, 64, 64>(p, s);
+cudaError_t launch_dims(const ChunkArgs& p, const CUtensorMap* tm, cudaStream_t s) {
+  if (p.l.key_dim == 128) return p.l.value_dim == 128 ? launch<T, 128, 128>(p, tm, s) : launch<T, 128, 64>(p, tm, s);
+  return p.l.value_dim == 128 ? launch<T, 64, 128>(p, tm, s) : launch<T, 64, 64>(p, tm, s);
 }
 
 }  // namespace
@@ -758,7 +889,7 @@ LinearCut linear_cut(int heads, int key_dim, int value_dim, int sms, int num_seq
   return best;
 }
 
-cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearCut& cut, void* workspace, int dtype, cudaStream_t s) {
+int launch_linear_chunks(const LinearArgs& a, const LinearCut& cut, void* workspace, int dtype, cudaStream_t s) {
   ChunkArgs p{};
   p.l = a;
   p.piece = cut.piece;
@@ -767,7 +898,24 @@ cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearCut& cut, void
   p.states = static_cast<float*>(workspace);
   p.firsts = p.states + cut.pieces * state;
   p.decays = p.firsts + a.num_seqs * state;
-  return dtype == RIMURU_BF16 ? launch_dims<__nv_bfloat16>(p, s) : launch_dims<__half>(p, s);
+  CUtensorMap tm[3];
+  const int key_heads = a.heads / a.per_key_head;
+  const auto map = [&](CUtensorMap* m, const void* x, int64_t ts, int64_t hs, int heads, int dim, int* one) {
+    *one = heads == 1 || hs == 0;
+    if (ts == 0 || ts >= 1ll << 39 || hs >= 1ll << 39)
+      return fail(RIMURU_ERR_UNSUPPORTED, "token and head strides must be below 2^39, and tokens may not lie on one another");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(*one ? 1 : heads),
+                                static_cast<cuuint64_t>(a.num_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(*one ? dim : hs) * 2, static_cast<cuuint64_t>(ts) * 2};
+    const cuuint32_t box[3] = {64, 1, kC};
+    return make_bf16_map(m, const_cast<void*>(x), 3, dims, strides, box);
+  };
+  int st = map(&tm[0], a.q, a.q_ts, a.q_hs, key_heads, a.key_dim, &p.q_one);
+  if (st == RIMURU_OK) st = map(&tm[1], a.k, a.k_ts, a.k_hs, key_heads, a.key_dim, &p.k_one);
+  if (st == RIMURU_OK) st = map(&tm[2], a.v, a.v_ts, a.v_hs, a.heads, a.value_dim, &p.v_one);
+  if (st != RIMURU_OK) return st;
+  const cudaError_t e = dtype == RIMURU_BF16 ? launch_dims<__nv_bfloat16>(p, tm, s) : launch_dims<__half>(p, tm, s);
+  return e == cudaSuccess ? RIMURU_OK : fail(RIMURU_ERR_CUDA, kv_cuda_msg("linear attention launch", e));
 }
 
 }  // namespace rimuru
