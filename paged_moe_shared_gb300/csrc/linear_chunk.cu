@@ -39,6 +39,7 @@ constexpr int kC = 64;               // tokens of a chunk
 constexpr uint32_t kBlock = 8192;    // 64 rows of 128 bytes, swizzled
 constexpr int kGates = 4;            // chunks whose decays are ready
 constexpr int kThreads = 768;
+constexpr int kKeysByP = 16;         // keys of a chunk that the warps of P decay
 constexpr int kStateRegs = 104, kProductRegs = 72, kOutRegs = 72, kOtherRegs = 56;
 static_assert((2 * kStateRegs + 2 * kProductRegs + kOutRegs + kOtherRegs) * 128 <= 80 * kThreads, "");
 
@@ -56,8 +57,9 @@ static_assert(sizeof(Gate) % 16 == 0 && offsetof(Gate, col) % 16 == 0 && offseto
 
 struct ChunkShared {
   Gate gate[kGates];
-  uint64_t full[2], empty[2];             // loaded tiles
-  uint64_t raw;                           // f16: tiles before they are split
+  uint64_t full[2], empty[2];             // loaded queries and values (f16: all tiles, split)
+  uint64_t keys_full[2], keys_empty[2];   // loaded keys
+  uint64_t raw;                           // f16: all tiles before they are split
   uint64_t gate_full[kGates], gate_empty[kGates];
   uint64_t score_full[2], score_empty[2];
   uint64_t key_full[2], key_empty[2];     // decayed keys
@@ -105,7 +107,7 @@ struct Unit {
 };
 __device__ __forceinline__ Unit find_unit(const ChunkArgs& p, int u, bool record) {
   const LinearArgs& a = p.l;
-  Unit x;
+  Unit x{};
   x.slot = u / a.heads;
   x.h = u - x.slot * a.heads;
   int start;
@@ -192,17 +194,19 @@ __device__ __forceinline__ uint32_t tops(float lo, float hi) {
 }
 __device__ __forceinline__ float top(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
 
-// Two numbers less their upper halves.
-__device__ __forceinline__ uint64_t below(uint64_t x) {
-  const float2 f = split(x);
-  return fma2(pair(top(f.x), top(f.y)), pair(-1.f, -1.f), x);
+__device__ __forceinline__ uint32_t tops(uint64_t x) { return tops(split(x).x, split(x).y); }
+// Two bf16 as fp32.  The lower one moves up by a product, which is not the logic unit's work:
+// with the cutting of parts that has more to do than any other here.
+__device__ __forceinline__ uint64_t widen(uint32_t two) {
+  return pair(__uint_as_float(two * 65536u), __uint_as_float(two & 0xFFFF0000u));
 }
+// Two numbers less their upper halves.
+__device__ __forceinline__ uint64_t below(uint64_t x, uint32_t upper) { return fma2(widen(upper), pair(-1.f, -1.f), x); }
 // That, as a pair of bf16.
-__device__ __forceinline__ uint32_t rest(uint64_t x) {
-  const float2 r = split(below(x));
+__device__ __forceinline__ uint32_t rest(uint64_t x, uint32_t upper) {
+  const float2 r = split(below(x, upper));
   return pack_bf16x2(r.x, r.y);
 }
-__device__ __forceinline__ uint32_t tops(uint64_t x) { return tops(split(x).x, split(x).y); }
 
 // Eight f16 as two bf16 parts: their 11 bits are 8 and 3.
 __device__ __forceinline__ void split_f16(const uint4& w, uint4* hi, uint4* lo) {
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<T, kDk, kDv>;
   constexpr int kStages = C::kStages, kIn = C::kIn;
-  constexpr int kKeyWarps = kOut ? 4 : 12;  // the first kernel has no outputs to make
+  constexpr int kKeyWarps = kOut ? 8 : 12;  // the first kernel has no outputs to make
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ ChunkShared sh_;
@@ -266,8 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->full[i], kIn == 1 ? 1 : 2 + kKeyWarps);
-      mbar_init(&sh->empty[i], 1 + kKeyWarps);  // the MMAs, the warps that decay keys
+      mbar_init(&sh->full[i], kIn == 1 ? 1 : 12);  // f16: warps 8 to 19 split the tiles
+      mbar_init(&sh->empty[i], kOut ? 2 : 1);      // both MMA warps
+      mbar_init(&sh->keys_full[i], 1);
+      mbar_init(&sh->keys_empty[i], (kOut ? 1 : 0) + kKeyWarps);
       mbar_init(&sh->score_full[i], 1);
       mbar_init(&sh->score_empty[i], 4);
       mbar_init(&sh->key_full[i], kKeyWarps);
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kGates; ++i) {
       mbar_init(&sh->gate_full[i], 1);
-      mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + 4 + kKeyWarps : 8 + kKeyWarps);
+      mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + kKeyWarps : 8 + kKeyWarps);
     }
     mbar_init(&sh->raw, 1);
     mbar_init(&sh->p_full, 4);
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->update_empty, 8);
     mbar_init(&sh->out_full, 1);
     mbar_init(&sh->out_empty, 4);
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->drain, 2);
     sh->abort = 0;
     fence_barrier_init();
   }
@@ -311,192 +317,212 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(bar);
   };
   Walk<kOut> walk{-1};
-  Unit x;
+  Unit x{};
   uint32_t it = 0;  // chunks so far
 
+  // f16: eight rows of 16 bytes a turn, thread `tid` of `threads`; rows past `n` become zeros.
+  const auto split_block = [&](uint8_t* dst, uint32_t part, int n, int tid, int threads) {
+#pragma unroll 2
+    for (int v = tid; v < static_cast<int>(kBlock / 16); v += threads) {
+      uint4* at = reinterpret_cast<uint4*>(dst + 16 * v);
+      uint4 lo, hi = *at;
+      if (v / 8 >= n) hi = make_uint4(0, 0, 0, 0);
+      split_f16(hi, &hi, &lo);
+      *at = hi;
+      *reinterpret_cast<uint4*>(dst + part + 16 * v) = lo;
+    }
+  };
+  // Decayed keys of rows [r0, r1) of the chunk that begins at c, by vectors of eight.
+  constexpr int kVec = kDk / 8;
+  const auto decay_keys = [&](int c, int r0, int r1, int tid, int threads) {
+    const uint32_t slot = it % kGates, stage = it % kStages, buffer = it & 1u;
+    const int n = min(kC, x.n - c), col = tid % kVec;
+    const Gate& t = sh->gate[slot];
+    uint8_t* src = smem + stage * C::kStage + kBlock + col / 8 * (2 * kBlock);
+    uint8_t* dst = smem + C::kKeyAt + col / 8 * kBlock + buffer * 3 * C::kKeyPart;
+#pragma unroll 1
+    for (int r = r0 + tid / kVec; r < r1; r += threads / kVec) {
+      const uint32_t o = place(r, col & 7);
+      const uint64_t w2 = pair(t.after[r], t.after[r]);
+      uint4 h = *reinterpret_cast<const uint4*>(src + o);
+      if (r >= n) h = make_uint4(0, 0, 0, 0);
+      uint32_t part[3][4];
+      const uint32_t in[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint64_t y;
+        if constexpr (kIn == 2) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[e]));
+          y = pair(f.x, f.y);
+        } else {
+          y = widen(in[e]);
+        }
+        y = mul2(y, w2);
+        part[0][e] = tops(y);
+        y = below(y, part[0][e]);
+        part[1][e] = tops(y);
+        part[2][e] = tops(below(y, part[1][e]));
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint4*>(dst + k * C::kKeyPart + o) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
+      if (kIn == 2) {
+        uint4 lo;
+        split_f16(h, &h, &lo);
+        *reinterpret_cast<uint4*>(src + o) = h;
+        *reinterpret_cast<uint4*>(src + C::kQk + o) = lo;
+      }
+    }
+  };
+  const auto wait_for_keys = [&]() {
+    const uint32_t slot = it % kGates, stage = it % kStages, buffer = it & 1u;
+    wait(&sh->gate_full[slot], it / kGates);
+    wait(kIn == 1 ? &sh->keys_full[stage] : &sh->raw, kIn == 1 ? it / kStages : it);
+    wait(&sh->key_empty[buffer], (it >> 1) ^ 1u);
+  };
+  // What this warp wrote of the keys (and, f16, of other tiles) can be used.
+  const auto give_keys = [&]() {
+    fence_proxy_async_smem();
+    arrive(&sh->key_full[it & 1u]);
+    if (lane == 0) mbar_arrive(kIn == 2 ? &sh->full[it % kStages] : &sh->keys_empty[it % kStages]);
+  };
+
   const auto products = [&]() {
-    // P: a thread has row i (token i) and columns [32 half, 32 half + 32)
+    // P: a thread has row i (token i) and columns [32 half, 32 half + 32), eight at a time.  These
+    // warps also decay some of the keys, so that all four schedulers do, and split the queries (f16).
     const int quad = warp & 3, half = (warp - 8) >> 2, i = quad * 32 + lane;
+    const int tid = (half * 2 + quad) * 32 + lane;  // of 128
     const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kScore + 32 * half;
     uint8_t* dst = smem + C::kPAt;
     while (ok && walk.next(p, &x)) {
       for (int c = 0; ok && c < x.n; c += kC, ++it) {
         const uint32_t slot = it % kGates, buffer = it & 1u;
-        wait(&sh->gate_full[slot], it / kGates);
-        wait(&sh->score_full[buffer], it >> 1);
+        wait_for_keys();
         if (!ok) break;
-        tc_fence_after();
-        uint32_t s[32];
-        tmem_ld32(at + 64 * buffer, s);
-        tmem_ld_wait32(s);
-        tc_fence_before();
-        arrive(&sh->score_empty[buffer]);
-        const Gate& t = sh->gate[slot];
-        if (half > quad) {  // all columns are later tokens
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = 0u;
-        } else if (!t.wide) {
-          const uint64_t mine = pair(t.row[i], t.row[i]);
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&t.col[32 * half + j]);
-            const float2 y0 = split(mul2(pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), mul2(f.x, mine)));
-            const float2 y1 = split(mul2(pair(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), mul2(f.y, mine)));
-            s[j] = __float_as_uint(y0.x), s[j + 1] = __float_as_uint(y0.y);
-            s[j + 2] = __float_as_uint(y1.x), s[j + 3] = __float_as_uint(y1.y);
-          }
-        } else {
-          const float2 mine = t.sum[i];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 other = t.sum[32 * half + j];
-            const float f = ex2((mine.x - other.x) + (mine.y - other.y));
-            s[j] = __float_as_uint(__uint_as_float(s[j]) * (f * a.scale));
-          }
+        decay_keys(c, kC - kKeysByP, kC, tid, 128);
+        if (kIn == 2) {
+          uint8_t* base = smem + it % kStages * C::kStage;
+          for (int b = 0; b < C::kKb; ++b) split_block(base + 2 * b * kBlock, C::kQk, min(kC, x.n - c), tid, 128);
         }
-        if (half == quad) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = j <= lane ? s[j] : 0u;
-        }
-        arrive(&sh->gate_empty[slot]);
+        give_keys();
+        wait(&sh->score_full[buffer], it >> 1);
         wait(&sh->p_empty, it ^ 1u);
         if (!ok) break;
-#pragma unroll
+        tc_fence_after();
+        const Gate& t = sh->gate[slot];
+        const float row = t.row[i];
+        const float2 sum = t.sum[i];
+        const bool wide = t.wide;
+        uint32_t next[8];
+        tmem_ld8(at + 64 * buffer, next);
+#pragma unroll 1
         for (int v = 0; v < 4; ++v) {
+          uint64_t y[4];
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = pair(__uint_as_float(next[2 * e]), __uint_as_float(next[2 * e + 1]));
+          if (v < 3) tmem_ld8(at + 64 * buffer + 8 * (v + 1), next);
+          const int j0 = 32 * half + 8 * v;
+          if (!wide) {
+            const ulonglong2 f0 = *reinterpret_cast<const ulonglong2*>(&t.col[j0]), f1 = *reinterpret_cast<const ulonglong2*>(&t.col[j0 + 4]);
+            const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], mul2(f[e], pair(row, row)));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 o = *reinterpret_cast<const float4*>(&t.sum[j0 + 2 * e]);
+              y[e] = mul2(y[e], pair(ex2((sum.x - o.x) + (sum.y - o.y)) * a.scale, ex2((sum.x - o.z) + (sum.y - o.w)) * a.scale));
+            }
+          }
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float a0 = __uint_as_float(s[8 * v + 2 * e]), a1 = __uint_as_float(s[8 * v + 2 * e + 1]);
-            hi[e] = tops(a0, a1);
-            lo[e] = rest(pair(a0, a1));
+            const float2 z = split(y[e]);  // later tokens do not count
+            const uint64_t w = pair(j0 + 2 * e <= i ? z.x : 0.f, j0 + 2 * e + 1 <= i ? z.y : 0.f);
+            hi[e] = tops(w);
+            lo[e] = rest(w, hi[e]);
           }
           const uint32_t o = place(i, 4 * half + v);
           *reinterpret_cast<uint4*>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(dst + kBlock + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        tc_fence_before();
         fence_proxy_async_smem();
-        arrive(&sh->p_full);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh->score_empty[buffer]);
+          mbar_arrive(&sh->p_full);
+          mbar_arrive(&sh->gate_empty[slot]);
+        }
       }
     }
   };
   const auto keys = [&](int which) {
-    // decayed keys, by vectors of eight
+    constexpr int kThreads1 = 32 * (kOut ? 4 : 12);
     const int tid = which * 32 + lane;
-    constexpr int kVec = kDk / 8, kStep = 32 * kKeyWarps / kVec;
-    const int col = tid % kVec, r0 = tid / kVec;
-    const uint32_t from = kBlock + col / 8 * (2 * kBlock), to = C::kKeyAt + col / 8 * kBlock;
     while (ok && walk.next(p, &x)) {
       for (int c = 0; ok && c < x.n; c += kC, ++it) {
-        const uint32_t slot = it % kGates, stage = it % kStages, buffer = it & 1u;
-        wait(&sh->gate_full[slot], it / kGates);
-        if (kIn == 1) wait(&sh->full[stage], it / kStages);
-        else wait(&sh->raw, it);
-        wait(&sh->key_empty[buffer], (it >> 1) ^ 1u);
-        if (!ok) break;
-        const Gate& t = sh->gate[slot];
         const int n = min(kC, x.n - c);
-        uint8_t* src = smem + stage * C::kStage + from;
-        uint8_t* dst = smem + to + buffer * 3 * C::kKeyPart;
-#pragma unroll 2
-        for (int r = r0; r < kC; r += kStep) {
-          const uint32_t o = place(r, col & 7);
-          const uint64_t w2 = pair(t.after[r], t.after[r]);
-          uint4 h = *reinterpret_cast<const uint4*>(src + o);
-          if (r >= n) h = make_uint4(0, 0, 0, 0);
-          uint32_t part[3][4];
-          const uint32_t in[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint64_t y;
-            if constexpr (kIn == 2) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[e]));
-              y = pair(f.x, f.y);
-            } else {
-              y = pair(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u));
-            }
-            y = mul2(y, w2);
-            part[0][e] = tops(y);
-            y = below(y);
-            part[1][e] = tops(y);
-            part[2][e] = tops(below(y));
-          }
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<uint4*>(dst + k * C::kKeyPart + o) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
-          if (kIn == 2) {
-            uint4 lo;
-            split_f16(h, &h, &lo);
-            *reinterpret_cast<uint4*>(src + o) = h;
-            *reinterpret_cast<uint4*>(src + C::kQk + o) = lo;
-          }
-        }
+        uint8_t* v = smem + it % kStages * C::kStage + kIn * C::kQk;
+        wait_for_keys();
+        if (!ok) break;
+        decay_keys(c, 0, kOut ? kC - kKeysByP : kC, tid, kThreads1);
+        if (kIn == 2 && !kOut)
+          for (int b = 0; b < C::kVb; ++b) split_block(v + b * kBlock, C::kV, n, tid, kThreads1);
         if (kIn == 1 && n < kC) {  // values past the piece: 0 times what they hold may be NaN
-          uint8_t* v = smem + stage * C::kStage + kIn * C::kQk;
-          for (int i = tid; i < (kC - n) * 8 * C::kVb; i += 32 * kKeyWarps) {
+          wait(&sh->full[it % kStages], it / kStages);
+          if (!ok) break;
+          for (int i = tid; i < (kC - n) * 8 * C::kVb; i += kThreads1) {
             const int b = i / ((kC - n) * 8), k = i - b * ((kC - n) * 8);
             *reinterpret_cast<uint4*>(v + b * kBlock + n * 128 + 16 * k) = make_uint4(0, 0, 0, 0);
           }
         }
-        fence_proxy_async_smem();
-        arrive(&sh->key_full[buffer]);
-        if (lane == 0) {
-          if (kIn == 2) mbar_arrive(&sh->full[stage]);
-          mbar_arrive(&sh->empty[stage]);
-          mbar_arrive(&sh->gate_empty[slot]);
-        }
+        give_keys();
+        if (lane == 0) mbar_arrive(&sh->gate_empty[it % kGates]);
       }
     }
   };
 
   if (warp >= 20) {
     regs_down<kOtherRegs>();
-    if (warp >= 22) {
+    if (warp == 22) {
       // ------------------------------------------------------------------ loads
       // Rows past the piece come along: their outputs are not written, their scores and decayed
       // keys are replaced by zeros, and the warps that decay keys clear their values.
-      while ((kIn == 2 || warp == 22) && ok && walk.next(p, &x)) {
+      // bf16: keys have barriers of their own.  They are needed for less time than the other tiles,
+      // and the warps that decay them then run ahead of the MMAs.
+      while (ok && walk.next(p, &x)) {
         const int hq = p.q_one ? 0 : x.h / a.per_key_head, hk = p.k_one ? 0 : x.h / a.per_key_head;
         const int hv = p.v_one ? 0 : x.h;
         for (int c = 0; ok && c < x.n; c += kC, ++it) {
           const uint32_t stage = it % kStages;
           uint8_t* base = smem + stage * C::kStage;
-          uint64_t* bar = kIn == 1 ? &sh->full[stage] : &sh->raw;
-          wait(&sh->empty[stage], (it / kStages) ^ 1u);
+          const int row = static_cast<int>(x.row) + c;
+          const uint64_t pol = policy_evict_normal();
+          uint64_t* bar = kIn == 2 ? &sh->raw : &sh->keys_full[stage];
+          constexpr uint32_t kKeyBytes = C::kKb * kBlock, kRestBytes = ((kOut ? C::kKb : 0) + C::kVb) * kBlock;
+          wait(kIn == 2 ? &sh->empty[stage] : &sh->keys_empty[stage], (it / kStages) ^ 1u);
           if (!ok) break;
-          if (warp == 22 && elect_one()) {
-            const uint64_t pol = policy_evict_normal();
-            const int row = static_cast<int>(x.row) + c;
-            mbar_arrive_expect_tx(bar, ((kOut ? 2 : 1) * C::kKb + C::kVb) * kBlock);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, kIn == 2 ? kKeyBytes + kRestBytes : kKeyBytes);
 #pragma unroll
-            for (int b = 0; b < C::kKb; ++b) {
-              tma_load_3d(base + (2 * b + 1) * kBlock, &tm_k, bar, 64 * b, hk, row, pol);
-              if (kOut) tma_load_3d(base + 2 * b * kBlock, &tm_q, bar, 64 * b, hq, row, pol);
-            }
+            for (int b = 0; b < C::kKb; ++b) tma_load_3d(base + (2 * b + 1) * kBlock, &tm_k, bar, 64 * b, hk, row, pol);
+          }
+          __syncwarp();
+          if (kIn == 1) {
+            bar = &sh->full[stage];
+            wait(&sh->empty[stage], (it / kStages) ^ 1u);
+            if (!ok) break;
+          }
+          if (elect_one()) {
+            if (kIn == 1) mbar_arrive_expect_tx(bar, kRestBytes);
+#pragma unroll
+            for (int b = 0; kOut && b < C::kKb; ++b) tma_load_3d(base + 2 * b * kBlock, &tm_q, bar, 64 * b, hq, row, pol);
 #pragma unroll
             for (int b = 0; b < C::kVb; ++b) tma_load_3d(base + kIn * C::kQk + b * kBlock, &tm_v, bar, 64 * b, hv, row, pol);
           }
           __syncwarp();
-          if (kIn == 2) {
-            // queries and values into their parts; keys are split where they are decayed
-            wait(&sh->raw, it);
-            if (!ok) break;
-            const int n = min(kC, x.n - c), tid = threadIdx.x - 22 * 32;
-            const auto split = [&](uint8_t* dst, uint32_t part) {
-#pragma unroll 4
-              for (int v = tid; v < static_cast<int>(kBlock / 16); v += 64) {
-                uint4* at = reinterpret_cast<uint4*>(dst + 16 * v);
-                uint4 lo, hi = *at;
-                if (v / 8 >= n) hi = make_uint4(0, 0, 0, 0);
-                split_f16(hi, &hi, &lo);
-                *at = hi;
-                *reinterpret_cast<uint4*>(dst + part + 16 * v) = lo;
-              }
-            };
-            for (int b = 0; kOut && b < C::kKb; ++b) split(base + 2 * b * kBlock, C::kQk);
-            for (int b = 0; b < C::kVb; ++b) split(base + kIn * C::kQk + b * kBlock, C::kV);
-            fence_proxy_async_smem();
-            arrive(&sh->full[stage]);
-          }
         }
       }
     } else if (warp == 21) {
@@ -573,12 +599,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const auto scores = [&]() {  // of chunk `scored`
         const uint32_t stage = scored % kStages, buffer = scored & 1u;
         wait(&sh->full[stage], scored / kStages);
+        if (kIn == 1) wait(&sh->keys_full[stage], scored / kStages);
         wait(&sh->score_empty[buffer], (scored >> 1) ^ 1u);
         tc_fence_after();
         if (ok && elect_one()) {
           const uint32_t q0 = base_lo + stage * (C::kStage / 16), k0 = q0 + kBlock / 16;
           uint32_t more = 0;
-#pragma unroll
+#pragma unroll 1
           for (int pair = (kIn == 2 ? 2 : 0); pair >= 0; --pair) {  // parts (0, 1), (1, 0), then (0, 0)
             const uint32_t pa = pair == 1 ? C::kQk / 16 : 0, pb = pair == 2 ? C::kQk / 16 : 0;
 #pragma unroll
@@ -589,17 +616,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           umma_commit(&sh->score_full[buffer]);
+          if (kIn == 1) umma_commit(&sh->keys_empty[stage]);
         }
         __syncwarp();
         ++scored;
       };
-      while (ok && walk.next(p, &x)) {
+      // Two warps issue, since an MMA of this size takes longer to issue than it runs: one the
+      // scores and the updates, which need no state, the other what makes outputs.
+      while (warp == 20 && ok && walk.next(p, &x)) {
         const int chunks = (x.n + kC - 1) / kC;
         if (kOut && chunks > 0) scores();
         for (int c = 0; ok && c < chunks; ++c, ++it) {
           const uint32_t stage = it % kStages, buffer = it & 1u;
           const uint32_t v0 = cols_lo + (stage * C::kStage + kIn * C::kQk) / 16;
-          if (!kOut) wait(&sh->full[stage], it / kStages);
+          wait(&sh->full[stage], it / kStages);
           wait(&sh->key_full[buffer], it >> 1);
           wait(&sh->update_empty, it ^ 1u);
           tc_fence_after();
@@ -607,9 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t k0 = cols_lo + (C::kKeyAt + buffer * 3 * C::kKeyPart) / 16;
             uint32_t more = 0;
             // small parts first: what the sum cuts off is then small too
-#pragma unroll
+#pragma unroll 1
             for (int pv = kIn - 1; pv >= 0; --pv) {
-#pragma unroll
+#pragma unroll 1
               for (int pk = pv == 1 ? 1 : 2; pk >= 0; --pk) {
 #pragma unroll
                 for (int s = 0; s < kC / 16; ++s) {
@@ -621,19 +651,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             umma_commit(&sh->update_full);
             umma_commit(&sh->key_empty[buffer]);
-            if (!kOut) umma_commit(&sh->empty[stage]);
+            umma_commit(&sh->empty[stage]);
           }
           __syncwarp();
-          if (!kOut) continue;
-          if (kStages > 1 && c + 1 < chunks) scores();
+          if (kOut && c + 1 < chunks) scores();
+        }
+      }
+      while (kOut && warp == 23 && ok && walk.next(p, &x)) {
+        const int chunks = (x.n + kC - 1) / kC;
+        for (int c = 0; ok && c < chunks; ++c, ++it) {
+          const uint32_t stage = it % kStages;
+          const uint32_t v0 = cols_lo + (stage * C::kStage + kIn * C::kQk) / 16;
+          wait(&sh->full[stage], it / kStages);
           wait(&sh->state_full, it);
           wait(&sh->out_empty, it ^ 1u);
           tc_fence_after();
           if (ok && elect_one()) {
             const uint32_t q0 = base_lo + stage * (C::kStage / 16);
             uint32_t more = 0;
-#pragma unroll
-            for (int pair = (kIn == 2 ? 2 : 1); pair >= 0; --pair) {  // (lo, 0), (hi, 1), (hi, 0) of S and Q
+#pragma unroll 1
+            for (int pair = (kIn == 2 ? 2 : 1); pair >= 0; --pair) {  // (hi, 1), (lo, 0), (hi, 0) of S and Q
               const uint32_t ps = pair == 1 ? kDk / 2 : 0, pq = pair == 2 ? C::kQk / 16 : 0;
 #pragma unroll
               for (int s = 0; s < kDk / 16; ++s) {
@@ -646,12 +683,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           wait(&sh->p_full, it);
+          wait(&sh->key_full[it & 1u], it >> 1);  // the values past the piece have been cleared
           tc_fence_after();
           if (ok && elect_one()) {
             const uint32_t p0 = base_lo + C::kPAt / 16;
             uint32_t more = 0;
-#pragma unroll
-            for (int pair = (kIn == 2 ? 2 : 1); pair >= 0; --pair) {  // (0, lo), (1, hi), (0, hi) of V and P
+#pragma unroll 1
+            for (int pair = (kIn == 2 ? 2 : 1); pair >= 0; --pair) {  // (1, hi), (0, lo), (0, hi) of V and P
               const uint32_t pp = pair == 1 ? kBlock / 16 : 0, pv = pair == 2 ? C::kV / 16 : 0;
 #pragma unroll
               for (int s = 0; s < kC / 16; ++s) {
@@ -664,7 +702,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(&sh->empty[stage]);
           }
           __syncwarp();
-          if (kStages == 1 && c + 1 < chunks) scores();
         }
       }
       if (elect_one()) umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
@@ -685,51 +722,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; ok && c < x.n; c += kC, ++it) {
         const uint32_t slot = it % kGates;
         const int n = min(kC, x.n - c) - (lane & 3);
+        if (kIn == 2) {  // these warps split the values
+          wait(&sh->raw, it);
+          if (!ok) break;
+          uint8_t* v = smem + it % kStages * C::kStage + kIn * C::kQk;
+          for (int b = 0; b < C::kVb; ++b) split_block(v + b * kBlock, C::kV, min(kC, x.n - c), threadIdx.x - 16 * 32, 128);
+          fence_proxy_async_smem();
+          arrive(&sh->full[it % kStages]);
+        }
         wait(&sh->gate_full[slot], it / kGates);
         wait(&sh->out_full, it);
         if (!ok) break;
         tc_fence_after();
         const Gate& t = sh->gate[slot];
+        T* o = out + c * a.o_ts;
+        const int64_t four = 4 * a.o_ts;
 #pragma unroll 1
-        for (int h = 0; h < kC; h += 32) {
-          uint32_t y[16];  // pairs of columns
+        for (int h = 0; h < kC; h += 16) {
+          uint32_t u[16], w[16];
+          tmem_ld16(at + kInter + h, u);
+          tmem_ld16(at + kIntra + h, w);
+          tmem_ld_wait();
 #pragma unroll
-          for (int j0 = 0; j0 < 32; j0 += 16) {
-            uint32_t u[16], w[16];
-            tmem_ld16(at + kInter + h + j0, u);
-            tmem_ld16(at + kIntra + h + j0, w);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const ulonglong2 before = *reinterpret_cast<const ulonglong2*>(&t.before[h + j0 + j]);
-              const auto two = [](uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); };
-              const float2 f01 = split(fma2(before.x, two(u[j], u[j + 1]), two(w[j], w[j + 1])));
-              const float2 f23 = split(fma2(before.y, two(u[j + 2], u[j + 3]), two(w[j + 2], w[j + 3])));
-              const float f[4] = {f01.x, f01.y, f23.x, f23.y};
-              // even lanes take tokens 0 and 2, odd ones 1 and 3
-              const bool odd = lane & 1;
-              const float g0 = __shfl_xor_sync(0xffffffffu, odd ? f[0] : f[1], 1);
-              const float g1 = __shfl_xor_sync(0xffffffffu, odd ? f[2] : f[3], 1);
-              y[(j0 + j) / 2] = odd ? pack<T>(g0, f[1]) : pack<T>(f[0], g0);
-              y[(j0 + j) / 2 + 1] = odd ? pack<T>(g1, f[3]) : pack<T>(f[2], g1);
-            }
-          }
-          if (h + 32 == kC) {
-            tc_fence_before();
-            arrive(&sh->out_empty);
-            if (lane == 0) mbar_arrive(&sh->gate_empty[slot]);
-          }
-          T* o = out + (c + h) * a.o_ts;
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < 16; j += 4) {
+            const ulonglong2 before = *reinterpret_cast<const ulonglong2*>(&t.before[h + j]);
+            const auto two = [](uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); };
+            const float2 f01 = split(fma2(before.x, two(u[j], u[j + 1]), two(w[j], w[j + 1])));
+            const float2 f23 = split(fma2(before.y, two(u[j + 2], u[j + 3]), two(w[j + 2], w[j + 3])));
+            // even lanes take tokens 0 and 2, odd ones 1 and 3
+            const bool odd = lane & 1, up = lane & 2;
+            const float g0 = __shfl_xor_sync(0xffffffffu, odd ? f01.x : f01.y, 1);
+            const float g1 = __shfl_xor_sync(0xffffffffu, odd ? f23.x : f23.y, 1);
+            const uint32_t y0 = odd ? pack<T>(g0, f01.y) : pack<T>(f01.x, g0);
+            const uint32_t y1 = odd ? pack<T>(g1, f23.y) : pack<T>(f23.x, g1);
             // the lower lanes of each four keep tokens 0 and 1, the upper ones 2 and 3
-            const bool up = lane & 2;
-            const uint32_t mine = up ? y[j / 2 + 1] : y[j / 2];
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? y[j / 2] : y[j / 2 + 1], 2);
-            if (col < kDv && h + j < n)
-              *reinterpret_cast<uint2*>(o + j * a.o_ts) = up ? make_uint2(other, mine) : make_uint2(mine, other);
+            const uint32_t mine = up ? y1 : y0, other = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 2);
+            if (col < kDv && h + j < n) *reinterpret_cast<uint2*>(o) = up ? make_uint2(other, mine) : make_uint2(mine, other);
+            o += four;
           }
         }
+        tc_fence_before();
+        arrive(&sh->out_empty);
+        if (lane == 0) mbar_arrive(&sh->gate_empty[slot]);
       }
     }
   } else if (warp >= 8) {
@@ -793,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int d = 0; d < 16; ++d) {
               hi[d] = tops(S[d0 / 2 + d]);
-              lo[d] = rest(S[d0 / 2 + d]);
+              lo[d] = rest(S[d0 / 2 + d], hi[d]);
             }
             tmem_st16(at + kState + (wg * kN + d0) / 2, hi);
             tmem_st16(at + kState + kDk / 2 + (wg * kN + d0) / 2, lo);
