@@ -731,7 +731,7 @@ int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int 
  *   v, out    device [num_tokens][heads][value_dim], the same type
  *   log_decay device float: g of token t and head h is log_decay[t * decay_token_stride + h *
  *             decay_head_stride].  A stride of 0 makes it one for all tokens (heads).  Any value
- *             <= 0, also -inf (the state starts anew with that token).  A g above 0 grows the state.
+ *             <= 0, also -inf (the state starts anew with that token); one above 0 counts as 0
  *   cu_new    device int32 [num_seqs + 1]: sequence b's new tokens are rows cu_new[b] ..
  *             cu_new[b + 1] - 1; or NULL for one token a sequence (num_tokens == num_seqs).
  *             Offsets do not decrease and need not begin at 0; other rows are neither read nor

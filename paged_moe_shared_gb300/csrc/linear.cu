@@ -67,7 +67,10 @@ __global__ void __launch_bounds__(kStepThreads) linear_steps_kernel(const __grid
       const int t = i / kCols, d = i - t * kCols;
       vs[t][d] = to_f(v[(t0 + t) * a.v_ts + d]);
     }
-    if (tid < n) decay[tid] = expf(a.decay[(s.row + t0 + tid) * a.g_ts + h * a.g_hs]);
+    if (tid < n) {
+      const float g = a.decay[(s.row + t0 + tid) * a.g_ts + h * a.g_hs];
+      decay[tid] = expf(g > 0.f ? 0.f : g);  // a NaN stays one
+    }
     __syncthreads();
     for (int t = 0; t < n; ++t) {
       const float f = decay[t];

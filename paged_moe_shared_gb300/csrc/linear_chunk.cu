@@ -2,13 +2,16 @@
 //
 // With G_i the sum of the decays of a chunk's tokens up to i, S the state before it and
 // T the state after it, a head's chunk is
-//   out_i = scale (exp(G_i) S^T q_i + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
+//   out_i = scale exp(G_i) (S^T q_i + sum_{j <= i} exp(-G_j) (q_i . k_j) v_j)
 //   T     = exp(G_last) S + sum_j exp(G_last - G_j) k_j v_j^T.
+// exp(-G_j) leaves fp32 where a chunk forgets more than 2^64.  There exp(G_i) outside the
+// bracket is held at 2^-64 and what is missing goes into the sum's weights; S, which by then
+// should have been forgotten altogether, is then forgotten by 2^-64.
 // All products are made transposed, with the value columns in the 128 lanes of TMEM and
 // 64 tokens or the key columns across, so that every MMA has full height:
 //   scores  Q K^T          (64 x 64; the lanes below take K K^T, which nobody reads)
 //   inter   S^T Q^T        S^T in TMEM, as two bf16 parts that its owners write there
-//   intra   V^T P^T        P = scores * decays, two bf16 parts in shared memory
+//   intra   V^T P^T        onto it; P = scores * decays, two bf16 parts in shared memory
 //   update  V^T Kd         Kd = decayed keys, three bf16 parts: an fp32 number exactly
 // S^T itself stays in the registers of eight warps in fp32 and takes each chunk's update
 // there: sums inside the tensor cores truncate, and over thousands of tokens that would
@@ -45,18 +48,32 @@ static_assert((2 * kStateRegs + 2 * kProductRegs + kOutRegs + kOtherRegs) * 128 
 
 struct alignas(16) Gate {  // read four numbers at a time
   float2 sum[kC];   // G in two parts whose differences are exact, log2
-  float row[kC], col[kC];  // scale * exp(G - G_middle), exp(G_middle - G)
+  float col[kC];    // exp(-G)
   float before[kC]; // scale * exp(G)
   float after[kC];  // exp(G_last - G)
   float all;        // exp(G_last)
-  int wide;         // G spans too much for row * col: decays come from `sum`
+  int wide;         // G leaves 2^-64: `col` is of no use
   int pad[2];
 };
-
 static_assert(sizeof(Gate) % 16 == 0 && offsetof(Gate, col) % 16 == 0 && offsetof(Gate, before) % 16 == 0, "");
+constexpr float kLeast = -64.f;   // of exp(G) outside the bracket, log2
+
+// One unit: a piece of a sequence and a head.
+struct Unit {
+  int b, h, slot;   // slot: the piece's among all
+  int64_t row;      // first row
+  int n;            // rows
+  int seq0;         // the sequence's first row
+  bool first, last; // piece of its sequence
+  const float* in;  // of the sequence, or null
+  float* out;
+  bool ok;
+};
+constexpr int kUnits = 64;  // of a CTA
 
 struct ChunkShared {
   Gate gate[kGates];
+  Unit units[kUnits];
   uint64_t full[2], empty[2];             // loaded queries and values (f16: all tiles, split)
   uint64_t keys_full[2], keys_empty[2];   // loaded keys
   uint64_t raw;                           // f16: all tiles before they are split
@@ -66,7 +83,7 @@ struct ChunkShared {
   uint64_t p_full, p_empty;
   uint64_t state_full, state_empty;       // parts of S
   uint64_t update_full, update_empty;
-  uint64_t out_full, out_empty;
+  uint64_t out_full[2], out_empty[2];
   uint64_t drain;
   int abort;
   uint32_t tmem_base;
@@ -94,17 +111,6 @@ struct ChunkArgs {
   float* decays;  // [pieces][heads]
 };
 
-// One unit: a piece of a sequence and a head.
-struct Unit {
-  int b, h, slot;   // slot: the piece's among all
-  int64_t row;      // first row
-  int n;            // rows
-  int seq0;         // the sequence's first row
-  bool first, last; // piece of its sequence
-  const float* in;  // of the sequence, or null
-  float* out;
-  bool ok;
-};
 __device__ __forceinline__ Unit find_unit(const ChunkArgs& p, int u, bool record) {
   const LinearArgs& a = p.l;
   Unit x{};
@@ -137,21 +143,6 @@ __device__ __forceinline__ Unit find_unit(const ChunkArgs& p, int u, bool record
   x.out = s.out;
   return x;
 }
-
-// Walks the units of this CTA; every warp does so by itself.
-template <bool kOut>
-struct Walk {
-  int u;
-  __device__ __forceinline__ bool next(const ChunkArgs& p, Unit* x, bool record = false) {
-    for (;; ) {
-      u = u < 0 ? static_cast<int>(blockIdx.x) : u + static_cast<int>(gridDim.x);
-      if (u >= p.units) return false;
-      *x = find_unit(p, u, record);
-      // the first kernel is about pieces that others follow
-      if (x->ok && (kOut || !x->last)) return true;
-    }
-  }
-};
 
 template <int kRegs>
 __device__ __forceinline__ void regs_up() {
@@ -224,7 +215,7 @@ __device__ __forceinline__ void split_f16(const uint4& w, uint4* hi, uint4* lo) 
 
 // Fixed point with 40 bits below the point.
 __device__ __forceinline__ int64_t fixed_log2(float g) {
-  g = fminf(fmaxf(g, -1400.f), 1400.f);  // 2^2000 either way is 0 or infinity
+  g = fminf(fmaxf(g, -1400.f), 0.f);  // 2^-2000 is 0; decays above 0 are none
   constexpr float kHi = 1.4426950408889634f, kLo = 1.925963033500e-8f;  // log2(e)
   const float x = g * kHi;
   const float rest = fmaf(g, kHi, -x) + g * kLo;
@@ -253,6 +244,26 @@ __device__ __forceinline__ float exp2_of(float2 a, float2 b) {
   return fmaf(y, f, 1.f) * __int_as_float(e << 23);
 }
 
+// mbar_wait_idle in fewer instructions: the loops of six kinds of warps together are what the
+// instruction cache has to hold.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  uint64_t start = 0;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+        : "memory");
+    if (done) return true;
+    const uint64_t now = globaltimer();
+    if (start == 0) start = now;
+    if (*abort || now - start > kWaitTimeoutNs) return false;
+  }
+}
+
 template <typename T, int kDk, int kDv, bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const __grid_constant__ ChunkArgs p, const __grid_constant__ CUtensorMap tm_q,
@@ -278,6 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->score_empty[i], 4);
       mbar_init(&sh->key_full[i], kKeyWarps);
       mbar_init(&sh->key_empty[i], 1);
+      mbar_init(&sh->out_full[i], 1);
+      mbar_init(&sh->out_empty[i], 4);
     }
     for (int i = 0; i < kGates; ++i) {
       mbar_init(&sh->gate_full[i], 1);
@@ -290,8 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->state_empty, 1);
     mbar_init(&sh->update_full, 1);
     mbar_init(&sh->update_empty, 8);
-    mbar_init(&sh->out_full, 1);
-    mbar_init(&sh->out_empty, 4);
     mbar_init(&sh->drain, 2);
     sh->abort = 0;
     fence_barrier_init();
@@ -300,15 +311,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sh->tmem_base, 512);
     tmem_relinquish();
   }
+  for (int i = threadIdx.x; i < kUnits; i += kThreads) {
+    const int u = blockIdx.x + i * gridDim.x;
+    Unit x{};
+    if (u < p.units) {
+      x = find_unit(p, u, kOut);
+      x.ok = x.ok && (kOut || !x.last);  // the first kernel is about pieces that others follow
+    }
+    sh->units[i] = x;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   // columns of TMEM
-  constexpr uint32_t kScore = 0, kInter = 128, kIntra = 192, kUpdate = 256, kState = 384;
+  constexpr uint32_t kScore = 0, kOutAt = 128, kUpdate = 256, kState = 384;  // two buffers of scores and outputs
   bool ok = true;
   const auto wait = [&](uint64_t* bar, uint32_t phase) {
-    ok = ok && mbar_wait_idle(bar, phase & 1u, abort);
+    ok = ok && wait_for(bar, phase & 1u, abort);
     ok = __all_sync(0xffffffffu, ok);
   };
   // one arrival of a converged warp
@@ -316,8 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  Walk<kOut> walk{-1};
+  // Units of this CTA in order; every warp goes through them by itself.
+  int next_unit = 0;
   Unit x{};
+  const auto next = [&]() {
+    while (next_unit < kUnits) {
+      x = sh->units[next_unit++];
+      if (x.ok) return true;
+    }
+    return false;
+  };
   uint32_t it = 0;  // chunks so far
 
   // f16: eight rows of 16 bytes a turn, thread `tid` of `threads`; rows past `n` become zeros.
@@ -394,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = (half * 2 + quad) * 32 + lane;  // of 128
     const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kScore + 32 * half;
     uint8_t* dst = smem + C::kPAt;
-    while (ok && walk.next(p, &x)) {
+    while (ok && next()) {
       for (int c = 0; ok && c < x.n; c += kC, ++it) {
         const uint32_t slot = it % kGates, buffer = it & 1u;
         wait_for_keys();
@@ -410,8 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const Gate& t = sh->gate[slot];
-        const float row = t.row[i];
-        const float2 sum = t.sum[i];
+        float2 sum = t.sum[i];
+        // what exp(G_i) is held back by
+        sum = sum.x >= kLeast ? make_float2(0.f, 0.f) : make_float2(sum.x - kLeast, sum.y);
         const bool wide = t.wide;
         uint32_t next[8];
         tmem_ld8(at + 64 * buffer, next);
@@ -427,12 +456,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const ulonglong2 f0 = *reinterpret_cast<const ulonglong2*>(&t.col[j0]), f1 = *reinterpret_cast<const ulonglong2*>(&t.col[j0 + 4]);
             const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], mul2(f[e], pair(row, row)));
+            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], f[e]);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float4 o = *reinterpret_cast<const float4*>(&t.sum[j0 + 2 * e]);
-              y[e] = mul2(y[e], pair(ex2((sum.x - o.x) + (sum.y - o.y)) * a.scale, ex2((sum.x - o.z) + (sum.y - o.w)) * a.scale));
+              y[e] = mul2(y[e], pair(ex2((sum.x - o.x) + (sum.y - o.y)), ex2((sum.x - o.z) + (sum.y - o.w))));
             }
           }
           uint32_t hi[4], lo[4];
@@ -461,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto keys = [&](int which) {
     constexpr int kThreads1 = 32 * (kOut ? 4 : 12);
     const int tid = which * 32 + lane;
-    while (ok && walk.next(p, &x)) {
+    while (ok && next()) {
       for (int c = 0; ok && c < x.n; c += kC, ++it) {
         const int n = min(kC, x.n - c);
         uint8_t* v = smem + it % kStages * C::kStage + kIn * C::kQk;
@@ -492,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // keys are replaced by zeros, and the warps that decay keys clear their values.
       // bf16: keys have barriers of their own.  They are needed for less time than the other tiles,
       // and the warps that decay them then run ahead of the MMAs.
-      while (ok && walk.next(p, &x)) {
+      while (ok && next()) {
         const int hq = p.q_one ? 0 : x.h / a.per_key_head, hk = p.k_one ? 0 : x.h / a.per_key_head;
         const int hv = p.v_one ? 0 : x.h;
         for (int c = 0; ok && c < x.n; c += kC, ++it) {
@@ -527,9 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 21) {
       // ------------------------------------------------------------------ decays
-      while (ok && walk.next(p, &x)) {
+      while (ok && next()) {
         const float* g = a.decay + x.row * a.g_ts + x.h * a.g_hs;
-        constexpr int64_t kFar = 1ll << 53;  // 2^8192 either way is 0 or infinity
+        constexpr int64_t kFar = 1ll << 50;  // 2^-1024 is 0, and the parts hold 2^17
         int64_t total = 0;
         bool nan = false;
         const int i = 2 * lane;
@@ -561,28 +590,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           Gate& t = sh->gate[slot];
           if (kOut) {
+            const bool wide = !(end.x >= kLeast) || bad1 != 0;
             if (nan0) p0.x = none;
             if (nan1) p1.x = none;
             *reinterpret_cast<float4*>(&t.sum[i]) = make_float4(p0.x, p0.y, p1.x, p1.y);
-            *reinterpret_cast<float2*>(&t.before[i]) = make_float2(exp2_of(p0, zero) * a.scale, exp2_of(p1, zero) * a.scale);
-            // products of exp(G - middle) and its inverse do while these stay within 2^40
-            const float2 middle = parts_of(last / 2);
-            const bool far = !(fabsf(p0.x - middle.x) <= 40.f && fabsf(p1.x - middle.x) <= 40.f);
-            const bool wide = __any_sync(0xffffffffu, far);
+            // fmaxf would lose a NaN
+            const float2 least = make_float2(kLeast, 0.f);
+            *reinterpret_cast<float2*>(&t.before[i]) = make_float2(exp2_of(p0.x < kLeast ? least : p0, zero) * a.scale,
+                                                                   exp2_of(p1.x < kLeast ? least : p1, zero) * a.scale);
+            *reinterpret_cast<float2*>(&t.col[i]) = make_float2(exp2_of(zero, p0), exp2_of(zero, p1));
             if (lane == 0) t.wide = wide;
-            *reinterpret_cast<float2*>(&t.row[i]) = make_float2(exp2_of(p0, middle) * a.scale, exp2_of(p1, middle) * a.scale);
-            *reinterpret_cast<float2*>(&t.col[i]) = make_float2(exp2_of(middle, p0), exp2_of(middle, p1));
           }
           *reinterpret_cast<float2*>(&t.after[i]) = make_float2(after0, after1);
           if (lane == 0) t.all = bad1 ? none : all;
-          total = min(max(total + last, -kFar), kFar);
+          total = max(total + last, -kFar);
           nan |= bad1 != 0;
           arrive(&sh->gate_full[slot]);
         }
         if (!kOut && lane == 0) {
-          const int64_t far = 1ll << 50;  // the parts hold 2^17
           p.decays[static_cast<int64_t>(x.slot) * a.heads + x.h] =
-              nan ? __int_as_float(0x7FFFFFFF) : exp2_of(parts_of(min(max(total, -far), far)), make_float2(0.f, 0.f));
+              nan ? __int_as_float(0x7FFFFFFF) : exp2_of(parts_of(total), make_float2(0.f, 0.f));
         }
       }
     } else {
@@ -623,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // Two warps issue, since an MMA of this size takes longer to issue than it runs: one the
       // scores and the updates, which need no state, the other what makes outputs.
-      while (warp == 20 && ok && walk.next(p, &x)) {
+      while (warp == 20 && ok && next()) {
         const int chunks = (x.n + kC - 1) / kC;
         if (kOut && chunks > 0) scores();
         for (int c = 0; ok && c < chunks; ++c, ++it) {
@@ -657,15 +684,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kOut && c + 1 < chunks) scores();
         }
       }
-      while (kOut && warp == 23 && ok && walk.next(p, &x)) {
+      while (kOut && warp == 23 && ok && next()) {
         const int chunks = (x.n + kC - 1) / kC;
         for (int c = 0; ok && c < chunks; ++c, ++it) {
           const uint32_t stage = it % kStages;
           const uint32_t v0 = cols_lo + (stage * C::kStage + kIn * C::kQk) / 16;
           wait(&sh->full[stage], it / kStages);
           wait(&sh->state_full, it);
-          wait(&sh->out_empty, it ^ 1u);
+          wait(&sh->out_empty[it & 1u], (it >> 1) ^ 1u);
           tc_fence_after();
+          const uint32_t out = tb + kOutAt + 64 * (it & 1u);
           if (ok && elect_one()) {
             const uint32_t q0 = base_lo + stage * (C::kStage / 16);
             uint32_t more = 0;
@@ -674,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t ps = pair == 1 ? kDk / 2 : 0, pq = pair == 2 ? C::kQk / 16 : 0;
 #pragma unroll
               for (int s = 0; s < kDk / 16; ++s) {
-                umma_f16_ts_lo<kHi, id_inter>(tb + kInter, tb + kState + ps + 8 * s,
+                umma_f16_ts_lo<kHi, id_inter>(out, tb + kState + ps + 8 * s,
                                               q0 + pq + s / 4 * (2 * kBlock / 16) + s % 4 * 2, more);
                 more = 1;
               }
@@ -687,18 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (ok && elect_one()) {
             const uint32_t p0 = base_lo + C::kPAt / 16;
-            uint32_t more = 0;
 #pragma unroll 1
             for (int pair = (kIn == 2 ? 2 : 1); pair >= 0; --pair) {  // (1, hi), (0, lo), (0, hi) of V and P
               const uint32_t pp = pair == 1 ? kBlock / 16 : 0, pv = pair == 2 ? C::kV / 16 : 0;
 #pragma unroll
               for (int s = 0; s < kC / 16; ++s) {
-                umma_f16_lo<kHi, kHi, id_intra>(tb + kIntra, v0 + pv + 128 * s, p0 + pp + 2 * s, more);
-                more = 1;
+                umma_f16_lo<kHi, kHi, id_intra>(out, v0 + pv + 128 * s, p0 + pp + 2 * s, 1u);
               }
             }
             umma_commit(&sh->p_empty);
-            umma_commit(&sh->out_full);
+            umma_commit(&sh->out_full[it & 1u]);
             umma_commit(&sh->empty[stage]);
           }
           __syncwarp();
@@ -715,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!kOut) keys(warp - 8);
     const int quad = warp & 3, col = quad * 32 + lane;
     const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    while (kOut && ok && walk.next(p, &x, warp == 16 && lane == 0)) {
+    while (kOut && ok && next()) {
       // Lanes are value columns.  Four neighbouring lanes change places for four tokens, so that each
       // writes four columns of one token.
       T* out = static_cast<T*>(a.out) + (x.row + (lane & 3)) * a.o_ts + x.h * a.o_hs + (col & ~3);
@@ -731,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           arrive(&sh->full[it % kStages]);
         }
         wait(&sh->gate_full[slot], it / kGates);
-        wait(&sh->out_full, it);
+        wait(&sh->out_full[it & 1u], it >> 1);
         if (!ok) break;
         tc_fence_after();
         const Gate& t = sh->gate[slot];
@@ -739,16 +765,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t four = 4 * a.o_ts;
 #pragma unroll 1
         for (int h = 0; h < kC; h += 16) {
-          uint32_t u[16], w[16];
-          tmem_ld16(at + kInter + h, u);
-          tmem_ld16(at + kIntra + h, w);
+          uint32_t u[16];
+          tmem_ld16(at + kOutAt + 64 * (it & 1u) + h, u);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const ulonglong2 before = *reinterpret_cast<const ulonglong2*>(&t.before[h + j]);
             const auto two = [](uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); };
-            const float2 f01 = split(fma2(before.x, two(u[j], u[j + 1]), two(w[j], w[j + 1])));
-            const float2 f23 = split(fma2(before.y, two(u[j + 2], u[j + 3]), two(w[j + 2], w[j + 3])));
+            const float2 f01 = split(mul2(before.x, two(u[j], u[j + 1])));
+            const float2 f23 = split(mul2(before.y, two(u[j + 2], u[j + 3])));
             // even lanes take tokens 0 and 2, odd ones 1 and 3
             const bool odd = lane & 1, up = lane & 2;
             const float g0 = __shfl_xor_sync(0xffffffffu, odd ? f01.x : f01.y, 1);
@@ -762,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
-        arrive(&sh->out_empty);
+        arrive(&sh->out_empty[it & 1u]);
         if (lane == 0) mbar_arrive(&sh->gate_empty[slot]);
       }
     }
@@ -779,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool real = col < kDv;
     const int64_t mine = static_cast<int64_t>(wg) * kN * kDv + col;
     constexpr int64_t kState1 = static_cast<int64_t>(kDk) * kDv;
-    while (ok && walk.next(p, &x, !kOut && warp == 0 && lane == 0)) {
+    while (ok && next()) {
       uint64_t S[kN / 2];  // pairs of key rows
       const auto load = [&](const float* src) {
 #pragma unroll
@@ -877,7 +902,8 @@ cudaError_t launch_one(const ChunkArgs& p, const CUtensorMap* tm, cudaStream_t s
   static SmemOnce once;
   const cudaError_t e = once.set(reinterpret_cast<const void*>(fn), smem);
   if (e != cudaSuccess) return e;
-  fn<<<std::min(p.units, p.l.sms), kThreads, smem, s>>>(p, tm[0], tm[1], tm[2]);
+  const int ctas = std::max(std::min(p.units, p.l.sms), (p.units + kUnits - 1) / kUnits);
+  fn<<<ctas, kThreads, smem, s>>>(p, tm[0], tm[1], tm[2]);
   return cudaGetLastError();
 }
 template <typename T, int kDk, int kDv>
