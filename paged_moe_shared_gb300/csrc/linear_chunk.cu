@@ -85,7 +85,6 @@ struct ChunkShared {
   uint64_t update_full, update_empty;
   uint64_t out_full[2], out_empty[2];
   uint64_t drain;
-  int abort;
   uint32_t tmem_base;
 };
 
@@ -244,24 +243,21 @@ __device__ __forceinline__ float exp2_of(float2 a, float2 b) {
   return fmaf(y, f, 1.f) * __int_as_float(e << 23);
 }
 
-// mbar_wait_idle in fewer instructions: the loops of six kinds of warps together are what the
-// instruction cache has to hold.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  uint64_t start = 0;
-  for (;;) {
-    uint32_t done;
+// Waits for a phase in as few instructions as that takes: the loops of six kinds of warps
+// together are what the instruction cache has to hold.  A try suspends the warp for up to a
+// microsecond, and gives up after a million of them.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  uint32_t done, left = 1u << 20;
+  do {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000)
         : "memory");
-    if (done) return true;
-    const uint64_t now = globaltimer();
-    if (start == 0) start = now;
-    if (*abort || now - start > kWaitTimeoutNs) return false;
-  }
+  } while (!done && --left);
+  return done;
 }
 
 template <typename T, int kDk, int kDv, bool kOut>
@@ -275,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ ChunkShared sh_;
   ChunkShared* sh = &sh_;
-  volatile int* abort = &sh->abort;
   const LinearArgs& a = p.l;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -304,7 +299,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->update_full, 1);
     mbar_init(&sh->update_empty, 8);
     mbar_init(&sh->drain, 2);
-    sh->abort = 0;
     fence_barrier_init();
   }
   if (warp == 20) {
@@ -328,8 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kScore = 0, kOutAt = 128, kUpdate = 256, kState = 384;  // two buffers of scores and outputs
   bool ok = true;
   const auto wait = [&](uint64_t* bar, uint32_t phase) {
-    ok = ok && wait_for(bar, phase & 1u, abort);
-    ok = __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, wait_for(bar, phase & 1u)) && ok;
   };
   // one arrival of a converged warp
   const auto arrive = [&](uint64_t* bar) {
@@ -732,8 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (elect_one()) umma_commit(&sh->drain);  // all MMAs are finished before TMEM is released
       __syncwarp();
-      volatile int never = 0;
-      mbar_wait_idle(&sh->drain, 0, &never);
+      wait_for(&sh->drain, 0);
     }
   } else if (warp >= 16) {
     // -------------------------------------------------------------------- outputs
@@ -763,13 +755,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Gate& t = sh->gate[slot];
         T* o = out + c * a.o_ts;
         const int64_t four = 4 * a.o_ts;
+        uint32_t ahead[8];
+        tmem_ld8(at + kOutAt + 64 * (it & 1u), ahead);
 #pragma unroll 1
-        for (int h = 0; h < kC; h += 16) {
-          uint32_t u[16];
-          tmem_ld16(at + kOutAt + 64 * (it & 1u) + h, u);
+        for (int h = 0; h < kC; h += 8) {
+          uint32_t u[8];
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
+          for (int j = 0; j < 8; ++j) u[j] = ahead[j];
+          if (h + 8 < kC) tmem_ld8(at + kOutAt + 64 * (it & 1u) + h + 8, ahead);
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
             const ulonglong2 before = *reinterpret_cast<const ulonglong2*>(&t.before[h + j]);
             const auto two = [](uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); };
             const float2 f01 = split(mul2(before.x, two(u[j], u[j + 1])));
@@ -885,10 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && dst && real) store(dst);
     }
   }
-  if (!ok && lane == 0) {
-    set_error(a.err, RIMURU_DEV_TIMEOUT);
-    sh->abort = 1;
-  }
+  if (!ok && lane == 0) set_error(a.err, RIMURU_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
