@@ -76,7 +76,8 @@ struct ChunkShared {
   Unit units[kUnits];
   uint64_t full[2], empty[2];             // loaded queries and values (f16: all tiles, split)
   uint64_t keys_full[2], keys_empty[2];   // loaded keys
-  uint64_t raw;                           // f16: all tiles before they are split
+  uint64_t raw, raw_empty;                // f16: all tiles before they are split
+  uint64_t values_full;                   // f16, second kernel: split values
   uint64_t gate_full[kGates], gate_empty[kGates];
   uint64_t score_full[2], score_empty[2];
   uint64_t key_full[2], key_empty[2];     // decayed keys
@@ -97,8 +98,11 @@ struct Cfg {
   static constexpr uint32_t kQk = kKb * 2 * kBlock, kV = kVb * kBlock;
   static constexpr uint32_t kStage = kIn * (kQk + kV);
   static constexpr uint32_t kKeyPart = kKb * kBlock;
-  static constexpr uint32_t kKeyAt = kStages * kStage, kPAt = kKeyAt + 2 * 3 * kKeyPart;
-  static constexpr uint32_t kSmem = kPAt + 2 * kBlock + 1024;
+  // decayed keys twice; f16: once, and the next chunk's tiles as they are loaded [keys, queries, values]
+  static constexpr int kKeyBufs = kIn == 1 ? 2 : 1;
+  static constexpr uint32_t kKeyAt = kStages * kStage, kPAt = kKeyAt + kKeyBufs * 3 * kKeyPart;
+  static constexpr uint32_t kRawAt = kPAt + 2 * kBlock;
+  static constexpr uint32_t kSmem = kRawAt + (kIn == 1 ? 0 : kQk + kV) + 1024;
 };
 
 struct ChunkArgs {
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->full[i], kIn == 1 ? 1 : 12);  // f16: warps 8 to 19 split the tiles
+      mbar_init(&sh->full[i], kIn == 1 ? 1 : kOut ? 8 : 12);  // f16: warps 8 to 15 (19) split the tiles
       mbar_init(&sh->empty[i], kOut ? 2 : 1);      // both MMA warps
       mbar_init(&sh->keys_full[i], 1);
       mbar_init(&sh->keys_empty[i], (kOut ? 1 : 0) + kKeyWarps);
@@ -292,6 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + kKeyWarps : 8 + kKeyWarps);
     }
     mbar_init(&sh->raw, 1);
+    mbar_init(&sh->raw_empty, 12);
+    mbar_init(&sh->values_full, 4);
     mbar_init(&sh->p_full, 4);
     mbar_init(&sh->p_empty, 1);
     mbar_init(&sh->state_full, 8);
@@ -341,22 +347,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   uint32_t it = 0;  // chunks so far
 
-  // f16: eight rows of 16 bytes a turn, thread `tid` of `threads`; rows past `n` become zeros.
-  const auto split_block = [&](uint8_t* dst, uint32_t part, int n, int tid, int threads) {
+  // f16: a loaded block into its parts, 16 bytes a turn of each of `threads`; rows past `n` become zeros.
+  const auto split_block = [&](const uint8_t* src, uint8_t* dst, uint32_t part, int n, int tid, int threads) {
 #pragma unroll 2
     for (int v = tid; v < static_cast<int>(kBlock / 16); v += threads) {
-      uint4* at = reinterpret_cast<uint4*>(dst + 16 * v);
-      uint4 lo, hi = *at;
+      uint4 lo, hi = *reinterpret_cast<const uint4*>(src + 16 * v);
       if (v / 8 >= n) hi = make_uint4(0, 0, 0, 0);
       split_f16(hi, &hi, &lo);
-      *at = hi;
+      *reinterpret_cast<uint4*>(dst + 16 * v) = hi;
       *reinterpret_cast<uint4*>(dst + part + 16 * v) = lo;
     }
+  };
+  const uint8_t* const raw_tiles = smem + C::kRawAt;
+  constexpr uint32_t kRawQ = C::kKb * kBlock, kRawV = 2 * kRawQ;
+  // f16: the tiles have been loaded and the places of their parts are free
+  const auto wait_for_raw = [&]() {
+    wait(&sh->raw, it);
+    wait(&sh->empty[0], it ^ 1u);
   };
   // Decayed keys of rows [r0, r1) of the chunk that begins at c, by vectors of eight.
   constexpr int kVec = kDk / 8;
   const auto decay_keys = [&](int c, int r0, int r1, int tid, int threads) {
-    const uint32_t slot = it % kGates, stage = it % kStages, buffer = it & 1u;
+    const uint32_t slot = it % kGates, stage = it % kStages, buffer = it % C::kKeyBufs;
     const int n = min(kC, x.n - c), col = tid % kVec;
     const Gate& t = sh->gate[slot];
     uint8_t* src = smem + stage * C::kStage + kBlock + col / 8 * (2 * kBlock);
@@ -365,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = r0 + tid / kVec; r < r1; r += threads / kVec) {
       const uint32_t o = place(r, col & 7);
       const uint64_t w2 = pair(t.after[r], t.after[r]);
-      uint4 h = *reinterpret_cast<const uint4*>(src + o);
+      uint4 h = *reinterpret_cast<const uint4*>(kIn == 1 ? src + o : raw_tiles + col / 8 * kBlock + o);
       if (r >= n) h = make_uint4(0, 0, 0, 0);
       uint32_t part[3][4];
       const uint32_t in[4] = {h.x, h.y, h.z, h.w};
@@ -396,16 +408,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
   const auto wait_for_keys = [&]() {
-    const uint32_t slot = it % kGates, stage = it % kStages, buffer = it & 1u;
+    const uint32_t slot = it % kGates;
     wait(&sh->gate_full[slot], it / kGates);
-    wait(kIn == 1 ? &sh->keys_full[stage] : &sh->raw, kIn == 1 ? it / kStages : it);
-    wait(&sh->key_empty[buffer], (it >> 1) ^ 1u);
+    if (kIn == 1) wait(&sh->keys_full[it % kStages], it / kStages);
+    else wait_for_raw();
+    wait(&sh->key_empty[it % C::kKeyBufs], (it / C::kKeyBufs) ^ 1u);
   };
   // What this warp wrote of the keys (and, f16, of other tiles) can be used.
   const auto give_keys = [&]() {
     fence_proxy_async_smem();
-    arrive(&sh->key_full[it & 1u]);
-    if (lane == 0) mbar_arrive(kIn == 2 ? &sh->full[it % kStages] : &sh->keys_empty[it % kStages]);
+    arrive(&sh->key_full[it % C::kKeyBufs]);
+    if (lane == 0) {
+      mbar_arrive(kIn == 2 ? &sh->full[it % kStages] : &sh->keys_empty[it % kStages]);
+      if (kIn == 2) mbar_arrive(&sh->raw_empty);
+    }
   };
 
   const auto products = [&]() {
@@ -423,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         decay_keys(c, kC - kKeysByP, kC, tid, 128);
         if (kIn == 2) {
           uint8_t* base = smem + it % kStages * C::kStage;
-          for (int b = 0; b < C::kKb; ++b) split_block(base + 2 * b * kBlock, C::kQk, min(kC, x.n - c), tid, 128);
+          for (int b = 0; b < C::kKb; ++b)
+            split_block(raw_tiles + kRawQ + b * kBlock, base + 2 * b * kBlock, C::kQk, min(kC, x.n - c), tid, 128);
         }
         give_keys();
         wait(&sh->score_full[buffer], it >> 1);
@@ -491,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         decay_keys(c, 0, kOut ? kC - kKeysByP : kC, tid, kThreads1);
         if (kIn == 2 && !kOut)
-          for (int b = 0; b < C::kVb; ++b) split_block(v + b * kBlock, C::kV, n, tid, kThreads1);
+          for (int b = 0; b < C::kVb; ++b) split_block(raw_tiles + kRawV + b * kBlock, v + b * kBlock, C::kV, n, tid, kThreads1);
         if (kIn == 1 && n < kC) {  // values past the piece: 0 times what they hold may be NaN
           wait(&sh->full[it % kStages], it / kStages);
           if (!ok) break;
@@ -524,12 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t pol = policy_evict_normal();
           uint64_t* bar = kIn == 2 ? &sh->raw : &sh->keys_full[stage];
           constexpr uint32_t kKeyBytes = C::kKb * kBlock, kRestBytes = ((kOut ? C::kKb : 0) + C::kVb) * kBlock;
-          wait(kIn == 2 ? &sh->empty[stage] : &sh->keys_empty[stage], (it / kStages) ^ 1u);
+          wait(kIn == 2 ? &sh->raw_empty : &sh->keys_empty[stage], (it / kStages) ^ 1u);
           if (!ok) break;
           if (elect_one()) {
             mbar_arrive_expect_tx(bar, kIn == 2 ? kKeyBytes + kRestBytes : kKeyBytes);
 #pragma unroll
-            for (int b = 0; b < C::kKb; ++b) tma_load_3d(base + (2 * b + 1) * kBlock, &tm_k, bar, 64 * b, hk, row, pol);
+            for (int b = 0; b < C::kKb; ++b)
+              tma_load_3d(kIn == 2 ? smem + C::kRawAt + b * kBlock : base + (2 * b + 1) * kBlock, &tm_k, bar, 64 * b, hk, row, pol);
           }
           __syncwarp();
           if (kIn == 1) {
@@ -540,9 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             if (kIn == 1) mbar_arrive_expect_tx(bar, kRestBytes);
 #pragma unroll
-            for (int b = 0; kOut && b < C::kKb; ++b) tma_load_3d(base + 2 * b * kBlock, &tm_q, bar, 64 * b, hq, row, pol);
+            for (int b = 0; kOut && b < C::kKb; ++b)
+              tma_load_3d(kIn == 2 ? smem + C::kRawAt + kRawQ + b * kBlock : base + 2 * b * kBlock, &tm_q, bar, 64 * b, hq, row, pol);
 #pragma unroll
-            for (int b = 0; b < C::kVb; ++b) tma_load_3d(base + kIn * C::kQk + b * kBlock, &tm_v, bar, 64 * b, hv, row, pol);
+            for (int b = 0; b < C::kVb; ++b)
+              tma_load_3d(kIn == 2 ? smem + C::kRawAt + kRawV + b * kBlock : base + kIn * C::kQk + b * kBlock, &tm_v, bar, 64 * b, hv, row, pol);
           }
           __syncwarp();
         }
@@ -647,10 +667,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int chunks = (x.n + kC - 1) / kC;
         if (kOut && chunks > 0) scores();
         for (int c = 0; ok && c < chunks; ++c, ++it) {
-          const uint32_t stage = it % kStages, buffer = it & 1u;
+          const uint32_t stage = it % kStages, buffer = it % C::kKeyBufs;
           const uint32_t v0 = cols_lo + (stage * C::kStage + kIn * C::kQk) / 16;
           wait(&sh->full[stage], it / kStages);
-          wait(&sh->key_full[buffer], it >> 1);
+          wait(&sh->key_full[buffer], it / C::kKeyBufs);
+          if (kIn == 2 && kOut) wait(&sh->values_full, it);
           wait(&sh->update_empty, it ^ 1u);
           tc_fence_after();
           if (ok && elect_one()) {
@@ -704,7 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           wait(&sh->p_full, it);
-          wait(&sh->key_full[it & 1u], it >> 1);  // the values past the piece have been cleared
+          wait(&sh->key_full[it % C::kKeyBufs], it / C::kKeyBufs);  // the values past the piece have been cleared
+          if (kIn == 2) wait(&sh->values_full, it);
           tc_fence_after();
           if (ok && elect_one()) {
             const uint32_t p0 = base_lo + C::kPAt / 16;
@@ -741,12 +763,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t slot = it % kGates;
         const int n = min(kC, x.n - c) - (lane & 3);
         if (kIn == 2) {  // these warps split the values
-          wait(&sh->raw, it);
+          wait_for_raw();
           if (!ok) break;
           uint8_t* v = smem + it % kStages * C::kStage + kIn * C::kQk;
-          for (int b = 0; b < C::kVb; ++b) split_block(v + b * kBlock, C::kV, min(kC, x.n - c), threadIdx.x - 16 * 32, 128);
+          for (int b = 0; b < C::kVb; ++b)
+            split_block(raw_tiles + kRawV + b * kBlock, v + b * kBlock, C::kV, min(kC, x.n - c), threadIdx.x - 16 * 32, 128);
           fence_proxy_async_smem();
-          arrive(&sh->full[it % kStages]);
+          arrive(&sh->values_full);
+          if (lane == 0) mbar_arrive(&sh->raw_empty);
         }
         wait(&sh->gate_full[slot], it / kGates);
         wait(&sh->out_full[it & 1u], it >> 1);
