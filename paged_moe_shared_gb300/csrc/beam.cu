@@ -22,8 +22,8 @@ namespace {
 constexpr int kChunk = 1024;           // tokens of a first-kernel warp
 constexpr int kScanThreads = 256;
 constexpr int kPickThreads = 1024;
-constexpr int kLeaders = 256;          // subsets whose best give the sieve
-constexpr int kShare = kPickThreads / kLeaders;
+constexpr int kLeaders = 256;          // subsets whose best give the sieve, where n_select is above 32; else half
+static_assert(kPickThreads == 4 * kLeaders, "");
 constexpr int kMostSelect = 128;
 constexpr int kList = 1024;            // candidates that are ranked by counting
 constexpr int kMostBeams = 128;
@@ -110,6 +110,27 @@ __device__ __forceinline__ float max8(const Raw<float>& r) {
   return m;
 }
 
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, uint64_t (&x)[4]) {
+  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = dev::pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack(const Raw<__half>& r, uint64_t (&x)[4]) {
+  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+    x[i] = dev::pair(f.x, f.y);
+  }
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, uint64_t (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[2 * i] = dev::pair(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+    x[2 * i + 1] = dev::pair(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
+  }
+}
+
 // A warp goes from chunk to chunk and loads the next one before it works on its own.
 // exp(x - m) is 2^(x L - fl(m L)) with L = log2(e) in fp32: one multiply-add; what the
 // rounding of m L puts into every term alike is taken out of the sum.
@@ -118,11 +139,12 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
   dev::grid_dep_launch();
   const int lane = threadIdx.x & 31;
   constexpr int kVec = kChunk / 256;  // vectors of eight of a lane
-  const int64_t total = static_cast<int64_t>(a.groups) * a.beams * a.n_chunks;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kScanThreads / 32);
+  const int rows = a.groups * a.beams, stride = gridDim.x * (kScanThreads / 32);
+  const int step_rows = stride / a.n_chunks, step_chunks = stride - step_rows * a.n_chunks;
   Raw<T> next[kVec];
-  const auto load = [&](int64_t at) {
-    const int row = static_cast<int>(at / a.n_chunks), chunk = static_cast<int>(at - static_cast<int64_t>(row) * a.n_chunks);
+  const int first = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5);
+  int row = first / a.n_chunks, chunk = first - row * a.n_chunks;
+  const auto load = [&]() {
     if (a.done && a.done[row]) return false;
     int skip;
     const T* base = row_base<T>(a, row, &skip);
@@ -130,14 +152,16 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     for (int j = 0; j < kVec; ++j) next[j] = load8(base, chunk * kChunk + j * 256 + lane * 8, skip, skip + a.vocab);
     return true;
   };
-  int64_t at = static_cast<int64_t>(blockIdx.x) * (kScanThreads / 32) + (threadIdx.x >> 5);
-  bool live = at < total && load(at);
-  for (; at < total; at += stride) {
+  bool live = row < rows && load();
+  while (row < rows) {
     Raw<T> raw[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) raw[j] = next[j];
     const bool mine = live;
-    live = at + stride < total && load(at + stride);
+    const int64_t at = static_cast<int64_t>(row) * a.n_chunks + chunk;
+    row += step_rows, chunk += step_chunks;
+    if (chunk >= a.n_chunks) chunk -= a.n_chunks, ++row;
+    live = row < rows && load();
     if (!mine) continue;
     float m = -INFINITY;  // fmaxf takes the number where the other is a NaN
 #pragma unroll
@@ -146,15 +170,22 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     m = fminf(m, 3.402823466e38f);
     const float scaled = m * kLog2e;
-    float s = 0.f;
+    uint64_t sums[kVec];
+    const uint64_t scale2 = dev::pair(kLog2e, kLog2e), minus2 = dev::pair(-scaled, -scaled);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      const T* x = reinterpret_cast<const T*>(&raw[j]);
-      float u = 0.f;
+      uint64_t x[4];
+      unpack(raw[j], x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u += ex2(fmaf(to_f(x[e]), kLog2e, -scaled));
-      s += u;
+      for (int e = 0; e < 4; ++e) {
+        const float2 y = dev::split(dev::fma2(x[e], scale2, minus2));
+        const uint64_t z = dev::pair(ex2(y.x), ex2(y.y));
+        sums[j] = e == 0 ? z : dev::add2(sums[j], z);
+      }
     }
+#pragma unroll
+    for (int j = 1; j < kVec; ++j) sums[0] = dev::add2(sums[0], sums[j]);
+    float s = dev::split(sums[0]).x + dev::split(sums[0]).y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     s *= ex2(-fmaf(m, kLog2e, -scaled));
@@ -262,27 +293,26 @@ __device__ void one_by_one(PickShared& s, int n, int want, const Item& item) {
 }
 
 // A lower bound of the want-th best of a stream of which each thread has seen a part; `m`
-// is the best of that part, from below.  The best of 256 subsets are ranked; a subset is
-// what threads 256 apart have seen, so that neighbours, which may all be good, count apart.
+// is the best of that part, from below.  The best of 128 or 256 subsets are ranked; a subset
+// is what threads so far apart have seen: neighbours, which may all be good, count apart.
 __device__ float bound_of(PickShared& s, float m, int want) {
   const int tid = threadIdx.x;
   s.seen[tid] = m;
   __syncthreads();
-  if (tid < kLeaders) {
+  const int shift = want > 32 ? 2 : 3, leaders = kPickThreads >> shift, share = 1 << shift;
+  if (tid < leaders) {
     m = s.seen[tid];
-#pragma unroll
-    for (int k = 1; k < kShare; ++k) m = fmaxf(m, s.seen[tid + k * kLeaders]);
+    for (int k = 1; k < share; ++k) m = fmaxf(m, s.seen[tid + k * leaders]);
     s.leader[tid] = m;
   }
   __syncthreads();
-  // kShare threads count for a leader, a part of the others each
-  const int me = tid / kShare;
+  // `share` threads count for a leader, a part of the others each
+  const int me = tid >> shift;
   const float mine = s.leader[me];
   int above = 0;
 #pragma unroll 8
-  for (int i = tid % kShare; i < kLeaders; i += kShare) above += s.leader[i] > mine || (s.leader[i] == mine && i < me);
-#pragma unroll
-  for (int o = 1; o < kShare; o <<= 1) above += __shfl_xor_sync(~0u, above, o);
+  for (int i = tid & (share - 1); i < leaders; i += share) above += s.leader[i] > mine || (s.leader[i] == mine && i < me);
+  for (int o = 1; o < share; o <<= 1) above += __shfl_xor_sync(~0u, above, o);
   if (above == want - 1) s.sieve = mine;
   __syncthreads();
   return s.sieve;
@@ -363,6 +393,11 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   const auto worth = [&](int b, float x) {
     return ordered((static_cast<double>(x) - static_cast<double>(s.m[b])) + s.c[b]);
   };
+  const uint32_t per = 0xFFFFFFFFu / static_cast<uint32_t>(N);
+  const auto beam_of = [&](int i) {  // i / N
+    const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(i), per));
+    return q + ((q + 1) * static_cast<int64_t>(N) <= i) + ((q + 2) * static_cast<int64_t>(N) <= i);
+  };
   const auto passes = [&](int b, float x, float sieve) {
     float err;
     const float r = sum32(b, x, &err);
@@ -379,13 +414,14 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     float best = -INFINITY;
     for (int i = tid; i < n_tops; i += kPickThreads) {
       float err;
-      const float r = sum32(i / N, chunk_top(i, i / N), &err);
+      const int b = beam_of(i);
+      const float r = sum32(b, chunk_top(i, b), &err);
       best = fmaxf(best, r - err);
     }
     sieve = bound_of(s, best, want);
   }
   const auto chunk = [&](int i, Candidate* c) {
-    const int b = i / N;
+    const int b = beam_of(i);
     const float x = chunk_top(i, b);
     if (!passes(b, x, sieve)) return false;
     *c = Candidate{worth(b, x), i};
