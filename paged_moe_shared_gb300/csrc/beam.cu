@@ -552,8 +552,11 @@ struct ReorderArgs {
 };
 constexpr int kReorderThreads = 256;
 
-// One CTA a (layer, child): the row of the table, and the page that is partly filled.
-__global__ void __launch_bounds__(kReorderThreads) kv_reorder_kernel(const __grid_constant__ ReorderArgs a) {
+// One CTA a (layer, child): the row of the table, and the page that is partly filled.  Few CTAs
+// have kPer = 8 vectors a thread in flight, a page of 32 KiB at once (one layer of 4 beams 2.7 us,
+// with 4 vectors 3.3); many share the SMs better with 4 (48 layers of 32 beams 11.2 us, 11.7 with 8).
+template <int kPer>
+__global__ void __launch_bounds__(kReorderThreads, kPer == 4 ? 8 : 4) kv_reorder_kernel(const __grid_constant__ ReorderArgs a) {
   const int layer = blockIdx.y, child = blockIdx.x, tid = threadIdx.x;
   const int64_t out_row = static_cast<int64_t>(layer) * a.n + child;
   const int fresh = a.fresh[out_row];
@@ -593,7 +596,6 @@ __global__ void __launch_bounds__(kReorderThreads) kv_reorder_kernel(const __gri
       const int words = 2 * a.g.kv_heads * P * a.g.head_dim / 16;
       const uint4* x = reinterpret_cast<const uint4*>(a.g.pool + static_cast<uint64_t>(src) * a.g.page_bytes);
       uint4* y = reinterpret_cast<uint4*>(a.g.pool + static_cast<uint64_t>(fresh) * a.g.page_bytes);
-      constexpr int kPer = 8;
 #pragma unroll 1
       for (int i0 = 0; i0 < words; i0 += kPer * kReorderThreads) {
         uint4 v[kPer];
@@ -720,7 +722,10 @@ extern "C" int rimuru_kv_reorder(rimuru_view_t view, const int32_t* parents, int
   a.stride = table_stride;
   a.g = kv_geom(v);
   a.max_len = max_len(v, table_stride);
-  kv_reorder_kernel<<<dim3(num_seqs, num_layers), kReorderThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const dim3 grid(num_seqs, num_layers);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (static_cast<int64_t>(num_seqs) * num_layers <= 4ll * v.kv->sms) kv_reorder_kernel<8><<<grid, kReorderThreads, 0, s>>>(a);
+  else kv_reorder_kernel<4><<<grid, kReorderThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("reordering launch", e));
   return RIMURU_OK;

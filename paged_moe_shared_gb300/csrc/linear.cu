@@ -123,11 +123,17 @@ cudaError_t launch_steps(const LinearArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// How a call is cut; the number of SMs is the device's, or the usual one without a device.
-LinearCut cut_of(const View& v, int num_seqs, int num_tokens, int max_new) {
-  if (max_new <= kStepsMost) return {};
+// The device's number of SMs, or the usual one without a device.
+int sms_here() {
   const int sms = rimuru_device_sm_count();
-  return linear_cut(v.state_heads, v.key_dim, v.value_dim, sms > 0 ? sms : 152, num_seqs, num_tokens, max_new);
+  return sms > 0 ? sms : 152;
+}
+bool by_steps(const View& v, int num_seqs, int max_new) {
+  return max_new <= steps_most(v.state_heads, v.key_dim, v.value_dim, sms_here(), num_seqs);
+}
+LinearCut cut_of(const View& v, int num_seqs, int num_tokens, int max_new) {
+  if (by_steps(v, num_seqs, max_new)) return {};
+  return linear_cut(v.state_heads, v.key_dim, v.value_dim, sms_here(), num_seqs, num_tokens, max_new);
 }
 
 int state_ready(View* v) {
@@ -248,8 +254,7 @@ extern "C" int rimuru_linear_attention(rimuru_view_t view, const rimuru_heads* q
   a.sms = v.kv->sms;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int dtype = num_tokens > 0 ? q->dtype : RIMURU_BF16;
-  // One by one a token costs about 0.6 us, a chunk of 64 with its start several us.
-  if (max_new > kStepsMost)
+  if (!by_steps(v, num_seqs, max_new))
     return launch_linear_chunks(a, cut_of(v, num_seqs, num_tokens, max_new), workspace, dtype, s);
   const cudaError_t e = launch_linear_steps(a, dtype, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("linear attention launch", e));

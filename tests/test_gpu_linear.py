@@ -296,3 +296,80 @@ def test_prompt_then_steps_equals_the_whole():
         c.run(cu=False)
     c.T, c.new, c.out = 90, [90], out
     c.check(want, True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(2, 1, 64, 128), (1, 1, 128, 64), (2, 2, 128, 128)])
+def test_pieces(shape, kind):
+    """Sequences long enough to be cut into pieces, in place, one from zeros, one that is short."""
+    c = Case([1300, 40, 2000], *shape, kind=kind, rate=0.02)
+    c.state_out = c.state_in.clone()
+    c.state_in[0] = -1
+    c.state_out[0] = [p for p in range(c.pages) if p not in c.state_in.tolist()][0]
+    want = c.plain()
+    c.run()
+    c.check(want, True)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [5, 3, 2], [70, 30, 65], [1200, 17, 700]])
+def test_a_sequence_of_nan_stays_alone(new):
+    """NaN and infinities in one sequence's tokens, and in the rows around the call's, reach no other."""
+    for hurt in range(3):
+        c = Case(new, 4, 2, 64, 128, rate=0.02)
+        want = c.plain()
+        rows = torch.tensor([0] + new).cumsum(0).tolist()
+        at = slice(rows[hurt], rows[hurt + 1])
+        for t, x in ((c.q, math.nan), (c.k, math.inf), (c.v, math.nan), (c.g, math.nan)):
+            t[at] = x
+        c.run()
+        torch.cuda.synchronize()
+        assert bool(c.out[at].isnan().all()) and bool(c.states()[c.state_out[hurt]].isnan().all())
+        for b in range(3):
+            if b != hurt:
+                at = slice(rows[b], rows[b + 1])
+                assert float((c.out[at].double() - want[0][at]).abs().max()) < 0.05
+                assert float((c.states()[c.state_out[b]].double() - want[2][int(c.state_out[b])][0]).abs().max()) < 1e-3
+        assert R.rimuru_get_device_error(c.view) == R.DEV_OK
+
+
+@pytest.mark.parametrize("new", [[3], [100]])
+def test_decays_above_zero_count_as_zero(new):
+    c = Case(new, 2, 1, 64, 64)
+    c.g[::3] = 0.0
+    want = c.plain()
+    c.g[::3] = 5.0
+    c.g[0, 1] = math.inf
+    c.run()
+    c.check(want, max(new) > 16)
+
+
+def test_many_sequences_equal_their_halves():
+    """More units than one CTA lists; what a sequence gives does not depend on the others of the call."""
+    g = torch.Generator().manual_seed(0)
+    new = torch.randint(0, 24, (1400,), generator=g).tolist()
+    new[7], new[1300] = 130, 64
+    c = Case(new, 8, 4, 64, 64)
+    c.run()
+    torch.cuda.synchronize()
+    out, states = c.out.clone(), c.mem[c.state_out.long()].clone()
+    assert bool(out.isfinite().all())
+    n = c.T
+    c.out.zero_()
+    c.mem[c.state_out.long()] = 0
+    cu, si, so = c.cu, c.state_in, c.state_out
+    for at in (slice(0, 500), slice(500, 1400)):
+        c.cu, c.state_in, c.state_out = cu[at.start:at.stop + 1].contiguous(), si[at].contiguous(), so[at].contiguous()
+        c.B = at.stop - at.start
+        c.run(max_new=130)
+    torch.cuda.synchronize()
+    assert c.T == n and torch.equal(c.out, out) and torch.equal(c.mem[so.long()], states)
+    assert R.rimuru_get_device_error(c.view) == R.DEV_OK
+
+
+def test_few_tokens_of_many_sequences():
+    """Where every SM has many states the chunked form begins at fewer tokens."""
+    for new, chunked in ([4] * 96, False), ([7] * 96, True):
+        c = Case(new, 8, 4, 128, 128)
+        want = c.plain()
+        c.run()
+        c.check(want, chunked)
