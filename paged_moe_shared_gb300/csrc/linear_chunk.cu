@@ -311,14 +311,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sh->tmem_base, 512);
     tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < kUnits; i += kThreads) {
-    const int u = blockIdx.x + i * gridDim.x;
-    Unit x{};
-    if (u < p.units) {
-      x = find_unit(p, u, kOut);
-      x.ok = x.ok && (kOut || !x.last);  // the first kernel is about pieces that others follow
+  // Units, the longest pieces first and every other round backwards: a CTA that got a long one
+  // gets a short one next (seven prompts of 558 to 1663 tokens, 32 heads: 95 us, in the order of the
+  // sequences 110).  More pieces than threads even out by themselves.
+  const int slots = p.units / a.heads, ctas = gridDim.x;
+  const bool sorted = slots <= kThreads && p.units > ctas;
+  int* const length = reinterpret_cast<int*>(smem);  // nothing has been loaded yet
+  int* const order = length + kThreads;
+  if (sorted) {
+    const int slot = threadIdx.x;
+    int mine = 0;
+    if (slot < slots) {
+      const Unit y = find_unit(p, slot * a.heads, false);
+      mine = y.ok && (kOut || !y.last) ? y.n : 0;
+      length[slot] = mine;
     }
-    sh->units[i] = x;
+    __syncthreads();
+    if (slot < slots) {
+      int before = 0;
+      for (int j = 0; j < slots; ++j) before += length[j] > mine || (length[j] == mine && j < slot);
+      order[before] = slot;
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < kUnits; i += kThreads) {
+    const int64_t u = static_cast<int64_t>(i) * ctas + (sorted && i % 2 ? ctas - 1 - blockIdx.x : blockIdx.x);
+    Unit y{};
+    if (u < p.units) {
+      const int v = static_cast<int>(u);
+      y = find_unit(p, sorted ? order[v / a.heads] * a.heads + v % a.heads : v, kOut);
+      y.ok = y.ok && (kOut || !y.last);  // the first kernel is about pieces that others follow
+    }
+    sh->units[i] = y;
   }
   tc_fence_before();
   __syncthreads();
