@@ -7,8 +7,8 @@
 // first kernel streams the logits once, a warp for each chunk of 1024 tokens, and keeps
 // the chunk's maximum and sum of exponentials.  The n best candidates lie in the n best
 // chunks (by maximum, then by position: whoever is outside has n better chunk leaders
-// before it), so the second kernel, one CTA a batch entry, picks those chunks, reads them
-// again and ranks what may be among the n best.  Comparisons that decide are made on
+// before it), so the second kernel, one CTA a batch entry, finds a worth that n leaders
+// reach, reads the chunks whose leaders reach it again and ranks what does.  Comparisons that decide are made on
 // doubles; fp32 only sieves, with a margin.
 //
 // 32 entries of 8 beams over 151,936 tokens in bf16 (78 MB), 16 best: 24.3 us, of which the
@@ -237,7 +237,8 @@ struct PickShared {
   double c[kMostBeams];  // a candidate is worth (x - m) + c
   float c32[kMostBeams], m[kMostBeams];
   uint8_t done[kMostBeams];
-  float leader[kLeaders], seen[kPickThreads];
+  float leader[kLeaders];
+  int chunks[kList];
   Candidate list[kList], chosen[kMostSelect], next[kPickThreads / 32];
   int count, n_chosen;
   float sieve;
@@ -299,27 +300,22 @@ __device__ void one_by_one(PickShared& s, int n, int want, const Item& item) {
 }
 
 // A lower bound of the want-th best of a stream of which each thread has seen a part; `m`
-// is the best of that part, from below.  The best of 128 or 256 subsets are ranked; a subset
-// is what threads so far apart have seen: neighbours, which may all be good, count apart.
+// is the best of that part, from below.  The best of 128 or 256 subsets, neighbouring lanes'
+// parts, are ranked, so neighbours should have seen things that have little to do with one
+// another.
 __device__ float bound_of(PickShared& s, float m, int want) {
   const int tid = threadIdx.x;
-  s.seen[tid] = m;
-  __syncthreads();
   const int shift = want > 32 ? 2 : 3, leaders = kPickThreads >> shift, share = 1 << shift;
-  if (tid < leaders) {
-    m = s.seen[tid];
-    for (int k = 1; k < share; ++k) m = fmaxf(m, s.seen[tid + k * leaders]);
-    s.leader[tid] = m;
-  }
+  for (int o = 1; o < share; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  const int me = tid >> shift;
+  if ((tid & (share - 1)) == 0) s.leader[me] = m;
   __syncthreads();
   // `share` threads count for a leader, a part of the others each
-  const int me = tid >> shift;
-  const float mine = s.leader[me];
   int above = 0;
 #pragma unroll 8
-  for (int i = tid & (share - 1); i < leaders; i += share) above += s.leader[i] > mine || (s.leader[i] == mine && i < me);
+  for (int i = tid & (share - 1); i < leaders; i += share) above += s.leader[i] > m || (s.leader[i] == m && i < me);
   for (int o = 1; o < share; o <<= 1) above += __shfl_xor_sync(~0u, above, o);
-  if (above == want - 1) s.sieve = mine;
+  if (above == want - 1) s.sieve = m;
   __syncthreads();
   return s.sieve;
 }
@@ -335,7 +331,6 @@ __device__ __forceinline__ double log_of(float y) {
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
   __shared__ PickShared s;
-  __shared__ int chunk_of[kMostSelect];
   const int entry = blockIdx.x, tid = threadIdx.x, lane = tid % 32;
   const int row0 = entry * a.beams;
   const int N = a.n_chunks, n_tops = a.beams * N;
@@ -413,12 +408,14 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     return fits ? s.tops[i] : s.done[b] ? (i == b * N ? 0.f : -INFINITY) : all_tops[i];
   };
 
-  // ---- the `want` best chunks
-  const int want = a.n_select;
+  // ---- the chunks that may hold one of the `want` best: those whose leaders pass a sieve that
+  // `want` leaders pass.  Lanes that share a leader look at chunks 128 or 256 apart: a beam's own
+  // chunks, which may all be good, then count apart.
+  const int want = a.n_select, mixed = want > 32 ? (tid & 3) << 8 | tid >> 2 : (tid & 7) << 7 | tid >> 3;
   float sieve = -INFINITY;
-  if (n_tops > 64) {  // below, all are ranked sooner
+  if (n_tops > 64) {  // below, all may
     float best = -INFINITY;
-    for (int i = tid; i < n_tops; i += kPickThreads) {
+    for (int i = mixed; i < n_tops; i += kPickThreads) {
       float err;
       const int b = beam_of(i);
       const float r = sum32(b, chunk_top(i, b), &err);
@@ -434,16 +431,21 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     return true;
   };
   for (int i = tid; i < n_tops; i += kPickThreads) {
-    Candidate c;
-    if (chunk(i, &c)) note(s, c);
+    const int b = beam_of(i);
+    if (passes(b, chunk_top(i, b), sieve)) {
+      const int at = atomicAdd(&s.count, 1);
+      if (at < kList) s.chunks[at] = i;
+    }
   }
   __syncthreads();
-  if (!rank(s, want)) one_by_one(s, n_tops, want, chunk);
-  const int n_chosen = s.n_chosen;
-  if (tid < n_chosen) chunk_of[tid] = s.chosen[tid].index;
-  // with `want` chunks the last one's leader is worth no more than the want-th best
-  sieve = n_chosen == want ? __double2float_rd(unordered(s.chosen[want - 1].key)) : -INFINITY;
-  __syncthreads();
+  int n_chosen = s.count;
+  if (n_chosen > kList) {  // chunks that are alike: the `want` best, whose last one's leader is a sieve too
+    one_by_one(s, n_tops, want, chunk);
+    n_chosen = s.n_chosen;
+    if (tid < n_chosen) s.chunks[tid] = s.chosen[tid].index;
+    if (n_chosen == want) sieve = fmaxf(sieve, __double2float_rd(unordered(s.chosen[want - 1].key)));
+    __syncthreads();
+  }
   if (tid == 0) s.count = s.n_chosen = 0;
 
   // ---- the candidates of those chunks, a warp for each; an index is beam * vocab + token.
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     if (turn == 1) {
       float best = -INFINITY;
       for (int k = tid / 32; k < n_chosen; k += kPickThreads / 32) {
-        const int g = chunk_of[k], b = g / N;
+        const int g = s.chunks[k], b = g / N;
         float top = s.done[b] && lane == 0 ? 0.f : -INFINITY;
         if (!s.done[b]) {
           Raw<T> x[kVec];
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       __syncthreads();
     }
     for (int k = tid / 32; k < n_chosen; k += kPickThreads / 32) {
-      const int g = chunk_of[k], b = g / N;
+      const int g = s.chunks[k], b = g / N;
       if (s.done[b]) {
         if (lane == 0) note(s, Candidate{worth(b, 0.f), b * a.vocab + a.pad});
         continue;
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   }
   if (!rank(s, want))
     one_by_one(s, n_chosen * kChunk, want, [&](int i, Candidate* c) {
-      const int g = chunk_of[i / kChunk], b = g / N, e = i % kChunk;
+      const int g = s.chunks[i / kChunk], b = g / N, e = i % kChunk;
       float f = e == 0 ? 0.f : -INFINITY;
       int token = a.pad;
       if (!s.done[b]) {
