@@ -728,7 +728,8 @@ int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int 
  * registers, more of them in chunks on the tensor cores; no choice needs the host.
  *   q, k      device [num_tokens][key heads][key_dim], RIMURU_BF16 or RIMURU_F16; the view's heads
  *             are a multiple of their heads
- *   v, out    device [num_tokens][heads][value_dim], the same type
+ *   v, out    device [num_tokens][heads][value_dim], the same type; out overlaps no input.  Tokens of
+ *             q, k and v may not lie on one another (a token stride of 0); heads may
  *   log_decay device float: g of token t and head h is log_decay[t * decay_token_stride + h *
  *             decay_head_stride].  A stride of 0 makes it one for all tokens (heads).  Any value
  *             <= 0, also -inf (the state starts anew with that token); one above 0 counts as 0

@@ -6,7 +6,7 @@
 // A thread holds four neighbouring columns of several key rows; per token it adds k v^T
 // and multiplies by q, and the parts of out that the CTA's rows give are added up in
 // shared memory.  A decode step moves 8 bytes for each state element and little else: 64
-// sequences of 32 heads of 128 x 128 (268 MB) 45.4 us, 0.87 of the copy rate; one sequence 3.2 us;
+// sequences of 32 heads of 128 x 128 (268 MB) 43.6 us, 0.91 of the copy rate; one sequence 3.2 us;
 // 16 sequences of 3 to 5 tokens, 16 heads of 64 x 128, 6.3 us, of which 2.6 are bytes.
 #include <algorithm>
 #include <cmath>
@@ -26,8 +26,8 @@ __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ void from_f(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f(float x, __half* y) { *y = __float2half_rn(x); }
 
-// kCols value columns of one head's state a CTA.
-template <typename T, int kKey, int kCols>
+// kCols value columns of one head's state a CTA.  kStream: states pass through L2 without staying.
+template <typename T, int kKey, int kCols, bool kStream>
 __global__ void __launch_bounds__(kStepThreads) linear_steps_kernel(const __grid_constant__ LinearArgs a) {
   constexpr int kLanes = kCols / 4;              // threads of a state row
   constexpr int kParts = kStepThreads / kLanes;  // threads that share a column
@@ -51,8 +51,10 @@ __global__ void __launch_bounds__(kStepThreads) linear_steps_kernel(const __grid
   const int64_t step = static_cast<int64_t>(kParts) * a.value_dim;
   float4 S[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    S[i] = s.in ? *reinterpret_cast<const float4*>(s.in + at + i * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kRows; ++i) {
+    const float4* from = reinterpret_cast<const float4*>(s.in + at + i * step);
+    S[i] = !s.in ? make_float4(0.f, 0.f, 0.f, 0.f) : kStream ? __ldcs(from) : *from;
+  }
 
   const T* q = static_cast<const T*>(a.q) + s.row * a.q_ts + h / a.per_key_head * a.q_hs;
   const T* k = static_cast<const T*>(a.k) + s.row * a.k_ts + h / a.per_key_head * a.k_hs;
@@ -109,7 +111,11 @@ __global__ void __launch_bounds__(kStepThreads) linear_steps_kernel(const __grid
     }
   }
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(s.out + at + i * step) = S[i];
+  for (int i = 0; i < kRows; ++i) {
+    float4* to = reinterpret_cast<float4*>(s.out + at + i * step);
+    if (kStream) __stcs(to, S[i]);
+    else *to = S[i];
+  }
 }
 
 template <typename T, int kKey>
@@ -120,8 +126,12 @@ cudaError_t launch_steps(const LinearArgs& a, cudaStream_t s) {
   // 54.8).  Where that leaves SMs without two CTAs, slices of 32.
   const bool wide = units * (a.value_dim / 64) >= 2ll * a.sms;
   const unsigned grid = static_cast<unsigned>(units * (a.value_dim / (wide ? 64 : 32)));
-  if (wide) linear_steps_kernel<T, kKey, 64><<<grid, kStepThreads, 0, s>>>(a);
-  else linear_steps_kernel<T, kKey, 32><<<grid, kStepThreads, 0, s>>>(a);
+  // States that pass L2 by go faster where there are many (the same 45.4 -> 43.6 us, 16 sequences
+  // 15.5 -> 14.3); 17 MB of them, read again soon, slower (6.3 -> 6.8).
+  const bool stream = units * kKey * a.value_dim * 8 > 32ll << 20;
+  if (!wide) linear_steps_kernel<T, kKey, 32, false><<<grid, kStepThreads, 0, s>>>(a);
+  else if (stream) linear_steps_kernel<T, kKey, 64, true><<<grid, kStepThreads, 0, s>>>(a);
+  else linear_steps_kernel<T, kKey, 64, false><<<grid, kStepThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -208,6 +218,9 @@ extern "C" int rimuru_linear_attention(rimuru_view_t view, const rimuru_heads* q
       if (all[i]->dtype == RIMURU_F32) return fail(RIMURU_ERR_UNSUPPORTED, "activations must be bf16 or f16");
       if (all[i]->dtype != q->dtype) return fail(RIMURU_ERR_ARG, "activations must have one type");
     }
+    for (int i = 0; num_tokens > 1 && i < 4; ++i)
+      if (all[i]->token_stride == 0 || (i == 3 && out->heads > 1 && out->head_stride == 0))
+        return fail(RIMURU_ERR_UNSUPPORTED, std::string(names[i]) + ": elements may not lie on one another");
     if (v_in->heads != v.state_heads || out->heads != v.state_heads)
       return fail(RIMURU_ERR_ARG, "values and output must have the view's heads");
     if (q->heads != k->heads) return fail(RIMURU_ERR_ARG, "queries and keys must have the same heads");

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->full[i], kIn == 1 ? 1 : kOut ? 8 : 12);  // f16: warps 8 to 15 (19) split the tiles
+      mbar_init(&sh->full[i], kIn == 1 ? 1 : kKeyWarps);  // f16: the warps that split the tiles
       mbar_init(&sh->empty[i], kOut ? 2 : 1);      // both MMA warps
       mbar_init(&sh->keys_full[i], 1);
       mbar_init(&sh->keys_empty[i], (kOut ? 1 : 0) + kKeyWarps);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + kKeyWarps : 8 + kKeyWarps);
     }
     mbar_init(&sh->raw, 1);
-    mbar_init(&sh->raw_empty, 12);
+    mbar_init(&sh->raw_empty, kKeyWarps);
     mbar_init(&sh->values_full, 4);
     mbar_init(&sh->p_full, 4);
     mbar_init(&sh->p_empty, 1);
@@ -452,12 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait(&sh->key_empty[it % C::kKeyBufs], (it / C::kKeyBufs) ^ 1u);
   };
   // What this warp wrote of the keys (and, f16, of other tiles) can be used.
-  const auto give_keys = [&]() {
+  const auto give_keys = [&](bool read_all) {  // f16: whether this warp has read all it will of the loaded tiles
     fence_proxy_async_smem();
     arrive(&sh->key_full[it % C::kKeyBufs]);
     if (lane == 0) {
       mbar_arrive(kIn == 2 ? &sh->full[it % kStages] : &sh->keys_empty[it % kStages]);
-      if (kIn == 2) mbar_arrive(&sh->raw_empty);
+      if (kIn == 2 && read_all) mbar_arrive(&sh->raw_empty);
     }
   };
 
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int b = 0; b < C::kKb; ++b)
             split_block(raw_tiles + kRawQ + b * kBlock, base + 2 * b * kBlock, C::kQk, min(kC, x.n - c), tid, 128);
         }
-        give_keys();
+        give_keys(true);
         wait(&sh->score_full[buffer], it >> 1);
         wait(&sh->p_empty, it ^ 1u);
         if (!ok) break;
@@ -554,8 +554,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(v + b * kBlock + n * 128 + 16 * k) = make_uint4(0, 0, 0, 0);
           }
         }
-        give_keys();
+        give_keys(!kOut);
         if (lane == 0) mbar_arrive(&sh->gate_empty[it % kGates]);
+        if (kIn == 2 && kOut) {  // the values may come later than the keys
+          for (int b = 0; b < C::kVb; ++b) split_block(raw_tiles + kRawV + b * kBlock, v + b * kBlock, C::kV, n, tid, kThreads1);
+          fence_proxy_async_smem();
+          arrive(&sh->values_full);
+          if (lane == 0) mbar_arrive(&sh->raw_empty);
+        }
       }
     }
   };
@@ -799,16 +805,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; ok && c < x.n; c += kC, ++it) {
         const uint32_t slot = it % kGates;
         const int n = min(kC, x.n - c) - (lane & 3);
-        if (kIn == 2) {  // these warps split the values
-          wait_for_raw();
-          if (!ok) break;
-          uint8_t* v = smem + it % kStages * C::kStage + kIn * C::kQk;
-          for (int b = 0; b < C::kVb; ++b)
-            split_block(raw_tiles + kRawV + b * kBlock, v + b * kBlock, C::kV, min(kC, x.n - c), threadIdx.x - 16 * 32, 128);
-          fence_proxy_async_smem();
-          arrive(&sh->values_full);
-          if (lane == 0) mbar_arrive(&sh->raw_empty);
-        }
         wait(&sh->gate_full[slot], it / kGates);
         wait(&sh->out_full[it & 1u], it >> 1);
         if (!ok) break;
@@ -1016,8 +1012,8 @@ int launch_linear_chunks(const LinearArgs& a, const LinearCut& cut, void* worksp
   const int key_heads = a.heads / a.per_key_head;
   const auto map = [&](CUtensorMap* m, const void* x, int64_t ts, int64_t hs, int heads, int dim, int* one) {
     *one = heads == 1 || hs == 0;
-    if (ts == 0 || ts >= 1ll << 39 || hs >= 1ll << 39)
-      return fail(RIMURU_ERR_UNSUPPORTED, "token and head strides must be below 2^39, and tokens may not lie on one another");
+    if (ts >= 1ll << 39 || hs >= 1ll << 39)
+      return fail(RIMURU_ERR_UNSUPPORTED, "token and head strides must be below 2^39");
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(*one ? 1 : heads),
                                 static_cast<cuuint64_t>(a.num_tokens)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(*one ? dim : hs) * 2, static_cast<cuuint64_t>(ts) * 2};

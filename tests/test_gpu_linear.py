@@ -373,3 +373,26 @@ def test_few_tokens_of_many_sequences():
         want = c.plain()
         c.run()
         c.check(want, chunked)
+
+
+@pytest.mark.parametrize("new", [[3, 2], [70, 140]])
+def test_heads_that_lie_on_one_another(new):
+    """Queries, keys and values broadcast over their heads, by a stride of 0."""
+    c = Case(new, 4, 2, 64, 128)
+    c.q, c.k = c.q[:, :1].expand(-1, 2, -1), c.k[:, 1:].expand(-1, 2, -1)
+    c.v = c.v[:, 2:3].expand(-1, 4, -1)
+    want = c.plain()
+    c.run()
+    c.check(want, max(new) > 16)
+
+
+def test_inputs_of_one_projection():
+    """q, k and v as neighbouring slices of one array, as a fused projection leaves them."""
+    for new in ([1, 1], [40, 25]):
+        c = Case(new, 4, 2, 64, 64, kind="f16")
+        fused = torch.cat([c.q.flatten(1), c.k.flatten(1), c.v.flatten(1)], 1)
+        c.q, c.k = (fused[:, 128 * i:128 * i + 128].view(c.T, 2, 64) for i in range(2))
+        c.v = fused[:, 256:].view(c.T, 4, 64)
+        want = c.plain()
+        c.run()
+        c.check(want, max(new) > 16)

@@ -98,7 +98,9 @@ def test_linear_attention(views):
            (dict(gts=-1), R.ERR_ARG), (dict(ghs=-1), R.ERR_ARG), (dict(cu=0), R.ERR_ARG), (dict(cu=4097), R.ERR_ALIGN),
            (dict(sin=0), R.ERR_ARG), (dict(sout=0), R.ERR_ARG), (dict(sout=4099), R.ERR_ALIGN), (dict(ws=0), R.ERR_ARG),
            (dict(ws=4096 + 512), R.ERR_ALIGN), (dict(nbytes=0), R.ERR_WORKSPACE),
-           (dict(seqs=1 << 29, tokens=1 << 29, most=1), R.ERR_UNSUPPORTED)]
+           (dict(seqs=1 << 29, tokens=1 << 29, most=1), R.ERR_UNSUPPORTED), (dict(q=heads(ts=0)), R.ERR_UNSUPPORTED),
+           (dict(v=heads(ts=0)), R.ERR_UNSUPPORTED), (dict(o=heads(ts=0)), R.ERR_UNSUPPORTED),
+           (dict(o=heads(hs=0)), R.ERR_UNSUPPORTED)]
     for kw, st in bad:
         refused(st, go, **kw)
     go(seqs=0)
