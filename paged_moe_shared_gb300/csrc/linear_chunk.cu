@@ -90,7 +90,7 @@ struct ChunkShared {
   uint64_t full[2], empty[2];             // loaded queries and values (f16: all tiles, split)
   uint64_t keys_full[2], keys_empty[2];   // loaded keys
   uint64_t raw, raw_empty;                // f16: all tiles before they are split
-  uint64_t values_full;                   // f16, second kernel: split values
+  uint64_t values_full, parts_empty;      // f16, second kernel: split values; queries' and keys' parts
   uint64_t gate_full[kGates], gate_empty[kGates];
   uint64_t score_full[2], score_empty[2];
   uint64_t key_full[2], key_empty[2];     // decayed keys
@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->raw, 1);
     mbar_init(&sh->raw_empty, kKeyWarps);
     mbar_init(&sh->values_full, 4);
+    mbar_init(&sh->parts_empty, 2);  // scores, inter
     mbar_init(&sh->p_full, 4);
     mbar_init(&sh->p_empty, 1);
     mbar_init(&sh->state_full, 8);
@@ -397,10 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const uint8_t* const raw_tiles = smem + C::kRawAt;
   constexpr uint32_t kRawQ = C::kKb * kBlock, kRawV = 2 * kRawQ;
-  // f16: the tiles have been loaded and the places of their parts are free
+  // f16: the tiles have been loaded and the places of the queries' and keys' parts are free, which
+  // the outputs of the last chunk need not be for that
   const auto wait_for_raw = [&]() {
     wait(&sh->raw, it);
-    wait(&sh->empty[0], it ^ 1u);
+    if (kOut) wait(&sh->parts_empty, it ^ 1u);
   };
   // Decayed keys of rows [r0, r1) of the chunk that begins at c, by vectors of eight.
   constexpr int kVec = kDk / 8;
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 3; ++k)
         *reinterpret_cast<uint4*>(dst + k * C::kKeyPart + o) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
-      if (kIn == 2) {
+      if (kIn == 2 && kOut) {
         uint4 lo;
         split_f16(h, &h, &lo);
         *reinterpret_cast<uint4*>(src + o) = h;
@@ -544,8 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_for_keys();
         if (!ok) break;
         decay_keys(c, 0, kOut ? kC - kKeysByP : kC, tid, kThreads1);
-        if (kIn == 2 && !kOut)
+        if (kIn == 2 && !kOut) {
+          wait(&sh->empty[0], it ^ 1u);
+          if (!ok) break;
           for (int b = 0; b < C::kVb; ++b) split_block(raw_tiles + kRawV + b * kBlock, v + b * kBlock, C::kV, n, tid, kThreads1);
+        }
         if (kIn == 1 && n < kC) {  // values past the piece: 0 times what they hold may be NaN
           wait(&sh->full[it % kStages], it / kStages);
           if (!ok) break;
@@ -557,6 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         give_keys(!kOut);
         if (lane == 0) mbar_arrive(&sh->gate_empty[it % kGates]);
         if (kIn == 2 && kOut) {  // the values may come later than the keys
+          wait(&sh->empty[0], it ^ 1u);
+          if (!ok) break;
           for (int b = 0; b < C::kVb; ++b) split_block(raw_tiles + kRawV + b * kBlock, v + b * kBlock, C::kV, n, tid, kThreads1);
           fence_proxy_async_smem();
           arrive(&sh->values_full);
@@ -699,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           umma_commit(&sh->score_full[buffer]);
-          if (kIn == 1) umma_commit(&sh->keys_empty[stage]);
+          umma_commit(kIn == 1 ? &sh->keys_empty[stage] : &sh->parts_empty);
         }
         __syncwarp();
         ++scored;
@@ -765,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             umma_commit(&sh->state_empty);
+            if (kIn == 2) umma_commit(&sh->parts_empty);
           }
           __syncwarp();
           wait(&sh->p_full, it);
