@@ -51,9 +51,13 @@ __global__ void __launch_bounds__(kStepThreads) linear_steps_kernel(const __grid
   const int64_t step = static_cast<int64_t>(kParts) * a.value_dim;
   float4 S[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const float4* from = reinterpret_cast<const float4*>(s.in + at + i * step);
-    S[i] = !s.in ? make_float4(0.f, 0.f, 0.f, 0.f) : kStream ? __ldcs(from) : *from;
+  for (int i = 0; i < kRows; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (s.in) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if constexpr (kStream) S[i] = __ldcs(reinterpret_cast<const float4*>(s.in + at + i * step));
+      else S[i] = *reinterpret_cast<const float4*>(s.in + at + i * step);
+    }
   }
 
   const T* q = static_cast<const T*>(a.q) + s.row * a.q_ts + h / a.per_key_head * a.q_hs;
@@ -112,9 +116,8 @@ __global__ void __launch_bounds__(kStepThreads) linear_steps_kernel(const __grid
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    float4* to = reinterpret_cast<float4*>(s.out + at + i * step);
-    if (kStream) __stcs(to, S[i]);
-    else *to = S[i];
+    if constexpr (kStream) __stcs(reinterpret_cast<float4*>(s.out + at + i * step), S[i]);
+    else *reinterpret_cast<float4*>(s.out + at + i * step) = S[i];
   }
 }
 
