@@ -303,8 +303,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
               const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(weight + off[s][v] + 2 * e);
-              y[v][e] = mul2(y[v][e], mul2(k2, w.x));
-              y[v][e + 1] = mul2(y[v][e + 1], mul2(k2, w.y));
+              // in this order: k times a weight may leave fp32 where the result does not
+              y[v][e] = mul2(mul2(y[v][e], k2), w.x);
+              y[v][e + 1] = mul2(mul2(y[v][e + 1], k2), w.y);
             }
           }
         }
@@ -356,7 +357,7 @@ template <typename T>
 cudaError_t launch(NormArgs a, int per_lane, int heads, int sms, cudaStream_t stream) {
   // A group takes several heads of its token where that leaves 512 threads an SM, else fewer, down
   // to one; more groups pay for the prologue more often (8192 tokens of 18 heads of 256: 31.8 us,
-  // 35.8 with 1024 threads, 39.1 with 3072; 1000 tokens 8.6, 9.9 and 17.5).
+  // 35.8 with 1024 threads; 1000 tokens 8.6 and 9.9).
   const int64_t want = 512ll * sms >> a.lanes_log2;  // groups
   const int64_t per_token = std::max<int64_t>(1, std::min<int64_t>(std::min(heads, 32768), (want + a.num_tokens - 1) / a.num_tokens));
   a.heads_per_group = static_cast<int>((heads + per_token - 1) / per_token);

@@ -113,6 +113,15 @@ def test_far_values():
     R.rimuru_rope_destroy(rope)
 
 
+@pytest.mark.parametrize("scale,weight", [(1e38, 1e-6), (1e-12, 1e30)])
+def test_the_norm_times_the_weight_may_leave_fp32(scale, weight):
+    """1 / rms times the weight is below fp32's normal numbers (or above them all); the result is not."""
+    x = (torch.rand(5, 3, 96, device=DEV) + 1) * scale
+    w = (torch.rand(96, device=DEV) + 1) * weight
+    y = run([x], [R.head_norm_of(w, 1e-20)], None, 96, None)[0]
+    check(y, *plain(x, w, 0, 1e-20, None, 0, False, 1.0))
+
+
 def test_equals_the_rotation_alone_after_a_norm_of_ones():
     """Heads of magnitude 1 everywhere have a norm of 1: what is left is rimuru_rope_apply, bit for bit
     but for the norm's own rounding (eps is far below a half step)."""
