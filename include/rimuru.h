@@ -732,7 +732,9 @@ int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int 
  *             q, k and v may not lie on one another (a token stride of 0); heads may
  *   log_decay device float: g of token t and head h is log_decay[t * decay_token_stride + h *
  *             decay_head_stride].  A stride of 0 makes it one for all tokens (heads).  Any value
- *             <= 0, also -inf (the state starts anew with that token); one above 0 counts as 0
+ *             <= 0, also -inf (the state starts anew with that token); one above 0 counts as 0.
+ *             What came before is multiplied by 0 then, so a NaN or an infinity in it stays a NaN:
+ *             a page that holds nothing yet is not read with -inf but replaced by -1
  *   cu_new    device int32 [num_seqs + 1]: sequence b's new tokens are rows cu_new[b] ..
  *             cu_new[b + 1] - 1; or NULL for one token a sequence (num_tokens == num_seqs).
  *             Offsets do not decrease and need not begin at 0; other rows are neither read nor

@@ -11,9 +11,9 @@
 // reach, reads the chunks whose leaders reach it again and ranks what does.  Comparisons that decide are made on
 // doubles; fp32 only sieves, with a margin.
 //
-// 32 entries of 8 beams over 151,936 tokens in bf16 (78 MB), 16 best: 24.3 us, of which the
-// scan takes 15.9 (0.72 of the copy rate; 72 % of the issue slots) and the pick 8.5, a chain of
-// a dozen barriers and three dependent loads on one SM an entry.  One entry of 4 beams 11 us.  With
+// 32 entries of 8 beams over 151,936 tokens in bf16 (78 MB), 16 best: 23.5 us, of which the
+// scan takes 15.7 (0.73 of the copy rate; 71 % of the issue slots) and the pick 8, a chain of
+// a dozen barriers and three dependent loads on one SM an entry.  One entry of 4 beams 10 us.  With
 // maxima of 64 tokens in place of chunks the scan took 20 us and the pick, which has then
 // sixteen times as many, 30.
 #include <algorithm>

@@ -6,8 +6,8 @@
 // A thread holds four neighbouring columns of several key rows; per token it adds k v^T
 // and multiplies by q, and the parts of out that the CTA's rows give are added up in
 // shared memory.  A decode step moves 8 bytes for each state element and little else: 64
-// sequences of 32 heads of 128 x 128 (268 MB) 43.6 us, 0.91 of the copy rate; one sequence 3.2 us;
-// 16 sequences of 3 to 5 tokens, 16 heads of 64 x 128, 6.3 us, of which 2.6 are bytes.
+// sequences of 32 heads of 128 x 128 (268 MB) 44.0 us, 0.90 of the copy rate; one sequence 3.2 us;
+// 16 sequences of 3 to 5 tokens, 16 heads of 64 x 128, 6.5 us, of which 2.6 are bytes.
 #include <algorithm>
 #include <cmath>
 #include <limits>
@@ -129,8 +129,8 @@ cudaError_t launch_steps(const LinearArgs& a, cudaStream_t s) {
   // 54.8).  Where that leaves SMs without two CTAs, slices of 32.
   const bool wide = units * (a.value_dim / 64) >= 2ll * a.sms;
   const unsigned grid = static_cast<unsigned>(units * (a.value_dim / (wide ? 64 : 32)));
-  // States that pass L2 by go faster where there are many (the same 45.4 -> 43.6 us, 16 sequences
-  // 15.5 -> 14.3); 17 MB of them, read again soon, slower (6.3 -> 6.8).
+  // States that pass L2 by go faster where there are many (the same 45.4 -> 44.0 us, 16 sequences
+  // 15.5 -> 14.5); 17 MB of them, read again soon, slower (6.3 -> 6.8).
   const bool stream = units * kKey * a.value_dim * 8 > 32ll << 20;
   if (!wide) linear_steps_kernel<T, kKey, 32, false><<<grid, kStepThreads, 0, s>>>(a);
   else if (stream) linear_steps_kernel<T, kKey, 64, true><<<grid, kStepThreads, 0, s>>>(a);

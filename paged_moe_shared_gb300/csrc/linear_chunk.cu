@@ -31,7 +31,7 @@
 //
 // One prompt of 8192 tokens, 32 heads on 16 key heads of 128 x 128, bf16: 116 us, 45 of
 // them in the first kernel (token by token 4550 us); seven prompts of 558 to 1663 tokens 93,
-// f16 182.  What bounds a chunk of the second kernel, 2.4 us, is instructions: 10,400 of them,
+// f16 171.  What bounds a chunk of the second kernel, 2.4 us, is instructions: 10,400 of them,
 // 63 % of the issue slots, half of them in the cutting into parts; the tensor pipe is busy for
 // a third.  On the way: loads by two warps of 16-byte copies 220 us, by TMA 150; packed fp32
 // 141; 103 KiB of code, which the instruction cache fetched again and again (71 % of its hits
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   // Units, the longest pieces first and every other round backwards: a CTA that got a long one
-  // gets a short one next (seven prompts of 558 to 1663 tokens, 32 heads: 95 us, in the order of the
+  // gets a short one next (seven prompts of 558 to 1663 tokens, 32 heads: 93 us, in the order of the
   // sequences 110).  More pieces than threads even out by themselves.
   const int slots = p.units / a.heads, ctas = gridDim.x;
   const bool sorted = slots <= kThreads && p.units > ctas;

@@ -7,11 +7,11 @@
 // so that pairs turn within a lane), and the squares are added up over the group by
 // shuffles.  A CTA computes its tokens' cosines and sines once, for all heads.
 //
-// 8192 tokens, 18 heads of 256 of which 64 elements turn (151 MB): 31.8 us, 0.70 of the copy
+// 8192 tokens, 18 heads of 256 of which 64 elements turn (151 MB): 31.7 us, 0.70 of the copy
 // rate; the rotation alone takes 30.4.  Bound by instructions and latency together: a group
 // that computed its own angles, with all its values in fp32 registers, took 96 us; values as they
 // were loaded 55; shared angles, packed products and the next heads loaded ahead 39; fewer
-// groups with more heads each 31.8.  One token of 36 heads of 128: 3.9 us.
+// groups with more heads each 31.8.  One token of 36 heads of 128: 3.7 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
