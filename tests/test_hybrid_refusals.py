@@ -2,6 +2,7 @@
 import math
 
 import pytest
+import torch
 
 from paged_moe_shared_gb300 import rimuru as R
 
@@ -144,3 +145,15 @@ def test_kv_reorder(views):
         refused(st, go, **kw)
     go(n=0)
     go(layers=0)
+
+
+def test_descriptors_of_the_wrong_kind_are_refused():
+    x = torch.zeros(2, 3, 64)
+    heads, norm = R.heads_of(x), R.head_norm_of(None)
+    for ins, outs, norms in (([heads], [norm], [norm]), ([heads], [heads], [heads]), ([x], [heads], [norm])):
+        with pytest.raises(TypeError):
+            R.rimuru_norm_rope_apply(None, 0, 2, 64, ins, outs, norms)
+    with pytest.raises(ValueError):
+        R.head_norm_of(torch.zeros(128)[::2])
+    with pytest.raises(ValueError):
+        R.rows_of(torch.zeros(64, 4).t())
