@@ -2,16 +2,17 @@
 // rot_p(x * r * (w + offset)) with r = 1 / sqrt(mean(x^2) + eps).
 //
 // Each element is read and written once; a head stays in the registers of the lanes
-// that loaded it.  A group of 2^n lanes takes some heads of one token: a lane holds two
-// vectors of eight elements of a head (in the half layout the two members of eight pairs,
-// so that pairs turn within a lane), and the squares are added up over the group by
-// shuffles.  A CTA computes its tokens' cosines and sines once, for all heads.
+// that loaded it.  A group of 2^n lanes takes a run of heads, counted through all tokens: a
+// lane holds two vectors of eight elements of a head (in the half layout the two members of
+// eight pairs, so that pairs turn within a lane), and the squares are added up over the group
+// by shuffles.  A CTA computes its tokens' cosines and sines once, for all heads.
 //
-// 8192 tokens, 18 heads of 256 of which 64 elements turn (151 MB): 31.7 us, 0.70 of the copy
-// rate; the rotation alone takes 30.4.  Bound by instructions and latency together: a group
-// that computed its own angles, with all its values in fp32 registers, took 96 us; values as they
-// were loaded 55; shared angles, packed products and the next heads loaded ahead 39; fewer
-// groups with more heads each 31.8.  One token of 36 heads of 128: 3.7 us.
+// 8192 tokens, 18 heads of 256 of which 64 elements turn (151 MB): 30.0 us, 0.74 of the copy
+// rate, 0.84 at 32,768 tokens; the rotation alone takes 30.4.  Bound by instructions and latency
+// together: a group that computed its own angles, with all its values in fp32 registers, took
+// 96 us; values as they were loaded 55; shared angles, packed products and the next heads loaded
+// ahead 39; fewer groups with more heads each 31.8; runs of one length that fill whole rounds
+// of CTAs 30.0 (6500 tokens 30.8 -> 25.3, 3000 18.7 -> 14.1).  One token of 36 heads of 128: 3.7 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -25,6 +26,7 @@ namespace {
 
 constexpr int kMaxArrays = 4;
 constexpr int kThreads = 256;
+constexpr int kLongest = 128;  // heads of a run (32,768 tokens: 105 us; with 24 116, with 64 108)
 
 struct NormArray {
   const void* in;
@@ -42,9 +44,9 @@ struct NormArgs {
   const int32_t* positions;
   int num_tokens, head_dim;
   int lanes_log2;         // of a group
-  int heads_per_group;
-  int groups, groups_mul; // groups of a token in a CTA; g / groups = g * groups_mul >> 16
-  int tokens;             // of a CTA
+  int run;                // heads of a group, counted through all tokens
+  int64_t all_heads;      // of all tokens
+  uint32_t heads_mul;     // 2^32 / heads of a token, rounded down
   int turn_slots, slots;  // of a head: slots whose vectors are a pair's members, and all
 };
 
@@ -144,10 +146,22 @@ __device__ __forceinline__ void begin(const NormArgs& p, Cursor<T>* c, unsigned 
   c->at = static_cast<T*>(kOut ? A.out : const_cast<void*>(A.in)) + static_cast<int64_t>(t) * (kOut ? A.out_ts : A.in_ts) +
           (h - p.first_head[i]) * c->hs;
 }
+// To the next head; false where that is the first one of the next token.
 template <bool kOut, typename T>
-__device__ __forceinline__ void step(const NormArgs& p, Cursor<T>* c, unsigned t) {
+__device__ __forceinline__ bool step(const NormArgs& p, Cursor<T>* c, unsigned* t) {
   c->at += c->hs;
-  if (--c->left == 0 && c->i + 1 < kMaxArrays) begin<kOut>(p, c, t, p.first_head[c->i + 1]);
+  if (--c->left > 0) return true;
+  const int h = p.first_head[c->i + 1];
+  const bool same = h < p.first_head[kMaxArrays];
+  if (!same) ++*t;
+  begin<kOut>(p, c, *t, same ? h : 0);
+  return same;
+}
+__device__ __forceinline__ unsigned token_of(const NormArgs& p, int64_t head) {
+  const unsigned heads = p.first_head[kMaxArrays];
+  if (head >> 32) return static_cast<unsigned>(static_cast<uint64_t>(head) / heads);
+  const uint32_t x = static_cast<uint32_t>(head), q = __umulhi(x, p.heads_mul);  // one short at most
+  return q + (x - q * heads >= heads);
 }
 
 // kSlots: slots of a lane; kFull: every lane has both vectors of each of its slots.  Heads
@@ -161,11 +175,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* const weights = reinterpret_cast<float*>(dynamic);  // [arrays][head_dim], the offset added, ones without a weight
   float2* const cosines = reinterpret_cast<float2*>(weights + kMaxArrays * p.head_dim);  // [tokens of the CTA][pairs]
   const int lanes = 1 << p.lanes_log2, lane = threadIdx.x & (lanes - 1);
-  const int g = threadIdx.x >> p.lanes_log2, u = g * p.groups_mul >> 16;
-  const unsigned t0 = blockIdx.x * p.tokens, t = t0 + u, num_tokens = p.num_tokens;
-  const int h0 = (blockIdx.y * p.groups + g - u * p.groups) * p.heads_per_group;
-  // groups past the last token or head stay for the shuffles and take none
-  const int heads = u < p.tokens && t < num_tokens ? min(p.heads_per_group, p.first_head[kMaxArrays] - h0) : 0;
+  const int groups = blockDim.x >> p.lanes_log2;  // of the CTA
+  const int64_t begin0 = static_cast<int64_t>(blockIdx.x) * groups * p.run, at0 = begin0 + static_cast<int64_t>(threadIdx.x >> p.lanes_log2) * p.run;
+  // groups past the last head stay for the shuffles and take none
+  int to_load = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(p.run), p.all_heads - at0)));
+  const unsigned t0 = token_of(p, begin0);
+  unsigned t_in = to_load > 0 ? token_of(p, at0) : t0, t_out = t_in;
   const int pairs = p.rope.pairs, rot = 2 * pairs;
   int off[kSlots][2];
 #pragma unroll
@@ -179,25 +194,33 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int v = 0; v < 2; ++v) next[r][s][v] = Raw<T>{};
   Cursor<T> in{}, out{};
-  if (heads > 0) {
-    begin<false>(p, &in, t, h0);
-    begin<true>(p, &out, t, h0);
+  if (to_load > 0) {
+    const int h = static_cast<int>(at0 - static_cast<int64_t>(t_in) * p.first_head[kMaxArrays]);
+    begin<false>(p, &in, t_in, h);
+    begin<true>(p, &out, t_out, h);
   }
-  const auto load = [&](int h) {
+  // The next heads, kRows of them unless the group's or the token's last comes before.
+  const auto load = [&]() {
+    int n = 0;
+    bool more = true;
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-      if (h + r < heads) {
+      if (more && to_load > 0) {
 #pragma unroll
         for (int s = 0; s < kSlots; ++s)
 #pragma unroll
           for (int v = 0; v < 2; ++v)
             if (kFull || off[s][v] >= 0) next[r][s][v] = load_raw(in.at + off[s][v]);
-        step<false>(p, &in, t);
+        more = step<false>(p, &in, &t_in);
+        --to_load;
+        ++n;
       }
+    return n;
   };
-  load(0);
+  int loaded = load();
   if (rot > 0) {
-    const int n = min(static_cast<unsigned>(p.tokens), num_tokens - t0);
+    const int64_t end = min(begin0 + static_cast<int64_t>(groups) * p.run, p.all_heads);
+    const int n = static_cast<int>(token_of(p, end - 1) - t0) + 1;
     for (int k = threadIdx.x; k < n * pairs; k += blockDim.x) {
       const int w = k / pairs, i = k - w * pairs;
       const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + w]));
@@ -221,22 +244,26 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // of the slot's eight pairs: elements (e, e) of its two vectors, or (2 e, 2 e + 1) of one
   uint64_t cs[kSlots][4], sn[kSlots][4];
+  const auto angles = [&]() {
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s)
+    for (int s = 0; s < kSlots; ++s)
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const int at = kHalf ? (off[s][0] >= 0 && off[s][0] < rot ? off[s][0] + e : -1)
-                           : (off[s][e / 4] >= 0 && off[s][e / 4] < rot ? off[s][e / 4] / 2 + e % 4 : -1);
-      const float2* w = cosines + u * pairs + at;
-      const float2 w0 = at >= 0 && heads > 0 ? w[0] : make_float2(1.f, 0.f), w1 = at >= 0 && heads > 0 ? w[1] : make_float2(1.f, 0.f);
-      cs[s][e / 2] = pair(w0.x, w1.x);
-      sn[s][e / 2] = pair(w0.y, w1.y);
-    }
+      for (int e = 0; e < 8; e += 2) {
+        const int at = kHalf ? (off[s][0] >= 0 && off[s][0] < rot ? off[s][0] + e : -1)
+                             : (off[s][e / 4] >= 0 && off[s][e / 4] < rot ? off[s][e / 4] / 2 + e % 4 : -1);
+        const float2* w = cosines + (t_out - t0) * pairs + at;
+        const float2 w0 = at >= 0 ? w[0] : make_float2(1.f, 0.f), w1 = at >= 0 ? w[1] : make_float2(1.f, 0.f);
+        cs[s][e / 2] = pair(w0.x, w1.x);
+        sn[s][e / 2] = pair(w0.y, w1.y);
+      }
+  };
+  angles();
 
   const float per_dim = 1.f / p.head_dim;
   const uint64_t minus = pair(-1.f, -1.f);
 #pragma unroll 1
-  for (int h = 0; h < p.heads_per_group; h += kRows) {  // as often in every group: shuffles take all lanes
+  while (__any_sync(~0u, loaded > 0)) {  // as often in every group of a warp: shuffles take all lanes
+    const int here = loaded;
     Raw<T> x[kRows][kSlots][2];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
@@ -244,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int s = 0; s < kSlots; ++s)
 #pragma unroll
         for (int v = 0; v < 2; ++v) x[r][s][v] = next[r][s][v];
-    load(h + kRows);
+    loaded = load();
+    bool same = true;
     float sum[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -290,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       float k = rsqrtf(mean);
       if (sizeof(T) == 4) k = isinf(mean) ? 0.f : k * fmaf(-0.5f * mean * k, k, 1.5f);  // to the last bit
       k *= f;
-      if (h + r >= heads) continue;
+      if (r >= here) continue;
       const uint64_t k2 = pair(k, k);
       const float* weight = weights + out.i * p.head_dim;
 #pragma unroll
@@ -335,13 +363,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int v = 0; v < 2; ++v)
           if (kFull || off[s][v] >= 0) store8(out.at + off[s][v], y[v]);
       }
-      step<true>(p, &out, t);
+      same = step<true>(p, &out, &t_out);
     }
+    if (!same && loaded > 0) angles();  // the next token's
   }
 }
 
 template <typename T, bool kHalf>
-cudaError_t launch_layout(const NormArgs& a, int per_lane, dim3 grid, int block, int smem, cudaStream_t stream) {
+cudaError_t launch_layout(const NormArgs& a, int per_lane, unsigned grid, int block, int smem, cudaStream_t stream) {
   const bool full = a.head_dim == 16 * (per_lane << a.lanes_log2);
   if (per_lane == 1) {
     if (full) norm_rope_kernel<T, kHalf, 1, true><<<grid, block, smem, stream>>>(a);
@@ -355,23 +384,29 @@ cudaError_t launch_layout(const NormArgs& a, int per_lane, dim3 grid, int block,
 
 template <typename T>
 cudaError_t launch(NormArgs a, int per_lane, int heads, int sms, cudaStream_t stream) {
-  // A group takes several heads of its token where that leaves 512 threads an SM, else fewer, down
-  // to one; more groups pay for the prologue more often (8192 tokens of 18 heads of 256: 31.8 us,
-  // 35.8 with 1024 threads; 1000 tokens 8.6 and 9.9).
-  const int64_t want = 512ll * sms >> a.lanes_log2;  // groups
-  const int64_t per_token = std::max<int64_t>(1, std::min<int64_t>(std::min(heads, 32768), (want + a.num_tokens - 1) / a.num_tokens));
-  a.heads_per_group = static_cast<int>((heads + per_token - 1) / per_token);
-  const int all = (heads + a.heads_per_group - 1) / a.heads_per_group;  // groups of a token
-  // few threads: small CTAs, on many SMs
-  const int most = (static_cast<int64_t>(a.num_tokens) * all << a.lanes_log2) < static_cast<int64_t>(sms) * kThreads ? 64 : kThreads;
-  const int fit = std::max(1, most >> a.lanes_log2);  // groups of a CTA
-  a.groups = std::min(all, fit);
-  a.groups_mul = 65536 / a.groups + 1;  // exact for g < 256
-  a.tokens = std::max(1, fit / a.groups);
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.num_tokens) + a.tokens - 1) / a.tokens), (all + a.groups - 1) / a.groups);
-  const int block = (((a.tokens * a.groups) << a.lanes_log2) + 31) / 32 * 32;
+  // Groups take equal runs of heads, as long as 512 threads an SM (what their registers allow) make
+  // whole rounds of them.
+  a.all_heads = static_cast<int64_t>(a.num_tokens) * heads;
+  a.heads_mul = static_cast<uint32_t>(std::min<uint64_t>((1ull << 32) / heads, 0xFFFFFFFFu));
+  const int64_t slots = 512ll * sms >> a.lanes_log2;  // groups at the same time
+  // few threads: small CTAs, on many SMs, but a thread for each angle of two tokens (36 heads of 128,
+  // 16 tokens: 4.1 us; 64 threads 4.7, 256 4.4)
+  const int block = a.all_heads << a.lanes_log2 < static_cast<int64_t>(sms) * kThreads ? 128 : kThreads;
+  const int groups = block >> a.lanes_log2;
+  // tokens whose cosines a CTA has room for, at least two: runs begin anywhere
+  const int64_t room = a.rope.pairs ? std::max<int64_t>(2, (32 << 10) / (a.rope.pairs * static_cast<int>(sizeof(float2)))) : 1 << 20;
+  const int64_t longest = std::max<int64_t>(1, std::min<int64_t>(kLongest, (room - 1) * heads / groups));
+  const int64_t rounds = (a.all_heads + slots * longest - 1) / (slots * longest);
+  a.run = static_cast<int>((a.all_heads + slots * rounds - 1) / (slots * rounds));
+  // kernels that take two heads at once: a token's heads then pair up in every run (30.4 -> 30.0 us)
+  if (per_lane == 1 && heads % 2 == 0 && a.run > 2 && a.run < longest) a.run += a.run & 1;
+  const int64_t per_cta = static_cast<int64_t>(groups) * a.run;
+  const int64_t ctas = (a.all_heads + per_cta - 1) / per_cta;
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const unsigned grid = static_cast<unsigned>(ctas);
+  const int64_t tokens = std::min<int64_t>(a.num_tokens, (per_cta + heads - 2) / heads + 1);
   const int smem = kMaxArrays * a.head_dim * static_cast<int>(sizeof(float)) +
-                   a.tokens * a.rope.pairs * static_cast<int>(sizeof(float2));
+                   static_cast<int>(tokens) * a.rope.pairs * static_cast<int>(sizeof(float2));
   return a.rope.layout == RIMURU_ROPE_HALF ? launch_layout<T, true>(a, per_lane, grid, block, smem, stream)
                                            : launch_layout<T, false>(a, per_lane, grid, block, smem, stream);
 }

@@ -113,6 +113,16 @@ def test_far_values():
     R.rimuru_rope_destroy(rope)
 
 
+@pytest.mark.parametrize("T,heads,D,rot,inter,kind", [
+    (20001, (3, 2), 64, 32, False, "bf16"), (6001, (1,), 1024, 256, False, "f32"), (3001, (1, 1, 1), 256, 256, True, "f16"),
+    (4097, (7, 6, 1, 3), 72, 16, False, "bf16"), (41000, (1,), 8, 8, True, "f32"), (9000, (2, 2), 1024, 16, False, "f16"),
+    (301, (64, 8), 128, 128, False, "bf16"),
+])
+def test_runs_of_heads_over_many_tokens(T, heads, D, rot, inter, kind):
+    """A group's heads begin and end inside tokens and pass over several of them."""
+    test_values(T, heads, D, rot, inter, kind)
+
+
 @pytest.mark.parametrize("scale,weight", [(1e38, 1e-6), (1e-12, 1e30)])
 def test_the_norm_times_the_weight_may_leave_fp32(scale, weight):
     """1 / rms times the weight is below fp32's normal numbers (or above them all); the result is not."""
