@@ -137,6 +137,37 @@ __device__ __forceinline__ void unpack(const Raw<float>& r, uint64_t (&x)[4]) {
   }
 }
 
+// A bit for each of eight elements that are at least `least`, as numbers that `tame` leaves.
+template <typename T>
+__device__ __forceinline__ uint32_t reaching(const Raw<T>& r, float least) {
+  uint64_t x[4];
+  unpack(r, x);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = dev::split(x[e]);
+    if (f.x >= least) bits |= 1u << (2 * e);
+    if (f.y >= least) bits |= 2u << (2 * e);
+  }
+  return bits;
+}
+// Element `at` of several vectors of eight, by choices between registers.
+template <typename T, int kN>
+__device__ __forceinline__ float element(const Raw<T> (&r)[kN], int at) {
+  constexpr int kWords = kN * static_cast<int>(sizeof(T)) * 2;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+  const int word = at * static_cast<int>(sizeof(T)) / 4;
+  uint32_t v = w[0];
+#pragma unroll
+  for (int i = 1; i < kWords; ++i) v = i == word ? w[i] : v;
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(v);
+  } else {
+    const uint16_t half = static_cast<uint16_t>(at % 2 ? v >> 16 : v);
+    return to_f(*reinterpret_cast<const T*>(&half));
+  }
+}
+
 // A warp goes from chunk to chunk and loads the next one before it works on its own.
 // exp(x - m) is 2^(x L - fl(m L)) with L = log2(e) in fp32: one multiply-add; what the
 // rounding of m L puts into every term alike is taken out of the sum.
@@ -251,19 +282,37 @@ __device__ __forceinline__ void note(PickShared& s, const Candidate& c) {
 }
 
 // The `want` first of the listed candidates, if the list holds them all; a warp for each
-// of them counts those before it.  Candidates worth -inf are left out.
+// of them counts those before it.  256 of the others wait in its lanes' registers: read anew
+// for each, they would keep shared memory busy (202 of them: 24,000 cycles).  Candidates worth
+// -inf are left out.
 __device__ bool rank(PickShared& s, int want) {
+  constexpr int kHeld = 8;
   const int count = s.count, lane = threadIdx.x % 32;
   if (count > kList) return false;
-  for (int i = threadIdx.x / 32; i < count; i += kPickThreads / 32) {
-    const Candidate mine = s.list[i];
-    int n = 0;
-    for (int j = lane; j < count; j += 32) n += before(s.list[j], mine);
-    n = __reduce_add_sync(~0u, n);
-    if (lane == 0 && n < want && mine.key > kNothing) {
-      s.chosen[n] = mine;
-      atomicAdd(&s.n_chosen, 1);
+  int* const places = s.chunks;  // no longer needed; one warp's each
+  for (int j0 = 0; j0 < count; j0 += 32 * kHeld) {
+    Candidate other[kHeld];
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      const int j = j0 + 32 * e + lane;
+      other[e] = j < count ? s.list[j] : Candidate{0, 0x7FFFFFFF};  // before none
     }
+    for (int i = threadIdx.x / 32; i < count; i += kPickThreads / 32) {
+      const Candidate mine = s.list[i];
+      int n = 0;
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) n += before(other[e], mine);
+      n = __reduce_add_sync(~0u, n);
+      if (lane > 0) continue;
+      if (j0 > 0) n += places[i];
+      if (j0 + 32 * kHeld < count) {
+        places[i] = n;
+      } else if (n < want && mine.key > kNothing) {
+        s.chosen[n] = mine;
+        atomicAdd(&s.n_chosen, 1);
+      }
+    }
+    __syncwarp();
   }
   __syncthreads();
   return true;
@@ -493,14 +542,16 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       // what a logit has to reach, from below
       const float least = sieve > -INFINITY ? s.m[b] + (sieve - s.c32[b]) - (fabsf(s.m[b]) + fabsf(sieve) + fabsf(s.c32[b])) * 0x1p-21f
                                             : -3.402823466e38f;
+      // a bit for each element that does; the lanes then take one of theirs at a time
+      uint32_t good = 0;
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        if (!(max8(x[j]) >= least)) continue;
-#pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          const float f = tame(to_f(reinterpret_cast<const T*>(&x[j])[e]));
-          if (f >= least && passes(b, f, sieve)) note(s, Candidate{worth(b, f), b * a.vocab + token + 256 * j + e});
-        }
+      for (int j = 0; j < kVec; ++j)
+        if (max8(x[j]) >= least) good |= reaching(x[j], least) << (8 * j);
+      while (good) {
+        const int at = __ffs(good) - 1;
+        good &= good - 1;
+        const float f = tame(element(x, at));
+        if (passes(b, f, sieve)) note(s, Candidate{worth(b, f), b * a.vocab + token + 256 * (at / 8) + at % 8});
       }
     }
     __syncthreads();
