@@ -11,9 +11,9 @@
 // reach, reads the chunks whose leaders reach it again and ranks what does.  Comparisons that decide are made on
 // doubles; fp32 only sieves, with a margin.
 //
-// 32 entries of 8 beams over 151,936 tokens in bf16 (78 MB), 16 best: 23.5 us, of which the
-// scan takes 15.7 (0.73 of the copy rate; 71 % of the issue slots) and the pick 8, a chain of
-// a dozen barriers and three dependent loads on one SM an entry.  One entry of 4 beams 10 us.  With
+// 32 entries of 8 beams over 151,936 tokens in bf16 (78 MB), 16 best: 21.8 us, of which the
+// scan takes 15.7 (0.73 of the copy rate; 71 % of the issue slots) and the pick 6, a chain of
+// a dozen barriers and three dependent loads on one SM an entry.  One entry of 4 beams 9.2 us.  With
 // maxima of 64 tokens in place of chunks the scan took 20 us and the pick, which has then
 // sixteen times as many, 30.
 #include <algorithm>
@@ -262,6 +262,21 @@ __device__ __forceinline__ bool before(Candidate a, Candidate b) {
   return a.key > b.key || (a.key == b.key && a.index < b.index);
 }
 
+// n + 1 if a is before b, else n: key and index as one number of 96 bits, b less a.
+__device__ __forceinline__ int count_before(int n, Candidate a, Candidate b) {
+  uint32_t t;
+  asm("{\n\t.reg .u32 al, ah, bl, bh;\n\t"
+      "mov.b64 {al, ah}, %2;\n\tmov.b64 {bl, bh}, %3;\n\t"
+      "sub.cc.u32 %1, %4, %5;\n\t"  // the lower index is the larger number
+      "subc.cc.u32 %1, bl, al;\n\t"
+      "subc.cc.u32 %1, bh, ah;\n\t"
+      "subc.u32 %1, 0, 0;\n\t"  // -1 where that borrowed
+      "sub.s32 %0, %6, %1;\n\t}\n"
+      : "=r"(n), "=&r"(t)
+      : "l"(a.key), "l"(b.key), "r"(a.index), "r"(b.index), "r"(n));
+  return n;
+}
+
 constexpr int kTops = 4096;  // chunk maxima that are kept in shared memory
 
 struct PickShared {
@@ -282,8 +297,8 @@ __device__ __forceinline__ void note(PickShared& s, const Candidate& c) {
 }
 
 // The `want` first of the listed candidates, if the list holds them all; a warp for each
-// of them counts those before it.  256 of the others wait in its lanes' registers: read anew
-// for each, they would keep shared memory busy (202 of them: 24,000 cycles).  Candidates worth
+// of them counts those before it.  256 of the others wait in its lanes' registers instead of
+// being read anew for each.  Candidates worth
 // -inf are left out.
 __device__ bool rank(PickShared& s, int want) {
   constexpr int kHeld = 8;
@@ -301,7 +316,10 @@ __device__ bool rank(PickShared& s, int want) {
       const Candidate mine = s.list[i];
       int n = 0;
 #pragma unroll
-      for (int e = 0; e < kHeld; ++e) n += before(other[e], mine);
+      for (int e = 0; e < kHeld; ++e) {
+        if (e > 0 && 32 * e >= count - j0) break;
+        n = count_before(n, other[e], mine);
+      }
       n = __reduce_add_sync(~0u, n);
       if (lane > 0) continue;
       if (j0 > 0) n += places[i];
@@ -542,7 +560,9 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       // what a logit has to reach, from below
       const float least = sieve > -INFINITY ? s.m[b] + (sieve - s.c32[b]) - (fabsf(s.m[b]) + fabsf(sieve) + fabsf(s.c32[b])) * 0x1p-21f
                                             : -3.402823466e38f;
-      // a bit for each element that does; the lanes then take one of theirs at a time
+      // a bit for each element that does; the lanes then take one of theirs at a time (128 best of 8
+      // beams: 38.7 us; all eight elements of such vectors one by one, indexed in local memory, and
+      // ranks by 64-bit comparisons of candidates in shared memory 58.5)
       uint32_t good = 0;
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
