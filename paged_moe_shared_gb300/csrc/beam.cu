@@ -286,7 +286,9 @@ struct PickShared {
   float leader[kLeaders];
   int chunks[kList];
   Candidate list[kList], chosen[kMostSelect], next[kPickThreads / 32];
-  int count, n_chosen;
+  int n_chunks;  // that pass; `chunks` has the first kList
+  int count;     // of listed candidates.  A counter of its own: slow warps still read the other one
+  int n_chosen;
   float sieve;
   float tops[kTops];
 };
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   const int entry = blockIdx.x, tid = threadIdx.x, lane = tid % 32;
   const int row0 = entry * a.beams;
   const int N = a.n_chunks, n_tops = a.beams * N;
-  if (tid == 0) s.count = s.n_chosen = 0;
+  if (tid == 0) s.n_chunks = s.count = s.n_chosen = 0;
   dev::grid_dep_wait();
   const float* all_tops = a.tops + static_cast<int64_t>(row0) * N;
   const bool fits = n_tops <= kTops;
@@ -500,20 +502,21 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   for (int i = tid; i < n_tops; i += kPickThreads) {
     const int b = beam_of(i);
     if (passes(b, chunk_top(i, b), sieve)) {
-      const int at = atomicAdd(&s.count, 1);
+      const int at = atomicAdd(&s.n_chunks, 1);
       if (at < kList) s.chunks[at] = i;
     }
   }
   __syncthreads();
-  int n_chosen = s.count;
+  int n_chosen = s.n_chunks;
   if (n_chosen > kList) {  // chunks that are alike: the `want` best, whose last one's leader is a sieve too
     one_by_one(s, n_tops, want, chunk);
     n_chosen = s.n_chosen;
     if (tid < n_chosen) s.chunks[tid] = s.chosen[tid].index;
     if (n_chosen == want) sieve = fmaxf(sieve, __double2float_rd(unordered(s.chosen[want - 1].key)));
+    __syncthreads();  // all have read the number that are chosen
+    if (tid == 0) s.n_chosen = 0;
     __syncthreads();
   }
-  if (tid == 0) s.count = s.n_chosen = 0;
 
   // ---- the candidates of those chunks, a warp for each; an index is beam * vocab + token.
   // What passes the chunks' sieve is listed.  Where that is too much (one beam far ahead of the
@@ -527,7 +530,6 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     for (int j = 0; j < kVec; ++j) x[j] = load8(base, at + 256 * j, skip, skip + a.vocab);
     return at - skip;
   };
-  __syncthreads();
   for (int turn = sieve == -INFINITY; turn < 2; ++turn) {
     if (turn == 1) {
       float best = -INFINITY;

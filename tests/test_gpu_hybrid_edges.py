@@ -1,0 +1,32 @@
+"""Norms, linear attention and beam selection where they can go wrong: many CTAs beside other work, ties
+over rows that begin anywhere, tokens that are not finite, histories that are forgotten."""
+import math
+
+import pytest
+import torch
+
+from paged_moe_shared_gb300 import rimuru as R
+from test_gpu_beam import check, plain, select
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+# ------------------------------------------------------------------ selection
+@pytest.mark.parametrize("V,N,K", [(5000, 3, 5), (1001, 4, 8), (70, 2, 3)])
+def test_every_entry_beside_other_work(V, N, K):
+    """Many entries, again and again while another stream keeps the SMs and their caches busy: no
+    candidate is lost where some warps of an entry are late."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    logits = torch.randn(2000 * N, V, generator=g, device=DEV).bfloat16()
+    scores = -torch.rand(2000, N, generator=g, device=DEV)
+    want, rows, tokens = plain(logits, scores, None, 0, K)
+    ws = torch.empty(R.rimuru_beam_select_workspace_bytes(2000, N, V, K) + 1024, dtype=torch.uint8, device=DEV)
+    busy, other = torch.randn(1 << 24, device=DEV), torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        with torch.cuda.stream(other):
+            busy.mul_(1.0)
+        best, r, t = select(logits, scores, K=K, ws=ws)
+        assert torch.equal(r, rows) and torch.equal(t, tokens)
+        assert bool(((best.double() - want).abs() <= 2.0 ** -24 * want.abs() + 2.0 ** -18).all())
