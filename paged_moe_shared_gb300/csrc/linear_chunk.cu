@@ -776,7 +776,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           wait(&sh->p_full, it);
-          wait(&sh->key_full[it % C::kKeyBufs], it / C::kKeyBufs);  // the values past the piece have been cleared
+          // The values past the piece have been cleared.  f16 clears them as it splits them, and its one buffer of
+          // keys may be a phase further by now: nothing of the next chunk's keys waits for these products.
+          if (kIn == 1) wait(&sh->key_full[it % C::kKeyBufs], it / C::kKeyBufs);
           if (kIn == 2) wait(&sh->values_full, it);
           tc_fence_after();
           if (ok && elect_one()) {

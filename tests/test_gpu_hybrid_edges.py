@@ -7,6 +7,7 @@ import torch
 
 from paged_moe_shared_gb300 import rimuru as R
 from test_gpu_beam import check, plain, select
+from test_gpu_linear import Case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -30,3 +31,22 @@ def test_every_entry_beside_other_work(V, N, K):
         best, r, t = select(logits, scores, K=K, ws=ws)
         assert torch.equal(r, rows) and torch.equal(t, tokens)
         assert bool(((best.double() - want).abs() <= 2.0 ** -24 * want.abs() + 2.0 ** -18).all())
+
+
+# ------------------------------------------------------------------ linear attention
+@pytest.mark.parametrize("new", [[1000, 700], [64 * 20] * 9])
+def test_f16_prompts_beside_other_work(new):
+    """Many chunks while another stream takes issue slots and caches: every pass ends in time and is the same."""
+    c = Case(new, 16, 8, 128, 128, kind="f16", rate=0.02)
+    c.run()
+    torch.cuda.synchronize()
+    out, states = c.out.clone(), c.mem[c.state_out.long()].clone()
+    assert bool(out.isfinite().all())
+    busy, other = torch.randn(1 << 24, device=DEV), torch.cuda.Stream()
+    for _ in range(30):
+        with torch.cuda.stream(other):
+            busy.mul_(1.0)
+        c.out.zero_()
+        c.run(ws=c.ws)
+        assert torch.equal(c.out, out) and torch.equal(c.mem[c.state_out.long()], states)
+    assert R.rimuru_get_device_error(c.view) == R.DEV_OK
