@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     sh->units[i] = y;
   }
+  if (sorted) fence_proxy_async_smem();  // the lists lie where TMA is going to write
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

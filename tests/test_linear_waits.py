@@ -181,3 +181,12 @@ def test_the_model_has_the_kernels_barriers():
     assert made == set(roles(1, True)[1]) | {"drain"}
     # the wait that only inputs of one part need
     assert re.search(r"if \(kIn == 1\) wait\(&sh->key_full\[it % C::kKeyBufs\], it / C::kKeyBufs\);", text)
+
+
+def test_lists_in_the_tiles_place_are_fenced():
+    """The units are sorted in shared memory that TMA fills next: writes of the two kinds need a fence
+    between them, by every thread, before the barrier behind which the loads begin."""
+    text = open(SOURCE).read()
+    lists = text.index("order[before] = slot;")
+    barrier = text.index("const uint32_t tmem = sh->tmem_base;", lists)
+    assert re.search(r"\n  if \(sorted\) fence_proxy_async_smem\(\);[^}]*__syncthreads\(\);", text[lists:barrier])
