@@ -784,8 +784,8 @@ typedef struct rimuru_rows {
  *              are -inf, -1, -1
  *   workspace  device, 1024-byte aligned, rimuru_beam_select_workspace_bytes(...) bytes; calls that
  *              may run at the same time need one each
- * Sums of exponentials are fp32, the worths that are compared are doubles of them and of the
- * logits.  At most 128 beams and n_select 128; beams * (vocabulary + 2048) at most 2^30.  A worth below
+ * Sums of exponentials are fp32, added up in an order of tokens that does not depend on where a row begins:
+ * equal rows tie.  The worths that are compared are doubles of them and of the logits.  At most 128 beams and n_select 128; beams * (vocabulary + 2048) at most 2^30.  A worth below
  * fp32's range counts as -inf.  The
  * descriptor's cols is the vocabulary.  Errors: RIMURU_ERR_ARG, _ALIGN, _WORKSPACE, _UNSUPPORTED,
  * _CUDA. */

@@ -69,7 +69,7 @@ __device__ __forceinline__ float tame(float x) {
   return x != x ? -INFINITY : fminf(x, 3.402823466e38f);
 }
 
-// Row r's first element lies `skip` elements past a 16-byte boundary; places count from there.
+// Row r's first element lies `skip` elements past a 16-byte boundary; places count from that.
 template <typename T>
 __device__ __forceinline__ const T* row_base(const BeamArgs& a, int row, int* skip) {
   const T* p = static_cast<const T*>(a.logits) + row * a.row_stride;
@@ -95,6 +95,83 @@ __device__ __forceinline__ Raw<T> load8(const T* base, int at, int skip, int end
     for (int e = 0; e < 8; ++e) t[e] = at + e >= skip && at + e < end ? base[at + e] : lowest(T());
   }
   return v;
+}
+// The same for the 16 bytes from place `at`, which is not below `skip`.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* base, int at, int end) {
+  constexpr int kN = 16 / sizeof(T);
+  if (at + kN <= end) return dev::ld_nc_na_v4(base + at);
+  uint4 v;
+  T* t = reinterpret_cast<T*>(&v);
+#pragma unroll
+  for (int e = 0; e < kN; ++e) t[e] = at + e < end ? base[at + e] : lowest(T());
+  return v;
+}
+
+// A warp's chunk of a row: tokens [kChunk chunk, kChunk (chunk + 1)), 256 j + 8 lane + (0 .. 7) of them in
+// vector j of a lane.  Chunks and lanes count tokens and not places, so that a row's sum is the same, to
+// the last bit, wherever the row begins, and beams that are alike tie.  Vectors are loaded from places, and
+// move down by `skip` elements once they are there (to_tokens): the first ones of the next lane follow a
+// lane's own, and lane 0 holds the 16 bytes behind the chunk for the last one.
+// kAny: rows may begin off the boundaries (32 x 8 beams over 151,935 tokens 28.6 us; grouped by places and
+// without moving, 22.0).  Where none does there is nothing to move (151,936 tokens 21.8; with the registers
+// that moving takes 22.8 to 24.7).
+constexpr int kVec = kChunk / 256;
+template <typename T, bool kAny>
+struct Loaded {
+  Raw<T> v[kVec];
+  uint4 behind;
+  int skip;
+};
+template <typename T>
+struct Loaded<T, false> {
+  Raw<T> v[kVec];
+};
+template <typename T, bool kAny>
+__device__ __forceinline__ void load_chunk(const BeamArgs& a, int row, int chunk, Loaded<T, kAny>* x) {
+  const int lane = threadIdx.x & 31, at = chunk * kChunk + lane * 8;
+  int skip = 0;
+  const T* base = static_cast<const T*>(a.logits) + row * a.row_stride;
+  if constexpr (kAny) {
+    base = row_base<T>(a, row, &skip);
+    x->skip = skip;
+  }
+  const int end = skip + a.vocab;
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) x->v[j] = load8(base, at + j * 256, skip, end);
+  if constexpr (kAny) {
+    if (skip > 0 && lane == 0) x->behind = load16(base, at + kChunk, end);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void to_tokens(Loaded<T, false>*) {}
+template <typename T>
+__device__ __forceinline__ void to_tokens(Loaded<T, true>* x) {
+  constexpr int kOwn = static_cast<int>(sizeof(T)) * 2;   // words of eight elements
+  constexpr int kMore = sizeof(T) == 2 ? 4 : 3;           // words of the next eight that may be needed
+  const int lane = threadIdx.x & 31, skip = x->skip;
+  if (skip == 0) return;  // as one: a warp has one row
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) {
+    uint32_t w[kOwn + kMore + 1];
+    uint32_t* own = reinterpret_cast<uint32_t*>(&x->v[j]);
+    const uint32_t* after = j + 1 < kVec ? reinterpret_cast<const uint32_t*>(&x->v[j + 1 < kVec ? j + 1 : j])
+                                         : reinterpret_cast<const uint32_t*>(&x->behind);
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) w[i] = own[i];
+#pragma unroll
+    for (int i = 0; i < kMore; ++i) w[kOwn + i] = __shfl_sync(~0u, lane == 0 ? after[i] : own[i], (lane + 1) & 31);
+    w[kOwn + kMore] = 0;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < kOwn + kMore; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], skip % 2 * 16);
+    }
+    const int words = skip * static_cast<int>(sizeof(T)) / 4;  // 0 to 3
+#pragma unroll
+    for (int i = 0; i + 1 < kOwn + kMore; ++i) w[i] = words & 1 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) own[i] = words & 2 ? w[i + 2] : w[i];
+  }
 }
 
 // Largest of eight elements and `m`, a number where there is one among them.
@@ -171,35 +248,31 @@ __device__ __forceinline__ float element(const Raw<T> (&r)[kN], int at) {
 // A warp goes from chunk to chunk and loads the next one before it works on its own.
 // exp(x - m) is 2^(x L - fl(m L)) with L = log2(e) in fp32: one multiply-add; what the
 // rounding of m L puts into every term alike is taken out of the sum.
-template <typename T>
+template <typename T, bool kAny>
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
   dev::grid_dep_launch();
   const int lane = threadIdx.x & 31;
-  constexpr int kVec = kChunk / 256;  // vectors of eight of a lane
   const int rows = a.groups * a.beams, stride = gridDim.x * (kScanThreads / 32);
   const int step_rows = stride / a.n_chunks, step_chunks = stride - step_rows * a.n_chunks;
-  Raw<T> next[kVec];
+  Loaded<T, kAny> next;
   const int first = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5);
   int row = first / a.n_chunks, chunk = first - row * a.n_chunks;
   const auto load = [&]() {
     if (a.done && a.done[row]) return false;
-    int skip;
-    const T* base = row_base<T>(a, row, &skip);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) next[j] = load8(base, chunk * kChunk + j * 256 + lane * 8, skip, skip + a.vocab);
+    load_chunk(a, row, chunk, &next);
     return true;
   };
   bool live = row < rows && load();
   while (row < rows) {
-    Raw<T> raw[kVec];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) raw[j] = next[j];
+    Loaded<T, kAny> now = next;
+    const auto& raw = now.v;
     const bool mine = live;
     const int64_t at = static_cast<int64_t>(row) * a.n_chunks + chunk;
     row += step_rows, chunk += step_chunks;
     if (chunk >= a.n_chunks) chunk -= a.n_chunks, ++row;
     live = row < rows && load();
     if (!mine) continue;
+    to_tokens(&now);
     float m = -INFINITY;  // fmaxf takes the number where the other is a NaN
 #pragma unroll
     for (int j = 0; j < kVec; ++j) m = fmaxf(m, max8(raw[j]));
@@ -397,7 +470,7 @@ __device__ __forceinline__ double log_of(float y) {
   return fma(static_cast<double>(e), 0.693147180559945309417, static_cast<double>(logf(f)));
 }
 
-template <typename T>
+template <typename T, bool kAny>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
   __shared__ PickShared s;
   const int entry = blockIdx.x, tid = threadIdx.x, lane = tid % 32;
@@ -521,14 +594,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   // ---- the candidates of those chunks, a warp for each; an index is beam * vocab + token.
   // What passes the chunks' sieve is listed.  Where that is too much (one beam far ahead of the
   // others) or there is no such sieve, the candidates themselves give one.
-  constexpr int kVec = kChunk / 256;
-  const auto load = [&](int b, int g, Raw<T> (&x)[kVec]) {  // the place of its first token
-    int skip;
-    const T* base = row_base<T>(a, row0 + b, &skip);
-    const int at = (g - b * N) * kChunk + lane * 8;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) x[j] = load8(base, at + 256 * j, skip, skip + a.vocab);
-    return at - skip;
+  const auto load = [&](int b, int g, Loaded<T, kAny>* x) {  // this lane's first token
+    load_chunk(a, row0 + b, g - b * N, x);
+    to_tokens(x);
+    return (g - b * N) * kChunk + lane * 8;
   };
   for (int turn = sieve == -INFINITY; turn < 2; ++turn) {
     if (turn == 1) {
@@ -537,10 +606,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
         const int g = s.chunks[k], b = g / N;
         float top = s.done[b] && lane == 0 ? 0.f : -INFINITY;
         if (!s.done[b]) {
-          Raw<T> x[kVec];
-          load(b, g, x);
+          Loaded<T, kAny> x;
+          load(b, g, &x);
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) top = fmaxf(top, max8(x[j]));
+          for (int j = 0; j < kVec; ++j) top = fmaxf(top, max8(x.v[j]));
           top = fminf(top, 3.402823466e38f);
         }
         float err;
@@ -557,8 +626,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
         if (lane == 0) note(s, Candidate{worth(b, 0.f), b * a.vocab + a.pad});
         continue;
       }
-      Raw<T> x[kVec];
-      const int token = load(b, g, x);
+      Loaded<T, kAny> x;
+      const int token = load(b, g, &x);
       // what a logit has to reach, from below
       const float least = sieve > -INFINITY ? s.m[b] + (sieve - s.c32[b]) - (fabsf(s.m[b]) + fabsf(sieve) + fabsf(s.c32[b])) * 0x1p-21f
                                             : -3.402823466e38f;
@@ -568,11 +637,11 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       uint32_t good = 0;
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
-        if (max8(x[j]) >= least) good |= reaching(x[j], least) << (8 * j);
+        if (max8(x.v[j]) >= least) good |= reaching(x.v[j], least) << (8 * j);
       while (good) {
         const int at = __ffs(good) - 1;
         good &= good - 1;
-        const float f = tame(element(x, at));
+        const float f = tame(element(x.v, at));
         if (passes(b, f, sieve)) note(s, Candidate{worth(b, f), b * a.vocab + token + 256 * (at / 8) + at % 8});
       }
     }
@@ -585,11 +654,9 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       float f = e == 0 ? 0.f : -INFINITY;
       int token = a.pad;
       if (!s.done[b]) {
-        int skip;
-        const T* base = row_base<T>(a, row0 + b, &skip);
-        const int at = (g - b * N) * kChunk + e;
-        token = at - skip;
-        f = at >= skip && at < skip + a.vocab ? tame(to_f(base[at])) : -INFINITY;
+        token = (g - b * N) * kChunk + e;
+        const T* x = static_cast<const T*>(a.logits) + (row0 + b) * a.row_stride;
+        f = token < a.vocab ? tame(to_f(x[token])) : -INFINITY;
       }
       if (!passes(b, f, sieve)) return false;
       *c = Candidate{worth(b, f), b * a.vocab + token};
@@ -605,9 +672,9 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   }
 }
 
-template <typename T>
-cudaError_t launch(const BeamArgs& a, cudaStream_t s) {
-  beam_scan_kernel<T><<<a.ctas, kScanThreads, 0, s>>>(a);
+template <typename T, bool kAny>
+cudaError_t launch_rows(const BeamArgs& a, cudaStream_t s) {
+  beam_scan_kernel<T, kAny><<<a.ctas, kScanThreads, 0, s>>>(a);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.groups);
   cfg.blockDim = dim3(kPickThreads);
@@ -617,9 +684,14 @@ cudaError_t launch(const BeamArgs& a, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, beam_pick_kernel<T>, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, beam_pick_kernel<T, kAny>, a);
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
+}
+template <typename T>
+cudaError_t launch(const BeamArgs& a, cudaStream_t s) {
+  const uint64_t at = reinterpret_cast<uintptr_t>(a.logits) | static_cast<uint64_t>(a.row_stride) * sizeof(T);
+  return at % 16 == 0 ? launch_rows<T, false>(a, s) : launch_rows<T, true>(a, s);
 }
 
 // ------------------------------------------------------------------ reordering
@@ -706,8 +778,7 @@ __global__ void __launch_bounds__(kReorderThreads, kPer == 4 ? 8 : 4) kv_reorder
 using rimuru::fail;
 
 namespace {
-// A row may begin up to seven elements past a 16-byte boundary.
-int64_t row_chunks(int vocab) { return (static_cast<int64_t>(vocab) + 7 + rimuru::kChunk - 1) / rimuru::kChunk; }
+int64_t row_chunks(int vocab) { return (static_cast<int64_t>(vocab) + rimuru::kChunk - 1) / rimuru::kChunk; }
 }  // namespace
 
 extern "C" uint64_t rimuru_beam_select_workspace_bytes(int num_groups, int beams, int vocab, int n_select) {

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from paged_moe_shared_gb300 import rimuru as R
-from test_gpu_beam import check, plain, select
+from test_gpu_beam import TYPES, check, plain, select
 from test_gpu_linear import Case
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +50,28 @@ def test_f16_prompts_beside_other_work(new):
         c.run(ws=c.ws)
         assert torch.equal(c.out, out) and torch.equal(c.mem[c.state_out.long()], states)
     assert R.rimuru_get_device_error(c.view) == R.DEV_OK
+
+
+def in_order(row, beams, K):
+    """The K best of equal beams with equal scores: by the logit, then the beam, then the token."""
+    x = row.double().nan_to_num(nan=-math.inf).expand(beams, -1).flatten()
+    at = torch.sort(x, descending=True, stable=True)[1][:K]
+    return (at // len(row)).int(), (at % len(row)).int()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V,N,stride", [(50257, 9, 50257), (1001, 12, 1001), (151935, 8, 151937), (7, 16, 7), (2049, 8, 2050),
+                                        (1024, 8, 1027), (8191, 9, 8193)])
+def test_equal_beams_tie_wherever_their_rows_begin(V, N, stride, kind):
+    """Beams that are alike have sums that are alike to the last bit: a first step from one prompt selects
+    by beam and token, not by where a row lies."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    for first in range(2):
+        x = torch.full((1 + 2 * N * stride,), math.inf, dtype=TYPES[kind], device=DEV)[first:first + 2 * N * stride].view(2 * N, stride)[:, :V]
+        K = min(3 * N, 128)
+        for e in range(2):
+            x[e * N:(e + 1) * N] = (torch.randn(V, generator=g, device=DEV) * 3).to(x.dtype)
+        best, rows, tokens = select(x, torch.full((2, N), -1.5, device=DEV), K=K)
+        for e in range(2):
+            want_b, want_t = in_order(x[e * N], N, K)
+            assert torch.equal(rows[e, :len(want_b)], want_b + e * N) and torch.equal(tokens[e, :len(want_b)], want_t)
