@@ -4,9 +4,9 @@
 // T the state after it, a head's chunk is
 //   out_i = scale exp(G_i) (S^T q_i + sum_{j <= i} exp(-G_j) (q_i . k_j) v_j)
 //   T     = exp(G_last) S + sum_j exp(G_last - G_j) k_j v_j^T.
-// exp(-G_j) leaves fp32 where a chunk forgets more than 2^64.  There exp(G_i) outside the
-// bracket is held at 2^-64 and what is missing goes into the sum's weights; S, which by then
-// should have been forgotten altogether, is then forgotten by 2^-64.
+// exp(-G_j) leaves fp32 where a chunk forgets more than 2^64.  There exp(G_i) outside the bracket is
+// held between 2^-64 and 2^-63, and the power of two that is missing goes into the sum's weights and
+// into q_i, exactly: what is left of S counts however little that is.
 // All products are made transposed, with the value columns in the 128 lanes of TMEM and
 // 64 tokens or the key columns across, so that every MMA has full height:
 //   scores  Q K^T          (64 x 64; the lanes below take K K^T, which nobody reads)
@@ -62,10 +62,10 @@ static_assert((2 * kStateRegs + 2 * kProductRegs + kOutRegs + kOtherRegs) * 128 
 struct alignas(16) Gate {  // read four numbers at a time
   float2 sum[kC];   // G in two parts whose differences are exact, log2
   float col[kC];    // exp(-G)
-  float before[kC]; // scale * exp(G)
+  float before[kC]; // scale * exp(G), at least 2^-64 of it
   float after[kC];  // exp(G_last - G)
   float all;        // exp(G_last)
-  int wide;         // G leaves 2^-64: `col` is of no use
+  int wide;         // G leaves 2^-64: `col` is of no use, queries are scaled
   int pad[2];
 };
 static_assert(sizeof(Gate) % 16 == 0 && offsetof(Gate, col) % 16 == 0 && offsetof(Gate, before) % 16 == 0, "");
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kGates; ++i) {
       mbar_init(&sh->gate_full[i], 1);
-      mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + kKeyWarps : 8 + kKeyWarps);
+      mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + 1 + kKeyWarps : 8 + kKeyWarps);
     }
     mbar_init(&sh->raw, 1);
     mbar_init(&sh->raw_empty, kKeyWarps);
@@ -464,6 +464,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
+  // Half of query i of a stage, times 2^e.  The state takes no other factor for each token.
+  const auto scale_query = [&](uint8_t* base, int i, int half, float e) {
+    // in two factors, which fp32 holds; the product then rounds to bf16's smallest numbers at most
+    const int k = static_cast<int>(fmaxf(e, -252.f)), k0 = max(k, -126);
+    const float f0 = __int_as_float((k0 + 127) << 23), f1 = __int_as_float((k - k0 + 127) << 23);
+    const uint64_t f2 = pair(f0, f0), more = pair(f1, f1);
+#pragma unroll 1
+    for (int v = half; v < kIn * kVec; v += 2) {
+      const int part = v / kVec, col = v - part * kVec;
+      uint4* at = reinterpret_cast<uint4*>(base + part * C::kQk + col / 8 * (2 * kBlock) + place(i, col & 7));
+      const uint4 x = *at;
+      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+      uint32_t y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 z = split(mul2(mul2(widen(in[k]), f2), more));
+        y[k] = pack_bf16x2(z.x, z.y);
+      }
+      *at = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  };
+
   const auto products = [&]() {
     // P: a thread has row i (token i) and columns [32 half, 32 half + 32), eight at a time.  These
     // warps also decay some of the keys, so that all four schedulers do, and split the queries (f16).
@@ -489,9 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const Gate& t = sh->gate[slot];
         float2 sum = t.sum[i];
-        // what exp(G_i) is held back by
-        sum = sum.x >= kLeast ? make_float2(0.f, 0.f) : make_float2(sum.x - kLeast, sum.y);
+        // what exp(G_i) is held back by, a power of two
+        sum = make_float2(sum.x >= kLeast ? 0.f : floorf(sum.x - kLeast), 0.f);
         const bool wide = t.wide;
+        // the scores have been made: the query may change for its product with S, which waits for P then
+        if (wide && sum.x < 0.f) scale_query(smem + it % kStages * C::kStage, i, half, sum.x);
         uint32_t next[8];
         tmem_ld8(at + 64 * buffer, next);
 #pragma unroll 2
@@ -658,10 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nan0) p0.x = none;
             if (nan1) p1.x = none;
             *reinterpret_cast<float4*>(&t.sum[i]) = make_float4(p0.x, p0.y, p1.x, p1.y);
-            // fmaxf would lose a NaN
-            const float2 least = make_float2(kLeast, 0.f);
-            *reinterpret_cast<float2*>(&t.before[i]) = make_float2(exp2_of(p0.x < kLeast ? least : p0, zero) * a.scale,
-                                                                   exp2_of(p1.x < kLeast ? least : p1, zero) * a.scale);
+            // less the power of two that P and q take; a NaN stays one
+            const auto held = [](float2 x) { return x.x < kLeast ? make_float2(x.x - floorf(x.x - kLeast), x.y) : x; };
+            *reinterpret_cast<float2*>(&t.before[i]) = make_float2(exp2_of(held(p0), zero) * a.scale, exp2_of(held(p1), zero) * a.scale);
             *reinterpret_cast<float2*>(&t.col[i]) = make_float2(exp2_of(zero, p0), exp2_of(zero, p1));
             if (lane == 0) t.wide = wide;
           }
@@ -754,6 +777,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; ok && c < chunks; ++c, ++it) {
           const uint32_t stage = it % kStages;
           const uint32_t v0 = cols_lo + (stage * C::kStage + kIn * C::kQk) / 16;
+          wait(&sh->gate_full[it % kGates], it / kGates);
+          if (sh->gate[it % kGates].wide) wait(&sh->p_full, it);  // with P come the scaled queries
+          arrive(&sh->gate_empty[it % kGates]);
           wait(&sh->full[stage], it / kStages);
           wait(&sh->state_full, it);
           wait(&sh->out_empty[it & 1u], (it >> 1) ^ 1u);

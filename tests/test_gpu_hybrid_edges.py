@@ -75,3 +75,24 @@ def test_equal_beams_tie_wherever_their_rows_begin(V, N, stride, kind):
         for e in range(2):
             want_b, want_t = in_order(x[e * N], N, K)
             assert torch.equal(rows[e, :len(want_b)], want_b + e * N) and torch.equal(tokens[e, :len(want_b)], want_t)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(4, 2, 128, 128), (2, 1, 64, 128), (2, 2, 128, 64)])
+@pytest.mark.parametrize("new", [[5, 3], [64, 40], [17, 200], [1300]])
+def test_a_history_that_is_forgotten_leaves_nothing(new, shape, kind):
+    """States far larger than what comes, and decays that forget them in one token, over a few or not at
+    all: what is left of them in the outputs is what the formula leaves, also far below 2^-64."""
+    c = Case(new, *shape, kind=kind, rate=0.02)
+    c.mem *= 1e25
+    c.g[:] = torch.where(torch.rand(c.T, c.H, generator=c.gen, device=DEV) < 0.15,
+                         -torch.rand(c.T, c.H, generator=c.gen, device=DEV) * 120, c.g)
+    first = 0
+    for b, n in enumerate(new):
+        c.g[first] = torch.linspace(-48, -90, c.H, device=DEV)  # 1e25 becomes 10^4 to 10^-14
+        c.g[first + min(n - 1, 2), 0] = -math.inf
+        c.g[first + n // 2, -1] = -math.inf
+        first += n
+    want = c.plain()
+    c.run()
+    c.check(want, max(new) > 16)

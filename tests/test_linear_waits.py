@@ -12,6 +12,7 @@ import pytest
 
 SOURCE = os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "paged_moe_shared_gb300", "csrc", "linear_chunk.cu")
 UNITS = [(3, True), (1, False), (1, True), (4, False)]  # chunks, and whether the last one is partly filled
+WIDE = {1, 2, 4, 7}  # chunks whose queries are scaled
 GATES = 4
 
 
@@ -23,7 +24,7 @@ def roles(kin, out, mistake=False):
     key_warps, names = (["p", "keys"], 2) if out else (["keys"], 1)
     count = {"full": 1 if kin == 1 else len(key_warps), "empty": 2 if out else 1, "keys_full": 1,
              "keys_empty": (1 if out else 0) + len(key_warps), "raw": 1, "raw_empty": len(key_warps),
-             "values_full": 1, "parts_empty": 2, "gate_full": 1, "gate_empty": 2 + len(key_warps) if out else 2,
+             "values_full": 1, "parts_empty": 2, "gate_full": 1, "gate_empty": (3 if out else 1) + len(key_warps),
              "score_full": 1, "score_empty": 1, "key_full": len(key_warps), "key_empty": 1, "p_full": 1,
              "p_empty": 1, "state_full": 1, "state_empty": 1, "update_full": 1, "update_empty": 1,
              "out_full": 1, "out_empty": 1}
@@ -104,6 +105,10 @@ def roles(kin, out, mistake=False):
             scores(it + 1)
         # outputs' products
         if out:
+            wait("inter", "gate_full", it, GATES)
+            if it in WIDE:
+                wait("inter", "p_full", it)
+            arrive("inter", "gate_empty", it, GATES)
             wait("inter", "full", it, stages)
             wait("inter", "state_full", it)
             wait("inter", "out_empty", it, 2, True)
