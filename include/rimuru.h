@@ -747,6 +747,9 @@ int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int 
  *             of the call reads or writes.
  *   workspace device, 1024-byte aligned, at least rimuru_linear_attention_workspace_bytes(...)
  *             bytes; calls that may run at the same time need one each
+ * A NaN or an infinity in a token's q reaches its own outputs, in k, v or g the outputs and the state
+ * from that token on (of v: its column), and never an earlier token, another head or sequence; an infinity
+ * may have become a NaN there.
  * States and sums are fp32; in the chunked form the factors of a product are held as sums of bf16
  * parts (2^-16 of a factor, 2^-24 where they add to the state).  A page outside the view or
  * bad offsets (a sequence longer than max_new, a row past num_tokens) are recorded in the view's

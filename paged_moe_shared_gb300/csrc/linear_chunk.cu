@@ -92,6 +92,10 @@ struct ChunkShared {
   uint64_t raw, raw_empty;                // f16: all tiles before they are split
   uint64_t values_full, parts_empty;      // f16, second kernel: split values; queries' and keys' parts
   uint64_t gate_full[kGates], gate_empty[kGates];
+  uint64_t seen[kGates];                  // second kernel: `bad` is known
+  uint64_t safe[kGates];                  // values that are not finite have become zeros
+  alignas(4) uint8_t bad[kGates][4];      // whether one may not be, in 32 columns each
+  uint8_t bad_from[kGates][128];          // where one was: the column's first token that had one, or kC
   uint64_t score_full[2], score_empty[2];
   uint64_t key_full[2], key_empty[2];     // decayed keys
   uint64_t p_full, p_empty;
@@ -186,6 +190,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // 16-byte piece `c` of row r in a swizzled block of 128-byte rows.
 __device__ __forceinline__ uint32_t place(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+template <typename T>
+__device__ __forceinline__ T not_a_number() {
+  const uint16_t bits = 0x7FFF;
+  return *reinterpret_cast<const T*>(&bits);
+}
 template <typename T>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   if constexpr (std::is_same<T, __half>::value) {
@@ -306,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kGates; ++i) {
       mbar_init(&sh->gate_full[i], 1);
+      mbar_init(&sh->seen[i], 4);
+      mbar_init(&sh->safe[i], 1);
       mbar_init(&sh->gate_empty[i], kOut ? 8 + 4 + 1 + kKeyWarps : 8 + kKeyWarps);
     }
     mbar_init(&sh->raw, 1);
@@ -807,6 +818,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           // keys may be a phase further by now: nothing of the next chunk's keys waits for these products.
           if (kIn == 1) wait(&sh->key_full[it % C::kKeyBufs], it / C::kKeyBufs);
           if (kIn == 2) wait(&sh->values_full, it);
+          // P is 0 for tokens to come, and 0 times a NaN or an infinity is NaN.  So values that are not
+          // finite, which the update has taken to the state by now, become zeros before the outputs'
+          // products, and their columns of the outputs NaN from their tokens on.
+          const uint32_t slot = it % kGates;
+          wait(&sh->seen[slot], it / kGates);
+          if (*reinterpret_cast<const uint32_t*>(sh->bad[slot]) != 0) {
+#pragma unroll 1
+            for (int col = lane; col < kDv; col += 32) {
+              int from = kC;
+              uint8_t* const tile = smem + stage * C::kStage + kIn * C::kQk + col / 64 * kBlock + col % 8 * 2;
+#pragma unroll 1
+              for (int r = min(kC, x.n - c * kC) - 1; r >= 0; --r) {
+                auto* const y = reinterpret_cast<uint16_t*>(tile + place(r, col / 8 % 8));
+                if ((*y & 0x7F80u) != 0x7F80u) continue;  // f16: of the upper part
+                from = r;
+                *y = 0;
+                if (kIn == 2) y[C::kV / 2] = 0;
+              }
+              sh->bad_from[slot][col] = static_cast<uint8_t>(from);
+            }
+            fence_proxy_async_smem();
+          }
+          arrive(&sh->safe[slot]);
           tc_fence_after();
           if (ok && elect_one()) {
             const uint32_t p0 = base_lo + C::kPAt / 16;
@@ -843,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t slot = it % kGates;
         const int n = min(kC, x.n - c) - (lane & 3);
         wait(&sh->gate_full[slot], it / kGates);
+        wait(&sh->safe[slot], it / kGates);
         wait(&sh->out_full[it & 1u], it >> 1);
         if (!ok) break;
         tc_fence_after();
@@ -875,6 +910,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (col < kDv && h + j < n) *reinterpret_cast<uint2*>(o) = up ? make_uint2(other, mine) : make_uint2(mine, other);
             o += four;
           }
+        }
+        if (sh->bad[slot][quad] && col < kDv) {  // after what the neighbours have written
+          const int rows = min(kC, x.n - c);
+#pragma unroll 1
+          for (int r = sh->bad_from[slot][col]; r < rows; ++r)
+            static_cast<T*>(a.out)[(x.row + c + r) * a.o_ts + x.h * a.o_hs + col] = not_a_number<T>();
         }
         tc_fence_before();
         arrive(&sh->out_empty[it & 1u]);
@@ -968,6 +1009,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int d = 0; d < 32; d += 2)
             S[(d0 + d) / 2] = fma2(S[(d0 + d) / 2], pair(f, f), pair(__uint_as_float(u[d]), __uint_as_float(u[d + 1])));
+        }
+        if (kOut && wg == 0) {
+          // row 0 has a product of every value of the column in it
+          const bool bad = __any_sync(0xffffffffu, real && !(fabsf(split(S[0]).x) < INFINITY));
+          if (lane == 0) sh->bad[slot][quad] = bad;
+          arrive(&sh->seen[slot]);
         }
         arrive(&sh->gate_empty[slot]);
       }

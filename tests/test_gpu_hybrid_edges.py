@@ -96,3 +96,39 @@ def test_a_history_that_is_forgotten_leaves_nothing(new, shape, kind):
     want = c.plain()
     c.run()
     c.check(want, max(new) > 16)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(4, 2, 128, 128), (2, 1, 64, 128), (2, 2, 128, 64)])
+@pytest.mark.parametrize("new", [[64], [9, 100, 33], [63, 130], [1300, 40]])
+def test_a_value_that_is_not_finite_reaches_no_earlier_token(new, shape, kind):
+    """A NaN or an infinity among the values makes its column of the head NaN or infinite from its token
+    on; the tokens before it, other columns, heads and sequences are what they are without it."""
+    c = Case(new, *shape, kind=kind, rate=0.02)
+    chunked = max(new) > 16
+    heads, dv = shape[0], shape[3]
+    g = torch.Generator().manual_seed(sum(new))
+    hurt = torch.zeros(c.T, heads, dv, dtype=torch.bool, device=DEV)
+    lost = {}
+    clean, first = c.v.clone(), 0
+    for b, n in enumerate(new):
+        for k in range(6):
+            t = [0, n - 1, n // 2, 5 % n][k] if k < 4 else int(torch.randint(0, n, (1,), generator=g))
+            h, col = k % heads, int(torch.randint(0, dv, (1,), generator=g))
+            c.v[first + t, h, col] = [math.nan, math.inf, -math.inf][k % 3]
+            clean[first + t, h, col] = 0
+            hurt[first + t:first + n, h, col] = True
+            lost.setdefault(int(c.state_out[b]), set()).add((h, col))
+        first += n
+    bad, c.v = c.v, clean
+    want = c.plain()
+    c.v = bad
+    c.run()
+    torch.cuda.synchronize()
+    assert not bool(c.out[hurt].isfinite().any())
+    c.out = torch.where(hurt, want[0].to(c.out.dtype), c.out)
+    for page, places in lost.items():
+        for h, col in places:
+            assert not bool(c.states()[page, h, :, col].isfinite().any())
+            c.states()[page, h, :, col] = want[2][page][0][h, :, col].float()
+    c.check(want, chunked)

@@ -23,7 +23,7 @@ def roles(kin, out, mistake=False):
     chunks = [(u, c, c + 1 == n, part and c + 1 == n) for u, (n, part) in enumerate(UNITS) for c in range(n)]
     key_warps, names = (["p", "keys"], 2) if out else (["keys"], 1)
     count = {"full": 1 if kin == 1 else len(key_warps), "empty": 2 if out else 1, "keys_full": 1,
-             "keys_empty": (1 if out else 0) + len(key_warps), "raw": 1, "raw_empty": len(key_warps),
+             "keys_empty": (1 if out else 0) + len(key_warps), "raw": 1, "raw_empty": len(key_warps), "seen": 1, "safe": 1,
              "values_full": 1, "parts_empty": 2, "gate_full": 1, "gate_empty": (3 if out else 1) + len(key_warps),
              "score_full": 1, "score_empty": 1, "key_full": len(key_warps), "key_empty": 1, "p_full": 1,
              "p_empty": 1, "state_full": 1, "state_empty": 1, "update_full": 1, "update_empty": 1,
@@ -118,8 +118,11 @@ def roles(kin, out, mistake=False):
                 wait("inter", "key_full", it, keybufs)
             if kin == 2:
                 wait("inter", "values_full", it)
+            wait("inter", "seen", it, GATES)
+            arrive("inter", "safe", it, GATES)
             commit("inter", ("p_empty", it, 1), ("out_full", it, 2), ("empty", it, stages))
             wait("outputs", "gate_full", it, GATES)
+            wait("outputs", "safe", it, GATES)
             wait("outputs", "out_full", it, 2)
             arrive("outputs", "out_empty", it, 2)
             arrive("outputs", "gate_empty", it, GATES)
@@ -130,6 +133,8 @@ def roles(kin, out, mistake=False):
         wait("states", "gate_full", it, GATES)
         wait("states", "update_full", it)
         arrive("states", "update_empty", it)
+        if out:
+            arrive("states", "seen", it, GATES)
         arrive("states", "gate_empty", it, GATES)
     return r, count
 
