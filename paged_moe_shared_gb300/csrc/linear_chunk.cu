@@ -911,7 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             o += four;
           }
         }
-        if (sh->bad[slot][quad] && col < kDv) {  // after what the neighbours have written
+        if (sh->bad[slot][quad] && col < kDv) {  // a warp's lanes alike
+          __syncwarp();  // after what the neighbours have written
           const int rows = min(kC, x.n - c);
 #pragma unroll 1
           for (int r = sh->bad_from[slot][col]; r < rows; ++r)
