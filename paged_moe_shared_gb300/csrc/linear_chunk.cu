@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
         for (int v = 0; v < 4; ++v) {
           uint64_t y[4];
-          tmem_ld_wait();
+          tmem_ld_wait8(next);
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = pair(__uint_as_float(next[2 * e]), __uint_as_float(next[2 * e + 1]));
           if (v < 3) tmem_ld8(at + 64 * buffer + 8 * (v + 1), next);
@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
         for (int h = 0; h < kC; h += 8) {
           uint32_t u[8];
-          tmem_ld_wait();
+          tmem_ld_wait8(ahead);
 #pragma unroll
           for (int j = 0; j < 8; ++j) u[j] = ahead[j];
           if (h + 8 < kC) tmem_ld8(at + kOutAt + 64 * (it & 1u) + h + 8, ahead);

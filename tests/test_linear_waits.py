@@ -200,3 +200,10 @@ def test_lists_in_the_tiles_place_are_fenced():
     lists = text.index("order[before] = slot;")
     barrier = text.index("const uint32_t tmem = sh->tmem_base;", lists)
     assert re.search(r"\n  if \(sorted\) fence_proxy_async_smem\(\);[^}]*__syncthreads\(\);", text[lists:barrier])
+
+
+def test_loaded_registers_pass_through_their_wait():
+    """What reads a register that tcgen05.ld fills depends on the wait: nothing else keeps it behind."""
+    text = open(SOURCE).read()
+    assert not re.search(r"tmem_ld_wait\(\)", text)
+    assert len(re.findall(r"tmem_ld(?:8|32)\(", text)) >= len(re.findall(r"tmem_ld_wait(?:8|32)\(", text)) == 3
