@@ -33,6 +33,37 @@ def test_every_entry_beside_other_work(V, N, K):
         assert bool(((best.double() - want).abs() <= 2.0 ** -24 * want.abs() + 2.0 ** -18).all())
 
 
+@pytest.mark.parametrize("kind,V", [("bf16", 151936), ("f32", 151935)])
+def test_more_chunks_than_shared_memory_keeps(kind, V):
+    """40 beams: 5960 chunk maxima, which are read again from the workspace."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    x = (torch.randn(2 * 40, V, generator=g, device=DEV) * 3).to(TYPES[kind])
+    scores = -3 * torch.rand(2, 40, generator=g, device=DEV)
+    check(x, scores, K=40)
+    check(x, scores, K=128)
+    check(x, scores, (torch.rand(2, 40, generator=g, device=DEV) < 0.5).to(torch.uint8), 7, K=80)
+    scores[:, 1:] = -math.inf
+    check(x, scores, K=16)
+
+
+@pytest.mark.parametrize("N,K", [(8, 16), (8, 128), (40, 128)])
+@pytest.mark.parametrize("kind,V", [("bf16", 151936), ("f32", 151935)])
+def test_more_alike_chunks_than_the_list_holds(kind, V, N, K):
+    """More than 1024 chunks whose leaders are the same: the first ones by beam and token."""
+    x, scores = torch.zeros(N, V, dtype=TYPES[kind], device=DEV), torch.full((1, N), -0.5, device=DEV)
+    want = torch.arange(K, dtype=torch.int32, device=DEV)
+    _, rows, tokens = select(x, scores, K=K)
+    assert torch.equal(rows[0], want * 0) and torch.equal(tokens[0], want)
+    x[3, 5000], x[1, V - 1], x[1, 70000] = 1.0, 1.0, 1.0  # a few better ones in beams that this makes different
+    scores[0, 2] = -math.inf
+    check(x, scores, K=K)
+    x[:] = 0
+    x[:, ::1024] = 2.0  # a leader in every chunk, better than the rest of it
+    _, rows, tokens = select(x, scores * 0, K=K)
+    n = (V + 1023) // 1024
+    assert torch.equal(rows[0], want // n) and torch.equal(tokens[0], want % n * 1024)
+
+
 # ------------------------------------------------------------------ linear attention
 @pytest.mark.parametrize("new", [[1000, 700], [64 * 20] * 9])
 def test_f16_prompts_beside_other_work(new):
@@ -132,3 +163,55 @@ def test_a_value_that_is_not_finite_reaches_no_earlier_token(new, shape, kind):
             assert not bool(c.states()[page, h, :, col].isfinite().any())
             c.states()[page, h, :, col] = want[2][page][0][h, :, col].float()
     c.check(want, chunked)
+
+
+@pytest.mark.parametrize("what", ["in", "out", "low", "long", "back", "past"])
+@pytest.mark.parametrize("max_new", [1, 40, 900])
+def test_bystanders_of_bad_tables(max_new, what):
+    """Sequences beside one with a bad page or bad offsets are computed as if it were not there; what it
+    would have read or written stays, pages as well as rows."""
+    new = [1, 1, 1] if max_new == 1 else [max_new, 30, 17]
+    c = Case(new, 4, 2, 64, 64, rate=0.02)
+    (want, size, states), before, out = c.plain(), c.mem.clone(), c.out.clone()
+    hurt, code = [1], R.DEV_BAD_PAGE if what in ("in", "out", "low") else R.DEV_BAD_SHAPE
+    pages = c.state_out.tolist()
+    if what in ("in", "low"):
+        c.state_in[1] = c.pages if what == "in" else -2
+    elif what == "out":
+        c.state_out[1] = -1
+    elif what == "long":  # longer than max_new, and the third one begins past the rows
+        c.cu[2] += 2 * max_new
+        c.cu[3] = c.cu[2]
+        hurt = [1, 2]
+    elif what == "back":  # the third one ends before it begins
+        c.cu[3] = c.cu[2] - 1
+        hurt = [2]
+    else:
+        c.cu[3] = c.T + 1
+        hurt = [2]
+    c.run(max_new=max_new)
+    torch.cuda.synchronize()
+    assert R.rimuru_get_device_error(c.view, True) == code
+    rows = torch.tensor([0] + new).cumsum(0).tolist()
+    for b in hurt:
+        at = slice(rows[b], rows[b + 1])
+        assert torch.equal(c.out[at], out[at]) and torch.equal(c.mem[pages[b]], before[pages[b]])
+        c.out[at] = want[at].to(c.out.dtype)
+        states.pop(pages[b])
+    c.check((want, size, states), max_new > 16)
+
+
+def test_states_pass_on_without_tokens():
+    """No tokens at all, in every form of the call: pages are copied, zeros for -1, nothing else changes."""
+    for new, max_new in (([0], 0), ([0, 0, 0], 5), ([0] * 5, 1000)):
+        c = Case(new, 3, 1, 64, 128, pages=12)
+        before = c.mem.clone()
+        c.state_in[0] = -1
+        c.run(max_new=max_new)
+        torch.cuda.synchronize()
+        assert R.rimuru_get_device_error(c.view) == R.DEV_OK
+        for b in range(c.B):
+            want = before[c.state_in[b]] if b else torch.zeros_like(before[0])
+            assert torch.equal(c.mem[c.state_out[b]], want)
+        others = [p for p in range(12) if p not in c.state_out.tolist()]
+        assert torch.equal(c.mem[others], before[others])
