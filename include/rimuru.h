@@ -577,6 +577,7 @@ typedef struct rimuru_head_norm {
  * the rotation its first rot_dim elements; nothing is rounded in between.  A squared sum past
  * fp32 is taken on scaled elements; a NaN or an infinity in a head makes the head NaN or 0 as the
  * formula does.  rope may be NULL: norms alone, positions is then not read.
+ * Tokens and heads of an output may not lie on one another (a stride of 0: RIMURU_ERR_UNSUPPORTED).
  * Other arguments, in-place use and errors as rimuru_rope_apply. */
 int rimuru_norm_rope_apply(rimuru_rope_t rope, const int32_t* positions, int num_tokens, int head_dim,
                            const rimuru_heads* in, const rimuru_heads* out, const rimuru_head_norm* norms,

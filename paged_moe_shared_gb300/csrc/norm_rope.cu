@@ -445,6 +445,8 @@ extern "C" int rimuru_norm_rope_apply(rimuru_rope_t rope, const int32_t* positio
     if (st != RIMURU_OK) return st;
     if (in[i].heads != out[i].heads || in[i].dtype != out[i].dtype || in[i].dtype != in[0].dtype)
       return fail(RIMURU_ERR_ARG, "inputs and outputs must agree in heads and type");
+    if ((num_tokens > 1 && out[i].token_stride == 0) || (out[i].heads > 1 && out[i].head_stride == 0))
+      return fail(RIMURU_ERR_UNSUPPORTED, "norm output: elements may not lie on one another");
     const rimuru_head_norm& n = norms[i];
     if (!(n.eps >= 1e-20 && n.eps <= 1.0)) return fail(RIMURU_ERR_ARG, "eps must be in [1e-20, 1]");
     if (!std::isfinite(static_cast<float>(n.offset))) return fail(RIMURU_ERR_ARG, "offset must be finite in fp32");
