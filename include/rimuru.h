@@ -785,7 +785,8 @@ typedef struct rimuru_rows {
  *              candidate, pad_token at scores[b]; its logits are not read
  *   out_scores, out_rows, out_tokens  device [num_groups][n_select]: the sum, the beam's row
  *              (entry * beams + b) and the token; where fewer candidates are above -inf the rest
- *              are -inf, -1, -1
+ *              are -inf, -1, -1.  out_scores may be scores itself where n_select == beams; outputs
+ *              overlap no input otherwise (RIMURU_ERR_ARG for the scores) and not one another
  *   workspace  device, 1024-byte aligned, rimuru_beam_select_workspace_bytes(...) bytes; calls that
  *              may run at the same time need one each
  * Sums of exponentials are fp32, added up in an order of tokens that does not depend on where a row begins:

@@ -820,6 +820,11 @@ extern "C" int rimuru_beam_select(const rimuru_rows* logits, const float* scores
   const uint64_t need = rimuru_beam_select_workspace_bytes(num_groups, beams, logits->cols, n_select);
   if (workspace_bytes < need)
     return fail(RIMURU_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  // an entry reads its scores before it writes, but not before another entry does
+  const uintptr_t s0 = reinterpret_cast<uintptr_t>(scores), o0 = reinterpret_cast<uintptr_t>(out_scores);
+  const uintptr_t entries = static_cast<uintptr_t>(num_groups) * sizeof(float);
+  if (o0 < s0 + entries * beams && s0 < o0 + entries * n_select && !(o0 == s0 && n_select == beams))
+    return fail(RIMURU_ERR_ARG, "out_scores may lie on the scores only where n_select is the number of beams");
   BeamArgs a{};
   a.logits = logits->data;
   a.row_stride = logits->row_stride;
