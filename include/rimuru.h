@@ -729,8 +729,9 @@ int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int 
  * registers, more of them in chunks on the tensor cores; no choice needs the host.
  *   q, k      device [num_tokens][key heads][key_dim], RIMURU_BF16 or RIMURU_F16; the view's heads
  *             are a multiple of their heads
- *   v, out    device [num_tokens][heads][value_dim], the same type; out overlaps no input.  Tokens of
- *             q, k and v may not lie on one another (a token stride of 0); heads may
+ *   v, out    device [num_tokens][heads][value_dim], the same type; out overlaps no input (RIMURU_ERR_ARG
+ *             where it is one).  Tokens of q, k and v may not lie on one another (a token stride of 0);
+ *             heads may
  *   log_decay device float: g of token t and head h is log_decay[t * decay_token_stride + h *
  *             decay_head_stride].  A stride of 0 makes it one for all tokens (heads).  Any value
  *             <= 0, also -inf (the state starts anew with that token); one above 0 counts as 0.
@@ -754,7 +755,8 @@ int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int 
  * States and sums are fp32; in the chunked form the factors of a product are held as sums of bf16
  * parts (2^-16 of a factor, 2^-24 where they add to the state).  A page outside the view or
  * bad offsets (a sequence longer than max_new, a row past num_tokens) are recorded in the view's
- * device error word (RIMURU_DEV_BAD_PAGE, RIMURU_DEV_BAD_SHAPE) and the sequence is left alone.
+ * device error word (RIMURU_DEV_BAD_PAGE, RIMURU_DEV_BAD_SHAPE) and the sequence is left alone; where
+ * offsets decrease, so may be parts of sequences whose rows others then claim too.
  * The first call on a view allocates its error word: make it outside a stream capture.  Later
  * calls only launch kernels and can be captured. */
 uint64_t rimuru_linear_attention_workspace_bytes(rimuru_view_t view, int num_seqs, int num_tokens,

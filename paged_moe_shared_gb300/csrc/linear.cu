@@ -245,6 +245,8 @@ extern "C" int rimuru_linear_attention(rimuru_view_t view, const rimuru_heads* q
     return fail(RIMURU_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
   if (4ll * num_seqs * v.state_heads > std::numeric_limits<int32_t>::max())
     return fail(RIMURU_ERR_UNSUPPORTED, "too many sequences for one call");
+  if (num_tokens > 0 && (out->data == q->data || out->data == k->data || out->data == v_in->data))
+    return fail(RIMURU_ERR_ARG, "the output may not be an input");
   const int st = state_ready(&v);
   if (st != RIMURU_OK) return st;
   LinearArgs a{};

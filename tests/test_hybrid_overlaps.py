@@ -2,7 +2,7 @@
 import pytest
 
 from paged_moe_shared_gb300 import rimuru as R
-from test_hybrid_refusals import heads, norm, refused
+from test_hybrid_refusals import heads, norm, refused, views  # noqa: F401
 
 
 @pytest.fixture(autouse=True)
@@ -37,3 +37,17 @@ def test_selection_over_its_scores():
     refused(R.ERR_CUDA, go, 8192, 8192, 4)  # each entry's own: gets as far as the device
     refused(R.ERR_CUDA, go, 8192, 8192 + 32, 4)
     refused(R.ERR_CUDA, go, 8192, 8192 - 32, 4)
+
+
+def test_linear_attention_over_its_inputs(views):  # noqa: F811
+    view = views[0]
+    R.rimuru_view_set_state_shape(view, 4, 128, 128)
+
+    def go(q, k, v, o):
+        R.rimuru_linear_attention(view, q, k, v, o, 4096, 4, 1, 4096, 1, 8, 8, 4096, 4096, 1.0, 4096, 1 << 40)
+
+    a, b, c, d = (heads(data=i << 20) for i in range(1, 5))
+    for which in (a, b, c):
+        refused(R.ERR_ARG, go, a, b, c, which)
+    refused(R.ERR_CUDA, go, a, b, c, d)
+    refused(R.ERR_CUDA, go, a, a, a, d)  # inputs may be one array
