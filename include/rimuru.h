@@ -749,11 +749,12 @@ int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int 
  *             of the call reads or writes.
  *   workspace device, 1024-byte aligned, at least rimuru_linear_attention_workspace_bytes(...)
  *             bytes; calls that may run at the same time need one each
- * A NaN or an infinity in a token's q reaches its own outputs, in k, v or g the outputs and the state
- * from that token on (of v: its column), and never an earlier token, another head or sequence; an infinity
- * may have become a NaN there.
+ * A NaN or an infinity in a token's q reaches its own outputs, in k, v or g the outputs and the state of
+ * their heads from that token on (of v: its column), and no earlier token, other head or sequence; an
+ * infinity may have become a NaN there.
  * States and sums are fp32; in the chunked form the factors of a product are held as sums of bf16
- * parts (2^-16 of a factor, 2^-24 where they add to the state).  A page outside the view or
+ * parts (2^-16 of a factor, 2^-24 where they add to the state), and the terms (q . k) v of an output may
+ * become infinite from 2^62 on, where the recurrent form goes to 2^127.  A page outside the view or
  * bad offsets (a sequence longer than max_new, a row past num_tokens) are recorded in the view's
  * device error word (RIMURU_DEV_BAD_PAGE, RIMURU_DEV_BAD_SHAPE) and the sequence is left alone; where
  * offsets decrease, so may be parts of sequences whose rows others then claim too.
@@ -809,9 +810,11 @@ int rimuru_beam_select(const rimuru_rows* logits, const float* scores, const uin
  *   table_out  device int32 [num_layers][num_seqs][table_stride]: receives the parent's row; where
  *              the last page is partly filled, the child's fresh page in its place, into which codes
  *              and scales are copied.  Entries past the tokens are left as they are
- *   fresh      device int32 [num_layers][num_seqs]: pages that hold nothing any table_in names
+ *   fresh      device int32 [num_layers][num_seqs]: pages that hold nothing any table_in names, each
+ *              another one
  *   lens_out   device int32 [num_seqs]: the children's lengths
- * Outputs may not overlap inputs.  References to pages are the host's: pages that several children
+ * Outputs may not overlap inputs.  Without sequences or layers nothing is written, lengths neither.
+ * References to pages are the host's: pages that several children
  * name, or none, are shared and freed there (rimuru_page_share, rimuru_page_free).  A bad parent,
  * length or page is recorded in the view's error word (RIMURU_DEV_BAD_SHAPE with length 0,
  * RIMURU_DEV_BAD_PAGE with -1 in the page's place).  First call and capture as above. */

@@ -64,6 +64,20 @@ def test_more_alike_chunks_than_the_list_holds(kind, V, N, K):
     assert torch.equal(rows[0], want // n) and torch.equal(tokens[0], want % n * 1024)
 
 
+@pytest.mark.parametrize("N,V", [(4, 5003), (16, 300), (128, 77)])
+def test_scores_in_place(N, V):
+    """The selected sums replace the scores, as a loop over steps may have it; all entries at once."""
+    g = torch.Generator(device=DEV).manual_seed(N)
+    x, scores = torch.randn(500 * N, V, generator=g, device=DEV).bfloat16(), -torch.rand(500, N, generator=g, device=DEV)
+    want = select(x, scores, K=N)
+    rows, tokens = (torch.empty(500, N, dtype=torch.int32, device=DEV) for _ in range(2))
+    nbytes = R.rimuru_beam_select_workspace_bytes(500, N, V, N)
+    ws = torch.empty(nbytes + 1024, dtype=torch.uint8, device=DEV)
+    R.rimuru_beam_select(R.rows_of(x), scores.data_ptr(), 0, 500, N, 0, N, scores.data_ptr(), rows.data_ptr(), tokens.data_ptr(),
+                         (ws.data_ptr() + 1023) // 1024 * 1024, nbytes, torch.cuda.current_stream().cuda_stream)
+    assert all(torch.equal(a, b) for a, b in zip((scores, rows, tokens), want))
+
+
 # ------------------------------------------------------------------ linear attention
 @pytest.mark.parametrize("new", [[1000, 700], [64 * 20] * 9])
 def test_f16_prompts_beside_other_work(new):
