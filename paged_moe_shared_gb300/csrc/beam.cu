@@ -35,6 +35,11 @@ constexpr int kList = 1024;            // candidates that are ranked by counting
 constexpr int kMostBeams = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
+using dev::ex2;  // far more exact than a sum of thousands of terms
+using dev::Raw;
+using dev::to_f;
+using dev::unpack;
+
 struct BeamArgs {
   const void* logits;
   int64_t row_stride;
@@ -48,17 +53,6 @@ struct BeamArgs {
   int ctas;          // of the scan
   float *tops, *sums;  // [rows][n_chunks]: a chunk's maximum, its sum of exp(x - maximum)
 };
-
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f(float x) { return x; }
-
-// 2^x; the instruction is good to 2^-22, far below what a sum of thousands of terms keeps.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ __nv_bfloat16 lowest(__nv_bfloat16) { return __ushort_as_bfloat16(0xFF80); }
 __device__ __forceinline__ __half lowest(__half) { return __ushort_as_half(0xFC00); }
@@ -79,10 +73,6 @@ __device__ __forceinline__ const T* row_base(const BeamArgs& a, int row, int* sk
 
 // Eight elements from place `at` (a multiple of 8), as they lie in memory; places outside
 // [skip, end) are -inf.
-template <typename T>
-struct Raw {
-  uint4 w[sizeof(T) / 2];
-};
 template <typename T>
 __device__ __forceinline__ Raw<T> load8(const T* base, int at, int skip, int end) {
   Raw<T> v;
@@ -191,27 +181,6 @@ __device__ __forceinline__ float max8(const Raw<float>& r) {
 #pragma unroll
   for (int e = 1; e < 8; ++e) m = fmaxf(m, x[e]);
   return m;
-}
-
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, uint64_t (&x)[4]) {
-  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = dev::pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
-}
-__device__ __forceinline__ void unpack(const Raw<__half>& r, uint64_t (&x)[4]) {
-  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-    x[i] = dev::pair(f.x, f.y);
-  }
-}
-__device__ __forceinline__ void unpack(const Raw<float>& r, uint64_t (&x)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    x[2 * i] = dev::pair(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
-    x[2 * i + 1] = dev::pair(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
-  }
 }
 
 // A bit for each of eight elements that are at least `least`, as numbers that `tame` leaves.
@@ -337,17 +306,17 @@ __device__ __forceinline__ bool before(Candidate a, Candidate b) {
 
 // n + 1 if a is before b, else n: key and index as one number of 96 bits, b less a.
 __device__ __forceinline__ int count_before(int n, Candidate a, Candidate b) {
-  uint32_t t;
-  asm("{\n\t.reg .u32 al, ah, bl, bh;\n\t"
-      "mov.b64 {al, ah}, %2;\n\tmov.b64 {bl, bh}, %3;\n\t"
-      "sub.cc.u32 %1, %4, %5;\n\t"  // the lower index is the larger number
-      "subc.cc.u32 %1, bl, al;\n\t"
-      "subc.cc.u32 %1, bh, ah;\n\t"
-      "subc.u32 %1, 0, 0;\n\t"  // -1 where that borrowed
-      "sub.s32 %0, %6, %1;\n\t}\n"
-      : "=r"(n), "=&r"(t)
+  int next;
+  asm("{\n\t.reg .u32 al, ah, bl, bh, t;\n\t"
+      "mov.b64 {al, ah}, %1;\n\tmov.b64 {bl, bh}, %2;\n\t"
+      "sub.cc.u32 t, %3, %4;\n\t"  // the lower index is the larger number
+      "subc.cc.u32 t, bl, al;\n\t"
+      "subc.cc.u32 t, bh, ah;\n\t"
+      "subc.u32 t, 0, 0;\n\t"  // -1 where that borrowed
+      "sub.s32 %0, %5, t;\n\t}\n"
+      : "=r"(next)
       : "l"(a.key), "l"(b.key), "r"(a.index), "r"(b.index), "r"(n));
-  return n;
+  return next;
 }
 
 constexpr int kTops = 4096;  // chunk maxima that are kept in shared memory

@@ -6,6 +6,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cstdint>
 
 #include "../../include/rimuru.h"
@@ -616,6 +617,45 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+// ------------------------------------------------------------- elements
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ void from_f(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f(float x, __half* y) { *y = __float2half_rn(x); }
+__device__ __forceinline__ void from_f(float x, float* y) { *y = x; }
+// 2^x; the instruction is good to 2^-22.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Eight elements as they lie in memory, and as packed fp32.
+template <typename T>
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+};
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, uint64_t (&x)[4]) {
+  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack(const Raw<__half>& r, uint64_t (&x)[4]) {
+  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+    x[i] = pair(f.x, f.y);
+  }
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, uint64_t (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[2 * i] = pair(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+    x[2 * i + 1] = pair(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
+  }
 }
 
 }  // namespace dev

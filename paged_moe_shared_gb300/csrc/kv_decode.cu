@@ -94,11 +94,6 @@ struct DecodeShared {
   float row_sum[4][kDecodeMaxRows];
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
@@ -124,10 +119,6 @@ __device__ __forceinline__ bool named_bar_or(bool v) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(float x, __half* y) { *y = __float2half_rn(x); }
 
 // Byte offset of byte d (of kRowBytes) of row r in a swizzled K-major block.
 template <int kRowBytes>

@@ -111,11 +111,6 @@ struct TileShared {
   float row_sum[2][128];          // and their sums
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Two 16-bit numbers of type T as floats, and the larger ones of two pairs.
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t x) {

@@ -18,13 +18,11 @@
 namespace rimuru {
 namespace {
 
+using dev::from_f;
+using dev::to_f;
+
 constexpr int kStepThreads = 256;
 constexpr int kStepTokens = 8;  // tokens between barriers
-
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(float x, __half* y) { *y = __float2half_rn(x); }
 
 // kCols value columns of one head's state a CTA.  kStream: states pass through L2 without staying.
 template <typename T, int kKey, int kCols, bool kStream>
@@ -32,9 +30,7 @@ __global__ void __launch_bounds__(kStepThreads) linear_steps_kernel(const __grid
   constexpr int kLanes = kCols / 4;              // threads of a state row
   constexpr int kParts = kStepThreads / kLanes;  // threads that share a column
   constexpr int kRows = kKey / kParts;           // rows of a thread
-  constexpr int kWarpParts = 32 / kLanes;        // row parts inside a warp
-  constexpr int kWarps = kStepThreads / 32;
-  constexpr int kSums = kWarps;                  // partial sums of a column that meet in shared memory
+  constexpr int kSums = kStepThreads / 32;       // partial sums of a column that meet in shared memory: a warp's
   static_assert(kLanes <= 32 && kRows >= 1, "");
   __shared__ alignas(16) float qs[kStepTokens][kKey], ks[kStepTokens][kKey], vs[kStepTokens][kCols];
   __shared__ float decay[kStepTokens];

@@ -183,11 +183,6 @@ __device__ __forceinline__ void umma_f16_lo(uint32_t d_tmem, uint32_t a_lo, uint
       "r"(a_lo), "r"(b_lo), "r"(accumulate), "n"(kAHi), "n"(kBHi), "n"(kIdesc)
       : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // 16-byte piece `c` of row r in a swizzled block of 128-byte rows.
 __device__ __forceinline__ uint32_t place(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 template <typename T>

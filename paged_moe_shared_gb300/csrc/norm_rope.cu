@@ -53,38 +53,16 @@ struct NormArgs {
 using dev::fma2;
 using dev::mul2;
 using dev::pair;
+using dev::Raw;
 using dev::split;
+using dev::unpack;
 
-template <typename T>
-struct Raw {  // eight elements as they lie in memory
-  uint4 w[sizeof(T) / 2];
-};
 template <typename T>
 __device__ __forceinline__ Raw<T> load_raw(const T* p) {
   Raw<T> v;
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v.w[i] = reinterpret_cast<const uint4*>(p)[i];
   return v;
-}
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, uint64_t (&x)[4]) {
-  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
-}
-__device__ __forceinline__ void unpack(const Raw<__half>& r, uint64_t (&x)[4]) {
-  const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-    x[i] = pair(f.x, f.y);
-  }
-}
-__device__ __forceinline__ void unpack(const Raw<float>& r, uint64_t (&x)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    x[2 * i] = pair(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
-    x[2 * i + 1] = pair(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
-  }
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const uint64_t (&x)[4]) {
   uint32_t v[4];

@@ -30,6 +30,9 @@
 namespace rimuru {
 namespace {
 
+using dev::from_f;
+using dev::to_f;
+
 constexpr int kMaxArrays = 4;
 constexpr int kMaxTokens = 4;  // of a CTA
 
@@ -66,12 +69,6 @@ __device__ __forceinline__ void store8(T* p, const Vec8<T>& v) {
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = v.w[i];
 }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ void from_f(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(float x, __half* y) { *y = __float2half_rn(x); }
-__device__ __forceinline__ void from_f(float x, float* y) { *y = x; }
 
 // An item is one thread's unit of work in a head: items below `turn_items` turn
 // pairs (two vectors of eight in the half layout, one in the interleaved one),
