@@ -50,7 +50,6 @@ struct BeamArgs {
   float* best;
   int32_t *rows, *tokens;
   int n_chunks;      // of a row
-  int ctas;          // of the scan
   float *tops, *sums;  // [rows][n_chunks]: a chunk's maximum, its sum of exp(x - maximum)
 };
 
@@ -103,7 +102,7 @@ __device__ __forceinline__ uint4 load16(const T* base, int at, int end) {
 // the last bit, wherever the row begins, and beams that are alike tie.  Vectors are loaded from places, and
 // move down by `skip` elements once they are there (to_tokens): the first ones of the next lane follow a
 // lane's own, and lane 0 holds the 16 bytes behind the chunk for the last one.
-// kAny: rows may begin off the boundaries (32 x 8 beams over 151,935 tokens 28.6 us; grouped by places and
+// kAny: rows may begin off the boundaries (32 x 8 beams over 151,935 tokens 26.8 us; grouped by places and
 // without moving, 22.0).  Where none does there is nothing to move (151,936 tokens 21.8; with the registers
 // that moving takes 22.8 to 24.7).
 constexpr int kVec = kChunk / 256;
@@ -642,8 +641,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
 }
 
 template <typename T, bool kAny>
-cudaError_t launch_rows(const BeamArgs& a, cudaStream_t s) {
-  beam_scan_kernel<T, kAny><<<a.ctas, kScanThreads, 0, s>>>(a);
+cudaError_t launch_rows(const BeamArgs& a, int sms, cudaStream_t s) {
+  // Four CTAs an SM, which bf16 has at the same time (fp32 two: 64 x 5 beams 20.7 us, with three 21.9); three
+  // where 16-bit rows are moved, which is what their registers allow (26.8 us, with four 28.6).
+  const int64_t chunks = static_cast<int64_t>(a.groups) * a.beams * a.n_chunks;
+  const int ctas = static_cast<int>(std::min<int64_t>((chunks + 7) / 8, (kAny && sizeof(T) == 2 ? 3ll : 4ll) * sms));
+  beam_scan_kernel<T, kAny><<<ctas, kScanThreads, 0, s>>>(a);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.groups);
   cfg.blockDim = dim3(kPickThreads);
@@ -658,9 +661,9 @@ cudaError_t launch_rows(const BeamArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : last;
 }
 template <typename T>
-cudaError_t launch(const BeamArgs& a, cudaStream_t s) {
+cudaError_t launch(const BeamArgs& a, int sms, cudaStream_t s) {
   const uint64_t at = reinterpret_cast<uintptr_t>(a.logits) | static_cast<uint64_t>(a.row_stride) * sizeof(T);
-  return at % 16 == 0 ? launch_rows<T, false>(a, s) : launch_rows<T, true>(a, s);
+  return at % 16 == 0 ? launch_rows<T, false>(a, sms, s) : launch_rows<T, true>(a, sms, s);
 }
 
 // ------------------------------------------------------------------ reordering
@@ -810,11 +813,10 @@ extern "C" int rimuru_beam_select(const rimuru_rows* logits, const float* scores
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("device attributes", e));
-  a.ctas = static_cast<int>(std::min<int64_t>((chunks + 7) / 8, 4ll * sms));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  e = logits->dtype == RIMURU_BF16  ? launch<__nv_bfloat16>(a, s)
-      : logits->dtype == RIMURU_F16 ? launch<__half>(a, s)
-                                    : launch<float>(a, s);
+  e = logits->dtype == RIMURU_BF16  ? launch<__nv_bfloat16>(a, sms, s)
+      : logits->dtype == RIMURU_F16 ? launch<__half>(a, sms, s)
+                                    : launch<float>(a, sms, s);
   if (e != cudaSuccess) return fail(RIMURU_ERR_CUDA, kv_cuda_msg("beam selection launch", e));
   return RIMURU_OK;
 }
