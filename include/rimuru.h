@@ -753,8 +753,8 @@ int rimuru_view_set_state_shape(rimuru_view_t view, int heads, int key_dim, int 
  * their heads from that token on (of v: its column), and no earlier token, other head or sequence; an
  * infinity may have become a NaN there.
  * States and sums are fp32; in the chunked form the factors of a product are held as sums of bf16
- * parts (2^-16 of a factor, 2^-24 where they add to the state), and the terms (q . k) v of an output may
- * become infinite from 2^62 on, where the recurrent form goes to 2^127.  A page outside the view or
+ * parts (2^-17 of a factor is lost, f16 2^-16, and 2^-24 where they add to the state), and the terms (q . k) v of an output may
+ * become infinite from 2^62 on, what a state's elements give from 2^127 on.  A page outside the view or
  * bad offsets (a sequence longer than max_new, a row past num_tokens) are recorded in the view's
  * device error word (RIMURU_DEV_BAD_PAGE, RIMURU_DEV_BAD_SHAPE) and the sequence is left alone; where
  * offsets decrease, so may be parts of sequences whose rows others then claim too.

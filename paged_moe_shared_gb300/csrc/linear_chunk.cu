@@ -10,9 +10,10 @@
 // All products are made transposed, with the value columns in the 128 lanes of TMEM and
 // 64 tokens or the key columns across, so that every MMA has full height:
 //   scores  Q K^T          (64 x 64; the lanes below take K K^T, which nobody reads)
-//   inter   S^T Q^T        S^T in TMEM, as two bf16 parts that its owners write there
+//   inter   S^T Q^T        S^T in TMEM, as two bf16 parts that its owners write there: 2^-17 of it is lost
 //   intra   V^T P^T        onto it; P = scores * decays, two bf16 parts in shared memory
 //   update  V^T Kd         Kd = decayed keys, three bf16 parts: an fp32 number exactly
+// Products of two lower parts (f16, inter and scores) are left out, 2^-16.
 // S^T itself stays in the registers of eight warps in fp32 and takes each chunk's update
 // there: sums inside the tensor cores truncate, and over thousands of tokens that would
 // show.  f16 inputs are split into two bf16 parts in shared memory, exactly.
@@ -203,15 +204,16 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ uint32_t tops(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
-__device__ __forceinline__ float top(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
-
 __device__ __forceinline__ uint32_t tops(uint64_t x) { return tops(split(x).x, split(x).y); }
+// The nearest bf16, which leave half as much as `tops` does: with `rest` 2^-17 of a number is lost, and it
+// costs nothing (half as many outputs of a prompt are rounded the other way than the exact ones).
+__device__ __forceinline__ uint32_t nearest(uint64_t x) { return pack_bf16x2(split(x).x, split(x).y); }
 // Two bf16 as fp32.  The lower one moves up by a product, which is not the logic unit's work:
 // with the cutting of parts that has more to do than any other here.
 __device__ __forceinline__ uint64_t widen(uint32_t two) {
   return pair(__uint_as_float(two * 65536u), __uint_as_float(two & 0xFFFF0000u));
 }
-// Two numbers less their upper halves.
+// Two numbers less those.
 __device__ __forceinline__ uint64_t below(uint64_t x, uint32_t upper) { return fma2(widen(upper), pair(-1.f, -1.f), x); }
 // That, as a pair of bf16.
 __device__ __forceinline__ uint32_t rest(uint64_t x, uint32_t upper) {
@@ -219,15 +221,15 @@ __device__ __forceinline__ uint32_t rest(uint64_t x, uint32_t upper) {
   return pack_bf16x2(r.x, r.y);
 }
 
-// Eight f16 as two bf16 parts: their 11 bits are 8 and 3.
+// Eight f16 as two bf16 parts: their 11 bits are 8, to the nearest, and the rest.
 __device__ __forceinline__ void split_f16(const uint4& w, uint4* hi, uint4* lo) {
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[i]));
-    h[i] = tops(f.x, f.y);
-    l[i] = tops(f.x - top(f.x), f.y - top(f.y));
+    h[i] = pack_bf16x2(f.x, f.y);
+    l[i] = tops(below(pair(f.x, f.y), h[i]));
   }
   *hi = make_uint4(h[0], h[1], h[2], h[3]);
   *lo = make_uint4(l[0], l[1], l[2], l[3]);
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             const float2 z = split(y[e]);  // later tokens do not count
             const uint64_t w = pair(j0 + 2 * e <= i ? z.x : 0.f, j0 + 2 * e + 1 <= i ? z.y : 0.f);
-            hi[e] = tops(w);
+            hi[e] = nearest(w);
             lo[e] = rest(w, hi[e]);
           }
           const uint32_t o = place(i, 4 * half + v);
@@ -978,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int d = 0; d < 16; ++d) {
-              hi[d] = tops(S[d0 / 2 + d]);
+              hi[d] = nearest(S[d0 / 2 + d]);
               lo[d] = rest(S[d0 / 2 + d], hi[d]);
             }
             tmem_st16(at + kState + (wg * kN + d0) / 2, hi);

@@ -229,3 +229,43 @@ def test_states_pass_on_without_tokens():
             assert torch.equal(c.mem[c.state_out[b]], want)
         others = [p for p in range(12) if p not in c.state_out.tolist()]
         assert torch.equal(c.mem[others], before[others])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(4, 2, 128, 128), (2, 1, 64, 64)])
+@pytest.mark.parametrize("where", ["scores", "state"])
+def test_what_parts_of_a_factor_lose(where, shape, kind):
+    """Outputs that are the difference of two almost equal products show what each of them has lost.  A factor
+    of 2^e to 2^(e + 1) less its nearest bf16 is 2^(e - 8) at most, and a number below that, to the nearest
+    bf16, 2^(e - 17) off: 2^-17 of the factor (cut off instead of rounded, the first part would leave twice
+    that).  Queries and keys are 1, one part.  fp32's own roundings (a decay, two products, sums) stay
+    below 2^-20."""
+    c = Case([64, 50, 900], *shape, kind=kind)
+    heads, key_heads, dk, dv = shape
+    c.scale = 1.0
+    c.q.zero_(), c.k.zero_(), c.v.zero_(), c.mem.zero_()
+    if where == "scores":  # one key of 1, one of -1 a moment later; what the decays leave of both
+        c.q[..., 0] = 1.0
+        c.g[:] = -torch.rand(c.T, heads, generator=c.gen, device=DEV) * 0.01
+        at = 0
+        for n in c.new:
+            for first in range(0, n - 1, 64):
+                c.k[at + first:at + first + 2, :, 0] = 1.0
+                c.v[at + first], c.v[at + first + 1] = 1.0, -1.0
+                c.g[at + first + 1] = -2.0 ** -11 * torch.rand(heads, generator=c.gen, device=DEV)
+            at += n
+        c.g[::64] -= 12.0  # chunks before have little left to say
+    else:  # queries that add two rows of the state
+        c.q[..., 0] = c.q[..., 1] = 1.0
+        c.g.zero_()
+        x = torch.rand(c.pages, heads, dv, generator=c.gen, device=DEV) + 1
+        c.states()[:, :, 0] = x
+        c.states()[:, :, 1] = -x * (1 + 2.0 ** -11 * torch.rand(x.shape, generator=c.gen, device=DEV))
+    want, size, _ = c.plain()
+    c.run()
+    torch.cuda.synchronize()
+    tol = torch.finfo(c.out.dtype).eps / 2 * want.abs() + (2.0 ** -17 + 2.0 ** -20) * size
+    tol += 2.0 ** -25 if kind == "f16" else 0
+    err = (c.out.double() - want).abs()
+    assert bool((err <= tol).all()), float((err / (tol + 1e-30)).max())
+    assert R.rimuru_get_device_error(c.view) == R.DEV_OK
