@@ -11,9 +11,9 @@
 // reach, reads the chunks whose leaders reach it again and ranks what does.  Comparisons that decide are made on
 // doubles; fp32 only sieves, with a margin.
 //
-// 32 entries of 8 beams over 151,936 tokens in bf16 (78 MB), 16 best: 21.8 us, of which the
-// scan takes 15.7 (0.73 of the copy rate; 71 % of the issue slots) and the pick 6, a chain of
-// a dozen barriers and three dependent loads on one SM an entry.  One entry of 4 beams 9.2 us.  With
+// 32 entries of 8 beams over 151,936 tokens in bf16 (78 MB), 16 best: 21.7 us, of which the
+// scan takes 15.7 (0.73 of the copy rate; 68 % of the issue slots) and the pick 6, a chain of
+// a dozen barriers and three dependent loads on one SM an entry.  One entry of 4 beams 8.4 us.  With
 // maxima of 64 tokens in place of chunks the scan took 20 us and the pick, which has then
 // sixteen times as many, 30.
 #include <algorithm>
@@ -103,7 +103,7 @@ __device__ __forceinline__ uint4 load16(const T* base, int at, int end) {
 // move down by `skip` elements once they are there (to_tokens): the first ones of the next lane follow a
 // lane's own, and lane 0 holds the 16 bytes behind the chunk for the last one.
 // kAny: rows may begin off the boundaries (32 x 8 beams over 151,935 tokens 26.8 us; grouped by places and
-// without moving, 22.0).  Where none does there is nothing to move (151,936 tokens 21.8; with the registers
+// without moving, 22.0).  Where none does there is nothing to move (151,936 tokens 21.7; with the registers
 // that moving takes 22.8 to 24.7).
 constexpr int kVec = kChunk / 256;
 template <typename T, bool kAny>
@@ -523,7 +523,9 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   // chunks, which may all be good, then count apart.
   const int want = a.n_select, mixed = want > 32 ? (tid & 3) << 8 | tid >> 2 : (tid & 7) << 7 | tid >> 3;
   float sieve = -INFINITY;
-  if (n_tops > 64) {  // below, all may
+  // Few chunks may all: their bound would be one that too many candidates pass.  (8 entries, tops and
+  // n_select: 32 and 16 9.3 us, with a sieve 18.2; 128 and 16 9.5, without one 14.8; but 64 and 8 10.9, with one 8.3.)
+  if (n_tops > 64) {
     float best = -INFINITY;
     for (int i = mixed; i < n_tops; i += kPickThreads) {
       float err;

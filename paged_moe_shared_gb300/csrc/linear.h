@@ -37,7 +37,8 @@ LinearCut linear_cut(int heads, int key_dim, int value_dim, int sms, int num_seq
 // every SM has at most one state of 128 x 128, and as much for each state of an SM beyond; the
 // chunked form costs 11 us, and 5 us for each further state of an SM, at any number of tokens up
 // to 64.  32 heads: one sequence of 16 tokens 8.3 and 10.8 us, of 24 11.1 and 10.8; 8 sequences of
-// 8 tokens 16.2 and 18.6, of 12 20.6 and 18.6; 64 of 4 58.7 and 72.6, of 8 90 and 73.
+// 8 tokens 16.2 and 18.6, of 12 20.6 and 18.6; 64 of 4 58.7 and 72.6, of 8 90 and 73.  That is bf16; f16
+// costs the same token by token and more in chunks, and changes over at the same numbers.
 inline int steps_most(int heads, int key_dim, int value_dim, int sms, int num_seqs) {
   const double states = static_cast<double>(num_seqs) * heads * key_dim * value_dim / (128 * 128) / sms;
   return states <= 1 ? 16 : states <= 4 ? 10 : 5;

@@ -30,9 +30,9 @@
 // by TMA.  One CTA an SM; tiles, scores, outputs and decayed keys have two buffers each
 // (f16 has twice the parts: one, and the next tiles behind it).
 //
-// One prompt of 8192 tokens, 32 heads on 16 key heads of 128 x 128, bf16: 116 us, 45 of
-// them in the first kernel (token by token 4550 us); seven prompts of 558 to 1663 tokens 93,
-// f16 171.  What bounds a chunk of the second kernel, 2.4 us, is instructions: 10,400 of them,
+// One prompt of 8192 tokens, 32 heads on 16 key heads of 128 x 128, bf16: 118 us, 45 of
+// them in the first kernel (token by token 4550 us); seven prompts of 558 to 1663 tokens 96,
+// f16 208 and 170.  What bounds a chunk of the second kernel, 2.4 us, is instructions: 10,400 of them,
 // 63 % of the issue slots, half of them in the cutting into parts; the tensor pipe is busy for
 // a third.  On the way: loads by two warps of 16-byte copies 220 us, by TMA 150; packed fp32
 // 141; 103 KiB of code, which the instruction cache fetched again and again (71 % of its hits
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   // Units, the longest pieces first and every other round backwards: a CTA that got a long one
-  // gets a short one next (seven prompts of 558 to 1663 tokens, 32 heads: 93 us, in the order of the
+  // gets a short one next (seven prompts of 558 to 1663 tokens, 32 heads: 96 us, in the order of the
   // sequences 110).  More pieces than threads even out by themselves.
   const int slots = p.units / a.heads, ctas = gridDim.x;
   const bool sorted = slots <= kThreads && p.units > ctas;
@@ -1056,7 +1056,10 @@ cudaError_t launch_dims(const ChunkArgs& p, const CUtensorMap* tm, cudaStream_t 
 
 LinearCut linear_cut(int heads, int key_dim, int value_dim, int sms, int num_seqs, int num_tokens, int max_new) {
   // Times in chunks of the second kernel: a chunk of the first costs 0.45, a unit's start one,
-  // another kernel four, and a piece reads the states of those before it at about 0.3 each.
+  // another kernel four, and a piece reads the states of those before it at about 0.3 each.  Several
+  // sequences seldom are all as long as the longest: 0.75 of that.  (32 heads of 128: 2048 tokens whole 71.5 us,
+  // in pieces of 512 47.3; 3 x 2048 whole 73.3, in pieces of 1408 89; 32,768 whole 1002, pieces of 1728 414; 2 x 4096
+  // takes pieces of 1088, 132, where 2048 would take 118.)
   const auto cost = [&](int piece) {
     const int64_t longest = piece > 0 ? std::min(piece, max_new) : max_new;
     const int64_t pieces = piece > 0 ? num_seqs + num_tokens / piece : num_seqs;
